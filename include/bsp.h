@@ -394,6 +394,122 @@ int bsp_attention_host(bsp_layout_t layout, int dtype, const void* Q, const void
                        size_t workspace_bytes, int flags, void* stream);
 size_t bsp_attention_host_workspace(bsp_layout_t layout, int dtype, int D, int z_slice);
 
+/* ---- windowed attention and paged cache -----------------------------------
+ * Causal attention for language models beside the block-sparse operations
+ * above: element-exact sliding window with sink tokens, query heads that share
+ * KV heads, lengths that are no multiple of a block, ragged batches and a
+ * paged cache.  No counterpart in the pages.
+ *
+ * Visibility: key j is visible to the query at position p when
+ *     j <= p and (p - j < window or j < sinks);
+ * window 0 = no limit.  A query that sees no key has output 0 and log-sum-exp
+ * -inf, and contributes nothing to a gradient.
+ *
+ * Tensors are strided (bsp_tensor_t): element (i, j, k, d) at
+ * ptr + (i * stride[0] + j * stride[1] + k * stride[2] + d) elements; the
+ * stride of an extent of 1 is ignored.  Pointers 16-byte aligned and strides
+ * multiples of 16 bytes (else BSP_ERR_ALIGNMENT), strides positive, outputs
+ * not overlapping themselves (else BSP_ERR_INVALID_ARG) nor any input.  So
+ * [Z][H][S][D] and [Z][S][H][D] tensors, slices of a fused projection and
+ * either order of a page are all taken as they are.
+ *
+ * Hq is a multiple of Hkv (query head h reads KV head h / (Hq / Hkv)), at most
+ * 64 query heads per KV head; D 16 .. 128, a multiple of 16; lengths up to
+ * 2^30 (beyond: BSP_ERR_UNSUPPORTED).  dtype, streams, errors as above; sums,
+ * softmax statistics and partial results are fp32, the 16-bit tensor-core
+ * paths round P and dS to the call's type (unnormalised P <= 2^8).
+ *
+ * Non-finite values: keys that no query of a call sees (behind a sequence's
+ * length, before every window) never reach an output, whatever their slots
+ * hold, and a hidden K row never reaches a query that does not see it.  A
+ * non-finite V row (in the gradient also K, Q, dO) that some query of a tile
+ * of 128 rows sees may reach the tile's other rows (0 * inf).
+ *
+ * Workspaces are the caller's (DEVICE, 256-byte aligned, else
+ * BSP_ERR_ALIGNMENT; too small: BSP_ERR_INVALID_ARG); their contents need not
+ * be kept between calls, and calls that may run at the same time need one
+ * each -- graphs captured with the same workspace must not replay at the same
+ * time.  Results do not depend on timing: partial results are joined in a
+ * fixed order. */
+
+typedef struct bsp_window_s* bsp_window_t;
+
+typedef struct {
+    void* ptr;
+    int64_t stride[3];
+} bsp_tensor_t;
+
+/* A visibility rule on the current device, with the device status word its
+ * calls report to.  window, sinks >= 0.  The handle is immutable and may be
+ * used from several streams of its device; the word is cleared on `stream`. */
+int bsp_window_create(int window, int sinks, void* stream, bsp_window_t* out);
+/* Free a handle (waits for the device).  NULL is ignored. */
+int bsp_window_destroy(bsp_window_t w);
+int bsp_window_info(bsp_window_t w, int* window, int* sinks);
+/* As bsp_status_check: synchronise `stream`, return and clear the status word
+ * (BSP_ERR_DEVICE_CHECK: a call met impossible lengths or a page out of range;
+ * BSP_ERR_TIMEOUT: a bounded wait ran out). */
+int bsp_window_status(bsp_window_t w, void* stream);
+
+/* O = softmax(scale Q K^T over the visible keys) V.  Q, O: (z, query head,
+ * row), K, V: (z, KV head, row), Sq and Sk rows; the queries are the last Sq
+ * positions, query i at p = Sk - Sq + i (negative: sees nothing).  lse: DEVICE
+ * float [Z][Hq][Sq], each row's ln sum exp of its visible scaled scores, or
+ * NULL.  Workspace: bsp_window_attention_workspace(Z, Hq, Sq, 0) bytes. */
+int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K,
+                         const bsp_tensor_t* V, const bsp_tensor_t* O, float* lse, int Z, int Hq, int Hkv, int Sq,
+                         int Sk, int D, float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of bsp_window_attention for the output gradient dO, given its O
+ * and lse: with P = exp(scale Q K^T - lse) on the visible pairs and
+ * dS = P .* (dO V^T - rowsum(dO .* O)),
+ *     dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K,
+ * dK and dV summed over the query heads that share the KV head.  Workspace:
+ * bsp_window_attention_workspace(Z, Hq, Sq, 1) bytes. */
+int bsp_window_attention_backward(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K,
+                                  const bsp_tensor_t* V, const bsp_tensor_t* O, const bsp_tensor_t* dO,
+                                  const float* lse, const bsp_tensor_t* dQ, const bsp_tensor_t* dK,
+                                  const bsp_tensor_t* dV, int Z, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+size_t bsp_window_attention_workspace(int Z, int Hq, int Sq, int backward);
+
+/* Paged cache.  K_cache, V_cache: (page, KV head, slot), n_pages pages of
+ * `page` slots (16, 32, 64 or 128).  table: DEVICE int32 [n_seq][max_pages],
+ * position j of sequence s is slot j % page of page table[s][j / page].
+ * q_start: DEVICE int32 [n_seq + 1], sequence s's new tokens are rows
+ * q_start[s] .. q_start[s + 1] - 1 of the T rows; kv_len: DEVICE int32
+ * [n_seq], its length with the new tokens, which stand at its last positions.
+ * The host never reads the three arrays, so a captured call follows their
+ * contents.  n_seq <= 16384 (beyond: BSP_ERR_UNSUPPORTED).
+ *
+ * Checked on the device, reported as BSP_ERR_DEVICE_CHECK by
+ * bsp_window_status: a sequence with q_start out of order or beyond T, or
+ * kv_len negative or beyond max_pages * page, is left out; a page of a visible
+ * position outside [0, n_pages) is never accessed (the output of the call is
+ * then undefined).  Table entries of pages without a visible position are not
+ * used and may hold anything. */
+
+/* Writes the new tokens' rows K, V (-, KV head, row) to their slots
+ * (bsp_tensor_t stride[0] unused).  Positions below 0 (kv_len smaller than the
+ * new tokens) are not written.  Two rows with the same slot: either one's
+ * values. */
+int bsp_paged_append(bsp_window_t w, int dtype, const bsp_tensor_t* K, const bsp_tensor_t* V,
+                     const bsp_tensor_t* K_cache, const bsp_tensor_t* V_cache, const int32_t* q_start,
+                     const int32_t* kv_len, const int32_t* table, int T, int n_seq, int max_pages, int n_pages,
+                     int page, int Hkv, int D, void* stream);
+
+/* Attention of the new tokens Q (-, query head, row) over the cache, which
+ * holds their own keys already (bsp_paged_append): one token per sequence
+ * (decoding), chunks of prompts, or both in one batch.  O like Q; lse: DEVICE
+ * float [T][Hq] or NULL.  Rows of no sequence are left as they were.
+ * Workspace: bsp_paged_attention_workspace() bytes. */
+int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K_cache,
+                        const bsp_tensor_t* V_cache, const bsp_tensor_t* O, float* lse, const int32_t* q_start,
+                        const int32_t* kv_len, const int32_t* table, int T, int n_seq, int max_pages, int n_pages,
+                        int page, int Hq, int Hkv, int D, float scale, void* workspace, size_t workspace_bytes,
+                        void* stream);
+size_t bsp_paged_attention_workspace(void);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Evaluate, on n DEVICE floats x, the software 2^x that the attention softmax
@@ -472,6 +588,18 @@ int bsp_diag_attention_split(bsp_layout_t layout, int max_steps);
  * restores normal operation.  Other inject bits: BSP_ERR_INVALID_ARG.  Not
  * from the pages: the robustness checks of this implementation. */
 int bsp_diag_wait_limit(bsp_layout_t layout, uint64_t wait_ns, int inject);
+
+/* Evaluate ON THE HOST the key tiles that the windowed attention kernels visit
+ * for a tile of query rows at positions a .. b (b - a < 128): into HOST int
+ * tiles [cap] the key tiles of 1 << shift keys in order, *n their number
+ * (may exceed cap; then only cap are written).  shift 4 .. 7.  One tile that
+ * hides every key stands for rows that see nothing. */
+int bsp_diag_window_tiles(int window, int sinks, int a, int b, int shift, int* n, int* tiles, int cap);
+
+/* The same for the key side: the query tiles of `tokens` consecutive tokens
+ * (of Sq, the last of Sk positions) that see a key of key tile t: *first and
+ * *n (tile 0, n = 1: none sees one). */
+int bsp_diag_window_queries(int window, int sinks, int Sq, int Sk, int tokens, int shift, int t, int* first, int* n);
 
 /* ---- status ------------------------------------------------------------ */
 

@@ -27,6 +27,12 @@ STATUS = {0: "BSP_OK", -1: "BSP_ERR_INVALID_ARG", -2: "BSP_ERR_UNSUPPORTED",
 _lib = None
 
 
+class Tensor(ctypes.Structure):
+    """bsp_tensor_t: a pointer and the element strides of the three outer dimensions."""
+
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride", ctypes.c_int64 * 3)]
+
+
 class BspError(RuntimeError):
     def __init__(self, code: int, what: str):
         self.code = code
@@ -80,6 +86,25 @@ def lib():
         L.bsp_status_string.restype = ctypes.c_char_p
         L.bsp_status_string.argtypes = [i32]
         L.bsp_version.restype = ctypes.c_char_p
+        sz, T = ctypes.c_size_t, ctypes.POINTER(Tensor)
+        L.bsp_window_create.argtypes = [i32, i32, P, ctypes.POINTER(P)]
+        L.bsp_window_destroy.argtypes = [P]
+        L.bsp_window_info.argtypes = [P, P, P]
+        L.bsp_window_status.argtypes = [P, P]
+        L.bsp_window_attention.argtypes = [P, i32, T, T, T, T, P] + [i32] * 6 + [f32, P, sz, P]
+        L.bsp_window_attention_backward.argtypes = [P, i32, T, T, T, T, T, P, T, T, T] + [i32] * 6 + [f32, P, sz, P]
+        L.bsp_paged_append.argtypes = [P, i32, T, T, T, T, P, P, P] + [i32] * 7 + [P]
+        L.bsp_paged_attention.argtypes = [P, i32, T, T, T, T, P, P, P, P] + [i32] * 8 + [f32, P, sz, P]
+        L.bsp_window_attention_workspace.argtypes = [i32, i32, i32, i32]
+        L.bsp_window_attention_workspace.restype = sz
+        L.bsp_paged_attention_workspace.argtypes = []
+        L.bsp_paged_attention_workspace.restype = sz
+        L.bsp_diag_window_tiles.argtypes = [i32] * 5 + [P, P, i32]
+        L.bsp_diag_window_queries.argtypes = [i32] * 7 + [P, P]
+        for name in ("bsp_window_create", "bsp_window_destroy", "bsp_window_info", "bsp_window_status",
+                     "bsp_window_attention", "bsp_window_attention_backward", "bsp_paged_append",
+                     "bsp_paged_attention", "bsp_diag_window_tiles", "bsp_diag_window_queries"):
+            getattr(L, name).restype = i32
         for name in ("bsp_layout_plan", "bsp_layout_compile", "bsp_layout_compile_device", "bsp_layout_destroy",
                      "bsp_layout_info",
                      "bsp_layout_get_luts", "bsp_layout_tiles", "bsp_sdd", "bsp_dsd", "bsp_dds", "bsp_softmax",
@@ -501,3 +526,260 @@ class _BlockSparseAttention(torch.autograd.Function):
 def block_sparse_attention(L: Layout, Q, K, V, scale: float, mask_kind: int = MASK_NONE, mask=None):
     """Differentiable block-sparse attention (torch autograd) on a compiled layout."""
     return _BlockSparseAttention.apply(Q, K, V, L, float(scale), int(mask_kind), mask)
+
+
+# ------------------------------------- windowed attention and paged cache --
+
+class Window:
+    """Owning wrapper of a bsp_window_t handle: a visibility rule (key j is
+    visible to the query at position p when j <= p and (p - j < window or
+    j < sinks); window 0 = no limit) on one device."""
+
+    def __init__(self, handle: ctypes.c_void_p, device: torch.device):
+        self.handle = handle
+        self.device = device
+        w, s = ctypes.c_int(), ctypes.c_int()
+        _check(lib().bsp_window_info(handle, ctypes.byref(w), ctypes.byref(s)), "bsp_window_info")
+        self.window, self.sinks = w.value, s.value
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.bsp_window_destroy(self.handle)
+            self.handle = None
+
+
+def bsp_window_create(window: int = 0, sinks: int = 0, stream=None) -> Window:
+    """A visibility rule on the current device."""
+    h = ctypes.c_void_p()
+    _check(lib().bsp_window_create(int(window), int(sinks), _stream(stream), ctypes.byref(h)), "bsp_window_create")
+    return Window(h, torch.device("cuda", torch.cuda.current_device()))
+
+
+def bsp_window_status(W: Window, stream=None) -> int:
+    return int(lib().bsp_window_status(W.handle, _stream(stream)))
+
+
+def _torch_stream(stream, device):
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    if not int(stream):
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(int(stream), device=device)
+
+
+class _Call:
+    """The device and stream of one call: the handle's device is made current,
+    and what the call allocates belongs to the stream the call runs on."""
+
+    def __init__(self, W: Window, stream):
+        self.W, self.stream = W, _torch_stream(stream, W.device)
+        if self.stream.device != W.device:
+            raise ValueError(f"the stream is on {self.stream.device}, the handle on {W.device}")
+
+    def __enter__(self):
+        self._ctx = torch.cuda.stream(self.stream)  # makes the stream's device current too
+        self._ctx.__enter__()
+        return self
+
+    def __exit__(self, *a):
+        return self._ctx.__exit__(*a)
+
+    @property
+    def ptr(self):
+        return ctypes.c_void_p(self.stream.cuda_stream)
+
+    def workspace(self, nbytes: int):
+        return torch.empty(nbytes, dtype=torch.uint8, device=self.W.device)
+
+    def dtype(self, *ts):
+        d = ts[0].dtype
+        if d not in _DTYPES:
+            raise TypeError(f"unsupported dtype {d}")
+        for t in ts:
+            if t.dtype != d:
+                raise TypeError("all tensors of a call must share one dtype")
+            self.on_device(t)
+        return _DTYPES[d]
+
+    def on_device(self, *ts):
+        for t in ts:
+            if t is not None and t.device != self.W.device:
+                raise ValueError(f"a tensor is on {t.device}, the handle on {self.W.device}")
+
+
+def _strided(t, order):
+    """bsp_tensor_t of t, its dimensions `order` as the three outer ones."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError("the last dimension must be contiguous")
+    return Tensor(t.data_ptr() if t.numel() else None, (ctypes.c_int64 * 3)(*[0 if d is None else t.stride(d) for d in order]))
+
+
+def _shape(t, shape, what):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _lse_ok(lse, shape):
+    _shape(lse, shape, "lse")
+    if lse.dtype != torch.float32 or not lse.is_contiguous():
+        raise ValueError("lse must be a contiguous float32 tensor")
+
+
+def _dense_sizes(Q, K, V):
+    if Q.dim() != 4 or K.dim() != 4:
+        raise ValueError("Q, K and V must be [Z, heads, rows, D]")
+    Z, Hq, Sq, D = Q.shape
+    Hkv, Sk = K.shape[1], K.shape[2]
+    _shape(K, (Z, Hkv, Sk, D), "K")
+    _shape(V, (Z, Hkv, Sk, D), "V")
+    if Hkv < 1 or Hq % Hkv:
+        raise ValueError("the query heads must be a multiple of the KV heads")
+    return Z, Hq, Hkv, Sq, Sk, D
+
+
+_HEADS = (0, 1, 2)        # [Z, heads, rows, D]
+_ROWS = (None, 1, 0)      # [rows, heads, D]
+
+
+def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.0, stream=None):
+    """Causal attention with the handle's window and sinks: (O, lse fp32
+    [Z, Hq, Sq]).  Q [Z, Hq, Sq, D], K and V [Z, Hkv, Sk, D] of any strides
+    that are multiples of 16 bytes with a contiguous last dimension; the
+    queries are the last Sq of the Sk positions."""
+    Z, Hq, Hkv, Sq, Sk, D = _dense_sizes(Q, K, V)
+    with _Call(W, stream) as c:
+        if O is None:
+            O = torch.empty((Z, Hq, Sq, D), dtype=Q.dtype, device=Q.device)
+        if lse is None:
+            lse = torch.empty((Z, Hq, Sq), dtype=torch.float32, device=Q.device)
+        dt = c.dtype(Q, K, V, O)
+        c.on_device(lse)
+        _shape(O, Q.shape, "O")
+        _lse_ok(lse, (Z, Hq, Sq))
+        n = int(lib().bsp_window_attention_workspace(Z, Hq, Sq, 0))
+        ws = c.workspace(n)
+        _check(lib().bsp_window_attention(W.handle, dt, *[ctypes.byref(_strided(t, _HEADS)) for t in (Q, K, V, O)],
+                                          _ptr(lse), Z, Hq, Hkv, Sq, Sk, D, float(scale), _ptr(ws), n, c.ptr),
+               "bsp_window_attention")
+    return O, lse
+
+
+def bsp_window_attention_backward(W: Window, Q, K, V, O, dO, lse, dQ=None, dK=None, dV=None, scale: float = 1.0,
+                                  stream=None):
+    """(dQ, dK, dV) of bsp_window_attention for the output gradient dO, given
+    its O and lse."""
+    Z, Hq, Hkv, Sq, Sk, D = _dense_sizes(Q, K, V)
+    with _Call(W, stream) as c:
+        dQ = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) if dQ is None else dQ
+        dK = torch.empty(K.shape, dtype=K.dtype, device=K.device) if dK is None else dK
+        dV = torch.empty(V.shape, dtype=V.dtype, device=V.device) if dV is None else dV
+        dt = c.dtype(Q, K, V, O, dO, dQ, dK, dV)
+        c.on_device(lse)
+        for t, like, what in ((O, Q, "O"), (dO, Q, "dO"), (dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
+            _shape(t, like.shape, what)
+        _lse_ok(lse, (Z, Hq, Sq))
+        n = int(lib().bsp_window_attention_workspace(Z, Hq, Sq, 1))
+        ws = c.workspace(n)
+        _check(lib().bsp_window_attention_backward(
+            W.handle, dt, *[ctypes.byref(_strided(t, _HEADS)) for t in (Q, K, V, O, dO)], _ptr(lse),
+            *[ctypes.byref(_strided(t, _HEADS)) for t in (dQ, dK, dV)], Z, Hq, Hkv, Sq, Sk, D, float(scale), _ptr(ws),
+            n, c.ptr), "bsp_window_attention_backward")
+    return dQ, dK, dV
+
+
+def _taken(t):
+    """t itself when the kernels take its strides, else a contiguous copy."""
+    e = 16 // t.element_size()
+    ok = t.data_ptr() % 16 == 0 and (t.shape[-1] <= 1 or t.stride(-1) == 1) and \
+        all(n <= 1 or (s > 0 and s % e == 0) for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+class _WindowAttention(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, V, W, scale):
+        Q, K, V = _taken(Q), _taken(K), _taken(V)
+        O, lse = bsp_window_attention(W, Q, K, V, scale=scale)
+        ctx.save_for_backward(Q, K, V, O, lse)
+        ctx.W, ctx.scale = W, scale
+        return O
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dO):
+        Q, K, V, O, lse = ctx.saved_tensors
+        dQ, dK, dV = bsp_window_attention_backward(ctx.W, Q, K, V, O, _taken(dO), lse, scale=ctx.scale)
+        return dQ, dK, dV, None, None
+
+
+def window_attention(W: Window, Q, K, V, scale: float):
+    """Differentiable bsp_window_attention (torch autograd); tensors whose
+    strides the kernels do not take are copied.  To capture a backward pass
+    into a CUDA graph, warm it up on the capturing side stream and keep no
+    other graph of the same leaves alive, as torch.cuda.graph asks."""
+    return _WindowAttention.apply(Q, K, V, W, float(scale))
+
+
+def _paged_sizes(rows, heads, K_cache, V_cache, q_start, kv_len, table):
+    if rows.dim() != 3 or K_cache.dim() != 4:
+        raise ValueError("token rows must be [T, heads, D], caches [n_pages, Hkv, page, D]")
+    T, H, D = rows.shape
+    n_pages, Hkv, page = K_cache.shape[:3]
+    _shape(K_cache, (n_pages, Hkv, page, D), "K_cache")
+    _shape(V_cache, (n_pages, Hkv, page, D), "V_cache")
+    if table.dim() != 2 or table.shape[1] < 1:
+        raise ValueError("table must be [n_seq, max_pages]")
+    n_seq = table.shape[0]
+    _shape(q_start, (n_seq + 1,), "q_start")
+    _shape(kv_len, (n_seq,), "kv_len")
+    for t in (q_start, kv_len, table):
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("q_start, kv_len and table must be contiguous int32 tensors")
+    if heads == "kv" and H != Hkv:
+        raise ValueError("new rows must have the cache's heads")
+    if Hkv < 1 or H % Hkv:
+        raise ValueError("the query heads must be a multiple of the KV heads")
+    return T, n_seq, table.shape[1], n_pages, page, H, Hkv, D
+
+
+def bsp_paged_append(W: Window, K, V, K_cache, V_cache, q_start, kv_len, table, stream=None):
+    """Write the new tokens' K and V rows [T, Hkv, D] to their slots of the
+    caches [n_pages, Hkv, page, D] (any strides; a permuted
+    [n_pages, page, Hkv, D] tensor serves too).  q_start int32 [n_seq + 1],
+    kv_len int32 [n_seq] (lengths with the new tokens), table int32
+    [n_seq, max_pages]."""
+    T, n_seq, max_pages, n_pages, page, _, Hkv, D = _paged_sizes(K, "kv", K_cache, V_cache, q_start, kv_len, table)
+    _shape(V, K.shape, "V")
+    with _Call(W, stream) as c:
+        dt = c.dtype(K, V, K_cache, V_cache)
+        c.on_device(q_start, kv_len, table)
+        _check(lib().bsp_paged_append(W.handle, dt, *[ctypes.byref(_strided(t, _ROWS)) for t in (K, V)],
+                                      *[ctypes.byref(_strided(t, _HEADS)) for t in (K_cache, V_cache)], _ptr(q_start),
+                                      _ptr(kv_len), _ptr(table), T, n_seq, max_pages, n_pages, page, Hkv, D, c.ptr),
+               "bsp_paged_append")
+
+
+def bsp_paged_attention(W: Window, Q, K_cache, V_cache, q_start, kv_len, table, O=None, lse=None, scale: float = 1.0,
+                        stream=None):
+    """Attention of a ragged batch of new tokens Q [T, Hq, D] over the caches,
+    which hold their own keys already: (O, lse fp32 [T, Hq])."""
+    T, n_seq, max_pages, n_pages, page, Hq, Hkv, D = _paged_sizes(Q, "q", K_cache, V_cache, q_start, kv_len, table)
+    with _Call(W, stream) as c:
+        if O is None:
+            O = torch.empty((T, Hq, D), dtype=Q.dtype, device=Q.device)
+        if lse is None:
+            lse = torch.empty((T, Hq), dtype=torch.float32, device=Q.device)
+        dt = c.dtype(Q, K_cache, V_cache, O)
+        c.on_device(lse, q_start, kv_len, table)
+        _shape(O, Q.shape, "O")
+        _lse_ok(lse, (T, Hq))
+        n = int(lib().bsp_paged_attention_workspace())
+        ws = c.workspace(n)
+        _check(lib().bsp_paged_attention(W.handle, dt, ctypes.byref(_strided(Q, _ROWS)),
+                                         *[ctypes.byref(_strided(t, _HEADS)) for t in (K_cache, V_cache)],
+                                         ctypes.byref(_strided(O, _ROWS)), _ptr(lse), _ptr(q_start), _ptr(kv_len),
+                                         _ptr(table), T, n_seq, max_pages, n_pages, page, Hq, Hkv, D, float(scale),
+                                         _ptr(ws), n, c.ptr), "bsp_paged_attention")
+    return O, lse

@@ -1,0 +1,54 @@
+// Host-side declarations of the windowed attention operators.
+#pragma once
+
+#include "bsp_internal.h"
+#include "window.cuh"
+
+struct bsp_window_s {
+    int window = 0, sinks = 0;  // as given (window 0: no limit)
+    int device = -1;
+    int* status = nullptr;      // device status word
+};
+
+namespace bsp {
+namespace win {
+
+// One call's tensors and sizes, checked.
+struct Call {
+    int dtype, D;
+    float scale;
+    View Q, K, V, O, dO, dQ, dK, dV;
+    float* lse;
+    int64_t lz, lh, lt;  // strides of lse (batch entry, head, row)
+    float* delta;        // rows' dO . O, laid out as lse (backward)
+    Prob p;              // TQ and kshift set by the launcher
+    int Z;
+    // workspace: partial results of cut tiles
+    Cut* cuts;
+    float* slots;
+    cudaStream_t stream;
+};
+
+// Floats of one partial-result slot: the rows' raw output, running maxima and
+// sums (forward), or raw dQ; the keys' raw dK and dV (backward).
+constexpr int kSlotD = 128;
+constexpr size_t slot_floats(int rows) { return (size_t)rows * (kSlotD + 2); }
+constexpr size_t kv_slot_floats(int rows) { return (size_t)rows * kSlotD * 2; }
+// CTAs per SM of the CUDA-core kernels (64-row tiles) and the tensor-core ones
+// (128-row tiles); both need the same workspace
+constexpr int kSimtPerSm = 2, kSimtRows = 64, kTcRows = 128;
+
+int launch_forward_simt(Call& c);
+int launch_backward_simt(Call& c);
+int launch_forward_tc(Call& c);   // BSP_ERR_UNSUPPORTED: not a 16-bit type
+int launch_backward_tc(Call& c);
+int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
+                  const Prob& p, int D, cudaStream_t s);
+// delta = rowsum(dO .* O) per row
+int launch_delta(const Call& c);
+// joins the pieces of cut tiles: forward / dQ (rows of query tiles) and dK, dV
+int launch_join(const Call& c, int rows, int n_cta, bool is_dq);
+int launch_join_kv(const Call& c, const KProb& kp, int rows, int n_cta);
+
+}  // namespace win
+}  // namespace bsp
