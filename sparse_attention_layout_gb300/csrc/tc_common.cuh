@@ -158,6 +158,15 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
         : "memory");
 }
 
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
+                                            int32_t w, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+
 // Non-tensor bulk copies (contiguous bytes; 16-byte aligned addresses, size a
 // multiple of 16).
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -430,6 +439,12 @@ int make_tmap_2d_f32(CUtensorMap* map, const void* base, uint64_t rows, uint64_t
 // box [1][box1][box0], swizzle 128 / 64 / 32 bytes or 0 (none)
 int make_tmap_3d(CUtensorMap* map, const void* base, int is_bf16, uint64_t d0, uint64_t d1, uint64_t d2,
                  uint32_t box0, uint32_t box1, int swizzle_bytes = 128);
+// host: 4-D tiled tensor map of 2-byte elements, d0 contiguous, the other
+// dimensions of extents n and strides s (elements, multiples of 8), box
+// [1][box2][box1][64], 128-byte swizzle; columns past d0 and rows past an
+// extent read as 0
+int make_tmap_4d(CUtensorMap* map, const void* base, int is_bf16, uint64_t d0, const uint64_t (&n)[3],
+                 const uint64_t (&s)[3], uint32_t box1, uint32_t box2);
 // host: a row-major [rows][cols] matrix of 2-byte elements (cols a multiple of
 // 64) seen as [cols/64 panels][rows][64]: one box of box_panels panels x
 // box_rows rows lands panel after panel, 128-byte swizzled (else

@@ -1,11 +1,684 @@
-// Tensor-core paths of the windowed attention: none yet, every call takes the
-// CUDA-core kernels.
+// Windowed attention forward on tcgen05 tensor cores (bf16 / fp16 in, fp32
+// accumulate), over dense tensors or a paged cache: one pass over the visible
+// key tiles with a running maximum and sum per row.
+//
+// A tile is 128 rows -- consecutive tokens of one sequence times the query
+// heads that share a KV head -- against steps of 128 keys.  Persistent CTAs,
+// one per SM, each take an equal run of the launch's steps (window.cuh), so
+// that ragged batches, long histories and few rows load the SMs evenly; a
+// tile cut between CTAs leaves its raw output, maxima and sums for the join.
+//
+// Roles (512 threads):
+//   warps 0, 3  TMA producers of Q and K, and of V.  Dense: one copy per 64
+//               columns; pages: one per page and 64 columns, each by its own
+//               lane, the page numbers read a step ahead.  Only pages with a
+//               key that a row of the tile sees are touched.
+//   warp 1      one thread issues S[g % 3] = Q K^T (M = N = 128, K = D)
+//   warp 2      one thread issues O += P V, P from TMEM, in pieces of 16 keys:
+//               those no row of the tile sees are left out
+//   warps 4..7  epilogue: O / l of a finished tile to memory while the next
+//               tile's softmax runs
+//   warps 8..15 softmax: thread = row, each warpgroup one half of its 128 keys;
+//               half-row maxima are swapped through shared memory
+// TMEM columns: S buffers at 0, 128, 256, each step's P over its own scores;
+// O at 384.
+//
+// V rows that no query of the sequence sees but that share a piece of 16 keys
+// with visible ones (the tail of the last page, keys before every window) are
+// zeroed in shared memory before the product, since 0 * NaN is NaN.
+#include <type_traits>
+
+#include "common.cuh"
+#include "tc_common.cuh"
 #include "window.h"
 
 namespace bsp {
 namespace win {
+namespace {
 
-int launch_forward_tc(Call&) { return BSP_ERR_UNSUPPORTED; }
+using namespace tc;
+
+constexpr int kThreads = 512;
+// Registers per thread: producers and issuers give some of the launch's 128 to
+// the two softmax warpgroups; 80 + 128 + 152 + 152 = 4 * 128.
+constexpr uint32_t kRegsLaunch = 128, kRegsCtl = 80, kRegsEpi = 128, kRegsSoftmax = 152;
+static_assert(kRegsCtl + kRegsEpi + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "register split exceeds the launch allocation");
+// O is rescaled only when a row's maximum grew by more than 2^8 (log2 units);
+// P stays below 2^8 then, and O / l is exact either way.
+constexpr float kRescaleThreshold = 8.0f;
+
+template <int DP>
+struct Smem {
+    static constexpr int KP = DP / 64;
+    static constexpr int kTile = 128 * DP * 2;
+    static constexpr int QST = 2;
+    static constexpr int KVST = DP == 128 ? 2 : 3;  // at most 3: a stage is freed by a ring of 3 barriers
+    static constexpr int kQ = 0;
+    static constexpr int kK = kQ + QST * kTile;
+    static constexpr int kV = kK + KVST * kTile;
+    static constexpr int kEpi = kV + KVST * kTile;  // one 32 x 64 panel per epilogue warp
+    static constexpr int kBytes = kEpi + 4 * 4096;
+    static constexpr int kAlloc = kBytes + 1024;
+};
+
+struct Args {
+    Prob p;
+    View O;
+    float* lse;
+    int64_t lz, lh, lt;
+    int D;
+    float c2;  // scale * log2(e)
+    int min_share;
+    Cut* cuts;
+    float* slots;
+    uint64_t wait_ns;
+};
+
+// Visible keys of a tile's rows: j <= hi and (j >= lo or j < sinks).
+struct Keys {
+    int lo, hi, sinks;
+    __device__ __forceinline__ bool any(int a, int b) const { return a <= hi && (b >= lo || a < sinks); }
+};
+__device__ __forceinline__ Keys tile_keys(const Prob& p, const QTile& q) {
+    return Keys{window_low(q.a, p.window), q.b, p.sinks};
+}
+
+// A producer's place: the tile it is in and the next step.
+template <typename W>
+struct Cursor {
+    W walk;
+    Item it;
+    Span sp;
+    Keys keys;
+    int n;
+    bool live;
+    __device__ __forceinline__ Cursor(const Prob& p, const Start& st) : walk(p, st), n(0) { enter(p); }
+    __device__ __forceinline__ void enter(const Prob& p) {
+        live = walk.next(it);
+        n = 0;
+        if (live) {
+            const QTile q = p.qtile(it.g, it.tile);
+            sp = p.span(q);
+            keys = tile_keys(p, q);
+        }
+    }
+    __device__ __forceinline__ void step(const Prob& p) {
+        if (++n >= it.ns) enter(p);
+    }
+    __device__ __forceinline__ int kb() const { return sp.tile(it.s0 + n) << 7; }
+};
+
+template <typename T, int DP, bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args args) {
+    using SM = Smem<DP>;
+    constexpr int KP = SM::KP, QST = SM::QST, NST = SM::KVST;
+    constexpr uint32_t kTileBytes = SM::kTile;
+    constexpr uint32_t kIdescQK = idesc_f16(128, 128, std::is_same<T, __nv_bfloat16>::value, 0, 0);
+    constexpr uint32_t kIdescPV = idesc_f16(128, DP, std::is_same<T, __nv_bfloat16>::value, 0, 1);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    // K and V of step g sit in stage g % NST; S buffer g % 3 has s_full (Q K^T
+    // done, which also frees the step's K stage), p_full (P written) and
+    // pv_done (P V done, which frees the buffer and the V stage).
+    __shared__ uint64_t q_full[QST], q_empty[QST], k_full[NST], v_full[NST], v_land;
+    __shared__ uint64_t s_full[3], p_full[3], pv_done[3];
+    __shared__ uint64_t o_full, o_empty, l_full[2], l_empty[2];
+    __shared__ float lsum[2][2][128], lref[2][2][128];
+    __shared__ float xm[2][2][128];
+    __shared__ uint64_t x_full[2][4];
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    __shared__ uint32_t issued[5];  // K steps, Q tiles, V steps, Q K^T steps, P V steps: drained after an abort
+    __shared__ Start start;
+    __shared__ int64_t red[32];
+
+    const Prob& p = args.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Abort ab{&abort_flag, p.status, args.wait_ns};
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        for (int i = 0; i < 5; ++i) issued[i] = 0;
+        for (int i = 0; i < QST; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+        }
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&v_full[i], 1);
+        }
+        mbar_init(&v_land, 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&pv_done[i], 1);
+            mbar_init(&p_full[i], 8);
+        }
+        mbar_init(&o_full, 1);
+        mbar_init(&o_empty, 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&l_full[i], 8);
+            mbar_init(&l_empty[i], 4);
+            for (int q = 0; q < 4; ++q) mbar_init(&x_full[i][q], 2);
+        }
+        fence_barrier_init();
+        args.cuts[blockIdx.x].pieces = 0;
+    }
+    if (PAGED && blockIdx.x == 0)
+        for (int s = threadIdx.x; s < p.nseg; s += kThreads)
+            if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
+    if (warp == 1) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    locate<kThreads>(p, gridDim.x, args.min_share, reinterpret_cast<int*>(smem), red, &start);
+    fence_proxy_async_smem();  // locate's scratch is where the copies land next
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tS = tmem_base;
+    const uint32_t tO = tmem_base + 384;
+
+    if (warp < 4) {
+    regs_dec<kRegsCtl>();
+    if (warp == 0 || warp == 3) {
+        // ----------------------------------------------- TMA producers ----
+        const bool is_v = warp == 3;
+        const CUtensorMap* tm = is_v ? &tmV : &tmK;
+        if (lane == 0) {
+            if (!is_v) tma_prefetch_desc(&tmQ);
+            tma_prefetch_desc(tm);
+        }
+        uint32_t q_it = 0, g = 0, lands = 0;
+        const uint32_t q_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
+        const int pages = PAGED ? 128 >> p.page_shift : 1;  // copies per 64 columns
+        const int my_page = lane % pages, my_panel = lane / pages;
+        const uint32_t page_bytes = PAGED ? 128u << p.page_shift : 128u * 128u;
+        // this lane's page of the cursor's step: -1 hidden (not copied)
+        auto lookup = [&](const Cursor<Walk<Prob>>& c) {
+            const int a = c.kb() + (my_page << p.page_shift);
+            if (!c.keys.any(a, a + (1 << p.page_shift) - 1)) return -1;
+            return p.table[(int64_t)c.it.seg * p.max_pages + (a >> p.page_shift)];
+        };
+        auto wanted = [&](const Cursor<Walk<Prob>>& c) {
+            const int a = c.kb() + (my_page << p.page_shift);
+            return c.keys.any(a, a + (1 << p.page_shift) - 1);
+        };
+        Cursor<Walk<Prob>> cur(p, start);
+        int pg = 0;
+        if (PAGED && cur.live) pg = lookup(cur);
+        while (cur.live) {
+            const Item it = cur.it;
+            const int kb = cur.kb(), n = cur.n, hk = PAGED ? it.rep : it.rep % p.Hkv, z = PAGED ? 0 : it.rep / p.Hkv;
+            const int my_pg = pg;
+            const bool want = PAGED ? wanted(cur) && my_panel < KP : lane < KP;
+            const Keys keys = cur.keys;
+            // the next step's page number is on its way while this step waits
+            cur.step(p);
+            if (PAGED && cur.live) pg = lookup(cur);
+            if (PAGED && !__all_sync(0xffffffffu, !want || (unsigned)my_pg < (unsigned)p.n_pages)) {
+                if (lane == 0) ab.fail(BSP_ERR_DEVICE_CHECK);
+                break;
+            }
+            if (!is_v && n == 0) {
+                const uint32_t qs = q_it % QST;
+                bool ok = mbar_wait(&q_empty[qs], ((q_it / QST) & 1) ^ 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&q_full[qs], q_bytes);
+                    for (int c = 0; c < KP; ++c)
+                        tma_load_4d(smem_u32(smem + SM::kQ + qs * kTileBytes + c * 16384), &tmQ, c * 64, hk * p.G,
+                                    it.g.t0 + it.tile * p.TQ, z, &q_full[qs]);
+                }
+                ++q_it;
+            }
+            const uint32_t st = g % NST;
+            if (g >= NST) {
+                const uint32_t gp = g - NST;
+                uint64_t* freed = is_v ? &pv_done[gp % 3] : &s_full[gp % 3];
+                bool ok = mbar_wait(freed, (gp / 3) & 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
+            const uint32_t bytes = PAGED ? page_bytes * __popc(__ballot_sync(0xffffffffu, want)) : kTileBytes;
+            uint64_t* full = is_v ? &v_full[st] : &k_full[st];
+            // rows of this V tile that no query of the sequence sees
+            const int zlo = window_low(it.g.kvlen - it.g.qlen, p.window), zhi = it.g.kvlen - 1;
+            const bool scrub = is_v && bytes > 0 &&
+                               ((kb + 127 > zhi && PAGED) || (kb < zlo && !(kb + 127 < p.sinks)));
+            uint64_t* bar = scrub ? &v_land : full;
+            if (lane == 0) {
+                if (bytes) mbar_arrive_expect_tx(bar, bytes);
+                else mbar_arrive(bar);
+            }
+            __syncwarp();
+            const uint32_t base = smem_u32(smem + (is_v ? SM::kV : SM::kK) + st * kTileBytes);
+            if (want) {
+                if (PAGED)
+                    tma_load_4d(base + my_panel * 16384 + my_page * page_bytes, tm, my_panel * 64, 0, hk, my_pg, bar);
+                else
+                    tma_load_4d(base + lane * 16384, tm, lane * 64, kb, hk, z, bar);
+            }
+            if (scrub) {
+                bool ok = mbar_wait(&v_land, lands & 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    if (lane == 0) mbar_drain(&v_land, lands & 1, ab);
+                    break;
+                }
+                ++lands;
+                for (int r = lane; r < 128; r += 32) {
+                    const int j = kb + r, j16 = kb + (r & ~15);
+                    const bool used = j <= zhi && (j >= zlo || j < p.sinks);
+                    if (!used && keys.any(j16, j16 + 15))
+                        for (int c = 0; c < KP; ++c)
+                            for (int i = 0; i < 8; ++i)
+                                *reinterpret_cast<uint4*>(smem + SM::kV + st * kTileBytes + c * 16384 + r * 128 + i * 16) =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full);
+            }
+            ++g;
+        }
+        if (lane == 0) {
+            if (is_v) {
+                issued[2] = g;
+            } else {
+                issued[0] = g;
+                issued[1] = q_it;
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------- Q K^T issuer (one thread) ----
+        if (lane == 0) {
+            const uint64_t dq = smem_desc(smem_u32(smem + SM::kQ), 16, 1024, kSw128);
+            const uint64_t dk = smem_desc(smem_u32(smem + SM::kK), 16, 1024, kSw128);
+            uint32_t q_it = 0, g = 0;
+            Walk<Prob> walk(p, start);
+            Item it;
+            while (walk.next(it)) {
+                const uint32_t qs = q_it % QST;
+                if (!mbar_wait(&q_full[qs], (q_it / QST) & 1, ab)) goto qk_done;
+                for (int n = 0; n < it.ns; ++n, ++g) {
+                    const uint32_t st = g % NST, sb = g % 3;
+                    if (g >= 3 && !mbar_wait(&pv_done[sb], ((g - 3) / 3) & 1, ab)) goto qk_done;
+                    if (!mbar_wait(&k_full[st], (g / NST) & 1, ab)) goto qk_done;
+                    tc_fence_after();
+                    const uint64_t aq = dq + ((qs * kTileBytes) >> 4), bk = dk + ((st * kTileBytes) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        mma_f16(tS + sb * 128, aq + off, bk + off, kIdescQK, ks > 0 ? 1u : 0u);
+                    }
+                    mma_commit(&s_full[sb]);
+                    if (n == it.ns - 1) mma_commit(&q_empty[qs]);
+                }
+                ++q_it;
+            }
+        qk_done:
+            issued[3] = g;
+        }
+    } else if (warp == 2) {
+        // --------------------------------------------- P V issuer (one thread) ----
+        if (lane == 0) {
+            const uint64_t dv = smem_desc(smem_u32(smem + SM::kV), 128 * 128, 1024, kSw128);
+            uint32_t g = 0, tc = 0;
+            Walk<Prob> walk(p, start);
+            Item it;
+            while (walk.next(it)) {
+                const QTile q = p.qtile(it.g, it.tile);
+                const Span sp = p.span(q);
+                const Keys keys = tile_keys(p, q);
+                if (tc > 0 && !mbar_wait(&o_empty, (tc - 1) & 1, ab)) goto pv_done_label;
+                uint32_t acc = 0;
+                for (int n = 0; n < it.ns; ++n, ++g) {
+                    const uint32_t st = g % NST, sb = g % 3;
+                    const int kb = sp.tile(it.s0 + n) << 7;
+                    if (!mbar_wait(&p_full[sb], (g / 3) & 1, ab)) goto pv_done_label;
+                    if (!mbar_wait(&v_full[st], (g / NST) & 1, ab)) goto pv_done_label;
+                    tc_fence_after();
+                    const uint64_t bv = dv + ((st * kTileBytes) >> 4);
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        if (keys.any(kb + ks * 16, kb + ks * 16 + 15)) {
+                            mma_f16_tmem_a(tO, tS + sb * 128 + ks * 8, bv + ((ks * 2048) >> 4), kIdescPV, acc);
+                            acc = 1;
+                        }
+                    mma_commit(&pv_done[sb]);
+                }
+                mma_commit(&o_full);
+                ++tc;
+            }
+        pv_done_label:
+            issued[4] = g;
+        }
+    }
+    } else if (warp < 8) {
+        if constexpr (kRegsEpi < kRegsLaunch) regs_dec<kRegsEpi>();
+        // ---------------------------------------------------- epilogue ----
+        const int quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        uint8_t* stage = smem + SM::kEpi + quad * 4096;
+        const uint32_t inv_g = 65536u / p.G + 1;  // r / G = r * inv_g >> 16 for r < 128
+        uint32_t tc = 0;
+        Walk<Prob> walk(p, start);
+        Item it;
+        while (walk.next(it)) {
+            const QTile q = p.qtile(it.g, it.tile);
+            const int rows = q.nt * p.G;
+            const int hk = PAGED ? it.rep : it.rep % p.Hkv, z = PAGED ? 0 : it.rep / p.Hkv;
+            const int t0 = it.g.t0 + q.tok0;
+            const uint32_t lb = tc & 1;
+            bool ok = mbar_wait(&l_full[lb], (tc >> 1) & 1, ab);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            const float m0 = lref[lb][0][row], m1 = lref[lb][1][row];
+            const float l0 = lsum[lb][0][row], l1 = lsum[lb][1][row];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&l_empty[lb]);
+            const float mf = fmaxf(m0, m1);
+            const float lt = mf == -INFINITY ? 0.f : l0 * ex2_approx(m0 - mf) + l1 * ex2_approx(m1 - mf);
+            const bool seen = lt > 0.f;
+            const float inv = seen ? 1.0f / lt : 0.f;
+            ok = mbar_wait(&o_full, tc & 1, ab);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            ++tc;
+            if (quad * 32 >= rows) {  // no live row in this quadrant
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty);
+                continue;
+            }
+            if (!it.whole()) {
+                // a piece: raw O (relative to mf), mf and the sum, for the join
+                float* slot = args.slots + (size_t)it.slot() * slot_floats(kTcRows);
+                float* orow = slot + (size_t)row * kSlotD;
+#pragma unroll 1
+                for (int c = 0; c < DP / 32; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32_sync(tO + lane_base + c * 32, r);
+                    if (row < rows) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            *reinterpret_cast<uint4*>(orow + c * 32 + 4 * k) =
+                                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&o_empty);
+                if (row < rows) {
+                    slot[kTcRows * kSlotD + row] = mf;
+                    slot[kTcRows * kSlotD + kTcRows + row] = lt;
+                }
+                if (threadIdx.x == 128 && it.s0 == 0) write_cut(args.cuts, it, start);
+                continue;
+            }
+            if (args.lse && row < rows) {
+                const int t = (row * inv_g) >> 16, h = row - t * p.G;
+                args.lse[z * args.lz + (hk * p.G + h) * args.lh + (t0 + t) * args.lt] =
+                    seen ? (mf + log2f(lt)) * kLn2 : -INFINITY;
+            }
+            // every column of O is read out of TMEM before the accumulator is
+            // handed to the next tile; then 64 columns at a time pass through
+            // the warp's staging panel, so that 8 lanes write 128 contiguous
+            // bytes of a row
+            uint32_t pk[KP][32];
+#pragma unroll
+            for (int c = 0; c < KP; ++c) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t r[32];
+                    tmem_ld32_sync(tO + lane_base + c * 64 + h * 32, r);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k)
+                        pk[c][h * 16 + k] = seen ? Pack2<T>::pack(__uint_as_float(r[2 * k]) * inv,
+                                                                  __uint_as_float(r[2 * k + 1]) * inv)
+                                                 : 0u;
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty);
+#pragma unroll
+            for (int c = 0; c < KP; ++c) {
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                        make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2], pk[c][4 * j + 3]);
+                __syncwarp();
+                const int j = lane & 7, col = c * 64 + j * 8;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = i * 4 + (lane >> 3), r = quad * 32 + rr;
+                    const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((j ^ (rr & 7)) << 4));
+                    if (r < rows && col < args.D) {
+                        const int t = (r * inv_g) >> 16, h = r - t * p.G;
+                        T* dst = static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
+                                 (int64_t)(t0 + t) * args.O.s[2] + col;
+                        *reinterpret_cast<uint4*>(dst) = v;
+                    }
+                }
+            }
+        }
+    } else {
+        regs_inc<kRegsSoftmax>();
+        // ---------------------------------------------------- softmax ----
+        const int wg = (warp - 8) >> 2, quad = warp & 3;
+        const int row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t inv_g = 65536u / p.G + 1;
+        uint32_t g = 0, tc = 0, xg = 0;  // xg: half-row exchanges so far
+        auto max64 = [](const float (&v)[64]) {
+            float m8[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m8[k] = fmax3(v[k], v[k + 8], v[k + 16]);
+#pragma unroll
+            for (int c = 24; c < 64; c += 16)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], v[c + k], c + 8 + k < 64 ? v[c + 8 + k] : v[c + k]);
+            return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
+        };
+        auto exp64 = [&](const float (&v)[64], float msub, uint32_t (&pk)[32]) {
+            const float2 c2v = make_float2(args.c2, args.c2), nm = make_float2(-msub, -msub);
+            float2 rs4[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rs4[k] = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const float2 y = __ffma2_rn(make_float2(v[2 * c], v[2 * c + 1]), c2v, nm);
+                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                rs4[c & 3] = __fadd2_rn(rs4[c & 3], e);
+                pk[c] = Pack2<T>::pack(e.x, e.y);
+            }
+            const float2 r2 = __fadd2_rn(__fadd2_rn(rs4[0], rs4[1]), __fadd2_rn(rs4[2], rs4[3]));
+            return r2.x + r2.y;
+        };
+        Walk<Prob> walk(p, start);
+        Item it;
+        while (walk.next(it)) {
+            const QTile q = p.qtile(it.g, it.tile);
+            const Span sp = p.span(q);
+            const int rows = q.nt * p.G;
+            const bool idle = quad * 32 >= rows;  // no live row in this warp's lanes
+            const int pos = row < rows ? q.a + (int)((row * inv_g) >> 16) : -1;
+            const int low = pos - p.window + 1;
+            float l = 0.f, m = -INFINITY;
+            for (int n = 0; n < it.ns; ++n, ++g) {
+                const uint32_t sb = g % 3;
+                const int kb = (sp.tile(it.s0 + n) << 7) + wg * 64;  // first key of this half
+                bool ok = mbar_wait(&s_full[sb], (g / 3) & 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
+                if (idle) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&p_full[sb]);
+                    continue;
+                }
+                tc_fence_after();
+                const uint32_t srow = tS + sb * 128 + lane_base;
+                const uint32_t xb = xg & 1, xph = (xg >> 1) & 1;
+                ++xg;
+                // visible keys of this half: bits [0, hi) minus [0, lo) plus [0, sk)
+                const int hi = imin(imax(pos - kb + 1, 0), 64), lo = imin(imax(low - kb, 0), 64);
+                const int sk = imin(imax(p.sinks - kb, 0), 64);
+                const bool all = hi == 64 && (lo == 0 || sk == 64);
+                const bool none = hi == 0 || (lo >= hi && sk == 0);
+                const bool skip = __all_sync(0xffffffffu, none);
+                float x[64];
+                float mx = -INFINITY;
+                if (!skip) {
+                    tmem_ld64_sync(srow + wg * 64, srow + wg * 64 + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
+                    if (!__all_sync(0xffffffffu, all)) {
+                        auto below = [](int c) { return c >= 64 ? ~0ull : (1ull << c) - 1; };
+                        const unsigned long long vis = below(hi) & (~below(lo) | below(sk));
+                        const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            x[j] = (v0 >> j) & 1 ? x[j] : -INFINITY;
+                            x[j + 32] = (v1 >> j) & 1 ? x[j + 32] : -INFINITY;
+                        }
+                    }
+                    mx = max64(x);
+                }
+                xm[xb][wg][row] = mx;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&x_full[xb][quad]);
+                ok = mbar_wait(&x_full[xb][quad], xph, ab);
+                if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
+                tc_fence_after();
+                const float mrow = fmaxf(mx, xm[xb][wg ^ 1][row]);
+                const float m_new = fmaxf(m, mrow * args.c2);
+                const bool need = m_new > m + kRescaleThreshold;  // also true for the first finite max
+                const float mnext = need ? m_new : m;
+                const float msub = (mnext == -INFINITY) ? 0.f : mnext;
+                uint32_t pk[32];
+                float rs = 0.f;
+                if (!skip) {
+                    rs = exp64(x, msub, pk);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) pk[k] = 0u;
+                }
+                tmem_st32_sync(srow + wg * 32, pk);
+                if (n > 0 && __any_sync(0xffffffffu, need)) {
+                    ok = mbar_wait(&pv_done[(g - 1) % 3], ((g - 1) / 3) & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
+                    tc_fence_after();
+                    const float alpha = need ? (m == -INFINITY ? 0.f : ex2_approx(m - mnext)) : 1.f;
+#pragma unroll
+                    for (int cc = 0; cc < DP / 64; ++cc) {
+                        uint32_t r[32];
+                        const uint32_t ta = tO + lane_base + wg * (DP / 2) + cc * 32;
+                        tmem_ld32_sync(ta, r);
+#pragma unroll
+                        for (int k = 0; k < 32; k += 2) {
+                            const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])),
+                                                        make_float2(alpha, alpha));
+                            r[k] = __float_as_uint(v.x);
+                            r[k + 1] = __float_as_uint(v.y);
+                        }
+                        tmem_st32_sync(ta, r);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[sb]);
+                l = (m == -INFINITY ? 0.f : l * ex2_approx(m - msub)) + rs;
+                m = mnext;
+            }
+            {
+                const uint32_t lb = tc & 1;
+                if (tc >= 2) {
+                    bool ok = mbar_wait(&l_empty[lb], ((tc - 2) >> 1) & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
+                }
+                lsum[lb][wg][row] = m == -INFINITY ? 0.f : l;
+                lref[lb][wg][row] = m;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&l_full[lb]);
+                ++tc;
+            }
+        }
+    softmax_done:;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (abort_flag) {
+        // the copies and products issued before the stop land before the CTA
+        // lets go of its shared memory and TMEM
+        if (threadIdx.x == 0) {
+            mbar_drain_ring(k_full, NST, issued[0], ab);
+            mbar_drain_ring(q_full, QST, issued[1], ab);
+            mbar_drain_ring(v_full, NST, issued[2], ab);
+            if (issued[3]) mbar_drain(&s_full[(issued[3] - 1) % 3], ((issued[3] - 1) / 3) & 1, ab);
+            if (issued[4]) mbar_drain(&pv_done[(issued[4] - 1) % 3], ((issued[4] - 1) / 3) & 1, ab);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+uint64_t extent(int64_t n) { return n > 0 ? (uint64_t)n : 1; }
+
+template <typename T, int DP, bool PAGED>
+int launch(Call& c) {
+    const int is_bf16 = std::is_same<T, __nv_bfloat16>::value;
+    const Prob& p = c.p;
+    CUtensorMap mq, mk, mv;
+    const uint64_t tokens = PAGED ? p.T : p.Sq, z = PAGED ? 1 : c.Z;
+    const uint64_t qn[3] = {(uint64_t)p.Hq, tokens, z};
+    const uint64_t qs[3] = {(uint64_t)c.Q.s[1], (uint64_t)c.Q.s[2], (uint64_t)c.Q.s[0]};
+    const uint64_t kn[3] = {PAGED ? 1ull << p.page_shift : extent(p.Sk), (uint64_t)p.Hkv,
+                            PAGED ? (uint64_t)p.n_pages : (uint64_t)c.Z};
+    const uint32_t krows = PAGED ? 1u << p.page_shift : 128u;
+    auto kv = [&](CUtensorMap* m, const View& v) {
+        const uint64_t s[3] = {(uint64_t)v.s[2], (uint64_t)v.s[1], (uint64_t)v.s[0]};
+        return make_tmap_4d(m, v.ptr, is_bf16, c.D, kn, s, krows, 1);
+    };
+    int rc = make_tmap_4d(&mq, c.Q.ptr, is_bf16, c.D, qn, qs, p.G, p.TQ);
+    if (!rc) rc = kv(&mk, c.K);
+    if (!rc) rc = kv(&mv, c.V);
+    if (rc) return rc;
+    auto kern = window_tc_kernel<T, DP, PAGED>;
+    constexpr int smem = Smem<DP>::kAlloc;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BSP_ERR_CUDA;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return BSP_ERR_CUDA;
+    // the register split at kernel start needs the full launch allocation
+    if ((uint32_t)fa.numRegs != kRegsLaunch) return BSP_ERR_UNSUPPORTED;
+    const int grid = sm_count();
+    Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, 2, c.cuts, c.slots, kDefaultWaitNs};
+    kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a);
+    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
+    return launch_join(c, kTcRows, grid, false);
+}
+
+template <typename T>
+int by_shape(Call& c) {
+    if (c.p.paged) return c.D <= 64 ? launch<T, 64, true>(c) : launch<T, 128, true>(c);
+    return c.D <= 64 ? launch<T, 64, false>(c) : launch<T, 128, false>(c);
+}
+
+}  // namespace
+
+int launch_forward_tc(Call& c) {
+    if (c.dtype == BSP_F32) return BSP_ERR_UNSUPPORTED;
+    // one new token per sequence (as far as the host can know): a tile is one
+    // token's heads; else as many tokens as fill 128 rows
+    c.p.kshift = 7;
+    c.p.TQ = c.p.paged && c.p.T <= c.p.nseg ? 1 : kTcRows / c.p.G;
+    return c.dtype == BSP_BF16 ? by_shape<__nv_bfloat16>(c) : by_shape<__half>(c);
+}
+
 int launch_backward_tc(Call&) { return BSP_ERR_UNSUPPORTED; }
 
 }  // namespace win

@@ -75,6 +75,20 @@ int make_tmap_3d(CUtensorMap* map, const void* base, int is_bf16, uint64_t d0, u
     return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_UNSUPPORTED;
 }
 
+int make_tmap_4d(CUtensorMap* map, const void* base, int is_bf16, uint64_t d0, const uint64_t (&n)[3],
+                 const uint64_t (&s)[3], uint32_t box1, uint32_t box2) {
+    auto fn = encode_fn();
+    if (!fn) return BSP_ERR_CUDA;
+    const cuuint64_t dims[4] = {d0, n[0], n[1], n[2]};
+    const cuuint64_t strides[3] = {s[0] * 2, s[1] * 2, s[2] * 2};
+    const cuuint32_t box[4] = {64, box1, box2, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    CUresult r = fn(map, is_bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                    const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? BSP_OK : BSP_ERR_UNSUPPORTED;
+}
+
 int make_tmap_panels(CUtensorMap* map, const void* base, int is_bf16, uint64_t rows, uint64_t cols,
                      uint32_t box_rows, uint32_t box_panels) {
     auto fn = encode_fn();
