@@ -455,7 +455,7 @@ int bsp_window_status(bsp_window_t w, void* stream);
  * row), K, V: (z, KV head, row), Sq and Sk rows; the queries are the last Sq
  * positions, query i at p = Sk - Sq + i (negative: sees nothing).  lse: DEVICE
  * float [Z][Hq][Sq], each row's ln sum exp of its visible scaled scores, or
- * NULL.  Workspace: bsp_window_attention_workspace(Z, Hq, Sq, 0) bytes. */
+ * NULL.  Workspace: bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 0) bytes. */
 int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K,
                          const bsp_tensor_t* V, const bsp_tensor_t* O, float* lse, int Z, int Hq, int Hkv, int Sq,
                          int Sk, int D, float scale, void* workspace, size_t workspace_bytes, void* stream);
@@ -465,13 +465,13 @@ int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const
  * dS = P .* (dO V^T - rowsum(dO .* O)),
  *     dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K,
  * dK and dV summed over the query heads that share the KV head.  Workspace:
- * bsp_window_attention_workspace(Z, Hq, Sq, 1) bytes. */
+ * bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1) bytes. */
 int bsp_window_attention_backward(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K,
                                   const bsp_tensor_t* V, const bsp_tensor_t* O, const bsp_tensor_t* dO,
                                   const float* lse, const bsp_tensor_t* dQ, const bsp_tensor_t* dK,
                                   const bsp_tensor_t* dV, int Z, int Hq, int Hkv, int Sq, int Sk, int D, float scale,
                                   void* workspace, size_t workspace_bytes, void* stream);
-size_t bsp_window_attention_workspace(int Z, int Hq, int Sq, int backward);
+size_t bsp_window_attention_workspace(int Z, int Hq, int Hkv, int Sq, int backward);
 
 /* Paged cache.  K_cache, V_cache: (page, KV head, slot), n_pages pages of
  * `page` slots (16, 32, 64 or 128).  table: DEVICE int32 [n_seq][max_pages],

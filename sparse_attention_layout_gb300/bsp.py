@@ -95,7 +95,7 @@ def lib():
         L.bsp_window_attention_backward.argtypes = [P, i32, T, T, T, T, T, P, T, T, T] + [i32] * 6 + [f32, P, sz, P]
         L.bsp_paged_append.argtypes = [P, i32, T, T, T, T, P, P, P] + [i32] * 7 + [P]
         L.bsp_paged_attention.argtypes = [P, i32, T, T, T, T, P, P, P, P] + [i32] * 8 + [f32, P, sz, P]
-        L.bsp_window_attention_workspace.argtypes = [i32, i32, i32, i32]
+        L.bsp_window_attention_workspace.argtypes = [i32] * 5
         L.bsp_window_attention_workspace.restype = sz
         L.bsp_paged_attention_workspace.argtypes = []
         L.bsp_paged_attention_workspace.restype = sz
@@ -658,7 +658,7 @@ def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.
         c.on_device(lse)
         _shape(O, Q.shape, "O")
         _lse_ok(lse, (Z, Hq, Sq))
-        n = int(lib().bsp_window_attention_workspace(Z, Hq, Sq, 0))
+        n = int(lib().bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 0))
         ws = c.workspace(n)
         _check(lib().bsp_window_attention(W.handle, dt, *[ctypes.byref(_strided(t, _HEADS)) for t in (Q, K, V, O)],
                                           _ptr(lse), Z, Hq, Hkv, Sq, Sk, D, float(scale), _ptr(ws), n, c.ptr),
@@ -680,7 +680,7 @@ def bsp_window_attention_backward(W: Window, Q, K, V, O, dO, lse, dQ=None, dK=No
         for t, like, what in ((O, Q, "O"), (dO, Q, "dO"), (dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
             _shape(t, like.shape, what)
         _lse_ok(lse, (Z, Hq, Sq))
-        n = int(lib().bsp_window_attention_workspace(Z, Hq, Sq, 1))
+        n = int(lib().bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1))
         ws = c.workspace(n)
         _check(lib().bsp_window_attention_backward(
             W.handle, dt, *[ctypes.byref(_strided(t, _HEADS)) for t in (Q, K, V, O, dO)], _ptr(lse),

@@ -26,23 +26,12 @@
 // V rows that no query of the sequence sees but that share a piece of 16 keys
 // with visible ones (the tail of the last page, keys before every window) are
 // zeroed in shared memory before the product, since 0 * NaN is NaN.
-#include <type_traits>
-
-#include "common.cuh"
-#include "tc_common.cuh"
-#include "window.h"
+#include "tc_window.cuh"
 
 namespace bsp {
 namespace win {
 namespace {
 
-using namespace tc;
-
-constexpr int kThreads = 512;
-// Registers per thread: producers and issuers give some of the launch's 128 to
-// the two softmax warpgroups; 80 + 128 + 152 + 152 = 4 * 128.
-constexpr uint32_t kRegsLaunch = 128, kRegsCtl = 80, kRegsEpi = 128, kRegsSoftmax = 152;
-static_assert(kRegsCtl + kRegsEpi + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "register split exceeds the launch allocation");
 // O is rescaled only when a row's maximum grew by more than 2^8 (log2 units);
 // P stays below 2^8 then, and O / l is exact either way.
 constexpr float kRescaleThreshold = 8.0f;
@@ -73,15 +62,6 @@ struct Args {
     float* slots;
     uint64_t wait_ns;
 };
-
-// Visible keys of a tile's rows: j <= hi and (j >= lo or j < sinks).
-struct Keys {
-    int lo, hi, sinks;
-    __device__ __forceinline__ bool any(int a, int b) const { return a <= hi && (b >= lo || a < sinks); }
-};
-__device__ __forceinline__ Keys tile_keys(const Prob& p, const QTile& q) {
-    return Keys{window_low(q.a, p.window), q.b, p.sinks};
-}
 
 // A producer's place: the tile it is in and the next step.
 template <typename W>
@@ -444,26 +424,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty);
 #pragma unroll
-            for (int c = 0; c < KP; ++c) {
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                        make_uint4(pk[c][4 * j], pk[c][4 * j + 1], pk[c][4 * j + 2], pk[c][4 * j + 3]);
-                __syncwarp();
-                const int j = lane & 7, col = c * 64 + j * 8;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int rr = i * 4 + (lane >> 3), r = quad * 32 + rr;
-                    const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * 128 + ((j ^ (rr & 7)) << 4));
-                    if (r < rows && col < args.D) {
-                        const int t = (r * inv_g) >> 16, h = r - t * p.G;
-                        T* dst = static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
-                                 (int64_t)(t0 + t) * args.O.s[2] + col;
-                        *reinterpret_cast<uint4*>(dst) = v;
-                    }
-                }
-            }
+            for (int c = 0; c < KP; ++c)
+                store_panel<T>(stage, pk[c], lane, args.D - c * 64, [&](int i) -> T* {
+                    const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
+                    if (r >= rows) return nullptr;
+                    return static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
+                           (int64_t)(t0 + t) * args.O.s[2] + c * 64;
+                });
         }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -522,26 +489,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t srow = tS + sb * 128 + lane_base;
                 const uint32_t xb = xg & 1, xph = (xg >> 1) & 1;
                 ++xg;
-                // visible keys of this half: bits [0, hi) minus [0, lo) plus [0, sk)
-                const int hi = imin(imax(pos - kb + 1, 0), 64), lo = imin(imax(low - kb, 0), 64);
-                const int sk = imin(imax(p.sinks - kb, 0), 64);
-                const bool all = hi == 64 && (lo == 0 || sk == 64);
-                const bool none = hi == 0 || (lo >= hi && sk == 0);
-                const bool skip = __all_sync(0xffffffffu, none);
+                const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
+                const bool skip = __all_sync(0xffffffffu, vis == 0);
                 float x[64];
                 float mx = -INFINITY;
                 if (!skip) {
                     tmem_ld64_sync(srow + wg * 64, srow + wg * 64 + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
-                    if (!__all_sync(0xffffffffu, all)) {
-                        auto below = [](int c) { return c >= 64 ? ~0ull : (1ull << c) - 1; };
-                        const unsigned long long vis = below(hi) & (~below(lo) | below(sk));
-                        const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            x[j] = (v0 >> j) & 1 ? x[j] : -INFINITY;
-                            x[j + 32] = (v1 >> j) & 1 ? x[j + 32] : -INFINITY;
-                        }
-                    }
+                    if (!__all_sync(0xffffffffu, vis == ~0ull)) hide(x, vis);
                     mx = max64(x);
                 }
                 xm[xb][wg][row] = mx;
@@ -627,34 +581,19 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
 }
 
-uint64_t extent(int64_t n) { return n > 0 ? (uint64_t)n : 1; }
-
 template <typename T, int DP, bool PAGED>
 int launch(Call& c) {
     const int is_bf16 = std::is_same<T, __nv_bfloat16>::value;
     const Prob& p = c.p;
     CUtensorMap mq, mk, mv;
-    const uint64_t tokens = PAGED ? p.T : p.Sq, z = PAGED ? 1 : c.Z;
-    const uint64_t qn[3] = {(uint64_t)p.Hq, tokens, z};
-    const uint64_t qs[3] = {(uint64_t)c.Q.s[1], (uint64_t)c.Q.s[2], (uint64_t)c.Q.s[0]};
-    const uint64_t kn[3] = {PAGED ? 1ull << p.page_shift : extent(p.Sk), (uint64_t)p.Hkv,
-                            PAGED ? (uint64_t)p.n_pages : (uint64_t)c.Z};
-    const uint32_t krows = PAGED ? 1u << p.page_shift : 128u;
-    auto kv = [&](CUtensorMap* m, const View& v) {
-        const uint64_t s[3] = {(uint64_t)v.s[2], (uint64_t)v.s[1], (uint64_t)v.s[0]};
-        return make_tmap_4d(m, v.ptr, is_bf16, c.D, kn, s, krows, 1);
-    };
-    int rc = make_tmap_4d(&mq, c.Q.ptr, is_bf16, c.D, qn, qs, p.G, p.TQ);
-    if (!rc) rc = kv(&mk, c.K);
-    if (!rc) rc = kv(&mv, c.V);
+    const int rows = PAGED ? 1 << p.page_shift : 128;
+    int rc = query_map(&mq, c.Q, c, is_bf16, PAGED ? p.T : p.Sq);
+    if (!rc) rc = key_map(&mk, c.K, c, is_bf16, rows);
+    if (!rc) rc = key_map(&mv, c.V, c, is_bf16, rows);
     if (rc) return rc;
     auto kern = window_tc_kernel<T, DP, PAGED>;
     constexpr int smem = Smem<DP>::kAlloc;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BSP_ERR_CUDA;
-    cudaFuncAttributes fa;
-    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return BSP_ERR_CUDA;
-    // the register split at kernel start needs the full launch allocation
-    if ((uint32_t)fa.numRegs != kRegsLaunch) return BSP_ERR_UNSUPPORTED;
+    if ((rc = prepare_kernel(kern, smem))) return rc;
     const int grid = sm_count();
     Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, 2, c.cuts, c.slots, kDefaultWaitNs};
     kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a);
@@ -678,8 +617,6 @@ int launch_forward_tc(Call& c) {
     c.p.TQ = c.p.paged && c.p.T <= c.p.nseg ? 1 : kTcRows / c.p.G;
     return c.dtype == BSP_BF16 ? by_shape<__nv_bfloat16>(c) : by_shape<__half>(c);
 }
-
-int launch_backward_tc(Call&) { return BSP_ERR_UNSUPPORTED; }
 
 }  // namespace win
 }  // namespace bsp

@@ -1,0 +1,98 @@
+// Shared by the tensor-core kernels of the windowed attention.
+#pragma once
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "tc_common.cuh"
+#include "window.h"
+
+namespace bsp {
+namespace win {
+
+using namespace tc;
+
+constexpr int kThreads = 512;
+// Registers per thread: producers and issuers give some of the launch's 128 to
+// the two softmax warpgroups; 80 + 128 + 152 + 152 = 4 * 128.
+constexpr uint32_t kRegsLaunch = 128, kRegsCtl = 80, kRegsEpi = 128, kRegsSoftmax = 152;
+static_assert(kRegsCtl + kRegsEpi + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "register split exceeds the launch allocation");
+
+// Visible keys of a tile's rows: j <= hi and (j >= lo or j < sinks).
+struct Keys {
+    int lo, hi, sinks;
+    __device__ __forceinline__ bool any(int a, int b) const { return a <= hi && (b >= lo || a < sinks); }
+};
+__device__ __forceinline__ Keys tile_keys(const Prob& p, const QTile& q) {
+    return Keys{window_low(q.a, p.window), q.b, p.sinks};
+}
+
+// bits [0, c) of 64
+__device__ __forceinline__ unsigned long long below(int c) { return c >= 64 ? ~0ull : (1ull << c) - 1; }
+
+// x[j] = -inf where bit j is clear
+__device__ __forceinline__ void hide(float (&x)[64], unsigned long long vis) {
+    const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        x[j] = (v0 >> j) & 1 ? x[j] : -INFINITY;
+        x[j + 32] = (v1 >> j) & 1 ? x[j + 32] : -INFINITY;
+    }
+}
+
+// Visible keys of one row at position pos among the 64 that start at kb.
+__device__ __forceinline__ unsigned long long row_keys(int pos, int low, int sinks, int kb) {
+    const int hi = imin(imax(pos - kb + 1, 0), 64), lo = imin(imax(low - kb, 0), 64);
+    const int sk = imin(imax(sinks - kb, 0), 64);
+    return below(hi) & (~below(lo) | below(sk));
+}
+
+// 64 columns of a warp's 32 rows (thread = row, two values per register) to
+// memory through the warp's 4 KB staging panel (16-byte piece j of row r at
+// j ^ (r % 8), so neither side meets a bank twice): 8 lanes then write 128
+// contiguous bytes of a row.  dst(r): where row r's 64 columns begin, or null.
+template <typename T, typename F>
+__device__ __forceinline__ void store_panel(uint8_t* stage, const uint32_t (&pk)[32], int lane, int cols, F dst) {
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+            make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
+    __syncwarp();
+    const int j = lane & 7;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int r = i * 4 + (lane >> 3);
+        const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ (r & 7)) << 4));
+        T* p = dst(r);
+        if (p && j * 8 < cols) *reinterpret_cast<uint4*>(p + j * 8) = v;
+    }
+}
+
+// Tensor maps of a call: rows of the query heads that share a KV head (box of
+// G heads x TQ tokens), and of keys (box of `rows` rows or slots).
+inline int query_map(CUtensorMap* m, const View& v, const Call& c, int is_bf16, int64_t tokens) {
+    const uint64_t n[3] = {(uint64_t)c.p.Hq, (uint64_t)tokens, (uint64_t)c.Z};
+    const uint64_t s[3] = {(uint64_t)v.s[1], (uint64_t)v.s[2], (uint64_t)v.s[0]};
+    return make_tmap_4d(m, v.ptr, is_bf16, c.D, n, s, c.p.G, c.p.TQ);
+}
+inline int key_map(CUtensorMap* m, const View& v, const Call& c, int is_bf16, int rows) {
+    const Prob& p = c.p;
+    const uint64_t n[3] = {p.paged ? 1ull << p.page_shift : (uint64_t)imax(p.Sk, 1), (uint64_t)p.Hkv,
+                           p.paged ? (uint64_t)p.n_pages : (uint64_t)c.Z};
+    const uint64_t s[3] = {(uint64_t)v.s[2], (uint64_t)v.s[1], (uint64_t)v.s[0]};
+    return make_tmap_4d(m, v.ptr, is_bf16, c.D, n, s, rows, 1);
+}
+
+// Launch preparation: the shared memory limit, and the register count that the
+// split at kernel start divides.
+template <typename K>
+int prepare_kernel(K kern, int smem) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BSP_ERR_CUDA;
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return BSP_ERR_CUDA;
+    return (uint32_t)fa.numRegs == kRegsLaunch ? BSP_OK : BSP_ERR_UNSUPPORTED;
+}
+
+}  // namespace win
+}  // namespace bsp

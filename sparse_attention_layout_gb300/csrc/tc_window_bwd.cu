@@ -1,0 +1,729 @@
+// Gradient of the windowed attention on tcgen05 tensor cores (bf16 / fp16 in,
+// fp32 accumulate).  With P = exp(scale Q K^T - lse) on the visible pairs and
+// dS = P (dO V^T - dO . O):
+//     dq kernel   per query tile, over the key tiles it sees:   dQ = scale dS K
+//     dkv kernel  per key tile, over the query tiles that see it (all heads of
+//                 the group in a tile's rows): dV = P^T dO, dK = scale dS^T Q
+// S and dP are computed in both, seven products where five would do with dQ
+// added up in memory: no atomics, so the same inputs give the same bits, and no
+// fp32 dQ in memory.  The dkv kernel forms the transposes S^T = K Q^T and
+// dP^T = V dO^T (thread = key), so that P^T and dS^T are tensor-memory operands
+// of the two products that contract over the rows, and nothing but the 16-bit
+// tiles passes through shared memory.  Persistent CTAs take equal runs of
+// steps, as in the forward; the tile with the sinks, which every query sees, is
+// cut among many.
+#include "tc_window.cuh"
+
+namespace bsp {
+namespace win {
+namespace {
+
+struct Args {
+    Prob p;
+    View dQ, dK, dV;
+    const float* stats;  // per query tile: -lse log2(e) of 128 rows, then dO . O
+    int D, ntiles;
+    float scale, c2;     // c2 = scale * log2(e)
+    int min_share;
+    Cut* cuts;
+    float* slots;
+    uint64_t wait_ns;
+};
+
+template <int DP>
+struct Smem {
+    static constexpr int KP = DP / 64;
+    static constexpr int kTile = 128 * DP * 2;
+    // dq: Q, dO one stage, K, V two; dkv: K, V one stage, Q, dO two
+    static constexpr int kA = 0, kB = kTile;            // the tile's own operands
+    static constexpr int kX = 2 * kTile, kY = 4 * kTile;  // the steps' operands, two stages each
+    static constexpr int kEpi = 6 * kTile;              // one 32 x 64 panel per epilogue warp
+    static constexpr int kStats = kEpi + 4 * 4096;      // dkv: two stages of 256 floats
+    static constexpr int kBytes = kStats + 2 * 1024;
+    static constexpr int kAlloc = kBytes + 1024;
+};
+
+// 128 x DP accumulator columns of a warp's 32 rows to the partial-result slot
+// (raw fp32) or, scaled and rounded, to memory; arrives on `empty` as soon as
+// the columns are in registers.
+template <typename T, int DP, typename F>
+__device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, int row, bool live, float* slot_rows,
+                                      float scale, int D, uint8_t* stage, F dst) {
+    if (slot_rows) {
+#pragma unroll 1
+        for (int c = 0; c < DP / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld32_sync(tacc + c * 32, r);
+            if (live) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    *reinterpret_cast<uint4*>(slot_rows + (size_t)row * kSlotD + c * 32 + 4 * k) =
+                        make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+            }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty);
+        return;
+    }
+    uint32_t pk[DP / 64][32];
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t r[32];
+            tmem_ld32_sync(tacc + c * 64 + h * 32, r);
+#pragma unroll
+            for (int k = 0; k < 16; ++k)
+                pk[c][h * 16 + k] =
+                    Pack2<T>::pack(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
+        }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty);
+#pragma unroll
+    for (int c = 0; c < DP / 64; ++c)
+        store_panel<T>(stage, pk[c], lane, D - c * 64, [&](int i) -> T* {
+            T* p = dst(i);
+            return p ? p + c * 64 : nullptr;
+        });
+}
+
+// ------------------------------------------------------------------- dQ ----
+// Roles: warps 0, 3 copy Q and K, dO and V; warp 1 issues S = Q K^T into
+// buffer g % 2 and dP = dO V^T; warp 2 issues dQ += dS K (dS from TMEM over its
+// own scores, K as it lies); warps 4..7 write dQ; warps 8..15 form dS, thread =
+// row, each warpgroup half of the step's keys.
+// TMEM columns: S 0 and 128, dP 256, dQ 384.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+             const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+             const __grid_constant__ Args args) {
+    using SM = Smem<DP>;
+    constexpr int KP = SM::KP;
+    constexpr uint32_t kTile = SM::kTile;
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kIdescS = idesc_f16(128, 128, kBf, 0, 0), kIdescD = idesc_f16(128, DP, kBf, 0, 1);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t a_full, a_free, k_full[2], v_full[2], s_full[2], dp_full, dp_free, ds_full[2], dq_done[2];
+    __shared__ uint64_t acc_full, acc_empty;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    __shared__ uint32_t issued[4];  // tiles and K steps, V steps, score steps, dQ steps
+    __shared__ uint32_t issued_a;
+    __shared__ Start start;
+    __shared__ int64_t red[32];
+
+    const Prob& p = args.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Abort ab{&abort_flag, p.status, args.wait_ns};
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        issued_a = 0;
+        for (int i = 0; i < 4; ++i) issued[i] = 0;
+        mbar_init(&a_full, 2);  // Q with K's producer, dO with V's
+        mbar_init(&a_free, 1);
+        mbar_init(&dp_full, 1);
+        mbar_init(&dp_free, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&v_full[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&ds_full[i], 8);
+            mbar_init(&dq_done[i], 1);
+        }
+        mbar_init(&acc_full, 1);
+        mbar_init(&acc_empty, 4);
+        fence_barrier_init();
+        args.cuts[blockIdx.x].pieces = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    locate<kThreads>(p, gridDim.x, args.min_share, reinterpret_cast<int*>(smem), red, &start);
+    tc_fence_after();
+    const uint32_t tS = tmem_base, tP = tmem_base + 256, tA = tmem_base + 384;
+
+    if (warp < 4) {
+        regs_dec<kRegsCtl>();
+        if ((warp == 0 || warp == 3) && lane == 0) {
+            // ------------------------------------------------ producers ----
+            const bool is_v = warp == 3;
+            const CUtensorMap* tm = is_v ? &tmV : &tmK;
+            const CUtensorMap* ta = is_v ? &tmG : &tmQ;
+            tma_prefetch_desc(tm);
+            tma_prefetch_desc(ta);
+            const uint32_t a_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
+            uint32_t g = 0, tiles = 0;
+            Walk<Prob> walk(p, start);
+            Item it;
+            while (walk.next(it)) {
+                const Span sp = p.span(p.qtile(it.g, it.tile));
+                const int hk = it.rep % p.Hkv, z = it.rep / p.Hkv;
+                // the previous tile's S and dP products have read Q and dO
+                if (tiles > 0 && !mbar_wait(&a_free, (tiles - 1) & 1, ab)) goto load_done;
+                mbar_arrive_expect_tx(&a_full, a_bytes);
+                for (int c = 0; c < KP; ++c)
+                    tma_load_4d(smem_u32(smem + (is_v ? SM::kB : SM::kA) + c * 16384), ta, c * 64, hk * p.G,
+                                it.tile * p.TQ, z, &a_full);
+                ++tiles;
+                for (int n = 0; n < it.ns; ++n, ++g) {
+                    const uint32_t st = g & 1;
+                    // K of step g - 2 is free after its dQ product, V after its dP product,
+                    // which the same step's dS follows
+                    if (g >= 2 && !mbar_wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto load_done;
+                    uint64_t* full = is_v ? &v_full[st] : &k_full[st];
+                    mbar_arrive_expect_tx(full, kTile);
+                    const int kb = sp.tile(it.s0 + n) << 7;
+                    for (int c = 0; c < KP; ++c)
+                        tma_load_4d(smem_u32(smem + (is_v ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64, kb, hk,
+                                    z, full);
+                }
+            }
+        load_done:
+            issued[is_v] = g;
+            atomicMax(&issued_a, tiles);
+        } else if (warp == 1 && lane == 0) {
+            // ------------------------------------ S and dP products ----
+            const uint64_t da = smem_desc(smem_u32(smem + SM::kA), 16, 1024, kSw128);
+            const uint64_t db = smem_desc(smem_u32(smem + SM::kB), 16, 1024, kSw128);
+            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 16, 1024, kSw128);
+            const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 16, 1024, kSw128);
+            uint32_t g = 0, tiles = 0;
+            Walk<Prob> walk(p, start);
+            Item it;
+            while (walk.next(it)) {
+                if (!mbar_wait(&a_full, tiles & 1, ab)) goto score_done;
+                for (int n = 0; n < it.ns; ++n, ++g) {
+                    const uint32_t st = g & 1;
+                    if (g >= 2 && !mbar_wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto score_done;
+                    if (!mbar_wait(&k_full[st], (g >> 1) & 1, ab)) goto score_done;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        mma_f16(tS + st * 128, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
+                    }
+                    mma_commit(&s_full[st]);
+                    if (g >= 1 && !mbar_wait(&dp_free, (g - 1) & 1, ab)) {
+                        ++g;
+                        goto score_done;
+                    }
+                    if (!mbar_wait(&v_full[st], (g >> 1) & 1, ab)) {
+                        ++g;
+                        goto score_done;
+                    }
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
+                    }
+                    mma_commit(&dp_full);
+                    if (n == it.ns - 1) mma_commit(&a_free);
+                }
+                ++tiles;
+            }
+        score_done:
+            issued[2] = g;
+        } else if (warp == 2 && lane == 0) {
+            // ------------------------------------------- dQ product ----
+            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 128 * 128, 1024, kSw128);
+            uint32_t g = 0, tiles = 0;
+            Walk<Prob> walk(p, start);
+            Item it;
+            while (walk.next(it)) {
+                if (tiles > 0 && !mbar_wait(&acc_empty, (tiles - 1) & 1, ab)) goto dq_end;
+                for (int n = 0; n < it.ns; ++n, ++g) {
+                    const uint32_t st = g & 1;
+                    if (!mbar_wait(&ds_full[st], (g >> 1) & 1, ab)) goto dq_end;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_f16_tmem_a(tA, tS + st * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
+                                       dx + ((st * kTile + ks * 2048) >> 4), kIdescD, ks > 0 || n > 0);
+                    mma_commit(&dq_done[st]);
+                }
+                mma_commit(&acc_full);
+                ++tiles;
+            }
+        dq_end:
+            issued[3] = g;
+        }
+    } else if (warp < 8) {
+        // ---------------------------------------------------- epilogue ----
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t inv_g = 65536u / p.G + 1;  // r / G = r * inv_g >> 16 for r < 128
+        uint32_t tiles = 0;
+        Walk<Prob> walk(p, start);
+        Item it;
+        while (walk.next(it)) {
+            const QTile q = p.qtile(it.g, it.tile);
+            const int rows = q.nt * p.G, hk = it.rep % p.Hkv, z = it.rep / p.Hkv;
+            const bool ok = mbar_wait(&acc_full, tiles & 1, ab);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            ++tiles;
+            float* slot = it.whole() ? nullptr : args.slots + (size_t)it.slot() * slot_floats(kTcRows);
+            drain<T, DP>(tA + lane_base, &acc_empty, lane, row, row < rows, slot, args.scale, args.D,
+                         smem + SM::kEpi + quad * 4096, [&](int i) -> T* {
+                             const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
+                             if (r >= rows) return nullptr;
+                             return static_cast<T*>(args.dQ.ptr) + z * args.dQ.s[0] + (hk * p.G + h) * args.dQ.s[1] +
+                                    (int64_t)(q.tok0 + t) * args.dQ.s[2];
+                         });
+            if (threadIdx.x == 128 && it.s0 == 0 && !it.whole()) write_cut(args.cuts, it, start);
+        }
+    } else {
+        regs_inc<kRegsSoftmax>();
+        // -------------------------------------------------------- dS ----
+        const int wg = (warp - 8) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        const uint32_t inv_g = 65536u / p.G + 1;
+        uint32_t g = 0;
+        Walk<Prob> walk(p, start), ahead(p, start);
+        Item it, nx;
+        // the next tile's statistics are on their way while this tile's steps run
+        float nl = 0.f, dl = 0.f;
+        auto fetch = [&]() {
+            if (!ahead.next(nx)) return;
+            const float* s = args.stats + ((int64_t)nx.rep * args.ntiles + nx.tile) * 256;
+            nl = s[row];
+            dl = s[128 + row];
+        };
+        fetch();
+        while (walk.next(it)) {
+            const float nlse = nl, delta = dl;
+            fetch();
+            const QTile q = p.qtile(it.g, it.tile);
+            const Span sp = p.span(q);
+            const int rows = q.nt * p.G;
+            const int pos = row < rows ? q.a + (int)((row * inv_g) >> 16) : -1, low = pos - p.window + 1;
+            for (int n = 0; n < it.ns; ++n, ++g) {
+                const uint32_t st = g & 1;
+                const int kb = (sp.tile(it.s0 + n) << 7) + wg * 64;
+                const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
+                bool ok = mbar_wait(&s_full[st], (g >> 1) & 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) goto ds_done;
+                tc_fence_after();
+                const uint32_t ts = tS + st * 128 + lane_base + wg * 64;
+                float x[64];
+                tmem_ld64_sync(ts, ts + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
+                if (!__all_sync(0xffffffffu, vis == ~0ull)) hide(x, vis);
+#pragma unroll
+                for (int j = 0; j < 64; j += 2) {
+                    const float2 y = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(args.c2, args.c2),
+                                                make_float2(nlse, nlse));
+                    x[j] = ex2_approx(y.x);
+                    x[j + 1] = ex2_approx(y.y);
+                }
+                ok = mbar_wait(&dp_full, g & 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) goto ds_done;
+                tc_fence_after();
+                uint32_t pk[32];
+                const float2 nd = make_float2(-delta, -delta);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32_sync(tP + lane_base + wg * 64 + c * 32, r);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const float2 d = __fadd2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), nd);
+                        const float2 e = __fmul2_rn(d, make_float2(x[c * 32 + j], x[c * 32 + j + 1]));
+                        pk[c * 16 + j / 2] = Pack2<T>::pack(e.x, e.y);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&dp_free);
+                tmem_st32_sync(ts, pk);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ds_full[st]);
+            }
+        }
+    ds_done:;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (abort_flag) {
+        if (threadIdx.x == 0) {
+            mbar_drain_ring(k_full, 2, issued[0], ab);
+            mbar_drain_ring(v_full, 2, issued[1], ab);
+            if (issued_a) mbar_drain(&a_full, (issued_a - 1) & 1, ab);
+            if (issued[2]) mbar_drain(&s_full[(issued[2] - 1) & 1], ((issued[2] - 1) >> 1) & 1, ab);
+            if (issued[2]) mbar_drain(&dp_full, (issued[2] - 1) & 1, ab);
+            if (issued[3]) mbar_drain(&dq_done[(issued[3] - 1) & 1], ((issued[3] - 1) >> 1) & 1, ab);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+// --------------------------------------------------------------- dK, dV ----
+// Roles: warps 0, 3 copy K and Q (with the query tile's statistics), V and dO;
+// warp 1 issues S^T = K Q^T and dP^T = V dO^T; warp 2 issues dV += P^T dO and
+// dK += dS^T Q; warps 4..7 write dV and dK; warps 8..15 form P^T and dS^T,
+// thread = key, each warpgroup half of the step's rows.
+// TMEM columns: S^T 0 (P^T over it), dP^T 128 (dS^T over it), dV 256, dK 384.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
+              const __grid_constant__ Args args, const __grid_constant__ KProb kp) {
+    using SM = Smem<DP>;
+    constexpr int KP = SM::KP;
+    constexpr uint32_t kTile = SM::kTile;
+    constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kIdescS = idesc_f16(128, 128, kBf, 0, 0), kIdescD = idesc_f16(128, DP, kBf, 0, 1);
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t a_full, a_free, q_full[2], g_full[2], s_full, p_full, dv_done, dp_full, ds_full, dk_done[2];
+    __shared__ uint64_t dv_full, dv_empty, dk_full, dk_empty;
+    __shared__ uint32_t tmem_base;
+    __shared__ int abort_flag;
+    __shared__ uint32_t issued[5];  // Q steps, dO steps, S^T steps, dP^T steps, dV steps
+    __shared__ uint32_t issued_a, issued_k;
+    __shared__ Start start;
+    __shared__ int64_t red[32];
+
+    const Prob& p = args.p;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    Abort ab{&abort_flag, p.status, args.wait_ns};
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        issued_a = issued_k = 0;
+        for (int i = 0; i < 5; ++i) issued[i] = 0;
+        mbar_init(&a_full, 2);  // K with Q's producer, V with dO's
+        mbar_init(&a_free, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&g_full[i], 1);
+            mbar_init(&dk_done[i], 1);
+        }
+        mbar_init(&s_full, 1);
+        mbar_init(&p_full, 8);
+        mbar_init(&dv_done, 1);
+        mbar_init(&dp_full, 1);
+        mbar_init(&ds_full, 8);
+        mbar_init(&dv_full, 1);
+        mbar_init(&dk_full, 1);
+        mbar_init(&dv_empty, 4);
+        mbar_init(&dk_empty, 4);
+        fence_barrier_init();
+        args.cuts[blockIdx.x].pieces = 0;
+    }
+    if (warp == 1) {
+        tmem_alloc(&tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    locate<kThreads>(kp, gridDim.x, args.min_share, reinterpret_cast<int*>(smem), red, &start);
+    // rows past TQ * G, which no copy writes, enter the products over the rows
+    // with P = 0: they must not hold NaN
+    for (int i = threadIdx.x; i < 4 * (int)kTile / 16; i += kThreads)
+        *reinterpret_cast<uint4*>(smem + SM::kX + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tS = tmem_base, tP = tmem_base + 128, tV = tmem_base + 256, tK = tmem_base + 384;
+
+    if (warp < 4) {
+        regs_dec<kRegsCtl>();
+        if ((warp == 0 || warp == 3) && lane == 0) {
+            // ------------------------------------------------ producers ----
+            const bool is_g = warp == 3;
+            const CUtensorMap* ta = is_g ? &tmV : &tmK;
+            const CUtensorMap* tm = is_g ? &tmG : &tmQ;
+            tma_prefetch_desc(ta);
+            tma_prefetch_desc(tm);
+            const uint32_t bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
+            uint32_t g = 0, tiles = 0;
+            Walk<KProb> walk(kp, start);
+            Item it;
+            while (walk.next(it)) {
+                const int hk = it.rep % p.Hkv, z = it.rep / p.Hkv;
+                int first, nq;
+                kp.qrange(it.tile, &first, &nq);
+                first += it.s0;
+                // the previous tile's score products have read K and V
+                if (tiles > 0 && !mbar_wait(&a_free, (tiles - 1) & 1, ab)) goto load_done;
+                mbar_arrive_expect_tx(&a_full, kTile);
+                for (int c = 0; c < KP; ++c)
+                    tma_load_4d(smem_u32(smem + (is_g ? SM::kB : SM::kA) + c * 16384), ta, c * 64, it.tile << 7, hk, z,
+                                &a_full);
+                ++tiles;
+                for (int n = 0; n < it.ns; ++n, ++g) {
+                    const uint32_t st = g & 1;
+                    if (g >= 2 && !mbar_wait(&dk_done[st], ((g - 2) >> 1) & 1, ab)) goto load_done;
+                    uint64_t* full = is_g ? &g_full[st] : &q_full[st];
+                    mbar_arrive_expect_tx(full, bytes + (is_g ? 0u : 1024u));
+                    for (int c = 0; c < KP; ++c)
+                        tma_load_4d(smem_u32(smem + (is_g ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64,
+                                    hk * p.G, (first + n) * p.TQ, z, full);
+                    if (!is_g)
+                        bulk_load(smem_u32(smem + SM::kStats + st * 1024),
+                                  args.stats + ((int64_t)it.rep * args.ntiles + first + n) * 256, 1024, full);
+                }
+            }
+        load_done:
+            issued[is_g] = g;
+            atomicMax(&issued_a, tiles);
+        } else if (warp == 1 && lane == 0) {
+            // --------------------------------- S^T and dP^T products ----
+            const uint64_t da = smem_desc(smem_u32(smem + SM::kA), 16, 1024, kSw128);
+            const uint64_t db = smem_desc(smem_u32(smem + SM::kB), 16, 1024, kSw128);
+            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 16, 1024, kSw128);
+            const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 16, 1024, kSw128);
+            uint32_t g = 0, gd = 0, tiles = 0;
+            Walk<KProb> walk(kp, start);
+            Item it;
+            while (walk.next(it)) {
+                if (!mbar_wait(&a_full, tiles & 1, ab)) goto score_done;
+                for (int n = 0; n < it.ns; ++n) {
+                    const uint32_t st = g & 1;
+                    if (g >= 1 && !mbar_wait(&dv_done, (g - 1) & 1, ab)) goto score_done;
+                    if (!mbar_wait(&q_full[st], (g >> 1) & 1, ab)) goto score_done;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        mma_f16(tS, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
+                    }
+                    mma_commit(&s_full);
+                    ++g;
+                    if (gd >= 1 && !mbar_wait(&dk_done[(gd - 1) & 1], ((gd - 1) >> 1) & 1, ab)) goto score_done;
+                    if (!mbar_wait(&g_full[st], (gd >> 1) & 1, ab)) goto score_done;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < DP / 16; ++ks) {
+                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
+                        mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
+                    }
+                    mma_commit(&dp_full);
+                    ++gd;
+                    if (n == it.ns - 1) mma_commit(&a_free);
+                }
+                ++tiles;
+            }
+        score_done:
+            issued[2] = g;
+            issued[3] = gd;
+        } else if (warp == 2 && lane == 0) {
+            // ----------------------------------- dV and dK products ----
+            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 128 * 128, 1024, kSw128);
+            const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 128 * 128, 1024, kSw128);
+            uint32_t g = 0, gk = 0, tiles = 0;
+            Walk<KProb> walk(kp, start);
+            Item it;
+            while (walk.next(it)) {
+                for (int n = 0; n < it.ns; ++n) {
+                    const uint32_t st = g & 1;
+                    if (n == 0 && tiles > 0 && !mbar_wait(&dv_empty, (tiles - 1) & 1, ab)) goto grad_done;
+                    if (!mbar_wait(&p_full, g & 1, ab)) goto grad_done;
+                    if (!mbar_wait(&g_full[st], (g >> 1) & 1, ab)) goto grad_done;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_f16_tmem_a(tV, tS + (ks >> 2) * 64 + (ks & 3) * 8, dy + ((st * kTile + ks * 2048) >> 4), kIdescD,
+                                       ks > 0 || n > 0);
+                    mma_commit(&dv_done);
+                    if (n == it.ns - 1) mma_commit(&dv_full);
+                    ++g;
+                    if (n == 0 && tiles > 0 && !mbar_wait(&dk_empty, (tiles - 1) & 1, ab)) goto grad_done;
+                    if (!mbar_wait(&ds_full, gk & 1, ab)) goto grad_done;
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_f16_tmem_a(tK, tP + (ks >> 2) * 64 + (ks & 3) * 8, dx + ((st * kTile + ks * 2048) >> 4), kIdescD,
+                                       ks > 0 || n > 0);
+                    mma_commit(&dk_done[st]);
+                    if (n == it.ns - 1) mma_commit(&dk_full);
+                    ++gk;
+                }
+                ++tiles;
+            }
+        grad_done:
+            issued[4] = g;
+            issued_k = gk;
+        }
+    } else if (warp < 8) {
+        // ---------------------------------------------------- epilogue ----
+        const int quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        uint8_t* stage = smem + SM::kEpi + quad * 4096;
+        uint32_t tiles = 0;
+        Walk<KProb> walk(kp, start);
+        Item it;
+        while (walk.next(it)) {
+            const int hk = it.rep % p.Hkv, z = it.rep / p.Hkv, kb = it.tile << 7;
+            float* slot = it.whole() ? nullptr : args.slots + (size_t)it.slot() * kv_slot_floats(kTcRows);
+            auto rows_of = [&](const View& v) {
+                return [&, z, hk, kb](int i) -> T* {
+                    const int j = kb + quad * 32 + i;
+                    if (j >= p.Sk) return nullptr;
+                    return static_cast<T*>(v.ptr) + z * v.s[0] + hk * v.s[1] + (int64_t)j * v.s[2];
+                };
+            };
+            bool ok = mbar_wait(&dv_full, tiles & 1, ab);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            drain<T, DP>(tV + lane_base, &dv_empty, lane, row, kb + row < p.Sk,
+                         slot ? slot + (size_t)kTcRows * kSlotD : nullptr, 1.0f, args.D, stage, rows_of(args.dV));
+            ok = mbar_wait(&dk_full, tiles & 1, ab);
+            if (!__all_sync(0xffffffffu, ok)) break;
+            tc_fence_after();
+            drain<T, DP>(tK + lane_base, &dk_empty, lane, row, kb + row < p.Sk, slot, args.scale, args.D, stage,
+                         rows_of(args.dK));
+            ++tiles;
+            if (threadIdx.x == 128 && it.s0 == 0 && !it.whole()) write_cut(args.cuts, it, start);
+        }
+    } else {
+        regs_inc<kRegsSoftmax>();
+        // ------------------------------------------------ P^T and dS^T ----
+        const int wg = (warp - 8) >> 2, quad = warp & 3, row = quad * 32 + lane;
+        const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        uint32_t g = 0;
+        Walk<KProb> walk(kp, start);
+        Item it;
+        while (walk.next(it)) {
+            int first, nq;
+            kp.qrange(it.tile, &first, &nq);
+            first += it.s0;
+            const int j = (it.tile << 7) + row;  // this thread's key
+            for (int n = 0; n < it.ns; ++n, ++g) {
+                const uint32_t st = g & 1;
+                // rows that see the key: tokens from the key's own to window - 1
+                // later ones (a sink: all later ones), G rows each
+                const int tok = p.Sk - p.Sq + (first + n) * p.TQ;  // position of row 0
+                const int c0 = imin(imax(j - tok, 0), 128) * p.G - wg * 64;
+                const int c1 = j < p.sinks ? 64 : imin(imax(j - tok + p.window, 0), 128) * p.G - wg * 64;
+                const unsigned long long vis = below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64));
+                const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 1024) + wg * 64;
+                bool ok = mbar_wait(&q_full[st], (g >> 1) & 1, ab);
+                ok = ok && mbar_wait(&s_full, g & 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) goto ds_done;
+                tc_fence_after();
+                float x[64];
+                tmem_ld64_sync(tS + lane_base + wg * 64, tS + lane_base + wg * 64 + 32,
+                               *reinterpret_cast<uint32_t(*)[64]>(x));
+                if (!__all_sync(0xffffffffu, vis == ~0ull)) hide(x, vis);
+                {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int i = 0; i < 64; i += 4) {
+                        const float4 nl = *reinterpret_cast<const float4*>(stats + i);
+                        const float2 c2v = make_float2(args.c2, args.c2);
+                        const float2 y0 = __ffma2_rn(make_float2(x[i], x[i + 1]), c2v, make_float2(nl.x, nl.y));
+                        const float2 y1 = __ffma2_rn(make_float2(x[i + 2], x[i + 3]), c2v, make_float2(nl.z, nl.w));
+                        x[i] = ex2_approx(y0.x);
+                        x[i + 1] = ex2_approx(y0.y);
+                        x[i + 2] = ex2_approx(y1.x);
+                        x[i + 3] = ex2_approx(y1.y);
+                        pk[i / 2] = Pack2<T>::pack(x[i], x[i + 1]);
+                        pk[i / 2 + 1] = Pack2<T>::pack(x[i + 2], x[i + 3]);
+                    }
+                    tmem_st32_sync(tS + lane_base + wg * 64, pk);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full);
+                ok = mbar_wait(&dp_full, g & 1, ab);
+                if (!__all_sync(0xffffffffu, ok)) goto ds_done;
+                tc_fence_after();
+                uint32_t pk[32];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    uint32_t r[32];
+                    tmem_ld32_sync(tP + lane_base + wg * 64 + c * 32, r);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 4) {
+                        const float4 dl = *reinterpret_cast<const float4*>(stats + 128 + c * 32 + i);
+                        const float2 d0 = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
+                                                     make_float2(-dl.x, -dl.y));
+                        const float2 d1 = __fadd2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
+                                                     make_float2(-dl.z, -dl.w));
+                        const float2 e0 = __fmul2_rn(d0, make_float2(x[c * 32 + i], x[c * 32 + i + 1]));
+                        const float2 e1 = __fmul2_rn(d1, make_float2(x[c * 32 + i + 2], x[c * 32 + i + 3]));
+                        pk[c * 16 + i / 2] = Pack2<T>::pack(e0.x, e0.y);
+                        pk[c * 16 + i / 2 + 1] = Pack2<T>::pack(e1.x, e1.y);
+                    }
+                }
+                tmem_st32_sync(tP + lane_base + wg * 64, pk);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ds_full);
+            }
+        }
+    ds_done:;
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (abort_flag) {
+        if (threadIdx.x == 0) {
+            mbar_drain_ring(q_full, 2, issued[0], ab);
+            mbar_drain_ring(g_full, 2, issued[1], ab);
+            if (issued_a) mbar_drain(&a_full, (issued_a - 1) & 1, ab);
+            if (issued[2]) mbar_drain(&s_full, (issued[2] - 1) & 1, ab);
+            if (issued[3]) mbar_drain(&dp_full, (issued[3] - 1) & 1, ab);
+            if (issued[4]) mbar_drain(&dv_done, (issued[4] - 1) & 1, ab);
+            if (issued_k) mbar_drain(&dk_done[(issued_k - 1) & 1], ((issued_k - 1) >> 1) & 1, ab);
+        }
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 512);
+    }
+}
+
+template <typename T, int DP>
+int launch(Call& c) {
+    const int is_bf16 = std::is_same<T, __nv_bfloat16>::value;
+    const Prob& p = c.p;
+    CUtensorMap mq, mk, mv, mg;
+    int rc = query_map(&mq, c.Q, c, is_bf16, p.Sq);
+    if (!rc) rc = query_map(&mg, c.dO, c, is_bf16, p.Sq);
+    if (!rc) rc = key_map(&mk, c.K, c, is_bf16, 128);
+    if (!rc) rc = key_map(&mv, c.V, c, is_bf16, 128);
+    if (rc) return rc;
+    constexpr int smem = Smem<DP>::kAlloc;
+    if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem))) return rc;
+    if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem))) return rc;
+    const int grid = sm_count();
+    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + p.TQ - 1) / p.TQ, c.scale, c.scale * kLog2e, 2, c.cuts, c.slots,
+           kDefaultWaitNs};
+    if ((rc = launch_tile_stats(c))) return rc;
+    dq_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a);
+    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
+    if ((rc = launch_join(c, kTcRows, grid, true))) return rc;
+    const KProb kp{1, p.rep, p.G, p.TQ, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
+    dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, kp);
+    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
+    return launch_join_kv(c, kp, kTcRows, grid);
+}
+
+}  // namespace
+
+int launch_backward_tc(Call& c) {
+    if (c.dtype == BSP_F32) return BSP_ERR_UNSUPPORTED;
+    c.p.kshift = 7;
+    c.p.TQ = kTcRows / c.p.G;
+    if (c.dtype == BSP_BF16) return c.D <= 64 ? launch<__nv_bfloat16, 64>(c) : launch<__nv_bfloat16, 128>(c);
+    return c.D <= 64 ? launch<__half, 64>(c) : launch<__half, 128>(c);
+}
+
+}  // namespace win
+}  // namespace bsp

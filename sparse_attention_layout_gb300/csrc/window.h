@@ -20,7 +20,9 @@ struct Call {
     View Q, K, V, O, dO, dQ, dK, dV;
     float* lse;
     int64_t lz, lh, lt;  // strides of lse (batch entry, head, row)
-    float* delta;        // rows' dO . O, laid out as lse (backward)
+    // backward: rows' dO . O, laid out as lse (CUDA cores), or per query tile
+    // -lse log2(e) and dO . O of its 128 rows (tensor cores)
+    float* stats;
     Prob p;              // TQ and kshift set by the launcher
     int Z;
     // workspace: partial results of cut tiles
@@ -44,8 +46,9 @@ int launch_forward_tc(Call& c);   // BSP_ERR_UNSUPPORTED: not a 16-bit type
 int launch_backward_tc(Call& c);
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
                   const Prob& p, int D, cudaStream_t s);
-// delta = rowsum(dO .* O) per row
+// stats = rowsum(dO .* O) per row; the same and the rows' -lse log2(e), per tile
 int launch_delta(const Call& c);
+int launch_tile_stats(const Call& c);
 // joins the pieces of cut tiles: forward / dQ (rows of query tiles) and dK, dV
 int launch_join(const Call& c, int rows, int n_cta, bool is_dq);
 int launch_join_kv(const Call& c, const KProb& kp, int rows, int n_cta);

@@ -70,7 +70,7 @@ int make_view(const bsp_tensor_t* t, int64_t n0, int64_t n1, int64_t n2, int D, 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace: one record per CTA, two partial-result slots per CTA, and for the
-// backward a float per query row.
+// backward two floats per row of a query tile.
 size_t cuts_bytes() { return round_up(sizeof(bsp::win::Cut) * bsp::win::kSimtPerSm * bsp::sm_count()); }
 size_t slots_bytes(bool backward) {
     const size_t rows = bsp::win::kTcRows;
@@ -170,10 +170,13 @@ extern "C" int bsp_window_status(bsp_window_t w, void* stream) {
     return word;
 }
 
-extern "C" size_t bsp_window_attention_workspace(int Z, int Hq, int Sq, int backward) {
-    if (Z < 0 || Hq < 1 || Sq < 0) return 0;
+extern "C" size_t bsp_window_attention_workspace(int Z, int Hq, int Hkv, int Sq, int backward) {
+    if (Z < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > kMaxGroup || Sq < 0) return 0;
     size_t n = cuts_bytes() + slots_bytes(backward != 0);
-    if (backward) n += round_up((size_t)Z * Hq * Sq * sizeof(float));
+    // two floats per row of each 128-row query tile (more than the one per row
+    // that the CUDA-core kernels keep)
+    const size_t tq = 128 / (Hq / Hkv);
+    if (backward) n += round_up((size_t)Z * Hkv * ((Sq + tq - 1) / tq) * 256 * sizeof(float));
     return n;
 }
 
@@ -196,7 +199,7 @@ extern "C" int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_
     }
     if ((rc = make_view(O, Z, Hq, Sq, D, elt, true, &c.O))) return rc;
     if ((uintptr_t)lse & 15u) return BSP_ERR_ALIGNMENT;
-    if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Sq, 0)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 0)))) return rc;
     if (Sk == 0) {  // no key at all: zeros and -inf, by the kernels' hidden step over Q's own rows
         c.K = c.V = View{Q->ptr, {D, D, D}};
     }
@@ -247,7 +250,7 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
         return rc;
     }
     if (Sk == 0) return zero_view(c.dQ, Z, Hq, Sq, (size_t)D * elt, elt, s);
-    if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Sq, 1)))) return rc;
+    if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1)))) return rc;
     c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
     c.lse = const_cast<float*>(lse);
     c.lz = (int64_t)Hq * Sq, c.lh = Sq, c.lt = 1;
@@ -255,9 +258,8 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
     char* ws = static_cast<char*>(workspace);
     c.cuts = reinterpret_cast<bsp::win::Cut*>(ws);
     c.slots = reinterpret_cast<float*>(ws + cuts_bytes());
-    c.delta = reinterpret_cast<float*>(ws + cuts_bytes() + slots_bytes(true));
+    c.stats = reinterpret_cast<float*>(ws + cuts_bytes() + slots_bytes(true));
     c.stream = s;
-    if ((rc = bsp::win::launch_delta(c))) return rc;
     if (!force_simt()) {
         rc = bsp::win::launch_backward_tc(c);
         if (rc != BSP_ERR_UNSUPPORTED) return rc;

@@ -143,6 +143,44 @@ __global__ void __launch_bounds__(256) delta_kernel(const View O, const View dO,
     }
 }
 
+// The same per query tile of 128 rows (row r: token r / G, head r % G, as the
+// tensor-core kernels lay them out): tile i's 128 values of -lse log2(e), then
+// its 128 of dO . O, so that one bulk copy brings a tile's statistics.  Rows
+// beyond the sequence and rows that see nothing get -inf: their P is then 0.
+template <typename T>
+__global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const View dO, const float* lse, float* stats,
+                                                         int64_t rows, int ntiles, int G, int TQ, int Hkv, int S, int D) {
+    constexpr int N = Vec16<T>::N;
+    const int sub = threadIdx.x & 7;
+    for (int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); i < rows; i += (int64_t)gridDim.x * 32) {
+        const int r = (int)(i & 127);
+        const int64_t tile = i >> 7, zh = tile / ntiles;
+        const int z = (int)(zh / Hkv), t = (int)(tile % ntiles) * TQ + r / G;
+        const int64_t h = zh % Hkv * G + r % G;
+        const bool live = r < TQ * G && t < S;
+        float x = 0.f;
+        if (live) {
+            const T* o = static_cast<const T*>(O.ptr) + z * O.s[0] + h * O.s[1] + t * O.s[2];
+            const T* g = static_cast<const T*>(dO.ptr) + z * dO.s[0] + h * dO.s[1] + t * dO.s[2];
+            for (int c = sub * N; c < D; c += 8 * N) {
+                float a[N], b[N];
+                Vec16<T>::load(o + c, a);
+                Vec16<T>::load(g + c, b);
+#pragma unroll
+                for (int k = 0; k < N; ++k) x = fmaf(a[k], b[k], x);
+            }
+        }
+        const unsigned group = 0xffu << (threadIdx.x & 24);  // the row's 8 lanes
+#pragma unroll
+        for (int k = 4; k; k >>= 1) x += __shfl_xor_sync(group, x, k);
+        if (sub == 0) {
+            const float l = live ? lse[(z * (int64_t)Hkv * G + h) * S + t] : -INFINITY;
+            stats[tile * 256 + r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+            stats[tile * 256 + 128 + r] = x;
+        }
+    }
+}
+
 // K and V rows of new tokens to their pages' slots: token t of sequence s goes
 // to position kv_len[s] - (new tokens of s) + its index.  A warp per token
 // finds the sequence by a 32-way search of q_start, then copies 16 bytes per
@@ -210,8 +248,18 @@ template <typename T>
 int delta_t(const Call& c) {
     const int64_t rows = (int64_t)c.Z * c.p.Hq * c.p.Sq;
     const int64_t blocks = (rows + 31) / 32, most = (int64_t)sm_count() * 16;
-    delta_kernel<T><<<(int)(blocks < most ? blocks : most), 256, 0, c.stream>>>(c.O, c.dO, c.delta, rows, c.p.Hq, c.p.Sq,
+    delta_kernel<T><<<(int)(blocks < most ? blocks : most), 256, 0, c.stream>>>(c.O, c.dO, c.stats, rows, c.p.Hq, c.p.Sq,
                                                                                  c.D);
+    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+}
+
+template <typename T>
+int tile_stats_t(const Call& c) {
+    const int ntiles = (c.p.Sq + c.p.TQ - 1) / c.p.TQ;
+    const int64_t rows = (int64_t)c.Z * c.p.Hkv * ntiles * 128;
+    const int64_t blocks = (rows + 31) / 32, most = (int64_t)sm_count() * 16;
+    tile_stats_kernel<T><<<(int)(blocks < most ? blocks : most), 256, 0, c.stream>>>(
+        c.O, c.dO, c.lse, c.stats, rows, ntiles, c.p.G, c.p.TQ, c.p.Hkv, c.p.Sq, c.D);
     return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
@@ -250,6 +298,10 @@ int launch_join_kv(const Call& c, const KProb& kp, int rows, int n_cta) {
 }
 
 int launch_delta(const Call& c) { BSP_WIN_TYPES(delta_t<float>(c), delta_t<__nv_bfloat16>(c), delta_t<__half>(c)) }
+
+int launch_tile_stats(const Call& c) {
+    BSP_WIN_TYPES(BSP_ERR_UNSUPPORTED, tile_stats_t<__nv_bfloat16>(c), tile_stats_t<__half>(c))
+}
 
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
                   const Prob& p, int D, cudaStream_t s) {

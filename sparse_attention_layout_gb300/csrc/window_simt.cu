@@ -485,7 +485,7 @@ Args make_args(const Call& c) {
     a.p.kshift = kShift;
     a.p.TQ = imin(R / c.p.G, imax(1, c.p.paged && c.p.T <= c.p.nseg ? 1 : R));
     a.Q = c.Q, a.K = c.K, a.V = c.V, a.O = c.O, a.dO = c.dO, a.dQ = c.dQ, a.dK = c.dK, a.dV = c.dV;
-    a.lse = c.lse, a.lz = c.lz, a.lh = c.lh, a.lt = c.lt, a.delta = c.delta;
+    a.lse = c.lse, a.lz = c.lz, a.lh = c.lh, a.lt = c.lt, a.delta = c.stats;
     a.D = c.D;
     a.scale = c.scale;
     a.c2 = c.scale * kLog2e;
@@ -520,7 +520,8 @@ int forward_t(Call& c, const Args& a, int grid) {
 template <typename T, int DP>
 int backward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
-    int rc = launch(dq_kernel<T, DP>, grid, tiles_bytes<DP>(4, 1), c.stream, a);
+    int rc = launch_delta(c);
+    if (!rc) rc = launch(dq_kernel<T, DP>, grid, tiles_bytes<DP>(4, 1), c.stream, a);
     if (!rc) rc = launch_join(c, R, grid, true);
     const KProb kp{1, c.p.rep, c.p.G, a.p.TQ, kShift, c.p.Hq, c.p.Hkv, c.p.Sq, c.p.Sk, c.p.window, c.p.sinks};
     if (!rc) rc = launch(dkv_kernel<T, DP>, grid, tiles_bytes<DP>(4, 2), c.stream, a, kp);

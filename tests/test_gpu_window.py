@@ -487,7 +487,7 @@ def test_refusals(bsp):
     # the C entry itself: workspace and alignment
     L = bsp.lib()
     t = [ctypes.byref(bsp._strided(a, (0, 1, 2))) for a in (*ok, x(1, 2, 8, 64))]
-    ws = torch.empty(int(L.bsp_window_attention_workspace(1, 2, 8, 0)), dtype=torch.uint8, device="cuda")
+    ws = torch.empty(int(L.bsp_window_attention_workspace(1, 2, 1, 8, 0)), dtype=torch.uint8, device="cuda")
 
     def call(ptr, n, lse=None, dtype=1):
         return L.bsp_window_attention(W.handle, dtype, *t, lse, 1, 2, 1, 8, 8, 64, 1.0, ctypes.c_void_p(ptr), n, None)
