@@ -63,31 +63,6 @@ struct Args {
     uint64_t wait_ns;
 };
 
-// A producer's place: the tile it is in and the next step.
-template <typename W>
-struct Cursor {
-    W walk;
-    Item it;
-    Span sp;
-    Keys keys;
-    int n;
-    bool live;
-    __device__ __forceinline__ Cursor(const Prob& p, const Start& st) : walk(p, st), n(0) { enter(p); }
-    __device__ __forceinline__ void enter(const Prob& p) {
-        live = walk.next(it);
-        n = 0;
-        if (live) {
-            const QTile q = p.qtile(it.g, it.tile);
-            sp = p.span(q);
-            keys = tile_keys(p, q);
-        }
-    }
-    __device__ __forceinline__ void step(const Prob& p) {
-        if (++n >= it.ns) enter(p);
-    }
-    __device__ __forceinline__ int kb() const { return sp.tile(it.s0 + n) << 7; }
-};
-
 template <typename T, int DP, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -114,6 +89,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     __shared__ uint32_t issued[5];  // K steps, Q tiles, V steps, Q K^T steps, P V steps: drained after an abort
     __shared__ Start start;
     __shared__ int64_t red[32];
+    __shared__ Ring ring;
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -143,6 +119,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             mbar_init(&l_empty[i], 4);
             for (int q = 0; q < 4; ++q) mbar_init(&x_full[i][q], 2);
         }
+        ring.init();
         fence_barrier_init();
         args.cuts[blockIdx.x].pieces = 0;
     }
@@ -154,7 +131,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tmem_relinquish();
     }
     tc_fence_before();
-    locate<kThreads>(p, gridDim.x, args.min_share, reinterpret_cast<int*>(smem), red, &start);
+    locate<kThreads>(p, args.min_share, reinterpret_cast<int*>(smem), red, &start);
     fence_proxy_async_smem();  // locate's scratch is where the copies land next
     __syncthreads();
     tc_fence_after();
@@ -165,109 +142,136 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     regs_dec<kRegsCtl>();
     if (warp == 0 || warp == 3) {
         // ----------------------------------------------- TMA producers ----
+        // warp 0 walks the share and hands the tiles out
         const bool is_v = warp == 3;
         const CUtensorMap* tm = is_v ? &tmV : &tmK;
         if (lane == 0) {
             if (!is_v) tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(tm);
         }
-        uint32_t q_it = 0, g = 0, lands = 0;
+        uint32_t i = 0, g = 0, lands = 0;
         const uint32_t q_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
         const int pages = PAGED ? 128 >> p.page_shift : 1;  // copies per 64 columns
         const int my_page = lane % pages, my_panel = lane / pages;
         const uint32_t page_bytes = PAGED ? 128u << p.page_shift : 128u * 128u;
-        // this lane's page of the cursor's step: -1 hidden (not copied)
-        auto lookup = [&](const Cursor<Walk<Prob>>& c) {
-            const int a = c.kb() + (my_page << p.page_shift);
-            if (!c.keys.any(a, a + (1 << p.page_shift) - 1)) return -1;
-            return p.table[(int64_t)c.it.seg * p.max_pages + (a >> p.page_shift)];
-        };
-        auto wanted = [&](const Cursor<Walk<Prob>>& c) {
-            const int a = c.kb() + (my_page << p.page_shift);
-            return c.keys.any(a, a + (1 << p.page_shift) - 1);
-        };
-        Cursor<Walk<Prob>> cur(p, start);
-        int pg = 0;
-        if (PAGED && cur.live) pg = lookup(cur);
-        while (cur.live) {
-            const Item it = cur.it;
-            const int kb = cur.kb(), n = cur.n, hk = PAGED ? it.rep : it.rep % p.Hkv, z = PAGED ? 0 : it.rep / p.Hkv;
-            const int my_pg = pg;
-            const bool want = PAGED ? wanted(cur) && my_panel < KP : lane < KP;
-            const Keys keys = cur.keys;
-            // the next step's page number is on its way while this step waits
-            cur.step(p);
-            if (PAGED && cur.live) pg = lookup(cur);
-            if (PAGED && !__all_sync(0xffffffffu, !want || (unsigned)my_pg < (unsigned)p.n_pages)) {
-                if (lane == 0) ab.fail(BSP_ERR_DEVICE_CHECK);
-                break;
+        Walk<Prob> walk(p, start);
+        Item it;
+        Work w;
+        bool live = true;
+        // the next tile, ready before this one's last step
+        auto advance = [&]() {
+            if (is_v) {
+                live = ring.take(i, w, lane == 0, true, ab);
+                ++i;
+                return;
             }
-            if (!is_v && n == 0) {
-                const uint32_t qs = q_it % QST;
-                bool ok = mbar_wait(&q_empty[qs], ((q_it / QST) & 1) ^ 1, ab);
+            live = walk.next(it);
+            if (live) w = make_work(p, it);
+        };
+        // this lane's page of step n: -1 hidden (not copied)
+        auto lookup = [&](int n) {
+            const Keys keys = tile_keys(p, w);
+            const int a = (w.key_tile(n) << 7) + (my_page << p.page_shift);
+            if (!keys.any(a, a + (1 << p.page_shift) - 1)) return -1;
+            const int pg = p.table[(int64_t)w.seg * p.max_pages + (a >> p.page_shift)];
+            return (unsigned)pg < (unsigned)p.n_pages ? pg : -2;  // -2: a bad page
+        };
+        advance();
+        int pg = 0;
+        if (PAGED && live) pg = lookup(0);
+        while (live) {
+            if (!is_v) {
+                if (!ring.put(i, w, lane, ab)) break;
+                const uint32_t qs = i % QST;
+                bool ok = mbar_wait(&q_empty[qs], ((i / QST) & 1) ^ 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 if (lane == 0) {
                     mbar_arrive_expect_tx(&q_full[qs], q_bytes);
                     for (int c = 0; c < KP; ++c)
-                        tma_load_4d(smem_u32(smem + SM::kQ + qs * kTileBytes + c * 16384), &tmQ, c * 64, hk * p.G,
-                                    it.g.t0 + it.tile * p.TQ, z, &q_full[qs]);
+                        tma_load_4d(smem_u32(smem + SM::kQ + qs * kTileBytes + c * 16384), &tmQ, c * 64, w.hk * p.G,
+                                    w.row0, w.z, &q_full[qs]);
                 }
-                ++q_it;
+                ++i;
             }
-            const uint32_t st = g % NST;
-            if (g >= NST) {
-                const uint32_t gp = g - NST;
-                uint64_t* freed = is_v ? &pv_done[gp % 3] : &s_full[gp % 3];
-                bool ok = mbar_wait(freed, (gp / 3) & 1, ab);
-                if (!__all_sync(0xffffffffu, ok)) break;
-            }
-            const uint32_t bytes = PAGED ? page_bytes * __popc(__ballot_sync(0xffffffffu, want)) : kTileBytes;
-            uint64_t* full = is_v ? &v_full[st] : &k_full[st];
-            // rows of this V tile that no query of the sequence sees
-            const int zlo = window_low(it.g.kvlen - it.g.qlen, p.window), zhi = it.g.kvlen - 1;
-            const bool scrub = is_v && bytes > 0 &&
-                               ((kb + 127 > zhi && PAGED) || (kb < zlo && !(kb + 127 < p.sinks)));
-            uint64_t* bar = scrub ? &v_land : full;
-            if (lane == 0) {
-                if (bytes) mbar_arrive_expect_tx(bar, bytes);
-                else mbar_arrive(bar);
-            }
-            __syncwarp();
-            const uint32_t base = smem_u32(smem + (is_v ? SM::kV : SM::kK) + st * kTileBytes);
-            if (want) {
-                if (PAGED)
-                    tma_load_4d(base + my_panel * 16384 + my_page * page_bytes, tm, my_panel * 64, 0, hk, my_pg, bar);
-                else
-                    tma_load_4d(base + lane * 16384, tm, lane * 64, kb, hk, z, bar);
-            }
-            if (scrub) {
-                bool ok = mbar_wait(&v_land, lands & 1, ab);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    if (lane == 0) mbar_drain(&v_land, lands & 1, ab);
-                    break;
+            const int ns = w.ns, hk = w.hk, z = w.z, zlo = w.zlo, zhi = w.zhi;
+            const Keys keys = tile_keys(p, w);
+            for (int n = 0; n < ns; ++n) {
+                const int kb = w.key_tile(n) << 7, my_pg = pg;
+                const bool want = PAGED ? my_pg >= 0 && my_panel < KP : lane < KP;
+                // the next step's page number is on its way while this step waits
+                if (n + 1 == ns && !is_v) {
+                    advance();
+                    if (PAGED && live) pg = lookup(0);
+                } else if (n + 1 < ns) {
+                    if (PAGED) pg = lookup(n + 1);
                 }
-                ++lands;
-                for (int r = lane; r < 128; r += 32) {
-                    const int j = kb + r, j16 = kb + (r & ~15);
-                    const bool used = j <= zhi && (j >= zlo || j < p.sinks);
-                    if (!used && keys.any(j16, j16 + 15))
-                        for (int c = 0; c < KP; ++c)
-                            for (int i = 0; i < 8; ++i)
-                                *reinterpret_cast<uint4*>(smem + SM::kV + st * kTileBytes + c * 16384 + r * 128 + i * 16) =
-                                    make_uint4(0u, 0u, 0u, 0u);
+                if (PAGED && __any_sync(0xffffffffu, my_pg == -2)) {
+                    if (lane == 0) ab.fail(BSP_ERR_DEVICE_CHECK);
+                    goto load_done;
                 }
-                fence_proxy_async_smem();
+                const uint32_t st = g % NST;
+                if (g >= NST) {
+                    const uint32_t gp = g - NST;
+                    uint64_t* freed = is_v ? &pv_done[gp % 3] : &s_full[gp % 3];
+                    bool ok = mbar_wait(freed, (gp / 3) & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) goto load_done;
+                }
+                const uint32_t bytes = PAGED ? page_bytes * __popc(__ballot_sync(0xffffffffu, want)) : kTileBytes;
+                uint64_t* full = is_v ? &v_full[st] : &k_full[st];
+                // rows of this V tile that no query of the sequence sees
+                const bool scrub =
+                    is_v && bytes > 0 && ((kb + 127 > zhi && PAGED) || (kb < zlo && !(kb + 127 < p.sinks)));
+                uint64_t* bar = scrub ? &v_land : full;
+                if (lane == 0) {
+                    if (bytes) mbar_arrive_expect_tx(bar, bytes);
+                    else mbar_arrive(bar);
+                }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(full);
+                const uint32_t base = smem_u32(smem + (is_v ? SM::kV : SM::kK) + st * kTileBytes);
+                if (want) {
+                    if (PAGED)
+                        tma_load_4d(base + my_panel * 16384 + my_page * page_bytes, tm, my_panel * 64, 0, hk, my_pg, bar);
+                    else
+                        tma_load_4d(base + lane * 16384, tm, lane * 64, kb, hk, z, bar);
+                }
+                if (scrub) {
+                    bool ok = mbar_wait(&v_land, lands & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) mbar_drain(&v_land, lands & 1, ab);
+                        goto load_done;
+                    }
+                    ++lands;
+                    for (int r = lane; r < 128; r += 32) {
+                        const int j = kb + r, j16 = kb + (r & ~15);
+                        const bool used = j <= zhi && (j >= zlo || j < p.sinks);
+                        if (!used && keys.any(j16, j16 + 15))
+                            for (int c = 0; c < KP; ++c)
+                                for (int k = 0; k < 8; ++k)
+                                    *reinterpret_cast<uint4*>(smem + SM::kV + st * kTileBytes + c * 16384 + r * 128 +
+                                                              k * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(full);
+                }
+                ++g;
             }
-            ++g;
+            if (is_v) {
+                advance();
+                if (PAGED && live) pg = lookup(0);
+            }
         }
+        if (!is_v && !live) {  // no further tile: the readers stop
+            Work end{};
+            ring.put(i, end, lane, ab);
+        }
+    load_done:
         if (lane == 0) {
             if (is_v) {
                 issued[2] = g;
             } else {
                 issued[0] = g;
-                issued[1] = q_it;
+                issued[1] = i;
             }
         }
     } else if (warp == 1) {
@@ -275,13 +279,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (lane == 0) {
             const uint64_t dq = smem_desc(smem_u32(smem + SM::kQ), 16, 1024, kSw128);
             const uint64_t dk = smem_desc(smem_u32(smem + SM::kK), 16, 1024, kSw128);
-            uint32_t q_it = 0, g = 0;
-            Walk<Prob> walk(p, start);
-            Item it;
-            while (walk.next(it)) {
-                const uint32_t qs = q_it % QST;
-                if (!mbar_wait(&q_full[qs], (q_it / QST) & 1, ab)) goto qk_done;
-                for (int n = 0; n < it.ns; ++n, ++g) {
+            uint32_t i = 0, g = 0;
+            Work w;
+            for (; ring.take(i, w, true, false, ab); ++i) {
+                const uint32_t qs = i % QST;
+                const int ns = w.ns;
+                if (!mbar_wait(&q_full[qs], (i / QST) & 1, ab)) goto qk_done;
+                for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g % NST, sb = g % 3;
                     if (g >= 3 && !mbar_wait(&pv_done[sb], ((g - 3) / 3) & 1, ab)) goto qk_done;
                     if (!mbar_wait(&k_full[st], (g / NST) & 1, ab)) goto qk_done;
@@ -293,9 +297,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                         mma_f16(tS + sb * 128, aq + off, bk + off, kIdescQK, ks > 0 ? 1u : 0u);
                     }
                     mma_commit(&s_full[sb]);
-                    if (n == it.ns - 1) mma_commit(&q_empty[qs]);
+                    if (n == ns - 1) mma_commit(&q_empty[qs]);
                 }
-                ++q_it;
             }
         qk_done:
             issued[3] = g;
@@ -305,27 +308,35 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         if (lane == 0) {
             const uint64_t dv = smem_desc(smem_u32(smem + SM::kV), 128 * 128, 1024, kSw128);
             uint32_t g = 0, tc = 0;
-            Walk<Prob> walk(p, start);
-            Item it;
-            while (walk.next(it)) {
-                const QTile q = p.qtile(it.g, it.tile);
-                const Span sp = p.span(q);
-                const Keys keys = tile_keys(p, q);
+            Work w;
+            while (ring.take(tc, w, true, false, ab)) {
+                const Keys keys = tile_keys(p, w);
                 if (tc > 0 && !mbar_wait(&o_empty, (tc - 1) & 1, ab)) goto pv_done_label;
                 uint32_t acc = 0;
-                for (int n = 0; n < it.ns; ++n, ++g) {
+                for (int n = 0; n < w.ns; ++n, ++g) {
                     const uint32_t st = g % NST, sb = g % 3;
-                    const int kb = sp.tile(it.s0 + n) << 7;
-                    if (!mbar_wait(&p_full[sb], (g / 3) & 1, ab)) goto pv_done_label;
-                    if (!mbar_wait(&v_full[st], (g / NST) & 1, ab)) goto pv_done_label;
-                    tc_fence_after();
+                    const int kb = w.key_tile(n) << 7;
                     const uint64_t bv = dv + ((st * kTileBytes) >> 4);
+                    uint32_t pieces = 0;  // bit ks: 16 keys that some row sees
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
-                        if (keys.any(kb + ks * 16, kb + ks * 16 + 15)) {
-                            mma_f16_tmem_a(tO, tS + sb * 128 + ks * 8, bv + ((ks * 2048) >> 4), kIdescPV, acc);
-                            acc = 1;
-                        }
+                        pieces |= keys.any(kb + ks * 16, kb + ks * 16 + 15) ? 1u << ks : 0u;
+                    if (!mbar_wait(&v_full[st], (g / NST) & 1, ab)) goto pv_done_label;
+                    if (!mbar_wait(&p_full[sb], (g / 3) & 1, ab)) goto pv_done_label;
+                    tc_fence_after();
+                    if (pieces == 0xffu) {
+#pragma unroll
+                        for (int ks = 0; ks < 8; ++ks)
+                            mma_f16_tmem_a(tO, tS + sb * 128 + ks * 8, bv + ((ks * 2048) >> 4), kIdescPV, ks > 0 ? 1u : acc);
+                        acc = 1;
+                    } else {
+#pragma unroll 1
+                        for (int ks = 0; ks < 8; ++ks)
+                            if ((pieces >> ks) & 1) {
+                                mma_f16_tmem_a(tO, tS + sb * 128 + ks * 8, bv + ((ks * 2048) >> 4), kIdescPV, acc);
+                                acc = 1;
+                            }
+                    }
                     mma_commit(&pv_done[sb]);
                 }
                 mma_commit(&o_full);
@@ -344,13 +355,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         uint8_t* stage = smem + SM::kEpi + quad * 4096;
         const uint32_t inv_g = 65536u / p.G + 1;  // r / G = r * inv_g >> 16 for r < 128
         uint32_t tc = 0;
-        Walk<Prob> walk(p, start);
-        Item it;
-        while (walk.next(it)) {
-            const QTile q = p.qtile(it.g, it.tile);
-            const int rows = q.nt * p.G;
-            const int hk = PAGED ? it.rep : it.rep % p.Hkv, z = PAGED ? 0 : it.rep / p.Hkv;
-            const int t0 = it.g.t0 + q.tok0;
+        Work w;
+        while (ring.take(tc, w, lane == 0, true, ab)) {
+            const int rows = w.nt * p.G, hk = w.hk, z = w.z, t0 = w.row0;
             const uint32_t lb = tc & 1;
             bool ok = mbar_wait(&l_full[lb], (tc >> 1) & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -372,9 +379,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 if (lane == 0) mbar_arrive(&o_empty);
                 continue;
             }
-            if (!it.whole()) {
+            if (!w.whole()) {
                 // a piece: raw O (relative to mf), mf and the sum, for the join
-                float* slot = args.slots + (size_t)it.slot() * slot_floats(kTcRows);
+                float* slot = args.slots + (size_t)w.slot() * slot_floats(kTcRows);
                 float* orow = slot + (size_t)row * kSlotD;
 #pragma unroll 1
                 for (int c = 0; c < DP / 32; ++c) {
@@ -394,7 +401,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     slot[kTcRows * kSlotD + row] = mf;
                     slot[kTcRows * kSlotD + kTcRows + row] = lt;
                 }
-                if (threadIdx.x == 128 && it.s0 == 0) write_cut(args.cuts, it, start);
+                if (threadIdx.x == 128 && w.s0 == 0) write_cut(args.cuts, w.seg, w.rep, w.tile, w.n - w.ns, start);
                 continue;
             }
             if (args.lse && row < rows) {
@@ -465,19 +472,24 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const float2 r2 = __fadd2_rn(__fadd2_rn(rs4[0], rs4[1]), __fadd2_rn(rs4[2], rs4[3]));
             return r2.x + r2.y;
         };
-        Walk<Prob> walk(p, start);
-        Item it;
-        while (walk.next(it)) {
-            const QTile q = p.qtile(it.g, it.tile);
-            const Span sp = p.span(q);
-            const int rows = q.nt * p.G;
+        while (true) {
+            int ns, s0, n_s, lo_tile, rows, pos;
+            {
+                Work w;
+                if (!ring.take(tc, w, lane == 0, true, ab)) break;
+                ns = w.ns, s0 = w.s0, n_s = w.n_s, lo_tile = w.lo;
+                rows = w.nt * p.G;
+                pos = row < rows ? w.a + (int)((row * inv_g) >> 16) : -1;
+            }
             const bool idle = quad * 32 >= rows;  // no live row in this warp's lanes
-            const int pos = row < rows ? q.a + (int)((row * inv_g) >> 16) : -1;
             const int low = pos - p.window + 1;
             float l = 0.f, m = -INFINITY;
-            for (int n = 0; n < it.ns; ++n, ++g) {
+            for (int n = 0; n < ns; ++n, ++g) {
                 const uint32_t sb = g % 3;
-                const int kb = (sp.tile(it.s0 + n) << 7) + wg * 64;  // first key of this half
+                const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
+                const int kb = (kt << 7) + wg * 64;  // first key of this half
+                const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
+                const bool skip = __all_sync(0xffffffffu, vis == 0), full = __all_sync(0xffffffffu, vis == ~0ull);
                 bool ok = mbar_wait(&s_full[sb], (g / 3) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                 if (idle) {
@@ -489,13 +501,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t srow = tS + sb * 128 + lane_base;
                 const uint32_t xb = xg & 1, xph = (xg >> 1) & 1;
                 ++xg;
-                const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
-                const bool skip = __all_sync(0xffffffffu, vis == 0);
                 float x[64];
                 float mx = -INFINITY;
                 if (!skip) {
                     tmem_ld64_sync(srow + wg * 64, srow + wg * 64 + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
-                    if (!__all_sync(0xffffffffu, vis == ~0ull)) hide(x, vis);
+                    if (!full) hide(x, vis);
                     mx = max64(x);
                 }
                 xm[xb][wg][row] = mx;
@@ -519,11 +529,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     for (int k = 0; k < 32; ++k) pk[k] = 0u;
                 }
                 tmem_st32_sync(srow + wg * 32, pk);
-                if (n > 0 && __any_sync(0xffffffffu, need)) {
+                // rows that saw nothing yet have O = 0, which no factor changes
+                const bool grew = need && m != -INFINITY;
+                if (__any_sync(0xffffffffu, grew)) {
                     ok = mbar_wait(&pv_done[(g - 1) % 3], ((g - 1) / 3) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                     tc_fence_after();
-                    const float alpha = need ? (m == -INFINITY ? 0.f : ex2_approx(m - mnext)) : 1.f;
+                    const float alpha = grew ? ex2_approx(m - mnext) : 1.f;
 #pragma unroll
                     for (int cc = 0; cc < DP / 64; ++cc) {
                         uint32_t r[32];

@@ -23,8 +23,79 @@ struct Keys {
     int lo, hi, sinks;
     __device__ __forceinline__ bool any(int a, int b) const { return a <= hi && (b >= lo || a < sinks); }
 };
-__device__ __forceinline__ Keys tile_keys(const Prob& p, const QTile& q) {
-    return Keys{window_low(q.a, p.window), q.b, p.sinks};
+// What the roles of a kernel need to know of a tile, handed out through a ring
+// in shared memory by the warp that walks the CTA's share: the walk's state and
+// its divisions then burden no other role's registers (with every role on a
+// walk of its own the softmax spilled, and a step of full attention took 1.33
+// us).  ns == 0 ends the share.
+struct __align__(16) Work {
+    int ns, s0, n;       // steps s0 .. s0 + ns - 1 of the tile's n
+    int tile;
+    int a, nt;           // position of its first token, tokens
+    int n_s, lo;         // sink steps, first window tile (dkv: first query tile in lo)
+    int row0, z, hk, seg;
+    int rep;
+    int zlo, zhi;        // keys that some query of the segment sees, sinks aside
+    int pad;
+    __device__ __forceinline__ bool whole() const { return ns == n; }
+    __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (s0 == 0); }
+    __device__ __forceinline__ int key_tile(int i) const { return s0 + i < n_s ? s0 + i : lo + (s0 + i - n_s); }
+};
+
+constexpr int kRing = 4;
+constexpr int kReaders = 15;  // three single-thread or producer roles, 4 epilogue warps, 8 softmax warps
+
+struct Ring {
+    uint64_t full[kRing], empty[kRing];
+    Work w[kRing];
+    __device__ __forceinline__ void init() {
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kReaders);
+        }
+    }
+    // by a whole warp, in order i = 0, 1, ...
+    __device__ __forceinline__ bool put(uint32_t i, const Work& x, int lane, const Abort& ab) {
+        const uint32_t s = i % kRing;
+        const bool ok = mbar_wait(&empty[s], ((i / kRing) & 1) ^ 1, ab);
+        if (!__all_sync(0xffffffffu, ok)) return false;
+        if (lane == 0) {
+            w[s] = x;
+            mbar_arrive(&full[s]);
+        }
+        return true;
+    }
+    // by one thread, or by all lanes of a warp (`one`: the lane that answers)
+    __device__ __forceinline__ bool take(uint32_t i, Work& x, bool one, bool warp, const Abort& ab) {
+        const uint32_t s = i % kRing;
+        bool ok = mbar_wait(&full[s], (i / kRing) & 1, ab);
+        if (warp) ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        x = w[s];
+        if (warp) __syncwarp();
+        if (one) mbar_arrive(&empty[s]);
+        return x.ns > 0;
+    }
+};
+
+__device__ __forceinline__ Keys tile_keys(const Prob& p, const Work& w) {
+    return Keys{window_low(w.a, p.window), w.a + w.nt - 1, p.sinks};
+}
+
+__device__ __forceinline__ Work make_work(const Prob& p, const Item& it) {
+    const QTile q = p.qtile(it.g, it.tile);
+    const Span sp = p.span(q);
+    Work w;
+    w.ns = it.ns, w.s0 = it.s0, w.n = it.n, w.tile = it.tile;
+    w.a = q.a, w.nt = q.nt, w.n_s = sp.n_s, w.lo = sp.lo;
+    w.row0 = it.g.t0 + q.tok0;
+    w.z = p.paged ? 0 : it.rep / p.Hkv;
+    w.hk = p.paged ? it.rep : it.rep % p.Hkv;
+    w.seg = it.seg, w.rep = it.rep;
+    w.zlo = window_low(it.g.kvlen - it.g.qlen, p.window);
+    w.zhi = it.g.kvlen - 1;
+    w.pad = 0;
+    return w;
 }
 
 // bits [0, c) of 64

@@ -116,6 +116,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __shared__ uint32_t issued_a;
     __shared__ Start start;
     __shared__ int64_t red[32];
+    __shared__ Ring ring;
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -137,6 +138,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         }
         mbar_init(&acc_full, 1);
         mbar_init(&acc_empty, 4);
+        ring.init();
         fence_barrier_init();
         args.cuts[blockIdx.x].pieces = 0;
     }
@@ -145,49 +147,69 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         tmem_relinquish();
     }
     tc_fence_before();
-    locate<kThreads>(p, gridDim.x, args.min_share, reinterpret_cast<int*>(smem), red, &start);
+    locate<kThreads>(p, args.min_share, reinterpret_cast<int*>(smem), red, &start);
     tc_fence_after();
     const uint32_t tS = tmem_base, tP = tmem_base + 256, tA = tmem_base + 384;
 
     if (warp < 4) {
         regs_dec<kRegsCtl>();
-        if ((warp == 0 || warp == 3) && lane == 0) {
+        if (warp == 0 || warp == 3) {
             // ------------------------------------------------ producers ----
+            // warp 0 walks the share and hands the tiles out
             const bool is_v = warp == 3;
             const CUtensorMap* tm = is_v ? &tmV : &tmK;
             const CUtensorMap* ta = is_v ? &tmG : &tmQ;
-            tma_prefetch_desc(tm);
-            tma_prefetch_desc(ta);
+            if (lane == 0) {
+                tma_prefetch_desc(tm);
+                tma_prefetch_desc(ta);
+            }
             const uint32_t a_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
             Walk<Prob> walk(p, start);
             Item it;
-            while (walk.next(it)) {
-                const Span sp = p.span(p.qtile(it.g, it.tile));
-                const int hk = it.rep % p.Hkv, z = it.rep / p.Hkv;
+            Work w;
+            while (true) {
+                if (is_v) {
+                    if (!ring.take(tiles, w, lane == 0, true, ab)) break;
+                } else {
+                    w.ns = 0;
+                    if (walk.next(it)) w = make_work(p, it);
+                    if (!ring.put(tiles, w, lane, ab) || w.ns == 0) break;
+                }
                 // the previous tile's S and dP products have read Q and dO
-                if (tiles > 0 && !mbar_wait(&a_free, (tiles - 1) & 1, ab)) goto load_done;
-                mbar_arrive_expect_tx(&a_full, a_bytes);
-                for (int c = 0; c < KP; ++c)
-                    tma_load_4d(smem_u32(smem + (is_v ? SM::kB : SM::kA) + c * 16384), ta, c * 64, hk * p.G,
-                                it.tile * p.TQ, z, &a_full);
+                if (tiles > 0) {
+                    const bool ok = mbar_wait(&a_free, (tiles - 1) & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) goto load_done;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&a_full, a_bytes);
+                    for (int c = 0; c < KP; ++c)
+                        tma_load_4d(smem_u32(smem + (is_v ? SM::kB : SM::kA) + c * 16384), ta, c * 64, w.hk * p.G, w.row0,
+                                    w.z, &a_full);
+                }
                 ++tiles;
-                for (int n = 0; n < it.ns; ++n, ++g) {
+                for (int n = 0; n < w.ns; ++n, ++g) {
                     const uint32_t st = g & 1;
                     // K of step g - 2 is free after its dQ product, V after its dP product,
                     // which the same step's dS follows
-                    if (g >= 2 && !mbar_wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto load_done;
+                    if (g >= 2) {
+                        const bool ok = mbar_wait(&dq_done[st], ((g - 2) >> 1) & 1, ab);
+                        if (!__all_sync(0xffffffffu, ok)) goto load_done;
+                    }
                     uint64_t* full = is_v ? &v_full[st] : &k_full[st];
-                    mbar_arrive_expect_tx(full, kTile);
-                    const int kb = sp.tile(it.s0 + n) << 7;
-                    for (int c = 0; c < KP; ++c)
-                        tma_load_4d(smem_u32(smem + (is_v ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64, kb, hk,
-                                    z, full);
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(full, kTile);
+                        for (int c = 0; c < KP; ++c)
+                            tma_load_4d(smem_u32(smem + (is_v ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64,
+                                        w.key_tile(n) << 7, w.hk, w.z, full);
+                    }
                 }
             }
         load_done:
-            issued[is_v] = g;
-            atomicMax(&issued_a, tiles);
+            if (lane == 0) {
+                issued[is_v] = g;
+                atomicMax(&issued_a, tiles);
+            }
         } else if (warp == 1 && lane == 0) {
             // ------------------------------------ S and dP products ----
             const uint64_t da = smem_desc(smem_u32(smem + SM::kA), 16, 1024, kSw128);
@@ -195,11 +217,11 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 16, 1024, kSw128);
             const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 16, 1024, kSw128);
             uint32_t g = 0, tiles = 0;
-            Walk<Prob> walk(p, start);
-            Item it;
-            while (walk.next(it)) {
+            Work w;
+            while (ring.take(tiles, w, true, false, ab)) {
+                const int ns = w.ns;
                 if (!mbar_wait(&a_full, tiles & 1, ab)) goto score_done;
-                for (int n = 0; n < it.ns; ++n, ++g) {
+                for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g & 1;
                     if (g >= 2 && !mbar_wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto score_done;
                     if (!mbar_wait(&k_full[st], (g >> 1) & 1, ab)) goto score_done;
@@ -225,7 +247,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
                     }
                     mma_commit(&dp_full);
-                    if (n == it.ns - 1) mma_commit(&a_free);
+                    if (n == ns - 1) mma_commit(&a_free);
                 }
                 ++tiles;
             }
@@ -235,11 +257,11 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             // ------------------------------------------- dQ product ----
             const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 128 * 128, 1024, kSw128);
             uint32_t g = 0, tiles = 0;
-            Walk<Prob> walk(p, start);
-            Item it;
-            while (walk.next(it)) {
+            Work w;
+            while (ring.take(tiles, w, true, false, ab)) {
+                const int ns = w.ns;
                 if (tiles > 0 && !mbar_wait(&acc_empty, (tiles - 1) & 1, ab)) goto dq_end;
-                for (int n = 0; n < it.ns; ++n, ++g) {
+                for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g & 1;
                     if (!mbar_wait(&ds_full[st], (g >> 1) & 1, ab)) goto dq_end;
                     tc_fence_after();
@@ -261,24 +283,23 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const uint32_t inv_g = 65536u / p.G + 1;  // r / G = r * inv_g >> 16 for r < 128
         uint32_t tiles = 0;
-        Walk<Prob> walk(p, start);
-        Item it;
-        while (walk.next(it)) {
-            const QTile q = p.qtile(it.g, it.tile);
-            const int rows = q.nt * p.G, hk = it.rep % p.Hkv, z = it.rep / p.Hkv;
+        Work w;
+        while (ring.take(tiles, w, lane == 0, true, ab)) {
+            const int rows = w.nt * p.G, hk = w.hk, z = w.z;
             const bool ok = mbar_wait(&acc_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             ++tiles;
-            float* slot = it.whole() ? nullptr : args.slots + (size_t)it.slot() * slot_floats(kTcRows);
+            float* slot = w.whole() ? nullptr : args.slots + (size_t)w.slot() * slot_floats(kTcRows);
             drain<T, DP>(tA + lane_base, &acc_empty, lane, row, row < rows, slot, args.scale, args.D,
                          smem + SM::kEpi + quad * 4096, [&](int i) -> T* {
                              const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
                              if (r >= rows) return nullptr;
                              return static_cast<T*>(args.dQ.ptr) + z * args.dQ.s[0] + (hk * p.G + h) * args.dQ.s[1] +
-                                    (int64_t)(q.tok0 + t) * args.dQ.s[2];
+                                    (int64_t)(w.row0 + t) * args.dQ.s[2];
                          });
-            if (threadIdx.x == 128 && it.s0 == 0 && !it.whole()) write_cut(args.cuts, it, start);
+            if (threadIdx.x == 128 && w.s0 == 0 && !w.whole())
+                write_cut(args.cuts, w.seg, w.rep, w.tile, w.n - w.ns, start);
         }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -287,35 +308,32 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const uint32_t inv_g = 65536u / p.G + 1;
         uint32_t g = 0;
-        Walk<Prob> walk(p, start), ahead(p, start);
-        Item it, nx;
-        // the next tile's statistics are on their way while this tile's steps run
-        float nl = 0.f, dl = 0.f;
-        auto fetch = [&]() {
-            if (!ahead.next(nx)) return;
-            const float* s = args.stats + ((int64_t)nx.rep * args.ntiles + nx.tile) * 256;
-            nl = s[row];
-            dl = s[128 + row];
-        };
-        fetch();
-        while (walk.next(it)) {
-            const float nlse = nl, delta = dl;
-            fetch();
-            const QTile q = p.qtile(it.g, it.tile);
-            const Span sp = p.span(q);
-            const int rows = q.nt * p.G;
-            const int pos = row < rows ? q.a + (int)((row * inv_g) >> 16) : -1, low = pos - p.window + 1;
-            for (int n = 0; n < it.ns; ++n, ++g) {
+        for (uint32_t i = 0;; ++i) {
+            int ns, s0, n_s, lo_tile, pos;
+            float nlse, delta;
+            {
+                Work w;
+                if (!ring.take(i, w, lane == 0, true, ab)) break;
+                ns = w.ns, s0 = w.s0, n_s = w.n_s, lo_tile = w.lo;
+                const float* s = args.stats + ((int64_t)w.rep * args.ntiles + w.tile) * 256;
+                nlse = s[row];
+                delta = s[128 + row];
+                pos = row < w.nt * p.G ? w.a + (int)((row * inv_g) >> 16) : -1;
+            }
+            const int low = pos - p.window + 1;
+            for (int n = 0; n < ns; ++n, ++g) {
                 const uint32_t st = g & 1;
-                const int kb = (sp.tile(it.s0 + n) << 7) + wg * 64;
+                const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
+                const int kb = (kt << 7) + wg * 64;
                 const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
+                const bool full = __all_sync(0xffffffffu, vis == ~0ull);
                 bool ok = mbar_wait(&s_full[st], (g >> 1) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 const uint32_t ts = tS + st * 128 + lane_base + wg * 64;
                 float x[64];
                 tmem_ld64_sync(ts, ts + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
-                if (!__all_sync(0xffffffffu, vis == ~0ull)) hide(x, vis);
+                if (!full) hide(x, vis);
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
                     const float2 y = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(args.c2, args.c2),
@@ -397,6 +415,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     __shared__ uint32_t issued_a, issued_k;
     __shared__ Start start;
     __shared__ int64_t red[32];
+    __shared__ Ring ring;
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -421,6 +440,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         mbar_init(&dk_full, 1);
         mbar_init(&dv_empty, 4);
         mbar_init(&dk_empty, 4);
+        ring.init();
         fence_barrier_init();
         args.cuts[blockIdx.x].pieces = 0;
     }
@@ -429,7 +449,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         tmem_relinquish();
     }
     tc_fence_before();
-    locate<kThreads>(kp, gridDim.x, args.min_share, reinterpret_cast<int*>(smem), red, &start);
+    locate<kThreads>(kp, args.min_share, reinterpret_cast<int*>(smem), red, &start);
     // rows past TQ * G, which no copy writes, enter the products over the rows
     // with P = 0: they must not hold NaN
     for (int i = threadIdx.x; i < 4 * (int)kTile / 16; i += kThreads)
@@ -441,45 +461,69 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
     if (warp < 4) {
         regs_dec<kRegsCtl>();
-        if ((warp == 0 || warp == 3) && lane == 0) {
+        if (warp == 0 || warp == 3) {
             // ------------------------------------------------ producers ----
             const bool is_g = warp == 3;
             const CUtensorMap* ta = is_g ? &tmV : &tmK;
             const CUtensorMap* tm = is_g ? &tmG : &tmQ;
-            tma_prefetch_desc(ta);
-            tma_prefetch_desc(tm);
+            if (lane == 0) {
+                tma_prefetch_desc(ta);
+                tma_prefetch_desc(tm);
+            }
             const uint32_t bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
             Walk<KProb> walk(kp, start);
             Item it;
-            while (walk.next(it)) {
-                const int hk = it.rep % p.Hkv, z = it.rep / p.Hkv;
-                int first, nq;
-                kp.qrange(it.tile, &first, &nq);
-                first += it.s0;
+            Work w;
+            while (true) {
+                if (is_g) {
+                    if (!ring.take(tiles, w, lane == 0, true, ab)) break;
+                } else {
+                    w = Work{};
+                    if (walk.next(it)) {
+                        int first, nq;
+                        kp.qrange(it.tile, &first, &nq);
+                        w.ns = it.ns, w.s0 = it.s0, w.n = it.n, w.tile = it.tile;
+                        w.lo = first + it.s0;
+                        w.z = it.rep / p.Hkv, w.hk = it.rep % p.Hkv, w.rep = it.rep;
+                    }
+                    if (!ring.put(tiles, w, lane, ab) || w.ns == 0) break;
+                }
                 // the previous tile's score products have read K and V
-                if (tiles > 0 && !mbar_wait(&a_free, (tiles - 1) & 1, ab)) goto load_done;
-                mbar_arrive_expect_tx(&a_full, kTile);
-                for (int c = 0; c < KP; ++c)
-                    tma_load_4d(smem_u32(smem + (is_g ? SM::kB : SM::kA) + c * 16384), ta, c * 64, it.tile << 7, hk, z,
-                                &a_full);
-                ++tiles;
-                for (int n = 0; n < it.ns; ++n, ++g) {
-                    const uint32_t st = g & 1;
-                    if (g >= 2 && !mbar_wait(&dk_done[st], ((g - 2) >> 1) & 1, ab)) goto load_done;
-                    uint64_t* full = is_g ? &g_full[st] : &q_full[st];
-                    mbar_arrive_expect_tx(full, bytes + (is_g ? 0u : 1024u));
+                if (tiles > 0) {
+                    const bool ok = mbar_wait(&a_free, (tiles - 1) & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) goto load_done;
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&a_full, kTile);
                     for (int c = 0; c < KP; ++c)
-                        tma_load_4d(smem_u32(smem + (is_g ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64,
-                                    hk * p.G, (first + n) * p.TQ, z, full);
-                    if (!is_g)
-                        bulk_load(smem_u32(smem + SM::kStats + st * 1024),
-                                  args.stats + ((int64_t)it.rep * args.ntiles + first + n) * 256, 1024, full);
+                        tma_load_4d(smem_u32(smem + (is_g ? SM::kB : SM::kA) + c * 16384), ta, c * 64, w.tile << 7, w.hk,
+                                    w.z, &a_full);
+                }
+                ++tiles;
+                for (int n = 0; n < w.ns; ++n, ++g) {
+                    const uint32_t st = g & 1;
+                    if (g >= 2) {
+                        const bool ok = mbar_wait(&dk_done[st], ((g - 2) >> 1) & 1, ab);
+                        if (!__all_sync(0xffffffffu, ok)) goto load_done;
+                    }
+                    uint64_t* full = is_g ? &g_full[st] : &q_full[st];
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(full, bytes + (is_g ? 0u : 1024u));
+                        for (int c = 0; c < KP; ++c)
+                            tma_load_4d(smem_u32(smem + (is_g ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64,
+                                        w.hk * p.G, (w.lo + n) * p.TQ, w.z, full);
+                        if (!is_g)
+                            bulk_load(smem_u32(smem + SM::kStats + st * 1024),
+                                      args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * 256, 1024, full);
+                    }
                 }
             }
         load_done:
-            issued[is_g] = g;
-            atomicMax(&issued_a, tiles);
+            if (lane == 0) {
+                issued[is_g] = g;
+                atomicMax(&issued_a, tiles);
+            }
         } else if (warp == 1 && lane == 0) {
             // --------------------------------- S^T and dP^T products ----
             const uint64_t da = smem_desc(smem_u32(smem + SM::kA), 16, 1024, kSw128);
@@ -487,11 +531,11 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 16, 1024, kSw128);
             const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 16, 1024, kSw128);
             uint32_t g = 0, gd = 0, tiles = 0;
-            Walk<KProb> walk(kp, start);
-            Item it;
-            while (walk.next(it)) {
+            Work w;
+            while (ring.take(tiles, w, true, false, ab)) {
+                const int ns = w.ns;
                 if (!mbar_wait(&a_full, tiles & 1, ab)) goto score_done;
-                for (int n = 0; n < it.ns; ++n) {
+                for (int n = 0; n < ns; ++n) {
                     const uint32_t st = g & 1;
                     if (g >= 1 && !mbar_wait(&dv_done, (g - 1) & 1, ab)) goto score_done;
                     if (!mbar_wait(&q_full[st], (g >> 1) & 1, ab)) goto score_done;
@@ -513,7 +557,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     }
                     mma_commit(&dp_full);
                     ++gd;
-                    if (n == it.ns - 1) mma_commit(&a_free);
+                    if (n == ns - 1) mma_commit(&a_free);
                 }
                 ++tiles;
             }
@@ -525,10 +569,10 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 128 * 128, 1024, kSw128);
             const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 128 * 128, 1024, kSw128);
             uint32_t g = 0, gk = 0, tiles = 0;
-            Walk<KProb> walk(kp, start);
-            Item it;
-            while (walk.next(it)) {
-                for (int n = 0; n < it.ns; ++n) {
+            Work w;
+            while (ring.take(tiles, w, true, false, ab)) {
+                const int ns = w.ns;
+                for (int n = 0; n < ns; ++n) {
                     const uint32_t st = g & 1;
                     if (n == 0 && tiles > 0 && !mbar_wait(&dv_empty, (tiles - 1) & 1, ab)) goto grad_done;
                     if (!mbar_wait(&p_full, g & 1, ab)) goto grad_done;
@@ -539,7 +583,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         mma_f16_tmem_a(tV, tS + (ks >> 2) * 64 + (ks & 3) * 8, dy + ((st * kTile + ks * 2048) >> 4), kIdescD,
                                        ks > 0 || n > 0);
                     mma_commit(&dv_done);
-                    if (n == it.ns - 1) mma_commit(&dv_full);
+                    if (n == ns - 1) mma_commit(&dv_full);
                     ++g;
                     if (n == 0 && tiles > 0 && !mbar_wait(&dk_empty, (tiles - 1) & 1, ab)) goto grad_done;
                     if (!mbar_wait(&ds_full, gk & 1, ab)) goto grad_done;
@@ -549,7 +593,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         mma_f16_tmem_a(tK, tP + (ks >> 2) * 64 + (ks & 3) * 8, dx + ((st * kTile + ks * 2048) >> 4), kIdescD,
                                        ks > 0 || n > 0);
                     mma_commit(&dk_done[st]);
-                    if (n == it.ns - 1) mma_commit(&dk_full);
+                    if (n == ns - 1) mma_commit(&dk_full);
                     ++gk;
                 }
                 ++tiles;
@@ -564,11 +608,10 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         uint8_t* stage = smem + SM::kEpi + quad * 4096;
         uint32_t tiles = 0;
-        Walk<KProb> walk(kp, start);
-        Item it;
-        while (walk.next(it)) {
-            const int hk = it.rep % p.Hkv, z = it.rep / p.Hkv, kb = it.tile << 7;
-            float* slot = it.whole() ? nullptr : args.slots + (size_t)it.slot() * kv_slot_floats(kTcRows);
+        Work w;
+        while (ring.take(tiles, w, lane == 0, true, ab)) {
+            const int hk = w.hk, z = w.z, kb = w.tile << 7;
+            float* slot = w.whole() ? nullptr : args.slots + (size_t)w.slot() * kv_slot_floats(kTcRows);
             auto rows_of = [&](const View& v) {
                 return [&, z, hk, kb](int i) -> T* {
                     const int j = kb + quad * 32 + i;
@@ -587,7 +630,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             drain<T, DP>(tK + lane_base, &dk_empty, lane, row, kb + row < p.Sk, slot, args.scale, args.D, stage,
                          rows_of(args.dK));
             ++tiles;
-            if (threadIdx.x == 128 && it.s0 == 0 && !it.whole()) write_cut(args.cuts, it, start);
+            if (threadIdx.x == 128 && w.s0 == 0 && !w.whole())
+                write_cut(args.cuts, w.seg, w.rep, w.tile, w.n - w.ns, start);
         }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -595,14 +639,15 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         const int wg = (warp - 8) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         uint32_t g = 0;
-        Walk<KProb> walk(kp, start);
-        Item it;
-        while (walk.next(it)) {
-            int first, nq;
-            kp.qrange(it.tile, &first, &nq);
-            first += it.s0;
-            const int j = (it.tile << 7) + row;  // this thread's key
-            for (int n = 0; n < it.ns; ++n, ++g) {
+        for (uint32_t i = 0;; ++i) {
+            int ns, first, j;
+            {
+                Work w;
+                if (!ring.take(i, w, lane == 0, true, ab)) break;
+                ns = w.ns, first = w.lo;
+                j = (w.tile << 7) + row;  // this thread's key
+            }
+            for (int n = 0; n < ns; ++n, ++g) {
                 const uint32_t st = g & 1;
                 // rows that see the key: tokens from the key's own to window - 1
                 // later ones (a sink: all later ones), G rows each
@@ -610,6 +655,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 const int c0 = imin(imax(j - tok, 0), 128) * p.G - wg * 64;
                 const int c1 = j < p.sinks ? 64 : imin(imax(j - tok + p.window, 0), 128) * p.G - wg * 64;
                 const unsigned long long vis = below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64));
+                const bool full = __all_sync(0xffffffffu, vis == ~0ull);
                 const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 1024) + wg * 64;
                 bool ok = mbar_wait(&q_full[st], (g >> 1) & 1, ab);
                 ok = ok && mbar_wait(&s_full, g & 1, ab);
@@ -618,7 +664,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 float x[64];
                 tmem_ld64_sync(tS + lane_base + wg * 64, tS + lane_base + wg * 64 + 32,
                                *reinterpret_cast<uint32_t(*)[64]>(x));
-                if (!__all_sync(0xffffffffu, vis == ~0ull)) hide(x, vis);
+                if (!full) hide(x, vis);
                 {
                     uint32_t pk[32];
 #pragma unroll

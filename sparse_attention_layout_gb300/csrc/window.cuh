@@ -10,13 +10,17 @@
 // r % G), so that one pass over the keys serves the whole group and the rows
 // of a single new token are the tile's first G.
 //
-// Split: the steps of all tiles, in the order (segment, repetition, tile,
-// step), form one line; CTA c of n takes [c tot / n, (c + 1) tot / n).  A
-// tile that a boundary cuts leaves partial results, which a second kernel
-// joins in the order of the pieces, so results do not depend on timing.  One
-// segment is a shape of tiles: the whole of a dense batch (repeated for each
-// (batch entry, KV head)), or one sequence of a ragged one (repeated for each
-// KV head), whose lengths only the device knows.
+// Split: the steps of all tiles form one line; CTA c of n takes
+// [c tot / n, (c + 1) tot / n).  A tile that a boundary cuts leaves partial
+// results, which a second kernel joins in the order of the pieces, so results
+// do not depend on timing.  Tiles are numbered (segment, repetition, tile); a
+// segment is a shape of tiles: the whole of a dense batch, repeated for each
+// (batch entry, KV head), or one sequence of a ragged one, whose lengths only
+// the device knows, repeated for each KV head.  The line holds them column by
+// column of a table with one column per CTA, filled row by row: CTAs then
+// work on neighbouring tiles at the same time and share their keys in L2
+// (with each CTA on a run of consecutive tiles instead, the band of 8192 keys
+// and 16 heads read 954 MB from HBM instead of the 402 MB that it holds).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -166,12 +170,33 @@ struct KProb {
 // Share of CTA c among n: [share_at(c), share_at(c + 1)).
 BSP_HD int64_t share_at(int64_t tot, int n, int c) { return c >= n ? tot : tot / n * c + tot % n * c / n; }
 
+// The table of `items` tiles in `cols` columns.
+struct Table {
+    int64_t items;
+    int cols;
+    // column and row of place l on the line
+    BSP_HD void place(int64_t l, int* col, int64_t* row) const {
+        const int64_t q = items / cols, r = items % cols;
+        if (l < r * (q + 1)) {
+            *col = (int)(l / (q + 1));
+            *row = l % (q + 1);
+        } else {
+            *col = (int)(r + (l - r * (q + 1)) / q);
+            *row = (l - r * (q + 1)) % q;
+        }
+    }
+    BSP_HD int64_t number(int col, int64_t row) const { return row * cols + col; }
+    BSP_HD int64_t height(int col) const { return items / cols + (col < items % cols); }
+};
+
 // Where a CTA's share begins, how long it is.
 struct Start {
     int64_t tot;
-    int n;         // CTAs that share the steps (the others do nothing)
-    int64_t count; // steps of this CTA
-    int seg, rep, tile, off;
+    int64_t items;
+    int n;          // CTAs that share the steps (the others do nothing)
+    int64_t count;  // steps of this CTA
+    int64_t place;  // place on the line of its first tile
+    int off;        // first step of it
 };
 
 // A tile that begins in CTA c and goes on in later ones: `pieces` of it (0:
@@ -185,17 +210,6 @@ struct Cut {
 };
 
 #if defined(__CUDACC__)
-
-template <int NT>
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int64_t t = 0;
-    for (int i = 0; i < NT / 32; ++i) t += red[i];
-    return t;
-}
 
 // exclusive prefix over the block's threads; *total = the block's sum
 template <int NT>
@@ -218,160 +232,198 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* 
     return before + x - v;
 }
 
-// Finds this CTA's share; called by every thread of the block.  seg_steps:
-// scratch of nseg ints in shared memory (unused when nseg == 1); red: 32
-// int64.  min_share: CTAs are used only while each gets this many steps.
+// Finds this CTA's share; called by every thread of the block.  seg_end:
+// scratch of nseg ints in shared memory (unused when nseg == 1): tiles of the
+// segments up to each, one repetition; red: 32 int64.  min_share: CTAs are
+// used only while each gets this many steps.  Each thread adds up a run of the
+// line, one scan gives the runs' starts, and the thread whose run holds the
+// share's first step finds it.
 template <int NT, typename P>
-__device__ __forceinline__ void locate(const P& p, int n_cta, int min_share, int* seg_steps, int64_t* red, Start* out) {
+__device__ __forceinline__ void locate(const P& p, int min_share, int* seg_end, int64_t* red, Start* out) {
     const int tid = threadIdx.x;
-    int64_t sum = 0;  // steps of all segments, one repetition
-    int64_t one = 0;  // dense: the only segment's
+    int64_t tiles = 0;  // one repetition of every segment
     if (p.nseg == 1) {
-        const Seg g = p.seg(0);
-        for (int t = tid; t < g.ntiles; t += NT) sum += p.steps(g, t);
-        one = sum = block_sum<NT>(sum, red);
+        tiles = p.seg(0).ntiles;
     } else {
-        const int lane = tid & 31;
-        for (int s0 = tid - lane; s0 < p.nseg; s0 += NT) {
-            const int s = s0 + lane;
-            const Seg g = s < p.nseg ? p.seg(s) : Seg{0, 0, 0, 0};
-            int w = 0;
-            const bool many = g.ntiles > 8;
-            if (!many)
-                for (int t = 0; t < g.ntiles; ++t) w += p.steps(g, t);
-            unsigned left = __ballot_sync(0xffffffffu, many);
-            while (left) {  // long chunks: the warp counts one together
-                const int src = __ffs(left) - 1;
-                left &= left - 1;
-                Seg h;
-                h.t0 = __shfl_sync(0xffffffffu, g.t0, src);
-                h.qlen = __shfl_sync(0xffffffffu, g.qlen, src);
-                h.kvlen = __shfl_sync(0xffffffffu, g.kvlen, src);
-                h.ntiles = __shfl_sync(0xffffffffu, g.ntiles, src);
-                int c = 0;
-                for (int t = lane; t < h.ntiles; t += 32) c += p.steps(h, t);
-                for (int o = 16; o; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-                if (lane == src) w = c;
-            }
-            if (s < p.nseg) seg_steps[s] = w;
-            sum += w;
-        }
-        sum = block_sum<NT>(sum, red);
-    }
-    Start st;
-    st.tot = sum * p.rep;
-    const int64_t most = (st.tot + min_share - 1) / min_share;
-    st.n = most < 1 ? 1 : (most < n_cta ? (int)most : n_cta);
-    const int c = blockIdx.x;
-    int64_t at = share_at(st.tot, st.n, c);
-    st.count = share_at(st.tot, st.n, c + 1) - at;
-    st.seg = st.rep = st.tile = st.off = 0;
-    if (st.count > 0) {
-        int64_t w = one;
-        if (p.nseg > 1) {
-            __syncthreads();
-            int64_t before = 0;
-            for (int s0 = 0; s0 < p.nseg; s0 += NT) {
-                const int s = s0 + tid;
-                const int64_t v = s < p.nseg ? (int64_t)seg_steps[s] * p.rep : 0;
-                int64_t total;
-                const int64_t ex = before + block_scan<NT>(v, red, &total);
-                if (v > 0 && ex <= at && at < ex + v) {
-                    out->seg = s;
-                    out->count = at - ex;  // step within the segment, all repetitions
-                }
-                before += total;
-                if (at < before) break;
-            }
-            __syncthreads();
-            st.seg = out->seg;
-            at = out->count;
-            w = seg_steps[st.seg];
-            __syncthreads();
-        }
-        st.rep = (int)(at / w);
-        at -= (int64_t)st.rep * w;
-        const Seg g = p.seg(st.seg);
-        int64_t before = 0;
-        for (int t0 = 0; t0 < g.ntiles; t0 += NT) {
-            const int t = t0 + tid;
-            const int64_t v = t < g.ntiles ? p.steps(g, t) : 0;
+        for (int s0 = 0; s0 < p.nseg; s0 += NT) {
+            const int s = s0 + tid;
+            const int64_t v = s < p.nseg ? p.seg(s).ntiles : 0;
             int64_t total;
-            const int64_t ex = before + block_scan<NT>(v, red, &total);
-            if (v > 0 && ex <= at && at < ex + v) {
-                out->tile = t;
-                out->off = (int)(at - ex);
-            }
-            before += total;
-            if (at < before) break;
+            const int64_t ex = block_scan<NT>(v, red, &total);
+            if (s < p.nseg) seg_end[s] = (int)(tiles + ex + v);
+            tiles += total;
         }
         __syncthreads();
-        st.tile = out->tile;
-        st.off = out->off;
     }
-    __syncthreads();
-    if (tid == 0) *out = st;
+    const Table tab{tiles * p.rep, (int)gridDim.x};
+    // this thread's run of the line, tile after tile
+    const int64_t run = (tab.items + NT - 1) / NT;
+    const int64_t l0 = tid * run, l1 = l0 + run < tab.items ? l0 + run : tab.items;
+    int64_t at = -1, sum = 0, found = -1;
+    int off = 0;
+    const Seg only = p.nseg == 1 ? p.seg(0) : Seg{0, 0, 0, 0};
+    const int hop = p.nseg == 1 && only.ntiles > 0 ? (int)(gridDim.x % only.ntiles) : 0;
+    // twice: the sum, then (for the thread that holds it) the first step's tile
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t before = sum;  // second pass: steps before this run
+        sum = 0;
+        int col = 0, tile = 0;
+        int64_t row = 0, height = 0;
+        for (int64_t l = l0; l < l1; ++l) {
+            if (l == l0 || ++row >= height) {
+                if (l == l0) {
+                    tab.place(l, &col, &row);
+                } else {
+                    ++col;
+                    row = 0;
+                }
+                height = tab.height(col);
+                if (p.nseg == 1) tile = (int)(tab.number(col, row) % only.ntiles);
+            } else if (p.nseg == 1) {
+                tile += hop;
+                if (tile >= only.ntiles) tile -= only.ntiles;
+            }
+            int v;
+            if (p.nseg == 1) {
+                v = p.steps(only, tile);
+            } else {
+                // the segment that holds tile number a
+                const int64_t a = tab.number(col, row);
+                int lo = 0, hi = p.nseg - 1;
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if ((int64_t)seg_end[mid] * p.rep > a) hi = mid;
+                    else lo = mid + 1;
+                }
+                const Seg g = p.seg(lo);
+                const int64_t first = (int64_t)(seg_end[lo] - g.ntiles) * p.rep;
+                v = p.steps(g, (int)((a - first) % g.ntiles));
+            }
+            if (pass == 1 && at >= before + sum && at < before + sum + v) {
+                found = l;
+                off = (int)(at - before - sum);
+                break;
+            }
+            sum += v;
+        }
+        if (pass == 0) {
+            Start st;
+            const int64_t ex = block_scan<NT>(sum, red, &st.tot);
+            const int64_t most = (st.tot + min_share - 1) / min_share;
+            st.items = tab.items;
+            st.n = most < 1 ? 1 : (most < (int64_t)gridDim.x ? (int)most : (int)gridDim.x);
+            at = share_at(st.tot, st.n, blockIdx.x);
+            st.count = share_at(st.tot, st.n, blockIdx.x + 1) - at;
+            st.place = 0;
+            st.off = 0;
+            __syncthreads();
+            if (tid == 0) *out = st;
+            __syncthreads();
+            const bool mine = st.count > 0 && at >= ex && at < ex + sum;
+            sum = ex;
+            if (!mine) break;
+        }
+    }
+    if (found >= 0) {
+        out->place = found;
+        out->off = off;
+    }
     __syncthreads();
 }
 
-// Walks the tiles of a CTA's share.
+// A tile of a CTA's share: steps s0 .. s0 + ns - 1 of its n.
 struct Item {
     int seg, rep, tile;
-    int s0, ns, n;  // steps s0 .. s0 + ns - 1 of the tile's n
+    int s0, ns, n;
     Seg g;
     __device__ __forceinline__ bool whole() const { return ns == n; }
     // where a piece's partial result goes
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (s0 == 0); }
 };
 
+// Walks the tiles of a CTA's share.  With several segments all lanes of a warp
+// walk together.
 template <typename P>
 struct Walk {
     const P& p;
+    Table tab;
     int64_t left;
-    int seg, rep, tile, off;
+    int col;
+    int64_t row, height;
+    int off;
+    int seg;       // segment that holds tile number seg0 ..
+    int64_t seg0;
     Seg g;
     __device__ __forceinline__ Walk(const P& prob, const Start& st)
-        : p(prob), left(st.count), seg(st.seg), rep(st.rep), tile(st.tile), off(st.off) {
-        if (left > 0) g = p.seg(seg);
+        : p(prob), tab{st.items, (int)gridDim.x}, left(st.count), off(st.off), seg(0), seg0(0) {
+        if (left > 0) {
+            tab.place(st.place, &col, &row);
+            height = tab.height(col);
+            if (p.nseg == 1) g = p.seg(0);
+        }
     }
     __device__ __forceinline__ bool next(Item& it) {
         if (left <= 0) return false;
-        while (tile >= g.ntiles) {  // next repetition, or next segment with tiles
-            tile = 0;
-            if (g.ntiles == 0 || ++rep >= p.rep) {
-                rep = 0;
-                if (++seg >= p.nseg) {
-                    left = 0;
-                    return false;
+        if (row >= height) {
+            ++col;
+            row = 0;
+            height = tab.height(col);
+            seg = 0;
+            seg0 = 0;
+        }
+        const int64_t a = tab.number(col, row++);
+        if (p.nseg > 1) {
+            // 32 segments at a time: the one that holds tile number a
+            const int lane = threadIdx.x & 31;
+            while (true) {
+                const int s = seg + lane;
+                const Seg h = s < p.nseg ? p.seg(s) : Seg{0, 0, 0, 0};
+                int64_t end = (int64_t)h.ntiles * p.rep;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+                    if (lane >= o) end += y;
                 }
-                g = p.seg(seg);
+                end += seg0;
+                const unsigned m = __ballot_sync(0xffffffffu, end > a);
+                if (m == 0 && seg + 32 < p.nseg) {
+                    seg += 32;
+                    seg0 = __shfl_sync(0xffffffffu, end, 31);
+                    continue;
+                }
+                const int src = m ? __ffs(m) - 1 : 31;  // m != 0: a lies below the last segment's end
+                seg += src;
+                seg0 = __shfl_sync(0xffffffffu, end - (int64_t)h.ntiles * p.rep, src);
+                g.t0 = __shfl_sync(0xffffffffu, h.t0, src);
+                g.qlen = __shfl_sync(0xffffffffu, h.qlen, src);
+                g.kvlen = __shfl_sync(0xffffffffu, h.kvlen, src);
+                g.ntiles = __shfl_sync(0xffffffffu, h.ntiles, src);
+                break;
             }
         }
         it.seg = seg;
-        it.rep = rep;
-        it.tile = tile;
+        it.rep = (int)((a - seg0) / g.ntiles);
+        it.tile = (int)((a - seg0) % g.ntiles);
         it.g = g;
-        it.n = p.steps(g, tile);
+        it.n = p.steps(g, it.tile);
         it.s0 = off;
         it.ns = it.n - off;
         if (it.ns > left) it.ns = (int)left;
         left -= it.ns;
         off = 0;
-        ++tile;
         return true;
     }
 };
 
 // The record of a tile that begins in this CTA and is cut at its end.
-__device__ __forceinline__ void write_cut(Cut* cuts, const Item& it, const Start& st) {
-    int left = it.n - it.ns, pieces = 1;
+__device__ __forceinline__ void write_cut(Cut* cuts, int seg, int rep, int tile, int left, const Start& st) {
+    int pieces = 1;  // left: the tile's steps after this CTA's
     for (int c = blockIdx.x + 1; left > 0 && c < st.n; ++c) {
         const int64_t sh = share_at(st.tot, st.n, c + 1) - share_at(st.tot, st.n, c);
         if (sh <= 0) continue;
         left -= (int)(sh < left ? sh : left);
         ++pieces;
     }
-    Cut c{pieces, it.seg, it.rep, it.tile, st.tot, st.n, 0};
+    Cut c{pieces, seg, rep, tile, st.tot, st.n, 0};
     cuts[blockIdx.x] = c;
 }
 

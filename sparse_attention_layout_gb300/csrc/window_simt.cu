@@ -168,7 +168,7 @@ __global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
     __shared__ int pages[R];  // page of each key's slot in this step
     const Prob& p = A.p;
     report_bad_segs(p);
-    locate<kT>(p, gridDim.x, A.min_share, reinterpret_cast<int*>(sm), red, &start);
+    locate<kT>(p, A.min_share, reinterpret_cast<int*>(sm), red, &start);
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
             if (A.lse && tx == 0)
                 A.lse[w.z * A.lz + h * A.lh + t * A.lt] = l[u] > 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it, start);
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, start);
     }
 }
 
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kT) dq_kernel(const Args A) {
     __shared__ Start start;
     __shared__ int64_t red[32];
     const Prob& p = A.p;
-    locate<kT>(p, gridDim.x, A.min_share, reinterpret_cast<int*>(sm), red, &start);
+    locate<kT>(p, A.min_share, reinterpret_cast<int*>(sm), red, &start);
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(kT) dq_kernel(const Args A) {
                     store4(dst + c, a.x * A.scale, a.y * A.scale, b.x * A.scale, b.y * A.scale);
             }
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it, start);
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, start);
     }
 }
 
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kT) dkv_kernel(const Args A, const KProb kp) {
     __shared__ int64_t red[32];
     __shared__ float lse_s[R], del_s[R];
     const Prob& p = A.p;
-    locate<kT>(kp, gridDim.x, A.min_share, reinterpret_cast<int*>(sm), red, &start);
+    locate<kT>(kp, A.min_share, reinterpret_cast<int*>(sm), red, &start);
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kT) dkv_kernel(const Args A, const KProb kp) {
                 }
             }
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it, start);
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, start);
     }
 }
 
