@@ -60,7 +60,6 @@ struct Args {
     int min_share;
     Cut* cuts;
     float* slots;
-    uint64_t wait_ns;
 };
 
 template <typename T, int DP, bool PAGED>
@@ -90,10 +89,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     __shared__ Start start;
     __shared__ int64_t red[32];
     __shared__ Ring ring;
+    __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Abort ab{&abort_flag, p.status, args.wait_ns};
+    Abort ab{&abort_flag, p.status, kDefaultWaitNs};
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -121,7 +121,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
         ring.init();
         fence_barrier_init();
-        args.cuts[blockIdx.x].pieces = 0;
+        cut.ns = 0;
     }
     if (PAGED && blockIdx.x == 0)
         for (int s = threadIdx.x; s < p.nseg; s += kThreads)
@@ -149,78 +149,83 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (!is_v) tma_prefetch_desc(&tmQ);
             tma_prefetch_desc(tm);
         }
-        uint32_t i = 0, g = 0, lands = 0;
+        uint32_t i = 0, g = 0, tiles = 0, lands = 0;  // Q tiles, steps, tiles handed out, scrubbed tiles
         const uint32_t q_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
         const int pages = PAGED ? 128 >> p.page_shift : 1;  // copies per 64 columns
         const int my_page = lane % pages, my_panel = lane / pages;
         const uint32_t page_bytes = PAGED ? 128u << p.page_shift : 128u * 128u;
-        Walk<Prob> walk(p, start);
-        Item it;
+        Walk<Prob, PAGED> walk(p, start);
         Work w;
-        bool live = true;
-        // the next tile, ready before this one's last step
-        auto advance = [&]() {
-            if (is_v) {
-                live = ring.take(i, w, lane == 0, true, ab);
-                ++i;
-                return;
-            }
-            live = walk.next(it);
-            if (live) w = make_work(p, it);
-        };
-        // this lane's page of step n: -1 hidden (not copied)
-        auto lookup = [&](int n) {
-            const Keys keys = tile_keys(p, w);
-            const int a = (w.key_tile(n) << 7) + (my_page << p.page_shift);
-            if (!keys.any(a, a + (1 << p.page_shift) - 1)) return -1;
-            const int pg = p.table[(int64_t)w.seg * p.max_pages + (a >> p.page_shift)];
-            return (unsigned)pg < (unsigned)p.n_pages ? pg : -2;  // -2: a bad page
-        };
-        advance();
-        int pg = 0;
-        if (PAGED && live) pg = lookup(0);
-        while (live) {
-            if (!is_v) {
-                if (!ring.put(i, w, lane, ab)) break;
-                const uint32_t qs = i % QST;
-                bool ok = mbar_wait(&q_empty[qs], ((i / QST) & 1) ^ 1, ab);
-                if (!__all_sync(0xffffffffu, ok)) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&q_full[qs], q_bytes);
-                    for (int c = 0; c < KP; ++c)
-                        tma_load_4d(smem_u32(smem + SM::kQ + qs * kTileBytes + c * 16384), &tmQ, c * 64, w.hk * p.G,
-                                    w.row0, w.z, &q_full[qs]);
+        // one step is loaded while the next one's place, and its page number,
+        // are on their way
+        struct Step {
+            int kb, pg, hk, z, row0, zlo, zhi;
+            Keys keys;
+            bool first;  // of its tile
+        } cur, nxt;
+        bool have = false;
+        int n = 0;
+        w.ns = 0;
+#pragma unroll 1
+        while (true) {
+            bool more = true;
+            if (n >= w.ns) {
+                if (is_v) {
+                    more = ring.take(tiles, w, lane == 0, true, ab);
+                } else {
+                    Item it;
+                    w.ns = 0;
+                    if (walk.next(it)) w = make_work(p, it);
+                    more = ring.put(tiles, w, lane, ab) && w.ns > 0;
                 }
-                ++i;
+                ++tiles;
+                n = 0;
             }
-            const int ns = w.ns, hk = w.hk, z = w.z, zlo = w.zlo, zhi = w.zhi;
-            const Keys keys = tile_keys(p, w);
-            for (int n = 0; n < ns; ++n) {
-                const int kb = w.key_tile(n) << 7, my_pg = pg;
-                const bool want = PAGED ? my_pg >= 0 && my_panel < KP : lane < KP;
-                // the next step's page number is on its way while this step waits
-                if (n + 1 == ns && !is_v) {
-                    advance();
-                    if (PAGED && live) pg = lookup(0);
-                } else if (n + 1 < ns) {
-                    if (PAGED) pg = lookup(n + 1);
+            if (more) {
+                nxt.kb = w.key_tile(n) << 7;
+                nxt.hk = w.hk, nxt.z = w.z, nxt.row0 = w.row0, nxt.zlo = w.zlo, nxt.zhi = w.zhi;
+                nxt.keys = tile_keys(p, w);
+                nxt.first = n == 0;
+                if (PAGED) {  // -1: hidden (not copied), -2: a bad page
+                    const int a = nxt.kb + (my_page << p.page_shift);
+                    nxt.pg = -1;
+                    if (nxt.keys.any(a, a + (1 << p.page_shift) - 1)) {
+                        nxt.pg = p.table[(int64_t)w.seg * p.max_pages + (a >> p.page_shift)];
+                        if ((unsigned)nxt.pg >= (unsigned)p.n_pages) nxt.pg = -2;
+                    }
                 }
-                if (PAGED && __any_sync(0xffffffffu, my_pg == -2)) {
+            }
+            if (have) {
+                if (!is_v && cur.first) {
+                    const uint32_t qs = i % QST;
+                    bool ok = wait(&q_empty[qs], ((i / QST) & 1) ^ 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&q_full[qs], q_bytes);
+#pragma unroll 1
+                        for (int c = 0; c < KP; ++c)
+                            tma_load_4d(smem_u32(smem + SM::kQ + qs * kTileBytes + c * 16384), &tmQ, c * 64, cur.hk * p.G,
+                                        cur.row0, cur.z, &q_full[qs]);
+                    }
+                    ++i;
+                }
+                if (PAGED && __any_sync(0xffffffffu, cur.pg == -2)) {
                     if (lane == 0) ab.fail(BSP_ERR_DEVICE_CHECK);
-                    goto load_done;
+                    break;
                 }
+                const bool want = PAGED ? cur.pg >= 0 && my_panel < KP : lane < KP;
                 const uint32_t st = g % NST;
                 if (g >= NST) {
                     const uint32_t gp = g - NST;
                     uint64_t* freed = is_v ? &pv_done[gp % 3] : &s_full[gp % 3];
-                    bool ok = mbar_wait(freed, (gp / 3) & 1, ab);
-                    if (!__all_sync(0xffffffffu, ok)) goto load_done;
+                    bool ok = wait(freed, (gp / 3) & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) break;
                 }
                 const uint32_t bytes = PAGED ? page_bytes * __popc(__ballot_sync(0xffffffffu, want)) : kTileBytes;
                 uint64_t* full = is_v ? &v_full[st] : &k_full[st];
                 // rows of this V tile that no query of the sequence sees
-                const bool scrub =
-                    is_v && bytes > 0 && ((kb + 127 > zhi && PAGED) || (kb < zlo && !(kb + 127 < p.sinks)));
+                const bool scrub = is_v && bytes > 0 &&
+                                   ((cur.kb + 127 > cur.zhi && PAGED) || (cur.kb < cur.zlo && !(cur.kb + 127 < p.sinks)));
                 uint64_t* bar = scrub ? &v_land : full;
                 if (lane == 0) {
                     if (bytes) mbar_arrive_expect_tx(bar, bytes);
@@ -230,25 +235,26 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t base = smem_u32(smem + (is_v ? SM::kV : SM::kK) + st * kTileBytes);
                 if (want) {
                     if (PAGED)
-                        tma_load_4d(base + my_panel * 16384 + my_page * page_bytes, tm, my_panel * 64, 0, hk, my_pg, bar);
+                        tma_load_4d(base + my_panel * 16384 + my_page * page_bytes, tm, my_panel * 64, 0, cur.hk, cur.pg, bar);
                     else
-                        tma_load_4d(base + lane * 16384, tm, lane * 64, kb, hk, z, bar);
+                        tma_load_4d(base + lane * 16384, tm, lane * 64, cur.kb, cur.hk, cur.z, bar);
                 }
                 if (scrub) {
-                    bool ok = mbar_wait(&v_land, lands & 1, ab);
+                    bool ok = wait(&v_land, lands & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) {
                         if (lane == 0) mbar_drain(&v_land, lands & 1, ab);
-                        goto load_done;
+                        break;
                     }
                     ++lands;
+#pragma unroll 1
                     for (int r = lane; r < 128; r += 32) {
-                        const int j = kb + r, j16 = kb + (r & ~15);
-                        const bool used = j <= zhi && (j >= zlo || j < p.sinks);
-                        if (!used && keys.any(j16, j16 + 15))
-                            for (int c = 0; c < KP; ++c)
-                                for (int k = 0; k < 8; ++k)
-                                    *reinterpret_cast<uint4*>(smem + SM::kV + st * kTileBytes + c * 16384 + r * 128 +
-                                                              k * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        const int j = cur.kb + r, j16 = cur.kb + (r & ~15);
+                        const bool used = j <= cur.zhi && (j >= cur.zlo || j < p.sinks);
+                        if (!used && cur.keys.any(j16, j16 + 15))
+#pragma unroll 1
+                            for (int k = 0; k < KP * 8; ++k)
+                                *reinterpret_cast<uint4*>(smem + SM::kV + st * kTileBytes + (k >> 3) * 16384 + r * 128 +
+                                                          (k & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     fence_proxy_async_smem();
                     __syncwarp();
@@ -256,16 +262,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 }
                 ++g;
             }
-            if (is_v) {
-                advance();
-                if (PAGED && live) pg = lookup(0);
-            }
+            if (!more) break;
+            cur = nxt;
+            have = true;
+            ++n;
         }
-        if (!is_v && !live) {  // no further tile: the readers stop
-            Work end{};
-            ring.put(i, end, lane, ab);
-        }
-    load_done:
         if (lane == 0) {
             if (is_v) {
                 issued[2] = g;
@@ -284,11 +285,12 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             for (; ring.take(i, w, true, false, ab); ++i) {
                 const uint32_t qs = i % QST;
                 const int ns = w.ns;
-                if (!mbar_wait(&q_full[qs], (i / QST) & 1, ab)) goto qk_done;
+                if (!wait(&q_full[qs], (i / QST) & 1, ab)) goto qk_done;
+#pragma unroll 1
                 for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g % NST, sb = g % 3;
-                    if (g >= 3 && !mbar_wait(&pv_done[sb], ((g - 3) / 3) & 1, ab)) goto qk_done;
-                    if (!mbar_wait(&k_full[st], (g / NST) & 1, ab)) goto qk_done;
+                    if (g >= 3 && !wait(&pv_done[sb], ((g - 3) / 3) & 1, ab)) goto qk_done;
+                    if (!wait(&k_full[st], (g / NST) & 1, ab)) goto qk_done;
                     tc_fence_after();
                     const uint64_t aq = dq + ((qs * kTileBytes) >> 4), bk = dk + ((st * kTileBytes) >> 4);
 #pragma unroll
@@ -311,8 +313,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             Work w;
             while (ring.take(tc, w, true, false, ab)) {
                 const Keys keys = tile_keys(p, w);
-                if (tc > 0 && !mbar_wait(&o_empty, (tc - 1) & 1, ab)) goto pv_done_label;
+                if (tc > 0 && !wait(&o_empty, (tc - 1) & 1, ab)) goto pv_done_label;
                 uint32_t acc = 0;
+#pragma unroll 1
                 for (int n = 0; n < w.ns; ++n, ++g) {
                     const uint32_t st = g % NST, sb = g % 3;
                     const int kb = w.key_tile(n) << 7;
@@ -321,8 +324,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         pieces |= keys.any(kb + ks * 16, kb + ks * 16 + 15) ? 1u << ks : 0u;
-                    if (!mbar_wait(&v_full[st], (g / NST) & 1, ab)) goto pv_done_label;
-                    if (!mbar_wait(&p_full[sb], (g / 3) & 1, ab)) goto pv_done_label;
+                    if (!wait(&v_full[st], (g / NST) & 1, ab)) goto pv_done_label;
+                    if (!wait(&p_full[sb], (g / 3) & 1, ab)) goto pv_done_label;
                     tc_fence_after();
                     if (pieces == 0xffu) {
 #pragma unroll
@@ -359,7 +362,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         while (ring.take(tc, w, lane == 0, true, ab)) {
             const int rows = w.nt * p.G, hk = w.hk, z = w.z, t0 = w.row0;
             const uint32_t lb = tc & 1;
-            bool ok = mbar_wait(&l_full[lb], (tc >> 1) & 1, ab);
+            bool ok = wait(&l_full[lb], (tc >> 1) & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             const float m0 = lref[lb][0][row], m1 = lref[lb][1][row];
             const float l0 = lsum[lb][0][row], l1 = lsum[lb][1][row];
@@ -369,7 +372,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const float lt = mf == -INFINITY ? 0.f : l0 * ex2_approx(m0 - mf) + l1 * ex2_approx(m1 - mf);
             const bool seen = lt > 0.f;
             const float inv = seen ? 1.0f / lt : 0.f;
-            ok = mbar_wait(&o_full, tc & 1, ab);
+            ok = wait(&o_full, tc & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             ++tc;
@@ -401,7 +404,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     slot[kTcRows * kSlotD + row] = mf;
                     slot[kTcRows * kSlotD + kTcRows + row] = lt;
                 }
-                if (threadIdx.x == 128 && w.s0 == 0) write_cut(args.cuts, w.seg, w.rep, w.tile, w.n - w.ns, start);
+                if (threadIdx.x == 128 && w.s0 == 0) cut = w;
                 continue;
             }
             if (args.lse && row < rows) {
@@ -409,35 +412,31 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 args.lse[z * args.lz + (hk * p.G + h) * args.lh + (t0 + t) * args.lt] =
                     seen ? (mf + log2f(lt)) * kLn2 : -INFINITY;
             }
-            // every column of O is read out of TMEM before the accumulator is
-            // handed to the next tile; then 64 columns at a time pass through
-            // the warp's staging panel, so that 8 lanes write 128 contiguous
-            // bytes of a row
-            uint32_t pk[KP][32];
-#pragma unroll
+            // 64 columns at a time, out of TMEM and through the warp's staging
+            // panel; the accumulator is the next tile's once all are read
+#pragma unroll 1
             for (int c = 0; c < KP; ++c) {
+                uint32_t pk[32];
+                {
+                    uint32_t r[64];
+                    tmem_ld64_sync(tO + lane_base + c * 64, tO + lane_base + c * 64 + 32, r);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t r[32];
-                    tmem_ld32_sync(tO + lane_base + c * 64 + h * 32, r);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)
-                        pk[c][h * 16 + k] = seen ? Pack2<T>::pack(__uint_as_float(r[2 * k]) * inv,
-                                                                  __uint_as_float(r[2 * k + 1]) * inv)
-                                                 : 0u;
+                    for (int k = 0; k < 32; ++k)
+                        pk[k] = seen ? Pack2<T>::pack(__uint_as_float(r[2 * k]) * inv, __uint_as_float(r[2 * k + 1]) * inv)
+                                     : 0u;
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&o_empty);
-#pragma unroll
-            for (int c = 0; c < KP; ++c)
-                store_panel<T>(stage, pk[c], lane, args.D - c * 64, [&](int i) -> T* {
+                if (c == KP - 1) {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_empty);
+                }
+                store_panel<T>(stage, pk, lane, args.D - c * 64, [&](int i) -> T* {
                     const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
                     if (r >= rows) return nullptr;
                     return static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
                            (int64_t)(t0 + t) * args.O.s[2] + c * 64;
                 });
+            }
         }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -484,13 +483,14 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             const bool idle = quad * 32 >= rows;  // no live row in this warp's lanes
             const int low = pos - p.window + 1;
             float l = 0.f, m = -INFINITY;
+#pragma unroll 1
             for (int n = 0; n < ns; ++n, ++g) {
                 const uint32_t sb = g % 3;
                 const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
                 const int kb = (kt << 7) + wg * 64;  // first key of this half
                 const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
                 const bool skip = __all_sync(0xffffffffu, vis == 0), full = __all_sync(0xffffffffu, vis == ~0ull);
-                bool ok = mbar_wait(&s_full[sb], (g / 3) & 1, ab);
+                bool ok = wait(&s_full[sb], (g / 3) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                 if (idle) {
                     __syncwarp();
@@ -512,7 +512,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&x_full[xb][quad]);
-                ok = mbar_wait(&x_full[xb][quad], xph, ab);
+                ok = wait(&x_full[xb][quad], xph, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                 tc_fence_after();
                 const float mrow = fmaxf(mx, xm[xb][wg ^ 1][row]);
@@ -532,11 +532,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 // rows that saw nothing yet have O = 0, which no factor changes
                 const bool grew = need && m != -INFINITY;
                 if (__any_sync(0xffffffffu, grew)) {
-                    ok = mbar_wait(&pv_done[(g - 1) % 3], ((g - 1) / 3) & 1, ab);
+                    ok = wait(&pv_done[(g - 1) % 3], ((g - 1) / 3) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                     tc_fence_after();
                     const float alpha = grew ? ex2_approx(m - mnext) : 1.f;
-#pragma unroll
+#pragma unroll 1
                     for (int cc = 0; cc < DP / 64; ++cc) {
                         uint32_t r[32];
                         const uint32_t ta = tO + lane_base + wg * (DP / 2) + cc * 32;
@@ -560,7 +560,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             {
                 const uint32_t lb = tc & 1;
                 if (tc >= 2) {
-                    bool ok = mbar_wait(&l_empty[lb], ((tc - 2) >> 1) & 1, ab);
+                    bool ok = wait(&l_empty[lb], ((tc - 2) >> 1) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                 }
                 lsum[lb][wg][row] = m == -INFINITY ? 0.f : l;
@@ -575,6 +575,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) {
+        args.cuts[blockIdx.x].pieces = 0;
+        if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
+    }
     if (abort_flag) {
         // the copies and products issued before the stop land before the CTA
         // lets go of its shared memory and TMEM
@@ -607,7 +611,7 @@ int launch(Call& c) {
     constexpr int smem = Smem<DP>::kAlloc;
     if ((rc = prepare_kernel(kern, smem))) return rc;
     const int grid = sm_count();
-    Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, 2, c.cuts, c.slots, kDefaultWaitNs};
+    Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, 2, c.cuts, c.slots};
     kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     return launch_join(c, kTcRows, grid, false);

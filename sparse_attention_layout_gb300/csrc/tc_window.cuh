@@ -18,6 +18,27 @@ constexpr int kThreads = 512;
 constexpr uint32_t kRegsLaunch = 128, kRegsCtl = 80, kRegsEpi = 128, kRegsSoftmax = 152;
 static_assert(kRegsCtl + kRegsEpi + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "register split exceeds the launch allocation");
 
+// mbar_wait for these kernels: as bounded, fewer instructions.  The roles' loops
+// have to stay in the instruction cache together, and each holds several waits.
+__device__ __forceinline__ uint32_t globaltimer_lo() {
+    uint32_t t;
+    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
+    return t;
+}
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Abort& ab) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint32_t t0 = globaltimer_lo();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*ab.flag) return false;
+        if (globaltimer_lo() - t0 > (uint32_t)kDefaultWaitNs) {  // 2 s, below the 2^32 ns of the counter
+            ab.fail(BSP_ERR_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+static_assert(kDefaultWaitNs < (1ull << 32), "the wait limit is counted in 32 bits");
+
 // Visible keys of a tile's rows: j <= hi and (j >= lo or j < sinks).
 struct Keys {
     int lo, hi, sinks;
@@ -57,7 +78,7 @@ struct Ring {
     // by a whole warp, in order i = 0, 1, ...
     __device__ __forceinline__ bool put(uint32_t i, const Work& x, int lane, const Abort& ab) {
         const uint32_t s = i % kRing;
-        const bool ok = mbar_wait(&empty[s], ((i / kRing) & 1) ^ 1, ab);
+        const bool ok = wait(&empty[s], ((i / kRing) & 1) ^ 1, ab);
         if (!__all_sync(0xffffffffu, ok)) return false;
         if (lane == 0) {
             w[s] = x;
@@ -68,7 +89,7 @@ struct Ring {
     // by one thread, or by all lanes of a warp (`one`: the lane that answers)
     __device__ __forceinline__ bool take(uint32_t i, Work& x, bool one, bool warp, const Abort& ab) {
         const uint32_t s = i % kRing;
-        bool ok = mbar_wait(&full[s], (i / kRing) & 1, ab);
+        bool ok = wait(&full[s], (i / kRing) & 1, ab);
         if (warp) ok = __all_sync(0xffffffffu, ok);
         if (!ok) return false;
         x = w[s];
@@ -131,7 +152,7 @@ __device__ __forceinline__ void store_panel(uint8_t* stage, const uint32_t (&pk)
             make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
     __syncwarp();
     const int j = lane & 7;
-#pragma unroll
+#pragma unroll 2
     for (int i = 0; i < 8; ++i) {
         const int r = i * 4 + (lane >> 3);
         const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ (r & 7)) << 4));

@@ -27,7 +27,6 @@ struct Args {
     int min_share;
     Cut* cuts;
     float* slots;
-    uint64_t wait_ns;
 };
 
 template <int DP>
@@ -66,27 +65,26 @@ __device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, 
         if (lane == 0) mbar_arrive(empty);
         return;
     }
-    uint32_t pk[DP / 64][32];
+#pragma unroll 1
+    for (int c = 0; c < DP / 64; ++c) {
+        uint32_t pk[32];
+        {
+            uint32_t r[64];
+            tmem_ld64_sync(tacc + c * 64, tacc + c * 64 + 32, r);
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t r[32];
-            tmem_ld32_sync(tacc + c * 64 + h * 32, r);
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                pk[c][h * 16 + k] =
-                    Pack2<T>::pack(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
+            for (int k = 0; k < 32; ++k)
+                pk[k] = Pack2<T>::pack(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
         }
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(empty);
-#pragma unroll
-    for (int c = 0; c < DP / 64; ++c)
-        store_panel<T>(stage, pk[c], lane, D - c * 64, [&](int i) -> T* {
+        if (c == DP / 64 - 1) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty);
+        }
+        store_panel<T>(stage, pk, lane, D - c * 64, [&](int i) -> T* {
             T* p = dst(i);
             return p ? p + c * 64 : nullptr;
         });
+    }
 }
 
 // ------------------------------------------------------------------- dQ ----
@@ -117,10 +115,11 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __shared__ Start start;
     __shared__ int64_t red[32];
     __shared__ Ring ring;
+    __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Abort ab{&abort_flag, p.status, args.wait_ns};
+    Abort ab{&abort_flag, p.status, kDefaultWaitNs};
     if (threadIdx.x == 0) {
         abort_flag = 0;
         issued_a = 0;
@@ -140,7 +139,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         mbar_init(&acc_empty, 4);
         ring.init();
         fence_barrier_init();
-        args.cuts[blockIdx.x].pieces = 0;
+        cut.ns = 0;
     }
     if (warp == 1) {
         tmem_alloc(&tmem_base, 512);
@@ -165,7 +164,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             }
             const uint32_t a_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
-            Walk<Prob> walk(p, start);
+            Walk<Prob, false> walk(p, start);
             Item it;
             Work w;
             while (true) {
@@ -178,7 +177,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 }
                 // the previous tile's S and dP products have read Q and dO
                 if (tiles > 0) {
-                    const bool ok = mbar_wait(&a_free, (tiles - 1) & 1, ab);
+                    const bool ok = wait(&a_free, (tiles - 1) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto load_done;
                 }
                 if (lane == 0) {
@@ -188,12 +187,13 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                                     w.z, &a_full);
                 }
                 ++tiles;
+#pragma unroll 1
                 for (int n = 0; n < w.ns; ++n, ++g) {
                     const uint32_t st = g & 1;
                     // K of step g - 2 is free after its dQ product, V after its dP product,
                     // which the same step's dS follows
                     if (g >= 2) {
-                        const bool ok = mbar_wait(&dq_done[st], ((g - 2) >> 1) & 1, ab);
+                        const bool ok = wait(&dq_done[st], ((g - 2) >> 1) & 1, ab);
                         if (!__all_sync(0xffffffffu, ok)) goto load_done;
                     }
                     uint64_t* full = is_v ? &v_full[st] : &k_full[st];
@@ -220,11 +220,12 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             Work w;
             while (ring.take(tiles, w, true, false, ab)) {
                 const int ns = w.ns;
-                if (!mbar_wait(&a_full, tiles & 1, ab)) goto score_done;
+                if (!wait(&a_full, tiles & 1, ab)) goto score_done;
+#pragma unroll 1
                 for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g & 1;
-                    if (g >= 2 && !mbar_wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto score_done;
-                    if (!mbar_wait(&k_full[st], (g >> 1) & 1, ab)) goto score_done;
+                    if (g >= 2 && !wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto score_done;
+                    if (!wait(&k_full[st], (g >> 1) & 1, ab)) goto score_done;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < DP / 16; ++ks) {
@@ -232,11 +233,11 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         mma_f16(tS + st * 128, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
                     }
                     mma_commit(&s_full[st]);
-                    if (g >= 1 && !mbar_wait(&dp_free, (g - 1) & 1, ab)) {
+                    if (g >= 1 && !wait(&dp_free, (g - 1) & 1, ab)) {
                         ++g;
                         goto score_done;
                     }
-                    if (!mbar_wait(&v_full[st], (g >> 1) & 1, ab)) {
+                    if (!wait(&v_full[st], (g >> 1) & 1, ab)) {
                         ++g;
                         goto score_done;
                     }
@@ -260,10 +261,11 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             Work w;
             while (ring.take(tiles, w, true, false, ab)) {
                 const int ns = w.ns;
-                if (tiles > 0 && !mbar_wait(&acc_empty, (tiles - 1) & 1, ab)) goto dq_end;
+                if (tiles > 0 && !wait(&acc_empty, (tiles - 1) & 1, ab)) goto dq_end;
+#pragma unroll 1
                 for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g & 1;
-                    if (!mbar_wait(&ds_full[st], (g >> 1) & 1, ab)) goto dq_end;
+                    if (!wait(&ds_full[st], (g >> 1) & 1, ab)) goto dq_end;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
@@ -286,7 +288,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         Work w;
         while (ring.take(tiles, w, lane == 0, true, ab)) {
             const int rows = w.nt * p.G, hk = w.hk, z = w.z;
-            const bool ok = mbar_wait(&acc_full, tiles & 1, ab);
+            const bool ok = wait(&acc_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             ++tiles;
@@ -298,8 +300,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                              return static_cast<T*>(args.dQ.ptr) + z * args.dQ.s[0] + (hk * p.G + h) * args.dQ.s[1] +
                                     (int64_t)(w.row0 + t) * args.dQ.s[2];
                          });
-            if (threadIdx.x == 128 && w.s0 == 0 && !w.whole())
-                write_cut(args.cuts, w.seg, w.rep, w.tile, w.n - w.ns, start);
+            if (threadIdx.x == 128 && w.s0 == 0 && !w.whole()) cut = w;
         }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -321,13 +322,14 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 pos = row < w.nt * p.G ? w.a + (int)((row * inv_g) >> 16) : -1;
             }
             const int low = pos - p.window + 1;
+#pragma unroll 1
             for (int n = 0; n < ns; ++n, ++g) {
                 const uint32_t st = g & 1;
                 const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
                 const int kb = (kt << 7) + wg * 64;
                 const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
                 const bool full = __all_sync(0xffffffffu, vis == ~0ull);
-                bool ok = mbar_wait(&s_full[st], (g >> 1) & 1, ab);
+                bool ok = wait(&s_full[st], (g >> 1) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 const uint32_t ts = tS + st * 128 + lane_base + wg * 64;
@@ -341,7 +343,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     x[j] = ex2_approx(y.x);
                     x[j + 1] = ex2_approx(y.y);
                 }
-                ok = mbar_wait(&dp_full, g & 1, ab);
+                ok = wait(&dp_full, g & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 uint32_t pk[32];
@@ -371,6 +373,10 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) {
+        args.cuts[blockIdx.x].pieces = 0;
+        if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
+    }
     if (abort_flag) {
         if (threadIdx.x == 0) {
             mbar_drain_ring(k_full, 2, issued[0], ab);
@@ -416,10 +422,11 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     __shared__ Start start;
     __shared__ int64_t red[32];
     __shared__ Ring ring;
+    __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Abort ab{&abort_flag, p.status, args.wait_ns};
+    Abort ab{&abort_flag, p.status, kDefaultWaitNs};
     if (threadIdx.x == 0) {
         abort_flag = 0;
         issued_a = issued_k = 0;
@@ -442,7 +449,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         mbar_init(&dk_empty, 4);
         ring.init();
         fence_barrier_init();
-        args.cuts[blockIdx.x].pieces = 0;
+        cut.ns = 0;
     }
     if (warp == 1) {
         tmem_alloc(&tmem_base, 512);
@@ -472,7 +479,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             }
             const uint32_t bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
-            Walk<KProb> walk(kp, start);
+            Walk<KProb, false> walk(kp, start);
             Item it;
             Work w;
             while (true) {
@@ -491,7 +498,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
                 // the previous tile's score products have read K and V
                 if (tiles > 0) {
-                    const bool ok = mbar_wait(&a_free, (tiles - 1) & 1, ab);
+                    const bool ok = wait(&a_free, (tiles - 1) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto load_done;
                 }
                 if (lane == 0) {
@@ -501,10 +508,11 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                                     w.z, &a_full);
                 }
                 ++tiles;
+#pragma unroll 1
                 for (int n = 0; n < w.ns; ++n, ++g) {
                     const uint32_t st = g & 1;
                     if (g >= 2) {
-                        const bool ok = mbar_wait(&dk_done[st], ((g - 2) >> 1) & 1, ab);
+                        const bool ok = wait(&dk_done[st], ((g - 2) >> 1) & 1, ab);
                         if (!__all_sync(0xffffffffu, ok)) goto load_done;
                     }
                     uint64_t* full = is_g ? &g_full[st] : &q_full[st];
@@ -534,11 +542,12 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             Work w;
             while (ring.take(tiles, w, true, false, ab)) {
                 const int ns = w.ns;
-                if (!mbar_wait(&a_full, tiles & 1, ab)) goto score_done;
+                if (!wait(&a_full, tiles & 1, ab)) goto score_done;
+#pragma unroll 1
                 for (int n = 0; n < ns; ++n) {
                     const uint32_t st = g & 1;
-                    if (g >= 1 && !mbar_wait(&dv_done, (g - 1) & 1, ab)) goto score_done;
-                    if (!mbar_wait(&q_full[st], (g >> 1) & 1, ab)) goto score_done;
+                    if (g >= 1 && !wait(&dv_done, (g - 1) & 1, ab)) goto score_done;
+                    if (!wait(&q_full[st], (g >> 1) & 1, ab)) goto score_done;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < DP / 16; ++ks) {
@@ -547,8 +556,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     }
                     mma_commit(&s_full);
                     ++g;
-                    if (gd >= 1 && !mbar_wait(&dk_done[(gd - 1) & 1], ((gd - 1) >> 1) & 1, ab)) goto score_done;
-                    if (!mbar_wait(&g_full[st], (gd >> 1) & 1, ab)) goto score_done;
+                    if (gd >= 1 && !wait(&dk_done[(gd - 1) & 1], ((gd - 1) >> 1) & 1, ab)) goto score_done;
+                    if (!wait(&g_full[st], (gd >> 1) & 1, ab)) goto score_done;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < DP / 16; ++ks) {
@@ -572,11 +581,12 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             Work w;
             while (ring.take(tiles, w, true, false, ab)) {
                 const int ns = w.ns;
+#pragma unroll 1
                 for (int n = 0; n < ns; ++n) {
                     const uint32_t st = g & 1;
-                    if (n == 0 && tiles > 0 && !mbar_wait(&dv_empty, (tiles - 1) & 1, ab)) goto grad_done;
-                    if (!mbar_wait(&p_full, g & 1, ab)) goto grad_done;
-                    if (!mbar_wait(&g_full[st], (g >> 1) & 1, ab)) goto grad_done;
+                    if (n == 0 && tiles > 0 && !wait(&dv_empty, (tiles - 1) & 1, ab)) goto grad_done;
+                    if (!wait(&p_full, g & 1, ab)) goto grad_done;
+                    if (!wait(&g_full[st], (g >> 1) & 1, ab)) goto grad_done;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
@@ -585,8 +595,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     mma_commit(&dv_done);
                     if (n == ns - 1) mma_commit(&dv_full);
                     ++g;
-                    if (n == 0 && tiles > 0 && !mbar_wait(&dk_empty, (tiles - 1) & 1, ab)) goto grad_done;
-                    if (!mbar_wait(&ds_full, gk & 1, ab)) goto grad_done;
+                    if (n == 0 && tiles > 0 && !wait(&dk_empty, (tiles - 1) & 1, ab)) goto grad_done;
+                    if (!wait(&ds_full, gk & 1, ab)) goto grad_done;
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
@@ -619,19 +629,18 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     return static_cast<T*>(v.ptr) + z * v.s[0] + hk * v.s[1] + (int64_t)j * v.s[2];
                 };
             };
-            bool ok = mbar_wait(&dv_full, tiles & 1, ab);
+            bool ok = wait(&dv_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             drain<T, DP>(tV + lane_base, &dv_empty, lane, row, kb + row < p.Sk,
                          slot ? slot + (size_t)kTcRows * kSlotD : nullptr, 1.0f, args.D, stage, rows_of(args.dV));
-            ok = mbar_wait(&dk_full, tiles & 1, ab);
+            ok = wait(&dk_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             drain<T, DP>(tK + lane_base, &dk_empty, lane, row, kb + row < p.Sk, slot, args.scale, args.D, stage,
                          rows_of(args.dK));
             ++tiles;
-            if (threadIdx.x == 128 && w.s0 == 0 && !w.whole())
-                write_cut(args.cuts, w.seg, w.rep, w.tile, w.n - w.ns, start);
+            if (threadIdx.x == 128 && w.s0 == 0 && !w.whole()) cut = w;
         }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -647,6 +656,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 ns = w.ns, first = w.lo;
                 j = (w.tile << 7) + row;  // this thread's key
             }
+#pragma unroll 1
             for (int n = 0; n < ns; ++n, ++g) {
                 const uint32_t st = g & 1;
                 // rows that see the key: tokens from the key's own to window - 1
@@ -657,8 +667,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 const unsigned long long vis = below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64));
                 const bool full = __all_sync(0xffffffffu, vis == ~0ull);
                 const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 1024) + wg * 64;
-                bool ok = mbar_wait(&q_full[st], (g >> 1) & 1, ab);
-                ok = ok && mbar_wait(&s_full, g & 1, ab);
+                bool ok = wait(&q_full[st], (g >> 1) & 1, ab);
+                ok = ok && wait(&s_full, g & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 float x[64];
@@ -685,7 +695,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full);
-                ok = mbar_wait(&dp_full, g & 1, ab);
+                ok = wait(&dp_full, g & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 uint32_t pk[32];
@@ -717,6 +727,10 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
     tc_fence_before();
     __syncthreads();
+    if (threadIdx.x == 0) {
+        args.cuts[blockIdx.x].pieces = 0;
+        if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
+    }
     if (abort_flag) {
         if (threadIdx.x == 0) {
             mbar_drain_ring(q_full, 2, issued[0], ab);
@@ -749,8 +763,7 @@ int launch(Call& c) {
     if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem))) return rc;
     if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem))) return rc;
     const int grid = sm_count();
-    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + p.TQ - 1) / p.TQ, c.scale, c.scale * kLog2e, 2, c.cuts, c.slots,
-           kDefaultWaitNs};
+    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + p.TQ - 1) / p.TQ, c.scale, c.scale * kLog2e, 2, c.cuts, c.slots};
     if ((rc = launch_tile_stats(c))) return rc;
     dq_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;

@@ -42,7 +42,7 @@ namespace win {
 // as every position has no effect), so sums of two of them fit an int
 constexpr int kMaxLen = 1 << 30;
 constexpr int kMaxGroup = 64;      // query heads per KV head
-constexpr int kMaxSeqs = 16384;    // sequences of one ragged call (their step counts sit in shared memory)
+constexpr int kMaxSeqs = 16384;    // sequences of one ragged call (their tile counts sit in shared memory)
 
 // element (i, j, k, d) at ptr + i * s[0] + j * s[1] + k * s[2] + d
 struct View {
@@ -167,35 +167,39 @@ struct KProb {
     }
 };
 
-// Share of CTA c among n: [share_at(c), share_at(c + 1)).
-BSP_HD int64_t share_at(int64_t tot, int n, int c) { return c >= n ? tot : tot / n * c + tot % n * c / n; }
+// CTA c's share of the steps: [at(c), at(c + 1)), the first `rem` CTAs with one
+// more than the `base` of the others.
+struct Shares {
+    int64_t base;
+    int n, rem;
+    BSP_HD int64_t at(int c) const { return base * c + imin(c, rem); }
+    BSP_HD int64_t of(int c) const { return base + (c < rem); }
+};
 
 // The table of `items` tiles in `cols` columns.
 struct Table {
-    int64_t items;
-    int cols;
+    int cols, q, r;  // every column has q rows, the first r one more
+    BSP_HD Table(int items, int columns) : cols(columns), q(items / columns), r(items % columns) {}
     // column and row of place l on the line
-    BSP_HD void place(int64_t l, int* col, int64_t* row) const {
-        const int64_t q = items / cols, r = items % cols;
+    BSP_HD void place(int l, int* col, int* row) const {
         if (l < r * (q + 1)) {
-            *col = (int)(l / (q + 1));
+            *col = l / (q + 1);
             *row = l % (q + 1);
         } else {
-            *col = (int)(r + (l - r * (q + 1)) / q);
+            *col = r + (l - r * (q + 1)) / q;
             *row = (l - r * (q + 1)) % q;
         }
     }
-    BSP_HD int64_t number(int col, int64_t row) const { return row * cols + col; }
-    BSP_HD int64_t height(int col) const { return items / cols + (col < items % cols); }
+    BSP_HD int number(int col, int row) const { return row * cols + col; }
+    BSP_HD int height(int col) const { return q + (col < r); }
 };
 
 // Where a CTA's share begins, how long it is.
 struct Start {
-    int64_t tot;
-    int64_t items;
-    int n;          // CTAs that share the steps (the others do nothing)
+    Shares shares;  // among shares.n CTAs; the others do nothing
     int64_t count;  // steps of this CTA
-    int64_t place;  // place on the line of its first tile
+    int items;      // tiles of the launch
+    int place;      // place on the line of its first tile
     int off;        // first step of it
 };
 
@@ -205,8 +209,7 @@ struct Start {
 struct Cut {
     int pieces;
     int seg, rep, tile;
-    int64_t tot;
-    int n, pad;
+    Shares shares;
 };
 
 #if defined(__CUDACC__)
@@ -238,38 +241,42 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* 
 // used only while each gets this many steps.  Each thread adds up a run of the
 // line, one scan gives the runs' starts, and the thread whose run holds the
 // share's first step finds it.
+// Out of line: the kernels' loops then stay within the instruction cache.
 template <int NT, typename P>
-__device__ __forceinline__ void locate(const P& p, int min_share, int* seg_end, int64_t* red, Start* out) {
+__device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, int64_t* red, Start* out) {
     const int tid = threadIdx.x;
-    int64_t tiles = 0;  // one repetition of every segment
+    int tiles = 0;  // one repetition of every segment
     if (p.nseg == 1) {
         tiles = p.seg(0).ntiles;
     } else {
+    #pragma unroll 1
         for (int s0 = 0; s0 < p.nseg; s0 += NT) {
             const int s = s0 + tid;
             const int64_t v = s < p.nseg ? p.seg(s).ntiles : 0;
             int64_t total;
             const int64_t ex = block_scan<NT>(v, red, &total);
-            if (s < p.nseg) seg_end[s] = (int)(tiles + ex + v);
-            tiles += total;
+            if (s < p.nseg) seg_end[s] = tiles + (int)(ex + v);
+            tiles += (int)total;
         }
         __syncthreads();
     }
-    const Table tab{tiles * p.rep, (int)gridDim.x};
+    const int items = tiles * p.rep;
+    const Table tab(items, gridDim.x);
     // this thread's run of the line, tile after tile
-    const int64_t run = (tab.items + NT - 1) / NT;
-    const int64_t l0 = tid * run, l1 = l0 + run < tab.items ? l0 + run : tab.items;
-    int64_t at = -1, sum = 0, found = -1;
-    int off = 0;
+    const int run = (items + NT - 1) / NT;
+    const int l0 = imin(tid * run, items), l1 = imin(l0 + run, items);
+    int64_t at = -1, sum = 0;
+    int found = -1, off = 0;
     const Seg only = p.nseg == 1 ? p.seg(0) : Seg{0, 0, 0, 0};
     const int hop = p.nseg == 1 && only.ntiles > 0 ? (int)(gridDim.x % only.ntiles) : 0;
     // twice: the sum, then (for the thread that holds it) the first step's tile
+#pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
         int64_t before = sum;  // second pass: steps before this run
         sum = 0;
-        int col = 0, tile = 0;
-        int64_t row = 0, height = 0;
-        for (int64_t l = l0; l < l1; ++l) {
+        int col = 0, tile = 0, row = 0, height = 0;
+#pragma unroll 1
+        for (int l = l0; l < l1; ++l) {
             if (l == l0 || ++row >= height) {
                 if (l == l0) {
                     tab.place(l, &col, &row);
@@ -278,7 +285,7 @@ __device__ __forceinline__ void locate(const P& p, int min_share, int* seg_end, 
                     row = 0;
                 }
                 height = tab.height(col);
-                if (p.nseg == 1) tile = (int)(tab.number(col, row) % only.ntiles);
+                if (p.nseg == 1) tile = tab.number(col, row) % only.ntiles;
             } else if (p.nseg == 1) {
                 tile += hop;
                 if (tile >= only.ntiles) tile -= only.ntiles;
@@ -288,16 +295,16 @@ __device__ __forceinline__ void locate(const P& p, int min_share, int* seg_end, 
                 v = p.steps(only, tile);
             } else {
                 // the segment that holds tile number a
-                const int64_t a = tab.number(col, row);
+                const int a = tab.number(col, row);
                 int lo = 0, hi = p.nseg - 1;
+#pragma unroll 1
                 while (lo < hi) {
                     const int mid = (lo + hi) >> 1;
-                    if ((int64_t)seg_end[mid] * p.rep > a) hi = mid;
+                    if (seg_end[mid] * p.rep > a) hi = mid;
                     else lo = mid + 1;
                 }
                 const Seg g = p.seg(lo);
-                const int64_t first = (int64_t)(seg_end[lo] - g.ntiles) * p.rep;
-                v = p.steps(g, (int)((a - first) % g.ntiles));
+                v = p.steps(g, (a - (seg_end[lo] - g.ntiles) * p.rep) % g.ntiles);
             }
             if (pass == 1 && at >= before + sum && at < before + sum + v) {
                 found = l;
@@ -308,17 +315,23 @@ __device__ __forceinline__ void locate(const P& p, int min_share, int* seg_end, 
         }
         if (pass == 0) {
             Start st;
-            const int64_t ex = block_scan<NT>(sum, red, &st.tot);
-            const int64_t most = (st.tot + min_share - 1) / min_share;
-            st.items = tab.items;
-            st.n = most < 1 ? 1 : (most < (int64_t)gridDim.x ? (int)most : (int)gridDim.x);
-            at = share_at(st.tot, st.n, blockIdx.x);
-            st.count = share_at(st.tot, st.n, blockIdx.x + 1) - at;
-            st.place = 0;
-            st.off = 0;
+            int64_t tot;
+            const int64_t ex = block_scan<NT>(sum, red, &tot);
+            if (tid == 0) {
+                const int n = tot >= (int64_t)min_share * gridDim.x ? (int)gridDim.x
+                                                                    : imax(1, (int)tot / min_share);
+                st.shares.n = n;
+                st.shares.base = tot / n;
+                st.shares.rem = (int)(tot - st.shares.base * n);
+                st.count = (int)blockIdx.x < n ? st.shares.of(blockIdx.x) : 0;
+                st.items = items;
+                st.place = 0;
+                st.off = 0;
+                *out = st;
+            }
             __syncthreads();
-            if (tid == 0) *out = st;
-            __syncthreads();
+            st = *out;
+            at = st.shares.at(blockIdx.x);
             const bool mine = st.count > 0 && at >= ex && at < ex + sum;
             sum = ex;
             if (!mine) break;
@@ -341,25 +354,23 @@ struct Item {
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (s0 == 0); }
 };
 
-// Walks the tiles of a CTA's share.  With several segments all lanes of a warp
-// walk together.
-template <typename P>
+// Walks the tiles of a CTA's share.  MANY: the problem may have several
+// segments, and all lanes of a warp walk together.
+template <typename P, bool MANY>
 struct Walk {
     const P& p;
     Table tab;
     int64_t left;
-    int col;
-    int64_t row, height;
+    int col, row, height;
     int off;
-    int seg;       // segment that holds tile number seg0 ..
-    int64_t seg0;
+    int seg, seg0;  // a segment and the number of its first tile
     Seg g;
     __device__ __forceinline__ Walk(const P& prob, const Start& st)
-        : p(prob), tab{st.items, (int)gridDim.x}, left(st.count), off(st.off), seg(0), seg0(0) {
+        : p(prob), tab(st.items, gridDim.x), left(st.count), off(st.off), seg(0), seg0(0) {
         if (left > 0) {
             tab.place(st.place, &col, &row);
             height = tab.height(col);
-            if (p.nseg == 1) g = p.seg(0);
+            if (!MANY) g = p.seg(0);
         }
     }
     __device__ __forceinline__ bool next(Item& it) {
@@ -371,16 +382,17 @@ struct Walk {
             seg = 0;
             seg0 = 0;
         }
-        const int64_t a = tab.number(col, row++);
-        if (p.nseg > 1) {
+        const int a = tab.number(col, row++);
+        if constexpr (MANY) {
             // 32 segments at a time: the one that holds tile number a
             const int lane = threadIdx.x & 31;
+#pragma unroll 1
             while (true) {
                 const int s = seg + lane;
                 const Seg h = s < p.nseg ? p.seg(s) : Seg{0, 0, 0, 0};
-                int64_t end = (int64_t)h.ntiles * p.rep;
+                int end = h.ntiles * p.rep;
                 for (int o = 1; o < 32; o <<= 1) {
-                    const int64_t y = __shfl_up_sync(0xffffffffu, end, o);
+                    const int y = __shfl_up_sync(0xffffffffu, end, o);
                     if (lane >= o) end += y;
                 }
                 end += seg0;
@@ -392,7 +404,7 @@ struct Walk {
                 }
                 const int src = m ? __ffs(m) - 1 : 31;  // m != 0: a lies below the last segment's end
                 seg += src;
-                seg0 = __shfl_sync(0xffffffffu, end - (int64_t)h.ntiles * p.rep, src);
+                seg0 = __shfl_sync(0xffffffffu, end - h.ntiles * p.rep, src);
                 g.t0 = __shfl_sync(0xffffffffu, h.t0, src);
                 g.qlen = __shfl_sync(0xffffffffu, h.qlen, src);
                 g.kvlen = __shfl_sync(0xffffffffu, h.kvlen, src);
@@ -401,8 +413,8 @@ struct Walk {
             }
         }
         it.seg = seg;
-        it.rep = (int)((a - seg0) / g.ntiles);
-        it.tile = (int)((a - seg0) % g.ntiles);
+        it.rep = (a - seg0) / g.ntiles;
+        it.tile = (a - seg0) % g.ntiles;
         it.g = g;
         it.n = p.steps(g, it.tile);
         it.s0 = off;
@@ -414,17 +426,17 @@ struct Walk {
     }
 };
 
-// The record of a tile that begins in this CTA and is cut at its end.
+// The record of a tile that begins in this CTA and goes on for `left` steps
+// after its share.
 __device__ __forceinline__ void write_cut(Cut* cuts, int seg, int rep, int tile, int left, const Start& st) {
-    int pieces = 1;  // left: the tile's steps after this CTA's
-    for (int c = blockIdx.x + 1; left > 0 && c < st.n; ++c) {
-        const int64_t sh = share_at(st.tot, st.n, c + 1) - share_at(st.tot, st.n, c);
-        if (sh <= 0) continue;
+    int pieces = 1;
+#pragma unroll 1
+    for (int c = blockIdx.x + 1; left > 0 && c < st.shares.n; ++c) {
+        const int64_t sh = st.shares.of(c);
         left -= (int)(sh < left ? sh : left);
         ++pieces;
     }
-    Cut c{pieces, seg, rep, tile, st.tot, st.n, 0};
-    cuts[blockIdx.x] = c;
+    cuts[blockIdx.x] = Cut{pieces, seg, rep, tile, st.shares};
 }
 
 #endif  // __CUDACC__

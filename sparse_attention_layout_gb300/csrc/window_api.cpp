@@ -94,6 +94,10 @@ int check_dense(int Z, int Hq, int Hkv, int Sq, int Sk, int D, float scale) {
     if (Z < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || Sk < 0 || !valid_d(D) || !valid_scale(scale)) return BSP_ERR_INVALID_ARG;
     if (Hq % Hkv) return BSP_ERR_INVALID_ARG;
     if (Hq / Hkv > kMaxGroup || Sq > kMaxLen || Sk > kMaxLen || (int64_t)Z * Hkv > kMaxLen) return BSP_ERR_UNSUPPORTED;
+    // tiles are numbered in 32 bits, of 64 rows (queries) and 64 keys at the least
+    const int64_t tq = 64 / (Hq / Hkv);
+    if (Z && (int64_t)Z * Hkv > kMaxLen / ((Sq + tq - 1) / tq + 1)) return BSP_ERR_UNSUPPORTED;
+    if (Z && (int64_t)Z * Hkv > kMaxLen / ((Sk + 63) / 64 + 1)) return BSP_ERR_UNSUPPORTED;
     return BSP_OK;
 }
 
@@ -275,6 +279,8 @@ int paged_prob(bsp_window_t w, const int32_t* q_start, const int32_t* kv_len, co
     if (Hq % Hkv) return BSP_ERR_INVALID_ARG;
     if (Hq / Hkv > kMaxGroup || T > kMaxLen || n_seq > kMaxSeqs || (int64_t)max_pages * page > kMaxLen)
         return BSP_ERR_UNSUPPORTED;
+    // tiles are numbered in 32 bits: at most one per token, and one per sequence
+    if (Hkv > kMaxLen / ((int64_t)T + n_seq + 1)) return BSP_ERR_UNSUPPORTED;
     if (T == 0 || n_seq == 0) return BSP_OK;
     if (!q_start || !kv_len || !table) return BSP_ERR_INVALID_ARG;
     if (((uintptr_t)q_start | (uintptr_t)kv_len | (uintptr_t)table) & 3u) return BSP_ERR_ALIGNMENT;

@@ -11,18 +11,9 @@ namespace {
 constexpr int kJoinParts = 8;  // blocks per cut tile, each an eighth of its rows
 constexpr int kJoinT = 128;    // a warp per row, four columns per lane
 
-// The slots of a cut tile's pieces, in order.
-struct Pieces {
-    int64_t tot;
-    int n, c;
-    __device__ __forceinline__ Pieces(const Cut& k) : tot(k.tot), n(k.n), c(blockIdx.x) {}
-    __device__ __forceinline__ int first() const { return 2 * blockIdx.x + 1; }
-    __device__ __forceinline__ int next() {
-        do ++c;
-        while (share_at(tot, n, c + 1) == share_at(tot, n, c));
-        return 2 * c;
-    }
-};
+// The slots of a cut tile's pieces, in order: every CTA among those that share
+// the steps has one of at least one step.
+__device__ __forceinline__ int piece_slot(int i) { return i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i); }
 
 struct JoinArgs {
     const Cut* cuts;
@@ -53,17 +44,12 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float m = -INFINITY, l = 0.f;
         if (!DQ) {
-            Pieces it(cut);
-            int s = it.first();
-            for (int i = 0; i < cut.pieces; ++i) {
-                m = fmaxf(m, a.slots[s * slot_floats(a.R) + ms]);
-                if (i + 1 < cut.pieces) s = it.next();
-            }
+#pragma unroll 4
+            for (int i = 0; i < cut.pieces; ++i) m = fmaxf(m, a.slots[piece_slot(i) * slot_floats(a.R) + ms]);
         }
-        Pieces it(cut);
-        int s = it.first();
+#pragma unroll 4
         for (int i = 0; i < cut.pieces; ++i) {
-            const float* sl = a.slots + s * slot_floats(a.R);
+            const float* sl = a.slots + piece_slot(i) * slot_floats(a.R);
             float w = 1.f;
             if (!DQ) {
                 const float mi = sl[ms];
@@ -74,7 +60,6 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
                 const float4 v = *reinterpret_cast<const float4*>(sl + row);
                 o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
             }
-            if (i + 1 < cut.pieces) s = it.next();
         }
         const float f = DQ ? a.scale : (l > 0.f ? 1.0f / l : 0.f);
         const int64_t h = (int64_t)hk * p.G + r % p.G, t = (int64_t)g.t0 + q.tok0 + r / p.G;
@@ -98,15 +83,13 @@ __global__ void __launch_bounds__(kJoinT) join_kv_kernel(const JoinArgs a, const
     if (4 * lane >= a.D) return;
     for (int r = blockIdx.y * (kJoinT / 32) + (threadIdx.x >> 5); r < rows; r += kJoinParts * (kJoinT / 32)) {
         float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-        Pieces it(cut);
-        int s = it.first();
+#pragma unroll 4
         for (int i = 0; i < cut.pieces; ++i) {
-            const float* sl = a.slots + s * kv_slot_floats(a.R) + 4 * lane;
+            const float* sl = a.slots + piece_slot(i) * kv_slot_floats(a.R) + 4 * lane;
             const float4 x = *reinterpret_cast<const float4*>(sl + (size_t)r * kSlotD);
             const float4 y = *reinterpret_cast<const float4*>(sl + (size_t)(a.R + r) * kSlotD);
             k.x += x.x, k.y += x.y, k.z += x.z, k.w += x.w;
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
-            if (i + 1 < cut.pieces) s = it.next();
         }
         const int64_t j = kb + r;
         T* dk = static_cast<T*>(a.out.ptr) + z * a.out.s[0] + hk * a.out.s[1] + j * a.out.s[2] + 4 * lane;

@@ -158,7 +158,7 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
         if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
 }
 
-template <typename T, int DP>
+template <typename T, int DP, bool PAGED>
 __global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<Prob> walk(p, start);
+    Walk<Prob, PAGED> walk(p, start);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
             // keys that some row of the tile sees; the others (behind the
             // sequence, before every row's window) are not read at all
             auto wanted = [&](int j) { return j <= q.b && (j >= lo || j < p.sinks); };
-            if (p.paged) {
+            if (PAGED) {
                 __syncthreads();
                 if (threadIdx.x < R) {
                     const int j = kb + threadIdx.x;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
             __syncthreads();
             auto keyrow = [&](const View& v, int r) -> const T* {
                 const int j = kb + r;
-                if (p.paged) {
+                if (PAGED) {
                     const int pg = pages[r];
                     return pg < 0 ? nullptr : at<const T>(v, pg, w.hk, j & ((1 << p.page_shift) - 1));
                 }
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kT) dq_kernel(const Args A) {
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<Prob> walk(p, start);
+    Walk<Prob, false> walk(p, start);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kT) dkv_kernel(const Args A, const KProb kp) {
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<KProb> walk(kp, start);
+    Walk<KProb, false> walk(kp, start);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -513,7 +513,8 @@ int forward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
     size_t smem = tiles_bytes<DP>(3, 1);
     if (smem < (size_t)c.p.nseg * sizeof(int)) smem = (size_t)c.p.nseg * sizeof(int);
-    const int rc = launch(forward_kernel<T, DP>, grid, smem, c.stream, a);
+    const int rc = c.p.paged ? launch(forward_kernel<T, DP, true>, grid, smem, c.stream, a)
+                             : launch(forward_kernel<T, DP, false>, grid, smem, c.stream, a);
     return rc ? rc : launch_join(c, R, grid, false);
 }
 
