@@ -488,8 +488,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t sb = g % 3;
                 const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
                 const int kb = (kt << 7) + wg * 64;  // first key of this half
-                const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
-                const bool skip = __all_sync(0xffffffffu, vis == 0), full = __all_sync(0xffffffffu, vis == ~0ull);
+                const bool full = __all_sync(0xffffffffu, row_all(pos, low, p.sinks, kb));
+                const bool skip = __all_sync(0xffffffffu, row_none(pos, low, p.sinks, kb));
+                unsigned long long vis = 0;
+                if (!full) vis = row_keys(pos, low, p.sinks, kb);
                 bool ok = wait(&s_full[sb], (g / 3) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                 if (idle) {

@@ -132,6 +132,14 @@ __device__ __forceinline__ void hide(float (&x)[64], unsigned long long vis) {
     }
 }
 
+// All 64 keys from kb are visible to a row at position pos; none is.  A few
+// comparisons per step, where the bits below cost sixty instructions.
+__device__ __forceinline__ bool row_all(int pos, int low, int sinks, int kb) {
+    return pos >= kb + 63 && (low <= kb || sinks >= kb + 64);
+}
+__device__ __forceinline__ bool row_none(int pos, int low, int sinks, int kb) {
+    return pos < kb || (low >= kb + 64 && sinks <= kb);
+}
 // Visible keys of one row at position pos among the 64 that start at kb.
 __device__ __forceinline__ unsigned long long row_keys(int pos, int low, int sinks, int kb) {
     const int hi = imin(imax(pos - kb + 1, 0), 64), lo = imin(imax(low - kb, 0), 64);

@@ -327,8 +327,9 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const uint32_t st = g & 1;
                 const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
                 const int kb = (kt << 7) + wg * 64;
-                const unsigned long long vis = row_keys(pos, low, p.sinks, kb);
-                const bool full = __all_sync(0xffffffffu, vis == ~0ull);
+                const bool full = __all_sync(0xffffffffu, row_all(pos, low, p.sinks, kb));
+                unsigned long long vis = 0;
+                if (!full) vis = row_keys(pos, low, p.sinks, kb);
                 bool ok = wait(&s_full[st], (g >> 1) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
@@ -664,8 +665,9 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 const int tok = p.Sk - p.Sq + (first + n) * p.TQ;  // position of row 0
                 const int c0 = imin(imax(j - tok, 0), 128) * p.G - wg * 64;
                 const int c1 = j < p.sinks ? 64 : imin(imax(j - tok + p.window, 0), 128) * p.G - wg * 64;
-                const unsigned long long vis = below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64));
-                const bool full = __all_sync(0xffffffffu, vis == ~0ull);
+                const bool full = __all_sync(0xffffffffu, c0 <= 0 && c1 >= 64);
+                unsigned long long vis = 0;
+                if (!full) vis = below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64));
                 const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 1024) + wg * 64;
                 bool ok = wait(&q_full[st], (g >> 1) & 1, ab);
                 ok = ok && wait(&s_full, g & 1, ab);
