@@ -473,12 +473,16 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         };
         while (true) {
             int ns, s0, n_s, lo_tile, rows, pos;
+            Seen seen;
             {
                 Work w;
                 if (!ring.take(tc, w, lane == 0, true, ab)) break;
                 ns = w.ns, s0 = w.s0, n_s = w.n_s, lo_tile = w.lo;
                 rows = w.nt * p.G;
-                pos = row < rows ? w.a + (int)((row * inv_g) >> 16) : -1;
+                // rows past the tile's last see what its last row sees; they are not stored
+                pos = w.a + (int)((imin(row, rows - 1) * inv_g) >> 16);
+                seen.first = w.a + (int)((imin(quad * 32, rows - 1) * inv_g) >> 16);
+                seen.last = w.a + (int)((imin(quad * 32 + 31, rows - 1) * inv_g) >> 16);
             }
             const bool idle = quad * 32 >= rows;  // no live row in this warp's lanes
             const int low = pos - p.window + 1;
@@ -488,10 +492,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t sb = g % 3;
                 const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
                 const int kb = (kt << 7) + wg * 64;  // first key of this half
-                const bool full = __all_sync(0xffffffffu, row_all(pos, low, p.sinks, kb));
-                const bool skip = __all_sync(0xffffffffu, row_none(pos, low, p.sinks, kb));
-                unsigned long long vis = 0;
-                if (!full) vis = row_keys(pos, low, p.sinks, kb);
+                const bool full = seen.all(p, kb), skip = seen.none(p, kb);
                 bool ok = wait(&s_full[sb], (g / 3) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                 if (idle) {
@@ -507,7 +508,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 float mx = -INFINITY;
                 if (!skip) {
                     tmem_ld64_sync(srow + wg * 64, srow + wg * 64 + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
-                    if (!full) hide(x, vis);
+                    if (!full) hide(x, row_keys(pos, low, p.sinks, kb));
                     mx = max64(x);
                 }
                 xm[xb][wg][row] = mx;

@@ -132,14 +132,19 @@ __device__ __forceinline__ void hide(float (&x)[64], unsigned long long vis) {
     }
 }
 
-// All 64 keys from kb are visible to a row at position pos; none is.  A few
-// comparisons per step, where the bits below cost sixty instructions.
-__device__ __forceinline__ bool row_all(int pos, int low, int sinks, int kb) {
-    return pos >= kb + 63 && (low <= kb || sinks >= kb + 64);
-}
-__device__ __forceinline__ bool row_none(int pos, int low, int sinks, int kb) {
-    return pos < kb || (low >= kb + 64 && sinks <= kb);
-}
+// What a warp's rows, at positions first .. last, see of the 64 keys from kb:
+// all of them, none, or (neither) the bits that row_keys gives each row.
+// Comparisons of per-tile values: a vote over the rows' own bits, or branches
+// here, put 400 cycles between a warp's steps (of 2300).
+struct Seen {
+    int first, last;  // positions of the warp's first and last live row
+    __device__ __forceinline__ bool all(const Prob& p, int kb) const {
+        return (first >= kb + 63) & ((last - p.window < kb) | (p.sinks >= kb + 64));
+    }
+    __device__ __forceinline__ bool none(const Prob& p, int kb) const {
+        return (last < kb) | ((first - p.window >= kb + 63) & (p.sinks <= kb));
+    }
+};
 // Visible keys of one row at position pos among the 64 that start at kb.
 __device__ __forceinline__ unsigned long long row_keys(int pos, int low, int sinks, int kb) {
     const int hi = imin(imax(pos - kb + 1, 0), 64), lo = imin(imax(low - kb, 0), 64);

@@ -312,6 +312,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         for (uint32_t i = 0;; ++i) {
             int ns, s0, n_s, lo_tile, pos;
             float nlse, delta;
+            Seen seen;
             {
                 Work w;
                 if (!ring.take(i, w, lane == 0, true, ab)) break;
@@ -319,7 +320,11 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const float* s = args.stats + ((int64_t)w.rep * args.ntiles + w.tile) * 256;
                 nlse = s[row];
                 delta = s[128 + row];
-                pos = row < w.nt * p.G ? w.a + (int)((row * inv_g) >> 16) : -1;
+                // rows past the tile's last have P = 0 by their statistics
+                const int end = w.nt * p.G - 1;
+                pos = w.a + (int)((imin(row, end) * inv_g) >> 16);
+                seen.first = w.a + (int)((imin(quad * 32, end) * inv_g) >> 16);
+                seen.last = w.a + (int)((imin(quad * 32 + 31, end) * inv_g) >> 16);
             }
             const int low = pos - p.window + 1;
 #pragma unroll 1
@@ -327,16 +332,14 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const uint32_t st = g & 1;
                 const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
                 const int kb = (kt << 7) + wg * 64;
-                const bool full = __all_sync(0xffffffffu, row_all(pos, low, p.sinks, kb));
-                unsigned long long vis = 0;
-                if (!full) vis = row_keys(pos, low, p.sinks, kb);
+                const bool full = seen.all(p, kb);
                 bool ok = wait(&s_full[st], (g >> 1) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 const uint32_t ts = tS + st * 128 + lane_base + wg * 64;
                 float x[64];
                 tmem_ld64_sync(ts, ts + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
-                if (!full) hide(x, vis);
+                if (!full) hide(x, row_keys(pos, low, p.sinks, kb));
 #pragma unroll
                 for (int j = 0; j < 64; j += 2) {
                     const float2 y = __ffma2_rn(make_float2(x[j], x[j + 1]), make_float2(args.c2, args.c2),
@@ -648,6 +651,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         // ------------------------------------------------ P^T and dS^T ----
         const int wg = (warp - 8) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
+        // tokens of this half's first and last row
+        const int t_first = wg * 64 / p.G, t_last = imin(wg * 64 + 63, p.TQ * p.G - 1) / p.G;
         uint32_t g = 0;
         for (uint32_t i = 0;; ++i) {
             int ns, first, j;
@@ -657,17 +662,16 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 ns = w.ns, first = w.lo;
                 j = (w.tile << 7) + row;  // this thread's key
             }
+            const int j_first = j - lane, j_last = j_first + 31;
 #pragma unroll 1
             for (int n = 0; n < ns; ++n, ++g) {
                 const uint32_t st = g & 1;
                 // rows that see the key: tokens from the key's own to window - 1
                 // later ones (a sink: all later ones), G rows each
                 const int tok = p.Sk - p.Sq + (first + n) * p.TQ;  // position of row 0
-                const int c0 = imin(imax(j - tok, 0), 128) * p.G - wg * 64;
-                const int c1 = j < p.sinks ? 64 : imin(imax(j - tok + p.window, 0), 128) * p.G - wg * 64;
-                const bool full = __all_sync(0xffffffffu, c0 <= 0 && c1 >= 64);
-                unsigned long long vis = 0;
-                if (!full) vis = below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64));
+                // the warp's keys against this half's first and last row
+                const bool full = (tok + t_first >= j_last) &
+                                  ((tok + t_last - j_first < p.window) | (j_last < p.sinks));
                 const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 1024) + wg * 64;
                 bool ok = wait(&q_full[st], (g >> 1) & 1, ab);
                 ok = ok && wait(&s_full, g & 1, ab);
@@ -676,7 +680,11 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 float x[64];
                 tmem_ld64_sync(tS + lane_base + wg * 64, tS + lane_base + wg * 64 + 32,
                                *reinterpret_cast<uint32_t(*)[64]>(x));
-                if (!full) hide(x, vis);
+                if (!full) {
+                    const int c0 = imin(imax(j - tok, 0), 128) * p.G - wg * 64;
+                    const int c1 = j < p.sinks ? 64 : imin(imax(j - tok + p.window, 0), 128) * p.G - wg * 64;
+                    hide(x, below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64)));
+                }
                 {
                     uint32_t pk[32];
 #pragma unroll
