@@ -330,13 +330,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     if (pieces == 0xffu) {
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
-                            mma_f16_tmem_a(tO, tS + sb * 128 + ks * 8, bv + ((ks * 2048) >> 4), kIdescPV, ks > 0 ? 1u : acc);
+                            mma_f16_tmem_a(tO, tS + sb * 128 + (ks >> 2) * 64 + (ks & 3) * 8, bv + ((ks * 2048) >> 4), kIdescPV, ks > 0 ? 1u : acc);
                         acc = 1;
                     } else {
 #pragma unroll 1
                         for (int ks = 0; ks < 8; ++ks)
                             if ((pieces >> ks) & 1) {
-                                mma_f16_tmem_a(tO, tS + sb * 128 + ks * 8, bv + ((ks * 2048) >> 4), kIdescPV, acc);
+                                mma_f16_tmem_a(tO, tS + sb * 128 + (ks >> 2) * 64 + (ks & 3) * 8, bv + ((ks * 2048) >> 4), kIdescPV, acc);
                                 acc = 1;
                             }
                     }
@@ -412,31 +412,33 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 args.lse[z * args.lz + (hk * p.G + h) * args.lh + (t0 + t) * args.lt] =
                     seen ? (mf + log2f(lt)) * kLn2 : -INFINITY;
             }
-            // 64 columns at a time, out of TMEM and through the warp's staging
-            // panel; the accumulator is the next tile's once all are read
-#pragma unroll 1
-            for (int c = 0; c < KP; ++c) {
-                uint32_t pk[32];
-                {
-                    uint32_t r[64];
-                    tmem_ld64_sync(tO + lane_base + c * 64, tO + lane_base + c * 64 + 32, r);
+            // O is read out of TMEM, scaled and packed before anything is stored, and
+            // the accumulator handed to the next tile (after the first panel's
+            // stores instead, its first product waited 5400 cycles)
+            uint32_t pk[KP][32];
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        pk[k] = seen ? Pack2<T>::pack(__uint_as_float(r[2 * k]) * inv, __uint_as_float(r[2 * k + 1]) * inv)
-                                     : 0u;
-                }
-                if (c == KP - 1) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&o_empty);
-                }
-                store_panel<T>(stage, pk, lane, args.D - c * 64, [&](int i) -> T* {
-                    const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
-                    if (r >= rows) return nullptr;
-                    return static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
-                           (int64_t)(t0 + t) * args.O.s[2] + c * 64;
-                });
+            for (int c = 0; c < KP; ++c) {
+                uint32_t r[64];
+                tmem_ld64_sync(tO + lane_base + c * 64, tO + lane_base + c * 64 + 32, r);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                    pk[c][k] = Pack2<T>::pack(__uint_as_float(r[2 * k]) * inv, __uint_as_float(r[2 * k + 1]) * inv);
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&o_empty);
+            if (!__all_sync(0xffffffffu, seen)) {  // a row that saw nothing: 0, whatever its accumulator holds
+#pragma unroll
+                for (int c = 0; c < KP; ++c)
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) pk[c][k] = seen ? pk[c][k] : 0u;
+            }
+            store_panels<T, KP>(stage, pk, lane, args.D, [&](int i) -> T* {
+                const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
+                if (r >= rows) return nullptr;
+                return static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
+                       (int64_t)(t0 + t) * args.O.s[2];
+            });
         }
     } else {
         regs_inc<kRegsSoftmax>();
@@ -446,31 +448,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
         const uint32_t inv_g = 65536u / p.G + 1;
         uint32_t g = 0, tc = 0, xg = 0;  // xg: half-row exchanges so far
-        auto max64 = [](const float (&v)[64]) {
-            float m8[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) m8[k] = fmax3(v[k], v[k + 8], v[k + 16]);
-#pragma unroll
-            for (int c = 24; c < 64; c += 16)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], v[c + k], c + 8 + k < 64 ? v[c + 8 + k] : v[c + k]);
-            return fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
-        };
-        auto exp64 = [&](const float (&v)[64], float msub, uint32_t (&pk)[32]) {
-            const float2 c2v = make_float2(args.c2, args.c2), nm = make_float2(-msub, -msub);
-            float2 rs4[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) rs4[k] = make_float2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const float2 y = __ffma2_rn(make_float2(v[2 * c], v[2 * c + 1]), c2v, nm);
-                const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-                rs4[c & 3] = __fadd2_rn(rs4[c & 3], e);
-                pk[c] = Pack2<T>::pack(e.x, e.y);
-            }
-            const float2 r2 = __fadd2_rn(__fadd2_rn(rs4[0], rs4[1]), __fadd2_rn(rs4[2], rs4[3]));
-            return r2.x + r2.y;
-        };
         while (true) {
             int ns, s0, n_s, lo_tile, rows, pos;
             Seen seen;
@@ -501,23 +478,28 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     continue;
                 }
                 tc_fence_after();
-                const uint32_t srow = tS + sb * 128 + lane_base;
+                const uint32_t srow = tS + sb * 128 + wg * 64 + lane_base;
                 const uint32_t xb = xg & 1, xph = (xg >> 1) & 1;
                 ++xg;
                 float x[64];
                 float mx = -INFINITY;
                 if (!skip) {
-                    tmem_ld64_sync(srow + wg * 64, srow + wg * 64 + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
+                    tmem_ld64_sync(srow, srow + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
                     if (!full) hide(x, row_keys(pos, low, p.sinks, kb));
-                    mx = max64(x);
+                    float m8[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) m8[k] = fmax3(x[k], x[k + 8], x[k + 16]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) m8[k] = fmax3(m8[k], x[k + 24], x[k + 32]);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) m8[k] = fmax3(fmaxf(m8[k], x[k + 40]), x[k + 48], x[k + 56]);
+                    mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]), fmaxf(m8[6], m8[7]));
                 }
                 xm[xb][wg][row] = mx;
-                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&x_full[xb][quad]);
                 ok = wait(&x_full[xb][quad], xph, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
-                tc_fence_after();
                 const float mrow = fmaxf(mx, xm[xb][wg ^ 1][row]);
                 const float m_new = fmaxf(m, mrow * args.c2);
                 const bool need = m_new > m + kRescaleThreshold;  // also true for the first finite max
@@ -526,12 +508,24 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 uint32_t pk[32];
                 float rs = 0.f;
                 if (!skip) {
-                    rs = exp64(x, msub, pk);
+                    const float2 c2v = make_float2(args.c2, args.c2), nm = make_float2(-msub, -msub);
+                    float2 rs4[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) rs4[k] = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const float2 y = __ffma2_rn(make_float2(x[2 * k], x[2 * k + 1]), c2v, nm);
+                        const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+                        rs4[k & 3] = __fadd2_rn(rs4[k & 3], e);
+                        pk[k] = Pack2<T>::pack(e.x, e.y);
+                    }
+                    const float2 r2 = __fadd2_rn(__fadd2_rn(rs4[0], rs4[1]), __fadd2_rn(rs4[2], rs4[3]));
+                    rs = r2.x + r2.y;
                 } else {
 #pragma unroll
                     for (int k = 0; k < 32; ++k) pk[k] = 0u;
                 }
-                tmem_st32_sync(srow + wg * 32, pk);
+                tmem_st32_sync(srow, pk);
                 // rows that saw nothing yet have O = 0, which no factor changes
                 const bool grew = need && m != -INFINITY;
                 if (__any_sync(0xffffffffu, grew)) {

@@ -122,6 +122,12 @@ __device__ __forceinline__ Work make_work(const Prob& p, const Item& it) {
 // bits [0, c) of 64
 __device__ __forceinline__ unsigned long long below(int c) { return c >= 64 ? ~0ull : (1ull << c) - 1; }
 
+// the same for 32 columns
+__device__ __forceinline__ void hide32(float (&x)[32], uint32_t vis) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) x[j] = (vis >> j) & 1 ? x[j] : -INFINITY;
+}
+
 // x[j] = -inf where bit j is clear
 __device__ __forceinline__ void hide(float (&x)[64], unsigned long long vis) {
     const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);
@@ -156,14 +162,16 @@ __device__ __forceinline__ unsigned long long row_keys(int pos, int low, int sin
 // memory through the warp's 4 KB staging panel (16-byte piece j of row r at
 // j ^ (r % 8), so neither side meets a bank twice): 8 lanes then write 128
 // contiguous bytes of a row.  dst(r): where row r's 64 columns begin, or null.
-template <typename T, typename F>
-__device__ __forceinline__ void store_panel(uint8_t* stage, const uint32_t (&pk)[32], int lane, int cols, F dst) {
+__device__ __forceinline__ void stage_panel(uint8_t* stage, const uint32_t (&pk)[32], int lane) {
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 8; ++j)
         *reinterpret_cast<uint4*>(stage + lane * 128 + ((j ^ (lane & 7)) << 4)) =
             make_uint4(pk[4 * j], pk[4 * j + 1], pk[4 * j + 2], pk[4 * j + 3]);
     __syncwarp();
+}
+template <typename T, typename F>
+__device__ __forceinline__ void store_panel(const uint8_t* stage, int lane, int cols, F dst) {
     const int j = lane & 7;
 #pragma unroll 2
     for (int i = 0; i < 8; ++i) {
@@ -171,6 +179,21 @@ __device__ __forceinline__ void store_panel(uint8_t* stage, const uint32_t (&pk)
         const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ (r & 7)) << 4));
         T* p = dst(r);
         if (p && j * 8 < cols) *reinterpret_cast<uint4*>(p + j * 8) = v;
+    }
+}
+// KP panels, one loop for all
+template <typename T, int KP, typename F>
+__device__ __forceinline__ void store_panels(uint8_t* stage, const uint32_t (&pk)[KP][32], int lane, int D, F dst) {
+#pragma unroll 1
+    for (int c = 0; c < KP; ++c) {
+        uint32_t x[32];
+#pragma unroll
+        for (int k = 0; k < 32; ++k) x[k] = c == 0 ? pk[0][k] : pk[KP - 1][k];
+        stage_panel(stage, x, lane);
+        store_panel<T>(stage, lane, D - c * 64, [&](int i) -> T* {
+            T* p = dst(i);
+            return p ? p + c * 64 : nullptr;
+        });
     }
 }
 

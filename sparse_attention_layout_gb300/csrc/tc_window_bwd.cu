@@ -65,26 +65,19 @@ __device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, 
         if (lane == 0) mbar_arrive(empty);
         return;
     }
-#pragma unroll 1
-    for (int c = 0; c < DP / 64; ++c) {
-        uint32_t pk[32];
-        {
-            uint32_t r[64];
-            tmem_ld64_sync(tacc + c * 64, tacc + c * 64 + 32, r);
+    uint32_t pk[DP / 64][32];
 #pragma unroll
-            for (int k = 0; k < 32; ++k)
-                pk[k] = Pack2<T>::pack(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
-        }
-        if (c == DP / 64 - 1) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty);
-        }
-        store_panel<T>(stage, pk, lane, D - c * 64, [&](int i) -> T* {
-            T* p = dst(i);
-            return p ? p + c * 64 : nullptr;
-        });
+    for (int c = 0; c < DP / 64; ++c) {
+        uint32_t r[64];
+        tmem_ld64_sync(tacc + c * 64, tacc + c * 64 + 32, r);
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            pk[c][k] = Pack2<T>::pack(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
     }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty);
+    store_panels<T, DP / 64>(stage, pk, lane, D, dst);
 }
 
 // ------------------------------------------------------------------- dQ ----
