@@ -93,7 +93,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Abort ab{&abort_flag, p.status, kDefaultWaitNs};
+    const Stop ab{&abort_flag};
 
     if (threadIdx.x == 0) {
         abort_flag = 0;
@@ -242,7 +242,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 if (scrub) {
                     bool ok = wait(&v_land, lands & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) {
-                        if (lane == 0) mbar_drain(&v_land, lands & 1, ab);
+                        if (lane == 0) drain_wait(&v_land, lands & 1);
                         break;
                     }
                     ++lands;
@@ -293,11 +293,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     if (!wait(&k_full[st], (g / NST) & 1, ab)) goto qk_done;
                     tc_fence_after();
                     const uint64_t aq = dq + ((qs * kTileBytes) >> 4), bk = dk + ((st * kTileBytes) >> 4);
+#pragma unroll 1
+                    for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                        mma_f16(tS + sb * 128, aq + off, bk + off, kIdescQK, ks > 0 ? 1u : 0u);
-                    }
+                        for (uint32_t ks = 0; ks < 4; ++ks) {
+                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
+                            mma_f16(tS + sb * 128, aq + off, bk + off, kIdescQK, ks > 0 ? 1u : c);
+                        }
                     mma_commit(&s_full[sb]);
                     if (n == ns - 1) mma_commit(&q_empty[qs]);
                 }
@@ -320,26 +322,19 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                     const uint32_t st = g % NST, sb = g % 3;
                     const int kb = w.key_tile(n) << 7;
                     const uint64_t bv = dv + ((st * kTileBytes) >> 4);
-                    uint32_t pieces = 0;  // bit ks: 16 keys that some row sees
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        pieces |= keys.any(kb + ks * 16, kb + ks * 16 + 15) ? 1u << ks : 0u;
+                    uint32_t pieces = keys.pieces(kb);
                     if (!wait(&v_full[st], (g / NST) & 1, ab)) goto pv_done_label;
                     if (!wait(&p_full[sb], (g / 3) & 1, ab)) goto pv_done_label;
                     tc_fence_after();
-                    if (pieces == 0xffu) {
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            mma_f16_tmem_a(tO, tS + sb * 128 + (ks >> 2) * 64 + (ks & 3) * 8, bv + ((ks * 2048) >> 4), kIdescPV, ks > 0 ? 1u : acc);
-                        acc = 1;
-                    } else {
 #pragma unroll 1
-                        for (int ks = 0; ks < 8; ++ks)
+                    for (uint32_t h = 0; h < 2; ++h, pieces >>= 4)
+#pragma unroll
+                        for (uint32_t ks = 0; ks < 4; ++ks)
                             if ((pieces >> ks) & 1) {
-                                mma_f16_tmem_a(tO, tS + sb * 128 + (ks >> 2) * 64 + (ks & 3) * 8, bv + ((ks * 2048) >> 4), kIdescPV, acc);
+                                mma_f16_tmem_a(tO, tS + sb * 128 + h * 64 + ks * 8,
+                                               bv + (((h * 4 + ks) * 2048) >> 4), kIdescPV, acc);
                                 acc = 1;
                             }
-                    }
                     mma_commit(&pv_done[sb]);
                 }
                 mma_commit(&o_full);
@@ -417,23 +412,12 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             // stores instead, its first product waited 5400 cycles)
             uint32_t pk[KP][32];
 #pragma unroll
-            for (int c = 0; c < KP; ++c) {
-                uint32_t r[64];
-                tmem_ld64_sync(tO + lane_base + c * 64, tO + lane_base + c * 64 + 32, r);
-#pragma unroll
-                for (int k = 0; k < 32; ++k)
-                    pk[c][k] = Pack2<T>::pack(__uint_as_float(r[2 * k]) * inv, __uint_as_float(r[2 * k + 1]) * inv);
-            }
+            for (int c = 0; c < KP; ++c) read_panel<T>(tO + lane_base + c * 64, inv, pk[c]);
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty);
-            if (!__all_sync(0xffffffffu, seen)) {  // a row that saw nothing: 0, whatever its accumulator holds
-#pragma unroll
-                for (int c = 0; c < KP; ++c)
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) pk[c][k] = seen ? pk[c][k] : 0u;
-            }
-            store_panels<T, KP>(stage, pk, lane, args.D, [&](int i) -> T* {
+            // a row that saw nothing: 0, whatever its accumulator holds
+            store_panels<T, KP>(stage, pk, seen ? ~0u : 0u, lane, args.D, [&](int i) -> T* {
                 const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
                 if (r >= rows) return nullptr;
                 return static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
@@ -573,6 +557,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
+        if (abort_flag) set_status(p.status, abort_flag);
         args.cuts[blockIdx.x].pieces = 0;
         if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
     }
@@ -580,11 +565,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         // the copies and products issued before the stop land before the CTA
         // lets go of its shared memory and TMEM
         if (threadIdx.x == 0) {
-            mbar_drain_ring(k_full, NST, issued[0], ab);
-            mbar_drain_ring(q_full, QST, issued[1], ab);
-            mbar_drain_ring(v_full, NST, issued[2], ab);
-            if (issued[3]) mbar_drain(&s_full[(issued[3] - 1) % 3], ((issued[3] - 1) / 3) & 1, ab);
-            if (issued[4]) mbar_drain(&pv_done[(issued[4] - 1) % 3], ((issued[4] - 1) / 3) & 1, ab);
+            drain_ring(k_full, NST, issued[0]);
+            drain_ring(q_full, QST, issued[1]);
+            drain_ring(v_full, NST, issued[2]);
+            if (issued[3]) drain_wait(&s_full[(issued[3] - 1) % 3], ((issued[3] - 1) / 3) & 1);
+            if (issued[4]) drain_wait(&pv_done[(issued[4] - 1) % 3], ((issued[4] - 1) / 3) & 1);
         }
         __syncthreads();
     }

@@ -18,31 +18,52 @@ constexpr int kThreads = 512;
 constexpr uint32_t kRegsLaunch = 128, kRegsCtl = 80, kRegsEpi = 128, kRegsSoftmax = 152;
 static_assert(kRegsCtl + kRegsEpi + 2 * kRegsSoftmax <= 4 * kRegsLaunch, "register split exceeds the launch allocation");
 
-// mbar_wait for these kernels: as bounded, fewer instructions.  The roles' loops
-// have to stay in the instruction cache together, and each holds several waits.
-__device__ __forceinline__ uint32_t globaltimer_lo() {
-    uint32_t t;
-    asm volatile("mov.u32 %0, %%globaltimer_lo;" : "=r"(t));
-    return t;
-}
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Abort& ab) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint32_t t0 = globaltimer_lo();
-    while (!mbar_try_wait(bar, parity)) {
+// The code that the roles run between them has to fit the SM's instruction
+// cache: at 120 KB of kernel its refills kept the cache behind it 88 % busy and
+// doubled the time of short windows.  So the waits are short (a count of
+// attempts in place of mbar_wait's clock, the code of a failure left to the end
+// of the kernel), loops are rolled where that costs nothing, and what runs once
+// is out of line.
+//
+// Shared abort flag: 0, or the BSP_ERR_* code that stopped the kernel.
+struct Stop {
+    volatile int* flag;
+    __device__ __forceinline__ void fail(int code) const { *flag = code; }
+};
+// attempts of a wait: each is a bounded suspension of at least tens of cycles,
+// and no legal wait is longer than a step of another role (microseconds)
+constexpr int kAttempts = 1 << 22;
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Stop& ab) {
+    for (int n = kAttempts; !mbar_try_wait(bar, parity);) {
         if (*ab.flag) return false;
-        if (globaltimer_lo() - t0 > (uint32_t)kDefaultWaitNs) {  // 2 s, below the 2^32 ns of the counter
-            ab.fail(BSP_ERR_TIMEOUT);
-            return false;
-        }
+        if (--n == 0) ab.fail(BSP_ERR_TIMEOUT);
     }
     return true;
 }
-static_assert(kDefaultWaitNs < (1ull << 32), "the wait limit is counted in 32 bits");
+// After an abort, by one thread: wait, bounded, for the phase of `bar` with the
+// given parity, whatever the flag says.
+__device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
+    for (int n = kAttempts; !mbar_try_wait(bar, parity) && --n;) {}
+}
+// The same for a ring of nst stages whose phases 0 .. next - 1 were begun.
+__device__ __forceinline__ void drain_ring(uint64_t* bars, uint32_t nst, uint32_t next) {
+#pragma unroll 1
+    for (uint32_t s = 0; s < nst && s < next; ++s)
+        drain_wait(&bars[s], (s + ((next - 1 - s) / nst) * nst) / nst & 1);
+}
 
 // Visible keys of a tile's rows: j <= hi and (j >= lo or j < sinks).
 struct Keys {
     int lo, hi, sinks;
-    __device__ __forceinline__ bool any(int a, int b) const { return a <= hi && (b >= lo || a < sinks); }
+    __device__ __forceinline__ bool any(int a, int b) const { return (a <= hi) & ((b >= lo) | (a < sinks)); }
+    // bit i: some of the 16 keys from kb + 16 i is visible (i < 8)
+    __device__ __forceinline__ uint32_t pieces(int kb) const {
+        const int end = imin(hi + 1 - kb, 128);  // > 0 bounds the visible part of the tile
+        const uint32_t upto = (1u << (imax(end + 15, 0) >> 4)) - 1;
+        const uint32_t from = ~0u << (imin(imax(lo - kb, 0), 128) >> 4);
+        const uint32_t sink = (1u << (imin(imax(sinks - kb + 15, 0), 128 + 15) >> 4)) - 1;
+        return upto & (from | sink) & 0xffu;
+    }
 };
 // What the roles of a kernel need to know of a tile, handed out through a ring
 // in shared memory by the warp that walks the CTA's share: the walk's state and
@@ -76,7 +97,7 @@ struct Ring {
         }
     }
     // by a whole warp, in order i = 0, 1, ...
-    __device__ __forceinline__ bool put(uint32_t i, const Work& x, int lane, const Abort& ab) {
+    __device__ __forceinline__ bool put(uint32_t i, const Work& x, int lane, const Stop& ab) {
         const uint32_t s = i % kRing;
         const bool ok = wait(&empty[s], ((i / kRing) & 1) ^ 1, ab);
         if (!__all_sync(0xffffffffu, ok)) return false;
@@ -87,7 +108,7 @@ struct Ring {
         return true;
     }
     // by one thread, or by all lanes of a warp (`one`: the lane that answers)
-    __device__ __forceinline__ bool take(uint32_t i, Work& x, bool one, bool warp, const Abort& ab) {
+    __device__ __forceinline__ bool take(uint32_t i, Work& x, bool one, bool warp, const Stop& ab) {
         const uint32_t s = i % kRing;
         bool ok = wait(&full[s], (i / kRing) & 1, ab);
         if (warp) ok = __all_sync(0xffffffffu, ok);
@@ -104,8 +125,8 @@ __device__ __forceinline__ Keys tile_keys(const Prob& p, const Work& w) {
 }
 
 __device__ __forceinline__ Work make_work(const Prob& p, const Item& it) {
-    const QTile q = p.qtile(it.g, it.tile);
-    const Span sp = p.span(q);
+    const QTile& q = it.q;
+    const Span& sp = it.sp;
     Work w;
     w.ns = it.ns, w.s0 = it.s0, w.n = it.n, w.tile = it.tile;
     w.a = q.a, w.nt = q.nt, w.n_s = sp.n_s, w.lo = sp.lo;
@@ -158,6 +179,19 @@ __device__ __forceinline__ unsigned long long row_keys(int pos, int low, int sin
     return below(hi) & (~below(lo) | below(sk));
 }
 
+// 64 accumulator columns of a thread's row, scaled and rounded
+template <typename T>
+__device__ __forceinline__ void read_panel(uint32_t tacc, float scale, uint32_t (&pk)[32]) {
+    uint32_t r[64];
+    tmem_ld64_sync(tacc, tacc + 32, r);
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        const float2 v = __fmul2_rn(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])),
+                                    make_float2(scale, scale));
+        pk[k] = Pack2<T>::pack(v.x, v.y);
+    }
+}
+
 // 64 columns of a warp's 32 rows (thread = row, two values per register) to
 // memory through the warp's 4 KB staging panel (16-byte piece j of row r at
 // j ^ (r % 8), so neither side meets a bank twice): 8 lanes then write 128
@@ -181,14 +215,15 @@ __device__ __forceinline__ void store_panel(const uint8_t* stage, int lane, int 
         if (p && j * 8 < cols) *reinterpret_cast<uint4*>(p + j * 8) = v;
     }
 }
-// KP panels, one loop for all
+// KP panels, one loop for all; `mask`: all ones, or 0 for a row of zeros
 template <typename T, int KP, typename F>
-__device__ __forceinline__ void store_panels(uint8_t* stage, const uint32_t (&pk)[KP][32], int lane, int D, F dst) {
+__device__ __forceinline__ void store_panels(uint8_t* stage, const uint32_t (&pk)[KP][32], uint32_t mask, int lane, int D,
+                                             F dst) {
 #pragma unroll 1
     for (int c = 0; c < KP; ++c) {
         uint32_t x[32];
 #pragma unroll
-        for (int k = 0; k < 32; ++k) x[k] = c == 0 ? pk[0][k] : pk[KP - 1][k];
+        for (int k = 0; k < 32; ++k) x[k] = (c == 0 ? pk[0][k] : pk[KP - 1][k]) & mask;
         stage_panel(stage, x, lane);
         store_panel<T>(stage, lane, D - c * 64, [&](int i) -> T* {
             T* p = dst(i);

@@ -67,17 +67,11 @@ __device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, 
     }
     uint32_t pk[DP / 64][32];
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) {
-        uint32_t r[64];
-        tmem_ld64_sync(tacc + c * 64, tacc + c * 64 + 32, r);
-#pragma unroll
-        for (int k = 0; k < 32; ++k)
-            pk[c][k] = Pack2<T>::pack(__uint_as_float(r[2 * k]) * scale, __uint_as_float(r[2 * k + 1]) * scale);
-    }
+    for (int c = 0; c < DP / 64; ++c) read_panel<T>(tacc + c * 64, scale, pk[c]);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(empty);
-    store_panels<T, DP / 64>(stage, pk, lane, D, dst);
+    store_panels<T, DP / 64>(stage, pk, ~0u, lane, D, dst);
 }
 
 // ------------------------------------------------------------------- dQ ----
@@ -112,7 +106,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Abort ab{&abort_flag, p.status, kDefaultWaitNs};
+    const Stop ab{&abort_flag};
     if (threadIdx.x == 0) {
         abort_flag = 0;
         issued_a = 0;
@@ -220,11 +214,13 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     if (g >= 2 && !wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto score_done;
                     if (!wait(&k_full[st], (g >> 1) & 1, ab)) goto score_done;
                     tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                        mma_f16(tS + st * 128, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
-                    }
+                        for (uint32_t ks = 0; ks < 4; ++ks) {
+                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
+                            mma_f16(tS + st * 128, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
+                        }
                     mma_commit(&s_full[st]);
                     if (g >= 1 && !wait(&dp_free, (g - 1) & 1, ab)) {
                         ++g;
@@ -235,11 +231,13 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         goto score_done;
                     }
                     tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                        mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
-                    }
+                        for (uint32_t ks = 0; ks < 4; ++ks) {
+                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
+                            mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
+                        }
                     mma_commit(&dp_full);
                     if (n == ns - 1) mma_commit(&a_free);
                 }
@@ -260,10 +258,12 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     const uint32_t st = g & 1;
                     if (!wait(&ds_full[st], (g >> 1) & 1, ab)) goto dq_end;
                     tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_f16_tmem_a(tA, tS + st * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
-                                       dx + ((st * kTile + ks * 2048) >> 4), kIdescD, ks > 0 || n > 0);
+                        for (uint32_t ks = 0; ks < 4; ++ks)
+                            mma_f16_tmem_a(tA, tS + st * 128 + h * 64 + ks * 8, dx + ((st * kTile + (h * 4 + ks) * 2048) >> 4),
+                                           kIdescD, ks > 0 ? 1u : h + n);
                     mma_commit(&dq_done[st]);
                 }
                 mma_commit(&acc_full);
@@ -371,17 +371,18 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
+        if (abort_flag) set_status(p.status, abort_flag);
         args.cuts[blockIdx.x].pieces = 0;
         if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
     }
     if (abort_flag) {
         if (threadIdx.x == 0) {
-            mbar_drain_ring(k_full, 2, issued[0], ab);
-            mbar_drain_ring(v_full, 2, issued[1], ab);
-            if (issued_a) mbar_drain(&a_full, (issued_a - 1) & 1, ab);
-            if (issued[2]) mbar_drain(&s_full[(issued[2] - 1) & 1], ((issued[2] - 1) >> 1) & 1, ab);
-            if (issued[2]) mbar_drain(&dp_full, (issued[2] - 1) & 1, ab);
-            if (issued[3]) mbar_drain(&dq_done[(issued[3] - 1) & 1], ((issued[3] - 1) >> 1) & 1, ab);
+            drain_ring(k_full, 2, issued[0]);
+            drain_ring(v_full, 2, issued[1]);
+            if (issued_a) drain_wait(&a_full, (issued_a - 1) & 1);
+            if (issued[2]) drain_wait(&s_full[(issued[2] - 1) & 1], ((issued[2] - 1) >> 1) & 1);
+            if (issued[2]) drain_wait(&dp_full, (issued[2] - 1) & 1);
+            if (issued[3]) drain_wait(&dq_done[(issued[3] - 1) & 1], ((issued[3] - 1) >> 1) & 1);
         }
         __syncthreads();
     }
@@ -423,7 +424,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
     const Prob& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    Abort ab{&abort_flag, p.status, kDefaultWaitNs};
+    const Stop ab{&abort_flag};
     if (threadIdx.x == 0) {
         abort_flag = 0;
         issued_a = issued_k = 0;
@@ -485,10 +486,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 } else {
                     w = Work{};
                     if (walk.next(it)) {
-                        int first, nq;
-                        kp.qrange(it.tile, &first, &nq);
                         w.ns = it.ns, w.s0 = it.s0, w.n = it.n, w.tile = it.tile;
-                        w.lo = first + it.s0;
+                        w.lo = it.sp.lo + it.s0;
                         w.z = it.rep / p.Hkv, w.hk = it.rep % p.Hkv, w.rep = it.rep;
                     }
                     if (!ring.put(tiles, w, lane, ab) || w.ns == 0) break;
@@ -546,21 +545,25 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     if (g >= 1 && !wait(&dv_done, (g - 1) & 1, ab)) goto score_done;
                     if (!wait(&q_full[st], (g >> 1) & 1, ab)) goto score_done;
                     tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                        mma_f16(tS, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
-                    }
+                        for (uint32_t ks = 0; ks < 4; ++ks) {
+                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
+                            mma_f16(tS, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
+                        }
                     mma_commit(&s_full);
                     ++g;
                     if (gd >= 1 && !wait(&dk_done[(gd - 1) & 1], ((gd - 1) >> 1) & 1, ab)) goto score_done;
                     if (!wait(&g_full[st], (gd >> 1) & 1, ab)) goto score_done;
                     tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
-                    for (int ks = 0; ks < DP / 16; ++ks) {
-                        const uint32_t off = ((ks >> 2) * 16384 + (ks & 3) * 32) >> 4;
-                        mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0);
-                    }
+                        for (uint32_t ks = 0; ks < 4; ++ks) {
+                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
+                            mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
+                        }
                     mma_commit(&dp_full);
                     ++gd;
                     if (n == ns - 1) mma_commit(&a_free);
@@ -585,20 +588,24 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     if (!wait(&p_full, g & 1, ab)) goto grad_done;
                     if (!wait(&g_full[st], (g >> 1) & 1, ab)) goto grad_done;
                     tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_f16_tmem_a(tV, tS + (ks >> 2) * 64 + (ks & 3) * 8, dy + ((st * kTile + ks * 2048) >> 4), kIdescD,
-                                       ks > 0 || n > 0);
+                        for (uint32_t ks = 0; ks < 4; ++ks)
+                            mma_f16_tmem_a(tV, tS + h * 64 + ks * 8, dy + ((st * kTile + (h * 4 + ks) * 2048) >> 4),
+                                           kIdescD, ks > 0 ? 1u : h + n);
                     mma_commit(&dv_done);
                     if (n == ns - 1) mma_commit(&dv_full);
                     ++g;
                     if (n == 0 && tiles > 0 && !wait(&dk_empty, (tiles - 1) & 1, ab)) goto grad_done;
                     if (!wait(&ds_full, gk & 1, ab)) goto grad_done;
                     tc_fence_after();
+#pragma unroll 1
+                    for (uint32_t h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_f16_tmem_a(tK, tP + (ks >> 2) * 64 + (ks & 3) * 8, dx + ((st * kTile + ks * 2048) >> 4), kIdescD,
-                                       ks > 0 || n > 0);
+                        for (uint32_t ks = 0; ks < 4; ++ks)
+                            mma_f16_tmem_a(tK, tP + h * 64 + ks * 8, dx + ((st * kTile + (h * 4 + ks) * 2048) >> 4),
+                                           kIdescD, ks > 0 ? 1u : h + n);
                     mma_commit(&dk_done[st]);
                     if (n == ns - 1) mma_commit(&dk_full);
                     ++gk;
@@ -731,18 +738,19 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     tc_fence_before();
     __syncthreads();
     if (threadIdx.x == 0) {
+        if (abort_flag) set_status(p.status, abort_flag);
         args.cuts[blockIdx.x].pieces = 0;
         if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
     }
     if (abort_flag) {
         if (threadIdx.x == 0) {
-            mbar_drain_ring(q_full, 2, issued[0], ab);
-            mbar_drain_ring(g_full, 2, issued[1], ab);
-            if (issued_a) mbar_drain(&a_full, (issued_a - 1) & 1, ab);
-            if (issued[2]) mbar_drain(&s_full, (issued[2] - 1) & 1, ab);
-            if (issued[3]) mbar_drain(&dp_full, (issued[3] - 1) & 1, ab);
-            if (issued[4]) mbar_drain(&dv_done, (issued[4] - 1) & 1, ab);
-            if (issued_k) mbar_drain(&dk_done[(issued_k - 1) & 1], ((issued_k - 1) >> 1) & 1, ab);
+            drain_ring(q_full, 2, issued[0]);
+            drain_ring(g_full, 2, issued[1]);
+            if (issued_a) drain_wait(&a_full, (issued_a - 1) & 1);
+            if (issued[2]) drain_wait(&s_full, (issued[2] - 1) & 1);
+            if (issued[3]) drain_wait(&dp_full, (issued[3] - 1) & 1);
+            if (issued[4]) drain_wait(&dv_done, (issued[4] - 1) & 1);
+            if (issued_k) drain_wait(&dk_done[(issued_k - 1) & 1], ((issued_k - 1) >> 1) & 1);
         }
         __syncthreads();
     }

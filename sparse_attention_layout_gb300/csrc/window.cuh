@@ -128,6 +128,11 @@ struct Prob {
     }
     BSP_HD Span span(const QTile& q) const { return span_of(q.a, q.b, window, sinks, kshift); }
     BSP_HD int steps(const Seg& g, int t) const { return span(qtile(g, t)).n; }
+    BSP_HD int describe(const Seg& g, int t, QTile& q, Span& sp) const {
+        q = qtile(g, t);
+        sp = span(q);
+        return sp.n;
+    }
 };
 
 // The dK / dV kernel's problem (dense only): tiles are key tiles, steps the
@@ -165,6 +170,11 @@ struct KProb {
         qrange(t, &f, &n);
         return n;
     }
+    // the first query tile as the span's lo
+    BSP_HD int describe(const Seg&, int t, QTile&, Span& sp) const {
+        qrange(t, &sp.lo, &sp.n);
+        return sp.n;
+    }
 };
 
 // CTA c's share of the steps: [at(c), at(c + 1)), the first `rem` CTAs with one
@@ -179,16 +189,14 @@ struct Shares {
 // The table of `items` tiles in `cols` columns.
 struct Table {
     int cols, q, r;  // every column has q rows, the first r one more
-    BSP_HD Table(int items, int columns) : cols(columns), q(items / columns), r(items % columns) {}
+    BSP_HD Table(int items, int columns)
+        : cols(columns), q((uint32_t)items / (uint32_t)columns), r((uint32_t)items % (uint32_t)columns) {}
     // column and row of place l on the line
     BSP_HD void place(int l, int* col, int* row) const {
-        if (l < r * (q + 1)) {
-            *col = l / (q + 1);
-            *row = l % (q + 1);
-        } else {
-            *col = r + (l - r * (q + 1)) / q;
-            *row = (l - r * (q + 1)) % q;
-        }
+        const bool tall = l < r * (q + 1);
+        const uint32_t at = tall ? l : l - r * (q + 1), h = tall ? q + 1 : q;
+        *col = (tall ? 0 : r) + at / h;
+        *row = at % h;
     }
     BSP_HD int number(int col, int row) const { return row * cols + col; }
     BSP_HD int height(int col) const { return q + (col < r); }
@@ -219,6 +227,7 @@ template <int NT>
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     int64_t x = v;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
@@ -227,6 +236,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* 
     if (lane == 31) red[warp] = x;
     __syncthreads();
     int64_t before = 0, t = 0;
+#pragma unroll 1
     for (int i = 0; i < NT / 32; ++i) {
         if (i < warp) before += red[i];
         t += red[i];
@@ -268,7 +278,7 @@ __device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, int
     int64_t at = -1, sum = 0;
     int found = -1, off = 0;
     const Seg only = p.nseg == 1 ? p.seg(0) : Seg{0, 0, 0, 0};
-    const int hop = p.nseg == 1 && only.ntiles > 0 ? (int)(gridDim.x % only.ntiles) : 0;
+    const int hop = p.nseg == 1 && only.ntiles > 0 ? (int)(gridDim.x % (uint32_t)only.ntiles) : 0;
     // twice: the sum, then (for the thread that holds it) the first step's tile
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
@@ -285,7 +295,7 @@ __device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, int
                     row = 0;
                 }
                 height = tab.height(col);
-                if (p.nseg == 1) tile = tab.number(col, row) % only.ntiles;
+                if (p.nseg == 1) tile = (uint32_t)tab.number(col, row) % (uint32_t)only.ntiles;
             } else if (p.nseg == 1) {
                 tile += hop;
                 if (tile >= only.ntiles) tile -= only.ntiles;
@@ -304,7 +314,7 @@ __device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, int
                     else lo = mid + 1;
                 }
                 const Seg g = p.seg(lo);
-                v = p.steps(g, (a - (seg_end[lo] - g.ntiles) * p.rep) % g.ntiles);
+                v = p.steps(g, (uint32_t)(a - (seg_end[lo] - g.ntiles) * p.rep) % (uint32_t)g.ntiles);
             }
             if (pass == 1 && at >= before + sum && at < before + sum + v) {
                 found = l;
@@ -321,8 +331,11 @@ __device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, int
                 const int n = tot >= (int64_t)min_share * gridDim.x ? (int)gridDim.x
                                                                     : imax(1, (int)tot / min_share);
                 st.shares.n = n;
-                st.shares.base = tot / n;
-                st.shares.rem = (int)(tot - st.shares.base * n);
+                // tot / n by two 32-bit divisions (n <= 1024, tot < 2^50)
+                const uint32_t hi = (uint32_t)(tot >> 20), lo = (uint32_t)tot & 0xfffffu, un = n;
+                const uint32_t mid = (hi % un) << 20 | lo;
+                st.shares.base = ((int64_t)(hi / un) << 20) + mid / un;
+                st.shares.rem = (int)(mid % un);
                 st.count = (int)blockIdx.x < n ? st.shares.of(blockIdx.x) : 0;
                 st.items = items;
                 st.place = 0;
@@ -349,6 +362,8 @@ struct Item {
     int seg, rep, tile;
     int s0, ns, n;
     Seg g;
+    QTile q;  // of a Prob
+    Span sp;
     __device__ __forceinline__ bool whole() const { return ns == n; }
     // where a piece's partial result goes
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (s0 == 0); }
@@ -413,10 +428,10 @@ struct Walk {
             }
         }
         it.seg = seg;
-        it.rep = (a - seg0) / g.ntiles;
-        it.tile = (a - seg0) % g.ntiles;
+        it.rep = (uint32_t)(a - seg0) / (uint32_t)g.ntiles;
+        it.tile = (uint32_t)(a - seg0) % (uint32_t)g.ntiles;
         it.g = g;
-        it.n = p.steps(g, it.tile);
+        it.n = p.describe(g, it.tile, it.q, it.sp);
         it.s0 = off;
         it.ns = it.n - off;
         if (it.ns > left) it.ns = (int)left;
