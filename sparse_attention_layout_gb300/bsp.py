@@ -9,7 +9,9 @@ fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 import numpy as np
 import torch
@@ -25,12 +27,6 @@ STATUS = {0: "BSP_OK", -1: "BSP_ERR_INVALID_ARG", -2: "BSP_ERR_UNSUPPORTED",
           -6: "BSP_ERR_TIMEOUT", -7: "BSP_ERR_DEVICE_CHECK"}
 
 _lib = None
-
-
-class Tensor(ctypes.Structure):
-    """bsp_tensor_t: a pointer and the element strides of the three outer dimensions."""
-
-    _fields_ = [("ptr", ctypes.c_void_p), ("stride", ctypes.c_int64 * 3)]
 
 
 class BspError(RuntimeError):
@@ -86,7 +82,7 @@ def lib():
         L.bsp_status_string.restype = ctypes.c_char_p
         L.bsp_status_string.argtypes = [i32]
         L.bsp_version.restype = ctypes.c_char_p
-        sz, T = ctypes.c_size_t, ctypes.POINTER(Tensor)
+        sz, T = ctypes.c_size_t, P  # T: a bsp_tensor_t
         L.bsp_window_create.argtypes = [i32, i32, P, ctypes.POINTER(P)]
         L.bsp_window_destroy.argtypes = [P]
         L.bsp_window_info.argtypes = [P, P, P]
@@ -559,133 +555,161 @@ def bsp_window_status(W: Window, stream=None) -> int:
     return int(lib().bsp_window_status(W.handle, _stream(stream)))
 
 
-def _torch_stream(stream, device):
-    if stream is None:
-        return torch.cuda.current_stream(device)
-    if isinstance(stream, torch.cuda.Stream):
-        return stream
-    if not int(stream):
-        return torch.cuda.default_stream(device)
-    return torch.cuda.ExternalStream(int(stream), device=device)
-
-
-class _Call:
-    """The device and stream of one call: the handle's device is made current,
-    and what the call allocates belongs to the stream the call runs on."""
+class _OnStream:
+    """Makes `stream` (a torch stream, or a raw handle) current, with its
+    device, so that what the call allocates belongs to the stream it runs on."""
 
     def __init__(self, W: Window, stream):
-        self.W, self.stream = W, _torch_stream(stream, W.device)
-        if self.stream.device != W.device:
-            raise ValueError(f"the stream is on {self.stream.device}, the handle on {W.device}")
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = (torch.cuda.ExternalStream(int(stream), device=W.device) if int(stream)
+                      else torch.cuda.default_stream(W.device))
+        if stream.device != W.device:
+            raise ValueError(f"the stream is on {stream.device}, the handle on {W.device}")
+        self.ctx = torch.cuda.stream(stream)
 
     def __enter__(self):
-        self._ctx = torch.cuda.stream(self.stream)  # makes the stream's device current too
-        self._ctx.__enter__()
-        return self
+        self.ctx.__enter__()
 
     def __exit__(self, *a):
-        return self._ctx.__exit__(*a)
-
-    @property
-    def ptr(self):
-        return ctypes.c_void_p(self.stream.cuda_stream)
-
-    def workspace(self, nbytes: int):
-        return torch.empty(nbytes, dtype=torch.uint8, device=self.W.device)
-
-    def dtype(self, *ts):
-        d = ts[0].dtype
-        if d not in _DTYPES:
-            raise TypeError(f"unsupported dtype {d}")
-        for t in ts:
-            if t.dtype != d:
-                raise TypeError("all tensors of a call must share one dtype")
-            self.on_device(t)
-        return _DTYPES[d]
-
-    def on_device(self, *ts):
-        for t in ts:
-            if t is not None and t.device != self.W.device:
-                raise ValueError(f"a tensor is on {t.device}, the handle on {self.W.device}")
+        self.ctx.__exit__(*a)
 
 
-def _strided(t, order):
-    """bsp_tensor_t of t, its dimensions `order` as the three outer ones."""
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+def _entry(f):
+    """A call of the handle W on `stream`: with none given, on W's device's
+    current stream, and without the cost of a context when W's device is the
+    current one (the wrappers are a large part of a small call's time)."""
+
+    def call(W, *args, stream=None, **kw):
+        if stream is None:
+            if torch.cuda.current_device() == W.device.index:
+                return f(W, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+            stream = torch.cuda.current_stream(W.device)
+        with _OnStream(W, stream):
+            return f(W, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+
+    return functools.update_wrapper(call, f)
+
+
+def _same(W: Window, *ts):
+    """The calls' dtype; every tensor on the handle's device."""
+    d = ts[0].dtype
+    if d not in _DTYPES:
+        raise TypeError(f"unsupported dtype {d}")
+    for t in ts:
+        if t.dtype != d:
+            raise TypeError("all tensors of a call must share one dtype")
+        if t.device != W.device:
+            raise ValueError(f"a tensor is on {t.device}, the handle on {W.device}")
+    return _DTYPES[d]
+
+
+def _int32(W: Window, *ts):
+    for t in ts:
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("q_start, kv_len and table must be contiguous int32 tensors")
+        if t.device != W.device:
+            raise ValueError(f"a tensor is on {t.device}, the handle on {W.device}")
+
+
+_PACK = struct.Struct("=Qqqq").pack  # a bsp_tensor_t
+
+
+def _heads(t):
+    """bsp_tensor_t of [Z or pages, heads, rows or slots, D]."""
+    a, b, c, d = t.stride()
+    if d != 1 and t.shape[3] > 1:
         raise ValueError("the last dimension must be contiguous")
-    return Tensor(t.data_ptr() if t.numel() else None, (ctypes.c_int64 * 3)(*[0 if d is None else t.stride(d) for d in order]))
+    return _PACK(t.data_ptr() if t.numel() else 0, a, b, c)
+
+
+def _rows(t):
+    """bsp_tensor_t of [rows, heads, D]."""
+    a, b, d = t.stride()
+    if d != 1 and t.shape[2] > 1:
+        raise ValueError("the last dimension must be contiguous")
+    return _PACK(t.data_ptr() if t.numel() else 0, 0, b, a)
 
 
 def _shape(t, shape, what):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{what} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _lse_ok(lse, shape):
+def _lse_ok(W: Window, lse, shape):
     _shape(lse, shape, "lse")
     if lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be a contiguous float32 tensor")
+    if lse.device != W.device:
+        raise ValueError(f"lse is on {lse.device}, the handle on {W.device}")
+
+
+@functools.lru_cache(maxsize=256)
+def _window_workspace(device, Z, Hq, Hkv, Sq, backward):
+    return int(lib().bsp_window_attention_workspace(Z, Hq, Hkv, Sq, backward))
+
+
+@functools.lru_cache(maxsize=16)
+def _paged_workspace(device):
+    return int(lib().bsp_paged_attention_workspace())
 
 
 def _dense_sizes(Q, K, V):
     if Q.dim() != 4 or K.dim() != 4:
         raise ValueError("Q, K and V must be [Z, heads, rows, D]")
     Z, Hq, Sq, D = Q.shape
-    Hkv, Sk = K.shape[1], K.shape[2]
-    _shape(K, (Z, Hkv, Sk, D), "K")
-    _shape(V, (Z, Hkv, Sk, D), "V")
+    Zk, Hkv, Sk, Dk = K.shape
+    if Zk != Z or Dk != D or V.shape != K.shape:
+        raise ValueError(f"K and V must be [{Z}, KV heads, rows, {D}], got {tuple(K.shape)} and {tuple(V.shape)}")
     if Hkv < 1 or Hq % Hkv:
         raise ValueError("the query heads must be a multiple of the KV heads")
     return Z, Hq, Hkv, Sq, Sk, D
 
 
-_HEADS = (0, 1, 2)        # [Z, heads, rows, D]
-_ROWS = (None, 1, 0)      # [rows, heads, D]
-
-
+@_entry
 def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.0, stream=None):
     """Causal attention with the handle's window and sinks: (O, lse fp32
     [Z, Hq, Sq]).  Q [Z, Hq, Sq, D], K and V [Z, Hkv, Sk, D] of any strides
     that are multiples of 16 bytes with a contiguous last dimension; the
     queries are the last Sq of the Sk positions."""
     Z, Hq, Hkv, Sq, Sk, D = _dense_sizes(Q, K, V)
-    with _Call(W, stream) as c:
-        if O is None:
-            O = torch.empty((Z, Hq, Sq, D), dtype=Q.dtype, device=Q.device)
-        if lse is None:
-            lse = torch.empty((Z, Hq, Sq), dtype=torch.float32, device=Q.device)
-        dt = c.dtype(Q, K, V, O)
-        c.on_device(lse)
+    if O is None:
+        O = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    else:
         _shape(O, Q.shape, "O")
-        _lse_ok(lse, (Z, Hq, Sq))
-        n = int(lib().bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 0))
-        ws = c.workspace(n)
-        _check(lib().bsp_window_attention(W.handle, dt, *[ctypes.byref(_strided(t, _HEADS)) for t in (Q, K, V, O)],
-                                          _ptr(lse), Z, Hq, Hkv, Sq, Sk, D, float(scale), _ptr(ws), n, c.ptr),
-               "bsp_window_attention")
+    if lse is None:
+        lse = torch.empty((Z, Hq, Sq), dtype=torch.float32, device=Q.device)
+    else:
+        _lse_ok(W, lse, (Z, Hq, Sq))
+    dt = _same(W, Q, K, V, O)
+    n = _window_workspace(W.device, Z, Hq, Hkv, Sq, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
+    rc = lib().bsp_window_attention(W.handle, dt, _heads(Q), _heads(K), _heads(V), _heads(O), lse.data_ptr(), Z, Hq,
+                                    Hkv, Sq, Sk, D, scale, ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_window_attention")
     return O, lse
 
 
+@_entry
 def bsp_window_attention_backward(W: Window, Q, K, V, O, dO, lse, dQ=None, dK=None, dV=None, scale: float = 1.0,
                                   stream=None):
     """(dQ, dK, dV) of bsp_window_attention for the output gradient dO, given
     its O and lse."""
     Z, Hq, Hkv, Sq, Sk, D = _dense_sizes(Q, K, V)
-    with _Call(W, stream) as c:
-        dQ = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) if dQ is None else dQ
-        dK = torch.empty(K.shape, dtype=K.dtype, device=K.device) if dK is None else dK
-        dV = torch.empty(V.shape, dtype=V.dtype, device=V.device) if dV is None else dV
-        dt = c.dtype(Q, K, V, O, dO, dQ, dK, dV)
-        c.on_device(lse)
-        for t, like, what in ((O, Q, "O"), (dO, Q, "dO"), (dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
-            _shape(t, like.shape, what)
-        _lse_ok(lse, (Z, Hq, Sq))
-        n = int(lib().bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1))
-        ws = c.workspace(n)
-        _check(lib().bsp_window_attention_backward(
-            W.handle, dt, *[ctypes.byref(_strided(t, _HEADS)) for t in (Q, K, V, O, dO)], _ptr(lse),
-            *[ctypes.byref(_strided(t, _HEADS)) for t in (dQ, dK, dV)], Z, Hq, Hkv, Sq, Sk, D, float(scale), _ptr(ws),
-            n, c.ptr), "bsp_window_attention_backward")
+    dQ = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) if dQ is None else dQ
+    dK = torch.empty(K.shape, dtype=K.dtype, device=K.device) if dK is None else dK
+    dV = torch.empty(V.shape, dtype=V.dtype, device=V.device) if dV is None else dV
+    dt = _same(W, Q, K, V, O, dO, dQ, dK, dV)
+    for t, like, what in ((O, Q, "O"), (dO, Q, "dO"), (dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
+        _shape(t, like.shape, what)
+    _lse_ok(W, lse, (Z, Hq, Sq))
+    n = _window_workspace(W.device, Z, Hq, Hkv, Sq, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
+    rc = lib().bsp_window_attention_backward(W.handle, dt, _heads(Q), _heads(K), _heads(V), _heads(O), _heads(dO),
+                                             lse.data_ptr(), _heads(dQ), _heads(dK), _heads(dV), Z, Hq, Hkv, Sq, Sk, D,
+                                             scale, ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_window_attention_backward")
     return dQ, dK, dV
 
 
@@ -722,64 +746,61 @@ def window_attention(W: Window, Q, K, V, scale: float):
     return _WindowAttention.apply(Q, K, V, W, float(scale))
 
 
-def _paged_sizes(rows, heads, K_cache, V_cache, q_start, kv_len, table):
-    if rows.dim() != 3 or K_cache.dim() != 4:
-        raise ValueError("token rows must be [T, heads, D], caches [n_pages, Hkv, page, D]")
+def _paged_sizes(W, rows, K_cache, V_cache, q_start, kv_len, table):
+    if rows.dim() != 3 or K_cache.dim() != 4 or table.dim() != 2:
+        raise ValueError("token rows must be [T, heads, D], caches [n_pages, Hkv, page, D], table [n_seq, max_pages]")
     T, H, D = rows.shape
-    n_pages, Hkv, page = K_cache.shape[:3]
-    _shape(K_cache, (n_pages, Hkv, page, D), "K_cache")
-    _shape(V_cache, (n_pages, Hkv, page, D), "V_cache")
-    if table.dim() != 2 or table.shape[1] < 1:
-        raise ValueError("table must be [n_seq, max_pages]")
-    n_seq = table.shape[0]
+    n_pages, Hkv, page, Dk = K_cache.shape
+    n_seq, max_pages = table.shape
+    if Dk != D or V_cache.shape != K_cache.shape:
+        raise ValueError(f"the caches must be [n_pages, Hkv, page, {D}], got {tuple(K_cache.shape)} and "
+                         f"{tuple(V_cache.shape)}")
     _shape(q_start, (n_seq + 1,), "q_start")
     _shape(kv_len, (n_seq,), "kv_len")
-    for t in (q_start, kv_len, table):
-        if t.dtype != torch.int32 or not t.is_contiguous():
-            raise ValueError("q_start, kv_len and table must be contiguous int32 tensors")
-    if heads == "kv" and H != Hkv:
-        raise ValueError("new rows must have the cache's heads")
+    _int32(W, q_start, kv_len, table)
     if Hkv < 1 or H % Hkv:
         raise ValueError("the query heads must be a multiple of the KV heads")
-    return T, n_seq, table.shape[1], n_pages, page, H, Hkv, D
+    return T, n_seq, max_pages, n_pages, page, H, Hkv, D
 
 
+@_entry
 def bsp_paged_append(W: Window, K, V, K_cache, V_cache, q_start, kv_len, table, stream=None):
     """Write the new tokens' K and V rows [T, Hkv, D] to their slots of the
     caches [n_pages, Hkv, page, D] (any strides; a permuted
     [n_pages, page, Hkv, D] tensor serves too).  q_start int32 [n_seq + 1],
     kv_len int32 [n_seq] (lengths with the new tokens), table int32
     [n_seq, max_pages]."""
-    T, n_seq, max_pages, n_pages, page, _, Hkv, D = _paged_sizes(K, "kv", K_cache, V_cache, q_start, kv_len, table)
+    T, n_seq, max_pages, n_pages, page, H, Hkv, D = _paged_sizes(W, K, K_cache, V_cache, q_start, kv_len, table)
+    if H != Hkv:
+        raise ValueError("new rows must have the cache's heads")
     _shape(V, K.shape, "V")
-    with _Call(W, stream) as c:
-        dt = c.dtype(K, V, K_cache, V_cache)
-        c.on_device(q_start, kv_len, table)
-        _check(lib().bsp_paged_append(W.handle, dt, *[ctypes.byref(_strided(t, _ROWS)) for t in (K, V)],
-                                      *[ctypes.byref(_strided(t, _HEADS)) for t in (K_cache, V_cache)], _ptr(q_start),
-                                      _ptr(kv_len), _ptr(table), T, n_seq, max_pages, n_pages, page, Hkv, D, c.ptr),
-               "bsp_paged_append")
+    dt = _same(W, K, V, K_cache, V_cache)
+    rc = lib().bsp_paged_append(W.handle, dt, _rows(K), _rows(V), _heads(K_cache), _heads(V_cache), q_start.data_ptr(),
+                                kv_len.data_ptr(), table.data_ptr(), T, n_seq, max_pages, n_pages, page, Hkv, D, stream)
+    if rc:
+        raise BspError(rc, "bsp_paged_append")
 
 
+@_entry
 def bsp_paged_attention(W: Window, Q, K_cache, V_cache, q_start, kv_len, table, O=None, lse=None, scale: float = 1.0,
                         stream=None):
     """Attention of a ragged batch of new tokens Q [T, Hq, D] over the caches,
     which hold their own keys already: (O, lse fp32 [T, Hq])."""
-    T, n_seq, max_pages, n_pages, page, Hq, Hkv, D = _paged_sizes(Q, "q", K_cache, V_cache, q_start, kv_len, table)
-    with _Call(W, stream) as c:
-        if O is None:
-            O = torch.empty((T, Hq, D), dtype=Q.dtype, device=Q.device)
-        if lse is None:
-            lse = torch.empty((T, Hq), dtype=torch.float32, device=Q.device)
-        dt = c.dtype(Q, K_cache, V_cache, O)
-        c.on_device(lse, q_start, kv_len, table)
+    T, n_seq, max_pages, n_pages, page, Hq, Hkv, D = _paged_sizes(W, Q, K_cache, V_cache, q_start, kv_len, table)
+    if O is None:
+        O = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    else:
         _shape(O, Q.shape, "O")
-        _lse_ok(lse, (T, Hq))
-        n = int(lib().bsp_paged_attention_workspace())
-        ws = c.workspace(n)
-        _check(lib().bsp_paged_attention(W.handle, dt, ctypes.byref(_strided(Q, _ROWS)),
-                                         *[ctypes.byref(_strided(t, _HEADS)) for t in (K_cache, V_cache)],
-                                         ctypes.byref(_strided(O, _ROWS)), _ptr(lse), _ptr(q_start), _ptr(kv_len),
-                                         _ptr(table), T, n_seq, max_pages, n_pages, page, Hq, Hkv, D, float(scale),
-                                         _ptr(ws), n, c.ptr), "bsp_paged_attention")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=Q.device)
+    else:
+        _lse_ok(W, lse, (T, Hq))
+    dt = _same(W, Q, K_cache, V_cache, O)
+    n = _paged_workspace(W.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
+    rc = lib().bsp_paged_attention(W.handle, dt, _rows(Q), _heads(K_cache), _heads(V_cache), _rows(O), lse.data_ptr(),
+                                   q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), T, n_seq, max_pages,
+                                   n_pages, page, Hq, Hkv, D, scale, ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_paged_attention")
     return O, lse

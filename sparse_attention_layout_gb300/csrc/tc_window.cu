@@ -591,7 +591,8 @@ int launch(Call& c) {
     if (rc) return rc;
     auto kern = window_tc_kernel<T, DP, PAGED>;
     constexpr int smem = Smem<DP>::kAlloc;
-    if ((rc = prepare_kernel(kern, smem))) return rc;
+    static std::atomic<uint64_t> prepared{0};
+    if ((rc = prepare_kernel(kern, smem, prepared))) return rc;
     const int grid = sm_count();
     Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, 2, c.cuts, c.slots};
     kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a);

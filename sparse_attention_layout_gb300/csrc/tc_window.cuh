@@ -1,6 +1,7 @@
 // Shared by the tensor-core kernels of the windowed attention.
 #pragma once
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -248,13 +249,20 @@ inline int key_map(CUtensorMap* m, const View& v, const Call& c, int is_bf16, in
 }
 
 // Launch preparation: the shared memory limit, and the register count that the
-// split at kernel start divides.
+// split at kernel start divides.  Both belong to the kernel on a device, so one
+// launch per device asks.
 template <typename K>
-int prepare_kernel(K kern, int smem) {
+int prepare_kernel(K kern, int smem, std::atomic<uint64_t>& done) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BSP_ERR_CUDA;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit) return BSP_OK;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BSP_ERR_CUDA;
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return BSP_ERR_CUDA;
-    return (uint32_t)fa.numRegs == kRegsLaunch ? BSP_OK : BSP_ERR_UNSUPPORTED;
+    if ((uint32_t)fa.numRegs != kRegsLaunch) return BSP_ERR_UNSUPPORTED;
+    done.fetch_or(bit, std::memory_order_release);
+    return BSP_OK;
 }
 
 }  // namespace win

@@ -771,8 +771,9 @@ int launch(Call& c) {
     if (!rc) rc = key_map(&mv, c.V, c, is_bf16, 128);
     if (rc) return rc;
     constexpr int smem = Smem<DP>::kAlloc;
-    if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem))) return rc;
-    if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem))) return rc;
+    static std::atomic<uint64_t> prepared[2];
+    if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem, prepared[0]))) return rc;
+    if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem, prepared[1]))) return rc;
     const int grid = sm_count();
     Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + p.TQ - 1) / p.TQ, c.scale, c.scale * kLog2e, 2, c.cuts, c.slots};
     if ((rc = launch_tile_stats(c))) return rc;

@@ -486,7 +486,7 @@ def test_refusals(bsp):
         bsp.bsp_paged_append(W, q, q, kc, kc, i(0, 2), i(5), i(0)[None])
     # the C entry itself: workspace and alignment
     L = bsp.lib()
-    t = [ctypes.byref(bsp._strided(a, (0, 1, 2))) for a in (*ok, x(1, 2, 8, 64))]
+    t = [bsp._heads(a) for a in (*ok, x(1, 2, 8, 64))]
     ws = torch.empty(int(L.bsp_window_attention_workspace(1, 2, 1, 8, 0)), dtype=torch.uint8, device="cuda")
 
     def call(ptr, n, lse=None, dtype=1):

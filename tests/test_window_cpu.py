@@ -81,8 +81,7 @@ def test_largest_positions_do_not_overflow(lib):
 
 
 def test_refusals_without_a_handle(lib):
-    t = bsp.Tensor(None, (ctypes.c_int64 * 3)(0, 0, 0))
-    r = ctypes.byref(t)
+    r = bytes(32)  # a bsp_tensor_t of zeros
     assert lib.bsp_window_create(-1, 0, None, ctypes.byref(ctypes.c_void_p())) == -1
     assert lib.bsp_window_create(0, -1, None, ctypes.byref(ctypes.c_void_p())) == -1
     assert lib.bsp_window_create(0, 0, None, None) == -1
