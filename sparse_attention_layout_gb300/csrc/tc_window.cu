@@ -35,6 +35,14 @@ namespace {
 // O is rescaled only when a row's maximum grew by more than 2^8 (log2 units);
 // P stays below 2^8 then, and O / l is exact either way.
 constexpr float kRescaleThreshold = 8.0f;
+// Ragged batches: steps below which a CTA is not worth starting for a part of a
+// tile.
+constexpr int kMinShare = 2;
+
+// A dense launch's split comes with it; a ragged one's is found in the kernel.
+struct None {};
+template <bool PAGED>
+using Split = std::conditional_t<PAGED, None, Plan>;
 
 template <int DP>
 struct Smem {
@@ -57,7 +65,6 @@ struct Args {
     int64_t lz, lh, lt;
     int D;
     float c2;  // scale * log2(e)
-    int min_share;
     Cut* cuts;
     float* slots;
 };
@@ -65,7 +72,8 @@ struct Args {
 template <typename T, int DP, bool PAGED>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args args) {
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args args,
+                 const __grid_constant__ Split<PAGED> plan) {
     using SM = Smem<DP>;
     constexpr int KP = SM::KP, QST = SM::QST, NST = SM::KVST;
     constexpr uint32_t kTileBytes = SM::kTile;
@@ -87,7 +95,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     __shared__ int abort_flag;
     __shared__ uint32_t issued[5];  // K steps, Q tiles, V steps, Q K^T steps, P V steps: drained after an abort
     __shared__ Start start;
-    __shared__ int64_t red[32];
+    __shared__ uint32_t red[32];
     __shared__ Ring ring;
     __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
 
@@ -131,8 +139,13 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         tmem_relinquish();
     }
     tc_fence_before();
-    locate<kThreads>(p, args.min_share, reinterpret_cast<int*>(smem), red, &start);
-    fence_proxy_async_smem();  // locate's scratch is where the copies land next
+    if constexpr (PAGED) {
+        locate<kThreads>(p, kMinShare, reinterpret_cast<int*>(smem), red, &start);
+        fence_proxy_async_smem();  // locate's scratch is where the copies land next
+    } else if (threadIdx.x == 0) {
+        start.tab = plan.tab;
+        start.cta = plan.s[blockIdx.x];
+    }
     __syncthreads();
     tc_fence_after();
     const uint32_t tS = tmem_base;
@@ -154,7 +167,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int pages = PAGED ? 128 >> p.page_shift : 1;  // copies per 64 columns
         const int my_page = lane % pages, my_panel = lane / pages;
         const uint32_t page_bytes = PAGED ? 128u << p.page_shift : 128u * 128u;
-        Walk<Prob, PAGED> walk(p, start);
+        Walk<Prob, PAGED> walk(p, start.tab, start.cta);
         Work w;
         // one step is loaded while the next one's place, and its page number,
         // are on their way
@@ -559,7 +572,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     if (threadIdx.x == 0) {
         if (abort_flag) set_status(p.status, abort_flag);
         args.cuts[blockIdx.x].pieces = 0;
-        if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
+        if (cut.ns)
+            write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, [&](int c) {
+                if constexpr (PAGED) return start.shares.of(c);
+                else return plan.s[c].count;
+            });
     }
     if (abort_flag) {
         // the copies and products issued before the stop land before the CTA
@@ -593,9 +610,12 @@ int launch(Call& c) {
     constexpr int smem = Smem<DP>::kAlloc;
     static std::atomic<uint64_t> prepared{0};
     if ((rc = prepare_kernel(kern, smem, prepared))) return rc;
-    const int grid = sm_count();
-    Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, 2, c.cuts, c.slots};
-    kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a);
+    const int grid = imin(sm_count(), kPlanCtas);
+    Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, c.cuts, c.slots};
+    Split<PAGED> plan;
+    if constexpr (!PAGED)
+        if ((rc = query_plan(c, grid, &plan))) return rc;
+    kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     return launch_join(c, kTcRows, grid, false);
 }

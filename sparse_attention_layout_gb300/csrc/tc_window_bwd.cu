@@ -24,7 +24,6 @@ struct Args {
     const float* stats;  // per query tile: -lse log2(e) of 128 rows, then dO . O
     int D, ntiles;
     float scale, c2;     // c2 = scale * log2(e)
-    int min_share;
     Cut* cuts;
     float* slots;
 };
@@ -84,7 +83,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-             const __grid_constant__ Args args) {
+             const __grid_constant__ Args args, const __grid_constant__ Plan plan) {
     using SM = Smem<DP>;
     constexpr int KP = SM::KP;
     constexpr uint32_t kTile = SM::kTile;
@@ -99,8 +98,6 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __shared__ int abort_flag;
     __shared__ uint32_t issued[4];  // tiles and K steps, V steps, score steps, dQ steps
     __shared__ uint32_t issued_a;
-    __shared__ Start start;
-    __shared__ int64_t red[32];
     __shared__ Ring ring;
     __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
 
@@ -133,7 +130,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         tmem_relinquish();
     }
     tc_fence_before();
-    locate<kThreads>(p, args.min_share, reinterpret_cast<int*>(smem), red, &start);
+    __syncthreads();
     tc_fence_after();
     const uint32_t tS = tmem_base, tP = tmem_base + 256, tA = tmem_base + 384;
 
@@ -151,7 +148,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             }
             const uint32_t a_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
-            Walk<Prob, false> walk(p, start);
+            Walk<Prob, false> walk(p, plan.tab, plan.s[blockIdx.x]);
             Item it;
             Work w;
             while (true) {
@@ -373,7 +370,8 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         if (abort_flag) set_status(p.status, abort_flag);
         args.cuts[blockIdx.x].pieces = 0;
-        if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
+        if (cut.ns)
+            write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, [&](int c) { return plan.s[c].count; });
     }
     if (abort_flag) {
         if (threadIdx.x == 0) {
@@ -402,7 +400,8 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-              const __grid_constant__ Args args, const __grid_constant__ KProb kp) {
+              const __grid_constant__ Args args, const __grid_constant__ KProb kp,
+              const __grid_constant__ Plan plan) {
     using SM = Smem<DP>;
     constexpr int KP = SM::KP;
     constexpr uint32_t kTile = SM::kTile;
@@ -417,8 +416,6 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     __shared__ int abort_flag;
     __shared__ uint32_t issued[5];  // Q steps, dO steps, S^T steps, dP^T steps, dV steps
     __shared__ uint32_t issued_a, issued_k;
-    __shared__ Start start;
-    __shared__ int64_t red[32];
     __shared__ Ring ring;
     __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
 
@@ -454,7 +451,6 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         tmem_relinquish();
     }
     tc_fence_before();
-    locate<kThreads>(kp, args.min_share, reinterpret_cast<int*>(smem), red, &start);
     // rows past TQ * G, which no copy writes, enter the products over the rows
     // with P = 0: they must not hold NaN
     for (int i = threadIdx.x; i < 4 * (int)kTile / 16; i += kThreads)
@@ -477,7 +473,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             }
             const uint32_t bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
-            Walk<KProb, false> walk(kp, start);
+            Walk<KProb, false> walk(kp, plan.tab, plan.s[blockIdx.x]);
             Item it;
             Work w;
             while (true) {
@@ -740,7 +736,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     if (threadIdx.x == 0) {
         if (abort_flag) set_status(p.status, abort_flag);
         args.cuts[blockIdx.x].pieces = 0;
-        if (cut.ns) write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, start);
+        if (cut.ns)
+            write_cut(args.cuts, cut.seg, cut.rep, cut.tile, cut.n - cut.ns, [&](int c) { return plan.s[c].count; });
     }
     if (abort_flag) {
         if (threadIdx.x == 0) {
@@ -774,14 +771,17 @@ int launch(Call& c) {
     static std::atomic<uint64_t> prepared[2];
     if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem, prepared[0]))) return rc;
     if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem, prepared[1]))) return rc;
-    const int grid = sm_count();
-    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + p.TQ - 1) / p.TQ, c.scale, c.scale * kLog2e, 2, c.cuts, c.slots};
+    const int grid = imin(sm_count(), kPlanCtas);
+    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + p.TQ - 1) / p.TQ, c.scale, c.scale * kLog2e, c.cuts, c.slots};
+    const KProb kp{1, p.rep, p.G, p.TQ, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
+    Plan plan;
+    if ((rc = query_plan(c, grid, &plan))) return rc;
     if ((rc = launch_tile_stats(c))) return rc;
-    dq_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a);
+    dq_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     if ((rc = launch_join(c, kTcRows, grid, true))) return rc;
-    const KProb kp{1, p.rep, p.G, p.TQ, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
-    dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, kp);
+    if ((rc = key_plan(c, kp, grid, &plan))) return rc;
+    dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, kp, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     return launch_join_kv(c, kp, kTcRows, grid);
 }

@@ -10,13 +10,13 @@
 // r % G), so that one pass over the keys serves the whole group and the rows
 // of a single new token are the tile's first G.
 //
-// Split: the steps of all tiles form one line; CTA c of n takes
-// [c tot / n, (c + 1) tot / n).  A tile that a boundary cuts leaves partial
+// Split: the steps of all tiles form one line, of which each CTA takes an equal
+// run (of a dense batch, up to the next short tile's edge).  A tile that a boundary cuts leaves partial
 // results, which a second kernel joins in the order of the pieces, so results
 // do not depend on timing.  Tiles are numbered (segment, repetition, tile); a
 // segment is a shape of tiles: the whole of a dense batch, repeated for each
-// (batch entry, KV head), or one sequence of a ragged one, whose lengths only
-// the device knows, repeated for each KV head.  The line holds them column by
+// (batch entry, KV head), which the host splits, or one sequence of a ragged
+// one, whose lengths only the device knows, repeated for each KV head.  The line holds them column by
 // column of a table with one column per CTA, filled row by row: CTAs then
 // work on neighbouring tiles at the same time and share their keys in L2
 // (with each CTA on a run of consecutive tiles instead, the band of 8192 keys
@@ -177,20 +177,23 @@ struct KProb {
     }
 };
 
-// CTA c's share of the steps: [at(c), at(c + 1)), the first `rem` CTAs with one
-// more than the `base` of the others.
+// CTA c's share of `tot` steps: [at(c), at(c + 1)), the first `rem` CTAs with
+// one more than the `base` of the others.
 struct Shares {
-    int64_t base;
-    int n, rem;
-    BSP_HD int64_t at(int c) const { return base * c + imin(c, rem); }
-    BSP_HD int64_t of(int c) const { return base + (c < rem); }
+    int n, base, rem;
+    BSP_HD Shares(int tot, int ctas) : n(ctas), base((uint32_t)tot / (uint32_t)ctas), rem((uint32_t)tot % (uint32_t)ctas) {}
+    Shares() = default;
+    BSP_HD int at(int c) const { return base * c + imin(c, rem); }
+    BSP_HD int of(int c) const { return c < n ? base + (c < rem) : 0; }
 };
 
-// The table of `items` tiles in `cols` columns.
+// The table of `items` tiles in `cols` columns: every column has q rows, the
+// first r one more.
 struct Table {
-    int cols, q, r;  // every column has q rows, the first r one more
+    int cols, q, r;
     BSP_HD Table(int items, int columns)
         : cols(columns), q((uint32_t)items / (uint32_t)columns), r((uint32_t)items % (uint32_t)columns) {}
+    Table() = default;
     // column and row of place l on the line
     BSP_HD void place(int l, int* col, int* row) const {
         const bool tall = l < r * (q + 1);
@@ -202,92 +205,95 @@ struct Table {
     BSP_HD int height(int col) const { return q + (col < r); }
 };
 
-// Where a CTA's share begins, how long it is.
-struct Start {
-    Shares shares;  // among shares.n CTAs; the others do nothing
-    int64_t count;  // steps of this CTA
-    int items;      // tiles of the launch
-    int place;      // place on the line of its first tile
-    int off;        // first step of it
+// Where a CTA's share begins: step `off` of the tile at (col, row), `count`
+// steps in all.
+struct CtaStart {
+    int col, row, off, count;
+};
+
+// A dense launch's split, which the host knows: one start per CTA, handed over
+// as a kernel parameter (finding them in the kernel took a call of one tile
+// 4.6 of its 12 us).
+constexpr int kPlanCtas = 320;
+struct Plan {
+    Table tab;
+    CtaStart s[kPlanCtas];
 };
 
 // A tile that begins in CTA c and goes on in later ones: `pieces` of it (0:
-// none), the first in slot 2 c + 1, the next in slot 2 c' of each further CTA
-// c' with a share.
+// none), the first in slot 2 c + 1, the others in slots 2 (c + 1), 2 (c + 2) ...
 struct Cut {
     int pieces;
     int seg, rep, tile;
-    Shares shares;
 };
 
 #if defined(__CUDACC__)
 
+// A ragged launch's split, found on the device.
+struct Start {
+    Table tab;
+    Shares shares;
+    CtaStart cta;
+};
+
 // exclusive prefix over the block's threads; *total = the block's sum
 template <int NT>
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* red, int64_t* total) {
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red, uint32_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t x = v;
-#pragma unroll 1
+    uint32_t x = v;
+#pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
     __syncthreads();
     if (lane == 31) red[warp] = x;
     __syncthreads();
-    int64_t before = 0, t = 0;
-#pragma unroll 1
-    for (int i = 0; i < NT / 32; ++i) {
-        if (i < warp) before += red[i];
-        t += red[i];
+    uint32_t w = lane < NT / 32 ? red[lane] : 0;
+#pragma unroll
+    for (int o = 1; o < NT / 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
     }
-    *total = t;
-    return before + x - v;
+    *total = __shfl_sync(0xffffffffu, w, NT / 32 - 1);
+    const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return (warp ? before : 0) + x - v;
 }
 
-// Finds this CTA's share; called by every thread of the block.  seg_end:
-// scratch of nseg ints in shared memory (unused when nseg == 1): tiles of the
-// segments up to each, one repetition; red: 32 int64.  min_share: CTAs are
-// used only while each gets this many steps.  Each thread adds up a run of the
-// line, one scan gives the runs' starts, and the thread whose run holds the
-// share's first step finds it.
-// Out of line: the kernels' loops then stay within the instruction cache.
-template <int NT, typename P>
-__device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, int64_t* red, Start* out) {
+// Finds this CTA's share of a ragged launch; called by every thread of the
+// block.  seg_end: scratch of nseg ints in shared memory, the tiles of the
+// segments up to each; red: 32 words.  min_share: CTAs are used only while each
+// gets this many steps.  Each thread adds up a run of the line, one scan gives
+// the runs' starts, and the thread whose run holds the share's first step finds
+// it.  Out of line: the kernels' loops then stay within the instruction cache.
+template <int NT>
+__device__ __noinline__ void locate(const Prob& p, int min_share, int* seg_end, uint32_t* red, Start* out) {
     const int tid = threadIdx.x;
     int tiles = 0;  // one repetition of every segment
-    if (p.nseg == 1) {
-        tiles = p.seg(0).ntiles;
-    } else {
-    #pragma unroll 1
-        for (int s0 = 0; s0 < p.nseg; s0 += NT) {
-            const int s = s0 + tid;
-            const int64_t v = s < p.nseg ? p.seg(s).ntiles : 0;
-            int64_t total;
-            const int64_t ex = block_scan<NT>(v, red, &total);
-            if (s < p.nseg) seg_end[s] = tiles + (int)(ex + v);
-            tiles += (int)total;
-        }
-        __syncthreads();
+#pragma unroll 1
+    for (int s0 = 0; s0 < p.nseg; s0 += NT) {
+        const int s = s0 + tid;
+        const uint32_t v = s < p.nseg ? p.seg(s).ntiles : 0;
+        uint32_t total;
+        const uint32_t ex = block_scan<NT>(v, red, &total);
+        if (s < p.nseg) seg_end[s] = tiles + (int)(ex + v);
+        tiles += (int)total;
     }
+    __syncthreads();
     const int items = tiles * p.rep;
     const Table tab(items, gridDim.x);
-    // this thread's run of the line, tile after tile
     const int run = (items + NT - 1) / NT;
     const int l0 = imin(tid * run, items), l1 = imin(l0 + run, items);
-    int64_t at = -1, sum = 0;
-    int found = -1, off = 0;
-    const Seg only = p.nseg == 1 ? p.seg(0) : Seg{0, 0, 0, 0};
-    const int hop = p.nseg == 1 && only.ntiles > 0 ? (int)(gridDim.x % (uint32_t)only.ntiles) : 0;
-    // twice: the sum, then (for the thread that holds it) the first step's tile
+    int at = -1, sum = 0;
+    // twice: the sum, then (by the thread that holds it) the first step's tile
 #pragma unroll 1
     for (int pass = 0; pass < 2; ++pass) {
-        int64_t before = sum;  // second pass: steps before this run
+        int pos = sum;  // second pass: steps before this run
         sum = 0;
-        int col = 0, tile = 0, row = 0, height = 0;
+        int col = 0, row = 0, height = 0;
 #pragma unroll 1
         for (int l = l0; l < l1; ++l) {
-            if (l == l0 || ++row >= height) {
+            if (++row >= height) {
                 if (l == l0) {
                     tab.place(l, &col, &row);
                 } else {
@@ -295,64 +301,44 @@ __device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, int
                     row = 0;
                 }
                 height = tab.height(col);
-                if (p.nseg == 1) tile = (uint32_t)tab.number(col, row) % (uint32_t)only.ntiles;
-            } else if (p.nseg == 1) {
-                tile += hop;
-                if (tile >= only.ntiles) tile -= only.ntiles;
             }
-            int v;
-            if (p.nseg == 1) {
-                v = p.steps(only, tile);
-            } else {
-                // the segment that holds tile number a
-                const int a = tab.number(col, row);
-                int lo = 0, hi = p.nseg - 1;
+            // the segment that holds tile number a
+            const int a = tab.number(col, row);
+            int lo = 0, hi = p.nseg - 1;
 #pragma unroll 1
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if (seg_end[mid] * p.rep > a) hi = mid;
-                    else lo = mid + 1;
-                }
-                const Seg g = p.seg(lo);
-                v = p.steps(g, (uint32_t)(a - (seg_end[lo] - g.ntiles) * p.rep) % (uint32_t)g.ntiles);
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (seg_end[mid] * p.rep > a) hi = mid;
+                else lo = mid + 1;
             }
-            if (pass == 1 && at >= before + sum && at < before + sum + v) {
-                found = l;
-                off = (int)(at - before - sum);
-                break;
+            const Seg g = p.seg(lo);
+            const int v = p.steps(g, (uint32_t)(a - (seg_end[lo] - g.ntiles) * p.rep) % (uint32_t)g.ntiles);
+            if (pass == 1) {
+                if (at < pos + v) {
+                    out->cta.col = col;
+                    out->cta.row = row;
+                    out->cta.off = at - pos;
+                    break;
+                }
+                pos += v;
             }
             sum += v;
         }
         if (pass == 0) {
-            Start st;
-            int64_t tot;
-            const int64_t ex = block_scan<NT>(sum, red, &tot);
+            uint32_t tot;
+            const uint32_t ex = block_scan<NT>(sum, red, &tot);
+            // as many CTAs as there are tiles, or more if each still gets min_share steps
+            const Shares sh(tot, imax(1, imin(gridDim.x, imax(items, (int)tot / min_share))));
+            const int count = sh.of(blockIdx.x);
             if (tid == 0) {
-                const int n = tot >= (int64_t)min_share * gridDim.x ? (int)gridDim.x
-                                                                    : imax(1, (int)tot / min_share);
-                st.shares.n = n;
-                // tot / n by two 32-bit divisions (n <= 1024, tot < 2^50)
-                const uint32_t hi = (uint32_t)(tot >> 20), lo = (uint32_t)tot & 0xfffffu, un = n;
-                const uint32_t mid = (hi % un) << 20 | lo;
-                st.shares.base = ((int64_t)(hi / un) << 20) + mid / un;
-                st.shares.rem = (int)(mid % un);
-                st.count = (int)blockIdx.x < n ? st.shares.of(blockIdx.x) : 0;
-                st.items = items;
-                st.place = 0;
-                st.off = 0;
-                *out = st;
+                out->tab = tab;
+                out->shares = sh;
+                out->cta.count = count;
             }
-            __syncthreads();
-            st = *out;
-            at = st.shares.at(blockIdx.x);
-            const bool mine = st.count > 0 && at >= ex && at < ex + sum;
-            sum = ex;
-            if (!mine) break;
+            at = sh.at(blockIdx.x);
+            if (count == 0 || at < (int)ex || at >= (int)ex + sum) break;
+            sum = (int)ex;
         }
-    }
-    if (found >= 0) {
-        out->place = found;
-        out->off = off;
     }
     __syncthreads();
 }
@@ -375,18 +361,15 @@ template <typename P, bool MANY>
 struct Walk {
     const P& p;
     Table tab;
-    int64_t left;
+    int left;
     int col, row, height;
     int off;
     int seg, seg0;  // a segment and the number of its first tile
     Seg g;
-    __device__ __forceinline__ Walk(const P& prob, const Start& st)
-        : p(prob), tab(st.items, gridDim.x), left(st.count), off(st.off), seg(0), seg0(0) {
-        if (left > 0) {
-            tab.place(st.place, &col, &row);
-            height = tab.height(col);
-            if (!MANY) g = p.seg(0);
-        }
+    __device__ __forceinline__ Walk(const P& prob, const Table& t, const CtaStart& st)
+        : p(prob), tab(t), left(st.count), col(st.col), row(st.row), height(t.height(st.col)), off(st.off), seg(0),
+          seg0(0) {
+        if (!MANY) g = p.seg(0);
     }
     __device__ __forceinline__ bool next(Item& it) {
         if (left <= 0) return false;
@@ -434,7 +417,7 @@ struct Walk {
         it.n = p.describe(g, it.tile, it.q, it.sp);
         it.s0 = off;
         it.ns = it.n - off;
-        if (it.ns > left) it.ns = (int)left;
+        if (it.ns > left) it.ns = left;
         left -= it.ns;
         off = 0;
         return true;
@@ -442,16 +425,13 @@ struct Walk {
 };
 
 // The record of a tile that begins in this CTA and goes on for `left` steps
-// after its share.
-__device__ __forceinline__ void write_cut(Cut* cuts, int seg, int rep, int tile, int left, const Start& st) {
+// after its share; count(c): steps of CTA c.
+template <typename F>
+__device__ __forceinline__ void write_cut(Cut* cuts, int seg, int rep, int tile, int left, F count) {
     int pieces = 1;
 #pragma unroll 1
-    for (int c = blockIdx.x + 1; left > 0 && c < st.shares.n; ++c) {
-        const int64_t sh = st.shares.of(c);
-        left -= (int)(sh < left ? sh : left);
-        ++pieces;
-    }
-    cuts[blockIdx.x] = Cut{pieces, seg, rep, tile, st.shares};
+    for (int c = blockIdx.x + 1; left > 0; ++c, ++pieces) left -= count(c);
+    cuts[blockIdx.x] = Cut{pieces, seg, rep, tile};
 }
 
 #endif  // __CUDACC__

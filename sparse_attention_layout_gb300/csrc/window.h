@@ -4,10 +4,19 @@
 #include "bsp_internal.h"
 #include "window.cuh"
 
+namespace bsp {
+namespace win {
+// Splits of dense launches, by their sizes (window_plan.cpp); the oldest give
+// way.
+struct Plans;
+}  // namespace win
+}  // namespace bsp
+
 struct bsp_window_s {
     int window = 0, sinks = 0;  // as given (window 0: no limit)
     int device = -1;
     int* status = nullptr;      // device status word
+    bsp::win::Plans* plans = nullptr;
 };
 
 namespace bsp {
@@ -15,6 +24,7 @@ namespace win {
 
 // One call's tensors and sizes, checked.
 struct Call {
+    const bsp_window_s* w;
     int dtype, D;
     float scale;
     View Q, K, V, O, dO, dQ, dK, dV;
@@ -46,6 +56,13 @@ int launch_forward_tc(Call& c);   // BSP_ERR_UNSUPPORTED: not a 16-bit type
 int launch_backward_tc(Call& c);
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
                   const Prob& p, int D, cudaStream_t s);
+// The split of a dense launch's query tiles (p) or key tiles (k) over `ctas`
+// CTAs.  BSP_ERR_OOM when the host has no memory for it.
+Plans* plans_create();
+void plans_destroy(Plans* p);
+int query_plan(const Call& c, int ctas, Plan* out);
+int key_plan(const Call& c, const KProb& k, int ctas, Plan* out);
+
 // stats = rowsum(dO .* O) per row; the same and the rows' -lse log2(e), per tile
 int launch_delta(const Call& c);
 int launch_tile_stats(const Call& c);

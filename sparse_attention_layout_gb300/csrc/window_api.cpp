@@ -94,10 +94,9 @@ int check_dense(int Z, int Hq, int Hkv, int Sq, int Sk, int D, float scale) {
     if (Z < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || Sk < 0 || !valid_d(D) || !valid_scale(scale)) return BSP_ERR_INVALID_ARG;
     if (Hq % Hkv) return BSP_ERR_INVALID_ARG;
     if (Hq / Hkv > kMaxGroup || Sq > kMaxLen || Sk > kMaxLen || (int64_t)Z * Hkv > kMaxLen) return BSP_ERR_UNSUPPORTED;
-    // tiles are numbered in 32 bits, of 64 rows (queries) and 64 keys at the least
-    const int64_t tq = 64 / (Hq / Hkv);
-    if (Z && (int64_t)Z * Hkv > kMaxLen / ((Sq + tq - 1) / tq + 1)) return BSP_ERR_UNSUPPORTED;
-    if (Z && (int64_t)Z * Hkv > kMaxLen / ((Sk + 63) / 64 + 1)) return BSP_ERR_UNSUPPORTED;
+    // tiles and steps are counted in 32 bits: at the least 64 rows x 64 keys
+    const int64_t tq = 64 / (Hq / Hkv), qt = (Sq + tq - 1) / tq + 1, kt = (Sk + 63) / 64 + 1;
+    if (Z && (qt > kMaxLen / kt || (int64_t)Z * Hkv > kMaxLen / (qt * kt))) return BSP_ERR_UNSUPPORTED;
     return BSP_OK;
 }
 
@@ -130,19 +129,24 @@ extern "C" int bsp_window_create(int window, int sinks, void* stream, bsp_window
     if (!w) return BSP_ERR_OOM;
     w->window = window;
     w->sinks = sinks;
-    if (cudaGetDevice(&w->device) != cudaSuccess) {
-        delete w;
-        return BSP_ERR_CUDA;
-    }
-    if (cudaMalloc(&w->status, sizeof(int)) != cudaSuccess) {
-        (void)cudaGetLastError();
+    if (!(w->plans = bsp::win::plans_create())) {
         delete w;
         return BSP_ERR_OOM;
     }
-    if (cudaMemsetAsync(w->status, 0, sizeof(int), (cudaStream_t)stream) != cudaSuccess) {
+    int rc = BSP_OK;
+    if (cudaGetDevice(&w->device) != cudaSuccess) {
+        rc = BSP_ERR_CUDA;
+    } else if (cudaMalloc(&w->status, sizeof(int)) != cudaSuccess) {
+        (void)cudaGetLastError();
+        rc = BSP_ERR_OOM;
+    } else if (cudaMemsetAsync(w->status, 0, sizeof(int), (cudaStream_t)stream) != cudaSuccess) {
         cudaFree(w->status);
+        rc = BSP_ERR_CUDA;
+    }
+    if (rc) {
+        bsp::win::plans_destroy(w->plans);
         delete w;
-        return BSP_ERR_CUDA;
+        return rc;
     }
     *out = w;
     return BSP_OK;
@@ -151,6 +155,7 @@ extern "C" int bsp_window_create(int window, int sinks, void* stream, bsp_window
 extern "C" int bsp_window_destroy(bsp_window_t w) {
     if (!w) return BSP_OK;
     cudaFree(w->status);  // waits for the device's work
+    bsp::win::plans_destroy(w->plans);
     delete w;
     return BSP_OK;
 }
@@ -207,7 +212,7 @@ extern "C" int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_
     if (Sk == 0) {  // no key at all: zeros and -inf, by the kernels' hidden step over Q's own rows
         c.K = c.V = View{Q->ptr, {D, D, D}};
     }
-    c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
+    c.w = w, c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
     c.lse = lse;
     c.lz = (int64_t)Hq * Sq, c.lh = Sq, c.lt = 1;
     dense_prob(w, Z, Hq, Hkv, Sq, Sk, &c.p);
@@ -255,7 +260,7 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
     }
     if (Sk == 0) return zero_view(c.dQ, Z, Hq, Sq, (size_t)D * elt, elt, s);
     if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1)))) return rc;
-    c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
+    c.w = w, c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
     c.lse = const_cast<float*>(lse);
     c.lz = (int64_t)Hq * Sq, c.lh = Sq, c.lt = 1;
     dense_prob(w, Z, Hq, Hkv, Sq, Sk, &c.p);
@@ -279,8 +284,11 @@ int paged_prob(bsp_window_t w, const int32_t* q_start, const int32_t* kv_len, co
     if (Hq % Hkv) return BSP_ERR_INVALID_ARG;
     if (Hq / Hkv > kMaxGroup || T > kMaxLen || n_seq > kMaxSeqs || (int64_t)max_pages * page > kMaxLen)
         return BSP_ERR_UNSUPPORTED;
-    // tiles are numbered in 32 bits: at most one per token, and one per sequence
-    if (Hkv > kMaxLen / ((int64_t)T + n_seq + 1)) return BSP_ERR_UNSUPPORTED;
+    // tiles and steps are counted in 32 bits; a tile holds 64 rows and a step 64
+    // keys at the least, but a sequence's last tile may hold one row
+    const int64_t tq = 64 / (Hq / Hkv), qt = T <= n_seq ? T : (T + tq - 1) / tq + n_seq;
+    const int64_t kt = ((int64_t)max_pages * page + 63) / 64 + 1;
+    if (qt > 0 && (kt > (1ll << 31) / qt || Hkv > (1ll << 31) / (qt * kt) - 1)) return BSP_ERR_UNSUPPORTED;
     if (T == 0 || n_seq == 0) return BSP_OK;
     if (!q_start || !kv_len || !table) return BSP_ERR_INVALID_ARG;
     if (((uintptr_t)q_start | (uintptr_t)kv_len | (uintptr_t)table) & 3u) return BSP_ERR_ALIGNMENT;
@@ -333,7 +341,7 @@ extern "C" int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t
     if ((rc = make_view(O, 1, Hq, T, D, elt, true, &c.O))) return rc;
     if ((uintptr_t)lse & 15u) return BSP_ERR_ALIGNMENT;
     if ((rc = check_workspace(workspace, workspace_bytes, bsp_paged_attention_workspace()))) return rc;
-    c.dtype = dtype, c.D = D, c.scale = scale, c.Z = 1;
+    c.w = w, c.dtype = dtype, c.D = D, c.scale = scale, c.Z = 1;
     c.lse = lse;
     c.lz = 0, c.lh = 1, c.lt = Hq;
     c.cuts = static_cast<bsp::win::Cut*>(workspace);

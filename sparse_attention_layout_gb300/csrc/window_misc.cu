@@ -32,6 +32,7 @@ struct JoinArgs {
 // The pieces are added in their order in fp32, whoever wrote them first.
 template <typename T, bool DQ>
 __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
+    cudaGridDependencySynchronize();  // launched while the kernel that writes the pieces still runs
     const Cut cut = a.cuts[blockIdx.x];
     if (cut.pieces == 0) return;
     const Prob& p = a.p;
@@ -76,6 +77,7 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
 // Keys of cut key tiles: dK (scaled) and dV as the sums of their pieces.
 template <typename T>
 __global__ void __launch_bounds__(kJoinT) join_kv_kernel(const JoinArgs a, const KProb kp) {
+    cudaGridDependencySynchronize();
     const Cut cut = a.cuts[blockIdx.x];
     if (cut.pieces == 0) return;
     const int z = cut.rep / kp.Hkv, hk = cut.rep % kp.Hkv, lane = threadIdx.x & 31;
@@ -217,14 +219,26 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
     }
 }
 
+// Launch of a join behind the kernel whose pieces it joins: its blocks may
+// start as soon as that kernel's have, and wait inside for its end, so the
+// launch itself costs no time of its own.
+template <typename... P, typename... A>
+int launch_behind(void (*kern)(P...), int n_cta, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(n_cta, kJoinParts);
+    cfg.blockDim = dim3(kJoinT);
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+}
+
 template <typename T>
 int join_t(const JoinArgs& a, int n_cta, bool is_dq, cudaStream_t s) {
-    const dim3 grid(n_cta, kJoinParts);
-    if (is_dq)
-        join_kernel<T, true><<<grid, kJoinT, 0, s>>>(a);
-    else
-        join_kernel<T, false><<<grid, kJoinT, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    return launch_behind(is_dq ? join_kernel<T, true> : join_kernel<T, false>, n_cta, s, a);
 }
 
 template <typename T>
@@ -270,14 +284,9 @@ int launch_join(const Call& c, int rows, int n_cta, bool is_dq) {
 
 int launch_join_kv(const Call& c, const KProb& kp, int rows, int n_cta) {
     JoinArgs a{c.cuts, c.slots, c.p, c.dK, c.dV, nullptr, 0, 0, 0, c.D, rows, c.scale};
-    const dim3 grid(n_cta, kJoinParts);
-    switch (c.dtype) {
-        case BSP_F32: join_kv_kernel<float><<<grid, kJoinT, 0, c.stream>>>(a, kp); break;
-        case BSP_BF16: join_kv_kernel<__nv_bfloat16><<<grid, kJoinT, 0, c.stream>>>(a, kp); break;
-        case BSP_F16: join_kv_kernel<__half><<<grid, kJoinT, 0, c.stream>>>(a, kp); break;
-        default: return BSP_ERR_INVALID_ARG;
-    }
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    BSP_WIN_TYPES(launch_behind(join_kv_kernel<float>, n_cta, c.stream, a, kp),
+                  launch_behind(join_kv_kernel<__nv_bfloat16>, n_cta, c.stream, a, kp),
+                  launch_behind(join_kv_kernel<__half>, n_cta, c.stream, a, kp))
 }
 
 int launch_delta(const Call& c) { BSP_WIN_TYPES(delta_t<float>(c), delta_t<__nv_bfloat16>(c), delta_t<__half>(c)) }

@@ -29,7 +29,6 @@ struct Args {
     const float* delta;
     int D;
     float scale, c2;  // c2 = scale * log2(e)
-    int min_share;
     Cut* cuts;
     float* slots;
 };
@@ -159,20 +158,21 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
 }
 
 template <typename T, int DP, bool PAGED>
-__global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
+__global__ void __launch_bounds__(kT) forward_kernel(const __grid_constant__ Args A,
+                                                     const __grid_constant__ Plan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Ks = Qs + R * PITCH, *Vs = Ks + R * PITCH, *Ps = Vs + R * PITCH;
     __shared__ Start start;
-    __shared__ int64_t red[32];
+    __shared__ uint32_t red[32];
     __shared__ int pages[R];  // page of each key's slot in this step
     const Prob& p = A.p;
     report_bad_segs(p);
-    locate<kT>(p, A.min_share, reinterpret_cast<int*>(sm), red, &start);
+    if constexpr (PAGED) locate<kT>(p, 1, reinterpret_cast<int*>(sm), red, &start);
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<Prob, PAGED> walk(p, start);
+    Walk<Prob, PAGED> walk(p, PAGED ? start.tab : plan.tab, PAGED ? start.cta : plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -288,24 +288,23 @@ __global__ void __launch_bounds__(kT) forward_kernel(const Args A) {
             if (A.lse && tx == 0)
                 A.lse[w.z * A.lz + h * A.lh + t * A.lt] = l[u] > 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, start);
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) 
+            write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns,
+                      [&](int c) { return PAGED ? start.shares.of(c) : plan.s[c].count; });
     }
 }
 
 // dQ = scale dS K with dS = P (dO V^T - delta), P = exp(scale Q K^T - lse)
 template <typename T, int DP>
-__global__ void __launch_bounds__(kT) dq_kernel(const Args A) {
+__global__ void __launch_bounds__(kT) dq_kernel(const __grid_constant__ Args A, const __grid_constant__ Plan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Gs = Qs + R * PITCH, *Ks = Gs + R * PITCH, *Vs = Ks + R * PITCH, *Ps = Vs + R * PITCH;
-    __shared__ Start start;
-    __shared__ int64_t red[32];
     const Prob& p = A.p;
-    locate<kT>(p, A.min_share, reinterpret_cast<int*>(sm), red, &start);
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<Prob, false> walk(p, start);
+    Walk<Prob, false> walk(p, plan.tab, plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -378,27 +377,26 @@ __global__ void __launch_bounds__(kT) dq_kernel(const Args A) {
                     store4(dst + c, a.x * A.scale, a.y * A.scale, b.x * A.scale, b.y * A.scale);
             }
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, start);
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) 
+            write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, [&](int c) { return plan.s[c].count; });
     }
 }
 
 // dV = P^T dO, dK = scale dS^T Q per key tile, over the query tiles that see
 // it and the heads that share it
 template <typename T, int DP>
-__global__ void __launch_bounds__(kT) dkv_kernel(const Args A, const KProb kp) {
+__global__ void __launch_bounds__(kT) dkv_kernel(const __grid_constant__ Args A, const __grid_constant__ KProb kp,
+                                                 const __grid_constant__ Plan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Gs = Qs + R * PITCH, *Ks = Gs + R * PITCH, *Vs = Ks + R * PITCH;
     float *Ps = Vs + R * PITCH, *Ds = Ps + R * PP;  // P and dS, [key][row]
-    __shared__ Start start;
-    __shared__ int64_t red[32];
     __shared__ float lse_s[R], del_s[R];
     const Prob& p = A.p;
-    locate<kT>(kp, A.min_share, reinterpret_cast<int*>(sm), red, &start);
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<KProb, false> walk(kp, start);
+    Walk<KProb, false> walk(kp, plan.tab, plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -475,7 +473,8 @@ __global__ void __launch_bounds__(kT) dkv_kernel(const Args A, const KProb kp) {
                 }
             }
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, start);
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) 
+            write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, [&](int c) { return plan.s[c].count; });
     }
 }
 
@@ -489,7 +488,6 @@ Args make_args(const Call& c) {
     a.D = c.D;
     a.scale = c.scale;
     a.c2 = c.scale * kLog2e;
-    a.min_share = 1;
     a.cuts = c.cuts;
     a.slots = c.slots;
     return a;
@@ -513,19 +511,25 @@ int forward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
     size_t smem = tiles_bytes<DP>(3, 1);
     if (smem < (size_t)c.p.nseg * sizeof(int)) smem = (size_t)c.p.nseg * sizeof(int);
-    const int rc = c.p.paged ? launch(forward_kernel<T, DP, true>, grid, smem, c.stream, a)
-                             : launch(forward_kernel<T, DP, false>, grid, smem, c.stream, a);
+    Plan plan{};
+    int rc = c.p.paged ? BSP_OK : query_plan(c, grid, &plan);
+    if (rc) return rc;
+    rc = c.p.paged ? launch(forward_kernel<T, DP, true>, grid, smem, c.stream, a, plan)
+                   : launch(forward_kernel<T, DP, false>, grid, smem, c.stream, a, plan);
     return rc ? rc : launch_join(c, R, grid, false);
 }
 
 template <typename T, int DP>
 int backward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
-    int rc = launch_delta(c);
-    if (!rc) rc = launch(dq_kernel<T, DP>, grid, tiles_bytes<DP>(4, 1), c.stream, a);
-    if (!rc) rc = launch_join(c, R, grid, true);
     const KProb kp{1, c.p.rep, c.p.G, a.p.TQ, kShift, c.p.Hq, c.p.Hkv, c.p.Sq, c.p.Sk, c.p.window, c.p.sinks};
-    if (!rc) rc = launch(dkv_kernel<T, DP>, grid, tiles_bytes<DP>(4, 2), c.stream, a, kp);
+    Plan plan, kplan;
+    int rc = query_plan(c, grid, &plan);
+    if (!rc) rc = key_plan(c, kp, grid, &kplan);
+    if (!rc) rc = launch_delta(c);
+    if (!rc) rc = launch(dq_kernel<T, DP>, grid, tiles_bytes<DP>(4, 1), c.stream, a, plan);
+    if (!rc) rc = launch_join(c, R, grid, true);
+    if (!rc) rc = launch(dkv_kernel<T, DP>, grid, tiles_bytes<DP>(4, 2), c.stream, a, kp, kplan);
     return rc ? rc : launch_join_kv(c, kp, R, grid);
 }
 
@@ -533,7 +537,7 @@ int backward_t(Call& c, const Args& a, int grid) {
 
 #define BSP_WIN_DISPATCH(fn)                                                                    \
     const Args a = make_args(c);                                                                \
-    const int grid = kSimtPerSm * sm_count();                                                   \
+    const int grid = imin(kSimtPerSm * sm_count(), kPlanCtas);                                                   \
     switch (c.dtype) {                                                                          \
         case BSP_F32: return c.D <= 64 ? fn<float, 64>(c, a, grid) : fn<float, 128>(c, a, grid); \
         case BSP_BF16: return c.D <= 64 ? fn<__nv_bfloat16, 64>(c, a, grid) : fn<__nv_bfloat16, 128>(c, a, grid); \
