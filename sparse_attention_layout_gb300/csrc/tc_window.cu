@@ -430,11 +430,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             __syncwarp();
             if (lane == 0) mbar_arrive(&o_empty);
             // a row that saw nothing: 0, whatever its accumulator holds
+            T* out = static_cast<T*>(args.O.ptr) + z * args.O.s[0] + hk * p.G * args.O.s[1] + t0 * args.O.s[2];
             store_panels<T, KP>(stage, pk, seen ? ~0u : 0u, lane, args.D, [&](int i) -> T* {
                 const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
-                if (r >= rows) return nullptr;
-                return static_cast<T*>(args.O.ptr) + z * args.O.s[0] + (hk * p.G + h) * args.O.s[1] +
-                       (int64_t)(t0 + t) * args.O.s[2];
+                return r < rows ? out + h * args.O.s[1] + t * args.O.s[2] : nullptr;
             });
         }
     } else {

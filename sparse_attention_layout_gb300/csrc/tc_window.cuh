@@ -208,7 +208,7 @@ __device__ __forceinline__ void stage_panel(uint8_t* stage, const uint32_t (&pk)
 template <typename T, typename F>
 __device__ __forceinline__ void store_panel(const uint8_t* stage, int lane, int cols, F dst) {
     const int j = lane & 7;
-#pragma unroll 2
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
         const int r = i * 4 + (lane >> 3);
         const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((j ^ (r & 7)) << 4));

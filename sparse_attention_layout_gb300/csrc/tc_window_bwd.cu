@@ -283,12 +283,11 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             tc_fence_after();
             ++tiles;
             float* slot = w.whole() ? nullptr : args.slots + (size_t)w.slot() * slot_floats(kTcRows);
+            T* out = static_cast<T*>(args.dQ.ptr) + z * args.dQ.s[0] + hk * p.G * args.dQ.s[1] + w.row0 * args.dQ.s[2];
             drain<T, DP>(tA + lane_base, &acc_empty, lane, row, row < rows, slot, args.scale, args.D,
                          smem + SM::kEpi + quad * 4096, [&](int i) -> T* {
                              const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
-                             if (r >= rows) return nullptr;
-                             return static_cast<T*>(args.dQ.ptr) + z * args.dQ.s[0] + (hk * p.G + h) * args.dQ.s[1] +
-                                    (int64_t)(w.row0 + t) * args.dQ.s[2];
+                             return r < rows ? out + h * args.dQ.s[1] + t * args.dQ.s[2] : nullptr;
                          });
             if (threadIdx.x == 128 && w.s0 == 0 && !w.whole()) cut = w;
         }
@@ -623,11 +622,10 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             const int hk = w.hk, z = w.z, kb = w.tile << 7;
             float* slot = w.whole() ? nullptr : args.slots + (size_t)w.slot() * kv_slot_floats(kTcRows);
             auto rows_of = [&](const View& v) {
-                return [&, z, hk, kb](int i) -> T* {
-                    const int j = kb + quad * 32 + i;
-                    if (j >= p.Sk) return nullptr;
-                    return static_cast<T*>(v.ptr) + z * v.s[0] + hk * v.s[1] + (int64_t)j * v.s[2];
-                };
+                T* out = static_cast<T*>(v.ptr) + z * v.s[0] + hk * v.s[1] + (kb + quad * 32) * v.s[2];
+                const int64_t row_stride = v.s[2];
+                const int end = p.Sk - kb - quad * 32;
+                return [=](int i) -> T* { return i < end ? out + i * row_stride : nullptr; };
             };
             bool ok = wait(&dv_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;

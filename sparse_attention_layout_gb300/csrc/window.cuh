@@ -187,22 +187,27 @@ struct Shares {
     BSP_HD int of(int c) const { return c < n ? base + (c < rem) : 0; }
 };
 
-// The table of `items` tiles in `cols` columns: every column has q rows, the
-// first r one more.
+// The table of `items` tiles in `cols` columns: every column has q rows, and r
+// of them, evenly spread, one more (with the first r columns the longer ones
+// instead, the shares' starts drifted over whole columns, neighbouring CTAs lost
+// step, and chunks of prompts read their 170 MB of keys 11 times from HBM).
 struct Table {
-    int cols, q, r;
-    BSP_HD Table(int items, int columns)
-        : cols(columns), q((uint32_t)items / (uint32_t)columns), r((uint32_t)items % (uint32_t)columns) {}
+    int cols, q, r, items;
+    BSP_HD Table(int n, int columns)
+        : cols(columns), q((uint32_t)n / (uint32_t)columns), r((uint32_t)n % (uint32_t)columns), items(n) {}
     Table() = default;
+    BSP_HD int longer(int col) const { return (uint32_t)(col * r) / (uint32_t)cols; }  // longer columns before col
+    BSP_HD int before(int col) const { return col * q + longer(col); }
+    BSP_HD int height(int col) const { return before(col + 1) - before(col); }
+    BSP_HD int number(int col, int row) const { return row * cols + (row < q ? col : longer(col)); }
     // column and row of place l on the line
     BSP_HD void place(int l, int* col, int* row) const {
-        const bool tall = l < r * (q + 1);
-        const uint32_t at = tall ? l : l - r * (q + 1), h = tall ? q + 1 : q;
-        *col = (tall ? 0 : r) + at / h;
-        *row = at % h;
+        int c = imin((int)(((float)l + 1.0f) * cols / items), cols - 1);
+        while (before(c) > l) --c;  // the float quotient is off by one or so
+        while (before(c + 1) <= l) ++c;
+        *col = c;
+        *row = l - before(c);
     }
-    BSP_HD int number(int col, int row) const { return row * cols + col; }
-    BSP_HD int height(int col) const { return q + (col < r); }
 };
 
 // Where a CTA's share begins: step `off` of the tile at (col, row), `count`
@@ -293,14 +298,16 @@ __device__ __noinline__ void locate(const Prob& p, int min_share, int* seg_end, 
         int col = 0, row = 0, height = 0;
 #pragma unroll 1
         for (int l = l0; l < l1; ++l) {
-            if (++row >= height) {
-                if (l == l0) {
-                    tab.place(l, &col, &row);
-                } else {
+            if (l == l0) {
+                tab.place(l, &col, &row);
+                height = tab.height(col);
+            } else {
+                ++row;
+                while (row >= height) {  // a column may be empty
                     ++col;
                     row = 0;
+                    height = tab.height(col);
                 }
-                height = tab.height(col);
             }
             // the segment that holds tile number a
             const int a = tab.number(col, row);
@@ -362,25 +369,27 @@ struct Walk {
     const P& p;
     Table tab;
     int left;
-    int col, row, height;
+    int col, row, height, tail;  // tail: place in the last row
     int off;
     int seg, seg0;  // a segment and the number of its first tile
     Seg g;
     __device__ __forceinline__ Walk(const P& prob, const Table& t, const CtaStart& st)
-        : p(prob), tab(t), left(st.count), col(st.col), row(st.row), height(t.height(st.col)), off(st.off), seg(0),
-          seg0(0) {
+        : p(prob), tab(t), left(st.count), col(st.col), row(st.row), height(t.height(st.col)), tail(t.longer(st.col)), off(st.off),
+          seg(0), seg0(0) {
         if (!MANY) g = p.seg(0);
     }
     __device__ __forceinline__ bool next(Item& it) {
         if (left <= 0) return false;
-        if (row >= height) {
+        while (row >= height) {  // a column may be empty
             ++col;
             row = 0;
             height = tab.height(col);
+            tail = tab.longer(col);
             seg = 0;
             seg0 = 0;
         }
-        const int a = tab.number(col, row++);
+        const int a = row * tab.cols + (row < tab.q ? col : tail);
+        ++row;
         if constexpr (MANY) {
             // 32 segments at a time: the one that holds tile number a
             const int lane = threadIdx.x & 31;

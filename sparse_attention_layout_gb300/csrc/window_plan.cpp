@@ -37,7 +37,7 @@ void split(const std::vector<int>& steps, int rep, int ctas, Plan* out) {
     out->tab = Table(items, ctas);
     std::vector<int> at(ctas + 1, tot);
     int c = 0, pos = 0;
-    for (int col = 0; col < imin(ctas, items) && c < sh.n; ++col)
+    for (int col = 0; col < ctas && c < sh.n; ++col)
         for (int row = 0; row < out->tab.height(col) && c < sh.n; ++row) {
             const int v = steps[out->tab.number(col, row) % ntiles];
             const bool keep_whole = v <= 4 || v <= sh.base / 32;
