@@ -601,7 +601,7 @@ int launch(Call& c) {
     const Prob& p = c.p;
     CUtensorMap mq, mk, mv;
     const int rows = PAGED ? 1 << p.page_shift : 128;
-    int rc = query_map(&mq, c.Q, c, is_bf16, PAGED ? p.T : p.Sq);
+    int rc = query_map(&mq, c.Q, c, is_bf16, PAGED ? p.T : p.Sq, p.TQ);
     if (!rc) rc = key_map(&mk, c.K, c, is_bf16, rows);
     if (!rc) rc = key_map(&mv, c.V, c, is_bf16, rows);
     if (rc) return rc;

@@ -234,11 +234,11 @@ __device__ __forceinline__ void store_panels(uint8_t* stage, const uint32_t (&pk
 }
 
 // Tensor maps of a call: rows of the query heads that share a KV head (box of
-// G heads x TQ tokens), and of keys (box of `rows` rows or slots).
-inline int query_map(CUtensorMap* m, const View& v, const Call& c, int is_bf16, int64_t tokens) {
+// G heads x tq tokens), and of keys (box of `rows` rows or slots).
+inline int query_map(CUtensorMap* m, const View& v, const Call& c, int is_bf16, int64_t tokens, int tq) {
     const uint64_t n[3] = {(uint64_t)c.p.Hq, (uint64_t)tokens, (uint64_t)c.Z};
     const uint64_t s[3] = {(uint64_t)v.s[1], (uint64_t)v.s[2], (uint64_t)v.s[0]};
-    return make_tmap_4d(m, v.ptr, is_bf16, c.D, n, s, c.p.G, c.p.TQ);
+    return make_tmap_4d(m, v.ptr, is_bf16, c.D, n, s, c.p.G, tq);
 }
 inline int key_map(CUtensorMap* m, const View& v, const Call& c, int is_bf16, int rows) {
     const Prob& p = c.p;

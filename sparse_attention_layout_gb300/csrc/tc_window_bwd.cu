@@ -21,8 +21,8 @@ namespace {
 struct Args {
     Prob p;
     View dQ, dK, dV;
-    const float* stats;  // per query tile: -lse log2(e) of 128 rows, then dO . O
-    int D, ntiles;
+    const float* stats;  // per tile of kStatRows rows: -lse log2(e), then dO . O
+    int D, ntiles;       // such tiles per (batch entry, KV head)
     float scale, c2;     // c2 = scale * log2(e)
     Cut* cuts;
     float* slots;
@@ -32,12 +32,12 @@ template <int DP>
 struct Smem {
     static constexpr int KP = DP / 64;
     static constexpr int kTile = 128 * DP * 2;
-    // dq: Q, dO one stage, K, V two; dkv: K, V one stage, Q, dO two
+    // dq: Q, dO one stage, K, V two; dkv: K, V one stage, Q, dO (64 rows) four
     static constexpr int kA = 0, kB = kTile;            // the tile's own operands
-    static constexpr int kX = 2 * kTile, kY = 4 * kTile;  // the steps' operands, two stages each
+    static constexpr int kX = 2 * kTile, kY = 4 * kTile;  // the steps' operands, two (four) stages each
     static constexpr int kEpi = 6 * kTile;              // one 32 x 64 panel per epilogue warp
-    static constexpr int kStats = kEpi + 4 * 4096;      // dkv: two stages of 256 floats
-    static constexpr int kBytes = kStats + 2 * 1024;
+    static constexpr int kStats = kEpi + 4 * 4096;      // dkv: four stages of 2 * kStatRows floats
+    static constexpr int kBytes = kStats + 4 * 2 * kStatRows * 4;
     static constexpr int kAlloc = kBytes + 1024;
 };
 
@@ -306,12 +306,14 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 Work w;
                 if (!ring.take(i, w, lane == 0, true, ab)) break;
                 ns = w.ns, s0 = w.s0, n_s = w.n_s, lo_tile = w.lo;
-                const float* s = args.stats + ((int64_t)w.rep * args.ntiles + w.tile) * 256;
-                nlse = s[row];
-                delta = s[128 + row];
-                // rows past the tile's last have P = 0 by their statistics
                 const int end = w.nt * p.G - 1;
-                pos = w.a + (int)((imin(row, end) * inv_g) >> 16);
+                const int t = (imin(row, end) * inv_g) >> 16, h = row - t * p.G;
+                const int tq = kStatRows / p.G, tok = w.row0 + t;
+                const float* s = args.stats + ((int64_t)w.rep * args.ntiles + tok / tq) * (2 * kStatRows) +
+                                 tok % tq * p.G + h;
+                nlse = row <= end ? s[0] : -INFINITY;  // rows past the tile's last: P = 0
+                delta = row <= end ? s[kStatRows] : 0.f;
+                pos = w.a + t;
                 seen.first = w.a + (int)((imin(quad * 32, end) * inv_g) >> 16);
                 seen.last = w.a + (int)((imin(quad * 32 + 31, end) * inv_g) >> 16);
             }
@@ -390,11 +392,16 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 }
 
 // --------------------------------------------------------------- dK, dV ----
-// Roles: warps 0, 3 copy K and Q (with the query tile's statistics), V and dO;
-// warp 1 issues S^T = K Q^T and dP^T = V dO^T; warp 2 issues dV += P^T dO and
+// Roles: warps 0, 3 copy K and Q (with the rows' statistics), V and dO; warp 1
+// issues S^T = K Q^T and dP^T = V dO^T; warp 2 issues dV += P^T dO and
 // dK += dS^T Q; warps 4..7 write dV and dK; warps 8..15 form P^T and dS^T,
-// thread = key, each warpgroup half of the step's rows.
-// TMEM columns: S^T 0 (P^T over it), dP^T 128 (dS^T over it), dV 256, dK 384.
+// thread = key, the warpgroups taking turns at the steps.
+// A step is 64 query rows: P^T lies over S^T and dS^T over dP^T, so a product of
+// the next scores has to wait for the products that read them, and with both
+// accumulators of D = 128 tensor memory has room for two steps of 64 rows but
+// only one of 128 (measured with those: 4150 cycles per 128 rows, the tensor
+// core idle half of the time).
+// TMEM columns: S^T 0 and 64, dP^T 128 and 192, dV 256, dK 384.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
@@ -403,13 +410,15 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
               const __grid_constant__ Plan plan) {
     using SM = Smem<DP>;
     constexpr int KP = SM::KP;
-    constexpr uint32_t kTile = SM::kTile;
+    constexpr uint32_t kTile = SM::kTile, kStep = kTile / 2, kPanel = kStatRows * 128;
     constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
-    constexpr uint32_t kIdescS = idesc_f16(128, 128, kBf, 0, 0), kIdescD = idesc_f16(128, DP, kBf, 0, 1);
+    constexpr uint32_t kIdescS = idesc_f16(128, kStatRows, kBf, 0, 0), kIdescD = idesc_f16(128, DP, kBf, 0, 1);
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    __shared__ uint64_t a_full, a_free, q_full[2], g_full[2], s_full, p_full, dv_done, dp_full, ds_full, dk_done[2];
+    // stages of Q and dO: step % 4; scores: step % 2
+    __shared__ uint64_t a_full, a_free, q_full[4], g_full[4], dk_done[4];
+    __shared__ uint64_t s_full[2], p_full[2], dv_done[2], dp_full[2], ds_full[2];
     __shared__ uint64_t dv_full, dv_empty, dk_full, dk_empty;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -427,16 +436,18 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         for (int i = 0; i < 5; ++i) issued[i] = 0;
         mbar_init(&a_full, 2);  // K with Q's producer, V with dO's
         mbar_init(&a_free, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < 4; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&g_full[i], 1);
             mbar_init(&dk_done[i], 1);
         }
-        mbar_init(&s_full, 1);
-        mbar_init(&p_full, 8);
-        mbar_init(&dv_done, 1);
-        mbar_init(&dp_full, 1);
-        mbar_init(&ds_full, 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], 4);
+            mbar_init(&dv_done[i], 1);
+            mbar_init(&dp_full[i], 1);
+            mbar_init(&ds_full[i], 4);
+        }
         mbar_init(&dv_full, 1);
         mbar_init(&dk_full, 1);
         mbar_init(&dv_empty, 4);
@@ -452,8 +463,9 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     tc_fence_before();
     // rows past TQ * G, which no copy writes, enter the products over the rows
     // with P = 0: they must not hold NaN
-    for (int i = threadIdx.x; i < 4 * (int)kTile / 16; i += kThreads)
-        *reinterpret_cast<uint4*>(smem + SM::kX + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+    if (kp.TQ * p.G < kStatRows)
+        for (int i = threadIdx.x; i < 4 * (int)kTile / 16; i += kThreads)
+            *reinterpret_cast<uint4*>(smem + SM::kX + i * 16) = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     __syncthreads();
     tc_fence_after();
@@ -470,7 +482,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tma_prefetch_desc(ta);
                 tma_prefetch_desc(tm);
             }
-            const uint32_t bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
+            const uint32_t bytes = (uint32_t)(kp.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
             Walk<KProb, false> walk(kp, plan.tab, plan.s[blockIdx.x]);
             Item it;
@@ -501,20 +513,21 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 ++tiles;
 #pragma unroll 1
                 for (int n = 0; n < w.ns; ++n, ++g) {
-                    const uint32_t st = g & 1;
-                    if (g >= 2) {
-                        const bool ok = wait(&dk_done[st], ((g - 2) >> 1) & 1, ab);
+                    const uint32_t st = g & 3;
+                    if (g >= 4) {
+                        const bool ok = wait(&dk_done[st], ((g - 4) >> 2) & 1, ab);
                         if (!__all_sync(0xffffffffu, ok)) goto load_done;
                     }
                     uint64_t* full = is_g ? &g_full[st] : &q_full[st];
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(full, bytes + (is_g ? 0u : 1024u));
+                        mbar_arrive_expect_tx(full, bytes + (is_g ? 0u : 8u * kStatRows));
                         for (int c = 0; c < KP; ++c)
-                            tma_load_4d(smem_u32(smem + (is_g ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64,
-                                        w.hk * p.G, (w.lo + n) * p.TQ, w.z, full);
+                            tma_load_4d(smem_u32(smem + (is_g ? SM::kY : SM::kX) + st * kStep + c * kPanel), tm, c * 64,
+                                        w.hk * p.G, (w.lo + n) * kp.TQ, w.z, full);
                         if (!is_g)
-                            bulk_load(smem_u32(smem + SM::kStats + st * 1024),
-                                      args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * 256, 1024, full);
+                            bulk_load(smem_u32(smem + SM::kStats + st * 8 * kStatRows),
+                                      args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * 2 * kStatRows,
+                                      8 * kStatRows, full);
                     }
                 }
             }
@@ -536,30 +549,30 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 if (!wait(&a_full, tiles & 1, ab)) goto score_done;
 #pragma unroll 1
                 for (int n = 0; n < ns; ++n) {
-                    const uint32_t st = g & 1;
-                    if (g >= 1 && !wait(&dv_done, (g - 1) & 1, ab)) goto score_done;
-                    if (!wait(&q_full[st], (g >> 1) & 1, ab)) goto score_done;
+                    const uint32_t st = g & 3, sb = g & 1;
+                    if (g >= 2 && !wait(&dv_done[sb], ((g - 2) >> 1) & 1, ab)) goto score_done;
+                    if (!wait(&q_full[st], (g >> 2) & 1, ab)) goto score_done;
                     tc_fence_after();
 #pragma unroll 1
                     for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
                         for (uint32_t ks = 0; ks < 4; ++ks) {
-                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
-                            mma_f16(tS, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
+                            mma_f16(tS + sb * 64, da + ((c * 16384 + ks * 32) >> 4),
+                                    dx + ((st * kStep + c * kPanel + ks * 32) >> 4), kIdescS, ks > 0 ? 1u : c);
                         }
-                    mma_commit(&s_full);
+                    mma_commit(&s_full[sb]);
                     ++g;
-                    if (gd >= 1 && !wait(&dk_done[(gd - 1) & 1], ((gd - 1) >> 1) & 1, ab)) goto score_done;
-                    if (!wait(&g_full[st], (gd >> 1) & 1, ab)) goto score_done;
+                    if (gd >= 2 && !wait(&dk_done[(gd - 2) & 3], ((gd - 2) >> 2) & 1, ab)) goto score_done;
+                    if (!wait(&g_full[st], (gd >> 2) & 1, ab)) goto score_done;
                     tc_fence_after();
 #pragma unroll 1
                     for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
                         for (uint32_t ks = 0; ks < 4; ++ks) {
-                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
-                            mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
+                            mma_f16(tP + sb * 64, db + ((c * 16384 + ks * 32) >> 4),
+                                    dy + ((st * kStep + c * kPanel + ks * 32) >> 4), kIdescS, ks > 0 ? 1u : c);
                         }
-                    mma_commit(&dp_full);
+                    mma_commit(&dp_full[sb]);
                     ++gd;
                     if (n == ns - 1) mma_commit(&a_free);
                 }
@@ -570,37 +583,33 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             issued[3] = gd;
         } else if (warp == 2 && lane == 0) {
             // ----------------------------------- dV and dK products ----
-            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 128 * 128, 1024, kSw128);
-            const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 128 * 128, 1024, kSw128);
+            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), kPanel, 1024, kSw128);
+            const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), kPanel, 1024, kSw128);
             uint32_t g = 0, gk = 0, tiles = 0;
             Work w;
             while (ring.take(tiles, w, true, false, ab)) {
                 const int ns = w.ns;
 #pragma unroll 1
                 for (int n = 0; n < ns; ++n) {
-                    const uint32_t st = g & 1;
+                    const uint32_t st = g & 3, sb = g & 1;
                     if (n == 0 && tiles > 0 && !wait(&dv_empty, (tiles - 1) & 1, ab)) goto grad_done;
-                    if (!wait(&p_full, g & 1, ab)) goto grad_done;
-                    if (!wait(&g_full[st], (g >> 1) & 1, ab)) goto grad_done;
+                    if (!wait(&g_full[st], (g >> 2) & 1, ab)) goto grad_done;
+                    if (!wait(&p_full[sb], (g >> 1) & 1, ab)) goto grad_done;
                     tc_fence_after();
-#pragma unroll 1
-                    for (uint32_t h = 0; h < 2; ++h)
 #pragma unroll
-                        for (uint32_t ks = 0; ks < 4; ++ks)
-                            mma_f16_tmem_a(tV, tS + h * 64 + ks * 8, dy + ((st * kTile + (h * 4 + ks) * 2048) >> 4),
-                                           kIdescD, ks > 0 ? 1u : h + n);
-                    mma_commit(&dv_done);
+                    for (uint32_t ks = 0; ks < kStatRows / 16; ++ks)
+                        mma_f16_tmem_a(tV, tS + sb * 64 + ks * 8, dy + ((st * kStep + ks * 2048) >> 4), kIdescD,
+                                       ks > 0 ? 1u : n);
+                    mma_commit(&dv_done[sb]);
                     if (n == ns - 1) mma_commit(&dv_full);
                     ++g;
                     if (n == 0 && tiles > 0 && !wait(&dk_empty, (tiles - 1) & 1, ab)) goto grad_done;
-                    if (!wait(&ds_full, gk & 1, ab)) goto grad_done;
+                    if (!wait(&ds_full[sb], (gk >> 1) & 1, ab)) goto grad_done;
                     tc_fence_after();
-#pragma unroll 1
-                    for (uint32_t h = 0; h < 2; ++h)
 #pragma unroll
-                        for (uint32_t ks = 0; ks < 4; ++ks)
-                            mma_f16_tmem_a(tK, tP + h * 64 + ks * 8, dx + ((st * kTile + (h * 4 + ks) * 2048) >> 4),
-                                           kIdescD, ks > 0 ? 1u : h + n);
+                    for (uint32_t ks = 0; ks < kStatRows / 16; ++ks)
+                        mma_f16_tmem_a(tK, tP + sb * 64 + ks * 8, dx + ((st * kStep + ks * 2048) >> 4), kIdescD,
+                                       ks > 0 ? 1u : n);
                     mma_commit(&dk_done[st]);
                     if (n == ns - 1) mma_commit(&dk_full);
                     ++gk;
@@ -645,8 +654,6 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         // ------------------------------------------------ P^T and dS^T ----
         const int wg = (warp - 8) >> 2, quad = warp & 3, row = quad * 32 + lane;
         const uint32_t lane_base = (uint32_t)(quad * 32) << 16;
-        // tokens of this half's first and last row
-        const int t_first = wg * 64 / p.G, t_last = imin(wg * 64 + 63, p.TQ * p.G - 1) / p.G;
         uint32_t g = 0;
         for (uint32_t i = 0;; ++i) {
             int ns, first, j;
@@ -659,25 +666,26 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             const int j_first = j - lane, j_last = j_first + 31;
 #pragma unroll 1
             for (int n = 0; n < ns; ++n, ++g) {
-                const uint32_t st = g & 1;
+                if ((g & 1) != (uint32_t)wg) continue;
+                const uint32_t st = g & 3, ph = (g >> 1) & 1;
                 // rows that see the key: tokens from the key's own to window - 1
                 // later ones (a sink: all later ones), G rows each
-                const int tok = p.Sk - p.Sq + (first + n) * p.TQ;  // position of row 0
-                // the warp's keys against this half's first and last row
-                const bool full = (tok + t_first >= j_last) &
-                                  ((tok + t_last - j_first < p.window) | (j_last < p.sinks));
-                const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 1024) + wg * 64;
-                bool ok = wait(&q_full[st], (g >> 1) & 1, ab);
-                ok = ok && wait(&s_full, g & 1, ab);
+                const int tok = p.Sk - p.Sq + (first + n) * kp.TQ;  // position of row 0
+                // the warp's keys against the first and last row
+                const bool full =
+                    (tok >= j_last) & ((tok + kp.TQ - 1 - j_first < p.window) | (j_last < p.sinks));
+                const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 8 * kStatRows);
+                bool ok = wait(&q_full[st], (g >> 2) & 1, ab);
+                ok = ok && wait(&s_full[wg], ph, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 float x[64];
                 tmem_ld64_sync(tS + lane_base + wg * 64, tS + lane_base + wg * 64 + 32,
                                *reinterpret_cast<uint32_t(*)[64]>(x));
                 if (!full) {
-                    const int c0 = imin(imax(j - tok, 0), 128) * p.G - wg * 64;
-                    const int c1 = j < p.sinks ? 64 : imin(imax(j - tok + p.window, 0), 128) * p.G - wg * 64;
-                    hide(x, below(imin(imax(c1, 0), 64)) & ~below(imin(imax(c0, 0), 64)));
+                    const int c0 = imin(imin(imax(j - tok, 0), 64) * p.G, 64);
+                    const int c1 = j < p.sinks ? 64 : imin(imin(imax(j - tok + p.window, 0), 64) * p.G, 64);
+                    hide(x, below(c1) & ~below(c0));
                 }
                 {
                     uint32_t pk[32];
@@ -698,8 +706,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&p_full);
-                ok = wait(&dp_full, g & 1, ab);
+                if (lane == 0) mbar_arrive(&p_full[wg]);
+                ok = wait(&dp_full[wg], ph, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
                 uint32_t pk[32];
@@ -709,7 +717,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     tmem_ld32_sync(tP + lane_base + wg * 64 + c * 32, r);
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
-                        const float4 dl = *reinterpret_cast<const float4*>(stats + 128 + c * 32 + i);
+                        const float4 dl = *reinterpret_cast<const float4*>(stats + kStatRows + c * 32 + i);
                         const float2 d0 = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
                                                      make_float2(-dl.x, -dl.y));
                         const float2 d1 = __fadd2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
@@ -723,7 +731,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tmem_st32_sync(tP + lane_base + wg * 64, pk);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&ds_full);
+                if (lane == 0) mbar_arrive(&ds_full[wg]);
             }
         }
     ds_done:;
@@ -739,13 +747,13 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     }
     if (abort_flag) {
         if (threadIdx.x == 0) {
-            drain_ring(q_full, 2, issued[0]);
-            drain_ring(g_full, 2, issued[1]);
+            drain_ring(q_full, 4, issued[0]);
+            drain_ring(g_full, 4, issued[1]);
             if (issued_a) drain_wait(&a_full, (issued_a - 1) & 1);
-            if (issued[2]) drain_wait(&s_full, (issued[2] - 1) & 1);
-            if (issued[3]) drain_wait(&dp_full, (issued[3] - 1) & 1);
-            if (issued[4]) drain_wait(&dv_done, (issued[4] - 1) & 1);
-            if (issued_k) drain_wait(&dk_done[(issued_k - 1) & 1], ((issued_k - 1) >> 1) & 1);
+            drain_ring(s_full, 2, issued[2]);
+            drain_ring(dp_full, 2, issued[3]);
+            drain_ring(dv_done, 2, issued[4]);
+            drain_ring(dk_done, 4, issued_k);
         }
         __syncthreads();
     }
@@ -759,9 +767,12 @@ template <typename T, int DP>
 int launch(Call& c) {
     const int is_bf16 = std::is_same<T, __nv_bfloat16>::value;
     const Prob& p = c.p;
-    CUtensorMap mq, mk, mv, mg;
-    int rc = query_map(&mq, c.Q, c, is_bf16, p.Sq);
-    if (!rc) rc = query_map(&mg, c.dO, c, is_bf16, p.Sq);
+    CUtensorMap mq, mk, mv, mg, mq2, mg2;
+    const int tq2 = kStatRows / p.G;
+    int rc = query_map(&mq, c.Q, c, is_bf16, p.Sq, p.TQ);
+    if (!rc) rc = query_map(&mg, c.dO, c, is_bf16, p.Sq, p.TQ);
+    if (!rc) rc = query_map(&mq2, c.Q, c, is_bf16, p.Sq, tq2);
+    if (!rc) rc = query_map(&mg2, c.dO, c, is_bf16, p.Sq, tq2);
     if (!rc) rc = key_map(&mk, c.K, c, is_bf16, 128);
     if (!rc) rc = key_map(&mv, c.V, c, is_bf16, 128);
     if (rc) return rc;
@@ -770,8 +781,8 @@ int launch(Call& c) {
     if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem, prepared[0]))) return rc;
     if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem, prepared[1]))) return rc;
     const int grid = imin(sm_count(), kPlanCtas);
-    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + p.TQ - 1) / p.TQ, c.scale, c.scale * kLog2e, c.cuts, c.slots};
-    const KProb kp{1, p.rep, p.G, p.TQ, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
+    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + tq2 - 1) / tq2, c.scale, c.scale * kLog2e, c.cuts, c.slots};
+    const KProb kp{1, p.rep, p.G, tq2, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
     Plan plan;
     if ((rc = query_plan(c, grid, &plan))) return rc;
     if ((rc = launch_tile_stats(c))) return rc;
@@ -779,7 +790,7 @@ int launch(Call& c) {
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     if ((rc = launch_join(c, kTcRows, grid, true))) return rc;
     if ((rc = key_plan(c, kp, grid, &plan))) return rc;
-    dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, kp, plan);
+    dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq2, mk, mv, mg2, a, kp, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     return launch_join_kv(c, kp, kTcRows, grid);
 }

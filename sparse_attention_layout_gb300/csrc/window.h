@@ -30,8 +30,8 @@ struct Call {
     View Q, K, V, O, dO, dQ, dK, dV;
     float* lse;
     int64_t lz, lh, lt;  // strides of lse (batch entry, head, row)
-    // backward: rows' dO . O, laid out as lse (CUDA cores), or per query tile
-    // -lse log2(e) and dO . O of its 128 rows (tensor cores)
+    // backward: rows' dO . O, laid out as lse (CUDA cores), or per tile of
+    // kStatRows rows their -lse log2(e) and dO . O (tensor cores)
     float* stats;
     Prob p;              // TQ and kshift set by the launcher
     int Z;
@@ -49,6 +49,8 @@ constexpr size_t kv_slot_floats(int rows) { return (size_t)rows * kSlotD * 2; }
 // CTAs per SM of the CUDA-core kernels (64-row tiles) and the tensor-core ones
 // (128-row tiles); both need the same workspace
 constexpr int kSimtPerSm = 2, kSimtRows = 64, kTcRows = 128;
+// query rows of a step of the tensor-core dK / dV kernel
+constexpr int kStatRows = 64;
 
 int launch_forward_simt(Call& c);
 int launch_backward_simt(Call& c);

@@ -70,7 +70,7 @@ int make_view(const bsp_tensor_t* t, int64_t n0, int64_t n1, int64_t n2, int D, 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace: one record per CTA, two partial-result slots per CTA, and for the
-// backward two floats per row of a query tile.
+// backward two floats per query row, in tiles.
 size_t cuts_bytes() { return round_up(sizeof(bsp::win::Cut) * bsp::win::kSimtPerSm * bsp::sm_count()); }
 size_t slots_bytes(bool backward) {
     const size_t rows = bsp::win::kTcRows;
@@ -182,10 +182,10 @@ extern "C" int bsp_window_status(bsp_window_t w, void* stream) {
 extern "C" size_t bsp_window_attention_workspace(int Z, int Hq, int Hkv, int Sq, int backward) {
     if (Z < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > kMaxGroup || Sq < 0) return 0;
     size_t n = cuts_bytes() + slots_bytes(backward != 0);
-    // two floats per row of each 128-row query tile (more than the one per row
-    // that the CUDA-core kernels keep)
-    const size_t tq = 128 / (Hq / Hkv);
-    if (backward) n += round_up((size_t)Z * Hkv * ((Sq + tq - 1) / tq) * 256 * sizeof(float));
+    // two floats per row of each tile (more than the one per row that the
+    // CUDA-core kernels keep)
+    const size_t rows = bsp::win::kStatRows, tq = rows / (Hq / Hkv);
+    if (backward) n += round_up((size_t)Z * Hkv * ((Sq + tq - 1) / tq) * 2 * rows * sizeof(float));
     return n;
 }
 

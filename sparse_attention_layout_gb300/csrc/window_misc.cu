@@ -128,18 +128,18 @@ __global__ void __launch_bounds__(256) delta_kernel(const View O, const View dO,
     }
 }
 
-// The same per query tile of 128 rows (row r: token r / G, head r % G, as the
-// tensor-core kernels lay them out): tile i's 128 values of -lse log2(e), then
-// its 128 of dO . O, so that one bulk copy brings a tile's statistics.  Rows
-// beyond the sequence and rows that see nothing get -inf: their P is then 0.
+// The same per tile of kStatRows rows (row r: token r / G, head r % G, as the
+// tensor-core kernels lay them out): tile i's values of -lse log2(e), then of
+// dO . O, so that one bulk copy brings a tile's statistics.  Rows beyond the
+// sequence and rows that see nothing get -inf: their P is then 0.
 template <typename T>
 __global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const View dO, const float* lse, float* stats,
                                                          int64_t rows, int ntiles, int G, int TQ, int Hkv, int S, int D) {
     constexpr int N = Vec16<T>::N;
     const int sub = threadIdx.x & 7;
     for (int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); i < rows; i += (int64_t)gridDim.x * 32) {
-        const int r = (int)(i & 127);
-        const int64_t tile = i >> 7, zh = tile / ntiles;
+        const int r = (int)(i % kStatRows);
+        const int64_t tile = i / kStatRows, zh = tile / ntiles;
         const int z = (int)(zh / Hkv), t = (int)(tile % ntiles) * TQ + r / G;
         const int64_t h = zh % Hkv * G + r % G;
         const bool live = r < TQ * G && t < S;
@@ -160,8 +160,8 @@ __global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const Vie
         for (int k = 4; k; k >>= 1) x += __shfl_xor_sync(group, x, k);
         if (sub == 0) {
             const float l = live ? lse[(z * (int64_t)Hkv * G + h) * S + t] : -INFINITY;
-            stats[tile * 256 + r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-            stats[tile * 256 + 128 + r] = x;
+            stats[tile * 2 * kStatRows + r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+            stats[tile * 2 * kStatRows + kStatRows + r] = x;
         }
     }
 }
@@ -252,11 +252,11 @@ int delta_t(const Call& c) {
 
 template <typename T>
 int tile_stats_t(const Call& c) {
-    const int ntiles = (c.p.Sq + c.p.TQ - 1) / c.p.TQ;
-    const int64_t rows = (int64_t)c.Z * c.p.Hkv * ntiles * 128;
+    const int tq = kStatRows / c.p.G, ntiles = (c.p.Sq + tq - 1) / tq;
+    const int64_t rows = (int64_t)c.Z * c.p.Hkv * ntiles * kStatRows;
     const int64_t blocks = (rows + 31) / 32, most = (int64_t)sm_count() * 16;
     tile_stats_kernel<T><<<(int)(blocks < most ? blocks : most), 256, 0, c.stream>>>(
-        c.O, c.dO, c.lse, c.stats, rows, ntiles, c.p.G, c.p.TQ, c.p.Hkv, c.p.Sq, c.D);
+        c.O, c.dO, c.lse, c.stats, rows, ntiles, c.p.G, tq, c.p.Hkv, c.p.Sq, c.D);
     return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 

@@ -158,7 +158,7 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
 }
 
 template <typename T, int DP, bool PAGED>
-__global__ void __launch_bounds__(kT) forward_kernel(const __grid_constant__ Args A,
+__global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __grid_constant__ Args A,
                                                      const __grid_constant__ Plan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kT) forward_kernel(const __grid_constant__ Arg
 
 // dQ = scale dS K with dS = P (dO V^T - delta), P = exp(scale Q K^T - lse)
 template <typename T, int DP>
-__global__ void __launch_bounds__(kT) dq_kernel(const __grid_constant__ Args A, const __grid_constant__ Plan plan) {
+__global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_constant__ Args A, const __grid_constant__ Plan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Gs = Qs + R * PITCH, *Ks = Gs + R * PITCH, *Vs = Ks + R * PITCH, *Ps = Vs + R * PITCH;
@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kT) dq_kernel(const __grid_constant__ Args A, 
 // dV = P^T dO, dK = scale dS^T Q per key tile, over the query tiles that see
 // it and the heads that share it
 template <typename T, int DP>
-__global__ void __launch_bounds__(kT) dkv_kernel(const __grid_constant__ Args A, const __grid_constant__ KProb kp,
+__global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_constant__ Args A, const __grid_constant__ KProb kp,
                                                  const __grid_constant__ Plan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
