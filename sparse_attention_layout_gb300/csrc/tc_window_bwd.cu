@@ -74,10 +74,12 @@ __device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, 
 }
 
 // ------------------------------------------------------------------- dQ ----
-// Roles: warps 0, 3 copy Q and K, dO and V; warp 1 issues S = Q K^T into
-// buffer g % 2 and dP = dO V^T; warp 2 issues dQ += dS K (dS from TMEM over its
-// own scores, K as it lies); warps 4..7 write dQ; warps 8..15 form dS, thread =
-// row, each warpgroup half of the step's keys.
+// Roles: warp 0 copies; warp 1 issues S = Q K^T into buffer g % 2, warp 3
+// dP = dO V^T, warp 2 dQ += dS K (dS from TMEM over its own scores, K as it
+// lies); warps 4..7 write dQ; warps 8..15 form dS, thread = row, each warpgroup
+// half of the step's keys.  Three issuing threads, because each spends more
+// time on its barriers (200 cycles for one that has long completed, while the
+// other warps load the shared-memory pipe) than on its products.
 // TMEM columns: S 0 and 128, dP 256, dQ 384.
 template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -96,7 +98,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     __shared__ uint64_t acc_full, acc_empty;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    __shared__ uint32_t issued[4];  // tiles and K steps, V steps, score steps, dQ steps
+    __shared__ uint32_t issued[5];  // K steps, V steps, S steps, dQ steps, dP steps
     __shared__ uint32_t issued_a;
     __shared__ Ring ring;
     __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
@@ -107,9 +109,9 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     if (threadIdx.x == 0) {
         abort_flag = 0;
         issued_a = 0;
-        for (int i = 0; i < 4; ++i) issued[i] = 0;
-        mbar_init(&a_full, 2);  // Q with K's producer, dO with V's
-        mbar_init(&a_free, 1);
+        for (int i = 0; i < 5; ++i) issued[i] = 0;
+        mbar_init(&a_full, 1);
+        mbar_init(&a_free, 2);  // S has read Q, dP has read dO
         mbar_init(&dp_full, 1);
         mbar_init(&dp_free, 8);
         for (int i = 0; i < 2; ++i) {
@@ -136,15 +138,14 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 
     if (warp < 4) {
         regs_dec<kRegsCtl>();
-        if (warp == 0 || warp == 3) {
-            // ------------------------------------------------ producers ----
-            // warp 0 walks the share and hands the tiles out
-            const bool is_v = warp == 3;
-            const CUtensorMap* tm = is_v ? &tmV : &tmK;
-            const CUtensorMap* ta = is_v ? &tmG : &tmQ;
+        if (warp == 0) {
+            // ------------------------------------------------- producer ----
+            // walks the share and hands the tiles out
             if (lane == 0) {
-                tma_prefetch_desc(tm);
-                tma_prefetch_desc(ta);
+                tma_prefetch_desc(&tmQ);
+                tma_prefetch_desc(&tmG);
+                tma_prefetch_desc(&tmK);
+                tma_prefetch_desc(&tmV);
             }
             const uint32_t a_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
@@ -152,23 +153,20 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             Item it;
             Work w;
             while (true) {
-                if (is_v) {
-                    if (!ring.take(tiles, w, lane == 0, true, ab)) break;
-                } else {
-                    w.ns = 0;
-                    if (walk.next(it)) w = make_work(p, it);
-                    if (!ring.put(tiles, w, lane, ab) || w.ns == 0) break;
-                }
+                w.ns = 0;
+                if (walk.next(it)) w = make_work(p, it);
+                if (!ring.put(tiles, w, lane, ab) || w.ns == 0) break;
                 // the previous tile's S and dP products have read Q and dO
                 if (tiles > 0) {
                     const bool ok = wait(&a_free, (tiles - 1) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto load_done;
                 }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&a_full, a_bytes);
-                    for (int c = 0; c < KP; ++c)
-                        tma_load_4d(smem_u32(smem + (is_v ? SM::kB : SM::kA) + c * 16384), ta, c * 64, w.hk * p.G, w.row0,
-                                    w.z, &a_full);
+                    mbar_arrive_expect_tx(&a_full, 2 * a_bytes);
+                    for (int c = 0; c < KP; ++c) {
+                        tma_load_4d(smem_u32(smem + SM::kA + c * 16384), &tmQ, c * 64, w.hk * p.G, w.row0, w.z, &a_full);
+                        tma_load_4d(smem_u32(smem + SM::kB + c * 16384), &tmG, c * 64, w.hk * p.G, w.row0, w.z, &a_full);
+                    }
                 }
                 ++tiles;
 #pragma unroll 1
@@ -180,26 +178,29 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         const bool ok = wait(&dq_done[st], ((g - 2) >> 1) & 1, ab);
                         if (!__all_sync(0xffffffffu, ok)) goto load_done;
                     }
-                    uint64_t* full = is_v ? &v_full[st] : &k_full[st];
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(full, kTile);
+                        const int kb = w.key_tile(n) << 7;
+                        mbar_arrive_expect_tx(&k_full[st], kTile);
                         for (int c = 0; c < KP; ++c)
-                            tma_load_4d(smem_u32(smem + (is_v ? SM::kY : SM::kX) + st * kTile + c * 16384), tm, c * 64,
-                                        w.key_tile(n) << 7, w.hk, w.z, full);
+                            tma_load_4d(smem_u32(smem + SM::kX + st * kTile + c * 16384), &tmK, c * 64, kb, w.hk, w.z,
+                                        &k_full[st]);
+                        mbar_arrive_expect_tx(&v_full[st], kTile);
+                        for (int c = 0; c < KP; ++c)
+                            tma_load_4d(smem_u32(smem + SM::kY + st * kTile + c * 16384), &tmV, c * 64, kb, w.hk, w.z,
+                                        &v_full[st]);
                     }
                 }
             }
         load_done:
             if (lane == 0) {
-                issued[is_v] = g;
-                atomicMax(&issued_a, tiles);
+                issued[0] = issued[1] = g;
+                issued_a = tiles;
             }
-        } else if (warp == 1 && lane == 0) {
-            // ------------------------------------ S and dP products ----
-            const uint64_t da = smem_desc(smem_u32(smem + SM::kA), 16, 1024, kSw128);
-            const uint64_t db = smem_desc(smem_u32(smem + SM::kB), 16, 1024, kSw128);
-            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 16, 1024, kSw128);
-            const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 16, 1024, kSw128);
+        } else if ((warp == 1 || warp == 3) && lane == 0) {
+            // ---------------------------------- S (warp 1), dP (warp 3) ----
+            const bool is_s = warp == 1;
+            const uint64_t da = smem_desc(smem_u32(smem + (is_s ? SM::kA : SM::kB)), 16, 1024, kSw128);
+            const uint64_t dx = smem_desc(smem_u32(smem + (is_s ? SM::kX : SM::kY)), 16, 1024, kSw128);
             uint32_t g = 0, tiles = 0;
             Work w;
             while (ring.take(tiles, w, true, false, ab)) {
@@ -208,40 +209,26 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 #pragma unroll 1
                 for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g & 1;
-                    if (g >= 2 && !wait(&dq_done[st], ((g - 2) >> 1) & 1, ab)) goto score_done;
-                    if (!wait(&k_full[st], (g >> 1) & 1, ab)) goto score_done;
+                    // S buffer free: dQ of step g - 2; dP's: step g - 1 has been read
+                    if (is_s ? g >= 2 : g >= 1)
+                        if (!wait(is_s ? &dq_done[st] : &dp_free, (is_s ? (g - 2) >> 1 : g - 1) & 1, ab)) goto score_done;
+                    if (!wait(is_s ? &k_full[st] : &v_full[st], (g >> 1) & 1, ab)) goto score_done;
                     tc_fence_after();
-#pragma unroll 1
+                    const uint32_t d = is_s ? tS + st * 128 : tP;
+#pragma unroll
                     for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
                         for (uint32_t ks = 0; ks < 4; ++ks) {
                             const uint32_t off = (c * 16384 + ks * 32) >> 4;
-                            mma_f16(tS + st * 128, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
+                            mma_f16(d, da + off, dx + ((st * kTile) >> 4) + off, kIdescS, c + ks > 0 ? 1u : 0u);
                         }
-                    mma_commit(&s_full[st]);
-                    if (g >= 1 && !wait(&dp_free, (g - 1) & 1, ab)) {
-                        ++g;
-                        goto score_done;
-                    }
-                    if (!wait(&v_full[st], (g >> 1) & 1, ab)) {
-                        ++g;
-                        goto score_done;
-                    }
-                    tc_fence_after();
-#pragma unroll 1
-                    for (uint32_t c = 0; c < KP; ++c)
-#pragma unroll
-                        for (uint32_t ks = 0; ks < 4; ++ks) {
-                            const uint32_t off = (c * 16384 + ks * 32) >> 4;
-                            mma_f16(tP, db + off, dy + ((st * kTile) >> 4) + off, kIdescS, ks > 0 ? 1u : c);
-                        }
-                    mma_commit(&dp_full);
+                    mma_commit(is_s ? &s_full[st] : &dp_full);
                     if (n == ns - 1) mma_commit(&a_free);
                 }
                 ++tiles;
             }
         score_done:
-            issued[2] = g;
+            issued[is_s ? 2 : 4] = g;
         } else if (warp == 2 && lane == 0) {
             // ------------------------------------------- dQ product ----
             const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 128 * 128, 1024, kSw128);
@@ -380,7 +367,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             drain_ring(v_full, 2, issued[1]);
             if (issued_a) drain_wait(&a_full, (issued_a - 1) & 1);
             if (issued[2]) drain_wait(&s_full[(issued[2] - 1) & 1], ((issued[2] - 1) >> 1) & 1);
-            if (issued[2]) drain_wait(&dp_full, (issued[2] - 1) & 1);
+            if (issued[4]) drain_wait(&dp_full, (issued[4] - 1) & 1);
             if (issued[3]) drain_wait(&dq_done[(issued[3] - 1) & 1], ((issued[3] - 1) >> 1) & 1);
         }
         __syncthreads();
@@ -392,9 +379,8 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
 }
 
 // --------------------------------------------------------------- dK, dV ----
-// Roles: warps 0, 3 copy K and Q (with the rows' statistics), V and dO; warp 1
-// issues S^T = K Q^T and dP^T = V dO^T; warp 2 issues dV += P^T dO and
-// dK += dS^T Q; warps 4..7 write dV and dK; warps 8..15 form P^T and dS^T,
+// Roles: warp 0 copies; warp 1 issues S^T = K Q^T, warp 3 dP^T = V dO^T, warp 2
+// dV += P^T dO and dK += dS^T Q; warps 4..7 write dV and dK; warps 8..15 form P^T and dS^T,
 // thread = key, the warpgroups taking turns at the steps.
 // A step is 64 query rows: P^T lies over S^T and dS^T over dP^T, so a product of
 // the next scores has to wait for the products that read them, and with both
@@ -434,8 +420,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         abort_flag = 0;
         issued_a = issued_k = 0;
         for (int i = 0; i < 5; ++i) issued[i] = 0;
-        mbar_init(&a_full, 2);  // K with Q's producer, V with dO's
-        mbar_init(&a_free, 1);
+        mbar_init(&a_full, 1);
+        mbar_init(&a_free, 2);  // S^T has read K, dP^T has read V
         for (int i = 0; i < 4; ++i) {
             mbar_init(&q_full[i], 1);
             mbar_init(&g_full[i], 1);
@@ -473,14 +459,13 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
     if (warp < 4) {
         regs_dec<kRegsCtl>();
-        if (warp == 0 || warp == 3) {
-            // ------------------------------------------------ producers ----
-            const bool is_g = warp == 3;
-            const CUtensorMap* ta = is_g ? &tmV : &tmK;
-            const CUtensorMap* tm = is_g ? &tmG : &tmQ;
+        if (warp == 0) {
+            // ------------------------------------------------- producer ----
             if (lane == 0) {
-                tma_prefetch_desc(ta);
-                tma_prefetch_desc(tm);
+                tma_prefetch_desc(&tmQ);
+                tma_prefetch_desc(&tmG);
+                tma_prefetch_desc(&tmK);
+                tma_prefetch_desc(&tmV);
             }
             const uint32_t bytes = (uint32_t)(kp.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
@@ -488,27 +473,24 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             Item it;
             Work w;
             while (true) {
-                if (is_g) {
-                    if (!ring.take(tiles, w, lane == 0, true, ab)) break;
-                } else {
-                    w = Work{};
-                    if (walk.next(it)) {
-                        w.ns = it.ns, w.s0 = it.s0, w.n = it.n, w.tile = it.tile;
-                        w.lo = it.sp.lo + it.s0;
-                        w.z = it.rep / p.Hkv, w.hk = it.rep % p.Hkv, w.rep = it.rep;
-                    }
-                    if (!ring.put(tiles, w, lane, ab) || w.ns == 0) break;
+                w = Work{};
+                if (walk.next(it)) {
+                    w.ns = it.ns, w.s0 = it.s0, w.n = it.n, w.tile = it.tile;
+                    w.lo = it.sp.lo + it.s0;
+                    w.z = it.rep / p.Hkv, w.hk = it.rep % p.Hkv, w.rep = it.rep;
                 }
+                if (!ring.put(tiles, w, lane, ab) || w.ns == 0) break;
                 // the previous tile's score products have read K and V
                 if (tiles > 0) {
                     const bool ok = wait(&a_free, (tiles - 1) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto load_done;
                 }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&a_full, kTile);
-                    for (int c = 0; c < KP; ++c)
-                        tma_load_4d(smem_u32(smem + (is_g ? SM::kB : SM::kA) + c * 16384), ta, c * 64, w.tile << 7, w.hk,
-                                    w.z, &a_full);
+                    mbar_arrive_expect_tx(&a_full, 2 * kTile);
+                    for (int c = 0; c < KP; ++c) {
+                        tma_load_4d(smem_u32(smem + SM::kA + c * 16384), &tmK, c * 64, w.tile << 7, w.hk, w.z, &a_full);
+                        tma_load_4d(smem_u32(smem + SM::kB + c * 16384), &tmV, c * 64, w.tile << 7, w.hk, w.z, &a_full);
+                    }
                 }
                 ++tiles;
 #pragma unroll 1
@@ -518,69 +500,63 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                         const bool ok = wait(&dk_done[st], ((g - 4) >> 2) & 1, ab);
                         if (!__all_sync(0xffffffffu, ok)) goto load_done;
                     }
-                    uint64_t* full = is_g ? &g_full[st] : &q_full[st];
                     if (lane == 0) {
-                        mbar_arrive_expect_tx(full, bytes + (is_g ? 0u : 8u * kStatRows));
+                        const int tok = (w.lo + n) * kp.TQ;
+                        mbar_arrive_expect_tx(&q_full[st], bytes + 8u * kStatRows);
                         for (int c = 0; c < KP; ++c)
-                            tma_load_4d(smem_u32(smem + (is_g ? SM::kY : SM::kX) + st * kStep + c * kPanel), tm, c * 64,
-                                        w.hk * p.G, (w.lo + n) * kp.TQ, w.z, full);
-                        if (!is_g)
-                            bulk_load(smem_u32(smem + SM::kStats + st * 8 * kStatRows),
-                                      args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * 2 * kStatRows,
-                                      8 * kStatRows, full);
+                            tma_load_4d(smem_u32(smem + SM::kX + st * kStep + c * kPanel), &tmQ, c * 64, w.hk * p.G, tok,
+                                        w.z, &q_full[st]);
+                        bulk_load(smem_u32(smem + SM::kStats + st * 8 * kStatRows),
+                                  args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * 2 * kStatRows, 8 * kStatRows,
+                                  &q_full[st]);
+                        mbar_arrive_expect_tx(&g_full[st], bytes);
+                        for (int c = 0; c < KP; ++c)
+                            tma_load_4d(smem_u32(smem + SM::kY + st * kStep + c * kPanel), &tmG, c * 64, w.hk * p.G, tok,
+                                        w.z, &g_full[st]);
                     }
                 }
             }
         load_done:
             if (lane == 0) {
-                issued[is_g] = g;
-                atomicMax(&issued_a, tiles);
+                issued[0] = issued[1] = g;
+                issued_a = tiles;
             }
-        } else if (warp == 1 && lane == 0) {
-            // --------------------------------- S^T and dP^T products ----
-            const uint64_t da = smem_desc(smem_u32(smem + SM::kA), 16, 1024, kSw128);
-            const uint64_t db = smem_desc(smem_u32(smem + SM::kB), 16, 1024, kSw128);
-            const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), 16, 1024, kSw128);
-            const uint64_t dy = smem_desc(smem_u32(smem + SM::kY), 16, 1024, kSw128);
-            uint32_t g = 0, gd = 0, tiles = 0;
+        } else if ((warp == 1 || warp == 3) && lane == 0) {
+            // ------------------------------ S^T (warp 1), dP^T (warp 3) ----
+            const bool is_s = warp == 1;
+            const uint64_t da = smem_desc(smem_u32(smem + (is_s ? SM::kA : SM::kB)), 16, 1024, kSw128);
+            const uint64_t dx = smem_desc(smem_u32(smem + (is_s ? SM::kX : SM::kY)), 16, 1024, kSw128);
+            uint64_t* const full = is_s ? q_full : g_full;
+            uint64_t* const out = is_s ? s_full : dp_full;
+            const uint32_t d = is_s ? tS : tP;
+            uint32_t g = 0, tiles = 0;
             Work w;
             while (ring.take(tiles, w, true, false, ab)) {
                 const int ns = w.ns;
                 if (!wait(&a_full, tiles & 1, ab)) goto score_done;
 #pragma unroll 1
-                for (int n = 0; n < ns; ++n) {
+                for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g & 3, sb = g & 1;
-                    if (g >= 2 && !wait(&dv_done[sb], ((g - 2) >> 1) & 1, ab)) goto score_done;
-                    if (!wait(&q_full[st], (g >> 2) & 1, ab)) goto score_done;
+                    if (!wait(&full[st], (g >> 2) & 1, ab)) goto score_done;
+                    // the buffer's previous step has been read: P^T by dV, dS^T by dK
+                    if (g >= 2) {
+                        uint64_t* used = is_s ? &dv_done[sb] : &dk_done[(g - 2) & 3];
+                        if (!wait(used, (is_s ? (g - 2) >> 1 : (g - 2) >> 2) & 1, ab)) goto score_done;
+                    }
                     tc_fence_after();
-#pragma unroll 1
+#pragma unroll
                     for (uint32_t c = 0; c < KP; ++c)
 #pragma unroll
-                        for (uint32_t ks = 0; ks < 4; ++ks) {
-                            mma_f16(tS + sb * 64, da + ((c * 16384 + ks * 32) >> 4),
-                                    dx + ((st * kStep + c * kPanel + ks * 32) >> 4), kIdescS, ks > 0 ? 1u : c);
-                        }
-                    mma_commit(&s_full[sb]);
-                    ++g;
-                    if (gd >= 2 && !wait(&dk_done[(gd - 2) & 3], ((gd - 2) >> 2) & 1, ab)) goto score_done;
-                    if (!wait(&g_full[st], (gd >> 2) & 1, ab)) goto score_done;
-                    tc_fence_after();
-#pragma unroll 1
-                    for (uint32_t c = 0; c < KP; ++c)
-#pragma unroll
-                        for (uint32_t ks = 0; ks < 4; ++ks) {
-                            mma_f16(tP + sb * 64, db + ((c * 16384 + ks * 32) >> 4),
-                                    dy + ((st * kStep + c * kPanel + ks * 32) >> 4), kIdescS, ks > 0 ? 1u : c);
-                        }
-                    mma_commit(&dp_full[sb]);
-                    ++gd;
+                        for (uint32_t ks = 0; ks < 4; ++ks)
+                            mma_f16(d + sb * 64, da + ((c * 16384 + ks * 32) >> 4),
+                                    dx + ((st * kStep + c * kPanel + ks * 32) >> 4), kIdescS, c + ks > 0 ? 1u : 0u);
+                    mma_commit(&out[sb]);
                     if (n == ns - 1) mma_commit(&a_free);
                 }
                 ++tiles;
             }
         score_done:
-            issued[2] = g;
-            issued[3] = gd;
+            issued[is_s ? 2 : 3] = g;
         } else if (warp == 2 && lane == 0) {
             // ----------------------------------- dV and dK products ----
             const uint64_t dx = smem_desc(smem_u32(smem + SM::kX), kPanel, 1024, kSw128);
