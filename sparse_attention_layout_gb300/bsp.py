@@ -555,6 +555,12 @@ def bsp_window_status(W: Window, stream=None) -> int:
     return int(lib().bsp_window_status(W.handle, _stream(stream)))
 
 
+# the current stream of a device as a raw handle, without the 3 us that building
+# a torch.cuda.Stream costs
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+
+
 class _OnStream:
     """Makes `stream` (a torch stream, or a raw handle) current, with its
     device, so that what the call allocates belongs to the stream it runs on."""
@@ -580,12 +586,13 @@ def _entry(f):
     current one (the wrappers are a large part of a small call's time)."""
 
     def call(W, *args, stream=None, **kw):
+        dev = W.device.index
         if stream is None:
-            if torch.cuda.current_device() == W.device.index:
-                return f(W, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+            if torch.cuda.current_device() == dev:
+                return f(W, *args, stream=_raw_stream(dev), **kw)
             stream = torch.cuda.current_stream(W.device)
         with _OnStream(W, stream):
-            return f(W, *args, stream=torch.cuda.current_stream().cuda_stream, **kw)
+            return f(W, *args, stream=_raw_stream(dev), **kw)
 
     return functools.update_wrapper(call, f)
 

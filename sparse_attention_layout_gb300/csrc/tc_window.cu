@@ -42,7 +42,7 @@ constexpr int kMinShare = 2;
 // A dense launch's split comes with it; a ragged one's is found in the kernel.
 struct None {};
 template <bool PAGED>
-using Split = std::conditional_t<PAGED, None, Plan>;
+using Split = std::conditional_t<PAGED, None, TcPlan>;
 
 template <int DP>
 struct Smem {
@@ -609,11 +609,11 @@ int launch(Call& c) {
     constexpr int smem = Smem<DP>::kAlloc;
     static std::atomic<uint64_t> prepared{0};
     if ((rc = prepare_kernel(kern, smem, prepared))) return rc;
-    const int grid = imin(sm_count(), kPlanCtas);
+    const int grid = imin(sm_count(), TcPlan::kCtas);
     Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, c.cuts, c.slots};
     Split<PAGED> plan;
     if constexpr (!PAGED)
-        if ((rc = query_plan(c, grid, &plan))) return rc;
+        if ((rc = query_plan(c, grid, &plan.tab, plan.s))) return rc;
     kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     return launch_join(c, kTcRows, grid, false);

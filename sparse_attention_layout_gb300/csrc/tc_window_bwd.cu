@@ -85,7 +85,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(kThreads, 1)
 dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
              const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
-             const __grid_constant__ Args args, const __grid_constant__ Plan plan) {
+             const __grid_constant__ Args args, const __grid_constant__ TcPlan plan) {
     using SM = Smem<DP>;
     constexpr int KP = SM::KP;
     constexpr uint32_t kTile = SM::kTile;
@@ -393,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
               const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmG,
               const __grid_constant__ Args args, const __grid_constant__ KProb kp,
-              const __grid_constant__ Plan plan) {
+              const __grid_constant__ TcPlan plan) {
     using SM = Smem<DP>;
     constexpr int KP = SM::KP;
     constexpr uint32_t kTile = SM::kTile, kStep = kTile / 2, kPanel = kStatRows * 128;
@@ -402,13 +402,13 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    // stages of Q and dO: step % 4; scores: step % 2
-    __shared__ uint64_t a_full, a_free, q_full[4], g_full[4], dk_done[4];
+    // stages of Q, dO and the rows' statistics: step % 4; scores: step % 2
+    __shared__ uint64_t a_full, a_free, x_full[4], dk_done[4];
     __shared__ uint64_t s_full[2], p_full[2], dv_done[2], dp_full[2], ds_full[2];
     __shared__ uint64_t dv_full, dv_empty, dk_full, dk_empty;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
-    __shared__ uint32_t issued[5];  // Q steps, dO steps, S^T steps, dP^T steps, dV steps
+    __shared__ uint32_t issued[5];  // steps: copied, -, S^T, dP^T, dV
     __shared__ uint32_t issued_a, issued_k;
     __shared__ Ring ring;
     __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
@@ -423,8 +423,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         mbar_init(&a_full, 1);
         mbar_init(&a_free, 2);  // S^T has read K, dP^T has read V
         for (int i = 0; i < 4; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&g_full[i], 1);
+            mbar_init(&x_full[i], 1);
             mbar_init(&dk_done[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
@@ -502,23 +501,22 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     }
                     if (lane == 0) {
                         const int tok = (w.lo + n) * kp.TQ;
-                        mbar_arrive_expect_tx(&q_full[st], bytes + 8u * kStatRows);
+                        mbar_arrive_expect_tx(&x_full[st], 2 * bytes + 8u * kStatRows);
                         for (int c = 0; c < KP; ++c)
                             tma_load_4d(smem_u32(smem + SM::kX + st * kStep + c * kPanel), &tmQ, c * 64, w.hk * p.G, tok,
-                                        w.z, &q_full[st]);
+                                        w.z, &x_full[st]);
                         bulk_load(smem_u32(smem + SM::kStats + st * 8 * kStatRows),
                                   args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * 2 * kStatRows, 8 * kStatRows,
-                                  &q_full[st]);
-                        mbar_arrive_expect_tx(&g_full[st], bytes);
+                                  &x_full[st]);
                         for (int c = 0; c < KP; ++c)
                             tma_load_4d(smem_u32(smem + SM::kY + st * kStep + c * kPanel), &tmG, c * 64, w.hk * p.G, tok,
-                                        w.z, &g_full[st]);
+                                        w.z, &x_full[st]);
                     }
                 }
             }
         load_done:
             if (lane == 0) {
-                issued[0] = issued[1] = g;
+                issued[0] = g;
                 issued_a = tiles;
             }
         } else if ((warp == 1 || warp == 3) && lane == 0) {
@@ -526,7 +524,6 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             const bool is_s = warp == 1;
             const uint64_t da = smem_desc(smem_u32(smem + (is_s ? SM::kA : SM::kB)), 16, 1024, kSw128);
             const uint64_t dx = smem_desc(smem_u32(smem + (is_s ? SM::kX : SM::kY)), 16, 1024, kSw128);
-            uint64_t* const full = is_s ? q_full : g_full;
             uint64_t* const out = is_s ? s_full : dp_full;
             const uint32_t d = is_s ? tS : tP;
             uint32_t g = 0, tiles = 0;
@@ -537,7 +534,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll 1
                 for (int n = 0; n < ns; ++n, ++g) {
                     const uint32_t st = g & 3, sb = g & 1;
-                    if (!wait(&full[st], (g >> 2) & 1, ab)) goto score_done;
+                    if (!wait(&x_full[st], (g >> 2) & 1, ab)) goto score_done;
                     // the buffer's previous step has been read: P^T by dV, dS^T by dK
                     if (g >= 2) {
                         uint64_t* used = is_s ? &dv_done[sb] : &dk_done[(g - 2) & 3];
@@ -569,7 +566,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 for (int n = 0; n < ns; ++n) {
                     const uint32_t st = g & 3, sb = g & 1;
                     if (n == 0 && tiles > 0 && !wait(&dv_empty, (tiles - 1) & 1, ab)) goto grad_done;
-                    if (!wait(&g_full[st], (g >> 2) & 1, ab)) goto grad_done;
+                    // (the softmax has seen the step's copies land before it wrote P^T)
                     if (!wait(&p_full[sb], (g >> 1) & 1, ab)) goto grad_done;
                     tc_fence_after();
 #pragma unroll
@@ -651,7 +648,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 const bool full =
                     (tok >= j_last) & ((tok + kp.TQ - 1 - j_first < p.window) | (j_last < p.sinks));
                 const float* stats = reinterpret_cast<const float*>(smem + SM::kStats + st * 8 * kStatRows);
-                bool ok = wait(&q_full[st], (g >> 2) & 1, ab);
+                bool ok = wait(&x_full[st], (g >> 2) & 1, ab);
                 ok = ok && wait(&s_full[wg], ph, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto ds_done;
                 tc_fence_after();
@@ -723,8 +720,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     }
     if (abort_flag) {
         if (threadIdx.x == 0) {
-            drain_ring(q_full, 4, issued[0]);
-            drain_ring(g_full, 4, issued[1]);
+            drain_ring(x_full, 4, issued[0]);
             if (issued_a) drain_wait(&a_full, (issued_a - 1) & 1);
             drain_ring(s_full, 2, issued[2]);
             drain_ring(dp_full, 2, issued[3]);
@@ -756,16 +752,16 @@ int launch(Call& c) {
     static std::atomic<uint64_t> prepared[2];
     if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem, prepared[0]))) return rc;
     if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem, prepared[1]))) return rc;
-    const int grid = imin(sm_count(), kPlanCtas);
+    const int grid = imin(sm_count(), TcPlan::kCtas);
     Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + tq2 - 1) / tq2, c.scale, c.scale * kLog2e, c.cuts, c.slots};
     const KProb kp{1, p.rep, p.G, tq2, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
-    Plan plan;
-    if ((rc = query_plan(c, grid, &plan))) return rc;
+    TcPlan plan;
+    if ((rc = query_plan(c, grid, &plan.tab, plan.s))) return rc;
     if ((rc = launch_tile_stats(c))) return rc;
     dq_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     if ((rc = launch_join(c, kTcRows, grid, true))) return rc;
-    if ((rc = key_plan(c, kp, grid, &plan))) return rc;
+    if ((rc = key_plan(c, kp, grid, &plan.tab, plan.s))) return rc;
     dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq2, mk, mv, mg2, a, kp, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
     return launch_join_kv(c, kp, kTcRows, grid);

@@ -219,11 +219,14 @@ struct CtaStart {
 // A dense launch's split, which the host knows: one start per CTA, handed over
 // as a kernel parameter (finding them in the kernel took a call of one tile
 // 4.6 of its 12 us).
-constexpr int kPlanCtas = 320;
+template <int N>
 struct Plan {
+    static constexpr int kCtas = N;  // the most CTAs of a launch
     Table tab;
-    CtaStart s[kPlanCtas];
+    CtaStart s[N];
 };
+using TcPlan = Plan<160>;    // one CTA per SM
+using SimtPlan = Plan<320>;  // two
 
 // A tile that begins in CTA c and goes on in later ones: `pieces` of it (0:
 // none), the first in slot 2 c + 1, the others in slots 2 (c + 1), 2 (c + 2) ...

@@ -62,8 +62,8 @@ int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& 
 // CTAs.  BSP_ERR_OOM when the host has no memory for it.
 Plans* plans_create();
 void plans_destroy(Plans* p);
-int query_plan(const Call& c, int ctas, Plan* out);
-int key_plan(const Call& c, const KProb& k, int ctas, Plan* out);
+int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts);
+int key_plan(const Call& c, const KProb& k, int ctas, Table* tab, CtaStart* starts);
 
 // stats = rowsum(dO .* O) per row; the same and the rows' -lse log2(e), per tile
 int launch_delta(const Call& c);

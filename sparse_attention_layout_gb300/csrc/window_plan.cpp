@@ -28,29 +28,29 @@ struct Key {
 
 // Boundaries lie at equal steps, but never inside a tile of at most 4 steps or
 // a 32nd of a share: cutting one saves less than its join costs.
-void split(const std::vector<int>& steps, int rep, int ctas, Plan* out) {
+void split(const std::vector<int>& steps, int rep, int ctas, Table* tab, CtaStart* out) {
     const int ntiles = (int)steps.size(), items = ntiles * rep;
     int64_t one = 0;
     for (int s : steps) one += s;
     const int tot = (int)(one * rep);
     const Shares sh(tot, imax(1, imin(ctas, imax(items, tot / kMinShare))));
-    out->tab = Table(items, ctas);
+    *tab = Table(items, ctas);
     std::vector<int> at(ctas + 1, tot);
     int c = 0, pos = 0;
     for (int col = 0; col < ctas && c < sh.n; ++col)
-        for (int row = 0; row < out->tab.height(col) && c < sh.n; ++row) {
-            const int v = steps[out->tab.number(col, row) % ntiles];
+        for (int row = 0; row < tab->height(col) && c < sh.n; ++row) {
+            const int v = steps[tab->number(col, row) % ntiles];
             const bool keep_whole = v <= 4 || v <= sh.base / 32;
             while (c < sh.n && sh.at(c) < pos + v) {
                 const int off = keep_whole ? 0 : sh.at(c) - pos;
-                out->s[c] = CtaStart{col, row, off, 0};
+                out[c] = CtaStart{col, row, off, 0};
                 at[c++] = pos + off;
             }
             pos += v;
         }
     for (int i = 0; i < ctas; ++i) {
-        if (i >= c) out->s[i] = CtaStart{0, 0, 0, 0};
-        out->s[i].count = at[i + 1] - at[i];
+        if (i >= c) out[i] = CtaStart{0, 0, 0, 0};
+        out[i].count = at[i + 1] - at[i];
     }
 }
 
@@ -72,21 +72,21 @@ void plans_destroy(Plans* p) { delete p; }
 namespace {
 
 template <typename F>
-int find(const Call& c, const Key& key, int ntiles, F steps_of, Plan* out) {
+int find(const Call& c, const Key& key, int ntiles, F steps_of, Table* tab, CtaStart* out) {
     try {
         Plans& P = *c.w->plans;
         std::lock_guard<std::mutex> lock(P.mu);
         for (const auto& e : P.kept)
             if (e.key == key) {
-                out->tab = e.tab;
-                for (int i = 0; i < key.ctas; ++i) out->s[i] = e.s[i];
+                *tab = e.tab;
+                for (int i = 0; i < key.ctas; ++i) out[i] = e.s[i];
                 return BSP_OK;
             }
         std::vector<int> steps(ntiles);
         for (int t = 0; t < ntiles; ++t) steps[t] = steps_of(t);
-        split(steps, key.rep, key.ctas, out);
+        split(steps, key.rep, key.ctas, tab, out);
         if (P.kept.size() >= kKeep) P.kept.pop_front();
-        P.kept.push_back({key, out->tab, std::vector<CtaStart>(out->s, out->s + key.ctas)});
+        P.kept.push_back({key, *tab, std::vector<CtaStart>(out, out + key.ctas)});
         return BSP_OK;
     } catch (...) {
         return BSP_ERR_OOM;
@@ -95,16 +95,17 @@ int find(const Call& c, const Key& key, int ntiles, F steps_of, Plan* out) {
 
 }  // namespace
 
-int query_plan(const Call& c, int ctas, Plan* out) {
+int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts) {
     const Prob& p = c.p;
     const Seg g{0, p.Sq, p.Sk, (p.Sq + p.TQ - 1) / p.TQ};
-    return find(c, Key{0, p.rep, p.TQ, p.kshift, p.Sq, p.Sk, ctas}, g.ntiles, [&](int t) { return p.steps(g, t); }, out);
+    return find(c, Key{0, p.rep, p.TQ, p.kshift, p.Sq, p.Sk, ctas}, g.ntiles, [&](int t) { return p.steps(g, t); }, tab,
+                starts);
 }
 
-int key_plan(const Call& c, const KProb& k, int ctas, Plan* out) {
+int key_plan(const Call& c, const KProb& k, int ctas, Table* tab, CtaStart* starts) {
     const int ntiles = (int)(((int64_t)k.Sk + (1 << k.kshift) - 1) >> k.kshift);
     return find(c, Key{1, k.rep, k.TQ, k.kshift, k.Sq, k.Sk, ctas}, ntiles,
-                [&](int t) { return k.steps(Seg{}, t); }, out);
+                [&](int t) { return k.steps(Seg{}, t); }, tab, starts);
 }
 
 }  // namespace win

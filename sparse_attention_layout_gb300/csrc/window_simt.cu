@@ -159,7 +159,7 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
 
 template <typename T, int DP, bool PAGED>
 __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __grid_constant__ Args A,
-                                                     const __grid_constant__ Plan plan) {
+                                                     const __grid_constant__ SimtPlan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Ks = Qs + R * PITCH, *Vs = Ks + R * PITCH, *Ps = Vs + R * PITCH;
@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
 
 // dQ = scale dS K with dS = P (dO V^T - delta), P = exp(scale Q K^T - lse)
 template <typename T, int DP>
-__global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_constant__ Args A, const __grid_constant__ Plan plan) {
+__global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_constant__ Args A, const __grid_constant__ SimtPlan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Gs = Qs + R * PITCH, *Ks = Gs + R * PITCH, *Vs = Ks + R * PITCH, *Ps = Vs + R * PITCH;
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_c
 // it and the heads that share it
 template <typename T, int DP>
 __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_constant__ Args A, const __grid_constant__ KProb kp,
-                                                 const __grid_constant__ Plan plan) {
+                                                 const __grid_constant__ SimtPlan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Gs = Qs + R * PITCH, *Ks = Gs + R * PITCH, *Vs = Ks + R * PITCH;
@@ -511,8 +511,8 @@ int forward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
     size_t smem = tiles_bytes<DP>(3, 1);
     if (smem < (size_t)c.p.nseg * sizeof(int)) smem = (size_t)c.p.nseg * sizeof(int);
-    Plan plan{};
-    int rc = c.p.paged ? BSP_OK : query_plan(c, grid, &plan);
+    SimtPlan plan{};
+    int rc = c.p.paged ? BSP_OK : query_plan(c, grid, &plan.tab, plan.s);
     if (rc) return rc;
     rc = c.p.paged ? launch(forward_kernel<T, DP, true>, grid, smem, c.stream, a, plan)
                    : launch(forward_kernel<T, DP, false>, grid, smem, c.stream, a, plan);
@@ -523,9 +523,9 @@ template <typename T, int DP>
 int backward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
     const KProb kp{1, c.p.rep, c.p.G, a.p.TQ, kShift, c.p.Hq, c.p.Hkv, c.p.Sq, c.p.Sk, c.p.window, c.p.sinks};
-    Plan plan, kplan;
-    int rc = query_plan(c, grid, &plan);
-    if (!rc) rc = key_plan(c, kp, grid, &kplan);
+    SimtPlan plan, kplan;
+    int rc = query_plan(c, grid, &plan.tab, plan.s);
+    if (!rc) rc = key_plan(c, kp, grid, &kplan.tab, kplan.s);
     if (!rc) rc = launch_delta(c);
     if (!rc) rc = launch(dq_kernel<T, DP>, grid, tiles_bytes<DP>(4, 1), c.stream, a, plan);
     if (!rc) rc = launch_join(c, R, grid, true);
@@ -537,7 +537,7 @@ int backward_t(Call& c, const Args& a, int grid) {
 
 #define BSP_WIN_DISPATCH(fn)                                                                    \
     const Args a = make_args(c);                                                                \
-    const int grid = imin(kSimtPerSm * sm_count(), kPlanCtas);                                                   \
+    const int grid = imin(kSimtPerSm * sm_count(), SimtPlan::kCtas);                                                   \
     switch (c.dtype) {                                                                          \
         case BSP_F32: return c.D <= 64 ? fn<float, 64>(c, a, grid) : fn<float, 128>(c, a, grid); \
         case BSP_BF16: return c.D <= 64 ? fn<__nv_bfloat16, 64>(c, a, grid) : fn<__nv_bfloat16, 128>(c, a, grid); \
