@@ -140,11 +140,14 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
     tc_fence_before();
     if constexpr (PAGED) {
-        locate<kThreads>(p, kMinShare, reinterpret_cast<int*>(smem), red, &start);
+        // (a tile of one token per sequence: launch_forward_tc)
+        if (p.TQ == 1 && p.nseg <= kThreads) locate_plain<kThreads>(p, kMinShare, red, &start);
+        else locate<kThreads>(p, kMinShare, reinterpret_cast<int*>(smem), red, &start);
         fence_proxy_async_smem();  // locate's scratch is where the copies land next
     } else if (threadIdx.x == 0) {
         start.tab = plan.tab;
         start.cta = plan.s[blockIdx.x];
+        start.plain = false;
     }
     __syncthreads();
     tc_fence_after();
@@ -167,7 +170,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int pages = PAGED ? 128 >> p.page_shift : 1;  // copies per 64 columns
         const int my_page = lane % pages, my_panel = lane / pages;
         const uint32_t page_bytes = PAGED ? 128u << p.page_shift : 128u * 128u;
-        Walk<Prob, PAGED> walk(p, start.tab, start.cta);
+        Walk<Prob, PAGED> walk(p, start);
         Work w;
         // one step is loaded while the next one's place, and its page number,
         // are on their way

@@ -237,11 +237,15 @@ struct Cut {
 
 #if defined(__CUDACC__)
 
-// A ragged launch's split, found on the device.
+// A ragged launch's split, found on the device.  A batch of single tokens, whose
+// tiles share no keys, takes the tiles as they are numbered (`plain`): finding
+// the shares then is one scan, and the walk a count.
 struct Start {
     Table tab;
     Shares shares;
     CtaStart cta;
+    bool plain;
+    int seg, rep, tile;  // plain: the first tile
 };
 
 // exclusive prefix over the block's threads; *total = the block's sum
@@ -266,6 +270,41 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t* red, uint32
     *total = __shfl_sync(0xffffffffu, w, NT / 32 - 1);
     const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
     return (warp ? before : 0) + x - v;
+}
+
+// as many CTAs as there are tiles, or more if each still gets min_share steps
+__device__ __forceinline__ Shares shares_of(int tot, int items, int min_share) {
+    return Shares(tot, imax(1, imin(gridDim.x, imax(items, tot / min_share))));
+}
+
+// The plain split of at most NT segments; called by every thread of the block.
+template <int NT>
+__device__ __forceinline__ void locate_plain(const Prob& p, int min_share, uint32_t* red, Start* out) {
+    const int s = threadIdx.x;
+    const Seg g = s < p.nseg ? p.seg(s) : Seg{0, 0, 0, 0};
+    int w = 0;
+#pragma unroll 1
+    for (int t = 0; t < g.ntiles; ++t) w += p.steps(g, t);
+    uint32_t tot;
+    const int ex = (int)block_scan<NT>(w * p.rep, red, &tot);
+    // (items counted as if every segment had one tile: close enough)
+    const Shares sh = shares_of(tot, p.nseg * p.rep, min_share);
+    const int at = sh.at(blockIdx.x), count = sh.of(blockIdx.x);
+    if (threadIdx.x == 0) {
+        out->shares = sh;
+        out->cta.count = count;
+        out->plain = true;
+    }
+    if (count > 0 && at >= ex && at < ex + w * p.rep) {
+        out->seg = s;
+        out->rep = (uint32_t)(at - ex) / (uint32_t)w;
+        int off = (uint32_t)(at - ex) % (uint32_t)w, t = 0;
+#pragma unroll 1
+        for (int v; off >= (v = p.steps(g, t)); ++t) off -= v;
+        out->tile = t;
+        out->cta.off = off;
+    }
+    __syncthreads();
 }
 
 // Finds this CTA's share of a ragged launch; called by every thread of the
@@ -337,11 +376,11 @@ __device__ __noinline__ void locate(const Prob& p, int min_share, int* seg_end, 
         if (pass == 0) {
             uint32_t tot;
             const uint32_t ex = block_scan<NT>(sum, red, &tot);
-            // as many CTAs as there are tiles, or more if each still gets min_share steps
-            const Shares sh(tot, imax(1, imin(gridDim.x, imax(items, (int)tot / min_share))));
+            const Shares sh = shares_of(tot, items, min_share);
             const int count = sh.of(blockIdx.x);
             if (tid == 0) {
                 out->tab = tab;
+                out->plain = false;
                 out->shares = sh;
                 out->cta.count = count;
             }
@@ -376,6 +415,16 @@ struct Walk {
     int off;
     int seg, seg0;  // a segment and the number of its first tile
     Seg g;
+    // a plain walk: the tile that comes next
+    bool plain = false;
+    int rep = 0, tile = 0;
+    __device__ __forceinline__ Walk(const P& prob, const Start& st) : Walk(prob, st.tab, st.cta) {
+        plain = st.plain;
+        if (plain) {
+            seg = st.seg, rep = st.rep, tile = st.tile;
+            if (left > 0) g = p.seg(seg);
+        }
+    }
     __device__ __forceinline__ Walk(const P& prob, const Table& t, const CtaStart& st)
         : p(prob), tab(t), left(st.count), col(st.col), row(st.row), height(t.height(st.col)), tail(t.longer(st.col)), off(st.off),
           seg(0), seg0(0) {
@@ -383,6 +432,19 @@ struct Walk {
     }
     __device__ __forceinline__ bool next(Item& it) {
         if (left <= 0) return false;
+        if (MANY && plain) {
+            it.seg = seg, it.rep = rep, it.tile = tile, it.g = g;
+            take(it);
+            if (left > 0 && ++tile >= g.ntiles) {
+                tile = 0;
+                if (++rep >= p.rep) {
+                    rep = 0;
+                    do g = p.seg(++seg);  // steps are left, so a segment with tiles follows
+                    while (g.ntiles == 0);
+                }
+            }
+            return true;
+        }
         while (row >= height) {  // a column may be empty
             ++col;
             row = 0;
@@ -426,13 +488,16 @@ struct Walk {
         it.rep = (uint32_t)(a - seg0) / (uint32_t)g.ntiles;
         it.tile = (uint32_t)(a - seg0) % (uint32_t)g.ntiles;
         it.g = g;
-        it.n = p.describe(g, it.tile, it.q, it.sp);
+        take(it);
+        return true;
+    }
+    // the steps of the tile that fall into the share
+    __device__ __forceinline__ void take(Item& it) {
+        it.n = p.describe(it.g, it.tile, it.q, it.sp);
         it.s0 = off;
-        it.ns = it.n - off;
-        if (it.ns > left) it.ns = left;
+        it.ns = imin(it.n - off, left);
         left -= it.ns;
         off = 0;
-        return true;
     }
 };
 
