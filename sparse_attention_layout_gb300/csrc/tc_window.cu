@@ -615,11 +615,12 @@ int launch(Call& c) {
     const int grid = imin(sm_count(), TcPlan::kCtas);
     Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, c.cuts, c.slots};
     Split<PAGED> plan;
+    bool cut = true;
     if constexpr (!PAGED)
-        if ((rc = query_plan(c, grid, &plan.tab, plan.s))) return rc;
+        if ((rc = query_plan(c, grid, &plan.tab, plan.s, &cut))) return rc;
     kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
-    return launch_join(c, kTcRows, grid, false);
+    return cut ? launch_join(c, kTcRows, grid, false) : BSP_OK;
 }
 
 template <typename T>

@@ -756,15 +756,16 @@ int launch(Call& c) {
     Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + tq2 - 1) / tq2, c.scale, c.scale * kLog2e, c.cuts, c.slots};
     const KProb kp{1, p.rep, p.G, tq2, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
     TcPlan plan;
-    if ((rc = query_plan(c, grid, &plan.tab, plan.s))) return rc;
+    bool cut;
+    if ((rc = query_plan(c, grid, &plan.tab, plan.s, &cut))) return rc;
     if ((rc = launch_tile_stats(c))) return rc;
     dq_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
-    if ((rc = launch_join(c, kTcRows, grid, true))) return rc;
-    if ((rc = key_plan(c, kp, grid, &plan.tab, plan.s))) return rc;
+    if (cut && (rc = launch_join(c, kTcRows, grid, true))) return rc;
+    if ((rc = key_plan(c, kp, grid, &plan.tab, plan.s, &cut))) return rc;
     dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq2, mk, mv, mg2, a, kp, plan);
     if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
-    return launch_join_kv(c, kp, kTcRows, grid);
+    return cut ? launch_join_kv(c, kp, kTcRows, grid) : BSP_OK;
 }
 
 }  // namespace

@@ -59,11 +59,12 @@ int launch_backward_tc(Call& c);
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
                   const Prob& p, int D, cudaStream_t s);
 // The split of a dense launch's query tiles (p) or key tiles (k) over `ctas`
-// CTAs.  BSP_ERR_OOM when the host has no memory for it.
+// CTAs; *cut: some tile is shared between CTAs, so that a join has to follow.
+// BSP_ERR_OOM when the host has no memory for it.
 Plans* plans_create();
 void plans_destroy(Plans* p);
-int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts);
-int key_plan(const Call& c, const KProb& k, int ctas, Table* tab, CtaStart* starts);
+int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts, bool* cut);
+int key_plan(const Call& c, const KProb& k, int ctas, Table* tab, CtaStart* starts, bool* cut);
 
 // stats = rowsum(dO .* O) per row; the same and the rows' -lse log2(e), per tile
 int launch_delta(const Call& c);

@@ -61,6 +61,7 @@ struct Plans {
     struct Entry {
         Key key;
         Table tab;
+        bool cut;
         std::vector<CtaStart> s;
     };
     std::list<Entry> kept;
@@ -72,21 +73,25 @@ void plans_destroy(Plans* p) { delete p; }
 namespace {
 
 template <typename F>
-int find(const Call& c, const Key& key, int ntiles, F steps_of, Table* tab, CtaStart* out) {
+int find(const Call& c, const Key& key, int ntiles, F steps_of, Table* tab, CtaStart* out,
+         bool* cut) {
     try {
         Plans& P = *c.w->plans;
         std::lock_guard<std::mutex> lock(P.mu);
         for (const auto& e : P.kept)
             if (e.key == key) {
                 *tab = e.tab;
+                *cut = e.cut;
                 for (int i = 0; i < key.ctas; ++i) out[i] = e.s[i];
                 return BSP_OK;
             }
         std::vector<int> steps(ntiles);
         for (int t = 0; t < ntiles; ++t) steps[t] = steps_of(t);
         split(steps, key.rep, key.ctas, tab, out);
+        *cut = false;
+        for (int i = 0; i < key.ctas; ++i) *cut |= out[i].off > 0;
         if (P.kept.size() >= kKeep) P.kept.pop_front();
-        P.kept.push_back({key, *tab, std::vector<CtaStart>(out, out + key.ctas)});
+        P.kept.push_back({key, *tab, *cut, std::vector<CtaStart>(out, out + key.ctas)});
         return BSP_OK;
     } catch (...) {
         return BSP_ERR_OOM;
@@ -95,17 +100,17 @@ int find(const Call& c, const Key& key, int ntiles, F steps_of, Table* tab, CtaS
 
 }  // namespace
 
-int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts) {
+int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts, bool* cut) {
     const Prob& p = c.p;
     const Seg g{0, p.Sq, p.Sk, (p.Sq + p.TQ - 1) / p.TQ};
     return find(c, Key{0, p.rep, p.TQ, p.kshift, p.Sq, p.Sk, ctas}, g.ntiles, [&](int t) { return p.steps(g, t); }, tab,
-                starts);
+                starts, cut);
 }
 
-int key_plan(const Call& c, const KProb& k, int ctas, Table* tab, CtaStart* starts) {
+int key_plan(const Call& c, const KProb& k, int ctas, Table* tab, CtaStart* starts, bool* cut) {
     const int ntiles = (int)(((int64_t)k.Sk + (1 << k.kshift) - 1) >> k.kshift);
     return find(c, Key{1, k.rep, k.TQ, k.kshift, k.Sq, k.Sk, ctas}, ntiles,
-                [&](int t) { return k.steps(Seg{}, t); }, tab, starts);
+                [&](int t) { return k.steps(Seg{}, t); }, tab, starts, cut);
 }
 
 }  // namespace win

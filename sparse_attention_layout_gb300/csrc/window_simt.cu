@@ -512,11 +512,12 @@ int forward_t(Call& c, const Args& a, int grid) {
     size_t smem = tiles_bytes<DP>(3, 1);
     if (smem < (size_t)c.p.nseg * sizeof(int)) smem = (size_t)c.p.nseg * sizeof(int);
     SimtPlan plan{};
-    int rc = c.p.paged ? BSP_OK : query_plan(c, grid, &plan.tab, plan.s);
+    bool cut = true;
+    int rc = c.p.paged ? BSP_OK : query_plan(c, grid, &plan.tab, plan.s, &cut);
     if (rc) return rc;
     rc = c.p.paged ? launch(forward_kernel<T, DP, true>, grid, smem, c.stream, a, plan)
                    : launch(forward_kernel<T, DP, false>, grid, smem, c.stream, a, plan);
-    return rc ? rc : launch_join(c, R, grid, false);
+    return rc || !cut ? rc : launch_join(c, R, grid, false);
 }
 
 template <typename T, int DP>
@@ -524,13 +525,14 @@ int backward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
     const KProb kp{1, c.p.rep, c.p.G, a.p.TQ, kShift, c.p.Hq, c.p.Hkv, c.p.Sq, c.p.Sk, c.p.window, c.p.sinks};
     SimtPlan plan, kplan;
-    int rc = query_plan(c, grid, &plan.tab, plan.s);
-    if (!rc) rc = key_plan(c, kp, grid, &kplan.tab, kplan.s);
+    bool cut = false, kcut = false;
+    int rc = query_plan(c, grid, &plan.tab, plan.s, &cut);
+    if (!rc) rc = key_plan(c, kp, grid, &kplan.tab, kplan.s, &kcut);
     if (!rc) rc = launch_delta(c);
     if (!rc) rc = launch(dq_kernel<T, DP>, grid, tiles_bytes<DP>(4, 1), c.stream, a, plan);
-    if (!rc) rc = launch_join(c, R, grid, true);
+    if (!rc && cut) rc = launch_join(c, R, grid, true);
     if (!rc) rc = launch(dkv_kernel<T, DP>, grid, tiles_bytes<DP>(4, 2), c.stream, a, kp, kplan);
-    return rc ? rc : launch_join_kv(c, kp, R, grid);
+    return rc || !kcut ? rc : launch_join_kv(c, kp, R, grid);
 }
 
 }  // namespace
