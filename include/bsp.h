@@ -409,7 +409,8 @@ size_t bsp_attention_host_workspace(bsp_layout_t layout, int dtype, int D, int z
  * ptr + (i * stride[0] + j * stride[1] + k * stride[2] + d) elements; the
  * stride of an extent of 1 is ignored.  Pointers 16-byte aligned and strides
  * multiples of 16 bytes (else BSP_ERR_ALIGNMENT), strides positive, outputs
- * not overlapping themselves (else BSP_ERR_INVALID_ARG) nor any input.  So
+ * not overlapping themselves and not at an input's address (else
+ * BSP_ERR_INVALID_ARG) nor otherwise over any input.  So
  * [Z][H][S][D] and [Z][S][H][D] tensors, slices of a fused projection and
  * either order of a page are all taken as they are.
  *

@@ -672,13 +672,32 @@ def _dense_sizes(Q, K, V):
     return Z, Hq, Hkv, Sq, Sk, D
 
 
+def _forward(W, dt, Q, K, V, O, lse, Z, Hq, Hkv, Sq, Sk, D, scale, stream):
+    n = _window_workspace(W.device, Z, Hq, Hkv, Sq, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
+    rc = lib().bsp_window_attention(W.handle, dt, _heads(Q), _heads(K), _heads(V), _heads(O), lse.data_ptr(), Z, Hq,
+                                    Hkv, Sq, Sk, D, scale, ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_window_attention")
+
+
+def _backward(W, dt, Q, K, V, O, dO, lse, dQ, dK, dV, Z, Hq, Hkv, Sq, Sk, D, scale, stream):
+    n = _window_workspace(W.device, Z, Hq, Hkv, Sq, 1)
+    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
+    rc = lib().bsp_window_attention_backward(W.handle, dt, _heads(Q), _heads(K), _heads(V), _heads(O), _heads(dO),
+                                             lse.data_ptr(), _heads(dQ), _heads(dK), _heads(dV), Z, Hq, Hkv, Sq, Sk, D,
+                                             scale, ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_window_attention_backward")
+
+
 @_entry
 def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.0, stream=None):
     """Causal attention with the handle's window and sinks: (O, lse fp32
     [Z, Hq, Sq]).  Q [Z, Hq, Sq, D], K and V [Z, Hkv, Sk, D] of any strides
     that are multiples of 16 bytes with a contiguous last dimension; the
     queries are the last Sq of the Sk positions."""
-    Z, Hq, Hkv, Sq, Sk, D = _dense_sizes(Q, K, V)
+    Z, Hq, Hkv, Sq, Sk, D = sizes = _dense_sizes(Q, K, V)
     if O is None:
         O = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
     else:
@@ -687,13 +706,7 @@ def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.
         lse = torch.empty((Z, Hq, Sq), dtype=torch.float32, device=Q.device)
     else:
         _lse_ok(W, lse, (Z, Hq, Sq))
-    dt = _same(W, Q, K, V, O)
-    n = _window_workspace(W.device, Z, Hq, Hkv, Sq, 0)
-    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
-    rc = lib().bsp_window_attention(W.handle, dt, _heads(Q), _heads(K), _heads(V), _heads(O), lse.data_ptr(), Z, Hq,
-                                    Hkv, Sq, Sk, D, scale, ws.data_ptr(), n, stream)
-    if rc:
-        raise BspError(rc, "bsp_window_attention")
+    _forward(W, _same(W, Q, K, V, O), Q, K, V, O, lse, *sizes, scale, stream)
     return O, lse
 
 
@@ -702,21 +715,14 @@ def bsp_window_attention_backward(W: Window, Q, K, V, O, dO, lse, dQ=None, dK=No
                                   stream=None):
     """(dQ, dK, dV) of bsp_window_attention for the output gradient dO, given
     its O and lse."""
-    Z, Hq, Hkv, Sq, Sk, D = _dense_sizes(Q, K, V)
+    Z, Hq, Hkv, Sq, Sk, D = sizes = _dense_sizes(Q, K, V)
     dQ = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) if dQ is None else dQ
     dK = torch.empty(K.shape, dtype=K.dtype, device=K.device) if dK is None else dK
     dV = torch.empty(V.shape, dtype=V.dtype, device=V.device) if dV is None else dV
-    dt = _same(W, Q, K, V, O, dO, dQ, dK, dV)
     for t, like, what in ((O, Q, "O"), (dO, Q, "dO"), (dQ, Q, "dQ"), (dK, K, "dK"), (dV, V, "dV")):
         _shape(t, like.shape, what)
     _lse_ok(W, lse, (Z, Hq, Sq))
-    n = _window_workspace(W.device, Z, Hq, Hkv, Sq, 1)
-    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
-    rc = lib().bsp_window_attention_backward(W.handle, dt, _heads(Q), _heads(K), _heads(V), _heads(O), _heads(dO),
-                                             lse.data_ptr(), _heads(dQ), _heads(dK), _heads(dV), Z, Hq, Hkv, Sq, Sk, D,
-                                             scale, ws.data_ptr(), n, stream)
-    if rc:
-        raise BspError(rc, "bsp_window_attention_backward")
+    _backward(W, _same(W, Q, K, V, O, dO, dQ, dK, dV), Q, K, V, O, dO, lse, dQ, dK, dV, *sizes, scale, stream)
     return dQ, dK, dV
 
 
@@ -726,6 +732,16 @@ def _taken(t):
     ok = t.data_ptr() % 16 == 0 and (t.shape[-1] <= 1 or t.stride(-1) == 1) and \
         all(n <= 1 or (s > 0 and s % e == 0) for n, s in zip(t.shape[:-1], t.stride()[:-1]))
     return t if ok else t.clone(memory_format=torch.contiguous_format)
+
+
+@_entry
+def _differentiated(W, Q, K, V, O, dO, lse, scale, stream=None):
+    """The gradient of saved tensors, which the forward has checked; autograd
+    gives dO in O's shape and type."""
+    dQ, dK, dV = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device), \
+        torch.empty(K.shape, dtype=K.dtype, device=K.device), torch.empty(V.shape, dtype=V.dtype, device=V.device)
+    _backward(W, _DTYPES[Q.dtype], Q, K, V, O, _taken(dO), lse, dQ, dK, dV, *_dense_sizes(Q, K, V), scale, stream)
+    return dQ, dK, dV, None, None
 
 
 class _WindowAttention(torch.autograd.Function):
@@ -741,8 +757,7 @@ class _WindowAttention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dO):
         Q, K, V, O, lse = ctx.saved_tensors
-        dQ, dK, dV = bsp_window_attention_backward(ctx.W, Q, K, V, O, _taken(dO), lse, scale=ctx.scale)
-        return dQ, dK, dV, None, None
+        return _differentiated(ctx.W, Q, K, V, O, dO, lse, ctx.scale)
 
 
 def window_attention(W: Window, Q, K, V, scale: float):

@@ -3,6 +3,7 @@
 // kernels.
 #include <cstdint>
 #include <cstdlib>
+#include <initializer_list>
 #include <new>
 
 #include "window.h"
@@ -65,6 +66,19 @@ int make_view(const bsp_tensor_t* t, int64_t n0, int64_t n1, int64_t n2, int D, 
         }
     }
     return BSP_OK;
+}
+
+// An output in an input's place (or another output's) would be overwritten
+// while other blocks still read it.
+bool clash(std::initializer_list<const bsp_tensor_t*> out, std::initializer_list<const bsp_tensor_t*> in) {
+    for (auto o = out.begin(); o != out.end(); ++o) {
+        if (!(*o)->ptr) continue;
+        for (const bsp_tensor_t* i : in)
+            if (i->ptr == (*o)->ptr) return true;
+        for (auto q = out.begin(); q != o; ++q)
+            if ((*q)->ptr == (*o)->ptr) return true;
+    }
+    return false;
 }
 
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
@@ -207,6 +221,7 @@ extern "C" int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_
         if ((rc = make_view(V, Z, Hkv, Sk, D, elt, false, &c.V))) return rc;
     }
     if ((rc = make_view(O, Z, Hq, Sq, D, elt, true, &c.O))) return rc;
+    if (Sk > 0 ? clash({O}, {Q, K, V}) : clash({O}, {Q})) return BSP_ERR_INVALID_ARG;
     if ((uintptr_t)lse & 15u) return BSP_ERR_ALIGNMENT;
     if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 0)))) return rc;
     if (Sk == 0) {  // no key at all: zeros and -inf, by the kernels' hidden step over Q's own rows
@@ -252,6 +267,7 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
         if (!lse) return BSP_ERR_INVALID_ARG;
         if ((uintptr_t)lse & 15u) return BSP_ERR_ALIGNMENT;
     }
+    if (Sq > 0 && Sk > 0 && clash({dQ, dK, dV}, {Q, K, V, O, dO})) return BSP_ERR_INVALID_ARG;
     // no pair at all: every gradient is 0
     if (Sq == 0) {
         if (Sk > 0 && !(rc = zero_view(c.dK, Z, Hkv, Sk, (size_t)D * elt, elt, s)))
@@ -320,6 +336,7 @@ extern "C" int bsp_paged_append(bsp_window_t w, int dtype, const bsp_tensor_t* K
     if ((rc = make_view(V, 1, Hkv, T, D, elt, false, &vn))) return rc;
     if ((rc = make_view(K_cache, n_pages, Hkv, page, D, elt, true, &kc))) return rc;
     if ((rc = make_view(V_cache, n_pages, Hkv, page, D, elt, true, &vc))) return rc;
+    if (clash({K_cache, V_cache}, {K, V})) return BSP_ERR_INVALID_ARG;
     return bsp::win::launch_append(w, dtype, kn, vn, kc, vc, p, D, (cudaStream_t)stream);
 }
 
@@ -339,6 +356,7 @@ extern "C" int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t
     if ((rc = make_view(K_cache, n_pages, Hkv, page, D, elt, false, &c.K))) return rc;
     if ((rc = make_view(V_cache, n_pages, Hkv, page, D, elt, false, &c.V))) return rc;
     if ((rc = make_view(O, 1, Hq, T, D, elt, true, &c.O))) return rc;
+    if (clash({O}, {Q, K_cache, V_cache})) return BSP_ERR_INVALID_ARG;
     if ((uintptr_t)lse & 15u) return BSP_ERR_ALIGNMENT;
     if ((rc = check_workspace(workspace, workspace_bytes, bsp_paged_attention_workspace()))) return rc;
     c.w = w, c.dtype = dtype, c.D = D, c.scale = scale, c.Z = 1;

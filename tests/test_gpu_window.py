@@ -223,6 +223,57 @@ def test_paged(bsp, path, case, dtype):
     assert torch.equal(O2[:b.starts[-1]], O[:b.starts[-1]]) and torch.equal(lse2[:b.starts[-1]], lse[:b.starts[-1]])
 
 
+@pytest.mark.parametrize("new,kv", [
+    ([1] * 700, [1 + i % 97 for i in range(700)]),           # more sequences than threads of a block
+    ([2, 0, 0, 1, 3, 0, 0, 0], [300, 5, 0, 700, 3, 9, 9, 9]),  # as few tokens as sequences, but not one each
+    ([0, 0, 0], [10, 0, 5]),                                  # no new token at all, rows of nobody
+], ids=["700", "uneven", "none"])
+def test_batches_of_few_tokens(bsp, path, new, kv):
+    b = Paged(new, kv, 4, 2, 64, 16, torch.float16, 70 + len(new), extra_tokens=2)
+    W = bsp.bsp_window_create(250, 3)
+    O, lse = torch.full_like(b.Q, 7.0), torch.full(b.Q.shape[:2], 7.0, device="cuda")
+    b.attend(bsp, W, O=O, lse=lse, scale=0.125)
+    assert bsp.bsp_window_status(W) == 0
+    b.check(O, lse, 0.125, 250, 3)
+    assert bool((O[b.starts[-1]:] == 7.0).all()) and bool((lse[b.starts[-1]:] == 7.0).all())
+
+
+def test_cache_beyond_32_bit_offsets(bsp, path):
+    """Pages whose elements lie past 2^31 of the cache."""
+    n_pages, Hkv, page, D = 2 ** 31 // (2 * 16 * 128) + 40, 2, 16, 128
+    W = bsp.bsp_window_create()
+    Kc, Vc = (torch.empty(n_pages, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.tensor([[n_pages - 1, 3, n_pages - 30, n_pages - 2]], dtype=torch.int32, device="cuda")
+    S = 61
+    Q, K, V = (randn((1, H, S, D), torch.bfloat16, 90 + i) for i, H in enumerate((4, 2, 2)))
+    rows = [t[0].transpose(0, 1) for t in (Q, K, V)]
+    qs = torch.tensor([0, S], dtype=torch.int32, device="cuda")
+    kl = torch.tensor([S], dtype=torch.int32, device="cuda")
+    bsp.bsp_paged_append(W, rows[1], rows[2], Kc, Vc, qs, kl, table)
+    O, lse = bsp.bsp_paged_attention(W, rows[0], Kc, Vc, qs, kl, table, scale=0.09)
+    assert bsp.bsp_window_status(W) == 0
+    r = ref.dense(Q, K, V, 0.09, 0, 0)
+    check(O.transpose(0, 1)[None], r["O"], r["eO"], "O")
+    check(lse.T[None], r["lse"], r["else_"], "lse")
+
+
+def test_dense_beyond_32_bit_offsets(bsp):
+    """Batch entries and rows whose elements lie past 2^31 of their tensors."""
+    W = bsp.bsp_window_create(40, 1)
+    Z, H, S, D = 2, 2, 150, 64
+    wide = 2 ** 31 // (S * 2) // 8 * 8 + 64  # row stride: the second batch entry starts past 2^31
+    def far(seed):
+        t = torch.empty(Z * S * wide, dtype=torch.bfloat16, device="cuda").as_strided((Z, H, S, D), (S * wide, D, wide, 1))
+        return t.copy_(randn((Z, H, S, D), torch.bfloat16, seed))
+    Q, K, V, dO = (far(95 + i) for i in range(4))
+    O, dQ, dK, dV = (far(0) for _ in range(4))
+    _, lse = bsp.bsp_window_attention(W, Q, K, V, O=O, scale=0.125)
+    bsp.bsp_window_attention_backward(W, Q, K, V, O, dO, lse, dQ, dK, dV, scale=0.125)
+    r = ref.dense(Q.contiguous(), K.contiguous(), V.contiguous(), 0.125, 40, 1, dO.contiguous())
+    for name, got in (("O", O), ("dQ", dQ), ("dK", dK), ("dV", dV)):
+        check(got.contiguous(), r[name], r["e" + name[-1]], name)
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_freed_pages_before_the_window(bsp, path, dtype):
     """Pages wholly between the sinks and every row's window may be given away:
@@ -473,6 +524,15 @@ def test_refusals(bsp):
         bsp.bsp_window_attention(W, *ok, O=x(1, 1, 20, 64).as_strided((1, 2, 8, 64), (64, 64, 64, 1)))
     with pytest.raises(ValueError):
         bsp.bsp_window_attention(W, *ok, lse=x(1, 2, 8))
+    same = x(1, 2, 8, 64)
+    with pytest.raises(bsp.BspError):  # in place of an input
+        bsp.bsp_window_attention(W, same, ok[1], ok[2], O=same)
+    O, l = bsp.bsp_window_attention(W, *ok)
+    with pytest.raises(bsp.BspError):  # two gradients in one place
+        bsp.bsp_window_attention_backward(W, *ok, O, x(1, 2, 8, 64), l, dK=ok[1].clone(), dV=ok[1])
+    both = torch.empty_like(ok[1])
+    with pytest.raises(bsp.BspError):
+        bsp.bsp_window_attention_backward(W, *ok, O, x(1, 2, 8, 64), l, dK=both, dV=both)
     i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
     q, kc = x(2, 2, 64), x(3, 1, 16, 64)
     bsp.bsp_paged_attention(W, q, kc, kc, i(0, 2), i(5), i(0, 1)[None].contiguous())
