@@ -167,23 +167,39 @@ __global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const Vie
 }
 
 // K and V rows of new tokens to their pages' slots: token t of sequence s goes
-// to position kv_len[s] - (new tokens of s) + its index.  A warp per token
-// finds the sequence by a 32-way search of q_start, then copies 16 bytes per
-// lane: all heads of K, then of V.  Moves each byte once in and once out.
+// to position kv_len[s] - (new tokens of s) + its index.  A warp per token, 16
+// bytes per lane and copy.  Moves each byte once in and once out; the rows are
+// on their way into registers while the warp finds the sequence (by a 32-way
+// search of q_start), its length and its page, three dependent reads.
 struct AppendArgs {
     View Kn, Vn, Kc, Vc;
     Prob p;
     int row16;  // 16-byte pieces per head row
 };
 
-__global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
+constexpr int kAhead = 4;  // pieces of K and of V that a lane holds
+
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendArgs a) {
     const Prob& p = a.p;
     const int lane = threadIdx.x & 31;
-    const int per = gridDim.y;  // blocks that share a token's row
     if (blockIdx.x == 0 && blockIdx.y == 0)
         for (int s = threadIdx.x; s < p.nseg; s += blockDim.x)
             if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
+    const int n = p.Hkv * a.row16, stride = gridDim.y * 32;  // gridDim.y blocks share a token's row
     for (int64_t t = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); t < p.T; t += (int64_t)gridDim.x * 8) {
+        uint4 k[kAhead], v[kAhead];
+        auto fetch = [&](int first) {
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = first + j * stride, h = i / a.row16, c = i - h * a.row16;
+                if (i < n) {
+                    k[j] = static_cast<const uint4*>(a.Kn.ptr)[h * a.Kn.s[1] + t * a.Kn.s[2] + c];
+                    v[j] = static_cast<const uint4*>(a.Vn.ptr)[h * a.Vn.s[1] + t * a.Vn.s[2] + c];
+                }
+            }
+        };
+        const int i0 = blockIdx.y * 32 + lane;
+        fetch(i0);
         // last s in [0, nseg) with q_start[s] <= t: each round asks 32 places
         int lo = 0, hi = p.nseg;
         while (hi - lo > 1) {
@@ -207,14 +223,18 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
             continue;
         }
         const int slot = pos & ((1 << p.page_shift) - 1);
-        const int n = p.Hkv * a.row16;
-        for (int i = blockIdx.y * 32 + lane; i < n; i += per * 32) {
-            const int h = i / a.row16, c = i % a.row16;
-            auto src = [&](const View& v) { return static_cast<const uint4*>(v.ptr) + h * v.s[1] + t * v.s[2] + c; };
-            auto dst = [&](const View& v) { return static_cast<uint4*>(v.ptr) + pg * v.s[0] + h * v.s[1] + slot * v.s[2] + c; };
-            const uint4 k = *src(a.Kn), v = *src(a.Vn);
-            *dst(a.Kc) = k;
-            *dst(a.Vc) = v;
+        uint4* kd = static_cast<uint4*>(a.Kc.ptr) + pg * a.Kc.s[0] + slot * a.Kc.s[2];
+        uint4* vd = static_cast<uint4*>(a.Vc.ptr) + pg * a.Vc.s[0] + slot * a.Vc.s[2];
+        for (int first = i0; first < n; first += kAhead * stride) {
+            if (first != i0) fetch(first);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = first + j * stride, h = i / a.row16, c = i - h * a.row16;
+                if (i < n) {
+                    kd[h * a.Kc.s[1] + c] = k[j];
+                    vd[h * a.Vc.s[1] + c] = v[j];
+                }
+            }
         }
     }
 }
