@@ -131,13 +131,14 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         fence_barrier_init();
         cut.ns = 0;
     }
-    if (PAGED && blockIdx.x == 0)
-        for (int s = threadIdx.x; s < p.nseg; s += kThreads)
-            if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
     if (warp == 1) {
         tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
+    cudaGridDependencySynchronize();
+    if (PAGED && blockIdx.x == 0)
+        for (int s = threadIdx.x; s < p.nseg; s += kThreads)
+            if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
     tc_fence_before();
     if constexpr (PAGED) {
         // (a tile of one token per sequence: launch_forward_tc)
@@ -618,8 +619,7 @@ int launch(Call& c) {
     bool cut = true;
     if constexpr (!PAGED)
         if ((rc = query_plan(c, grid, &plan.tab, plan.s, &cut))) return rc;
-    kern<<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, a, plan);
-    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
+    if ((rc = launch_behind(kern, dim3(grid), kThreads, smem, c.stream, mq, mk, mv, a, plan))) return rc;
     return cut ? launch_join(c, kTcRows, grid, false) : BSP_OK;
 }
 

@@ -131,6 +131,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
+    cudaGridDependencySynchronize();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -445,6 +446,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         tmem_alloc(&tmem_base, 512);
         tmem_relinquish();
     }
+    cudaGridDependencySynchronize();
     tc_fence_before();
     // rows past TQ * G, which no copy writes, enter the products over the rows
     // with P = 0: they must not hold NaN
@@ -759,12 +761,12 @@ int launch(Call& c) {
     bool cut;
     if ((rc = query_plan(c, grid, &plan.tab, plan.s, &cut))) return rc;
     if ((rc = launch_tile_stats(c))) return rc;
-    dq_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq, mk, mv, mg, a, plan);
-    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
+    if ((rc = launch_behind(dq_tc_kernel<T, DP>, dim3(grid), kThreads, smem, c.stream, mq, mk, mv, mg, a, plan)))
+        return rc;
     if (cut && (rc = launch_join(c, kTcRows, grid, true))) return rc;
     if ((rc = key_plan(c, kp, grid, &plan.tab, plan.s, &cut))) return rc;
-    dkv_tc_kernel<T, DP><<<grid, kThreads, smem, c.stream>>>(mq2, mk, mv, mg2, a, kp, plan);
-    if (cudaGetLastError() != cudaSuccess) return BSP_ERR_CUDA;
+    if ((rc = launch_behind(dkv_tc_kernel<T, DP>, dim3(grid), kThreads, smem, c.stream, mq2, mk, mv, mg2, a, kp, plan)))
+        return rc;
     return cut ? launch_join_kv(c, kp, kTcRows, grid) : BSP_OK;
 }
 

@@ -22,6 +22,25 @@ struct bsp_window_s {
 namespace bsp {
 namespace win {
 
+// A launch that may be set up while the kernel before it in the stream still
+// runs; the kernel waits for that one's end (cudaGridDependencySynchronize)
+// before it touches memory, so the order of a stream holds and only the
+// launch's own latency is hidden.
+template <typename... P, typename... A>
+int launch_behind(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const A&... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+}
+
 // One call's tensors and sizes, checked.
 struct Call {
     const bsp_window_s* w;

@@ -32,7 +32,7 @@ struct JoinArgs {
 // The pieces are added in their order in fp32, whoever wrote them first.
 template <typename T, bool DQ>
 __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
-    cudaGridDependencySynchronize();  // launched while the kernel that writes the pieces still runs
+    cudaGridDependencySynchronize();
     const Cut cut = a.cuts[blockIdx.x];
     if (cut.pieces == 0) return;
     const Prob& p = a.p;
@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const Vie
                                                          int64_t rows, int ntiles, int G, int TQ, int Hkv, int S, int D) {
     constexpr int N = Vec16<T>::N;
     const int sub = threadIdx.x & 7;
+    cudaGridDependencySynchronize();
     for (int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); i < rows; i += (int64_t)gridDim.x * 32) {
         const int r = (int)(i % kStatRows);
         const int64_t tile = i / kStatRows, zh = tile / ntiles;
@@ -180,6 +181,7 @@ struct AppendArgs {
 constexpr int kAhead = 4;  // pieces of K and of V that a lane holds
 
 __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendArgs a) {
+    cudaGridDependencySynchronize();
     const Prob& p = a.p;
     const int lane = threadIdx.x & 31;
     if (blockIdx.x == 0 && blockIdx.y == 0)
@@ -239,26 +241,9 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     }
 }
 
-// Launch of a join behind the kernel whose pieces it joins: its blocks may
-// start as soon as that kernel's have, and wait inside for its end, so the
-// launch itself costs no time of its own.
-template <typename... P, typename... A>
-int launch_behind(void (*kern)(P...), int n_cta, cudaStream_t s, const A&... args) {
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(n_cta, kJoinParts);
-    cfg.blockDim = dim3(kJoinT);
-    cfg.stream = s;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
-}
-
 template <typename T>
 int join_t(const JoinArgs& a, int n_cta, bool is_dq, cudaStream_t s) {
-    return launch_behind(is_dq ? join_kernel<T, true> : join_kernel<T, false>, n_cta, s, a);
+    return launch_behind(is_dq ? join_kernel<T, true> : join_kernel<T, false>, dim3(n_cta, kJoinParts), kJoinT, 0, s, a);
 }
 
 template <typename T>
@@ -275,9 +260,8 @@ int tile_stats_t(const Call& c) {
     const int tq = kStatRows / c.p.G, ntiles = (c.p.Sq + tq - 1) / tq;
     const int64_t rows = (int64_t)c.Z * c.p.Hkv * ntiles * kStatRows;
     const int64_t blocks = (rows + 31) / 32, most = (int64_t)sm_count() * 16;
-    tile_stats_kernel<T><<<(int)(blocks < most ? blocks : most), 256, 0, c.stream>>>(
-        c.O, c.dO, c.lse, c.stats, rows, ntiles, c.p.G, tq, c.p.Hkv, c.p.Sq, c.D);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    return launch_behind(tile_stats_kernel<T>, dim3((int)(blocks < most ? blocks : most)), 256, 0, c.stream, c.O, c.dO,
+                         (const float*)c.lse, c.stats, rows, ntiles, c.p.G, tq, c.p.Hkv, c.p.Sq, c.D);
 }
 
 View in_16(const View& v, int elt) {
@@ -304,9 +288,9 @@ int launch_join(const Call& c, int rows, int n_cta, bool is_dq) {
 
 int launch_join_kv(const Call& c, const KProb& kp, int rows, int n_cta) {
     JoinArgs a{c.cuts, c.slots, c.p, c.dK, c.dV, nullptr, 0, 0, 0, c.D, rows, c.scale};
-    BSP_WIN_TYPES(launch_behind(join_kv_kernel<float>, n_cta, c.stream, a, kp),
-                  launch_behind(join_kv_kernel<__nv_bfloat16>, n_cta, c.stream, a, kp),
-                  launch_behind(join_kv_kernel<__half>, n_cta, c.stream, a, kp))
+    BSP_WIN_TYPES(launch_behind(join_kv_kernel<float>, dim3(n_cta, kJoinParts), kJoinT, 0, c.stream, a, kp),
+                  launch_behind(join_kv_kernel<__nv_bfloat16>, dim3(n_cta, kJoinParts), kJoinT, 0, c.stream, a, kp),
+                  launch_behind(join_kv_kernel<__half>, dim3(n_cta, kJoinParts), kJoinT, 0, c.stream, a, kp))
 }
 
 int launch_delta(const Call& c) { BSP_WIN_TYPES(delta_t<float>(c), delta_t<__nv_bfloat16>(c), delta_t<__half>(c)) }
@@ -324,8 +308,7 @@ int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& 
     const int64_t blocks = ((int64_t)p.T + 7) / 8, most = (int64_t)sm_count() * 8;
     const int pieces = (p.Hkv * a.row16 + 31) / 32;
     const int share = imax(1, imin(pieces, (int)(sm_count() / blocks)));
-    append_kernel<<<dim3((int)(blocks < most ? blocks : most), share), 256, 0, s>>>(a);
-    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
+    return launch_behind(append_kernel, dim3((int)(blocks < most ? blocks : most), share), 256, 0, s, a);
 }
 
 }  // namespace win
