@@ -238,6 +238,18 @@ def test_batches_of_few_tokens(bsp, path, new, kv):
     assert bool((O[b.starts[-1]:] == 7.0).all()) and bool((lse[b.starts[-1]:] == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_long_history_of_one_sequence(bsp, path, dtype):
+    """One token, and a short chunk, over a history cut into many pieces."""
+    for new, G in ((1, 4), (3, 5)):
+        b = Paged([new], [9000], 2 * G, 2, 128, 64, DT[dtype], 17 + G)
+        W = bsp.bsp_window_create()
+        O, lse = b.attend(bsp, W, scale=0.09)
+        assert bsp.bsp_window_status(W) == 0
+        b.check(O, lse, 0.09, 0, 0)
+        assert torch.equal(O, b.attend(bsp, W, scale=0.09)[0])
+
+
 def test_cache_beyond_32_bit_offsets(bsp, path):
     """Pages whose elements lie past 2^31 of the cache."""
     n_pages, Hkv, page, D = 2 ** 31 // (2 * 16 * 128) + 40, 2, 16, 128
