@@ -41,8 +41,8 @@ constexpr int kMinShare = 2;
 
 // A dense launch's split comes with it; a ragged one's is found in the kernel.
 struct None {};
-template <bool PAGED>
-using Split = std::conditional_t<PAGED, None, TcPlan>;
+template <int MODE>
+using Split = std::conditional_t<MODE == kDense, TcPlan, None>;
 
 template <int DP>
 struct Smem {
@@ -69,12 +69,13 @@ struct Args {
     float* slots;
 };
 
-template <typename T, int DP, bool PAGED>
+template <typename T, int DP, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args args,
-                 const __grid_constant__ Split<PAGED> plan) {
+                 const __grid_constant__ Split<MODE> plan) {
     using SM = Smem<DP>;
+    constexpr bool PAGED = MODE != kDense;
     constexpr int KP = SM::KP, QST = SM::QST, NST = SM::KVST;
     constexpr uint32_t kTileBytes = SM::kTile;
     constexpr uint32_t kIdescQK = idesc_f16(128, 128, std::is_same<T, __nv_bfloat16>::value, 0, 0);
@@ -140,15 +141,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         for (int s = threadIdx.x; s < p.nseg; s += kThreads)
             if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
     tc_fence_before();
-    if constexpr (PAGED) {
-        // (a tile of one token per sequence: launch_forward_tc)
-        if (p.TQ == 1 && p.nseg <= kThreads) locate_plain<kThreads>(p, kMinShare, red, &start);
-        else locate<kThreads>(p, kMinShare, reinterpret_cast<int*>(smem), red, &start);
+    if constexpr (MODE == kPlain) locate_plain<kThreads>(p, kMinShare, red, &start);
+    if constexpr (MODE == kRagged) {
+        locate<kThreads>(p, kMinShare, reinterpret_cast<int*>(smem), red, &start);
         fence_proxy_async_smem();  // locate's scratch is where the copies land next
-    } else if (threadIdx.x == 0) {
-        start.tab = plan.tab;
-        start.cta = plan.s[blockIdx.x];
-        start.plain = false;
     }
     __syncthreads();
     tc_fence_after();
@@ -171,7 +167,11 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int pages = PAGED ? 128 >> p.page_shift : 1;  // copies per 64 columns
         const int my_page = lane % pages, my_panel = lane / pages;
         const uint32_t page_bytes = PAGED ? 128u << p.page_shift : 128u * 128u;
-        Walk<Prob, PAGED> walk(p, start);
+        auto begin = [&] {
+            if constexpr (PAGED) return Walk<Prob, MODE>(p, start);
+            else return Walk<Prob, MODE>(p, plan.tab, plan.s[blockIdx.x]);
+        };
+        Walk<Prob, MODE> walk = begin();
         Work w;
         // one step is loaded while the next one's place, and its page number,
         // are on their way
@@ -599,8 +599,9 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
 }
 
-template <typename T, int DP, bool PAGED>
+template <typename T, int DP, int MODE>
 int launch(Call& c) {
+    constexpr bool PAGED = MODE != kDense;
     const int is_bf16 = std::is_same<T, __nv_bfloat16>::value;
     const Prob& p = c.p;
     CUtensorMap mq, mk, mv;
@@ -609,13 +610,13 @@ int launch(Call& c) {
     if (!rc) rc = key_map(&mk, c.K, c, is_bf16, rows);
     if (!rc) rc = key_map(&mv, c.V, c, is_bf16, rows);
     if (rc) return rc;
-    auto kern = window_tc_kernel<T, DP, PAGED>;
+    auto kern = window_tc_kernel<T, DP, MODE>;
     constexpr int smem = Smem<DP>::kAlloc;
     static std::atomic<uint64_t> prepared{0};
     if ((rc = prepare_kernel(kern, smem, prepared))) return rc;
     const int grid = imin(sm_count(), TcPlan::kCtas);
     Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, c.cuts, c.slots};
-    Split<PAGED> plan;
+    Split<MODE> plan;
     bool cut = true;
     if constexpr (!PAGED)
         if ((rc = query_plan(c, grid, &plan.tab, plan.s, &cut))) return rc;
@@ -623,10 +624,15 @@ int launch(Call& c) {
     return cut ? launch_join(c, kTcRows, grid, false) : BSP_OK;
 }
 
+template <typename T, int MODE>
+int by_width(Call& c) {
+    return c.D <= 64 ? launch<T, 64, MODE>(c) : launch<T, 128, MODE>(c);
+}
+
 template <typename T>
-int by_shape(Call& c) {
-    if (c.p.paged) return c.D <= 64 ? launch<T, 64, true>(c) : launch<T, 128, true>(c);
-    return c.D <= 64 ? launch<T, 64, false>(c) : launch<T, 128, false>(c);
+int by_mode(Call& c) {
+    if (!c.p.paged) return by_width<T, kDense>(c);
+    return c.p.TQ == 1 && c.p.nseg <= kThreads ? by_width<T, kPlain>(c) : by_width<T, kRagged>(c);
 }
 
 }  // namespace
@@ -637,7 +643,7 @@ int launch_forward_tc(Call& c) {
     // token's heads; else as many tokens as fill 128 rows
     c.p.kshift = 7;
     c.p.TQ = c.p.paged && c.p.T <= c.p.nseg ? 1 : kTcRows / c.p.G;
-    return c.dtype == BSP_BF16 ? by_shape<__nv_bfloat16>(c) : by_shape<__half>(c);
+    return c.dtype == BSP_BF16 ? by_mode<__nv_bfloat16>(c) : by_mode<__half>(c);
 }
 
 }  // namespace win

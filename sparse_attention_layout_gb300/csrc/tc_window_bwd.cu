@@ -150,7 +150,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             }
             const uint32_t a_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
-            Walk<Prob, false> walk(p, plan.tab, plan.s[blockIdx.x]);
+            Walk<Prob, kDense> walk(p, plan.tab, plan.s[blockIdx.x]);
             Item it;
             Work w;
             while (true) {
@@ -470,7 +470,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             }
             const uint32_t bytes = (uint32_t)(kp.TQ * p.G) * 128 * KP;
             uint32_t g = 0, tiles = 0;
-            Walk<KProb, false> walk(kp, plan.tab, plan.s[blockIdx.x]);
+            Walk<KProb, kDense> walk(kp, plan.tab, plan.s[blockIdx.x]);
             Item it;
             Work w;
             while (true) {

@@ -237,15 +237,18 @@ struct Cut {
 
 #if defined(__CUDACC__)
 
-// A ragged launch's split, found on the device.  A batch of single tokens, whose
-// tiles share no keys, takes the tiles as they are numbered (`plain`): finding
-// the shares then is one scan, and the walk a count.
+// How a launch is split: a dense batch, by the host; a ragged batch, on the
+// device; a ragged batch of single tokens, whose tiles share no keys, in the
+// order of their numbers: finding the shares then is one scan, and the walk a
+// count.
+enum Mode { kDense, kRagged, kPlain };
+
+// A ragged launch's split.
 struct Start {
     Table tab;
     Shares shares;
     CtaStart cta;
-    bool plain;
-    int seg, rep, tile;  // plain: the first tile
+    int seg, rep, tile;  // kPlain: the first tile
 };
 
 // exclusive prefix over the block's threads; *total = the block's sum
@@ -293,7 +296,6 @@ __device__ __forceinline__ void locate_plain(const Prob& p, int min_share, uint3
     if (threadIdx.x == 0) {
         out->shares = sh;
         out->cta.count = count;
-        out->plain = true;
     }
     if (count > 0 && at >= ex && at < ex + w * p.rep) {
         out->seg = s;
@@ -380,7 +382,6 @@ __device__ __noinline__ void locate(const Prob& p, int min_share, int* seg_end, 
             const int count = sh.of(blockIdx.x);
             if (tid == 0) {
                 out->tab = tab;
-                out->plain = false;
                 out->shares = sh;
                 out->cta.count = count;
             }
@@ -404,9 +405,9 @@ struct Item {
     __device__ __forceinline__ int slot() const { return 2 * blockIdx.x + (s0 == 0); }
 };
 
-// Walks the tiles of a CTA's share.  MANY: the problem may have several
-// segments, and all lanes of a warp walk together.
-template <typename P, bool MANY>
+// Walks the tiles of a CTA's share; of a ragged batch, all lanes of a warp
+// together.
+template <typename P, int MODE>
 struct Walk {
     const P& p;
     Table tab;
@@ -415,24 +416,31 @@ struct Walk {
     int off;
     int seg, seg0;  // a segment and the number of its first tile
     Seg g;
-    // a plain walk: the tile that comes next
-    bool plain = false;
-    int rep = 0, tile = 0;
-    __device__ __forceinline__ Walk(const P& prob, const Start& st) : Walk(prob, st.tab, st.cta) {
-        plain = st.plain;
-        if (plain) {
+    int rep = 0, tile = 0;  // kPlain: the tile that comes next
+    __device__ __forceinline__ Walk(const P& prob, const Start& st)
+        : p(prob), tab(st.tab), left(st.cta.count), off(st.cta.off), seg(0), seg0(0) {
+        if (left <= 0) return;
+        if (MODE == kPlain) {
             seg = st.seg, rep = st.rep, tile = st.tile;
-            if (left > 0) g = p.seg(seg);
+            g = p.seg(seg);
+        } else {
+            enter(st.cta.col, st.cta.row);
         }
     }
     __device__ __forceinline__ Walk(const P& prob, const Table& t, const CtaStart& st)
-        : p(prob), tab(t), left(st.count), col(st.col), row(st.row), height(t.height(st.col)), tail(t.longer(st.col)), off(st.off),
-          seg(0), seg0(0) {
-        if (!MANY) g = p.seg(0);
+        : p(prob), tab(t), left(st.count), off(st.off), seg(0), seg0(0) {
+        enter(st.col, st.row);
+        g = p.seg(0);
+    }
+    __device__ __forceinline__ void enter(int c, int r) {
+        col = c;
+        row = r;
+        height = tab.height(c);
+        tail = tab.longer(c);
     }
     __device__ __forceinline__ bool next(Item& it) {
         if (left <= 0) return false;
-        if (MANY && plain) {
+        if constexpr (MODE == kPlain) {
             it.seg = seg, it.rep = rep, it.tile = tile, it.g = g;
             take(it);
             if (left > 0 && ++tile >= g.ntiles) {
@@ -444,18 +452,19 @@ struct Walk {
                 }
             }
             return true;
+        } else {
+            return next_in_table(it);
         }
+    }
+    __device__ __forceinline__ bool next_in_table(Item& it) {
         while (row >= height) {  // a column may be empty
-            ++col;
-            row = 0;
-            height = tab.height(col);
-            tail = tab.longer(col);
+            enter(col + 1, 0);
             seg = 0;
             seg0 = 0;
         }
         const int a = row * tab.cols + (row < tab.q ? col : tail);
         ++row;
-        if constexpr (MANY) {
+        if constexpr (MODE == kRagged) {
             // 32 segments at a time: the one that holds tile number a
             const int lane = threadIdx.x & 31;
 #pragma unroll 1

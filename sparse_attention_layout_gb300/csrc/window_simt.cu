@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<Prob, PAGED> walk(p, PAGED ? start.tab : plan.tab, PAGED ? start.cta : plan.s[blockIdx.x]);
+    Walk<Prob, PAGED ? kRagged : kDense> walk(p, PAGED ? start.tab : plan.tab, PAGED ? start.cta : plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_c
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<Prob, false> walk(p, plan.tab, plan.s[blockIdx.x]);
+    Walk<Prob, kDense> walk(p, plan.tab, plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<KProb, false> walk(kp, plan.tab, plan.s[blockIdx.x]);
+    Walk<KProb, kDense> walk(kp, plan.tab, plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
