@@ -581,7 +581,9 @@ class _OnStream:
 
 
 def _entry(f):
-    """A call of the handle W on `stream`: with none given, on W's device's
+    """A call of the handle W on `stream`, which what the call returns then
+    belongs to (a tensor of another stream has to be made ready for it by the
+    caller, as for any torch operation): with none given, on W's device's
     current stream, and without the cost of a context when W's device is the
     current one (the wrappers are a large part of a small call's time)."""
 
@@ -692,7 +694,7 @@ def _backward(W, dt, Q, K, V, O, dO, lse, dQ, dK, dV, Z, Hq, Hkv, Sq, Sk, D, sca
 
 
 @_entry
-def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.0, stream=None):
+def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.0, *, stream=None):
     """Causal attention with the handle's window and sinks: (O, lse fp32
     [Z, Hq, Sq]).  Q [Z, Hq, Sq, D], K and V [Z, Hkv, Sk, D] of any strides
     that are multiples of 16 bytes with a contiguous last dimension; the
@@ -711,7 +713,7 @@ def bsp_window_attention(W: Window, Q, K, V, O=None, lse=None, scale: float = 1.
 
 
 @_entry
-def bsp_window_attention_backward(W: Window, Q, K, V, O, dO, lse, dQ=None, dK=None, dV=None, scale: float = 1.0,
+def bsp_window_attention_backward(W: Window, Q, K, V, O, dO, lse, dQ=None, dK=None, dV=None, scale: float = 1.0, *,
                                   stream=None):
     """(dQ, dK, dV) of bsp_window_attention for the output gradient dO, given
     its O and lse."""
@@ -786,7 +788,7 @@ def _paged_sizes(W, rows, K_cache, V_cache, q_start, kv_len, table):
 
 
 @_entry
-def bsp_paged_append(W: Window, K, V, K_cache, V_cache, q_start, kv_len, table, stream=None):
+def bsp_paged_append(W: Window, K, V, K_cache, V_cache, q_start, kv_len, table, *, stream=None):
     """Write the new tokens' K and V rows [T, Hkv, D] to their slots of the
     caches [n_pages, Hkv, page, D] (any strides; a permuted
     [n_pages, page, Hkv, D] tensor serves too).  q_start int32 [n_seq + 1],
@@ -804,7 +806,7 @@ def bsp_paged_append(W: Window, K, V, K_cache, V_cache, q_start, kv_len, table, 
 
 
 @_entry
-def bsp_paged_attention(W: Window, Q, K_cache, V_cache, q_start, kv_len, table, O=None, lse=None, scale: float = 1.0,
+def bsp_paged_attention(W: Window, Q, K_cache, V_cache, q_start, kv_len, table, O=None, lse=None, scale: float = 1.0, *,
                         stream=None):
     """Attention of a ragged batch of new tokens Q [T, Hq, D] over the caches,
     which hold their own keys already: (O, lse fp32 [T, Hq])."""

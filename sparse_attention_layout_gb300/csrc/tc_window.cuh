@@ -144,12 +144,6 @@ __device__ __forceinline__ Work make_work(const Prob& p, const Item& it) {
 // bits [0, c) of 64
 __device__ __forceinline__ unsigned long long below(int c) { return c >= 64 ? ~0ull : (1ull << c) - 1; }
 
-// the same for 32 columns
-__device__ __forceinline__ void hide32(float (&x)[32], uint32_t vis) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = (vis >> j) & 1 ? x[j] : -INFINITY;
-}
-
 // x[j] = -inf where bit j is clear
 __device__ __forceinline__ void hide(float (&x)[64], unsigned long long vis) {
     const uint32_t v0 = (uint32_t)vis, v1 = (uint32_t)(vis >> 32);

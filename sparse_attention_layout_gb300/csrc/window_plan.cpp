@@ -27,7 +27,9 @@ struct Key {
 };
 
 // Boundaries lie at equal steps, but never inside a tile of at most 4 steps or
-// a 32nd of a share: cutting one saves less than its join costs.
+// a 32nd of a share: cutting one saves less than its join costs (256 rows of 4
+// heads, window 64: 23.6 us cut, 11.5 whole; up to an eighth of a share instead,
+// full attention over 8192 keys took 244 us for 224).
 void split(const std::vector<int>& steps, int rep, int ctas, Table* tab, CtaStart* out) {
     const int ntiles = (int)steps.size(), items = ntiles * rep;
     int64_t one = 0;
