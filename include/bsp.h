@@ -424,7 +424,8 @@ size_t bsp_attention_host_workspace(bsp_layout_t layout, int dtype, int D, int z
  * length, before every window) never reach an output, whatever their slots
  * hold, and a hidden K row never reaches a query that does not see it.  A
  * non-finite V row (in the gradient also K, Q, dO) that some query of a tile
- * of 128 rows sees may reach the tile's other rows (0 * inf).
+ * of 128 rows sees may reach the tile's other rows (0 * inf).  A query with
+ * NaN or +inf among its own scores has NaN for its output and lse.
  *
  * Workspaces are the caller's (DEVICE, 256-byte aligned, else
  * BSP_ERR_ALIGNMENT; too small: BSP_ERR_INVALID_ARG); their contents need not
@@ -484,10 +485,10 @@ size_t bsp_window_attention_workspace(int Z, int Hq, int Hkv, int Sq, int backwa
  * contents.  n_seq <= 16384 (beyond: BSP_ERR_UNSUPPORTED).
  *
  * Checked on the device, reported as BSP_ERR_DEVICE_CHECK by
- * bsp_window_status: a sequence with q_start out of order or beyond T, or
- * kv_len negative or beyond max_pages * page, is left out; a page of a visible
- * position outside [0, n_pages) is never accessed (the output of the call is
- * then undefined).  Table entries of pages without a visible position are not
+ * bsp_window_status: a sequence that q_start places outside the T rows, or
+ * with kv_len negative or beyond max_pages * page, is left out; where q_start
+ * descends, no row is attended to; a page of a visible position outside
+ * [0, n_pages) is never accessed (the output of the call is then undefined).  Table entries of pages without a visible position are not
  * used and may hold anything. */
 
 /* Writes the new tokens' rows K, V (-, KV head, row) to their slots

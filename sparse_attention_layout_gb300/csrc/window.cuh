@@ -117,6 +117,9 @@ struct Prob {
         if (bad_seg(q0, q1, kv)) return Seg{0, 0, 0, 0};
         return Seg{q0, q1 - q0, kv, (q1 - q0 + TQ - 1) / TQ};
     }
+    // Offsets that descend let sequences overlap, and their steps then add up to
+    // more than the host has allowed for: such a call has no tiles at all.
+    __device__ __forceinline__ bool descends(int s) const { return q_start[s + 1] < q_start[s]; }
 #endif
     BSP_HD QTile qtile(const Seg& g, int t) const {
         QTile q;
@@ -288,6 +291,7 @@ __device__ __forceinline__ void locate_plain(const Prob& p, int min_share, uint3
     int w = 0;
 #pragma unroll 1
     for (int t = 0; t < g.ntiles; ++t) w += p.steps(g, t);
+    if (__syncthreads_or(s < p.nseg && p.descends(s))) w = 0;
     uint32_t tot;
     const int ex = (int)block_scan<NT>(w * p.rep, red, &tot);
     // (items counted as if every segment had one tile: close enough)
@@ -319,16 +323,18 @@ template <int NT>
 __device__ __noinline__ void locate(const Prob& p, int min_share, int* seg_end, uint32_t* red, Start* out) {
     const int tid = threadIdx.x;
     int tiles = 0;  // one repetition of every segment
+    bool bad = false;
 #pragma unroll 1
     for (int s0 = 0; s0 < p.nseg; s0 += NT) {
         const int s = s0 + tid;
         const uint32_t v = s < p.nseg ? p.seg(s).ntiles : 0;
+        bad |= s < p.nseg && p.descends(s);
         uint32_t total;
         const uint32_t ex = block_scan<NT>(v, red, &total);
         if (s < p.nseg) seg_end[s] = tiles + (int)(ex + v);
         tiles += (int)total;
     }
-    __syncthreads();
+    if (__syncthreads_or(bad)) tiles = 0;
     const int items = tiles * p.rep;
     const Table tab(items, gridDim.x);
     const int run = (items + NT - 1) / NT;
@@ -447,8 +453,13 @@ struct Walk {
                 tile = 0;
                 if (++rep >= p.rep) {
                     rep = 0;
-                    do g = p.seg(++seg);  // steps are left, so a segment with tiles follows
-                    while (g.ntiles == 0);
+                    do {
+                        if (++seg >= p.nseg) {  // only when q_start or kv_len changed under the call
+                            left = 0;
+                            break;
+                        }
+                        g = p.seg(seg);
+                    } while (g.ntiles == 0);
                 }
             }
             return true;
@@ -478,12 +489,16 @@ struct Walk {
                 }
                 end += seg0;
                 const unsigned m = __ballot_sync(0xffffffffu, end > a);
-                if (m == 0 && seg + 32 < p.nseg) {
+                if (m == 0) {
+                    if (seg + 32 >= p.nseg) {  // only when q_start or kv_len changed under the call
+                        left = 0;
+                        return false;
+                    }
                     seg += 32;
                     seg0 = __shfl_sync(0xffffffffu, end, 31);
                     continue;
                 }
-                const int src = m ? __ffs(m) - 1 : 31;  // m != 0: a lies below the last segment's end
+                const int src = __ffs(m) - 1;
                 seg += src;
                 seg0 = __shfl_sync(0xffffffffu, end - h.ntiles * p.rep, src);
                 g.t0 = __shfl_sync(0xffffffffu, h.t0, src);
@@ -516,7 +531,7 @@ template <typename F>
 __device__ __forceinline__ void write_cut(Cut* cuts, int seg, int rep, int tile, int left, F count) {
     int pieces = 1;
 #pragma unroll 1
-    for (int c = blockIdx.x + 1; left > 0; ++c, ++pieces) left -= count(c);
+    for (int c = blockIdx.x + 1; left > 0 && c < gridDim.x; ++c, ++pieces) left -= count(c);
     cuts[blockIdx.x] = Cut{pieces, seg, rep, tile};
 }
 

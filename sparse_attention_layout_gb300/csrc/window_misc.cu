@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
                 o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
             }
         }
-        const float f = DQ ? a.scale : (l > 0.f ? 1.0f / l : 0.f);
+        const float f = DQ ? a.scale : (l != 0.f ? 1.0f / l : 0.f);  // l may be no number
         const int64_t h = (int64_t)hk * p.G + r % p.G, t = (int64_t)g.t0 + q.tok0 + r / p.G;
         if (4 * lane < a.D) {
             T* dst = static_cast<T*>(a.out.ptr) + z * a.out.s[0] + h * a.out.s[1] + t * a.out.s[2] + 4 * lane;
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
             dst[2] = from_f32<T>(o.z * f), dst[3] = from_f32<T>(o.w * f);
         }
         if (!DQ && a.lse && lane == 0)
-            a.lse[z * a.lz + h * a.lh + t * a.lt] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            a.lse[z * a.lz + h * a.lh + t * a.lt] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
 }
 
@@ -337,7 +337,7 @@ int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& 
     const int elt = dtype == BSP_F32 ? 4 : 2;
     AppendArgs a{in_16(Kn, elt), in_16(Vn, elt), in_16(Kc, elt), in_16(Vc, elt), p, D * elt / 16};
     // few tokens: several blocks copy one token's heads, so that a batch of
-    // single tokens still spreads over the SMs
+    // single tokens still spreads over the SMs (64 tokens: 3.3 us, 3.7 without)
     const int64_t blocks = ((int64_t)p.T + 7) / 8, most = (int64_t)sm_count() * 8;
     const int pieces = (p.Hkv * a.row16 + 31) / 32;
     const int share = imax(1, imin(pieces, (int)(sm_count() / blocks)));

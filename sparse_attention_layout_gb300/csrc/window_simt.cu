@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
                 continue;
             }
             const int h = w.hk * p.G + r % p.G, t = it.g.t0 + q.tok0 + r / p.G;
-            const float inv = l[u] > 0.f ? 1.0f / l[u] : 0.f;
+            const float inv = l[u] != 0.f ? 1.0f / l[u] : 0.f;  // l may be no number
             T* dst = at<T>(A.O, w.z, h, t);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
@@ -286,9 +286,9 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
                     store4(dst + c, acc[u][g][0].x * inv, acc[u][g][0].y * inv, acc[u][g][1].x * inv, acc[u][g][1].y * inv);
             }
             if (A.lse && tx == 0)
-                A.lse[w.z * A.lz + h * A.lh + t * A.lt] = l[u] > 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
+                A.lse[w.z * A.lz + h * A.lh + t * A.lt] = l[u] != 0.f ? (m[u] + log2f(l[u])) * kLn2 : -INFINITY;
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) 
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole())
             write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns,
                       [&](int c) { return PAGED ? start.shares.of(c) : plan.s[c].count; });
     }
@@ -377,7 +377,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_c
                     store4(dst + c, a.x * A.scale, a.y * A.scale, b.x * A.scale, b.y * A.scale);
             }
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) 
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole())
             write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, [&](int c) { return plan.s[c].count; });
     }
 }
@@ -473,7 +473,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_
                 }
             }
         }
-        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole()) 
+        if (threadIdx.x == 0 && it.s0 == 0 && !it.whole())
             write_cut(A.cuts, it.seg, it.rep, it.tile, it.n - it.ns, [&](int c) { return plan.s[c].count; });
     }
 }

@@ -317,6 +317,37 @@ def test_hidden_keys_of_infinite_score(bsp, path):
     assert torch.equal(O[:, :, :150], O2[:, :, :150])
 
 
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("Sq,Sk", [(300, 300), (2, 9000)])  # whole tiles; pieces that are joined
+def test_rows_of_no_number_stay_so(bsp, path, Sq, Sk, value):
+    """A row that is no number, or that sees a key of infinite score, gets NaN,
+    not zeros as if it saw nothing; the other rows keep their values."""
+    Q, K, V = randn((1, 4, Sq, 64), torch.bfloat16, 70), *(randn((1, 2, Sk, 64), torch.bfloat16, 71 + i) for i in range(2))
+    W = bsp.bsp_window_create(0, 0)
+    O, lse = bsp.bsp_window_attention(W, Q, K, V, scale=0.125)
+    Q2 = Q.clone()
+    Q2[0, 1, 1] = math.nan
+    O2, lse2 = bsp.bsp_window_attention(W, Q2, K, V, scale=0.125)
+    assert bool(O2[0, 1, 1].isnan().all()) and bool(lse2[0, 1, 1].isnan())
+    O2[0, 1, 1], lse2[0, 1, 1] = O[0, 1, 1], lse[0, 1, 1]
+    assert torch.equal(O, O2) and torch.equal(lse, lse2)
+    # one element: the scores' signs are the queries', +inf in some rows and heads, -inf (no weight) in others
+    K2 = K.clone()
+    K2[0, 0, Sk - 1, 5] = value
+    O3, lse3 = bsp.bsp_window_attention(W, Q, K2, V, scale=0.125)
+    none = (Q[0, :2, Sq - 1, 5] * value > 0) | torch.tensor(math.isnan(value), device="cuda")
+    assert torch.equal(O3[0, :2, Sq - 1].isnan().all(-1), none) and torch.equal(lse3[0, :2, Sq - 1].isnan(), none)
+    assert torch.equal(O3[:, :, :Sq - 1], O[:, :, :Sq - 1]) and torch.equal(O3[:, 2:], O[:, 2:])
+    # one token over pages
+    b = Paged([1, 1], [40, 5000], 4, 2, 64, 16, torch.bfloat16, 5)
+    b.Q[1, 2] = math.nan
+    O, lse = b.attend(bsp, W, scale=0.125)
+    want = torch.zeros(2, 4, dtype=torch.bool, device="cuda")
+    want[1, 2] = True
+    assert torch.equal(O.isnan().all(-1), want) and torch.equal(O.isnan().any(-1), want)
+    assert torch.equal(lse.isnan(), want) and bsp.bsp_window_status(W) == 0
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("new,kv,page,D", [([1], [1], 16, 16), ([5, 0, 1, 130], [5, 40, 77, 600], 32, 80),
                                            ([3, 2], [1, 1], 16, 128), ([1] * 70, [1 + 9 * i for i in range(70)], 64, 64),
@@ -498,6 +529,24 @@ def test_bad_pages_and_lengths_are_reported(bsp, path):
             assert torch.equal(out[0], O[0]) and torch.equal(out[3], O[3]) and bool((out[1:3] == 7.0).all())
         t.copy_(keep)
     O2, _ = b.attend(bsp, W)
+    assert bsp.bsp_window_status(W) == 0
+
+
+@pytest.mark.parametrize("new", [[40, 0, 30, 25], [1] * 90, [1] * 700], ids=len)
+def test_descending_offsets_attend_to_nothing(bsp, path, new):
+    """Sequences that overlap could hold more tiles than the call's sizes allow
+    for: reported, and no row is written."""
+    b = Paged(new, [50] * len(new), 2, 1, 64, 16, torch.bfloat16, 6)
+    W = bsp.bsp_window_create()
+    t = b.q_start.clone()
+    b.q_start[2:] = (t[2:] - t[2]).clamp(min=0)  # the third sequence begins at row 0 again
+    O, lse = torch.full_like(b.Q, 7.0), torch.full(b.Q.shape[:2], 7.0, device="cuda")
+    b.attend(bsp, W, O=O, lse=lse)
+    assert bsp.bsp_window_status(W) == -7
+    assert bool((O == 7).all()) and bool((lse == 7).all())
+    b.q_start.copy_(t)
+    O, lse = b.attend(bsp, W, scale=0.1)
+    b.check(O, lse, 0.1, 0, 0)
     assert bsp.bsp_window_status(W) == 0
 
 
