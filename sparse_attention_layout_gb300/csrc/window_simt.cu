@@ -6,15 +6,27 @@
 // Tiles of 64 query rows x 64 keys, 256 threads; a thread holds a 4 x 4 patch
 // of scores (rows ty + 16 u, keys tx + 16 v) and 4 rows x D / 16 columns of the
 // output.  Shared-memory rows are padded by 4 floats, so the float4 reads of 16
-// neighbouring rows meet no bank twice.  Bound by the fp32 multiply-add rate:
-// per four steps of the contraction a thread reads 8 float4 for 64
-// multiply-adds.
+// neighbouring rows meet no bank twice.  fp32 tiles are copied asynchronously,
+// each as soon as the product that read its place is done, so that one product
+// or the softmax covers every copy (24 heads of 4096 tokens, D 64, window 512:
+// forward 494 -> 437 us, gradient 1585 -> 1425; pages of 32 sequences of 2000
+// keys, D 128: 443 -> 268).
+//
+// Bound by shared memory: per four steps of the contraction a thread reads 8
+// float4 for 64 multiply-adds, three wavefronts a read: the pipe is 73..78 %
+// busy, that of the multiply-adds 54 %.  4 x 8 patches read less (0.19 float4 a
+// pair of multiply-adds, not 0.25) but leave 8 warps an SM, and take as long
+// (435 and 1510 us; D 128: 997 and 3740 for 914 and 3039); 8 x 8 spill.
+#include <type_traits>
+
 #include "common.cuh"
 #include "window.h"
 
 namespace bsp {
 namespace win {
 namespace {
+
+__device__ float4 kNothing[1];  // where copies of no row point
 
 constexpr int kT = 256;
 constexpr int R = kSimtRows;      // query rows, and keys, per tile
@@ -47,24 +59,40 @@ __device__ __forceinline__ T* at(const View& v, int64_t i, int64_t j, int64_t k)
 }
 
 // 64 rows of `DP` columns into shared memory (pitch DP + 4); row r from
-// rowptr(r), or zeros where that is null
+// rowptr(r), or zeros where that is null.  fp32 rows are copied behind the
+// thread's back: landed() and a barrier make them visible.
 template <typename T, int DP, typename F>
 __device__ __forceinline__ void load_tile(float* dst, int D, F rowptr) {
     constexpr int N = Vec16<T>::N, C = DP / N;
+#pragma unroll 4
     for (int i = threadIdx.x; i < R * C; i += kT) {
         const int r = i / C, c = (i % C) * N;
-        float v[N];
         const T* src = rowptr(r);
-        if (src && c < D) {
-            Vec16<T>::load(src + c, v);
+        const bool live = src && c < D;
+        float* to = dst + r * (DP + 4) + c;
+        if constexpr (std::is_same<T, float>::value) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                         "l"(live ? src + c : reinterpret_cast<const T*>(kNothing)), "r"(live ? 16 : 0)
+                         : "memory");
         } else {
+            float v[N];
+            if (live) {
+                Vec16<T>::load(src + c, v);
+            } else {
 #pragma unroll
-            for (int k = 0; k < N; ++k) v[k] = 0.f;
+                for (int k = 0; k < N; ++k) v[k] = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < N; k += 4)
+                *reinterpret_cast<float4*>(to + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
         }
-#pragma unroll
-        for (int k = 0; k < N; k += 4)
-            *reinterpret_cast<float4*>(dst + r * (DP + 4) + c + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
     }
+}
+// ends a group of copies; waits until all but the last n groups have landed
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void landed() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // s[u][v] = sum_d A[ty + 16 u][d] B[tx + 16 v][d]
@@ -165,7 +193,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
     float *Qs = sm, *Ks = Qs + R * PITCH, *Vs = Ks + R * PITCH, *Ps = Vs + R * PITCH;
     __shared__ Start start;
     __shared__ uint32_t red[32];
-    __shared__ int pages[R];  // page of each key's slot in this step
+    __shared__ int pages[2][R];  // page of each key's slot, of this step and the next
     const Prob& p = A.p;
     report_bad_segs(p);
     if constexpr (PAGED) locate<kT>(p, 1, reinterpret_cast<int*>(sm), red, &start);
@@ -197,40 +225,50 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
 #pragma unroll
             for (int g = 0; g < NG; ++g) acc[u][g][0] = acc[u][g][1] = make_float2(0.f, 0.f);
         }
-        for (int n = 0; n < it.ns; ++n) {
-            const int kb = sp.tile(it.s0 + n) << kShift;
-            // keys that some row of the tile sees; the others (behind the
-            // sequence, before every row's window) are not read at all
-            auto wanted = [&](int j) { return j <= q.b && (j >= lo || j < p.sinks); };
-            if (PAGED) {
-                __syncthreads();
-                if (threadIdx.x < R) {
-                    const int j = kb + threadIdx.x;
-                    int pg = -1;
-                    if (wanted(j)) {
-                        pg = p.table[(int64_t)it.seg * p.max_pages + (j >> p.page_shift)];
-                        if ((unsigned)pg >= (unsigned)p.n_pages) {
-                            set_status(p.status, BSP_ERR_DEVICE_CHECK);
-                            pg = -1;
-                        }
-                    }
-                    pages[threadIdx.x] = pg;
+        // keys that some row of the tile sees; the others (behind the sequence,
+        // before every row's window) are not read at all
+        auto wanted = [&](int j) { return j <= q.b && (j >= lo || j < p.sinks); };
+        auto first_key = [&](int n) { return sp.tile(it.s0 + n) << kShift; };
+        auto find_pages = [&](int n) {  // by the barrier before the step's copies
+            if (!PAGED || threadIdx.x >= R || n >= it.ns) return;
+            const int j = first_key(n) + threadIdx.x;
+            int pg = -1;
+            if (wanted(j)) {
+                pg = p.table[(int64_t)it.seg * p.max_pages + (j >> p.page_shift)];
+                if ((unsigned)pg >= (unsigned)p.n_pages) {
+                    set_status(p.status, BSP_ERR_DEVICE_CHECK);
+                    pg = -1;
                 }
             }
-            __syncthreads();
-            auto keyrow = [&](const View& v, int r) -> const T* {
-                const int j = kb + r;
-                if (PAGED) {
-                    const int pg = pages[r];
-                    return pg < 0 ? nullptr : at<const T>(v, pg, w.hk, j & ((1 << p.page_shift) - 1));
-                }
-                return wanted(j) ? at<const T>(v, w.z, w.hk, j) : nullptr;
-            };
-            load_tile<T, DP>(Ks, A.D, [&](int r) { return keyrow(A.K, r); });
-            load_tile<T, DP>(Vs, A.D, [&](int r) { return keyrow(A.V, r); });
+            pages[n & 1][threadIdx.x] = pg;
+        };
+        auto copy = [&](float* dst, const View& v, int n) {
+            const int kb = first_key(n);
+            if (n < it.ns)
+                load_tile<T, DP>(dst, A.D, [&](int r) -> const T* {
+                    const int j = kb + r;
+                    if (PAGED) {
+                        const int pg = pages[n & 1][r];
+                        return pg < 0 ? nullptr : at<const T>(v, pg, w.hk, j & ((1 << p.page_shift) - 1));
+                    }
+                    return wanted(j) ? at<const T>(v, w.z, w.hk, j) : nullptr;
+                });
+            copies_end();
+        };
+        find_pages(0);
+        if (PAGED) __syncthreads();
+        copy(Ks, A.K, 0);
+        copy(Vs, A.V, 0);
+        // K's next tile is on its way from the scores on, V's from the product on
+        for (int n = 0; n < it.ns; ++n) {
+            const int kb = first_key(n);
+            find_pages(n + 1);
+            landed<1>();
             __syncthreads();
             float s[4][4];
             dots<DP>(Qs, Ks, ty, tx, s);
+            __syncthreads();
+            copy(Ks, A.K, n + 1);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 float cm = -INFINITY;
@@ -257,8 +295,11 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
 #pragma unroll
                     for (int c = 0; c < 2; ++c) acc[u][g][c] = __fmul2_rn(acc[u][g][c], make_float2(alpha, alpha));
             }
+            landed<1>();
             __syncthreads();
             accumulate<DP>(Ps, Vs, ty, tx, acc);
+            __syncthreads();
+            copy(Vs, A.V, n + 1);
         }
         float* slot = A.slots + (size_t)it.slot() * slot_floats(R);
 #pragma unroll
@@ -337,19 +378,29 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_c
 #pragma unroll
             for (int g = 0; g < NG; ++g) acc[u][g][0] = acc[u][g][1] = make_float2(0.f, 0.f);
         }
+        auto first_key = [&](int n) { return sp.tile(it.s0 + n) << kShift; };
+        auto copy = [&](float* dst, const View& v, int n) {
+            const int kb = first_key(n);
+            if (n < it.ns)
+                load_tile<T, DP>(dst, A.D, [&](int r) -> const T* {
+                    const int j = kb + r;
+                    return j <= q.b && (j >= lo || j < p.sinks) ? at<const T>(v, w.z, w.hk, j) : nullptr;
+                });
+            copies_end();
+        };
+        copy(Vs, A.V, 0);
+        copy(Ks, A.K, 0);
+        // V's next tile is on its way from dP on, K's from the product on
         for (int n = 0; n < it.ns; ++n) {
-            const int kb = sp.tile(it.s0 + n) << kShift;
-            __syncthreads();
-            auto keyrow = [&](const View& v, int r) -> const T* {
-                const int j = kb + r;
-                return j <= q.b && (j >= lo || j < p.sinks) ? at<const T>(v, w.z, w.hk, j) : nullptr;
-            };
-            load_tile<T, DP>(Ks, A.D, [&](int r) { return keyrow(A.K, r); });
-            load_tile<T, DP>(Vs, A.D, [&](int r) { return keyrow(A.V, r); });
-            __syncthreads();
+            const int kb = first_key(n);
             float s[4][4], d[4][4];
-            dots<DP>(Qs, Ks, ty, tx, s);
+            landed<1>();
+            __syncthreads();
             dots<DP>(Gs, Vs, ty, tx, d);
+            landed<0>();
+            __syncthreads();
+            copy(Vs, A.V, n + 1);
+            dots<DP>(Qs, Ks, ty, tx, s);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -358,8 +409,10 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_c
                     const float e = exp2f(s[u][v] * A.c2 - lse2[u]);
                     Ps[(ty + 16 * u) * PP + tx + 16 * v] = vis ? e * (d[u][v] - dl[u]) : 0.f;
                 }
-            __syncthreads();
+            __syncwarp();  // a warp's rows of dS are its own
             accumulate<DP>(Ps, Ks, ty, tx, acc);
+            __syncthreads();
+            copy(Ks, A.K, n + 1);
         }
         float* slot = A.slots + (size_t)it.slot() * slot_floats(R);
 #pragma unroll
@@ -415,15 +468,22 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_
 #pragma unroll
             for (int g = 0; g < NG; ++g)
                 ak[u][g][0] = ak[u][g][1] = av[u][g][0] = av[u][g][1] = make_float2(0.f, 0.f);
-        for (int n = 0; n < it.ns; ++n) {
-            const QTile q = p.qtile(Seg{0, p.Sq, p.Sk, 0}, first + it.s0 + n);
+        auto qtile = [&](int n) { return p.qtile(Seg{0, p.Sq, p.Sk, 0}, first + it.s0 + n); };
+        auto copy = [&](float* dst, const View& v, int n) {
+            const QTile q = qtile(n);
             const int rows = q.nt * p.G;
-            __syncthreads();
-            auto qrow = [&](const View& v, int r) -> const T* {
-                return r < rows ? at<const T>(v, w.z, (int64_t)w.hk * p.G + r % p.G, q.tok0 + r / p.G) : nullptr;
-            };
-            load_tile<T, DP>(Qs, A.D, [&](int r) { return qrow(A.Q, r); });
-            load_tile<T, DP>(Gs, A.D, [&](int r) { return qrow(A.dO, r); });
+            if (n < it.ns)
+                load_tile<T, DP>(dst, A.D, [&](int r) -> const T* {
+                    return r < rows ? at<const T>(v, w.z, (int64_t)w.hk * p.G + r % p.G, q.tok0 + r / p.G) : nullptr;
+                });
+            copies_end();
+        };
+        copy(Gs, A.dO, 0);
+        copy(Qs, A.Q, 0);
+        // dO's next tile is on its way from dV's product on, Q's from dK's on
+        for (int n = 0; n < it.ns; ++n) {
+            const QTile q = qtile(n);
+            const int rows = q.nt * p.G;
             if (threadIdx.x < R) {
                 const int r = threadIdx.x;
                 float x = INFINITY, dl = 0.f;
@@ -436,10 +496,13 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_
                 lse_s[r] = x;
                 del_s[r] = dl;
             }
-            __syncthreads();
             float s[4][4], d[4][4];
-            dots<DP>(Ks, Qs, ty, tx, s);  // keys ty + 16 u, rows tx + 16 v
+            landed<1>();
+            __syncthreads();
             dots<DP>(Vs, Gs, ty, tx, d);
+            landed<0>();
+            __syncthreads();
+            dots<DP>(Ks, Qs, ty, tx, s);  // keys ty + 16 u, rows tx + 16 v
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
                 const int r = tx + 16 * v;
@@ -451,9 +514,13 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_
                     Ds[(ty + 16 * u) * PP + r] = e == 0.f ? 0.f : e * (d[u][v] - del_s[r]);
                 }
             }
-            __syncthreads();
+            __syncwarp();
             accumulate<DP>(Ps, Gs, ty, tx, av);
+            __syncthreads();
+            copy(Gs, A.dO, n + 1);
             accumulate<DP>(Ds, Qs, ty, tx, ak);
+            __syncthreads();
+            copy(Qs, A.Q, n + 1);
         }
         float* slot = A.slots + (size_t)it.slot() * kv_slot_floats(R);
 #pragma unroll
