@@ -68,6 +68,7 @@ constexpr size_t kv_slot_floats(int rows) { return (size_t)rows * kSlotD * 2; }
 // CTAs per SM of the CUDA-core kernels (64-row tiles) and the tensor-core ones
 // (128-row tiles); both need the same workspace
 constexpr int kSimtPerSm = 2, kSimtRows = 64, kTcRows = 128;
+static_assert(kSimtPerSm * kSimtRows <= kTcRows, "the workspace holds two slots of kTcRows rows per SM");
 // query rows of a step of the tensor-core dK / dV kernel
 constexpr int kStatRows = 64;
 
