@@ -398,16 +398,17 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             if (!w.whole()) {
                 // a piece: raw O (relative to mf), mf and the sum, for the join
                 float* slot = args.slots + (size_t)w.slot() * slot_floats(kTcRows);
-                float* orow = slot + (size_t)row * kSlotD;
-#pragma unroll 1
+                // (unrolled by 1 or 4, the whole kernel was 1..4 % slower, cut tiles or not)
+                const SlotRows sr(rows);
+                float* at = slot + sr.at(row, 0);
+#pragma unroll 2
                 for (int c = 0; c < DP / 32; ++c) {
                     uint32_t r[32];
                     tmem_ld32_sync(tO + lane_base + c * 32, r);
                     if (row < rows) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            *reinterpret_cast<uint4*>(orow + c * 32 + 4 * k) =
-                                make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                        for (int k = 0; k < 8; ++k, at += sr.step)
+                            *reinterpret_cast<uint4*>(at) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
                     }
                 }
                 tc_fence_before();

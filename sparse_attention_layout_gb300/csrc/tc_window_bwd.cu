@@ -45,18 +45,19 @@ struct Smem {
 // (raw fp32) or, scaled and rounded, to memory; arrives on `empty` as soon as
 // the columns are in registers.
 template <typename T, int DP, typename F>
-__device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, int row, bool live, float* slot_rows,
+__device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, int row, int rows, float* slot,
                                       float scale, int D, uint8_t* stage, F dst) {
-    if (slot_rows) {
+    if (slot) {
+        const SlotRows sr(rows);
+        float* at = slot + sr.at(row, 0);
 #pragma unroll 1
         for (int c = 0; c < DP / 32; ++c) {
             uint32_t r[32];
             tmem_ld32_sync(tacc + c * 32, r);
-            if (live) {
+            if (row < rows) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    *reinterpret_cast<uint4*>(slot_rows + (size_t)row * kSlotD + c * 32 + 4 * k) =
-                        make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+                for (int k = 0; k < 8; ++k, at += sr.step)
+                    *reinterpret_cast<uint4*>(at) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
             }
         }
         tc_fence_before();
@@ -272,7 +273,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             ++tiles;
             float* slot = w.whole() ? nullptr : args.slots + (size_t)w.slot() * slot_floats(kTcRows);
             T* out = static_cast<T*>(args.dQ.ptr) + z * args.dQ.s[0] + hk * p.G * args.dQ.s[1] + w.row0 * args.dQ.s[2];
-            drain<T, DP>(tA + lane_base, &acc_empty, lane, row, row < rows, slot, args.scale, args.D,
+            drain<T, DP>(tA + lane_base, &acc_empty, lane, row, rows, slot, args.scale, args.D,
                          smem + SM::kEpi + quad * 4096, [&](int i) -> T* {
                              const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
                              return r < rows ? out + h * args.dQ.s[1] + t * args.dQ.s[2] : nullptr;
@@ -614,12 +615,12 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             bool ok = wait(&dv_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            drain<T, DP>(tV + lane_base, &dv_empty, lane, row, kb + row < p.Sk,
+            drain<T, DP>(tV + lane_base, &dv_empty, lane, row, kTcRows,
                          slot ? slot + (size_t)kTcRows * kSlotD : nullptr, 1.0f, args.D, stage, rows_of(args.dV));
             ok = wait(&dk_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            drain<T, DP>(tK + lane_base, &dk_empty, lane, row, kb + row < p.Sk, slot, args.scale, args.D, stage,
+            drain<T, DP>(tK + lane_base, &dk_empty, lane, row, kTcRows, slot, args.scale, args.D, stage,
                          rows_of(args.dK));
             ++tiles;
             if (threadIdx.x == 128 && w.s0 == 0 && !w.whole()) cut = w;

@@ -65,6 +65,18 @@ struct Call {
 constexpr int kSlotD = 128;
 constexpr size_t slot_floats(int rows) { return (size_t)rows * (kSlotD + 2); }
 constexpr size_t kv_slot_floats(int rows) { return (size_t)rows * kSlotD * 2; }
+// Place in a slot of column col (a multiple of 4) of one of the tile's `rows`
+// rows.  Many rows: four columns of all rows, then the next four, so that a warp
+// whose threads are rows writes and reads 512 contiguous bytes (row after row,
+// 16 bytes of 32 rows at a time: the gradient of 1037 tokens of 12 heads took 60
+// us, not 37).  Few rows (a new token's heads): row after row (31 such tokens'
+// join 5.1 us; by columns 7.1).
+constexpr int kManyRows = 32;
+struct SlotRows {
+    int row, step;  // floats from a row to the next, from four columns to the next
+    BSP_HD explicit SlotRows(int rows) : row(rows >= kManyRows ? 4 : kSlotD), step(rows >= kManyRows ? 4 * rows : 4) {}
+    BSP_HD int at(int r, int col) const { return r * row + (col >> 2) * step; }
+};
 // CTAs per SM of the CUDA-core kernels (64-row tiles) and the tensor-core ones
 // (128-row tiles); both need the same workspace
 constexpr int kSimtPerSm = 2, kSimtRows = 64, kTcRows = 128;

@@ -8,8 +8,9 @@ namespace bsp {
 namespace win {
 namespace {
 
-constexpr int kJoinParts = 8;  // blocks per cut tile, each an eighth of its rows
-constexpr int kJoinT = 128;    // a warp per row, four columns per lane
+constexpr int kJoinT = 128;
+constexpr int kJoinCols = 16;                    // columns of a block
+constexpr int kJoinParts = kSlotD / kJoinCols;  // blocks per cut tile
 
 // The slots of a cut tile's pieces, in order: every CTA among those that share
 // the steps has one of at least one step.
@@ -26,113 +27,176 @@ struct JoinArgs {
     float scale;
 };
 
+// 16 columns of a row of a piece (MANY: of a tile of many rows)
+template <bool MANY>
+__device__ __forceinline__ void load_piece(const float* slot, int rows, int row, int col, bool on, float (&v)[kJoinCols]) {
+    const float* at = slot + (MANY ? 4 * row + col * rows : kSlotD * row + col);
+    const int step = MANY ? 4 * rows : 4;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; k += 4) {
+        const float4 x = on ? *reinterpret_cast<const float4*>(at + k / 4 * step) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[k] = x.x, v[k + 1] = x.y, v[k + 2] = x.z, v[k + 3] = x.w;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_cols(T* dst, float (&v)[kJoinCols], float f) {
+    constexpr int N = Vec16<T>::N;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; k += N) {
+        float x[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = v[k + j] * f;
+        Vec16<T>::store(dst + k, x);
+    }
+}
+
+// The pieces of row r that a thread group adds up: group, group + np, ...
+template <bool DQ, bool MANY>
+__device__ __forceinline__ void add_pieces(const JoinArgs& a, int pieces, int group, int np, int r, int rows, int c0,
+                                           float& m, float& l, float (&o)[kJoinCols]) {
+    m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) o[k] = 0.f;
+#pragma unroll 1
+    for (int i0 = group; i0 < pieces; i0 += 4 * np) {
+        float mi[4], li[4], v[4][kJoinCols];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j * np;
+            const bool on = r < rows && i < pieces;
+            const float* slot = a.slots + piece_slot(on ? i : 0) * slot_floats(a.R);
+            if (!DQ) {
+                mi[j] = on ? slot[a.R * kSlotD + r] : -INFINITY;
+                li[j] = on ? slot[a.R * kSlotD + a.R + r] : 0.f;
+            }
+            load_piece<MANY>(slot, rows, r, c0, on, v[j]);
+        }
+        if (DQ) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int k = 0; k < kJoinCols; ++k) o[k] += v[j][k];
+            continue;
+        }
+        const float mn = fmaxf(fmaxf(fmaxf(mi[0], mi[1]), fmaxf(mi[2], mi[3])), m);
+        const float keep = m == -INFINITY ? 0.f : exp2f(m - mn);
+        l *= keep;
+#pragma unroll
+        for (int k = 0; k < kJoinCols; ++k) o[k] *= keep;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float w = mi[j] == -INFINITY ? 0.f : exp2f(mi[j] - mn);
+            l += w * li[j];
+#pragma unroll
+            for (int k = 0; k < kJoinCols; ++k)
+                if (w != 0.f) o[k] = fmaf(w, v[j][k], o[k]);  // a piece that saw nothing may hold anything
+        }
+        m = mn;
+    }
+}
+
 // Rows of cut query tiles.  Forward: the pieces' outputs are relative to each
 // piece's own maximum m_i (in log2 units): with m = max m_i,
 // o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i.  dQ: their sum, scaled.
 // The order of the sums is fixed, whoever wrote the pieces first.
 //
-// A tile of many rows has few pieces: a warp per row.  A tile of many pieces
-// (a long history under a small batch) has few rows: the block's warps share a
-// row, each every fourth piece, and add up in shared memory (16000 keys, one
-// token, 38 pieces: a warp alone spent 12 us of the call's 30 on its reads).
+// A thread holds 16 columns of a row and has four pieces on their way at once:
+// bound by the latency of one read (a warp per row, piece after piece, four
+// rows in turn took 11.4 us behind a launch with cut tiles of 128 rows; this 6.7).
+// A tile of few rows (a new token's heads over a long history) has many pieces: groups
+// of threads then take every np-th piece and add up in shared memory.
 template <typename T, bool DQ>
 __global__ void __launch_bounds__(kJoinT) join_kernel(const JoinArgs a) {
     cudaGridDependencySynchronize();
-    constexpr int NW = kJoinT / 32;
     const Cut cut = a.cuts[blockIdx.x];
-    if (cut.pieces == 0) return;
+    const int c0 = blockIdx.y * kJoinCols;
+    if (cut.pieces == 0 || c0 >= a.D) return;
     const Prob& p = a.p;
     const Seg g = p.seg(cut.seg);
     const QTile q = p.qtile(g, cut.tile);
     const int z = p.paged ? 0 : cut.rep / p.Hkv, hk = p.paged ? cut.rep : cut.rep % p.Hkv;
-    const int rows = q.nt * p.G, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool shared_row = cut.pieces > 4;
-    const int first = shared_row ? 0 : warp, per = shared_row ? 1 : NW;  // rows of a block at a time
-    __shared__ float part_m[NW], part_l[NW];
-    __shared__ float4 part_o[NW][32];
-    for (int r = blockIdx.y * per + first; r < rows; r += kJoinParts * per) {
-        const size_t row = (size_t)r * kSlotD + 4 * lane, ms = (size_t)a.R * kSlotD + r;
-        const int i0 = shared_row ? warp : 0, step = shared_row ? NW : 1;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float m = -INFINITY, l = 0.f;
-        if (!DQ) {
-            // maxima of this warp's pieces, a lane each
-            for (int i = i0 + lane * step; i < cut.pieces; i += 32 * step)
-                m = fmaxf(m, a.slots[piece_slot(i) * slot_floats(a.R) + ms]);
+    const int rows = imin(q.nt * p.G, kJoinT), tid = threadIdx.x;
+    // a thread group is 2^wide >= rows threads
+    const int wide = cut.pieces <= 4 ? 7 : rows <= 1 ? 0 : 32 - __clz(rows - 1);
+    const int np = kJoinT >> wide, parts = imin(np, cut.pieces);
+    const int r = tid & ((1 << wide) - 1), group = tid >> wide;
+    float m = -INFINITY, l = 0.f, o[kJoinCols];
+    // (with strides that are known only at run time, 31 tokens' join took 6.9 us, not 5)
+    if (rows >= kManyRows) add_pieces<DQ, true>(a, cut.pieces, group, np, r, rows, c0, m, l, o);
+    else add_pieces<DQ, false>(a, cut.pieces, group, np, r, rows, c0, m, l, o);
+    auto place = [&](int row, int64_t* h, int64_t* t) {
+        *h = (int64_t)hk * p.G + row % p.G;
+        *t = (int64_t)g.t0 + q.tok0 + row / p.G;
+    };
+    auto out = [&](int64_t h, int64_t t) { return static_cast<T*>(a.out.ptr) + z * a.out.s[0] + h * a.out.s[1] + t * a.out.s[2] + c0; };
+    auto put_lse = [&](int64_t h, int64_t t, float mx, float sum) {
+        if (!DQ && a.lse && c0 == 0)
+            a.lse[z * a.lz + h * a.lh + t * a.lt] = sum != 0.f ? (mx + log2f(sum)) * kLn2 : -INFINITY;
+    };
+    int64_t h, t;
+    if (np == 1) {
+        if (r >= rows) return;
+        place(r, &h, &t);
+        store_cols(out(h, t), o, DQ ? a.scale : (l != 0.f ? 1.0f / l : 0.f));  // l may be no number
+        put_lse(h, t, m, l);
+        return;
+    }
+    __shared__ float part_m[kJoinT], part_l[kJoinT], part_o[kJoinCols][kJoinT + 1];
+    part_m[tid] = m, part_l[tid] = l;
 #pragma unroll
-            for (int k = 16; k; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    for (int k = 0; k < kJoinCols; ++k) part_o[k][tid] = o[k];
+    __syncthreads();
+    for (int x = tid; x < rows * kJoinCols; x += kJoinT) {
+        const int row = x / kJoinCols, k = x % kJoinCols;
+        float mx = -INFINITY, sum = 0.f, y = 0.f;
+        if (!DQ)
+#pragma unroll 8
+            for (int i = 0; i < parts; ++i) mx = fmaxf(mx, part_m[(i << wide) + row]);
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) {
+            const int at = (i << wide) + row;
+            const float w = DQ ? 1.f : (part_m[at] == -INFINITY ? 0.f : exp2f(part_m[at] - mx));
+            sum += w * part_l[at];
+            y += w * part_o[k][at];
         }
-#pragma unroll 4
-        for (int i = i0; i < cut.pieces; i += step) {
-            const float* sl = a.slots + piece_slot(i) * slot_floats(a.R);
-            float w = 1.f;
-            if (!DQ) {
-                const float mi = sl[ms];
-                w = mi == -INFINITY ? 0.f : exp2f(mi - m);
-                l += w * sl[ms + a.R];
-            }
-            if (4 * lane < a.D && w != 0.f) {  // a piece that saw nothing may hold anything
-                const float4 v = *reinterpret_cast<const float4*>(sl + row);
-                o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
-            }
-        }
-        if (shared_row) {
-            __syncthreads();  // the last row's parts have been read
-            part_o[warp][lane] = o;
-            if (lane == 0) part_m[warp] = m, part_l[warp] = l;
-            __syncthreads();
-            if (warp) continue;
-            o = make_float4(0.f, 0.f, 0.f, 0.f);
-            l = 0.f;
-            m = -INFINITY;
-            if (!DQ)
-                for (int k = 0; k < NW; ++k) m = fmaxf(m, part_m[k]);
-#pragma unroll
-            for (int k = 0; k < NW; ++k) {
-                const float w = DQ ? 1.f : (part_m[k] == -INFINITY ? 0.f : exp2f(part_m[k] - m));
-                const float4 v = part_o[k][lane];
-                l += w * part_l[k];
-                o.x += w * v.x, o.y += w * v.y, o.z += w * v.z, o.w += w * v.w;
-            }
-        }
-        const float f = DQ ? a.scale : (l != 0.f ? 1.0f / l : 0.f);  // l may be no number
-        const int64_t h = (int64_t)hk * p.G + r % p.G, t = (int64_t)g.t0 + q.tok0 + r / p.G;
-        if (4 * lane < a.D) {
-            T* dst = static_cast<T*>(a.out.ptr) + z * a.out.s[0] + h * a.out.s[1] + t * a.out.s[2] + 4 * lane;
-            dst[0] = from_f32<T>(o.x * f), dst[1] = from_f32<T>(o.y * f);
-            dst[2] = from_f32<T>(o.z * f), dst[3] = from_f32<T>(o.w * f);
-        }
-        if (!DQ && a.lse && lane == 0)
-            a.lse[z * a.lz + h * a.lh + t * a.lt] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        place(row, &h, &t);
+        out(h, t)[k] = from_f32<T>(y * (DQ ? a.scale : (sum != 0.f ? 1.0f / sum : 0.f)));
+        if (k == 0) put_lse(h, t, mx, sum);
     }
 }
 
-// Keys of cut key tiles: dK (scaled) and dV as the sums of their pieces.
+// Keys of cut key tiles: dK (scaled) and dV as the sums of their pieces.  A
+// thread holds 16 columns of a key's dK or dV.
 template <typename T>
 __global__ void __launch_bounds__(kJoinT) join_kv_kernel(const JoinArgs a, const KProb kp) {
     cudaGridDependencySynchronize();
     const Cut cut = a.cuts[blockIdx.x];
-    if (cut.pieces == 0) return;
-    const int z = cut.rep / kp.Hkv, hk = cut.rep % kp.Hkv, lane = threadIdx.x & 31;
-    const int kb = cut.tile << kp.kshift, rows = imin(a.R, kp.Sk - kb);
-    if (4 * lane >= a.D) return;
-    for (int r = blockIdx.y * (kJoinT / 32) + (threadIdx.x >> 5); r < rows; r += kJoinParts * (kJoinT / 32)) {
-        float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-#pragma unroll 4
-        for (int i = 0; i < cut.pieces; ++i) {
-            const float* sl = a.slots + piece_slot(i) * kv_slot_floats(a.R) + 4 * lane;
-            const float4 x = *reinterpret_cast<const float4*>(sl + (size_t)r * kSlotD);
-            const float4 y = *reinterpret_cast<const float4*>(sl + (size_t)(a.R + r) * kSlotD);
-            k.x += x.x, k.y += x.y, k.z += x.z, k.w += x.w;
-            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+    const bool is_v = blockIdx.y >= kJoinParts;
+    const int c0 = (blockIdx.y % kJoinParts) * kJoinCols;
+    if (cut.pieces == 0 || c0 >= a.D) return;
+    const int z = cut.rep / kp.Hkv, hk = cut.rep % kp.Hkv, r = threadIdx.x;
+    const int kb = cut.tile << kp.kshift;
+    if (r >= imin(a.R, kp.Sk - kb)) return;
+    float o[kJoinCols];
+#pragma unroll
+    for (int k = 0; k < kJoinCols; ++k) o[k] = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < cut.pieces; i0 += 4) {
+        float v[4][kJoinCols];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const bool on = i0 + j < cut.pieces;
+            const float* slot = a.slots + piece_slot(on ? i0 + j : 0) * kv_slot_floats(a.R);
+            load_piece<true>(slot + (is_v ? a.R * kSlotD : 0), a.R, r, c0, on, v[j]);
         }
-        const int64_t j = kb + r;
-        T* dk = static_cast<T*>(a.out.ptr) + z * a.out.s[0] + hk * a.out.s[1] + j * a.out.s[2] + 4 * lane;
-        T* dv = static_cast<T*>(a.out2.ptr) + z * a.out2.s[0] + hk * a.out2.s[1] + j * a.out2.s[2] + 4 * lane;
-        dk[0] = from_f32<T>(k.x * a.scale), dk[1] = from_f32<T>(k.y * a.scale);
-        dk[2] = from_f32<T>(k.z * a.scale), dk[3] = from_f32<T>(k.w * a.scale);
-        dv[0] = from_f32<T>(v.x), dv[1] = from_f32<T>(v.y), dv[2] = from_f32<T>(v.z), dv[3] = from_f32<T>(v.w);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < kJoinCols; ++k) o[k] += v[j][k];
     }
+    const View& out = is_v ? a.out2 : a.out;
+    store_cols(static_cast<T*>(out.ptr) + z * out.s[0] + hk * out.s[1] + (int64_t)(kb + r) * out.s[2] + c0, o,
+               is_v ? 1.0f : a.scale);
 }
 
 // delta[z][h][t] = dO . O of the row, fp32: a group of 8 lanes per row, 16
@@ -321,9 +385,9 @@ int launch_join(const Call& c, int rows, int n_cta, bool is_dq) {
 
 int launch_join_kv(const Call& c, const KProb& kp, int rows, int n_cta) {
     JoinArgs a{c.cuts, c.slots, c.p, c.dK, c.dV, nullptr, 0, 0, 0, c.D, rows, c.scale};
-    BSP_WIN_TYPES(launch_behind(join_kv_kernel<float>, dim3(n_cta, kJoinParts), kJoinT, 0, c.stream, a, kp),
-                  launch_behind(join_kv_kernel<__nv_bfloat16>, dim3(n_cta, kJoinParts), kJoinT, 0, c.stream, a, kp),
-                  launch_behind(join_kv_kernel<__half>, dim3(n_cta, kJoinParts), kJoinT, 0, c.stream, a, kp))
+    BSP_WIN_TYPES(launch_behind(join_kv_kernel<float>, dim3(n_cta, 2 * kJoinParts), kJoinT, 0, c.stream, a, kp),
+                  launch_behind(join_kv_kernel<__nv_bfloat16>, dim3(n_cta, 2 * kJoinParts), kJoinT, 0, c.stream, a, kp),
+                  launch_behind(join_kv_kernel<__half>, dim3(n_cta, 2 * kJoinParts), kJoinT, 0, c.stream, a, kp))
 }
 
 int launch_delta(const Call& c) { BSP_WIN_TYPES(delta_t<float>(c), delta_t<__nv_bfloat16>(c), delta_t<__half>(c)) }

@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
             if (!it.whole()) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g)
-                    *reinterpret_cast<float4*>(slot + r * kSlotD + 64 * g + 4 * tx) =
+                    *reinterpret_cast<float4*>(slot + SlotRows(rows).at(r, 64 * g + 4 * tx)) =
                         make_float4(acc[u][g][0].x, acc[u][g][0].y, acc[u][g][1].x, acc[u][g][1].y);
                 if (tx == 0) {
                     slot[R * kSlotD + r] = m[u];
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dq_kernel(const __grid_c
                 const int c = 64 * g + 4 * tx;
                 const float2 a = acc[u][g][0], b = acc[u][g][1];
                 if (!it.whole())
-                    *reinterpret_cast<float4*>(slot + r * kSlotD + c) = make_float4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<float4*>(slot + SlotRows(rows).at(r, c)) = make_float4(a.x, a.y, b.x, b.y);
                 else if (c < A.D)
                     store4(dst + c, a.x * A.scale, a.y * A.scale, b.x * A.scale, b.y * A.scale);
             }
@@ -532,8 +532,8 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) dkv_kernel(const __grid_
                 const int c = 64 * g + 4 * tx;
                 const float2 a = ak[u][g][0], b = ak[u][g][1], e = av[u][g][0], f = av[u][g][1];
                 if (!it.whole()) {
-                    *reinterpret_cast<float4*>(slot + r * kSlotD + c) = make_float4(a.x, a.y, b.x, b.y);
-                    *reinterpret_cast<float4*>(slot + (R + r) * kSlotD + c) = make_float4(e.x, e.y, f.x, f.y);
+                    *reinterpret_cast<float4*>(slot + SlotRows(R).at(r, c)) = make_float4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<float4*>(slot + R * kSlotD + SlotRows(R).at(r, c)) = make_float4(e.x, e.y, f.x, f.y);
                 } else if (c < A.D) {
                     store4(at<T>(A.dK, w.z, w.hk, kb + r) + c, a.x * A.scale, a.y * A.scale, b.x * A.scale, b.y * A.scale);
                     store4(at<T>(A.dV, w.z, w.hk, kb + r) + c, e.x, e.y, f.x, f.y);
