@@ -445,7 +445,8 @@ typedef struct {
  * calls report to.  window, sinks >= 0.  The handle is immutable and may be
  * used from several streams of its device; the word is cleared on `stream`. */
 int bsp_window_create(int window, int sinks, void* stream, bsp_window_t* out);
-/* Free a handle (waits for the device).  NULL is ignored. */
+/* Free a handle (waits for the device).  NULL is ignored.  Graphs that captured
+ * its calls must not be replayed afterwards. */
 int bsp_window_destroy(bsp_window_t w);
 int bsp_window_info(bsp_window_t w, int* window, int* sinks);
 /* As bsp_status_check: synchronise `stream`, return and clear the status word

@@ -529,7 +529,8 @@ def block_sparse_attention(L: Layout, Q, K, V, scale: float, mask_kind: int = MA
 class Window:
     """Owning wrapper of a bsp_window_t handle: a visibility rule (key j is
     visible to the query at position p when j <= p and (p - j < window or
-    j < sinks); window 0 = no limit) on one device."""
+    j < sinks); window 0 = no limit) on one device.  Keep it as long as graphs
+    that captured its calls are replayed."""
 
     def __init__(self, handle: ctypes.c_void_p, device: torch.device):
         self.handle = handle

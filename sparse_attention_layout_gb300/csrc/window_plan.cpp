@@ -27,9 +27,11 @@ struct Key {
 };
 
 // Boundaries lie at equal steps, but never inside a tile of at most 4 steps or
-// a 32nd of a share: cutting one saves less than its join costs (256 rows of 4
-// heads, window 64: 23.6 us cut, 11.5 whole; up to an eighth of a share instead,
-// full attention over 8192 keys took 244 us for 224).
+// a 32nd of a share: cutting one saves less than its join costs (us, whole and
+// cut: 256 rows of 4 heads, window 64: 11.4 and 13.6; 4 x 16 heads of 8192 rows,
+// window 128, with gradient: 475 and 494; the gradient of 1037 rows of 12 heads
+// 39.6 and 43.2, with tiles of 8 steps whole 47.6; up to an eighth of a share,
+// full attention over 8192 keys took 244 for 224).
 void split(const std::vector<int>& steps, int rep, int ctas, Table* tab, CtaStart* out) {
     const int ntiles = (int)steps.size(), items = ntiles * rep;
     int64_t one = 0;

@@ -92,6 +92,18 @@ def test_dense(bsp, path, shape, dtype):
         assert torch.equal(a, b)
 
 
+# few to many rows over a history that many CTAs share; the last: ten keys whose
+# queries many CTAs share
+JOINED = [(1, 1, 1, Sq, 9000, D, 0, 0) for Sq, D in ((1, 64), (20, 16), (31, 128), (33, 64), (40, 48), (100, 128))]
+JOINED += [(1, 6, 2, 7, 12345, 80, 0, 0), (1, 64, 1, 400, 394, 64, 0, 0)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", JOINED, ids=str)
+def test_tiles_of_many_pieces(bsp, path, shape, dtype):
+    test_dense(bsp, path, shape, dtype)
+
+
 def test_large_scores(bsp, path):
     """Scores of +-1000 with a moving maximum: no overflow, one key takes all."""
     Z, H, S, D = 1, 2, 400, 64
