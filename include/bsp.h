@@ -403,7 +403,7 @@ size_t bsp_attention_host_workspace(bsp_layout_t layout, int dtype, int D, int z
  * Visibility: key j is visible to the query at position p when
  *     j <= p and (p - j < window or j < sinks);
  * window 0 = no limit.  A query that sees no key has output 0 and log-sum-exp
- * -inf, and contributes nothing to a gradient.
+ * -inf, and contributes nothing to a gradient, whatever its rows hold.
  *
  * Tensors are strided (bsp_tensor_t): element (i, j, k, d) at
  * ptr + (i * stride[0] + j * stride[1] + k * stride[2] + d) elements; the

@@ -49,8 +49,8 @@ struct Call {
     View Q, K, V, O, dO, dQ, dK, dV;
     float* lse;
     int64_t lz, lh, lt;  // strides of lse (batch entry, head, row)
-    // backward: rows' dO . O, laid out as lse (CUDA cores), or per tile of
-    // kStatRows rows their -lse log2(e) and dO . O (tensor cores)
+    // backward: rows' dO . O, with the strides of lse (CUDA cores), or per tile
+    // of kStatRows rows their -lse log2(e) and dO . O (tensor cores)
     float* stats;
     Prob p;              // TQ and kshift set by the launcher
     int Z;
@@ -90,6 +90,8 @@ int launch_forward_tc(Call& c);   // BSP_ERR_UNSUPPORTED: not a 16-bit type
 int launch_backward_tc(Call& c);
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
                   const Prob& p, int D, cudaStream_t s);
+// zeros n0 x n1 x n2 rows of row16 16-byte pieces (elt: bytes of an element of v)
+int launch_zero(const View& v, int elt, int64_t n0, int64_t n1, int64_t n2, int row16, cudaStream_t s);
 // The split of a dense launch's query tiles (p) or key tiles (k) over `ctas`
 // CTAs; *cut: some tile is shared between CTAs, so that a join has to follow.
 // BSP_ERR_OOM when the host has no memory for it.

@@ -123,17 +123,6 @@ void dense_prob(const bsp_window_s* w, int Z, int Hq, int Hkv, int Sq, int Sk, P
     p->Hq = Hq, p->Hkv = Hkv, p->Sq = Sq, p->Sk = Sk;
 }
 
-// zero `n0 x n1 x n2` rows of D elements of a strided tensor
-int zero_view(const View& v, int64_t n0, int64_t n1, int64_t n2, size_t row_bytes, int elt, cudaStream_t s) {
-    for (int64_t i = 0; i < n0; ++i)
-        for (int64_t j = 0; j < n1; ++j) {
-            char* p = static_cast<char*>(v.ptr) + (i * v.s[0] + j * v.s[1]) * elt;
-            if (n2 > 0 && cudaMemset2DAsync(p, (size_t)v.s[2] * elt, 0, row_bytes, (size_t)n2, s) != cudaSuccess)
-                return BSP_ERR_CUDA;
-        }
-    return BSP_OK;
-}
-
 }  // namespace
 
 extern "C" int bsp_window_create(int window, int sinks, void* stream, bsp_window_t* out) {
@@ -269,16 +258,26 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
     }
     if (Sq > 0 && Sk > 0 && clash({dQ, dK, dV}, {Q, K, V, O, dO})) return BSP_ERR_INVALID_ARG;
     // no pair at all: every gradient is 0
+    const int row16 = D * elt / 16;
     if (Sq == 0) {
-        if (Sk > 0 && !(rc = zero_view(c.dK, Z, Hkv, Sk, (size_t)D * elt, elt, s)))
-            rc = zero_view(c.dV, Z, Hkv, Sk, (size_t)D * elt, elt, s);
+        if (Sk > 0 && !(rc = bsp::win::launch_zero(c.dK, elt, Z, Hkv, Sk, row16, s)))
+            rc = bsp::win::launch_zero(c.dV, elt, Z, Hkv, Sk, row16, s);
         return rc;
     }
-    if (Sk == 0) return zero_view(c.dQ, Z, Hq, Sq, (size_t)D * elt, elt, s);
+    if (Sk == 0) return bsp::win::launch_zero(c.dQ, elt, Z, Hq, Sq, row16, s);
     if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1)))) return rc;
     c.w = w, c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
     c.lse = const_cast<float*>(lse);
     c.lz = (int64_t)Hq * Sq, c.lh = Sq, c.lt = 1;
+    if (Sq > Sk) {
+        // the first queries stand before position 0: their dQ is 0, and the
+        // kernels never meet their rows, which may hold anything
+        const int none = Sq - Sk;
+        if ((rc = bsp::win::launch_zero(c.dQ, elt, Z, Hq, none, row16, s))) return rc;
+        for (View* v : {&c.Q, &c.O, &c.dO, &c.dQ}) v->ptr = static_cast<char*>(v->ptr) + v->s[2] * none * elt;
+        c.lse += none;
+        Sq = Sk;
+    }
     dense_prob(w, Z, Hq, Hkv, Sq, Sk, &c.p);
     char* ws = static_cast<char*>(workspace);
     c.cuts = reinterpret_cast<bsp::win::Cut*>(ws);

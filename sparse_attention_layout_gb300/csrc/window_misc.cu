@@ -199,11 +199,16 @@ __global__ void __launch_bounds__(kJoinT) join_kv_kernel(const JoinArgs a, const
                is_v ? 1.0f : a.scale);
 }
 
-// delta[z][h][t] = dO . O of the row, fp32: a group of 8 lanes per row, 16
-// bytes per lane and step.  Reads both tensors once: HBM-bound.
+// Strides of the rows' log-sum-exp (and dO . O): batch entry, head, row.
+struct RowStrides {
+    int64_t z, h, t;
+};
+
+// delta = dO . O of the row, fp32, where the strides say: a group of 8 lanes per
+// row, 16 bytes per lane and step.  Reads both tensors once: HBM-bound.
 template <typename T>
-__global__ void __launch_bounds__(256) delta_kernel(const View O, const View dO, float* delta, int64_t rows, int Hq, int S,
-                                                    int D) {
+__global__ void __launch_bounds__(256) delta_kernel(const View O, const View dO, float* delta, const RowStrides at,
+                                                    int64_t rows, int Hq, int S, int D) {
     constexpr int N = Vec16<T>::N;
     const int sub = threadIdx.x & 7;
     for (int64_t r = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); r < rows; r += (int64_t)gridDim.x * 32) {
@@ -221,7 +226,7 @@ __global__ void __launch_bounds__(256) delta_kernel(const View O, const View dO,
         const unsigned group = 0xffu << (threadIdx.x & 24);  // the row's 8 lanes
 #pragma unroll
         for (int k = 4; k; k >>= 1) x += __shfl_xor_sync(group, x, k);
-        if (sub == 0) delta[r] = x;
+        if (sub == 0) delta[z * at.z + h * at.h + t * at.t] = x;
     }
 }
 
@@ -230,8 +235,9 @@ __global__ void __launch_bounds__(256) delta_kernel(const View O, const View dO,
 // dO . O, so that one bulk copy brings a tile's statistics.  Rows beyond the
 // sequence and rows that see nothing get -inf: their P is then 0.
 template <typename T>
-__global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const View dO, const float* lse, float* stats,
-                                                         int64_t rows, int ntiles, int G, int TQ, int Hkv, int S, int D) {
+__global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const View dO, const float* lse,
+                                                         const RowStrides at, float* stats, int64_t rows, int ntiles,
+                                                         int G, int TQ, int Hkv, int S, int D) {
     constexpr int N = Vec16<T>::N;
     const int sub = threadIdx.x & 7;
     cudaGridDependencySynchronize();
@@ -257,7 +263,7 @@ __global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const Vie
 #pragma unroll
         for (int k = 4; k; k >>= 1) x += __shfl_xor_sync(group, x, k);
         if (sub == 0) {
-            const float l = live ? lse[(z * (int64_t)Hkv * G + h) * S + t] : -INFINITY;
+            const float l = live ? lse[z * at.z + h * at.h + t * at.t] : -INFINITY;
             stats[tile * 2 * kStatRows + r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
             stats[tile * 2 * kStatRows + kStatRows + r] = x;
         }
@@ -338,6 +344,14 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     }
 }
 
+// zeros rows of row16 16-byte pieces of a strided tensor (strides in pieces)
+__global__ void __launch_bounds__(256) zero_kernel(const View v, int64_t pieces, int64_t n1, int64_t n2, int row16) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
+        const int64_t c = i % row16, r = i / row16, k = r % n2, jk = r / n2, j = jk % n1, z = jk / n1;
+        static_cast<uint4*>(v.ptr)[z * v.s[0] + j * v.s[1] + k * v.s[2] + c] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
+
 template <typename T>
 int join_t(const JoinArgs& a, int n_cta, bool is_dq, cudaStream_t s) {
     return launch_behind(is_dq ? join_kernel<T, true> : join_kernel<T, false>, dim3(n_cta, kJoinParts), kJoinT, 0, s, a);
@@ -347,8 +361,8 @@ template <typename T>
 int delta_t(const Call& c) {
     const int64_t rows = (int64_t)c.Z * c.p.Hq * c.p.Sq;
     const int64_t blocks = (rows + 31) / 32, most = (int64_t)sm_count() * 16;
-    delta_kernel<T><<<(int)(blocks < most ? blocks : most), 256, 0, c.stream>>>(c.O, c.dO, c.stats, rows, c.p.Hq, c.p.Sq,
-                                                                                 c.D);
+    delta_kernel<T><<<(int)(blocks < most ? blocks : most), 256, 0, c.stream>>>(
+        c.O, c.dO, c.stats, RowStrides{c.lz, c.lh, c.lt}, rows, c.p.Hq, c.p.Sq, c.D);
     return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
@@ -358,7 +372,7 @@ int tile_stats_t(const Call& c) {
     const int64_t rows = (int64_t)c.Z * c.p.Hkv * ntiles * kStatRows;
     const int64_t blocks = (rows + 31) / 32, most = (int64_t)sm_count() * 16;
     return launch_behind(tile_stats_kernel<T>, dim3((int)(blocks < most ? blocks : most)), 256, 0, c.stream, c.O, c.dO,
-                         (const float*)c.lse, c.stats, rows, ntiles, c.p.G, tq, c.p.Hkv, c.p.Sq, c.D);
+                         (const float*)c.lse, RowStrides{c.lz, c.lh, c.lt}, c.stats, rows, ntiles, c.p.G, tq, c.p.Hkv, c.p.Sq, c.D);
 }
 
 View in_16(const View& v, int elt) {
@@ -394,6 +408,13 @@ int launch_delta(const Call& c) { BSP_WIN_TYPES(delta_t<float>(c), delta_t<__nv_
 
 int launch_tile_stats(const Call& c) {
     BSP_WIN_TYPES(BSP_ERR_UNSUPPORTED, tile_stats_t<__nv_bfloat16>(c), tile_stats_t<__half>(c))
+}
+
+int launch_zero(const View& v, int elt, int64_t n0, int64_t n1, int64_t n2, int row16, cudaStream_t s) {
+    const int64_t pieces = n0 * n1 * n2 * row16, blocks = (pieces + 255) / 256, most = (int64_t)sm_count() * 8;
+    if (pieces == 0) return BSP_OK;
+    zero_kernel<<<(int)(blocks < most ? blocks : most), 256, 0, s>>>(in_16(v, elt), pieces, n1, n2, row16);
+    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,

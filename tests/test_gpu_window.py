@@ -633,3 +633,42 @@ def test_refusals(bsp):
     assert call(ws.data_ptr(), ws.numel(), None, 9) == -1
     torch.cuda.synchronize()
     assert bsp.bsp_window_status(W) == 0
+
+
+# --------------------------------------------------- what no query may reach --
+
+def _gradients(bsp, W, Q, K, V, dO, scale=0.125):
+    O, lse = bsp.bsp_window_attention(W, Q, K, V, scale=scale)
+    return (O, lse, *bsp.bsp_window_attention_backward(W, Q, K, V, O, dO, lse, scale=scale))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", [(4, 2, 300, 170, 64, 40, 2), (1, 1, 700, 1, 128, 0, 0), (6, 2, 901, 400, 80, 60, 9)],
+                         ids=str)
+def test_gradient_of_queries_that_see_nothing(bsp, path, shape, dtype):
+    """More queries than keys: the first ones see nothing, whatever they and
+    their output gradient hold, their dQ is 0 and the rest is as without them."""
+    Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    Q, dO = (randn((2, Hq, Sq, D), DT[dtype], 110 + i, "rows") for i in range(2))
+    K, V = (randn((2, Hkv, Sk, D), DT[dtype], 112 + i) for i in range(2))
+    W = bsp.bsp_window_create(window, sinks)
+    n = Sq - Sk
+    O, lse = bsp.bsp_window_attention(W, Q, K, V, scale=0.125)
+    want = bsp.bsp_window_attention_backward(W, Q[:, :, n:], K, V, O[:, :, n:], dO[:, :, n:],
+                                             lse[:, :, n:].contiguous(), scale=0.125)
+    r = ref.dense(Q, K, V, 0.125, window, sinks, dO)
+    for value in (None, math.nan, math.inf):
+        if value is not None:
+            Q[:, :, :n] = value
+            dO[:, :, :n] = value
+        O, lse, dQ, dK, dV = _gradients(bsp, W, Q, K, V, dO)
+        assert bool((O[:, :, :n] == 0).all()) and bool((lse[:, :, :n] == -math.inf).all())
+        assert bool((dQ[:, :, :n] == 0).all())
+        for name, got in (("dQ", dQ), ("dK", dK), ("dV", dV)):
+            check(got, r[name], r["e" + name[-1]], name)
+        assert torch.equal(dQ[:, :, n:], want[0]) and torch.equal(dK, want[1]) and torch.equal(dV, want[2])
+    # a key of no number reaches those that see it, not the queries that see nothing
+    K[:, :, 0] = math.nan
+    dQ = _gradients(bsp, W, Q, K, V, dO)[2]
+    assert bool((dQ[:, :, :n] == 0).all())
+    assert bsp.bsp_window_status(W) == 0
