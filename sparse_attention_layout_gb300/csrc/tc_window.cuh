@@ -121,6 +121,23 @@ struct Ring {
     }
 };
 
+// Rows r0 .. r1 - 1 of a tile in shared memory (KP panels of 128 rows of 128
+// bytes) set to 0 by a warp.
+template <int KP>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1, int lane) {
+#pragma unroll 1
+    for (int i = r0 * 8 + lane; i < r1 * 8; i += 32)
+#pragma unroll
+        for (int c = 0; c < KP; ++c) *reinterpret_cast<uint4*>(tile + c * 16384 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+}
+// The rows of the key tile that begins at key kb that no query of a dense call
+// sees (the keys between the sinks and the first query's window), as a range.
+struct Unseen {
+    int r0, r1;
+    __device__ __forceinline__ Unseen(int kb, int sinks, int zlo) : r0(imax(sinks - kb, 0)), r1(imin(zlo - kb, 128)) {}
+    __device__ __forceinline__ bool any() const { return r0 < r1; }
+};
+
 __device__ __forceinline__ Keys tile_keys(const Prob& p, const Work& w) {
     return Keys{window_low(w.a, p.window), w.a + w.nt - 1, p.sinks};
 }

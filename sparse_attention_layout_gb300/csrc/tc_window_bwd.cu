@@ -12,6 +12,10 @@
 // tiles passes through shared memory.  Persistent CTAs take equal runs of
 // steps, as in the forward; the tile with the sinks, which every query sees, is
 // cut among many.
+//
+// K and V rows that no query sees but that share a tile with visible ones are
+// zeroed in shared memory where a product sums over them or their dP enters a
+// product, since 0 * NaN is NaN.
 #include "tc_window.cuh"
 
 namespace bsp {
@@ -96,6 +100,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t a_full, a_free, k_full[2], v_full[2], s_full[2], dp_full, dp_free, ds_full[2], dq_done[2];
+    __shared__ uint64_t land;  // K and V of a step with rows to be zeroed
     __shared__ uint64_t acc_full, acc_empty;
     __shared__ uint32_t tmem_base;
     __shared__ int abort_flag;
@@ -115,6 +120,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         mbar_init(&a_free, 2);  // S has read Q, dP has read dO
         mbar_init(&dp_full, 1);
         mbar_init(&dp_free, 8);
+        mbar_init(&land, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&k_full[i], 1);
             mbar_init(&v_full[i], 1);
@@ -150,7 +156,8 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 tma_prefetch_desc(&tmV);
             }
             const uint32_t a_bytes = (uint32_t)(p.TQ * p.G) * 128 * KP;
-            uint32_t g = 0, tiles = 0;
+            const int zlo = window_low(p.Sk - p.Sq, p.window);
+            uint32_t g = 0, tiles = 0, lands = 0;
             Walk<Prob, kDense> walk(p, plan.tab, plan.s[blockIdx.x]);
             Item it;
             Work w;
@@ -180,16 +187,35 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                         const bool ok = wait(&dq_done[st], ((g - 2) >> 1) & 1, ab);
                         if (!__all_sync(0xffffffffu, ok)) goto load_done;
                     }
+                    const int kb = w.key_tile(n) << 7;
+                    const Unseen un(kb, p.sinks, zlo);
+                    uint64_t* const kbar = un.any() ? &land : &k_full[st];
+                    uint64_t* const vbar = un.any() ? &land : &v_full[st];
                     if (lane == 0) {
-                        const int kb = w.key_tile(n) << 7;
-                        mbar_arrive_expect_tx(&k_full[st], kTile);
+                        if (un.any()) mbar_expect_tx(&land, kTile);
+                        else mbar_arrive_expect_tx(kbar, kTile);
                         for (int c = 0; c < KP; ++c)
-                            tma_load_4d(smem_u32(smem + SM::kX + st * kTile + c * 16384), &tmK, c * 64, kb, w.hk, w.z,
-                                        &k_full[st]);
-                        mbar_arrive_expect_tx(&v_full[st], kTile);
+                            tma_load_4d(smem_u32(smem + SM::kX + st * kTile + c * 16384), &tmK, c * 64, kb, w.hk, w.z, kbar);
+                        mbar_arrive_expect_tx(vbar, kTile);
                         for (int c = 0; c < KP; ++c)
-                            tma_load_4d(smem_u32(smem + SM::kY + st * kTile + c * 16384), &tmV, c * 64, kb, w.hk, w.z,
-                                        &v_full[st]);
+                            tma_load_4d(smem_u32(smem + SM::kY + st * kTile + c * 16384), &tmV, c * 64, kb, w.hk, w.z, vbar);
+                    }
+                    if (un.any()) {
+                        __syncwarp();
+                        const bool ok = wait(&land, lands & 1, ab);
+                        if (!__all_sync(0xffffffffu, ok)) {
+                            if (lane == 0) drain_wait(&land, lands & 1);
+                            goto load_done;
+                        }
+                        ++lands;
+                        zero_rows<KP>(smem + SM::kX + st * kTile, un.r0, un.r1, lane);
+                        zero_rows<KP>(smem + SM::kY + st * kTile, un.r0, un.r1, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&k_full[st]);
+                            mbar_arrive(&v_full[st]);
+                        }
                     }
                 }
             }
@@ -406,6 +432,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
     uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     // stages of Q, dO and the rows' statistics: step % 4; scores: step % 2
     __shared__ uint64_t a_full, a_free, x_full[4], dk_done[4];
+    __shared__ uint64_t land;  // V of a tile with rows to be zeroed
     __shared__ uint64_t s_full[2], p_full[2], dv_done[2], dp_full[2], ds_full[2];
     __shared__ uint64_t dv_full, dv_empty, dk_full, dk_empty;
     __shared__ uint32_t tmem_base;
@@ -424,6 +451,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         for (int i = 0; i < 5; ++i) issued[i] = 0;
         mbar_init(&a_full, 1);
         mbar_init(&a_free, 2);  // S^T has read K, dP^T has read V
+        mbar_init(&land, 1);
         for (int i = 0; i < 4; ++i) {
             mbar_init(&x_full[i], 1);
             mbar_init(&dk_done[i], 1);
@@ -470,7 +498,8 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 tma_prefetch_desc(&tmV);
             }
             const uint32_t bytes = (uint32_t)(kp.TQ * p.G) * 128 * KP;
-            uint32_t g = 0, tiles = 0;
+            const int zlo = window_low(p.Sk - p.Sq, p.window);
+            uint32_t g = 0, tiles = 0, lands = 0;
             Walk<KProb, kDense> walk(kp, plan.tab, plan.s[blockIdx.x]);
             Item it;
             Work w;
@@ -487,12 +516,30 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                     const bool ok = wait(&a_free, (tiles - 1) & 1, ab);
                     if (!__all_sync(0xffffffffu, ok)) goto load_done;
                 }
+                const Unseen un(w.tile << 7, p.sinks, zlo);
+                uint64_t* const vbar = un.any() ? &land : &a_full;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&a_full, 2 * kTile);
-                    for (int c = 0; c < KP; ++c) {
-                        tma_load_4d(smem_u32(smem + SM::kA + c * 16384), &tmK, c * 64, w.tile << 7, w.hk, w.z, &a_full);
-                        tma_load_4d(smem_u32(smem + SM::kB + c * 16384), &tmV, c * 64, w.tile << 7, w.hk, w.z, &a_full);
+                    if (un.any()) mbar_arrive_expect_tx(&land, kTile);
+                    else mbar_expect_tx(&a_full, kTile);
+                    for (int c = 0; c < KP; ++c)
+                        tma_load_4d(smem_u32(smem + SM::kB + c * 16384), &tmV, c * 64, w.tile << 7, w.hk, w.z, vbar);
+                }
+                if (un.any()) {
+                    __syncwarp();
+                    const bool ok = wait(&land, lands & 1, ab);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        if (lane == 0) drain_wait(&land, lands & 1);
+                        goto load_done;
                     }
+                    ++lands;
+                    zero_rows<KP>(smem + SM::kB, un.r0, un.r1, lane);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&a_full, kTile);
+                    for (int c = 0; c < KP; ++c)
+                        tma_load_4d(smem_u32(smem + SM::kA + c * 16384), &tmK, c * 64, w.tile << 7, w.hk, w.z, &a_full);
                 }
                 ++tiles;
 #pragma unroll 1

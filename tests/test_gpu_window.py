@@ -672,3 +672,36 @@ def test_gradient_of_queries_that_see_nothing(bsp, path, shape, dtype):
     dQ = _gradients(bsp, W, Q, K, V, dO)[2]
     assert bool((dQ[:, :, :n] == 0).all())
     assert bsp.bsp_window_status(W) == 0
+
+
+# (Hq, Hkv, Sq, Sk, D, window, sinks): queries fewer than keys, so that the keys
+# before every window are seen by nobody
+UNSEEN = [(2, 1, 100, 1000, 64, 50, 0), (4, 2, 16, 256, 128, 32, 0), (6, 2, 130, 700, 80, 60, 5),
+          (1, 1, 1, 130, 64, 1, 1), (2, 2, 400, 5000, 128, 300, 200)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("shape", UNSEEN, ids=str)
+def test_gradient_without_the_keys_that_nobody_sees(bsp, path, shape, dtype):
+    """K and V rows before every window may hold anything: no gradient changes
+    by a bit, and their own is 0."""
+    Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    Q, dO = (randn((2, Hq, Sq, D), DT[dtype], 120 + i) for i in range(2))
+    K, V = (randn((2, Hkv, Sk, D), DT[dtype], 122 + i, "rows") for i in range(2))
+    W = bsp.bsp_window_create(window, sinks)
+    want = _gradients(bsp, W, Q, K, V, dO)
+    r = ref.dense(Q, K, V, 0.125, window, sinks, dO)
+    for i, name in ((2, "dQ"), (3, "dK"), (4, "dV")):
+        check(want[i], r[name], r["e" + name[-1]], name)
+    unseen = torch.zeros(Sk, dtype=torch.bool, device="cuda")
+    unseen[sinks:Sk - Sq - window + 1] = True
+    assert bool(unseen.any())
+    for value in (math.nan, math.inf, -60000.0):
+        for both in ((K,), (V,), (K, V)):
+            k, v = (t.clone() for t in (K, V))
+            for t in (k if x is K else v for x in both):
+                t[:, :, unseen] = value
+            got = _gradients(bsp, W, Q, k, v, dO)
+            assert all(torch.equal(a, b) for a, b in zip(got, want)), value
+            assert bool((got[3][:, :, unseen] == 0).all()) and bool((got[4][:, :, unseen] == 0).all())
+    assert bsp.bsp_window_status(W) == 0
