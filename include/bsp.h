@@ -418,7 +418,10 @@ size_t bsp_attention_host_workspace(bsp_layout_t layout, int dtype, int D, int z
  * 64 query heads per KV head; D 16 .. 128, a multiple of 16; lengths up to
  * 2^30 (beyond: BSP_ERR_UNSUPPORTED).  dtype, streams, errors as above; sums,
  * softmax statistics and partial results are fp32, the 16-bit tensor-core
- * paths round P and dS to the call's type (unnormalised P <= 2^8).
+ * paths round P and dS to the call's type (unnormalised P <= 2^8).  The fp16
+ * gradient holds P and dS times powers of two, dS by the longest rows of dO and
+ * V of its batch entry and KV head, so that neither leaves the type's range for
+ * a dO of any size.
  *
  * Non-finite values: keys that no query of a call sees (behind a sequence's
  * length, before every window) never reach an output, whatever their slots

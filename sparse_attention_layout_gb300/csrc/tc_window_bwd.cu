@@ -13,6 +13,10 @@
 // steps, as in the forward; the tile with the sinks, which every query sees, is
 // cut among many.
 //
+// P and dS are rounded to the call's type on their way to the products that
+// contract over them, which take no fp32 operands; all sums stay in fp32.  fp16
+// holds both times powers of two (window.h, DsFactor).
+//
 // K and V rows that no query sees but that share a tile with visible ones are
 // zeroed in shared memory where a product sums over them or their dP enters a
 // product, since 0 * NaN is NaN.
@@ -25,7 +29,8 @@ namespace {
 struct Args {
     Prob p;
     View dQ, dK, dV;
-    const float* stats;  // per tile of kStatRows rows: -lse log2(e), then dO . O
+    float* stats;        // kStatTile floats per tile of kStatRows rows
+    const DsFactor* factor;  // fp16: per (batch entry, KV head)
     int D, ntiles;       // such tiles per (batch entry, KV head)
     float scale, c2;     // c2 = scale * log2(e)
     Cut* cuts;
@@ -47,10 +52,11 @@ struct Smem {
 
 // 128 x DP accumulator columns of a warp's 32 rows to the partial-result slot
 // (raw fp32) or, scaled and rounded, to memory; arrives on `empty` as soon as
-// the columns are in registers.
+// the columns are in registers.  down: what takes fp16's factors out.
 template <typename T, int DP, typename F>
 __device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, int row, int rows, float* slot,
-                                      float scale, int D, uint8_t* stage, F dst) {
+                                      float scale, float down, int D, uint8_t* stage, F dst) {
+    constexpr bool kF16 = std::is_same<T, __half>::value;
     if (slot) {
         const SlotRows sr(rows);
         float* at = slot + sr.at(row, 0);
@@ -58,6 +64,10 @@ __device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, 
         for (int c = 0; c < DP / 32; ++c) {
             uint32_t r[32];
             tmem_ld32_sync(tacc + c * 32, r);
+            if (kF16) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) r[k] = __float_as_uint(__uint_as_float(r[k]) * down);
+            }
             if (row < rows) {
 #pragma unroll
                 for (int k = 0; k < 8; ++k, at += sr.step)
@@ -71,7 +81,7 @@ __device__ __forceinline__ void drain(uint32_t tacc, uint64_t* empty, int lane, 
     }
     uint32_t pk[DP / 64][32];
 #pragma unroll
-    for (int c = 0; c < DP / 64; ++c) read_panel<T>(tacc + c * 64, scale, pk[c]);
+    for (int c = 0; c < DP / 64; ++c) read_panel<T>(tacc + c * 64, kF16 ? scale * down : scale, pk[c]);
     tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(empty);
@@ -299,7 +309,8 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             ++tiles;
             float* slot = w.whole() ? nullptr : args.slots + (size_t)w.slot() * slot_floats(kTcRows);
             T* out = static_cast<T*>(args.dQ.ptr) + z * args.dQ.s[0] + hk * p.G * args.dQ.s[1] + w.row0 * args.dQ.s[2];
-            drain<T, DP>(tA + lane_base, &acc_empty, lane, row, rows, slot, args.scale, args.D,
+            const float down = kBf ? 1.0f : args.factor[w.rep].down;
+            drain<T, DP>(tA + lane_base, &acc_empty, lane, row, rows, slot, args.scale, down, args.D,
                          smem + SM::kEpi + quad * 4096, [&](int i) -> T* {
                              const int r = quad * 32 + i, t = (r * inv_g) >> 16, h = r - t * p.G;
                              return r < rows ? out + h * args.dQ.s[1] + t * args.dQ.s[2] : nullptr;
@@ -315,7 +326,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         uint32_t g = 0;
         for (uint32_t i = 0;; ++i) {
             int ns, s0, n_s, lo_tile, pos;
-            float nlse, delta;
+            float nlse, delta, up = 1.f;
             Seen seen;
             {
                 Work w;
@@ -324,10 +335,14 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                 const int end = w.nt * p.G - 1;
                 const int t = (imin(row, end) * inv_g) >> 16, h = row - t * p.G;
                 const int tq = kStatRows / p.G, tok = w.row0 + t;
-                const float* s = args.stats + ((int64_t)w.rep * args.ntiles + tok / tq) * (2 * kStatRows) +
-                                 tok % tq * p.G + h;
-                nlse = row <= end ? s[0] : -INFINITY;  // rows past the tile's last: P = 0
-                delta = row <= end ? s[kStatRows] : 0.f;
+                float* s = args.stats + ((int64_t)w.rep * args.ntiles + tok / tq) * kStatTile + tok % tq * p.G + h;
+                nlse = row <= end ? s[kStatLse] : -INFINITY;  // rows past the tile's last: P = 0
+                delta = row <= end ? s[kBf ? kStatDelta : kStatDot] : 0.f;
+                if (!kBf) {
+                    up = args.factor[w.rep].up;
+                    delta *= up;
+                    if (wg == 0 && row <= end) s[kStatDelta] = delta;  // for the dkv kernel
+                }
                 pos = w.a + t;
                 seen.first = w.a + (int)((imin(quad * 32, end) * inv_g) >> 16);
                 seen.last = w.a + (int)((imin(quad * 32 + 31, end) * inv_g) >> 16);
@@ -364,7 +379,8 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
                     tmem_ld32_sync(tP + lane_base + wg * 64 + c * 32, r);
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        const float2 d = __fadd2_rn(make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1])), nd);
+                        const float2 dp = make_float2(__uint_as_float(r[j]), __uint_as_float(r[j + 1]));
+                        const float2 d = kBf ? __fadd2_rn(dp, nd) : __ffma2_rn(dp, make_float2(up, up), nd);
                         const float2 e = __fmul2_rn(d, make_float2(x[c * 32 + j], x[c * 32 + j + 1]));
                         pk[c * 16 + j / 2] = Pack2<T>::pack(e.x, e.y);
                     }
@@ -556,7 +572,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                             tma_load_4d(smem_u32(smem + SM::kX + st * kStep + c * kPanel), &tmQ, c * 64, w.hk * p.G, tok,
                                         w.z, &x_full[st]);
                         bulk_load(smem_u32(smem + SM::kStats + st * 8 * kStatRows),
-                                  args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * 2 * kStatRows, 8 * kStatRows,
+                                  args.stats + ((int64_t)w.rep * args.ntiles + w.lo + n) * kStatTile + kStatLse, 8 * kStatRows,
                                   &x_full[st]);
                         for (int c = 0; c < KP; ++c)
                             tma_load_4d(smem_u32(smem + SM::kY + st * kStep + c * kPanel), &tmG, c * 64, w.hk * p.G, tok,
@@ -662,12 +678,13 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             bool ok = wait(&dv_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            drain<T, DP>(tV + lane_base, &dv_empty, lane, row, kTcRows,
-                         slot ? slot + (size_t)kTcRows * kSlotD : nullptr, 1.0f, args.D, stage, rows_of(args.dV));
+            drain<T, DP>(tV + lane_base, &dv_empty, lane, row, kTcRows, slot ? slot + (size_t)kTcRows * kSlotD : nullptr,
+                         1.0f, 1.0f / (1 << kPUp), args.D, stage, rows_of(args.dV));
             ok = wait(&dk_full, tiles & 1, ab);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
-            drain<T, DP>(tK + lane_base, &dk_empty, lane, row, kTcRows, slot, args.scale, args.D, stage,
+            const float down = kBf ? 1.0f : args.factor[w.rep].down;
+            drain<T, DP>(tK + lane_base, &dk_empty, lane, row, kTcRows, slot, args.scale, down, args.D, stage,
                          rows_of(args.dK));
             ++tiles;
             if (threadIdx.x == 128 && w.s0 == 0 && !w.whole()) cut = w;
@@ -680,11 +697,13 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
         uint32_t g = 0;
         for (uint32_t i = 0;; ++i) {
             int ns, first, j;
+            float up = 1.f;
             {
                 Work w;
                 if (!ring.take(i, w, lane == 0, true, ab)) break;
                 ns = w.ns, first = w.lo;
                 j = (w.tile << 7) + row;  // this thread's key
+                if (!kBf) up = args.factor[w.rep].up;
             }
             const int j_first = j - lane, j_last = j_first + 31;
 #pragma unroll 1
@@ -741,10 +760,11 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
 #pragma unroll
                     for (int i = 0; i < 32; i += 4) {
                         const float4 dl = *reinterpret_cast<const float4*>(stats + kStatRows + c * 32 + i);
-                        const float2 d0 = __fadd2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])),
-                                                     make_float2(-dl.x, -dl.y));
-                        const float2 d1 = __fadd2_rn(make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3])),
-                                                     make_float2(-dl.z, -dl.w));
+                        const float2 dp0 = make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
+                        const float2 dp1 = make_float2(__uint_as_float(r[i + 2]), __uint_as_float(r[i + 3]));
+                        const float2 n0 = make_float2(-dl.x, -dl.y), n1 = make_float2(-dl.z, -dl.w);
+                        const float2 d0 = kBf ? __fadd2_rn(dp0, n0) : __ffma2_rn(dp0, make_float2(up, up), n0);
+                        const float2 d1 = kBf ? __fadd2_rn(dp1, n1) : __ffma2_rn(dp1, make_float2(up, up), n1);
                         const float2 e0 = __fmul2_rn(d0, make_float2(x[c * 32 + i], x[c * 32 + i + 1]));
                         const float2 e1 = __fmul2_rn(d1, make_float2(x[c * 32 + i + 2], x[c * 32 + i + 3]));
                         pk[c * 16 + i / 2] = Pack2<T>::pack(e0.x, e0.y);
@@ -803,7 +823,7 @@ int launch(Call& c) {
     if ((rc = prepare_kernel(dq_tc_kernel<T, DP>, smem, prepared[0]))) return rc;
     if ((rc = prepare_kernel(dkv_tc_kernel<T, DP>, smem, prepared[1]))) return rc;
     const int grid = imin(sm_count(), TcPlan::kCtas);
-    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.D, (p.Sq + tq2 - 1) / tq2, c.scale, c.scale * kLog2e, c.cuts, c.slots};
+    Args a{p, c.dQ, c.dK, c.dV, c.stats, c.factor, c.D, (p.Sq + tq2 - 1) / tq2, c.scale, c.scale * kLog2e, c.cuts, c.slots};
     const KProb kp{1, p.rep, p.G, tq2, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
     TcPlan plan;
     bool cut;

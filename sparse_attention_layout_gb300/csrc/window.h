@@ -41,6 +41,27 @@ int launch_behind(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaS
     return cudaLaunchKernelEx(&cfg, kern, args...) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
+// The tensor cores take P and dS in the call's type.  fp16 ends at 65504 and
+// 2^-24 (its last full-precision value is 2^-14), and dS = P (dP - delta) leaves
+// it on either side: over 16384 keys P is 2^-14, and dO may be 1e-4 or 1e4.  So
+// the fp16 gradient holds P times 2^15, which its last position 1 allows, and dS
+// times a power of two, one per (batch entry, KV head) since dK sums over the
+// rows: |dP - delta| <= 2 |dO| |V| over the longest rows of dO and V, which
+// leaves the largest dS below 2^15.  Both factors are taken out of the fp32 sums
+// at the end, and are exact.  (Relative error of dQ over 6000 keys, dO of 1, 1e-2,
+// 1e-3: 3.0e-4, 2.1e-4 of it the result's own rounding; unscaled 3.0e-4, 9.3e-4,
+// 9.1e-3.  Cost: a pass over V and one small launch, 4 us of 41 for 1037 rows of
+// 12 heads, 8 of 475 for 8192 rows of 32.)
+constexpr int kPUp = 15;
+struct DsFactor {
+    float up;    // of dP - delta, which P times 2^kPUp then multiplies
+    float down;  // 1 / (up 2^kPUp)
+};
+constexpr int kRangeParts = 512;  // at most, blocks that look for the longest rows of one (batch entry, KV head)
+struct RangePart {
+    float dO2, V2;  // largest sum of squares of a row
+};
+
 // One call's tensors and sizes, checked.
 struct Call {
     const bsp_window_s* w;
@@ -49,9 +70,13 @@ struct Call {
     View Q, K, V, O, dO, dQ, dK, dV;
     float* lse;
     int64_t lz, lh, lt;  // strides of lse (batch entry, head, row)
-    // backward: rows' dO . O, with the strides of lse (CUDA cores), or per tile
-    // of kStatRows rows their -lse log2(e) and dO . O (tensor cores)
+    // backward: rows' dO . O, with the strides of lse (CUDA cores), or kStatTile
+    // floats per tile of kStatRows rows (tensor cores)
     float* stats;
+    // fp16 gradient on the tensor cores: of each (batch entry, KV head) up to
+    // kRangeParts partial results, and the factors
+    RangePart* range;
+    DsFactor* factor;
     Prob p;              // TQ and kshift set by the launcher
     int Z;
     // workspace: partial results of cut tiles
@@ -83,6 +108,9 @@ constexpr int kSimtPerSm = 2, kSimtRows = 64, kTcRows = 128;
 static_assert(kSimtPerSm * kSimtRows <= kTcRows, "the workspace holds two slots of kTcRows rows per SM");
 // query rows of a step of the tensor-core dK / dV kernel
 constexpr int kStatRows = 64;
+// such a step's statistics: fp16's dO . O, -lse log2(e), and dO . O as the dK /
+// dV kernel takes it (fp16: with the factor of dS, which the dQ kernel puts in)
+constexpr int kStatDot = 0, kStatLse = kStatRows, kStatDelta = 2 * kStatRows, kStatTile = 3 * kStatRows;
 
 int launch_forward_simt(Call& c);
 int launch_backward_simt(Call& c);
@@ -100,7 +128,8 @@ void plans_destroy(Plans* p);
 int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts, bool* cut);
 int key_plan(const Call& c, const KProb& k, int ctas, Table* tab, CtaStart* starts, bool* cut);
 
-// stats = rowsum(dO .* O) per row; the same and the rows' -lse log2(e), per tile
+// stats = rowsum(dO .* O) per row; the same and the rows' -lse log2(e), per
+// tile, and fp16's factors
 int launch_delta(const Call& c);
 int launch_tile_stats(const Call& c);
 // joins the pieces of cut tiles: forward / dQ (rows of query tiles) and dK, dV

@@ -84,12 +84,21 @@ bool clash(std::initializer_list<const bsp_tensor_t*> out, std::initializer_list
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace: one record per CTA, two partial-result slots per CTA, and for the
-// backward two floats per query row, in tiles.
+// backward the query rows' statistics, in tiles, and what fp16 scales dS by.
 size_t cuts_bytes() { return round_up(sizeof(bsp::win::Cut) * bsp::win::kSimtPerSm * bsp::sm_count()); }
 size_t slots_bytes(bool backward) {
     const size_t rows = bsp::win::kTcRows;
     const size_t f = backward ? bsp::win::kv_slot_floats(rows) : bsp::win::slot_floats(rows);
     return round_up(f * sizeof(float) * 2 * bsp::sm_count());
+}
+
+size_t range_bytes(int Z, int Hkv) { return round_up((size_t)Z * Hkv * bsp::win::kRangeParts * sizeof(bsp::win::RangePart)); }
+size_t factor_bytes(int Z, int Hkv) { return round_up((size_t)Z * Hkv * sizeof(bsp::win::DsFactor)); }
+// of each tile's rows (more than the one float per row that the CUDA-core kernels
+// keep)
+size_t stats_bytes(int Z, int Hq, int Hkv, int Sq) {
+    const size_t rows = bsp::win::kStatRows, tq = rows / (Hq / Hkv);
+    return round_up((size_t)Z * Hkv * ((Sq + tq - 1) / tq) * bsp::win::kStatTile * sizeof(float));
 }
 
 void set_rule(const bsp_window_s* w, Prob* p) {
@@ -185,10 +194,7 @@ extern "C" int bsp_window_status(bsp_window_t w, void* stream) {
 extern "C" size_t bsp_window_attention_workspace(int Z, int Hq, int Hkv, int Sq, int backward) {
     if (Z < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv || Hq / Hkv > kMaxGroup || Sq < 0) return 0;
     size_t n = cuts_bytes() + slots_bytes(backward != 0);
-    // two floats per row of each tile (more than the one per row that the
-    // CUDA-core kernels keep)
-    const size_t rows = bsp::win::kStatRows, tq = rows / (Hq / Hkv);
-    if (backward) n += round_up((size_t)Z * Hkv * ((Sq + tq - 1) / tq) * 2 * rows * sizeof(float));
+    if (backward) n += range_bytes(Z, Hkv) + factor_bytes(Z, Hkv) + stats_bytes(Z, Hq, Hkv, Sq);
     return n;
 }
 
@@ -282,7 +288,10 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
     char* ws = static_cast<char*>(workspace);
     c.cuts = reinterpret_cast<bsp::win::Cut*>(ws);
     c.slots = reinterpret_cast<float*>(ws + cuts_bytes());
-    c.stats = reinterpret_cast<float*>(ws + cuts_bytes() + slots_bytes(true));
+    ws += cuts_bytes() + slots_bytes(true);
+    c.range = reinterpret_cast<bsp::win::RangePart*>(ws);
+    c.factor = reinterpret_cast<bsp::win::DsFactor*>(ws + range_bytes(Z, Hkv));
+    c.stats = reinterpret_cast<float*>(ws + range_bytes(Z, Hkv) + factor_bytes(Z, Hkv));
     c.stream = s;
     if (!force_simt()) {
         rc = bsp::win::launch_backward_tc(c);

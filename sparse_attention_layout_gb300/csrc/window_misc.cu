@@ -1,6 +1,8 @@
 // Small kernels around the windowed attention: joining the pieces of cut
 // tiles, the rows' dO . O, and the append of new tokens' keys and values to
 // the pages.
+#include <type_traits>
+
 #include "common.cuh"
 #include "window.h"
 
@@ -230,44 +232,122 @@ __global__ void __launch_bounds__(256) delta_kernel(const View O, const View dO,
     }
 }
 
-// The same per tile of kStatRows rows (row r: token r / G, head r % G, as the
-// tensor-core kernels lay them out): tile i's values of -lse log2(e), then of
-// dO . O, so that one bulk copy brings a tile's statistics.  Rows beyond the
-// sequence and rows that see nothing get -inf: their P is then 0.
-template <typename T>
-__global__ void __launch_bounds__(256) tile_stats_kernel(const View O, const View dO, const float* lse,
-                                                         const RowStrides at, float* stats, int64_t rows, int ntiles,
-                                                         int G, int TQ, int Hkv, int S, int D) {
-    constexpr int N = Vec16<T>::N;
-    const int sub = threadIdx.x & 7;
-    cudaGridDependencySynchronize();
-    for (int64_t i = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); i < rows; i += (int64_t)gridDim.x * 32) {
-        const int r = (int)(i % kStatRows);
-        const int64_t tile = i / kStatRows, zh = tile / ntiles;
-        const int z = (int)(zh / Hkv), t = (int)(tile % ntiles) * TQ + r / G;
-        const int64_t h = zh % Hkv * G + r % G;
-        const bool live = r < TQ * G && t < S;
-        float x = 0.f;
-        if (live) {
-            const T* o = static_cast<const T*>(O.ptr) + z * O.s[0] + h * O.s[1] + t * O.s[2];
-            const T* g = static_cast<const T*>(dO.ptr) + z * dO.s[0] + h * dO.s[1] + t * dO.s[2];
-            for (int c = sub * N; c < D; c += 8 * N) {
-                float a[N], b[N];
-                Vec16<T>::load(o + c, a);
-                Vec16<T>::load(g + c, b);
+// Largest of x over the block's threads, in thread 0; scratch: 8 floats.
+__device__ __forceinline__ float block_most(float x, float* scratch) {
 #pragma unroll
-                for (int k = 0; k < N; ++k) x = fmaf(a[k], b[k], x);
+    for (int k = 16; k; k >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, k));
+    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = x;
+    __syncthreads();
+    for (int k = 1; k < 8; ++k) x = fmaxf(x, scratch[k]);
+    return x;
+}
+
+struct StatsArgs {
+    View O, dO, V;
+    const float* lse;
+    RowStrides at;
+    float* stats;
+    RangePart* range;  // fp16
+    int parts;         // fp16: blocks per (batch entry, KV head); else all
+    int64_t rows;      // of each, in whole tiles; else all
+    int ntiles, G, TQ, Hkv, S, D;
+    int Sk, zlo, sinks;  // fp16: V rows below min(sinks, zlo) and from zlo on are seen
+};
+
+// dO . O per tile of kStatRows rows (row r: token r / G, head r % G, as the
+// tensor-core kernels lay them out), and -lse log2(e), side by side, so that one
+// bulk copy brings a tile's statistics.  Rows beyond the sequence get -inf: their
+// P is then 0.  fp16 also looks for the longest rows of dO and V of each (batch
+// entry, KV head); V rows that no query sees are left out, rows of no finite
+// length too, since neither may move the factor of the others.
+template <typename T>
+__global__ void __launch_bounds__(256) tile_stats_kernel(const __grid_constant__ StatsArgs a) {
+    constexpr int N = Vec16<T>::N;
+    constexpr bool kF16 = std::is_same<T, __half>::value;
+    const int sub = threadIdx.x & 7;
+    const unsigned group = 0xffu << (threadIdx.x & 24);  // the row's 8 lanes
+    const int rep = kF16 ? blockIdx.x / a.parts : 0, part = kF16 ? blockIdx.x % a.parts : blockIdx.x;
+    float o2 = 0.f;
+    cudaGridDependencySynchronize();
+    for (int64_t j = (int64_t)part * 32 + (threadIdx.x >> 3); j < a.rows; j += (int64_t)a.parts * 32) {
+        const int64_t i = rep * a.rows + j;
+        const int r = (int)(i % kStatRows);
+        const int64_t tile = i / kStatRows, zh = tile / a.ntiles;
+        const int z = (int)(zh / a.Hkv), t = (int)(tile % a.ntiles) * a.TQ + r / a.G;
+        const int64_t h = zh % a.Hkv * a.G + r % a.G;
+        const bool live = r < a.TQ * a.G && t < a.S;
+        float x = 0.f, y = 0.f;
+        if (live) {
+            const T* o = static_cast<const T*>(a.O.ptr) + z * a.O.s[0] + h * a.O.s[1] + t * a.O.s[2];
+            const T* g = static_cast<const T*>(a.dO.ptr) + z * a.dO.s[0] + h * a.dO.s[1] + t * a.dO.s[2];
+            for (int c = sub * N; c < a.D; c += 8 * N) {
+                float u[N], v[N];
+                Vec16<T>::load(o + c, u);
+                Vec16<T>::load(g + c, v);
+#pragma unroll
+                for (int k = 0; k < N; ++k) {
+                    x = fmaf(u[k], v[k], x);
+                    if (kF16) y = fmaf(v[k], v[k], y);
+                }
             }
         }
-        const unsigned group = 0xffu << (threadIdx.x & 24);  // the row's 8 lanes
 #pragma unroll
-        for (int k = 4; k; k >>= 1) x += __shfl_xor_sync(group, x, k);
+        for (int k = 4; k; k >>= 1) {
+            x += __shfl_xor_sync(group, x, k);
+            if (kF16) y += __shfl_xor_sync(group, y, k);
+        }
+        if (y < INFINITY) o2 = fmaxf(o2, y);
         if (sub == 0) {
-            const float l = live ? lse[z * at.z + h * at.h + t * at.t] : -INFINITY;
-            stats[tile * 2 * kStatRows + r] = l == -INFINITY ? -INFINITY : -l * kLog2e;
-            stats[tile * 2 * kStatRows + kStatRows + r] = x;
+            const float l = live ? a.lse[z * a.at.z + h * a.at.h + t * a.at.t] : -INFINITY;
+            float* s = a.stats + tile * kStatTile + r;
+            if (kF16) s[kStatDot] = x;
+            s[kStatLse] = l == -INFINITY ? -INFINITY : -l * kLog2e + (kF16 ? (float)kPUp : 0.f);
+            s[kStatDelta] = kF16 ? 0.f : x;
         }
     }
+    if constexpr (kF16) {
+        float v2 = 0.f;
+        const int z = rep / a.Hkv, hk = rep % a.Hkv, head = imin(a.sinks, a.zlo);
+        for (int64_t j = (int64_t)part * 32 + (threadIdx.x >> 3); j < (int64_t)head + a.Sk - a.zlo; j += (int64_t)a.parts * 32) {
+            const int64_t t = j < head ? j : j - head + a.zlo;
+            const T* v = static_cast<const T*>(a.V.ptr) + z * a.V.s[0] + hk * a.V.s[1] + t * a.V.s[2];
+            float y = 0.f;
+            for (int c = sub * N; c < a.D; c += 8 * N) {
+                float u[N];
+                Vec16<T>::load(v + c, u);
+#pragma unroll
+                for (int k = 0; k < N; ++k) y = fmaf(u[k], u[k], y);
+            }
+#pragma unroll
+            for (int k = 4; k; k >>= 1) y += __shfl_xor_sync(group, y, k);
+            if (y < INFINITY) v2 = fmaxf(v2, y);
+        }
+        __shared__ float most[2][8];
+        o2 = block_most(o2, most[0]);
+        v2 = block_most(v2, most[1]);
+        if (threadIdx.x == 0) a.range[blockIdx.x] = RangePart{o2, v2};
+    }
+}
+
+// What the fp16 gradient scales dS by: a warp per (batch entry, KV head).
+__global__ void __launch_bounds__(256) factor_kernel(const RangePart* range, int parts, DsFactor* factor, int rep) {
+    const int lane = threadIdx.x & 31, r = blockIdx.x * 8 + (threadIdx.x >> 5);
+    cudaGridDependencySynchronize();
+    if (r >= rep) return;
+    float o2 = 0.f, v2 = 0.f;
+    for (int i = lane; i < parts; i += 32) {
+        const RangePart x = range[(int64_t)r * parts + i];
+        o2 = fmaxf(o2, x.dO2), v2 = fmaxf(v2, x.V2);
+    }
+#pragma unroll
+    for (int k = 16; k; k >>= 1) {
+        o2 = fmaxf(o2, __shfl_xor_sync(0xffffffffu, o2, k));
+        v2 = fmaxf(v2, __shfl_xor_sync(0xffffffffu, v2, k));
+    }
+    const float most = 2.0f * sqrtf(o2) * sqrtf(v2);  // of |dP - delta|
+    // most < 2^(e + 1): times 2^(14 - e) below 2^15
+    const int e = most > 0.f ? ilogbf(most) : 14;
+    if (lane == 0) factor[r] = DsFactor{scalbnf(1.0f, 14 - kPUp - e), scalbnf(1.0f, e - 14)};
 }
 
 // K and V rows of new tokens to their pages' slots: token t of sequence s goes
@@ -368,11 +448,29 @@ int delta_t(const Call& c) {
 
 template <typename T>
 int tile_stats_t(const Call& c) {
-    const int tq = kStatRows / c.p.G, ntiles = (c.p.Sq + tq - 1) / tq;
-    const int64_t rows = (int64_t)c.Z * c.p.Hkv * ntiles * kStatRows;
-    const int64_t blocks = (rows + 31) / 32, most = (int64_t)sm_count() * 16;
-    return launch_behind(tile_stats_kernel<T>, dim3((int)(blocks < most ? blocks : most)), 256, 0, c.stream, c.O, c.dO,
-                         (const float*)c.lse, RowStrides{c.lz, c.lh, c.lt}, c.stats, rows, ntiles, c.p.G, tq, c.p.Hkv, c.p.Sq, c.D);
+    constexpr bool kF16 = std::is_same<T, __half>::value;
+    const Prob& p = c.p;
+    const int tq = kStatRows / p.G, ntiles = (p.Sq + tq - 1) / tq;
+    const int64_t per = (int64_t)ntiles * kStatRows, most = (int64_t)sm_count() * 16;
+    const int64_t rows = kF16 ? per : per * p.rep;  // of a part's share
+    int64_t parts = (rows + 31) / 32;
+    if (kF16) {
+        // enough blocks to fill the GPU; V may have many more rows than Q
+        parts = p.Sk / 32 > parts ? p.Sk / 32 : parts;
+        const int64_t fill = (most + p.rep - 1) / p.rep;
+        parts = parts < fill ? parts : fill;
+        parts = parts < kRangeParts ? parts : kRangeParts;
+    } else {
+        parts = parts < most ? parts : most;
+    }
+    const StatsArgs a{c.O, c.dO, c.V, c.lse, RowStrides{c.lz, c.lh, c.lt}, c.stats, c.range, (int)parts, rows, ntiles,
+                      p.G, tq, p.Hkv, p.Sq, c.D, p.Sk, window_low(p.Sk - p.Sq, p.window), p.sinks};
+    const int64_t grid = kF16 ? parts * p.rep : parts;
+    int rc = launch_behind(tile_stats_kernel<T>, dim3((uint32_t)grid), 256, 0, c.stream, a);
+    if (kF16 && !rc)
+        rc = launch_behind(factor_kernel, dim3((p.rep + 7) / 8), 256, 0, c.stream, (const RangePart*)c.range, (int)parts,
+                           c.factor, p.rep);
+    return rc;
 }
 
 View in_16(const View& v, int elt) {

@@ -705,3 +705,42 @@ def test_gradient_without_the_keys_that_nobody_sees(bsp, path, shape, dtype):
             assert all(torch.equal(a, b) for a, b in zip(got, want)), value
             assert bool((got[3][:, :, unseen] == 0).all()) and bool((got[4][:, :, unseen] == 0).all())
     assert bsp.bsp_window_status(W) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("size", [1e-4, 1e-3, 1.0])
+def test_gradient_of_a_small_output_gradient(bsp, path, dtype, size):
+    """dS over 6000 keys is 1e-4 of dO and below 16 bits' range where dO is
+    small; dQ, dK and dV are in it.  Their norms are off by at most 4 u: one
+    rounding each of P or dS, of the O in delta, and of the result, which are
+    independent and so add up as the terms themselves do, and the fp32 sums; and
+    by the rounding of subnormal results."""
+    dt = DT[dtype]
+    Q = randn((1, 4, 200, 64), dt, 130) * 0.08
+    K = randn((1, 2, 6000, 64), dt, 131) * 0.08
+    V = randn((1, 2, 6000, 64), dt, 132)
+    dO = (randn((1, 4, 200, 64), torch.float32, 133) * size).to(dt)
+    W = bsp.bsp_window_create()
+    got = _gradients(bsp, W, Q, K, V, dO, 16.0)[2:]
+    r = ref.dense(Q, K, V, 16.0, 0, 0, dO)
+    for name, g in zip(("dQ", "dK", "dV"), got):
+        check(g, r[name], r["e" + name[-1]], name)
+        off = (g.double() - r[name]).norm().item()
+        assert off <= 4 * ref.U[dt] * r[name].norm().item() + ref.AB[dt] * math.sqrt(g.numel()), name
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_gradient_of_a_large_output_gradient(bsp, path, dtype):
+    """dS beyond 65504 with gradients that are far below it."""
+    dt = DT[dtype]
+    Q, K = (randn((1, H, 5, 64), dt, 140 + H) for H in (4, 2))
+    V = randn((1, 2, 5, 64), dt, 142) * 16
+    dO = randn((1, 4, 5, 64), dt, 143) * 4000
+    W = bsp.bsp_window_create(0, 0)
+    got = _gradients(bsp, W, Q, K, V, dO, 0.01)[2:]
+    r = ref.dense(Q, K, V, 0.01, 0, 0, dO)
+    for name, g in zip(("dQ", "dK", "dV"), got):
+        assert r[name].abs().max().item() < 40000
+        check(g, r[name], r["e" + name[-1]], name)
+        off = (g.double() - r[name]).norm().item()
+        assert off <= 4 * ref.U[dt] * r[name].norm().item(), name
