@@ -595,6 +595,11 @@ int bsp_diag_attention_split(bsp_layout_t layout, int max_steps);
  * from the pages: the robustness checks of this implementation. */
 int bsp_diag_wait_limit(bsp_layout_t layout, uint64_t wait_ns, int inject);
 
+/* Which kernels the handle's last attention or gradient call chose: 1 tensor
+ * cores (bf16 and fp16), 2 CUDA cores (fp32, or every type with BSP_FORCE_SIMT=1
+ * in the environment), 0 none yet.  The type alone decides. */
+int bsp_diag_window_family(bsp_window_t w);
+
 /* Evaluate ON THE HOST the key tiles that the windowed attention kernels visit
  * for a tile of query rows at positions a .. b (b - a < 128): into HOST int
  * tiles [cap] the key tiles of 1 << shift keys in order, *n their number

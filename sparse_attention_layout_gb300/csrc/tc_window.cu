@@ -640,7 +640,6 @@ int by_mode(Call& c) {
 }  // namespace
 
 int launch_forward_tc(Call& c) {
-    if (c.dtype == BSP_F32) return BSP_ERR_UNSUPPORTED;
     // one new token per sequence (as far as the host can know): a tile is one
     // token's heads, and its copies are no wider (64 such tokens 180 us, with
     // 128-row tiles 185; one over 1000 keys 13.1 and 16.2); else as many tokens

@@ -260,8 +260,9 @@ inline int key_map(CUtensorMap* m, const View& v, const Call& c, int is_bf16, in
 }
 
 // Launch preparation: the shared memory limit, and the register count that the
-// split at kernel start divides.  Both belong to the kernel on a device, so one
-// launch per device asks.
+// split at kernel start divides: with any other the split would wait forever, so
+// a library built that way gets an error.  Both belong to the kernel on a device,
+// so one launch per device asks.
 template <typename K>
 int prepare_kernel(K kern, int smem, std::atomic<uint64_t>& done) {
     int dev = 0;
@@ -271,7 +272,7 @@ int prepare_kernel(K kern, int smem, std::atomic<uint64_t>& done) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) return BSP_ERR_CUDA;
     cudaFuncAttributes fa;
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess) return BSP_ERR_CUDA;
-    if ((uint32_t)fa.numRegs != kRegsLaunch) return BSP_ERR_UNSUPPORTED;
+    if ((uint32_t)fa.numRegs != kRegsLaunch) return BSP_ERR_CUDA;
     done.fetch_or(bit, std::memory_order_release);
     return BSP_OK;
 }

@@ -841,7 +841,6 @@ int launch(Call& c) {
 }  // namespace
 
 int launch_backward_tc(Call& c) {
-    if (c.dtype == BSP_F32) return BSP_ERR_UNSUPPORTED;
     c.p.kshift = 7;
     c.p.TQ = kTcRows / c.p.G;
     if (c.dtype == BSP_BF16) return c.D <= 64 ? launch<__nv_bfloat16, 64>(c) : launch<__nv_bfloat16, 128>(c);

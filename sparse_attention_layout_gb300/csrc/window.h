@@ -1,6 +1,8 @@
 // Host-side declarations of the windowed attention operators.
 #pragma once
 
+#include <atomic>
+
 #include "bsp_internal.h"
 #include "window.cuh"
 
@@ -17,6 +19,7 @@ struct bsp_window_s {
     int device = -1;
     int* status = nullptr;      // device status word
     bsp::win::Plans* plans = nullptr;
+    std::atomic<int> family{0};  // kernels of the last call: 1 tensor cores, 2 CUDA cores
 };
 
 namespace bsp {
@@ -114,7 +117,7 @@ constexpr int kStatDot = 0, kStatLse = kStatRows, kStatDelta = 2 * kStatRows, kS
 
 int launch_forward_simt(Call& c);
 int launch_backward_simt(Call& c);
-int launch_forward_tc(Call& c);   // BSP_ERR_UNSUPPORTED: not a 16-bit type
+int launch_forward_tc(Call& c);  // 16-bit types
 int launch_backward_tc(Call& c);
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
                   const Prob& p, int D, cudaStream_t s);

@@ -26,6 +26,14 @@ bool force_simt() {
     return e && e[0] == '1';
 }
 
+// The type alone decides the kernels: whatever keeps the tensor-core ones from
+// running is an error, not a reason to take 15 to 37 times as long.
+bool on_tensor_cores(bsp_window_t w, int dtype) {
+    const bool tc = dtype != BSP_F32 && !force_simt();
+    w->family = tc ? 1 : 2;
+    return tc;
+}
+
 int check_handle(bsp_window_t w, int dtype) {
     if (!w || !valid_dtype(dtype)) return BSP_ERR_INVALID_ARG;
     int dev = -1;
@@ -229,11 +237,7 @@ extern "C" int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_
     c.cuts = static_cast<bsp::win::Cut*>(workspace);
     c.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + cuts_bytes());
     c.stream = (cudaStream_t)stream;
-    if (!force_simt()) {
-        rc = bsp::win::launch_forward_tc(c);
-        if (rc != BSP_ERR_UNSUPPORTED) return rc;
-    }
-    return bsp::win::launch_forward_simt(c);
+    return on_tensor_cores(w, dtype) ? bsp::win::launch_forward_tc(c) : bsp::win::launch_forward_simt(c);
 }
 
 extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K,
@@ -293,11 +297,7 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
     c.factor = reinterpret_cast<bsp::win::DsFactor*>(ws + range_bytes(Z, Hkv));
     c.stats = reinterpret_cast<float*>(ws + range_bytes(Z, Hkv) + factor_bytes(Z, Hkv));
     c.stream = s;
-    if (!force_simt()) {
-        rc = bsp::win::launch_backward_tc(c);
-        if (rc != BSP_ERR_UNSUPPORTED) return rc;
-    }
-    return bsp::win::launch_backward_simt(c);
+    return on_tensor_cores(w, dtype) ? bsp::win::launch_backward_tc(c) : bsp::win::launch_backward_simt(c);
 }
 
 namespace {
@@ -373,12 +373,10 @@ extern "C" int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t
     c.cuts = static_cast<bsp::win::Cut*>(workspace);
     c.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + cuts_bytes());
     c.stream = (cudaStream_t)stream;
-    if (!force_simt()) {
-        rc = bsp::win::launch_forward_tc(c);
-        if (rc != BSP_ERR_UNSUPPORTED) return rc;
-    }
-    return bsp::win::launch_forward_simt(c);
+    return on_tensor_cores(w, dtype) ? bsp::win::launch_forward_tc(c) : bsp::win::launch_forward_simt(c);
 }
+
+extern "C" int bsp_diag_window_family(bsp_window_t w) { return w ? w->family.load() : BSP_ERR_INVALID_ARG; }
 
 extern "C" int bsp_diag_window_tiles(int window, int sinks, int a, int b, int shift, int* n, int* tiles, int cap) {
     if (window < 0 || sinks < 0 || b < a || b - a >= 128 || shift < 4 || shift > 7 || !n || cap < 0 || (cap && !tiles))

@@ -744,3 +744,22 @@ def test_gradient_of_a_large_output_gradient(bsp, path, dtype):
         check(g, r[name], r["e" + name[-1]], name)
         off = (g.double() - r[name]).norm().item()
         assert off <= 4 * ref.U[dt] * r[name].norm().item(), name
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("D", [16, 48, 64, 80, 128])
+def test_the_type_decides_the_kernels(bsp, path, D, dtype):
+    """Both widths of every kernel of a family; nothing falls to the other."""
+    W = bsp.bsp_window_create(60, 2)
+    assert bsp.bsp_diag_window_family(W) == "none"
+    want = "tensor cores" if path == "tc" and dtype != "f32" else "CUDA cores"
+    Q, K, V, dO = (randn((2, H, 150, D), DT[dtype], 150 + i, "rows") for i, H in enumerate((6, 2, 2, 6)))
+    O, lse = bsp.bsp_window_attention(W, Q, K, V, scale=0.1)
+    assert bsp.bsp_diag_window_family(W) == want
+    bsp.bsp_window_attention_backward(W, Q, K, V, O, dO, lse, scale=0.1)
+    assert bsp.bsp_diag_window_family(W) == want
+    for new in ([1, 1], [30, 2], [1] * 3 + [0] * 600):  # plain and ragged splits
+        P = bsp.bsp_window_create(60, 2)
+        b = Paged(new, [50 + n for n in new], 6, 2, D, 32, DT[dtype], 155)
+        b.check(*b.attend(bsp, P, scale=0.1), 0.1, 60, 2)
+        assert bsp.bsp_diag_window_family(P) == want and bsp.bsp_window_status(P) == 0

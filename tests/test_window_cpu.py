@@ -96,3 +96,7 @@ def test_refusals_without_a_handle(lib):
     assert lib.bsp_diag_window_tiles(0, 0, 5, 4, 7, ctypes.byref(n), None, 0) == -1
     assert lib.bsp_diag_window_tiles(0, 0, 0, 4, 9, ctypes.byref(n), None, 0) == -1
     assert lib.bsp_diag_window_queries(0, 0, 4, 4, 1, 7, 1, ctypes.byref(n), ctypes.byref(n)) == -1
+
+
+def test_family_without_a_handle(lib):
+    assert lib.bsp_diag_window_family(None) == -1
