@@ -34,7 +34,9 @@
  *    tables that lies outside the layout in the fused attention kernel) skip
  *    the access, record a code in the handle's device status word, wait for
  *    their own copies and products in flight and return; bsp_status_check
- *    reads it (bsp_diag_wait_limit provokes both on purpose).
+ *    reads it (bsp_diag_wait_limit provokes both on purpose).  The windowed
+ *    operators have a status word and limits of their own (bsp_window_status,
+ *    bsp_diag_window_wait_limit).
  *  - The handle is immutable after compilation and may be used concurrently
  *    from several streams of the device it was compiled on.
  */
@@ -594,6 +596,16 @@ int bsp_diag_attention_split(bsp_layout_t layout, int max_steps);
  * restores normal operation.  Other inject bits: BSP_ERR_INVALID_ARG.  Not
  * from the pages: the robustness checks of this implementation. */
 int bsp_diag_wait_limit(bsp_layout_t layout, uint64_t wait_ns, int inject);
+
+/* Set how long the tensor-core kernels of this handle's calls wait for a tile
+ * from now on, in attempts of about 1.4 us; 0 restores the default,
+ * bsp_diag_window_attempts(steps of the longest tile): 2^21, the limit of every
+ * other wait, and 128 for each step, at most 2^31 - 1.  A limit below what a tile
+ * takes makes the wait run out: every role stops, waits for the copies and matrix
+ * products it had already issued, frees its tensor memory and returns; the
+ * outputs are then undefined and bsp_window_status reports BSP_ERR_TIMEOUT. */
+int bsp_diag_window_wait_limit(bsp_window_t w, int attempts);
+int bsp_diag_window_attempts(int64_t steps);
 
 /* Which kernels the handle's last attention or gradient call chose: 1 tensor
  * cores (bf16 and fp16), 2 CUDA cores (fp32, or every type with BSP_FORCE_SIMT=1

@@ -96,12 +96,14 @@ def lib():
         L.bsp_paged_attention_workspace.argtypes = []
         L.bsp_paged_attention_workspace.restype = sz
         L.bsp_diag_window_family.argtypes = [P]
+        L.bsp_diag_window_wait_limit.argtypes = [P, i32]
+        L.bsp_diag_window_attempts.argtypes = [ctypes.c_int64]
         L.bsp_diag_window_tiles.argtypes = [i32] * 5 + [P, P, i32]
         L.bsp_diag_window_queries.argtypes = [i32] * 7 + [P, P]
         for name in ("bsp_window_create", "bsp_window_destroy", "bsp_window_info", "bsp_window_status",
                      "bsp_window_attention", "bsp_window_attention_backward", "bsp_paged_append",
-                     "bsp_paged_attention", "bsp_diag_window_family", "bsp_diag_window_tiles",
-                     "bsp_diag_window_queries"):
+                     "bsp_paged_attention", "bsp_diag_window_family", "bsp_diag_window_wait_limit",
+                     "bsp_diag_window_attempts", "bsp_diag_window_tiles", "bsp_diag_window_queries"):
             getattr(L, name).restype = i32
         for name in ("bsp_layout_plan", "bsp_layout_compile", "bsp_layout_compile_device", "bsp_layout_destroy",
                      "bsp_layout_info",
@@ -556,6 +558,12 @@ def bsp_window_create(window: int = 0, sinks: int = 0, stream=None) -> Window:
 
 def bsp_window_status(W: Window, stream=None) -> int:
     return int(lib().bsp_window_status(W.handle, _stream(stream)))
+
+
+def bsp_diag_window_wait_limit(W: Window, attempts: int = 0):
+    """Limit of the tensor-core kernels' waits, in attempts of about 1.4 us (0:
+    the default), to see what a wait that runs out does."""
+    _check(lib().bsp_diag_window_wait_limit(W.handle, int(attempts)), "bsp_diag_window_wait_limit")
 
 
 def bsp_diag_window_family(W: Window) -> str:

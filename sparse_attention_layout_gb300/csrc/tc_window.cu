@@ -375,7 +375,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         while (ring.take(tc, w, lane == 0, true, ab)) {
             const int rows = w.nt * p.G, hk = w.hk, z = w.z, t0 = w.row0;
             const uint32_t lb = tc & 1;
-            bool ok = wait(&l_full[lb], (tc >> 1) & 1, ab);
+            bool ok = wait(&l_full[lb], (tc >> 1) & 1, ab, p.attempts);
             if (!__all_sync(0xffffffffu, ok)) break;
             const float m0 = lref[lb][0][row], m1 = lref[lb][1][row];
             const float l0 = lsum[lb][0][row], l1 = lsum[lb][1][row];
@@ -592,6 +592,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
             drain_ring(v_full, NST, issued[2]);
             if (issued[3]) drain_wait(&s_full[(issued[3] - 1) % 3], ((issued[3] - 1) / 3) & 1);
             if (issued[4]) drain_wait(&pv_done[(issued[4] - 1) % 3], ((issued[4] - 1) / 3) & 1);
+            drain_end();
         }
         __syncthreads();
     }
@@ -646,6 +647,8 @@ int launch_forward_tc(Call& c) {
     // as fill 128 rows
     c.p.kshift = 7;
     c.p.TQ = c.p.paged && c.p.T <= c.p.nseg ? 1 : kTcRows / c.p.G;
+    const int64_t keys = c.p.paged ? (int64_t)c.p.max_pages << c.p.page_shift : c.p.Sk;
+    c.p.attempts = wait_attempts(c, (keys >> 7) + 2);
     return c.dtype == BSP_BF16 ? by_mode<__nv_bfloat16>(c) : by_mode<__half>(c);
 }
 

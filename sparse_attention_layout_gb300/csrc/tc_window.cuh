@@ -31,21 +31,26 @@ struct Stop {
     volatile int* flag;
     __device__ __forceinline__ void fail(int code) const { *flag = code; }
 };
-// attempts of a wait: each is a bounded suspension of at least tens of cycles,
-// and no legal wait is longer than a step of another role (microseconds)
-constexpr int kAttempts = 1 << 22;
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Stop& ab) {
-    for (int n = kAttempts; !mbar_try_wait(bar, parity);) {
+// Attempts: a constant where a wait lasts about a step of another role (held in a
+// register or read from the parameters there, the forward took 2 % longer), the
+// call's own for an epilogue's wait for its tile, the only one that lasts as long
+// as the tile's steps.
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, const Stop& ab, int attempts = kLeastAttempts) {
+    for (int n = attempts; !mbar_try_wait(bar, parity);) {
         if (*ab.flag) return false;
         if (--n == 0) ab.fail(BSP_ERR_TIMEOUT);
     }
     return true;
 }
 // After an abort, by one thread: wait, bounded, for the phase of `bar` with the
-// given parity, whatever the flag says.
+// given parity, whatever the flag says: copies and products in flight end by
+// themselves.
 __device__ __forceinline__ void drain_wait(uint64_t* bar, uint32_t parity) {
-    for (int n = kAttempts; !mbar_try_wait(bar, parity) && --n;) {}
+    for (int n = kLeastAttempts; !mbar_try_wait(bar, parity) && --n;) {}
 }
+// The arrivals of commits that no role waits for any more follow the drained
+// ones at once; the CTA's shared memory outlasts them.
+__device__ __forceinline__ void drain_end() { __nanosleep(10000); }
 // The same for a ring of nst stages whose phases 0 .. next - 1 were begun.
 __device__ __forceinline__ void drain_ring(uint64_t* bars, uint32_t nst, uint32_t next) {
 #pragma unroll 1

@@ -303,7 +303,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
         Work w;
         while (ring.take(tiles, w, lane == 0, true, ab)) {
             const int rows = w.nt * p.G, hk = w.hk, z = w.z;
-            const bool ok = wait(&acc_full, tiles & 1, ab);
+            const bool ok = wait(&acc_full, tiles & 1, ab, p.attempts);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             ++tiles;
@@ -413,6 +413,7 @@ dq_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CU
             if (issued[2]) drain_wait(&s_full[(issued[2] - 1) & 1], ((issued[2] - 1) >> 1) & 1);
             if (issued[4]) drain_wait(&dp_full, (issued[4] - 1) & 1);
             if (issued[3]) drain_wait(&dq_done[(issued[3] - 1) & 1], ((issued[3] - 1) >> 1) & 1);
+            drain_end();
         }
         __syncthreads();
     }
@@ -675,12 +676,12 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
                 const int end = p.Sk - kb - quad * 32;
                 return [=](int i) -> T* { return i < end ? out + i * row_stride : nullptr; };
             };
-            bool ok = wait(&dv_full, tiles & 1, ab);
+            bool ok = wait(&dv_full, tiles & 1, ab, p.attempts);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             drain<T, DP>(tV + lane_base, &dv_empty, lane, row, kTcRows, slot ? slot + (size_t)kTcRows * kSlotD : nullptr,
                          1.0f, 1.0f / (1 << kPUp), args.D, stage, rows_of(args.dV));
-            ok = wait(&dk_full, tiles & 1, ab);
+            ok = wait(&dk_full, tiles & 1, ab, p.attempts);
             if (!__all_sync(0xffffffffu, ok)) break;
             tc_fence_after();
             const float down = kBf ? 1.0f : args.factor[w.rep].down;
@@ -796,6 +797,7 @@ dkv_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ C
             drain_ring(dp_full, 2, issued[3]);
             drain_ring(dv_done, 2, issued[4]);
             drain_ring(dk_done, 4, issued_k);
+            drain_end();
         }
         __syncthreads();
     }
@@ -843,6 +845,9 @@ int launch(Call& c) {
 int launch_backward_tc(Call& c) {
     c.p.kshift = 7;
     c.p.TQ = kTcRows / c.p.G;
+    // a tile's steps: key tiles, or half tiles of query rows
+    const int64_t keys = c.p.Sk >> 7, rows = c.p.Sq / (kStatRows / c.p.G);
+    c.p.attempts = wait_attempts(c, (keys > rows ? keys : rows) + 2);
     if (c.dtype == BSP_BF16) return c.D <= 64 ? launch<__nv_bfloat16, 64>(c) : launch<__nv_bfloat16, 128>(c);
     return c.D <= 64 ? launch<__half, 64>(c) : launch<__half, 128>(c);
 }

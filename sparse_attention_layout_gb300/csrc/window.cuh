@@ -44,6 +44,17 @@ constexpr int kMaxLen = 1 << 30;
 constexpr int kMaxGroup = 64;      // query heads per KV head
 constexpr int kMaxSeqs = 16384;    // sequences of one ragged call (their tile counts sit in shared memory)
 
+// Attempts of a bounded wait of the tensor-core kernels.  A failed one takes 1.4
+// us (measured: 20 in 27.6 us), and tens of cycles at the least: 2^21 are 3 s, and
+// 40 ms at the least, for waits that last about a step of another role.  An
+// epilogue waits for its whole tile, some microseconds for each of its steps: 128
+// attempts more for each, enough even at the least.
+constexpr int kLeastAttempts = 1 << 21;
+inline int wait_attempts(int64_t steps) {
+    const int64_t n = kLeastAttempts + 128 * steps;
+    return n > INT32_MAX ? INT32_MAX : (int)n;
+}
+
 // element (i, j, k, d) at ptr + i * s[0] + j * s[1] + k * s[2] + d
 struct View {
     void* ptr;
@@ -106,6 +117,7 @@ struct Prob {
     const int* kv_len;
     const int* table;
     int* status;
+    int attempts;   // of the wait for a tile (tensor-core kernels)
 
     BSP_HD bool bad_seg(int q0, int q1, int kv) const {
         return q0 < 0 || q1 < q0 || q1 > T || kv < 0 || kv > (max_pages << page_shift);

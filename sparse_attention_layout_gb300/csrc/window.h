@@ -19,6 +19,7 @@ struct bsp_window_s {
     int device = -1;
     int* status = nullptr;      // device status word
     bsp::win::Plans* plans = nullptr;
+    std::atomic<int> attempts{0};  // of the wait for a tile, 0: as many as the call's sizes ask for
     std::atomic<int> family{0};  // kernels of the last call: 1 tensor cores, 2 CUDA cores
 };
 
@@ -117,6 +118,10 @@ constexpr int kStatDot = 0, kStatLse = kStatRows, kStatDelta = 2 * kStatRows, kS
 
 int launch_forward_simt(Call& c);
 int launch_backward_simt(Call& c);
+inline int wait_attempts(const Call& c, int64_t steps) {
+    const int n = c.w->attempts.load();
+    return n ? n : wait_attempts(steps);
+}
 int launch_forward_tc(Call& c);  // 16-bit types
 int launch_backward_tc(Call& c);
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,

@@ -376,6 +376,14 @@ extern "C" int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t
     return on_tensor_cores(w, dtype) ? bsp::win::launch_forward_tc(c) : bsp::win::launch_forward_simt(c);
 }
 
+extern "C" int bsp_diag_window_wait_limit(bsp_window_t w, int attempts) {
+    if (!w || attempts < 0) return BSP_ERR_INVALID_ARG;
+    w->attempts = attempts;
+    return BSP_OK;
+}
+
+extern "C" int bsp_diag_window_attempts(int64_t steps) { return steps < 0 ? 0 : bsp::win::wait_attempts(steps); }
+
 extern "C" int bsp_diag_window_family(bsp_window_t w) { return w ? w->family.load() : BSP_ERR_INVALID_ARG; }
 
 extern "C" int bsp_diag_window_tiles(int window, int sinks, int a, int b, int shift, int* n, int* tiles, int cap) {

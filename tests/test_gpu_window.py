@@ -763,3 +763,37 @@ def test_the_type_decides_the_kernels(bsp, path, D, dtype):
         b = Paged(new, [50 + n for n in new], 6, 2, D, 32, DT[dtype], 155)
         b.check(*b.attend(bsp, P, scale=0.1), 0.1, 60, 2)
         assert bsp.bsp_diag_window_family(P) == want and bsp.bsp_window_status(P) == 0
+
+
+@pytest.mark.parametrize("limit", [1, 2, 3, 5])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("what", ["dense", "gradient", "plain", "ragged"])
+def test_a_wait_that_runs_out_is_reported(bsp, monkeypatch, what, D, limit):
+    """Tiles of 48 steps take tens of microseconds, the limits are 1.4 to 7: every
+    role stops, the call ends with its status, and the next one is right."""
+    import time
+    monkeypatch.delenv("BSP_FORCE_SIMT", raising=False)
+    W = bsp.bsp_window_create(0, 0)
+    if what in ("dense", "gradient"):
+        Q, K, V, dO = (randn((1, H, 6144, D), torch.bfloat16, 160 + i) for i, H in enumerate((4, 2, 2, 4)))
+        O, lse = bsp.bsp_window_attention(W, Q, K, V, scale=0.1)
+        if what == "dense":
+            run = lambda: bsp.bsp_window_attention(W, Q, K, V, scale=0.1)
+        else:
+            run = lambda: bsp.bsp_window_attention_backward(W, Q, K, V, O, dO, lse, scale=0.1)
+    else:
+        new = [1] * 150 if what == "plain" else [30, 1] * 75
+        b = Paged(new, [6144] * 150, 4, 2, D, 64, torch.bfloat16, 165)
+        run = lambda: b.attend(bsp, W, scale=0.1)
+    want = run()
+    assert bsp.bsp_window_status(W) == 0
+    bsp.bsp_diag_window_wait_limit(W, limit)
+    t0 = time.perf_counter()
+    run()
+    assert bsp.bsp_window_status(W) == -6
+    assert time.perf_counter() - t0 < 2.0
+    assert bsp.bsp_window_status(W) == 0
+    bsp.bsp_diag_window_wait_limit(W)
+    for _ in range(2):
+        assert all(torch.equal(a, c) for a, c in zip(run(), want))
+    assert bsp.bsp_window_status(W) == 0

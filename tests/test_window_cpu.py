@@ -100,3 +100,13 @@ def test_refusals_without_a_handle(lib):
 
 def test_family_without_a_handle(lib):
     assert lib.bsp_diag_window_family(None) == -1
+
+
+def test_wait_limits_grow_with_a_tile(lib):
+    """A legal wait takes up to a tile's steps, of about a microsecond; an attempt
+    takes tens of cycles (20 ns) at the least."""
+    for steps in (1, 16384, 28000, 1 << 20, 1 << 23):
+        n = lib.bsp_diag_window_attempts(steps)
+        assert n * 20e-9 >= 2 * steps * 1e-6 and n < 2 ** 31
+    assert lib.bsp_diag_window_attempts(1 << 40) == 2 ** 31 - 1
+    assert lib.bsp_diag_window_wait_limit(None, 1) == -1
