@@ -557,7 +557,9 @@ def bsp_window_create(window: int = 0, sinks: int = 0, stream=None) -> Window:
 
 
 def bsp_window_status(W: Window, stream=None) -> int:
-    return int(lib().bsp_window_status(W.handle, _stream(stream)))
+    """The status word of the calls on `stream` (the current one of W's device),
+    for which this waits, and clears it."""
+    return _status(W, stream=stream)
 
 
 def bsp_diag_window_wait_limit(W: Window, attempts: int = 0):
@@ -613,6 +615,11 @@ def _entry(f):
             return f(W, *args, stream=_raw_stream(dev), **kw)
 
     return functools.update_wrapper(call, f)
+
+
+@_entry
+def _status(W, *, stream):
+    return int(lib().bsp_window_status(W.handle, stream))
 
 
 def _same(W: Window, *ts):

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <mutex>
 
 #include "bsp_internal.h"
 #include "window.cuh"
@@ -17,7 +18,8 @@ struct Plans;
 struct bsp_window_s {
     int window = 0, sinks = 0;  // as given (window 0: no limit)
     int device = -1;
-    int* status = nullptr;      // device status word
+    int* status = nullptr;      // device status word, and where it is read from
+    std::mutex reading;
     bsp::win::Plans* plans = nullptr;
     std::atomic<int> attempts{0};  // of the wait for a tile, 0: as many as the call's sizes ask for
     std::atomic<int> family{0};  // kernels of the last call: 1 tensor cores, 2 CUDA cores
@@ -126,6 +128,8 @@ int launch_forward_tc(Call& c);  // 16-bit types
 int launch_backward_tc(Call& c);
 int launch_append(const bsp_window_s* w, int dtype, const View& Kn, const View& Vn, const View& Kc, const View& Vc,
                   const Prob& p, int D, cudaStream_t s);
+// the status word to its neighbour, and 0 in its place
+int launch_take_status(const bsp_window_s* w, cudaStream_t s);
 // zeros n0 x n1 x n2 rows of row16 16-byte pieces (elt: bytes of an element of v)
 int launch_zero(const View& v, int elt, int64_t n0, int64_t n1, int64_t n2, int row16, cudaStream_t s);
 // The split of a dense launch's query tiles (p) or key tiles (k) over `ctas`

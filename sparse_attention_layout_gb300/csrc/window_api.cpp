@@ -156,10 +156,10 @@ extern "C" int bsp_window_create(int window, int sinks, void* stream, bsp_window
     int rc = BSP_OK;
     if (cudaGetDevice(&w->device) != cudaSuccess) {
         rc = BSP_ERR_CUDA;
-    } else if (cudaMalloc(&w->status, sizeof(int)) != cudaSuccess) {
+    } else if (cudaMalloc(&w->status, 2 * sizeof(int)) != cudaSuccess) {
         (void)cudaGetLastError();
         rc = BSP_ERR_OOM;
-    } else if (cudaMemsetAsync(w->status, 0, sizeof(int), (cudaStream_t)stream) != cudaSuccess) {
+    } else if (cudaMemsetAsync(w->status, 0, 2 * sizeof(int), (cudaStream_t)stream) != cudaSuccess) {
         cudaFree(w->status);
         rc = BSP_ERR_CUDA;
     }
@@ -188,15 +188,16 @@ extern "C" int bsp_window_info(bsp_window_t w, int* window, int* sinks) {
 }
 
 extern "C" int bsp_window_status(bsp_window_t w, void* stream) {
-    if (!w) return BSP_ERR_INVALID_ARG;
-    if (cudaStreamSynchronize((cudaStream_t)stream) != cudaSuccess) return BSP_ERR_CUDA;
+    int rc = check_handle(w, BSP_F32);
+    if (rc) return rc;
+    // read and cleared in one step on the stream: what a call on another stream
+    // reports meanwhile stays for the next reader
+    std::lock_guard<std::mutex> lock(w->reading);
+    cudaStream_t s = (cudaStream_t)stream;
     int word = 0;
-    if (cudaMemcpy(&word, w->status, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess) return BSP_ERR_CUDA;
-    if (word != 0) {
-        const int zero = 0;
-        if (cudaMemcpy(w->status, &zero, sizeof(int), cudaMemcpyHostToDevice) != cudaSuccess) return BSP_ERR_CUDA;
-    }
-    return word;
+    if ((rc = bsp::win::launch_take_status(w, s))) return rc;
+    if (cudaMemcpyAsync(&word, w->status + 1, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess) return BSP_ERR_CUDA;
+    return cudaStreamSynchronize(s) == cudaSuccess ? word : BSP_ERR_CUDA;
 }
 
 extern "C" size_t bsp_window_attention_workspace(int Z, int Hq, int Hkv, int Sq, int backward) {

@@ -424,6 +424,8 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     }
 }
 
+__global__ void take_status_kernel(int* status) { status[1] = atomicExch(status, 0); }
+
 // zeros rows of row16 16-byte pieces of a strided tensor (strides in pieces)
 __global__ void __launch_bounds__(256) zero_kernel(const View v, int64_t pieces, int64_t n1, int64_t n2, int row16) {
     for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < pieces; i += (int64_t)gridDim.x * 256) {
@@ -506,6 +508,11 @@ int launch_delta(const Call& c) { BSP_WIN_TYPES(delta_t<float>(c), delta_t<__nv_
 
 int launch_tile_stats(const Call& c) {
     BSP_WIN_TYPES(BSP_ERR_UNSUPPORTED, tile_stats_t<__nv_bfloat16>(c), tile_stats_t<__half>(c))
+}
+
+int launch_take_status(const bsp_window_s* w, cudaStream_t s) {
+    take_status_kernel<<<1, 1, 0, s>>>(w->status);
+    return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
 int launch_zero(const View& v, int elt, int64_t n0, int64_t n1, int64_t n2, int row16, cudaStream_t s) {

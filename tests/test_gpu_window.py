@@ -797,3 +797,20 @@ def test_a_wait_that_runs_out_is_reported(bsp, monkeypatch, what, D, limit):
     for _ in range(2):
         assert all(torch.equal(a, c) for a, c in zip(run(), want))
     assert bsp.bsp_window_status(W) == 0
+
+
+def test_status_of_two_streams(bsp):
+    """A report stays until a reader takes it, on any stream of the device, and
+    is taken once."""
+    b = Paged([1, 1], [40, 50], 2, 1, 64, 16, torch.bfloat16, 170)
+    b.table[1, 0] = b.n_pages
+    W = bsp.bsp_window_create()
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(3):
+        one.wait_stream(torch.cuda.current_stream())
+        b.attend(bsp, W, stream=one)
+        assert bsp.bsp_window_status(W, one) == -7
+        assert bsp.bsp_window_status(W, two) == 0 and bsp.bsp_window_status(W, one) == 0
+        b.attend(bsp, W, stream=one)
+        one.synchronize()
+        assert bsp.bsp_window_status(W, two.cuda_stream) == -7 and bsp.bsp_window_status(W) == 0

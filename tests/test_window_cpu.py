@@ -110,3 +110,50 @@ def test_wait_limits_grow_with_a_tile(lib):
         assert n * 20e-9 >= 2 * steps * 1e-6 and n < 2 ** 31
     assert lib.bsp_diag_window_attempts(1 << 40) == 2 ** 31 - 1
     assert lib.bsp_diag_window_wait_limit(None, 1) == -1
+
+
+def test_status_is_read_behind_the_handles_device(monkeypatch):
+    """With another device current, the word is read on the current stream of the
+    handle's own device, with that device current."""
+    import torch
+
+    cuda1 = torch.device("cuda", 1)
+    entered, read = [], []
+
+    class Stream:
+        def __init__(self, device):
+            self.device = device
+
+    class Using:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            entered.append(self.stream)
+
+        def __exit__(self, *a):
+            entered.append(None)
+
+    class Lib:
+        @staticmethod
+        def bsp_window_status(handle, stream):
+            read.append((handle, stream, entered[-1].device))
+            return -7
+
+    streams = {0: Stream(torch.device("cuda", 0)), 1: Stream(cuda1)}
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    monkeypatch.setattr(torch.cuda, "stream", Using)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda d=None: streams[0 if d is None else torch.device(d).index])
+    monkeypatch.setattr(bsp, "_raw_stream", lambda d: 1000 + d)
+    monkeypatch.setattr(bsp, "_stream", lambda s: 1000)
+    monkeypatch.setattr(bsp, "lib", lambda: Lib)
+    W = object.__new__(bsp.Window)
+    W.handle, W.device = 5, cuda1
+    try:
+        assert bsp.bsp_window_status(W) == -7
+        assert read == [(5, 1001, cuda1)] and entered[-1] is None
+        with pytest.raises(ValueError):  # another device's stream
+            bsp.bsp_window_status(W, streams[0])
+    finally:
+        W.handle = None
