@@ -228,9 +228,7 @@ extern "C" int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_
     if (Sk > 0 ? clash({O}, {Q, K, V}) : clash({O}, {Q})) return BSP_ERR_INVALID_ARG;
     if ((uintptr_t)lse & 15u) return BSP_ERR_ALIGNMENT;
     if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 0)))) return rc;
-    if (Sk == 0) {  // no key at all: zeros and -inf, by the kernels' hidden step over Q's own rows
-        c.K = c.V = View{Q->ptr, {D, D, D}};
-    }
+    if (Sk == 0) c.K = c.V = c.Q;  // no key at all: zeros and -inf, by the kernels' hidden step over Q's own first rows
     c.w = w, c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
     c.lse = lse;
     c.lz = (int64_t)Hq * Sq, c.lh = Sq, c.lt = 1;

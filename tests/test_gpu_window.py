@@ -814,3 +814,15 @@ def test_status_of_two_streams(bsp):
         b.attend(bsp, W, stream=one)
         one.synchronize()
         assert bsp.bsp_window_status(W, two.cuda_stream) == -7 and bsp.bsp_window_status(W) == 0
+
+
+def test_no_keys_for_queries_that_overlap(bsp, path):
+    """Without keys, nothing beyond Q's own rows is addressed, however they lie:
+    entries 8 elements apart here."""
+    W = bsp.bsp_window_create(10, 1)
+    room = torch.ones(8 * 299 + 64, dtype=torch.bfloat16, device="cuda")
+    Q = room.as_strided((300, 1, 1, 64), (8, 64, 64, 1))
+    none = torch.empty(300, 1, 0, 64, dtype=torch.bfloat16, device="cuda")
+    O, lse = bsp.bsp_window_attention(W, Q, none, none)
+    assert bool((O == 0).all()) and bool((lse == -math.inf).all())
+    assert bsp.bsp_window_status(W) == 0
