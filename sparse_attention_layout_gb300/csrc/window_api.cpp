@@ -265,13 +265,16 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
         if (!lse) return BSP_ERR_INVALID_ARG;
         if ((uintptr_t)lse & 15u) return BSP_ERR_ALIGNMENT;
     }
-    if (Sq > 0 && Sk > 0 && clash({dQ, dK, dV}, {Q, K, V, O, dO})) return BSP_ERR_INVALID_ARG;
+    if (Sq == 0 && Sk == 0) return BSP_OK;
+    if (Sq == 0   ? clash({dK, dV}, {K, V})
+        : Sk == 0 ? clash({dQ}, {Q, O, dO})
+                  : clash({dQ, dK, dV}, {Q, K, V, O, dO}))
+        return BSP_ERR_INVALID_ARG;
     // no pair at all: every gradient is 0
     const int row16 = D * elt / 16;
     if (Sq == 0) {
-        if (Sk > 0 && !(rc = bsp::win::launch_zero(c.dK, elt, Z, Hkv, Sk, row16, s)))
-            rc = bsp::win::launch_zero(c.dV, elt, Z, Hkv, Sk, row16, s);
-        return rc;
+        rc = bsp::win::launch_zero(c.dK, elt, Z, Hkv, Sk, row16, s);
+        return rc ? rc : bsp::win::launch_zero(c.dV, elt, Z, Hkv, Sk, row16, s);
     }
     if (Sk == 0) return bsp::win::launch_zero(c.dQ, elt, Z, Hq, Sq, row16, s);
     if ((rc = check_workspace(workspace, workspace_bytes, bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1)))) return rc;

@@ -826,3 +826,26 @@ def test_no_keys_for_queries_that_overlap(bsp, path):
     O, lse = bsp.bsp_window_attention(W, Q, none, none)
     assert bool((O == 0).all()) and bool((lse == -math.inf).all())
     assert bsp.bsp_window_status(W) == 0
+
+
+def test_gradients_over_inputs_are_refused_on_one_side_too(bsp):
+    """Without queries, or without keys, a gradient in an input's place would be
+    zeros over the input."""
+    W = bsp.bsp_window_create(10, 1)
+    x = lambda *s: torch.ones(*s, device="cuda", dtype=torch.bfloat16)
+    lse = torch.zeros(1, 2, 0, device="cuda")
+    none, K, V = x(1, 2, 0, 64), x(1, 1, 8, 64), x(1, 1, 8, 64)
+    both = x(1, 1, 8, 64)
+    for dK, dV in ((K, None), (None, V), (None, K), (both, both)):
+        with pytest.raises(bsp.BspError):
+            bsp.bsp_window_attention_backward(W, none, K, V, none, none, lse, dK=dK, dV=dV)
+    Q, O, dO, nokey = x(1, 2, 8, 64), x(1, 2, 8, 64), x(1, 2, 8, 64), x(1, 1, 0, 64)
+    lse = torch.zeros(1, 2, 8, device="cuda")
+    for dQ in (Q, O, dO):
+        with pytest.raises(bsp.BspError):
+            bsp.bsp_window_attention_backward(W, Q, nokey, nokey, O, dO, lse, dQ=dQ)
+    for t in (K, V, Q, O, dO):
+        assert bool((t == 1).all())
+    e = x(1, 2, 0, 64), x(1, 1, 0, 64)
+    bsp.bsp_window_attention_backward(W, e[0], e[1], e[1], e[0], e[0], torch.zeros(1, 2, 0, device="cuda"))
+    assert bsp.bsp_window_status(W) == 0
