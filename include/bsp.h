@@ -418,7 +418,9 @@ size_t bsp_attention_host_workspace(bsp_layout_t layout, int dtype, int D, int z
  *
  * Hq is a multiple of Hkv (query head h reads KV head h / (Hq / Hkv)), at most
  * 64 query heads per KV head; D 16 .. 128, a multiple of 16; lengths up to
- * 2^30 (beyond: BSP_ERR_UNSUPPORTED).  dtype, streams, errors as above; sums,
+ * 2^30, and together no more than 2^31 - 1 steps of a tile of 64 or 128 rows over
+ * a tile of as many keys (a paged call: as its sizes allow for, whatever the
+ * lengths; beyond: BSP_ERR_UNSUPPORTED).  dtype, streams, errors as above; sums,
  * softmax statistics and partial results are fp32, the 16-bit tensor-core
  * paths round P and dS to the call's type (unnormalised P <= 2^8).  The fp16
  * gradient holds P and dS times powers of two, dS by the longest rows of dO and

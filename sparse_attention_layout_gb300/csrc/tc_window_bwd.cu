@@ -827,17 +827,17 @@ int launch(Call& c) {
     const int grid = imin(sm_count(), TcPlan::kCtas);
     Args a{p, c.dQ, c.dK, c.dV, c.stats, c.factor, c.D, (p.Sq + tq2 - 1) / tq2, c.scale, c.scale * kLog2e, c.cuts, c.slots};
     const KProb kp{1, p.rep, p.G, tq2, p.kshift, p.Hq, p.Hkv, p.Sq, p.Sk, p.window, p.sinks};
-    TcPlan plan;
-    bool cut;
+    TcPlan plan, kplan;
+    bool cut, kcut;
     if ((rc = query_plan(c, grid, &plan.tab, plan.s, &cut))) return rc;
+    if ((rc = key_plan(c, kp, grid, &kplan.tab, kplan.s, &kcut))) return rc;
     if ((rc = launch_tile_stats(c))) return rc;
     if ((rc = launch_behind(dq_tc_kernel<T, DP>, dim3(grid), kThreads, smem, c.stream, mq, mk, mv, mg, a, plan)))
         return rc;
     if (cut && (rc = launch_join(c, kTcRows, grid, true))) return rc;
-    if ((rc = key_plan(c, kp, grid, &plan.tab, plan.s, &cut))) return rc;
-    if ((rc = launch_behind(dkv_tc_kernel<T, DP>, dim3(grid), kThreads, smem, c.stream, mq2, mk, mv, mg2, a, kp, plan)))
+    if ((rc = launch_behind(dkv_tc_kernel<T, DP>, dim3(grid), kThreads, smem, c.stream, mq2, mk, mv, mg2, a, kp, kplan)))
         return rc;
-    return cut ? launch_join_kv(c, kp, kTcRows, grid) : BSP_OK;
+    return kcut ? launch_join_kv(c, kp, kTcRows, grid) : BSP_OK;
 }
 
 }  // namespace

@@ -134,7 +134,8 @@ int launch_take_status(const bsp_window_s* w, cudaStream_t s);
 int launch_zero(const View& v, int elt, int64_t n0, int64_t n1, int64_t n2, int row16, cudaStream_t s);
 // The split of a dense launch's query tiles (p) or key tiles (k) over `ctas`
 // CTAs; *cut: some tile is shared between CTAs, so that a join has to follow.
-// BSP_ERR_OOM when the host has no memory for it.
+// BSP_ERR_UNSUPPORTED: more steps than 31 bits count; BSP_ERR_OOM: the host has no
+// memory for it.
 Plans* plans_create();
 void plans_destroy(Plans* p);
 int query_plan(const Call& c, int ctas, Table* tab, CtaStart* starts, bool* cut);

@@ -124,10 +124,8 @@ int check_workspace(const void* ws, size_t have, size_t need) {
 int check_dense(int Z, int Hq, int Hkv, int Sq, int Sk, int D, float scale) {
     if (Z < 0 || Hq < 1 || Hkv < 1 || Sq < 0 || Sk < 0 || !valid_d(D) || !valid_scale(scale)) return BSP_ERR_INVALID_ARG;
     if (Hq % Hkv) return BSP_ERR_INVALID_ARG;
+    // (the split refuses what has more steps than 32 bits count)
     if (Hq / Hkv > kMaxGroup || Sq > kMaxLen || Sk > kMaxLen || (int64_t)Z * Hkv > kMaxLen) return BSP_ERR_UNSUPPORTED;
-    // tiles and steps are counted in 32 bits: at the least 64 rows x 64 keys
-    const int64_t tq = 64 / (Hq / Hkv), qt = (Sq + tq - 1) / tq + 1, kt = (Sk + 63) / 64 + 1;
-    if (Z && (qt > kMaxLen / kt || (int64_t)Z * Hkv > kMaxLen / (qt * kt))) return BSP_ERR_UNSUPPORTED;
     return BSP_OK;
 }
 
@@ -281,11 +279,11 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
     c.w = w, c.dtype = dtype, c.D = D, c.scale = scale, c.Z = Z;
     c.lse = const_cast<float*>(lse);
     c.lz = (int64_t)Hq * Sq, c.lh = Sq, c.lt = 1;
-    if (Sq > Sk) {
+    const View all = c.dQ;
+    const int none = Sq > Sk ? Sq - Sk : 0;
+    if (none > 0) {
         // the first queries stand before position 0: their dQ is 0, and the
         // kernels never meet their rows, which may hold anything
-        const int none = Sq - Sk;
-        if ((rc = bsp::win::launch_zero(c.dQ, elt, Z, Hq, none, row16, s))) return rc;
         for (View* v : {&c.Q, &c.O, &c.dO, &c.dQ}) v->ptr = static_cast<char*>(v->ptr) + v->s[2] * none * elt;
         c.lse += none;
         Sq = Sk;
@@ -299,7 +297,8 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
     c.factor = reinterpret_cast<bsp::win::DsFactor*>(ws + range_bytes(Z, Hkv));
     c.stats = reinterpret_cast<float*>(ws + range_bytes(Z, Hkv) + factor_bytes(Z, Hkv));
     c.stream = s;
-    return on_tensor_cores(w, dtype) ? bsp::win::launch_backward_tc(c) : bsp::win::launch_backward_simt(c);
+    rc = on_tensor_cores(w, dtype) ? bsp::win::launch_backward_tc(c) : bsp::win::launch_backward_simt(c);
+    return rc || none == 0 ? rc : bsp::win::launch_zero(all, elt, Z, Hq, none, row16, s);
 }
 
 namespace {
@@ -310,15 +309,18 @@ int paged_prob(bsp_window_t w, const int32_t* q_start, const int32_t* kv_len, co
     if (Hq % Hkv) return BSP_ERR_INVALID_ARG;
     if (Hq / Hkv > kMaxGroup || T > kMaxLen || n_seq > kMaxSeqs || (int64_t)max_pages * page > kMaxLen)
         return BSP_ERR_UNSUPPORTED;
+    set_rule(w, p);
     // tiles and steps are counted in 32 bits; a tile holds 64 rows and a step 64
-    // keys at the least, but a sequence's last tile may hold one row
+    // keys at the least, but a sequence's last tile may hold one row, and a tile's
+    // steps go over the tables' keys or, if they are fewer, its sinks and windows
     const int64_t tq = 64 / (Hq / Hkv), qt = T <= n_seq ? T : (T + tq - 1) / tq + n_seq;
-    const int64_t kt = ((int64_t)max_pages * page + 63) / 64 + 1;
+    const int64_t all = ((int64_t)max_pages * page + 63) / 64 + 1;
+    const int64_t near = ((int64_t)p->sinks + 63) / 64 + ((int64_t)p->window + tq + 63) / 64 + 1;
+    const int64_t kt = near < all ? near : all;
     if (qt > 0 && (kt > (1ll << 31) / qt || Hkv > (1ll << 31) / (qt * kt) - 1)) return BSP_ERR_UNSUPPORTED;
     if (T == 0 || n_seq == 0) return BSP_OK;
     if (!q_start || !kv_len || !table) return BSP_ERR_INVALID_ARG;
     if (((uintptr_t)q_start | (uintptr_t)kv_len | (uintptr_t)table) & 3u) return BSP_ERR_ALIGNMENT;
-    set_rule(w, p);
     p->paged = 1;
     p->nseg = n_seq;
     p->rep = Hkv;

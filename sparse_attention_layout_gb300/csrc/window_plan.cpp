@@ -31,12 +31,13 @@ struct Key {
 // cut: 256 rows of 4 heads, window 64: 11.4 and 13.6; 4 x 16 heads of 8192 rows,
 // window 128, with gradient: 475 and 494; the gradient of 1037 rows of 12 heads
 // 39.6 and 43.2, with tiles of 8 steps whole 47.6; up to an eighth of a share,
-// full attention over 8192 keys took 244 for 224).
-void split(const std::vector<int>& steps, int rep, int ctas, Table* tab, CtaStart* out) {
-    const int ntiles = (int)steps.size(), items = ntiles * rep;
+// full attention over 8192 keys took 244 for 224).  False: more steps than an int
+// counts.
+bool split(const std::vector<int>& steps, int rep, int ctas, Table* tab, CtaStart* out) {
     int64_t one = 0;
-    for (int s : steps) one += s;
-    const int tot = (int)(one * rep);
+    for (int s : steps) one += s;  // every tile has a step
+    if (one > INT32_MAX / rep) return false;
+    const int ntiles = (int)steps.size(), items = ntiles * rep, tot = (int)one * rep;
     const Shares sh(tot, imax(1, imin(ctas, imax(items, tot / kMinShare))));
     *tab = Table(items, ctas);
     std::vector<int> at(ctas + 1, tot);
@@ -56,6 +57,7 @@ void split(const std::vector<int>& steps, int rep, int ctas, Table* tab, CtaStar
         if (i >= c) out[i] = CtaStart{0, 0, 0, 0};
         out[i].count = at[i + 1] - at[i];
     }
+    return true;
 }
 
 }  // namespace
@@ -91,7 +93,7 @@ int find(const Call& c, const Key& key, int ntiles, F steps_of, Table* tab, CtaS
             }
         std::vector<int> steps(ntiles);
         for (int t = 0; t < ntiles; ++t) steps[t] = steps_of(t);
-        split(steps, key.rep, key.ctas, tab, out);
+        if (!split(steps, key.rep, key.ctas, tab, out)) return BSP_ERR_UNSUPPORTED;
         *cut = false;
         for (int i = 0; i < key.ctas; ++i) *cut |= out[i].off > 0;
         if (P.kept.size() >= kKeep) P.kept.pop_front();

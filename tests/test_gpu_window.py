@@ -849,3 +849,62 @@ def test_gradients_over_inputs_are_refused_on_one_side_too(bsp):
     e = x(1, 2, 0, 64), x(1, 1, 0, 64)
     bsp.bsp_window_attention_backward(W, e[0], e[1], e[1], e[0], e[0], torch.zeros(1, 2, 0, device="cuda"))
     assert bsp.bsp_window_status(W) == 0
+
+
+def test_long_windowed_sequences(bsp, path):
+    """256 k tokens of 64 heads over 8: more (row tile, key tile) pairs than 2^31,
+    of which a window of 64 leaves few steps.  Rows in the middle and at the end
+    against the keys of their windows."""
+    S, window, n = 262144, 64, 100
+    W = bsp.bsp_window_create(window, 0)
+    Q, dO = (randn((1, 64, S, 16), torch.bfloat16, 180 + i, "rows") for i in range(2))
+    K, V = (randn((1, 8, S, 16), torch.bfloat16, 182 + i) for i in range(2))
+    O, lse, dQ, dK, dV = _gradients(bsp, W, Q, K, V, dO, 0.25)
+    assert bsp.bsp_window_status(W) == 0
+    for end in (S // 2, S):
+        rows, keys = slice(end - n, end), slice(end - n - window + 1, end)
+        r = ref.dense(Q[:, :, rows], K[:, :, keys], V[:, :, keys], 0.25, window, 0, dO[:, :, rows])
+        check(O[:, :, rows], r["O"], r["eO"], "O")
+        check(lse[:, :, rows], r["lse"], r["else_"], "lse")
+        check(dQ[:, :, rows], r["dQ"], r["eQ"], "dQ")
+        # keys whose queries are all among the rows
+        own = slice(end - n, end if end == S else end - window)
+        for name, got in (("dK", dK), ("dV", dV)):
+            at = slice(window - 1, window - 1 + own.stop - own.start)
+            check(got[:, :, own], r[name][:, :, at], r["e" + name[-1]][:, :, at], name)
+
+
+def test_long_windowed_pages(bsp, path):
+    """A chunk of 16 k tokens under a table of 16 M keys, of which a window leaves
+    few."""
+    S, window, n, page = 16384, 100, 50, 128
+    W = bsp.bsp_window_create(window, 0)
+    Q = randn((1, 64, S, 16), torch.bfloat16, 190)[0].transpose(0, 1).contiguous()
+    Kc, Vc = (randn((S // page, 8, page, 16), torch.bfloat16, 191 + i) for i in range(2))
+    table = torch.full((1, 1 << 17), -1, dtype=torch.int32, device="cuda")
+    table[0, :S // page] = torch.arange(S // page, dtype=torch.int32, device="cuda")
+    i = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    O, lse = bsp.bsp_paged_attention(W, Q, Kc, Vc, i(0, S), i(S), table, scale=0.25)
+    assert bsp.bsp_window_status(W) == 0
+    K, V = (c.transpose(0, 1).reshape(1, 8, S, 16)[:, :, S - n - window + 1:] for c in (Kc, Vc))
+    r = ref.dense(Q[S - n:].transpose(0, 1)[None], K, V, 0.25, window, 0)
+    check(O[S - n:].transpose(0, 1)[None], r["O"], r["eO"], "O")
+    check(lse[S - n:].T[None], r["lse"], r["else_"], "lse")
+
+
+def test_more_steps_than_31_bits_are_refused(bsp, path):
+    """Full attention of 2^21 tokens in 64 heads: refused before anything runs."""
+    W = bsp.bsp_window_create(0, 0)
+    S = 1 << 21
+    x = torch.empty(S + 64, 16, dtype=torch.bfloat16, device="cuda")
+    Q, K = (x.as_strided((1, H, S, 16), (S * 16, 8, 16, 1)) for H in (64, 8))  # heads that overlap
+    O = torch.full((1, 64, S, 16), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((1, 64, S), 7.0, device="cuda")
+    with pytest.raises(bsp.BspError) as e:
+        bsp.bsp_window_attention(W, Q, K, K, O=O, lse=lse)
+    assert e.value.code == -2
+    with pytest.raises(bsp.BspError) as e:
+        bsp.bsp_window_attention_backward(W, Q, K, K, O, O.clone(), lse, dQ=O.clone())
+    assert e.value.code == -2
+    assert bool((O == 7).all()) and bool((lse == 7).all())
+    assert bsp.bsp_window_status(W) == 0
