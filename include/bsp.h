@@ -429,10 +429,14 @@ size_t bsp_attention_host_workspace(bsp_layout_t layout, int dtype, int D, int z
  *
  * Non-finite values: keys that no query of a call sees (behind a sequence's
  * length, before every window) never reach an output, whatever their slots
- * hold, and a hidden K row never reaches a query that does not see it.  A
- * non-finite V row (in the gradient also K, Q, dO) that some query of a tile
- * of 128 rows sees may reach the tile's other rows (0 * inf).  A query with
- * NaN or +inf among its own scores has NaN for its output and lse.
+ * hold, and a hidden K row never reaches the output of a query that does not see
+ * it.  A non-finite V row that some query sees may reach (0 * inf) others that do
+ * not see it, where one of the same 128 rows -- consecutive tokens times the
+ * heads of a KV head -- sees one of its 16 keys from a multiple of 16 on.  In the
+ * gradient a non-finite row of V, K, Q or dO may reach the gradients of the same
+ * 128 rows, and of the 128 keys from a multiple of 128 on, where one of the rows
+ * sees one of the keys.  A query with NaN or +inf among its own scores has NaN
+ * for its output and lse.
  *
  * Workspaces are the caller's (DEVICE, 256-byte aligned, else
  * BSP_ERR_ALIGNMENT; too small: BSP_ERR_INVALID_ARG); their contents need not
@@ -497,13 +501,14 @@ size_t bsp_window_attention_workspace(int Z, int Hq, int Hkv, int Sq, int backwa
  * bsp_window_status: a sequence that q_start places outside the T rows, or
  * with kv_len negative or beyond max_pages * page, is left out; where q_start
  * descends, no row is attended to; a page of a visible position outside
- * [0, n_pages) is never accessed (the output of the call is then undefined).  Table entries of pages without a visible position are not
- * used and may hold anything. */
+ * [0, n_pages) is never accessed (the output of the call is then undefined).
+ * Table entries of pages without a visible position are not used and may hold
+ * anything. */
 
 /* Writes the new tokens' rows K, V (-, KV head, row) to their slots
  * (bsp_tensor_t stride[0] unused).  Positions below 0 (kv_len smaller than the
- * new tokens) are not written.  Two rows with the same slot: either one's
- * values. */
+ * new tokens) are not written.  Two rows with the same slot: each 16 bytes
+ * of it are either one's. */
 int bsp_paged_append(bsp_window_t w, int dtype, const bsp_tensor_t* K, const bsp_tensor_t* V,
                      const bsp_tensor_t* K_cache, const bsp_tensor_t* V_cache, const int32_t* q_start,
                      const int32_t* kv_len, const int32_t* table, int T, int n_seq, int max_pages, int n_pages,

@@ -908,3 +908,53 @@ def test_more_steps_than_31_bits_are_refused(bsp, path):
     assert e.value.code == -2
     assert bool((O == 7).all()) and bool((lse == 7).all())
     assert bsp.bsp_window_status(W) == 0
+
+
+def _tiles_that_meet(S, tokens, window, lo, hi):
+    """[S] rows whose tile of `tokens` tokens has a row that sees a key of lo .. hi."""
+    t = torch.arange(S, device="cuda") // tokens * tokens
+    last = (t + tokens - 1).clamp(max=S - 1)
+    return (last >= lo) & ((t - window + 1).clamp(min=0) <= hi)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_how_far_non_finite_rows_reach(bsp, path, dtype):
+    """Three heads a group: 42 tokens are 126 rows.  Rows that the header does not
+    name keep their bits, those that see the row have NaN."""
+    S, window, j = 600, 100, 300
+    W = bsp.bsp_window_create(window, 0)
+    Q, K, V, dO = (randn((1, H, S, 64), DT[dtype], 200 + i) for i, H in enumerate((6, 2, 2, 6)))
+    want = _gradients(bsp, W, Q, K, V, dO)
+    pos = torch.arange(S, device="cuda")
+    sees = (pos >= j) & (pos - j < window)
+    # a V row: pieces of 16 keys
+    V2 = V.clone()
+    V2[0, 0, j] = math.nan
+    O, lse, dQ, dK, dV = _gradients(bsp, W, Q, K, V2, dO)
+    near = _tiles_that_meet(S, 42, window, j // 16 * 16, j // 16 * 16 + 15)
+    assert torch.equal(O[:, 3:], want[0][:, 3:]) and torch.equal(lse, want[1])
+    assert torch.equal(O[:, :3, ~near], want[0][:, :3, ~near]) and bool(O[:, :3, sees].isnan().all())
+    near = _tiles_that_meet(S, 42, window, j // 128 * 128, j // 128 * 128 + 127)
+    assert torch.equal(dQ[:, 3:], want[2][:, 3:]) and torch.equal(dQ[:, :3, ~near], want[2][:, :3, ~near])
+    # a K row
+    K2 = K.clone()
+    K2[0, 1, j] = math.inf
+    O, lse, dQ, dK, dV = _gradients(bsp, W, Q, K2, V, dO)
+    for got, ref_ in ((O, want[0]), (lse, want[1])):
+        assert torch.equal(got[:, :3], ref_[:, :3]) and torch.equal(got[:, 3:, ~sees], ref_[:, 3:, ~sees])
+    assert torch.equal(dQ[:, :3], want[2][:, :3]) and torch.equal(dQ[:, 3:, ~near], want[2][:, 3:, ~near])
+    # rows of Q and dO: the keys that their tile's rows see
+    first = j // 42 * 42
+    keys = (pos >= max(first - window + 1, 0) // 128 * 128) & (pos < (first + 41) // 128 * 128 + 128)
+    for which in (0, 3):
+        x = [Q, K, V, dO]
+        x[which] = x[which].clone()
+        x[which][0, 1, j] = math.nan
+        O, lse, dQ, dK, dV = _gradients(bsp, W, *x)
+        assert bool(dQ[0, 1, j].isnan().all())
+        same = torch.ones(6, S, dtype=torch.bool, device="cuda")
+        same[1, j] = False
+        assert torch.equal(dQ[0][same], want[2][0][same])
+        for got, ref_ in ((dK, want[3]), (dV, want[4])):
+            assert torch.equal(got[:, 1], ref_[:, 1]) and torch.equal(got[:, 0, ~keys], ref_[:, 0, ~keys])
+    assert bsp.bsp_window_status(W) == 0
