@@ -63,7 +63,13 @@ struct DsFactor {
     float up;    // of dP - delta, which P times 2^kPUp then multiplies
     float down;  // 1 / (up 2^kPUp)
 };
-constexpr int kRangeParts = 512;  // at most, blocks that look for the longest rows of one (batch entry, KV head)
+// Blocks that look for the longest rows of one of `rep` (batch entry, KV head)
+// pairs: together enough to fill the GPU.
+constexpr int kRangeParts = 512;
+inline int range_parts(int64_t rep) {
+    const int64_t fill = (16 * (int64_t)sm_count() + rep - 1) / rep;
+    return fill < kRangeParts ? (int)fill : kRangeParts;
+}
 struct RangePart {
     float dO2, V2;  // largest sum of squares of a row
 };
@@ -80,7 +86,7 @@ struct Call {
     // floats per tile of kStatRows rows (tensor cores)
     float* stats;
     // fp16 gradient on the tensor cores: of each (batch entry, KV head) up to
-    // kRangeParts partial results, and the factors
+    // range_parts() partial results, and the factors
     RangePart* range;
     DsFactor* factor;
     Prob p;              // TQ and kshift set by the launcher

@@ -100,7 +100,10 @@ size_t slots_bytes(bool backward) {
     return round_up(f * sizeof(float) * 2 * bsp::sm_count());
 }
 
-size_t range_bytes(int Z, int Hkv) { return round_up((size_t)Z * Hkv * bsp::win::kRangeParts * sizeof(bsp::win::RangePart)); }
+size_t range_bytes(int Z, int Hkv) {
+    const int64_t rep = (int64_t)Z * Hkv;
+    return rep == 0 ? 0 : round_up((size_t)rep * bsp::win::range_parts(rep) * sizeof(bsp::win::RangePart));
+}
 size_t factor_bytes(int Z, int Hkv) { return round_up((size_t)Z * Hkv * sizeof(bsp::win::DsFactor)); }
 // of each tile's rows (more than the one float per row that the CUDA-core kernels
 // keep)

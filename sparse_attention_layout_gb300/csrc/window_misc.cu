@@ -457,11 +457,8 @@ int tile_stats_t(const Call& c) {
     const int64_t rows = kF16 ? per : per * p.rep;  // of a part's share
     int64_t parts = (rows + 31) / 32;
     if (kF16) {
-        // enough blocks to fill the GPU; V may have many more rows than Q
-        parts = p.Sk / 32 > parts ? p.Sk / 32 : parts;
-        const int64_t fill = (most + p.rep - 1) / p.rep;
-        parts = parts < fill ? parts : fill;
-        parts = parts < kRangeParts ? parts : kRangeParts;
+        parts = p.Sk / 32 > parts ? p.Sk / 32 : parts;  // V may have many more rows than Q
+        parts = parts < range_parts(p.rep) ? parts : range_parts(p.rep);
     } else {
         parts = parts < most ? parts : most;
     }
