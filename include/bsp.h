@@ -479,8 +479,9 @@ int bsp_window_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const
  * and lse: with P = exp(scale Q K^T - lse) on the visible pairs and
  * dS = P .* (dO V^T - rowsum(dO .* O)),
  *     dV = P^T dO,  dK = scale dS^T Q,  dQ = scale dS K,
- * dK and dV summed over the query heads that share the KV head.  Workspace:
- * bsp_window_attention_workspace(Z, Hq, Hkv, Sq, 1) bytes. */
+ * dK and dV summed over the query heads that share the KV head.  O's rounding to
+ * dtype enters dO .* O.  Workspace: bsp_window_attention_workspace(Z, Hq, Hkv,
+ * Sq, 1) bytes. */
 int bsp_window_attention_backward(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K,
                                   const bsp_tensor_t* V, const bsp_tensor_t* O, const bsp_tensor_t* dO,
                                   const float* lse, const bsp_tensor_t* dQ, const bsp_tensor_t* dK,

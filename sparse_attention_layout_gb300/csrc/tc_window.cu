@@ -23,6 +23,11 @@
 // TMEM columns: S buffers at 0, 128, 256, each step's P over its own scores;
 // O at 384.
 //
+// P is rounded to the call's type, which the product takes; its sum l is of the
+// unrounded values, in fp32, as O is.  Against an fp64 softmax O is off by 2.0 to
+// 2.4e-3 (bf16) and 2.7 to 2.9e-4 (fp16), 1.6e-3 and 2.0e-4 of it its own
+// rounding.
+//
 // V rows that no query of the sequence sees but that share a piece of 16 keys
 // with visible ones (the tail of the last page, keys before every window) are
 // zeroed in shared memory before the product, since 0 * NaN is NaN.
@@ -363,7 +368,6 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         }
     }
     } else if (warp < 8) {
-        if constexpr (kRegsEpi < kRegsLaunch) regs_dec<kRegsEpi>();
         // ---------------------------------------------------- epilogue ----
         const int quad = warp & 3;
         const int row = quad * 32 + lane;

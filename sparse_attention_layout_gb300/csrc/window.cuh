@@ -11,16 +11,17 @@
 // of a single new token are the tile's first G.
 //
 // Split: the steps of all tiles form one line, of which each CTA takes an equal
-// run (of a dense batch, up to the next short tile's edge).  A tile that a boundary cuts leaves partial
-// results, which a second kernel joins in the order of the pieces, so results
-// do not depend on timing.  Tiles are numbered (segment, repetition, tile); a
-// segment is a shape of tiles: the whole of a dense batch, repeated for each
-// (batch entry, KV head), which the host splits, or one sequence of a ragged
-// one, whose lengths only the device knows, repeated for each KV head.  The line holds them column by
-// column of a table with one column per CTA, filled row by row: CTAs then
-// work on neighbouring tiles at the same time and share their keys in L2
-// (with each CTA on a run of consecutive tiles instead, the band of 8192 keys
-// and 16 heads read 954 MB from HBM instead of the 402 MB that it holds).
+// run (of a dense batch, up to the next short tile's edge).  A tile that a
+// boundary cuts leaves partial results, which a second kernel joins in the order
+// of the pieces, so results do not depend on timing.  Tiles are numbered
+// (segment, repetition, tile); a segment is a shape of tiles: the whole of a
+// dense batch, repeated for each (batch entry, KV head), which the host splits,
+// or one sequence of a ragged one, whose lengths only the device knows, repeated
+// for each KV head.  The line holds them column by column of a table with one
+// column per CTA, filled row by row: CTAs then work on neighbouring tiles at the
+// same time and share their keys in L2 (with each CTA on a run of consecutive
+// tiles instead, the band of 8192 keys and 16 heads read 954 MB from HBM instead
+// of the 402 MB that it holds).
 #pragma once
 
 #include <cuda_runtime.h>
