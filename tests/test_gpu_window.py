@@ -973,3 +973,24 @@ def test_workspace_of_many_short_sequences(bsp):
     # |dO||V| < 300, times scale |K| < 1
     assert dQ.abs().max().item() <= 1e-2 and dK.abs().max().item() <= 1e-2
     assert bsp.bsp_window_status(W) == 0
+
+
+@pytest.mark.parametrize("size", [1.0, 2.0 ** -12])
+@pytest.mark.parametrize("shape", JOINED, ids=str)
+def test_tiles_of_many_pieces_in_fp16(bsp, path, shape, size):
+    """Partial results leave fp16's factors behind, for output gradients of either
+    size; the bound of the norms is that of test_gradient_of_a_small_output_gradient."""
+    Z, Hq, Hkv, Sq, Sk, D, window, sinks = shape
+    Q, dO = (randn((Z, Hq, Sq, D), torch.float16, sum(shape) + i) for i in range(2))
+    K, V = (randn((Z, Hkv, Sk, D), torch.float16, sum(shape) + 2 + i) for i in range(2))
+    dO = (dO * size).half()
+    W = bsp.bsp_window_create(window, sinks)
+    scale = 1.0 / math.sqrt(D)
+    O, lse, dQ, dK, dV = _gradients(bsp, W, Q, K, V, dO, scale)
+    r = ref.dense(Q, K, V, scale, window, sinks, dO)
+    for name, got in (("O", O), ("dQ", dQ), ("dK", dK), ("dV", dV)):
+        check(got, r[name], r["e" + name[-1]], name)
+        off = (got.double() - r[name]).norm().item()
+        assert off <= 4 * ref.U[torch.float16] * r[name].norm().item() + ref.AB[torch.float16] * math.sqrt(got.numel()), name
+    assert all(torch.equal(a, b) for a, b in zip(_gradients(bsp, W, Q, K, V, dO, scale), (O, lse, dQ, dK, dV)))
+    assert bsp.bsp_window_status(W) == 0
