@@ -527,6 +527,166 @@ int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const 
                         void* stream);
 size_t bsp_paged_attention_workspace(void);
 
+/* ---- drafted tokens ----------------------------------------------------
+ * A step that checks several drafted tokens of a sequence at once: their keys
+ * and values go to the cache (bsp_paged_append), each attends to the context
+ * and to its own ancestors (bsp_paged_tree_attention), the target's
+ * probabilities decide which of them stay (bsp_draft_verify), and the rows of
+ * those move next to the context (bsp_paged_keep).
+ *
+ * A sequence's new tokens are the nodes of a tree, in the rows q_start[s] ..
+ * q_start[s + 1] - 1 and at the last positions of its kv_len, as for the paged
+ * cache above, at most 1024 of them.  parent: DEVICE int32 [T], a node's parent,
+ * counted within the sequence, before the node itself, or -1: no parent.  Node 0
+ * is the last token that is known (its own keys are not in the cache yet), the
+ * nodes below it are drafted; a chain has parents -1, 0, 1, 2 ...  With ctx =
+ * kv_len - nodes, a node without a parent stands at position ctx, any other one
+ * behind its parent.  T rows, n_seq <= 16384 sequences. */
+
+/* positions: DEVICE int32 [T] (output), each node's position.  bits: DEVICE
+ * uint32 [T][words] (output), bit a % 32 of word a / 32: the node sees node a,
+ * that is itself or an ancestor, within the handle's window or at a sink's
+ * position.  words = at least the nodes of any sequence / 32, 1 .. 32.  One call
+ * serves all layers of a step.  Checked on the device (BSP_ERR_DEVICE_CHECK by
+ * bsp_window_status): a sequence outside the T rows, of more than 32 words nodes
+ * or more nodes than kv_len is left out; a parent that is not before its node
+ * counts as -1. */
+int bsp_draft_tree(bsp_window_t w, const int32_t* q_start, const int32_t* kv_len, const int32_t* parent,
+                   int32_t* positions, uint32_t* bits, int T, int n_seq, int words, void* stream);
+
+/* bsp_paged_attention for trees: node i sees key j < ctx by the handle's rule at
+ * its position (positions[i], at least ctx), and node a of its sequence where its
+ * bit says so; any bits will do, a row without a visible key gets output 0 and
+ * log-sum-exp -inf.  A sequence with more than 32 words nodes, or more nodes than
+ * kv_len, is left out and reported.  The rest as bsp_paged_attention, with its
+ * workspace. */
+int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K_cache,
+                             const bsp_tensor_t* V_cache, const bsp_tensor_t* O, float* lse, const int32_t* q_start,
+                             const int32_t* kv_len, const int32_t* table, const int32_t* positions,
+                             const uint32_t* bits, int T, int n_seq, int max_pages, int n_pages, int page, int Hq,
+                             int Hkv, int D, int words, float scale, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* Which drafted tokens stay, so that the tokens that come out are distributed as
+ * the target's.  target: DEVICE dtype, row t (target_stride elements from one to
+ * the next, V contiguous) = the probabilities of the token behind node t; draft:
+ * the same for the distribution that each child of node t was drawn from,
+ * independently, or NULL where the children were chosen without chance; rows of
+ * nodes whose children need no look are not read.  tokens: DEVICE int32 [T];
+ * accept, sample: DEVICE float [T], [n_seq], uniform numbers in [0, 1).
+ *
+ * From node 0 down, before the k-th child of a node (in the order of their rows):
+ *     r_0 = target row, s_0 = 1;  r_(k+1) = max(r_k - s_k draft row, 0), or r_k
+ *     without the child's token where draft is NULL;  s_(k+1) = sum r_(k+1);
+ * a child with the token x stays when accept * draft[x] * s_k < r_k[x] (NULL:
+ * accept * s_k < r_k[x]), and the walk goes on at it.  Where none does, the next
+ * token is the first one up to which r_k adds up to more than sample * sum r_k
+ * (the target's own row if r_k is all 0; no entry above 0 in it: -1).  Sums keep
+ * their rounding errors (relative error about 2^-45), so the tokens are those of
+ * fp64.  Entries that are negative or NaN count as 0.
+ *
+ * path: DEVICE int32 [T] (output), in the rows of each sequence its accepted nodes
+ * from node 0 on, then -1; count: DEVICE int32 [n_seq], their number (0 for a
+ * sequence without nodes); token: DEVICE int32 [n_seq], the next token.  Nodes
+ * with parent -1 behind node 0 are places without a token.  Checked on the device:
+ * a sequence outside the T rows or of more than 1024 nodes counts as without
+ * nodes, a node with a wrong parent or a token outside 0 .. V - 1 as without a
+ * token. */
+int bsp_draft_verify(bsp_window_t w, int dtype, const void* target, int64_t target_stride, const void* draft,
+                     int64_t draft_stride, const int32_t* tokens, const int32_t* q_start, const int32_t* parent,
+                     const float* accept, const float* sample, int32_t* path, int32_t* count, int32_t* token, int T,
+                     int n_seq, int V, void* stream);
+
+/* The rows of the accepted nodes (path and count as bsp_draft_verify gives them;
+ * kv_len still with all nodes) to the positions ctx, ctx + 1, ... of their
+ * sequences; the sequence's length is then ctx + count.  Rows behind stay as they
+ * are.  A sequence whose path does not ascend within its nodes, or of more nodes
+ * than kv_len, is left out, a row with a page outside [0, n_pages) is not moved,
+ * and both are reported. */
+int bsp_paged_keep(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const bsp_tensor_t* V_cache,
+                   const int32_t* q_start, const int32_t* kv_len, const int32_t* table, const int32_t* path,
+                   const int32_t* count, int T, int n_seq, int max_pages, int n_pages, int page, int Hkv, int D,
+                   void* stream);
+
+/* ---- pages of the cache ------------------------------------------------
+ * Which sequences hold which pages, kept on the device: refs: DEVICE int32
+ * [n_pages], how many table entries hold a page (0: free); table: DEVICE int32
+ * [n_seq][max_pages] as above, entries below 0 hold none.  The layers of a model
+ * share one such book; what it moves (src, dst) each layer's caches copy.  Pages
+ * are given out lowest first, in the order of (sequence, entry), so that results
+ * do not depend on timing.  refs has to agree with the table, and calls on one
+ * book have to follow one another.  n_seq <= 16384, n_seq * max_pages and
+ * max_pages * page <= 2^30 (beyond: BSP_ERR_UNSUPPORTED).
+ *
+ * Checked on the device, reported by bsp_window_status: a length below 0 or beyond
+ * max_pages * page (the sequence is left out) and an entry of n_pages or more (it
+ * counts as none) as BSP_ERR_DEVICE_CHECK, no free page left as BSP_ERR_OOM.
+ * Workspace of fork, reserve and compact: bsp_pages_workspace() bytes. */
+
+/* Gives up the pages behind each sequence's length (of a sequence that ended:
+ * length 0); their entries become -1. */
+int bsp_pages_free(bsp_window_t w, int32_t* refs, int32_t* table, const int32_t* kv_len, int n_seq, int max_pages,
+                   int n_pages, int page, void* stream);
+
+/* Every sequence s becomes a copy of what sequence parent[s] was before the call
+ * (DEVICE int32 [n_seq]; s itself: unchanged; -1: an empty sequence): its length,
+ * and its pages up to that, shared.  What s held before is given up.  A parent
+ * outside -1 .. n_seq - 1 or of a wrong length is reported, and s unchanged. */
+int bsp_pages_fork(bsp_window_t w, int32_t* refs, int32_t* table, int32_t* kv_len, const int32_t* parent, int n_seq,
+                   int max_pages, int n_pages, int page, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Pages of its own for the positions kv_len[s] .. lengths[s] - 1 of every sequence
+ * (none where lengths[s] <= kv_len[s]), so that they may be written: entries that
+ * hold none, or a page that others hold too, get free ones, except that of the
+ * entries here that share a page that nobody else holds the first keeps it.  src,
+ * dst: DEVICE int32 [n_seq] (output), for bsp_paged_copy: the page to copy for the
+ * tokens that a page given up for another one held already, else -1.  Where no
+ * page is left the entry stays as it is. */
+int bsp_pages_reserve(bsp_window_t w, int32_t* refs, int32_t* table, const int32_t* kv_len, const int32_t* lengths,
+                      int32_t* src, int32_t* dst, int n_seq, int max_pages, int n_pages, int page, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* The pages in use to the front: with n of them, the k-th one at n or behind goes
+ * to the k-th free place before n.  refs_out, table_out: the book afterwards
+ * (refs and table themselves, or other memory); src, dst: DEVICE int32
+ * [n_pages / 2] (output), for bsp_paged_copy, then -1. */
+int bsp_pages_compact(bsp_window_t w, const int32_t* refs, const int32_t* table, int32_t* refs_out, int32_t* table_out,
+                      int32_t* src, int32_t* dst, int n_seq, int max_pages, int n_pages, void* workspace,
+                      size_t workspace_bytes, void* stream);
+size_t bsp_pages_workspace(int n_seq, int max_pages, int n_pages);
+
+/* Copies page src[i] to page dst[i] of both caches, i < n (DEVICE int32; a pair
+ * with a number below 0 is left out, one with a number of n_pages or more reported
+ * and left out).  No page is both a source and a destination, or twice a
+ * destination (what such pages then hold is undefined). */
+int bsp_paged_copy(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const bsp_tensor_t* V_cache,
+                   const int32_t* src, const int32_t* dst, int n, int n_pages, int page, int Hkv, int D, void* stream);
+
+/* ---- rotary positions --------------------------------------------------
+ * Pair i of a head's first 2 n_pairs columns turns by the angle position *
+ * frequencies[i] and grows by the amplitude A:
+ *     y_a = A (x_a cos - x_b sin),  y_b = A (x_b cos + x_a sin)
+ * for the columns (a, b) = (i, i + n_pairs), or interleaved (2 i, 2 i + 1); the
+ * other columns stay.  Angles are exact to 2^-32 of a turn at any position. */
+
+typedef struct bsp_rotary_s* bsp_rotary_t;
+
+/* frequencies: HOST double [n_pairs], radians per position, finite; n_pairs 1 ..
+ * 64; interleaved 0 or 1.  A handle of the current device that holds no memory
+ * there; immutable. */
+int bsp_rotary_create(const double* frequencies, int n_pairs, double amplitude, int interleaved, bsp_rotary_t* out);
+int bsp_rotary_destroy(bsp_rotary_t r);
+
+/* Q_out, K_out = Q, K turned (tensors as above: (z, head, row), S rows; ragged
+ * tokens: Z = 1); Hkv = 0: Q alone.  positions: DEVICE int32, row i of batch entry
+ * z at positions[z * position_stride + i], or NULL: 0 .. S - 1.  inverse 1: by the
+ * opposite angles, which is also the gradient (dQ, dK from those of Q_out, K_out).
+ * A tensor may be turned in its own place (same pointer and strides), not over
+ * another. */
+int bsp_rotary(bsp_rotary_t r, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* Q_out, const bsp_tensor_t* K,
+               const bsp_tensor_t* K_out, const int32_t* positions, int64_t position_stride, int inverse, int Z, int Hq,
+               int Hkv, int S, int D, void* stream);
+
 /* ---- diagnostics ------------------------------------------------------- */
 
 /* Evaluate, on n DEVICE floats x, the software 2^x that the attention softmax

@@ -100,6 +100,24 @@ def lib():
         L.bsp_diag_window_attempts.argtypes = [ctypes.c_int64]
         L.bsp_diag_window_tiles.argtypes = [i32] * 5 + [P, P, i32]
         L.bsp_diag_window_queries.argtypes = [i32] * 7 + [P, P]
+        L.bsp_draft_tree.argtypes = [P] * 6 + [i32] * 3 + [P]
+        L.bsp_paged_tree_attention.argtypes = [P, i32, T, T, T, T] + [P] * 6 + [i32] * 9 + [f32, P, sz, P]
+        L.bsp_draft_verify.argtypes = [P, i32, P, i64, P, i64] + [P] * 8 + [i32] * 3 + [P]
+        L.bsp_paged_keep.argtypes = [P, i32, T, T] + [P] * 5 + [i32] * 7 + [P]
+        L.bsp_paged_copy.argtypes = [P, i32, T, T, P, P] + [i32] * 5 + [P]
+        L.bsp_pages_free.argtypes = [P] * 4 + [i32] * 4 + [P]
+        L.bsp_pages_fork.argtypes = [P] * 5 + [i32] * 4 + [P, sz, P]
+        L.bsp_pages_reserve.argtypes = [P] * 7 + [i32] * 4 + [P, sz, P]
+        L.bsp_pages_compact.argtypes = [P] * 7 + [i32] * 3 + [P, sz, P]
+        L.bsp_pages_workspace.argtypes = [i32] * 3
+        L.bsp_pages_workspace.restype = sz
+        L.bsp_rotary_create.argtypes = [P, i32, ctypes.c_double, i32, ctypes.POINTER(P)]
+        L.bsp_rotary_destroy.argtypes = [P]
+        L.bsp_rotary.argtypes = [P, i32, T, T, T, T, P, i64] + [i32] * 6 + [P]
+        for name in ("bsp_draft_tree", "bsp_paged_tree_attention", "bsp_draft_verify", "bsp_paged_keep", "bsp_paged_copy",
+                     "bsp_pages_free", "bsp_pages_fork", "bsp_pages_reserve", "bsp_pages_compact", "bsp_rotary_create",
+                     "bsp_rotary_destroy", "bsp_rotary"):
+            getattr(L, name).restype = i32
         for name in ("bsp_window_create", "bsp_window_destroy", "bsp_window_info", "bsp_window_status",
                      "bsp_window_attention", "bsp_window_attention_backward", "bsp_paged_append",
                      "bsp_paged_attention", "bsp_diag_window_family", "bsp_diag_window_wait_limit",
@@ -851,3 +869,395 @@ def bsp_paged_attention(W: Window, Q, K_cache, V_cache, q_start, kv_len, table, 
     if rc:
         raise BspError(rc, "bsp_paged_attention")
     return O, lse
+
+
+# ------------------------------------------------------- drafted tokens --
+
+def _ints(W, what, t, shape):
+    """A contiguous int32 tensor of that shape on the handle's device."""
+    _shape(t, shape, what)
+    if t.dtype != torch.int32 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous int32 tensor")
+    if t.device != W.device:
+        raise ValueError(f"{what} is on {t.device}, the handle on {W.device}")
+
+
+def _floats(W, what, t, shape):
+    _shape(t, shape, what)
+    if t.dtype != torch.float32 or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous float32 tensor")
+    if t.device != W.device:
+        raise ValueError(f"{what} is on {t.device}, the handle on {W.device}")
+
+
+def _starts(q_start):
+    if q_start.dim() != 1 or q_start.shape[0] < 1:
+        raise ValueError("q_start must have one entry more than there are sequences")
+    return q_start.shape[0] - 1
+
+
+@_entry
+def bsp_draft_tree(W: Window, q_start, kv_len, parent, nodes: int, positions=None, bits=None, *, stream=None):
+    """(positions int32 [T], bits int32 [T, words]) of trees of drafted tokens:
+    parent int32 [T] (within the sequence, before the node; -1: none), `nodes`
+    the most nodes of a sequence, words = ceil(nodes / 32).  Bit a of a row:
+    the node sees node a of its sequence (itself or an ancestor, within W's
+    window).  One call serves all layers of a step."""
+    n_seq, T = _starts(q_start), parent.shape[0]
+    words = max(1, -(-int(nodes) // 32))
+    _ints(W, "q_start", q_start, (n_seq + 1,))
+    _ints(W, "kv_len", kv_len, (n_seq,))
+    _ints(W, "parent", parent, (T,))
+    if positions is None:
+        positions = torch.empty(T, dtype=torch.int32, device=W.device)
+    else:
+        _ints(W, "positions", positions, (T,))
+    if bits is None:
+        bits = torch.empty((T, words), dtype=torch.int32, device=W.device)
+    else:
+        _ints(W, "bits", bits, (T, words))
+    rc = lib().bsp_draft_tree(W.handle, q_start.data_ptr(), kv_len.data_ptr(), parent.data_ptr(), positions.data_ptr(),
+                              bits.data_ptr(), T, n_seq, words, stream)
+    if rc:
+        raise BspError(rc, "bsp_draft_tree")
+    return positions, bits
+
+
+@_entry
+def bsp_paged_tree_attention(W: Window, Q, K_cache, V_cache, q_start, kv_len, table, positions, bits, O=None, lse=None,
+                             scale: float = 1.0, *, stream=None):
+    """bsp_paged_attention of trees of drafted tokens: node i of a sequence sees
+    the keys before its tree by W's rule at positions[i], and the nodes whose
+    bits are set (positions and bits of bsp_draft_tree): (O, lse fp32 [T, Hq])."""
+    T, n_seq, max_pages, n_pages, page, Hq, Hkv, D = _paged_sizes(W, Q, K_cache, V_cache, q_start, kv_len, table)
+    if bits.dim() != 2:
+        raise ValueError("bits must be [T, words]")
+    words = bits.shape[1]
+    _ints(W, "positions", positions, (T,))
+    _ints(W, "bits", bits, (T, words))
+    if O is None:
+        O = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    else:
+        _shape(O, Q.shape, "O")
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=Q.device)
+    else:
+        _lse_ok(W, lse, (T, Hq))
+    dt = _same(W, Q, K_cache, V_cache, O)
+    n = _paged_workspace(W.device)
+    ws = torch.empty(n, dtype=torch.uint8, device=W.device)
+    rc = lib().bsp_paged_tree_attention(W.handle, dt, _rows(Q), _heads(K_cache), _heads(V_cache), _rows(O), lse.data_ptr(),
+                                        q_start.data_ptr(), kv_len.data_ptr(), table.data_ptr(), positions.data_ptr(),
+                                        bits.data_ptr(), T, n_seq, max_pages, n_pages, page, Hq, Hkv, D, words, scale,
+                                        ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_paged_tree_attention")
+    return O, lse
+
+
+def _probabilities(t, what):
+    if t.dim() != 2:
+        raise ValueError(f"{what} must be [T, V]")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError("the last dimension must be contiguous")
+    return t.stride(0)
+
+
+@_entry
+def bsp_draft_verify(W: Window, target, draft, tokens, q_start, parent, accept, sample, path=None, count=None, token=None,
+                     *, stream=None):
+    """Which drafted tokens stay: (path int32 [T], count int32 [n_seq], token
+    int32 [n_seq]), the accepted nodes of each sequence in its rows (then -1),
+    their number and the next token.  target [T, V]: the probabilities behind
+    each node; draft [T, V]: those that the node's children were drawn from, or
+    None where they were chosen; tokens int32 [T]; accept [T] and sample
+    [n_seq]: uniform float32 numbers in [0, 1)."""
+    stride = _probabilities(target, "target")
+    T, V = target.shape
+    n_seq = _starts(q_start)
+    dt = _same(W, target) if draft is None else _same(W, target, draft)
+    draft_stride = 0
+    if draft is not None:
+        draft_stride = _probabilities(draft, "draft")
+        _shape(draft, target.shape, "draft")
+    _ints(W, "tokens", tokens, (T,))
+    _ints(W, "q_start", q_start, (n_seq + 1,))
+    _ints(W, "parent", parent, (T,))
+    _floats(W, "accept", accept, (T,))
+    _floats(W, "sample", sample, (n_seq,))
+    out = []
+    for what, t, n in (("path", path, T), ("count", count, n_seq), ("token", token, n_seq)):
+        if t is None:
+            t = torch.empty(n, dtype=torch.int32, device=W.device)
+        else:
+            _ints(W, what, t, (n,))
+        out.append(t)
+    path, count, token = out
+    rc = lib().bsp_draft_verify(W.handle, dt, target.data_ptr(), stride, None if draft is None else draft.data_ptr(),
+                                draft_stride, tokens.data_ptr(), q_start.data_ptr(), parent.data_ptr(), accept.data_ptr(),
+                                sample.data_ptr(), path.data_ptr(), count.data_ptr(), token.data_ptr(), T, n_seq, V, stream)
+    if rc:
+        raise BspError(rc, "bsp_draft_verify")
+    return path, count, token
+
+
+def _cache_sizes(K_cache, V_cache):
+    if K_cache.dim() != 4 or V_cache.shape != K_cache.shape:
+        raise ValueError(f"the caches must be [n_pages, Hkv, page, D], got {tuple(K_cache.shape)} and "
+                         f"{tuple(V_cache.shape)}")
+    return K_cache.shape
+
+
+@_entry
+def bsp_paged_keep(W: Window, K_cache, V_cache, q_start, kv_len, table, path, count, *, stream=None):
+    """Move the accepted nodes' rows (path and count of bsp_draft_verify) behind
+    the context of their sequences; kv_len is still with all nodes, and becomes
+    kv_len - nodes + count afterwards."""
+    n_pages, Hkv, page, D = _cache_sizes(K_cache, V_cache)
+    n_seq = _starts(q_start)
+    if table.dim() != 2 or path.dim() != 1:
+        raise ValueError("table must be [n_seq, max_pages], path [T]")
+    T, max_pages = path.shape[0], table.shape[1]
+    _ints(W, "q_start", q_start, (n_seq + 1,))
+    _ints(W, "kv_len", kv_len, (n_seq,))
+    _ints(W, "table", table, (n_seq, max_pages))
+    _ints(W, "path", path, (T,))
+    _ints(W, "count", count, (n_seq,))
+    dt = _same(W, K_cache, V_cache)
+    rc = lib().bsp_paged_keep(W.handle, dt, _heads(K_cache), _heads(V_cache), q_start.data_ptr(), kv_len.data_ptr(),
+                              table.data_ptr(), path.data_ptr(), count.data_ptr(), T, n_seq, max_pages, n_pages, page,
+                              Hkv, D, stream)
+    if rc:
+        raise BspError(rc, "bsp_paged_keep")
+
+
+# ---------------------------------------------------- pages of the cache --
+
+def _book(W, refs, table):
+    if refs.dim() != 1 or table.dim() != 2:
+        raise ValueError("refs must be [n_pages], table [n_seq, max_pages]")
+    _ints(W, "refs", refs, refs.shape)
+    _ints(W, "table", table, table.shape)
+    return table.shape[0], table.shape[1], refs.shape[0]
+
+
+@functools.lru_cache(maxsize=64)
+def _pages_bytes(n_seq, max_pages, n_pages):
+    return int(lib().bsp_pages_workspace(n_seq, max_pages, n_pages))
+
+
+def _pages_workspace(W, sizes):
+    n = _pages_bytes(*sizes)
+    return torch.empty(n, dtype=torch.uint8, device=W.device), n
+
+
+@_entry
+def bsp_pages_free(W: Window, refs, table, kv_len, page: int, *, stream=None):
+    """Give up the pages behind each sequence's length: refs int32 [n_pages]
+    (holders of each page, 0: free) and table int32 [n_seq, max_pages] (below 0:
+    none) are changed in place."""
+    sizes = _book(W, refs, table)
+    _ints(W, "kv_len", kv_len, sizes[:1])
+    rc = lib().bsp_pages_free(W.handle, refs.data_ptr(), table.data_ptr(), kv_len.data_ptr(), *sizes, int(page), stream)
+    if rc:
+        raise BspError(rc, "bsp_pages_free")
+
+
+@_entry
+def bsp_pages_fork(W: Window, refs, table, kv_len, parent, page: int, *, stream=None):
+    """Every sequence s becomes a copy of what sequence parent[s] was (s:
+    unchanged, -1: empty), its pages shared; refs, table and kv_len are changed
+    in place."""
+    sizes = _book(W, refs, table)
+    _ints(W, "kv_len", kv_len, sizes[:1])
+    _ints(W, "parent", parent, sizes[:1])
+    ws, n = _pages_workspace(W, sizes)
+    rc = lib().bsp_pages_fork(W.handle, refs.data_ptr(), table.data_ptr(), kv_len.data_ptr(), parent.data_ptr(), *sizes,
+                              int(page), ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_pages_fork")
+
+
+@_entry
+def bsp_pages_reserve(W: Window, refs, table, kv_len, lengths, page: int, *, stream=None):
+    """Pages of their own for the positions kv_len .. lengths - 1 of every
+    sequence; refs and table are changed in place.  (src, dst) int32 [n_seq]: the
+    pages that bsp_paged_copy has to copy in each layer's caches before the
+    positions are written."""
+    sizes = _book(W, refs, table)
+    _ints(W, "kv_len", kv_len, sizes[:1])
+    _ints(W, "lengths", lengths, sizes[:1])
+    src, dst = (torch.empty(sizes[0], dtype=torch.int32, device=W.device) for _ in range(2))
+    ws, n = _pages_workspace(W, sizes)
+    rc = lib().bsp_pages_reserve(W.handle, refs.data_ptr(), table.data_ptr(), kv_len.data_ptr(), lengths.data_ptr(),
+                                 src.data_ptr(), dst.data_ptr(), *sizes, int(page), ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_pages_reserve")
+    return src, dst
+
+
+@_entry
+def bsp_pages_compact(W: Window, refs, table, refs_out=None, table_out=None, *, stream=None):
+    """The pages in use to the front: (refs_out, table_out, src, dst), the book
+    afterwards (new tensors, or refs and table themselves where given) and the
+    pages that bsp_paged_copy has to copy in each layer's caches, int32
+    [n_pages // 2]."""
+    sizes = _book(W, refs, table)
+    refs_out = torch.empty_like(refs) if refs_out is None else refs_out
+    table_out = torch.empty_like(table) if table_out is None else table_out
+    _ints(W, "refs_out", refs_out, refs.shape)
+    _ints(W, "table_out", table_out, table.shape)
+    src, dst = (torch.empty(sizes[2] // 2, dtype=torch.int32, device=W.device) for _ in range(2))
+    ws, n = _pages_workspace(W, sizes)
+    rc = lib().bsp_pages_compact(W.handle, refs.data_ptr(), table.data_ptr(), refs_out.data_ptr(), table_out.data_ptr(),
+                                 src.data_ptr(), dst.data_ptr(), *sizes, ws.data_ptr(), n, stream)
+    if rc:
+        raise BspError(rc, "bsp_pages_compact")
+    return refs_out, table_out, src, dst
+
+
+@_entry
+def bsp_paged_copy(W: Window, K_cache, V_cache, src, dst, *, stream=None):
+    """Copy page src[i] to page dst[i] of both caches [n_pages, Hkv, page, D];
+    pairs below 0 are left out."""
+    n_pages, Hkv, page, D = _cache_sizes(K_cache, V_cache)
+    _ints(W, "src", src, (src.shape[0],))
+    _ints(W, "dst", dst, (src.shape[0],))
+    rc = lib().bsp_paged_copy(W.handle, _same(W, K_cache, V_cache), _heads(K_cache), _heads(V_cache), src.data_ptr(),
+                              dst.data_ptr(), src.shape[0], n_pages, page, Hkv, D, stream)
+    if rc:
+        raise BspError(rc, "bsp_paged_copy")
+
+
+# ------------------------------------------------------ rotary positions --
+
+def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                       length: int = 4096, slow: float = 1.0, fast: float = 32.0):
+    """(frequencies float64 [rot_dim / 2] in radians per position, amplitude) for
+    bsp_rotary_create: base^(-2 i / rot_dim), for contexts `factor` times as long
+    as the `length` positions of training:
+
+        "none"    as they are
+        "linear"  divided by factor
+        "base"    of the base times factor^(rot_dim / (rot_dim - 2)): the slowest
+                  pair turns 1 / factor as fast, the fastest as before
+        "parts"   pairs that turn more than `fast` times over `length` as they
+                  are, less than `slow` times divided by factor, a ramp in turns
+                  between; amplitude 0.1 ln(factor) + 1
+    """
+    if rot_dim < 2 or rot_dim % 2:
+        raise ValueError("rot_dim must be an even number of columns")
+    if not (base > 0 and factor > 0 and length > 0):
+        raise ValueError("base, factor and length must be positive")
+    if scaling not in ("none", "linear", "base", "parts"):
+        raise ValueError(f"unknown scaling {scaling!r}")
+    i = np.arange(rot_dim // 2, dtype=np.float64)
+    if scaling == "base" and rot_dim > 2:
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = float(base) ** (-2.0 * i / rot_dim)
+    if scaling == "linear":
+        f = f / factor
+    if scaling != "parts":
+        return f, 1.0
+    if not fast > slow:
+        raise ValueError("fast must be above slow")
+    kept = np.clip((length * f / (2 * np.pi) - slow) / (fast - slow), 0.0, 1.0)
+    return f * kept + f / factor * (1.0 - kept), 0.1 * float(np.log(factor)) + 1.0
+
+
+class Rotary:
+    """Owning wrapper of a bsp_rotary_t handle: the frequencies of the pairs of a
+    head's first columns, on one device."""
+
+    def __init__(self, handle: ctypes.c_void_p, device: torch.device, pairs: int):
+        self.handle, self.device, self.pairs = handle, device, pairs
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.bsp_rotary_destroy(self.handle)
+            self.handle = None
+
+
+def bsp_rotary_create(frequencies, amplitude: float = 1.0, interleaved: bool = False) -> Rotary:
+    """Rotary positions on the current device: frequencies (radians per position)
+    of the pairs (i, i + n) of a head's first 2 n columns, interleaved: (2 i,
+    2 i + 1)."""
+    f = np.ascontiguousarray(np.asarray(frequencies, dtype=np.float64))
+    if f.ndim != 1:
+        raise ValueError("frequencies must be a list of numbers")
+    h = ctypes.c_void_p()
+    _check(lib().bsp_rotary_create(f.ctypes.data, len(f), float(amplitude), int(bool(interleaved)), ctypes.byref(h)),
+           "bsp_rotary_create")
+    return Rotary(h, torch.device("cuda", torch.cuda.current_device()), len(f))
+
+
+def _turned_view(t):
+    """bsp_tensor_t, batch entries and heads of [Z, H, S, D] or [T, H, D]."""
+    if t.dim() == 4:
+        return _heads(t), t.shape[0], t.shape[1], t.shape[2]
+    return _rows(t), 1, t.shape[1], t.shape[0]
+
+
+@_entry
+def bsp_rotary(R: Rotary, Q, K=None, positions=None, Q_out=None, K_out=None, *, inverse: bool = False, stream=None):
+    """(Q_out, K_out): Q [Z, Hq, S, D] and K [Z, Hkv, S, D] (or ragged [T, H, D];
+    K None: Q alone) turned by their rows' positions, int32 [Z, S], [S] ([T]) or
+    None for 0 .. S - 1; inverse: by the opposite angles.  Strides as for
+    bsp_window_attention; Q_out may be Q itself, K_out K."""
+    if Q.dim() not in (3, 4) or (K is not None and K.dim() != Q.dim()):
+        raise ValueError("Q and K must be [Z, heads, rows, D] or [T, heads, D]")
+    Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) if Q_out is None else Q_out
+    _shape(Q_out, Q.shape, "Q_out")
+    q, Z, Hq, S = _turned_view(Q)
+    D, Hkv, k, ko, ts = Q.shape[-1], 0, None, None, [Q, Q_out]
+    if K is not None:
+        K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device) if K_out is None else K_out
+        _shape(K_out, K.shape, "K_out")
+        k, Zk, Hkv, Sk = _turned_view(K)
+        if (Zk, Sk, K.shape[-1]) != (Z, S, D):
+            raise ValueError(f"K must have Q's batch, rows and head size, got {tuple(K.shape)}")
+        if Hkv < 1:
+            raise ValueError("K must have a head")
+        ko = _turned_view(K_out)[0]
+        ts += [K, K_out]
+    elif K_out is not None:
+        raise ValueError("K_out without K")
+    step = 0
+    if positions is not None:
+        if positions.dim() == 2 and Q.dim() == 4:
+            _ints(R, "positions", positions, (Z, S))
+            step = S
+        else:
+            _ints(R, "positions", positions, (S,))
+    rc = lib().bsp_rotary(R.handle, _same(R, *ts), q, _turned_view(Q_out)[0], k, ko,
+                          None if positions is None else positions.data_ptr(), step, int(bool(inverse)), Z, Hq, Hkv, S, D,
+                          stream)
+    if rc:
+        raise BspError(rc, "bsp_rotary")
+    return Q_out, K_out
+
+
+class _RotaryPositions(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, Q, K, positions, R, inverse):
+        ctx.set_materialize_grads(False)
+        ctx.save_for_backward(positions)
+        ctx.R, ctx.inverse = R, inverse
+        return bsp_rotary(R, _taken(Q), None if K is None else _taken(K), positions, inverse=inverse)
+
+    @staticmethod
+    def backward(ctx, dQ, dK):
+        positions, = ctx.saved_tensors
+        got = [g for g in (dQ, dK) if g is not None]
+        if not got:
+            return None, None, None, None, None
+        got = list(_RotaryPositions.apply(got[0], got[1] if len(got) > 1 else None, positions, ctx.R, not ctx.inverse))
+        return (got.pop(0) if dQ is not None else None, got.pop(0) if dK is not None else None, None, None, None)
+
+
+def rotary(R: Rotary, Q, K=None, positions=None):
+    """Differentiable bsp_rotary (torch autograd): (Q_out, K_out); tensors whose
+    strides the kernels do not take are copied.  Its gradient may be
+    differentiated again, and is captured into a CUDA graph as
+    window_attention's."""
+    return _RotaryPositions.apply(Q, K, positions, R, False)

@@ -75,7 +75,11 @@ struct Args {
     float* slots;
 };
 
-template <typename T, int DP, int MODE>
+// TREE: the tokens are nodes of trees (a ragged batch), each with a position and
+// bits of its own; keys before a tree's first slot follow the rule at the node's
+// position, the others the node's bits.  Only the tiles that hold a tree's slots,
+// the last of each sequence, are looked at bit by bit.
+template <typename T, int DP, int MODE, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                  const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args args,
@@ -456,6 +460,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         uint32_t g = 0, tc = 0, xg = 0;  // xg: half-row exchanges so far
         while (true) {
             int ns, s0, n_s, lo_tile, rows, pos;
+            int ctx = 0, end = 0, node = 0;  // TREE: its first slot, the last one's successor, the row's token
             Seen seen;
             {
                 Work w;
@@ -464,8 +469,16 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 rows = w.nt * p.G;
                 // rows past the tile's last see what its last row sees; they are not stored
                 pos = w.a + (int)((imin(row, rows - 1) * inv_g) >> 16);
-                seen.first = w.a + (int)((imin(quad * 32, rows - 1) * inv_g) >> 16);
-                seen.last = w.a + (int)((imin(quad * 32 + 31, rows - 1) * inv_g) >> 16);
+                if constexpr (TREE) {
+                    ctx = w.a, end = w.zhi + 1;
+                    node = w.row0 + pos - w.a;
+                    pos = imax(p.pos[node], ctx);
+                    seen.first = __reduce_min_sync(0xffffffffu, pos);
+                    seen.last = __reduce_max_sync(0xffffffffu, pos);
+                } else {
+                    seen.first = w.a + (int)((imin(quad * 32, rows - 1) * inv_g) >> 16);
+                    seen.last = w.a + (int)((imin(quad * 32 + 31, rows - 1) * inv_g) >> 16);
+                }
             }
             const bool idle = quad * 32 >= rows;  // no live row in this warp's lanes
             const int low = pos - p.window + 1;
@@ -475,7 +488,19 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 const uint32_t sb = g % 3;
                 const int kt = s0 + n < n_s ? s0 + n : lo_tile + (s0 + n - n_s);
                 const int kb = (kt << 7) + wg * 64;  // first key of this half
-                const bool full = seen.all(p, kb), skip = seen.none(p, kb);
+                bool full = seen.all(p, kb), skip = seen.none(p, kb);
+                unsigned long long vis = 0;
+                if constexpr (TREE) {
+                    if (kb + 64 > ctx) {  // slots of the tree's nodes among these
+                        full = false;
+                        skip = kb >= end;
+                        if (!skip && !idle)
+                            vis = (row_keys(ctx - 1, low, p.sinks, kb) |
+                                   bits_at(p.bits + (int64_t)node * p.words, p.words, kb - ctx)) & below(imin(end - kb, 64));
+                    } else if (!full) {
+                        vis = row_keys(pos, low, p.sinks, kb);
+                    }
+                }
                 bool ok = wait(&s_full[sb], (g / 3) & 1, ab);
                 if (!__all_sync(0xffffffffu, ok)) goto softmax_done;
                 if (idle) {
@@ -491,7 +516,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 float mx = -INFINITY;
                 if (!skip) {
                     tmem_ld64_sync(srow, srow + 32, *reinterpret_cast<uint32_t(*)[64]>(x));
-                    if (!full) hide(x, row_keys(pos, low, p.sinks, kb));
+                    if (!full) hide(x, TREE ? vis : row_keys(pos, low, p.sinks, kb));
                     float m8[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) m8[k] = fmax3(x[k], x[k + 8], x[k + 16]);
@@ -606,7 +631,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     }
 }
 
-template <typename T, int DP, int MODE>
+template <typename T, int DP, int MODE, bool TREE>
 int launch(Call& c) {
     constexpr bool PAGED = MODE != kDense;
     const int is_bf16 = std::is_same<T, __nv_bfloat16>::value;
@@ -617,7 +642,7 @@ int launch(Call& c) {
     if (!rc) rc = key_map(&mk, c.K, c, is_bf16, rows);
     if (!rc) rc = key_map(&mv, c.V, c, is_bf16, rows);
     if (rc) return rc;
-    auto kern = window_tc_kernel<T, DP, MODE>;
+    auto kern = window_tc_kernel<T, DP, MODE, TREE>;
     constexpr int smem = Smem<DP>::kAlloc;
     static std::atomic<uint64_t> prepared{0};
     if ((rc = prepare_kernel(kern, smem, prepared))) return rc;
@@ -631,14 +656,15 @@ int launch(Call& c) {
     return cut ? launch_join(c, kTcRows, grid, false) : BSP_OK;
 }
 
-template <typename T, int MODE>
+template <typename T, int MODE, bool TREE = false>
 int by_width(Call& c) {
-    return c.D <= 64 ? launch<T, 64, MODE>(c) : launch<T, 128, MODE>(c);
+    return c.D <= 64 ? launch<T, 64, MODE, TREE>(c) : launch<T, 128, MODE, TREE>(c);
 }
 
 template <typename T>
 int by_mode(Call& c) {
     if (!c.p.paged) return by_width<T, kDense>(c);
+    if (c.p.words) return by_width<T, kRagged, true>(c);
     return c.p.TQ == 1 && c.p.nseg <= kThreads ? by_width<T, kPlain>(c) : by_width<T, kRagged>(c);
 }
 
@@ -651,6 +677,7 @@ int launch_forward_tc(Call& c) {
     // as fill 128 rows
     c.p.kshift = 7;
     c.p.TQ = c.p.paged && c.p.T <= c.p.nseg ? 1 : kTcRows / c.p.G;
+    if (c.p.words) c.p.TQ = imin(c.p.TQ, 32 * c.p.words);  // no sequence has more
     const int64_t keys = c.p.paged ? (int64_t)c.p.max_pages << c.p.page_shift : c.p.Sk;
     c.p.attempts = wait_attempts(c, (keys >> 7) + 2);
     return c.dtype == BSP_BF16 ? by_mode<__nv_bfloat16>(c) : by_mode<__half>(c);

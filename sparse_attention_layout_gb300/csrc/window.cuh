@@ -44,6 +44,7 @@ namespace win {
 constexpr int kMaxLen = 1 << 30;
 constexpr int kMaxGroup = 64;      // query heads per KV head
 constexpr int kMaxSeqs = 16384;    // sequences of one ragged call (their tile counts sit in shared memory)
+constexpr int kMaxNodes = 1024;    // drafted tokens of a sequence
 
 // Attempts of a bounded wait of the tensor-core kernels.  A failed one takes 1.4
 // us (measured: 20 in 27.6 us), and tens of cycles at the least: 2^21 are 3 s, and
@@ -93,6 +94,17 @@ BSP_HD Span span_of(int a, int b, int window, int sinks, int kshift) {
     return s;
 }
 
+#if defined(__CUDACC__)
+// Bits o .. o + 63 of a row of `words` words, 0 outside (o > -64).
+__device__ __forceinline__ unsigned long long bits_at(const uint32_t* row, int words, int o) {
+    const int w = o >> 5;
+    uint32_t v[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) v[k] = (unsigned)(w + k) < (unsigned)words ? row[w + k] : 0u;
+    return (unsigned long long)__funnelshift_r(v[1], v[2], o & 31) << 32 | __funnelshift_r(v[0], v[1], o & 31);
+}
+#endif
+
 struct Seg {
     int t0;     // first token's row in the ragged tensors (dense: 0)
     int qlen;   // query tokens
@@ -101,6 +113,8 @@ struct Seg {
 };
 
 // A query tile: tokens tok0 .. tok0 + nt - 1 of its segment at positions a .. b.
+// Of a tree of drafted tokens: a is the position of the tree's first node, b the
+// last slot, whichever of its nodes the tile holds.
 struct QTile {
     int tok0, nt, a, b;
 };
@@ -119,9 +133,14 @@ struct Prob {
     const int* table;
     int* status;
     int attempts;   // of the wait for a tile (tensor-core kernels)
+    // trees of drafted tokens: positions, and the nodes that each sees (words 0: none)
+    const int* pos;
+    const uint32_t* bits;
+    int words;
 
     BSP_HD bool bad_seg(int q0, int q1, int kv) const {
-        return q0 < 0 || q1 < q0 || q1 > T || kv < 0 || kv > (max_pages << page_shift);
+        return q0 < 0 || q1 < q0 || q1 > T || kv < 0 || kv > (max_pages << page_shift) ||
+               (words && (q1 - q0 > 32 * words || q1 - q0 > kv));
     }
 #if defined(__CUDACC__)
     __device__ __forceinline__ Seg seg(int s) const {
@@ -138,8 +157,8 @@ struct Prob {
         QTile q;
         q.tok0 = t * TQ;
         q.nt = imin(TQ, g.qlen - q.tok0);
-        q.a = g.kvlen - g.qlen + q.tok0;
-        q.b = q.a + q.nt - 1;
+        q.a = g.kvlen - g.qlen + (words ? 0 : q.tok0);
+        q.b = words ? g.kvlen - 1 : q.a + q.nt - 1;
         return q;
     }
     BSP_HD Span span(const QTile& q) const { return span_of(q.a, q.b, window, sinks, kshift); }

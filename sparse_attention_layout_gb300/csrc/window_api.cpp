@@ -3,24 +3,27 @@
 // kernels.
 #include <cstdint>
 #include <cstdlib>
-#include <initializer_list>
 #include <new>
 
-#include "window.h"
+#include "window_args.h"
 
 namespace {
 
 using bsp::win::Call;
+using bsp::win::check_handle;
+using bsp::win::check_workspace;
+using bsp::win::clash;
 using bsp::win::kMaxGroup;
 using bsp::win::kMaxLen;
 using bsp::win::kMaxSeqs;
+using bsp::win::make_view;
 using bsp::win::Prob;
+using bsp::win::round_up;
+using bsp::win::valid_d;
+using bsp::win::valid_dtype;
 using bsp::win::View;
 
-bool valid_dtype(int d) { return d == BSP_F32 || d == BSP_BF16 || d == BSP_F16; }
 bool valid_scale(float s) { return s > 0.f && s <= 3.0e38f; }
-bool valid_d(int D) { return D >= 16 && D <= 128 && D % 16 == 0; }
-
 bool force_simt() {
     const char* e = std::getenv("BSP_FORCE_SIMT");
     return e && e[0] == '1';
@@ -33,63 +36,6 @@ bool on_tensor_cores(bsp_window_t w, int dtype) {
     w->family = tc ? 1 : 2;
     return tc;
 }
-
-int check_handle(bsp_window_t w, int dtype) {
-    if (!w || !valid_dtype(dtype)) return BSP_ERR_INVALID_ARG;
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return BSP_ERR_CUDA;
-    return dev == w->device ? BSP_OK : BSP_ERR_INVALID_ARG;
-}
-
-// A tensor of extents n0, n1, n2 and D contiguous elements: pointer and the
-// strides that are used must be multiples of 16 bytes, strides positive (a
-// stride whose extent is 1 is never used).  Outputs must not overlap
-// themselves: taken from the smallest, each stride covers what lies below it.
-int make_view(const bsp_tensor_t* t, int64_t n0, int64_t n1, int64_t n2, int D, int elt, bool out, View* v) {
-    if (!t || !t->ptr) return BSP_ERR_INVALID_ARG;
-    if ((uintptr_t)t->ptr & 15u) return BSP_ERR_ALIGNMENT;
-    const int64_t n[3] = {n0, n1, n2};
-    v->ptr = t->ptr;
-    for (int i = 0; i < 3; ++i) {
-        int64_t s = t->stride[i];
-        if (n[i] <= 1) {
-            s = D;  // any legal value: the index is always 0
-        } else {
-            if (s <= 0 || s > (int64_t)1 << 38) return BSP_ERR_INVALID_ARG;
-            if (s * elt % 16) return BSP_ERR_ALIGNMENT;
-        }
-        v->s[i] = s;
-    }
-    if (out) {
-        int64_t below = D;  // elements from the first to the last of the dimensions so far, plus one
-        bool used[3] = {false, false, false};
-        for (int k = 0; k < 3; ++k) {
-            int at = -1;
-            for (int i = 0; i < 3; ++i)
-                if (!used[i] && n[i] > 1 && (at < 0 || v->s[i] < v->s[at])) at = i;
-            if (at < 0) break;
-            used[at] = true;
-            if (v->s[at] < below) return BSP_ERR_INVALID_ARG;
-            below += v->s[at] * (n[at] - 1);
-        }
-    }
-    return BSP_OK;
-}
-
-// An output in an input's place (or another output's) would be overwritten
-// while other blocks still read it.
-bool clash(std::initializer_list<const bsp_tensor_t*> out, std::initializer_list<const bsp_tensor_t*> in) {
-    for (auto o = out.begin(); o != out.end(); ++o) {
-        if (!(*o)->ptr) continue;
-        for (const bsp_tensor_t* i : in)
-            if (i->ptr == (*o)->ptr) return true;
-        for (auto q = out.begin(); q != o; ++q)
-            if ((*q)->ptr == (*o)->ptr) return true;
-    }
-    return false;
-}
-
-size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 // Workspace: one record per CTA, two partial-result slots per CTA, and for the
 // backward the query rows' statistics, in tiles, and what fp16 scales dS by.
@@ -113,15 +59,8 @@ size_t stats_bytes(int Z, int Hq, int Hkv, int Sq) {
 }
 
 void set_rule(const bsp_window_s* w, Prob* p) {
-    p->window = w->window == 0 || w->window > kMaxLen ? kMaxLen : w->window;
-    p->sinks = w->sinks > kMaxLen ? kMaxLen : w->sinks;
+    bsp::win::set_rule(w, &p->window, &p->sinks);
     p->status = w->status;
-}
-
-int check_workspace(const void* ws, size_t have, size_t need) {
-    if (!ws) return BSP_ERR_INVALID_ARG;
-    if ((uintptr_t)ws & 255u) return BSP_ERR_ALIGNMENT;
-    return have < need ? BSP_ERR_INVALID_ARG : BSP_OK;
 }
 
 int check_dense(int Z, int Hq, int Hkv, int Sq, int Sk, int D, float scale) {
@@ -305,8 +244,9 @@ extern "C" int bsp_window_attention_backward(bsp_window_t w, int dtype, const bs
 }
 
 namespace {
+// `nodes`: the most a tree may have, 0 for plain new tokens.
 int paged_prob(bsp_window_t w, const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int T, int n_seq,
-               int max_pages, int n_pages, int page, int Hq, int Hkv, int D, Prob* p) {
+               int max_pages, int n_pages, int page, int Hq, int Hkv, int D, int nodes, Prob* p) {
     if (T < 0 || n_seq < 0 || max_pages < 1 || n_pages < 1 || Hq < 1 || Hkv < 1 || !valid_d(D)) return BSP_ERR_INVALID_ARG;
     if (page != 16 && page != 32 && page != 64 && page != 128) return BSP_ERR_INVALID_ARG;
     if (Hq % Hkv) return BSP_ERR_INVALID_ARG;
@@ -318,7 +258,8 @@ int paged_prob(bsp_window_t w, const int32_t* q_start, const int32_t* kv_len, co
     // steps go over the tables' keys or, if they are fewer, its sinks and windows
     const int64_t tq = 64 / (Hq / Hkv), qt = T <= n_seq ? T : (T + tq - 1) / tq + n_seq;
     const int64_t all = ((int64_t)max_pages * page + 63) / 64 + 1;
-    const int64_t near = ((int64_t)p->sinks + 63) / 64 + ((int64_t)p->window + tq + 63) / 64 + 1;
+    const int64_t span = nodes > tq ? nodes : tq;  // of the rows' own slots
+    const int64_t near = ((int64_t)p->sinks + 63) / 64 + ((int64_t)p->window + span + 63) / 64 + 1;
     const int64_t kt = near < all ? near : all;
     if (qt > 0 && (kt > (1ll << 31) / qt || Hkv > (1ll << 31) / (qt * kt) - 1)) return BSP_ERR_UNSUPPORTED;
     if (T == 0 || n_seq == 0) return BSP_OK;
@@ -342,7 +283,7 @@ extern "C" int bsp_paged_append(bsp_window_t w, int dtype, const bsp_tensor_t* K
                                 int n_pages, int page, int Hkv, int D, void* stream) {
     int rc = check_handle(w, dtype);
     Prob p{};
-    if (!rc) rc = paged_prob(w, q_start, kv_len, table, T, n_seq, max_pages, n_pages, page, Hkv, Hkv, D, &p);
+    if (!rc) rc = paged_prob(w, q_start, kv_len, table, T, n_seq, max_pages, n_pages, page, Hkv, Hkv, D, 0, &p);
     if (rc || T == 0 || n_seq == 0) return rc;
     const int elt = dtype == BSP_F32 ? 4 : 2;
     View kn, vn, kc, vc;
@@ -355,17 +296,24 @@ extern "C" int bsp_paged_append(bsp_window_t w, int dtype, const bsp_tensor_t* K
     return bsp::win::launch_append(w, dtype, kn, vn, kc, vc, p, D, (cudaStream_t)stream);
 }
 
-extern "C" int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K_cache,
-                                   const bsp_tensor_t* V_cache, const bsp_tensor_t* O, float* lse,
-                                   const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int T,
-                                   int n_seq, int max_pages, int n_pages, int page, int Hq, int Hkv, int D, float scale,
-                                   void* workspace, size_t workspace_bytes, void* stream) {
+namespace {
+// Attention over pages: of plain new tokens, or (words > 0) of trees.
+int paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K_cache,
+                    const bsp_tensor_t* V_cache, const bsp_tensor_t* O, float* lse, const int32_t* q_start,
+                    const int32_t* kv_len, const int32_t* table, const int32_t* pos, const uint32_t* bits, int words, int T,
+                    int n_seq, int max_pages, int n_pages, int page, int Hq, int Hkv, int D, float scale, void* workspace,
+                    size_t workspace_bytes, void* stream) {
     int rc = check_handle(w, dtype);
     Call c{};
-    if (!rc) rc = paged_prob(w, q_start, kv_len, table, T, n_seq, max_pages, n_pages, page, Hq, Hkv, D, &c.p);
+    if (!rc) rc = paged_prob(w, q_start, kv_len, table, T, n_seq, max_pages, n_pages, page, Hq, Hkv, D, 32 * words, &c.p);
     if (rc) return rc;
     if (!valid_scale(scale)) return BSP_ERR_INVALID_ARG;
     if (T == 0 || n_seq == 0) return BSP_OK;
+    if (words) {
+        if (!pos || !bits) return BSP_ERR_INVALID_ARG;
+        if (((uintptr_t)pos | (uintptr_t)bits) & 3u) return BSP_ERR_ALIGNMENT;
+        c.p.pos = pos, c.p.bits = bits, c.p.words = words;
+    }
     const int elt = dtype == BSP_F32 ? 4 : 2;
     if ((rc = make_view(Q, 1, Hq, T, D, elt, false, &c.Q))) return rc;
     if ((rc = make_view(K_cache, n_pages, Hkv, page, D, elt, false, &c.K))) return rc;
@@ -381,6 +329,28 @@ extern "C" int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t
     c.slots = reinterpret_cast<float*>(static_cast<char*>(workspace) + cuts_bytes());
     c.stream = (cudaStream_t)stream;
     return on_tensor_cores(w, dtype) ? bsp::win::launch_forward_tc(c) : bsp::win::launch_forward_simt(c);
+}
+}  // namespace
+
+extern "C" int bsp_paged_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K_cache,
+                                   const bsp_tensor_t* V_cache, const bsp_tensor_t* O, float* lse,
+                                   const int32_t* q_start, const int32_t* kv_len, const int32_t* table, int T,
+                                   int n_seq, int max_pages, int n_pages, int page, int Hq, int Hkv, int D, float scale,
+                                   void* workspace, size_t workspace_bytes, void* stream) {
+    return paged_attention(w, dtype, Q, K_cache, V_cache, O, lse, q_start, kv_len, table, nullptr, nullptr, 0, T, n_seq,
+                           max_pages, n_pages, page, Hq, Hkv, D, scale, workspace, workspace_bytes, stream);
+}
+
+extern "C" int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* K_cache,
+                                        const bsp_tensor_t* V_cache, const bsp_tensor_t* O, float* lse,
+                                        const int32_t* q_start, const int32_t* kv_len, const int32_t* table,
+                                        const int32_t* positions, const uint32_t* bits, int T, int n_seq, int max_pages,
+                                        int n_pages, int page, int Hq, int Hkv, int D, int words, float scale,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+    if (words < 1) return BSP_ERR_INVALID_ARG;
+    if (words > bsp::win::kMaxNodes / 32) return BSP_ERR_UNSUPPORTED;
+    return paged_attention(w, dtype, Q, K_cache, V_cache, O, lse, q_start, kv_len, table, positions, bits, words, T, n_seq,
+                           max_pages, n_pages, page, Hq, Hkv, D, scale, workspace, workspace_bytes, stream);
 }
 
 extern "C" int bsp_diag_window_wait_limit(bsp_window_t w, int attempts) {

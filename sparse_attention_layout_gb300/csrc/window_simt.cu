@@ -185,7 +185,8 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
         if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
 }
 
-template <typename T, int DP, bool PAGED>
+// TREE: the tokens are nodes of trees of drafted tokens (pages only).
+template <typename T, int DP, bool PAGED, bool TREE>
 __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __grid_constant__ Args A,
                                                      const __grid_constant__ SimtPlan plan) {
     constexpr int NG = DP / 64, PITCH = DP + 4;
@@ -214,12 +215,16 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
             return at<const T>(A.Q, w.z, (int64_t)w.hk * p.G + r % p.G, (int64_t)it.g.t0 + q.tok0 + r / p.G);
         });
         float m[4], l[4];
-        int pos[4];
+        int pos[4], node[4];  // TREE: the row's token
         float2 acc[4][NG][2];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int r = ty + 16 * u;
             pos[u] = r < rows ? q.a + r / p.G : -1;  // dead rows see nothing
+            if (TREE && r < rows) {
+                node[u] = it.g.t0 + q.tok0 + r / p.G;
+                pos[u] = imax(p.pos[node[u]], q.a);
+            }
             m[u] = -INFINITY;
             l[u] = 0.f;
 #pragma unroll
@@ -229,6 +234,13 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
         // before every row's window) are not read at all
         auto wanted = [&](int j) { return j <= q.b && (j >= lo || j < p.sinks); };
         auto first_key = [&](int n) { return sp.tile(it.s0 + n) << kShift; };
+        // TREE: q.a is the first node's slot, q.b the last one's; the nodes' slots are
+        // seen where the row's bits say so
+        auto sees = [&](int u, int j) {
+            if (!TREE || j < q.a) return visible(pos[u], j, p);
+            const int b = j - q.a;
+            return pos[u] >= 0 && j <= q.b && (p.bits[(int64_t)node[u] * p.words + (b >> 5)] >> (b & 31) & 1);
+        };
         auto find_pages = [&](int n) {  // by the barrier before the step's copies
             if (!PAGED || threadIdx.x >= R || n >= it.ns) return;
             const int j = first_key(n) + threadIdx.x;
@@ -274,7 +286,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
                 float cm = -INFINITY;
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
-                    s[u][v] = visible(pos[u], kb + tx + 16 * v, p) ? s[u][v] * A.c2 : -INFINITY;
+                    s[u][v] = sees(u, kb + tx + 16 * v) ? s[u][v] * A.c2 : -INFINITY;
                     cm = fmaxf(cm, s[u][v]);
                 }
                 cm = row_max(cm);
@@ -582,8 +594,9 @@ int forward_t(Call& c, const Args& a, int grid) {
     bool cut = true;
     int rc = c.p.paged ? BSP_OK : query_plan(c, grid, &plan.tab, plan.s, &cut);
     if (rc) return rc;
-    rc = c.p.paged ? launch(forward_kernel<T, DP, true>, grid, smem, c.stream, a, plan)
-                   : launch(forward_kernel<T, DP, false>, grid, smem, c.stream, a, plan);
+    rc = c.p.words   ? launch(forward_kernel<T, DP, true, true>, grid, smem, c.stream, a, plan)
+         : c.p.paged ? launch(forward_kernel<T, DP, true, false>, grid, smem, c.stream, a, plan)
+                     : launch(forward_kernel<T, DP, false, false>, grid, smem, c.stream, a, plan);
     return rc || !cut ? rc : launch_join(c, R, grid, false);
 }
 
