@@ -98,77 +98,118 @@ struct Tree {
     float px[kMaxNodes], qx[kMaxNodes], u[kMaxNodes];
 };
 
-// A sum in two fp32 parts: the rounding error of every addition goes to the
-// second, so a sum of some thousand terms is off by 2^-46 of itself.
-struct Sum2 {
+// A number in two fp32 parts, the second the rounding error of the first, and a
+// sum whose additions' errors all go to its second part: some thousand terms are
+// off by 2^-45 of their sum.  (GB300 has two fp64 lanes an SM, and an fp64
+// operation takes over 100 cycles: with them for the walk and the sums of the
+// warps, one sequence of 32000 entries took 18 us, not 11, and with every warp
+// adding up the sums 69.)
+struct Two {
     float hi = 0.f, lo = 0.f;
+    __device__ __forceinline__ Two() {}
+    __device__ __forceinline__ Two(float h) : hi(h) {}
+    __device__ __forceinline__ Two(float h, float l) : hi(h), lo(l) {}
     __device__ __forceinline__ void add(float x, float e) {
         const float t = hi + x, b = t - hi;
         lo += ((hi - (t - b)) + (x - b)) + e;
         hi = t;
     }
-    __device__ __forceinline__ double value() const { return (double)hi + (double)lo; }
+    __device__ __forceinline__ Two whole() const {  // parts that do not overlap
+        const float h = hi + lo;
+        return Two(h, lo - (h - hi));
+    }
+    __device__ __forceinline__ bool above(Two x) const { return (hi - x.hi) + (lo - x.lo) > 0.f; }
 };
+__device__ __forceinline__ Two operator+(Two a, Two b) {
+    a.add(b.hi, b.lo);
+    return a.whole();
+}
+__device__ __forceinline__ Two operator-(Two a, Two b) { return a + Two(-b.hi, -b.lo); }
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    const float h = __fmul_rn(a.hi, b.hi);  // (not to be joined with an addition)
+    return Two(h, fmaf(a.hi, b.lo, fmaf(a.lo, b.hi, fmaf(a.hi, b.hi, -h)))).whole();
+}
+__device__ __forceinline__ Two from_lane(Two x, int lane) {
+    return Two(__shfl_sync(0xffffffffu, x.hi, lane), __shfl_sync(0xffffffffu, x.lo, lane));
+}
+// the sum over a warp, in lane 0 (other lanes' may be rounded otherwise)
+__device__ __forceinline__ Two over_warp(Two x) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x.add(__shfl_down_sync(0xffffffffu, x.hi, o), __shfl_down_sync(0xffffffffu, x.lo, o));
+    return x.whole();
+}
+// inclusive prefix over the lanes of a warp
+__device__ __forceinline__ Two warp_scan(Two x, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const Two z(__shfl_up_sync(0xffffffffu, x.hi, o), __shfl_up_sync(0xffffffffu, x.lo, o));
+        if (lane >= o) x = z + x;
+    }
+    return x;
+}
 
-// The rows at the node where the walk stands.
+// What is left of a row of the target: p - c q where that is positive, or p
+// without some tokens.
 template <typename T, bool DRAWN>
 struct Rows {
     static constexpr int N = 16 / sizeof(T);
     const T *p, *q;  // q: null while nothing was rejected
-    float ch, cl;    // what of q is taken away, in two parts
+    Two c;
     const int* out;  // tokens taken out of p, n_out of them
     int n_out;
     int V, off;      // a 16-byte piece k holds entries k N - off ..
 
-    // The piece's probabilities that are left, in two parts; entries of nothing
-    // (outside the row, not positive, no number) are 0.
-    __device__ __forceinline__ void load(int k, float (&a)[N], float (&b)[N]) const {
-        const int i0 = k * N - off;
-        if (i0 >= 0 && i0 + N <= V) {
-            Vec16<T>::load(p + i0, a);
-            if (DRAWN && q) {
-                if (((uintptr_t)(q + i0) & 15) == 0) {
-                    Vec16<T>::load(q + i0, b);
-                } else {
-#pragma unroll
-                    for (int j = 0; j < N; ++j) b[j] = to_f32(q[i0 + j]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const bool in = i0 + j >= 0 && i0 + j < V;
-                a[j] = in ? to_f32(p[i0 + j]) : 0.f;
-                if (DRAWN && q) b[j] = in ? to_f32(q[i0 + j]) : 0.f;
-            }
-        }
+    __device__ __forceinline__ uint4 piece(const T* row, int i0) const {
+        if (i0 >= 0 && i0 + N <= V && ((uintptr_t)(row + i0) & 15) == 0) return *reinterpret_cast<const uint4*>(row + i0);
+        return edge(row, i0, V);
     }
-    __device__ __forceinline__ void left(int k, float (&a)[N], float (&b)[N]) const {
+    static __device__ __noinline__ uint4 edge(const T* row, int i0, int V) {
+        uint32_t w[4] = {};
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (i0 + j >= 0 && i0 + j < V) {
+                if constexpr (sizeof(T) == 4)
+                    w[j] = __float_as_uint(row[i0 + j]);
+                else
+                    w[j >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[i0 + j] << (j & 1) * 16;
+            }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __device__ __forceinline__ void load(int k, uint4& a, uint4& b) const {
+        a = piece(p, k * N - off);
+        if (DRAWN && q) b = piece(q, k * N - off);
+    }
+    // the piece's entries in two parts; entries of nothing (outside the row, not
+    // positive, no number) are 0
+    __device__ __forceinline__ void left(int k, const uint4& a, const uint4& b, float (&x)[N], float (&y)[N]) const {
+        const T *pe = reinterpret_cast<const T*>(&a), *qe = reinterpret_cast<const T*>(&b);
         if (DRAWN && q) {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 // p - c q, every rounding error kept
-                const float m = ch * b[j], e = fmaf(cl, b[j], fmaf(ch, b[j], -m));
-                const float d = a[j] - m, t = d - a[j];
-                const float r = ((a[j] - (d - t)) - (m + t)) - e;
+                const float u = to_f32(pe[j]), v = to_f32(qe[j]);
+                const float m = __fmul_rn(c.hi, v), e = fmaf(c.lo, v, fmaf(c.hi, v, -m));
+                const float d = u - m, t = d - u;
+                const float r = ((u - (d - t)) - (m + t)) - e;
                 const bool on = d + r > 0.f;
-                a[j] = on ? d : 0.f;
-                b[j] = on ? r : 0.f;
+                x[j] = on ? d : 0.f;
+                y[j] = on ? r : 0.f;
             }
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                a[j] = a[j] > 0.f ? a[j] : 0.f;
-                b[j] = 0.f;
+                const float u = to_f32(pe[j]);
+                x[j] = u > 0.f ? u : 0.f;
+                y[j] = 0.f;
             }
             if (!DRAWN) {
                 const int i0 = k * N - off;
 #pragma unroll 1
-                for (int x = 0; x < n_out; ++x) {
-                    const unsigned at = (unsigned)(out[x] - i0);
+                for (int o = 0; o < n_out; ++o) {
+                    const unsigned at = (unsigned)(out[o] - i0);
                     if (at < (unsigned)N) {
 #pragma unroll
-                        for (int j = 0; j < N; ++j) a[j] = at == (unsigned)j ? 0.f : a[j];
+                        for (int j = 0; j < N; ++j) x[j] = at == (unsigned)j ? 0.f : x[j];
                     }
                 }
             }
@@ -176,14 +217,11 @@ struct Rows {
     }
 };
 
-__device__ __forceinline__ double warp_sum(double x) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
+__device__ __forceinline__ void block_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kVerifyT) : "memory"); }
 
-// The walk from node 0 down, by every warp of a sequence's cluster alike.  At a
-// node with the target's row p and the draft's row q, before its k-th child,
+// The walk from node 0 down, by the first warp of each CTA of a sequence's cluster
+// alike.  At a node with the target's row p and the draft's row q, before its k-th
+// child,
 //     r_0 = p, s_0 = 1;  r_(k+1) = max(r_k - s_k q, 0), s_(k+1) = sum r_(k+1)
 // and the child x is taken when u q(x) s_k < r_k(x).  Since r_k is where it is
 // not zero p - (s_0 + .. + s_(k-1)) q, one number c_k = s_0 + .. + s_(k-1) stands
@@ -192,28 +230,36 @@ __device__ __forceinline__ double warp_sum(double x) {
 // no row: u s_k < r_k(x), and r_(k+1) is r_k without x.  Where no child is taken,
 // the next token is the first one up to which r_k adds up to more than u sum r_k.
 //
-// Each warp of the cluster holds a run of the vocabulary; their sums, in fp64,
-// go to every CTA through the cluster's shared memory, and the warp that the
-// number falls to looks for the token in its run.
+// Each warp of the cluster holds a run of the vocabulary.  The sums of the runs go
+// to every CTA through the cluster's shared memory; the CTA that the number falls
+// to looks for the token in that run, a step of 32 pieces to a warp.
 template <typename T, bool DRAWN>
-__global__ void __launch_bounds__(kVerifyT) draft_verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyT, 2) draft_verify_kernel(const __grid_constant__ VerifyArgs a) {
     using R = Rows<T, DRAWN>;
-    constexpr int N = R::N;
+    constexpr int N = R::N, NW = kVerifyWarps;
     __shared__ Tree tree;
-    __shared__ double sums[2][kMaxCluster * kVerifyWarps];
+    __shared__ float2 sums[2][kMaxCluster * NW];  // Two's of the cluster's warps, of this pass and the last
     __shared__ int out[kMaxNodes];
+    __shared__ struct {
+        int node, n_out, walking, winner;
+        float2 c;
+        float2 before, want;  // the sum in front of the winner's run, and what is looked for
+    } now;
+    __shared__ float2 step_sum[NW];
+    auto two = [](float2 x) { return Two(x.x, x.y); };
+    auto pair = [](Two x) { return make_float2(x.hi, x.lo); };
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), C = (int)cluster.num_blocks();
     const int s = blockIdx.x / C, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int W = C * kVerifyWarps, me = rank * kVerifyWarps + warp;
+    const int W = C * NW;
     const T* target = static_cast<const T*>(a.target);
     const T* draft = static_cast<const T*>(a.draft);
     cudaGridDependencySynchronize();
+    const float number = a.sample[s];
     if (rank == 0) {
-        int q0 = 0, n = 0;
         if (warp == 0) {
-            q0 = a.q_start[s];
-            n = a.q_start[s + 1] - q0;
+            const int q0 = a.q_start[s];
+            int n = a.q_start[s + 1] - q0;
             if (q0 < 0 || n < 0 || n > kMaxNodes || q0 > a.T - n) {
                 if (lane == 0) set_status(a.status, BSP_ERR_DEVICE_CHECK);
                 n = 0;
@@ -225,7 +271,7 @@ __global__ void __launch_bounds__(kVerifyT) draft_verify_kernel(const __grid_con
             }
         }
         __syncthreads();
-        n = tree.n, q0 = tree.q0;
+        const int n = tree.n, q0 = tree.q0;
         for (int i = tid; i < n; i += kVerifyT) {
             int up = a.parent[q0 + i], tok = a.tokens[q0 + i];
             // (-1 past node 0: a place without a token)
@@ -240,7 +286,7 @@ __global__ void __launch_bounds__(kVerifyT) draft_verify_kernel(const __grid_con
             }
             const float u = a.accept[q0 + i];
             for (int r = 0; r < C; ++r) {
-                Tree* to = cluster.map_shared_rank(&tree, r);
+                Tree* to = r == 0 ? &tree : cluster.map_shared_rank(&tree, r);
                 to->up[i] = up;
                 to->tok[i] = tok;
                 to->px[i] = p;
@@ -251,62 +297,75 @@ __global__ void __launch_bounds__(kVerifyT) draft_verify_kernel(const __grid_con
     }
     cluster.sync();
     const int n = tree.n, q0 = tree.q0;
-    const bool writer = rank == 0 && tid == 0;
     if (n == 0) {
-        if (writer) {
+        if (rank == 0 && tid == 0) {
             a.count[s] = 0;
             a.token[s] = -1;
         }
         return;
     }
-    int passes = 0;
-    R rows;
-    rows.V = a.V;
-    rows.out = out;
-    rows.n_out = 0;
-    // pieces of the row, 32 a step, and this warp's run of steps
-    int first = 0, last = 0;
-    auto at_node = [&](int node) {
-        rows.p = target + (q0 + node) * a.target_row;
-        rows.q = nullptr;
-        rows.n_out = 0;
-        rows.off = (int)(((uintptr_t)rows.p & 15) / sizeof(T));
-        const int steps = (int)(((int64_t)a.V + rows.off + 32 * N - 1) / (32 * N));
-        first = (int)((int64_t)steps * me / W);
-        last = (int)((int64_t)steps * (me + 1) / W);
+    // the rows that `now` tells of, and a warp's run of steps of 32 pieces
+    auto rows_now = [&]() {
+        R r;
+        r.V = a.V;
+        r.p = target + (q0 + now.node) * a.target_row;
+        r.c = two(now.c);
+        r.q = DRAWN && now.c.x > 0.f ? draft + (q0 + now.node) * a.draft_row : nullptr;
+        r.out = out, r.n_out = now.n_out;
+        r.off = (int)(((uintptr_t)r.p & 15) / sizeof(T));
+        return r;
     };
-    // sum of what is left of the row, the same in every thread of the cluster
-    auto pass = [&]() -> double {
-        Sum2 sum;
-        int k = first;
+    auto steps_of = [&](const R& r) { return ((uint32_t)a.V + r.off + 32 * N - 1) / (32 * N); };  // at most 2^23
+    auto run_of = [&](const R& r, int w, int* first, int* last) {
+        const uint32_t steps = steps_of(r);
+        *first = (int)(steps * w / W);
+        *last = (int)(steps * (w + 1) / W);
+    };
+    // one pass over what is left: every warp's sum to every CTA
+    int parity = 1;
+    auto pass = [&]() {
+        const R rows = rows_now();
+        const int me = rank * NW + warp;
+        int k, last;
+        run_of(rows, me, &k, &last);
+        Two sum;
+        constexpr int kAhead = 2;
 #pragma unroll 1
-        for (; k + 4 <= last; k += 4) {
-            float x[4][N], y[4][N];
+        for (; k < last; k += kAhead) {
+            uint4 x[kAhead], y[kAhead];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) rows.load((k + j) * 32 + lane, x[j], y[j]);
+            for (int j = 0; j < kAhead; ++j)
+                if (k + j < last) rows.load((k + j) * 32 + lane, x[j], y[j]);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                rows.left((k + j) * 32 + lane, x[j], y[j]);
+            for (int j = 0; j < kAhead; ++j)
+                if (k + j < last) {
+                    float u[N], v[N];
+                    rows.left((k + j) * 32 + lane, x[j], y[j], u, v);
 #pragma unroll
-                for (int i = 0; i < N; ++i) sum.add(x[j][i], y[j][i]);
-            }
+                    for (int i = 0; i < N; ++i) sum.add(u[i], v[i]);
+                }
         }
-#pragma unroll 1
-        for (; k < last; ++k) {
-            float x[N], y[N];
-            rows.load(k * 32 + lane, x, y);
-            rows.left(k * 32 + lane, x, y);
-#pragma unroll
-            for (int i = 0; i < N; ++i) sum.add(x[i], y[i]);
-        }
-        const double mine = warp_sum(sum.value());
-        double* buf = sums[passes++ & 1];
-        if (lane < C) cluster.map_shared_rank(buf, lane)[me] = mine;
+        parity ^= 1;
+        const float2 mine = pair(from_lane(over_warp(sum), 0));  // the same bits for every CTA
+        if (lane < C) cluster.map_shared_rank(&sums[parity][0], lane)[me] = mine;
         cluster.sync();
-        double all = 0.0;
-#pragma unroll 1
-        for (int i = lane; i < W; i += 32) all += buf[i];
-        return warp_sum(all);
+    };
+    Two c, mass(1.f);
+    int n_out = 0;
+    // the sums in front of the lane's 4 runs, and each of theirs
+    constexpr int kRuns = kMaxCluster * NW / 32;
+    Two front, run[kRuns];
+    auto add_up = [&]() {
+        Two mine;
+#pragma unroll
+        for (int j = 0; j < kRuns; ++j) {
+            const int i = lane * kRuns + j;
+            run[j] = i < W ? two(sums[parity][i]) : Two();
+            mine = mine + run[j];
+        }
+        const Two incl = warp_scan(mine, lane);
+        front = incl - mine;
+        mass = from_lane(incl, 31);
     };
     auto next_child = [&](int node, int after) {
 #pragma unroll 1
@@ -316,115 +375,175 @@ __global__ void __launch_bounds__(kVerifyT) draft_verify_kernel(const __grid_con
         }
         return -1;
     };
-    int node = 0, depth = 0;
-    double c, mass;
-    bool fresh;  // the cluster's sums are of what is left now
+    int node = 0, depth = 0, child = 0;
+    bool fresh = false;   // the cluster's sums are of what is left now
+    bool later = false;   // shares were taken away behind the sums' pass
+    bool summed = false;  // nothing is taken any more, the sums are on their way
+    if (rank == 0 && lane == 0) a.path[q0] = 0;
+    // one turn for each pass that the walk asks for
+#pragma unroll 1
     while (true) {
-        if (writer) a.path[q0 + depth] = node;
-        at_node(node);
-        c = 0.0, mass = 1.0, fresh = false;
-        int child = next_child(node, node);
+        if (warp == 0) {
+            bool ask = false;
 #pragma unroll 1
-        for (; child >= 0; child = next_child(node, child)) {
-            const double u = tree.u[child], px = tree.px[child];
-            if (DRAWN) {
-                const double qx = tree.qx[child];
-                if (u * qx * mass < px - c * qx) break;
-                c += mass;
-                rows.q = draft + (q0 + node) * a.draft_row;
-                rows.ch = (float)c;
-                rows.cl = (float)(c - (double)rows.ch);
-                mass = pass();
-                fresh = true;
-            } else {
-                const int x = tree.tok[child];
-                double have = px;
-                for (int i = 0; i < rows.n_out; ++i)
-                    if (out[i] == x) have = 0.0;
-                if (u * mass < have) break;
-                __syncthreads();  // out[]'s readers of the last rejection are done
-                if (tid == 0) out[rows.n_out] = x;
-                ++rows.n_out;
-                __syncthreads();
-                // later ones only take their own share away
-                fresh = rows.n_out == 1;
-                mass = fresh ? pass() : fmax(mass - have, 0.0);
+            while (!summed && !ask) {
+                child = next_child(node, child);
+                if (child < 0) {
+                    summed = true;
+                    ask = !fresh;
+                    break;
+                }
+                const Two u(tree.u[child]), px(tree.px[child]);
+                bool take;
+                Two have = px;
+                if (DRAWN) {
+                    const Two qx(tree.qx[child]);
+                    take = (px - c * qx).above(u * qx * mass);
+                } else {
+                    const int x = tree.tok[child];
+#pragma unroll 1
+                    for (int i = 0; i < n_out; ++i)
+                        if (out[i] == x) have = Two();
+                    take = have.above(u * mass);
+                }
+                if (take) {
+                    node = child;
+                    ++depth;
+                    c = Two(), mass = Two(1.f), n_out = 0, fresh = later = false;
+                    if (rank == 0 && lane == 0) a.path[q0 + depth] = node;
+                } else if (DRAWN) {
+                    c = c + mass;
+                    ask = fresh = true;
+                } else {
+                    // the first one's pass sums up what is left; later ones take their
+                    // own share away, from the sum of the run that holds them too
+                    const int x = tree.tok[child];
+                    __syncwarp();
+                    if (lane == 0) {
+                        out[n_out] = x;
+                        if (n_out) {
+                            const R r = rows_now();
+                            const uint32_t step = (uint32_t)(x + r.off) / (32 * N);
+                            float2& sum = sums[parity][((step + 1) * W - 1) / steps_of(r)];
+                            sum = have.above(two(sum)) ? make_float2(0.f, 0.f) : pair(two(sum) - have);
+                        }
+                    }
+                    __syncwarp();
+                    ask = fresh = true;
+                    if (n_out++ > 0) {
+                        ask = false;
+                        mass = have.above(mass) ? Two() : mass - have;
+                        later = true;
+                    }
+                }
             }
+            bool done = false;
+            if (!ask) {
+                if (!DRAWN && later) add_up();
+                later = false;
+                done = mass.hi > 0.f || !(c.hi > 0.f || n_out);
+                // rounding left nothing: the target's own row
+                if (!done) c = Two(), n_out = 0;
+            }
+            if (lane == 0) {
+                now.node = node, now.n_out = n_out, now.walking = !done;
+                now.c = pair(c);
+            }
+            if (done) {
+                if (rank == 0) {
+                    if (lane == 0) {
+                        a.count[s] = depth + 1;
+                        if (!(mass.hi > 0.f)) a.token[s] = -1;
+                    }
+                    for (int i = depth + 1 + lane; i < n; i += 32) a.path[q0 + i] = -1;
+                }
+                // the run that the number falls to: the first up to which the sums are above
+                // it (none, for a number of 1 or more: the last with anything)
+                const Two want = Two(number) * mass;
+                int over = -1, some = -1;
+                Two over_front, some_front, at = front;
+#pragma unroll
+                for (int j = 0; j < kRuns; ++j) {
+                    if (run[j].hi > 0.f) {
+                        some = lane * kRuns + j, some_front = at;
+                        at = at + run[j];
+                        if (over < 0 && at.above(want)) over = some, over_front = some_front;
+                    }
+                }
+                const unsigned any_over = __ballot_sync(0xffffffffu, over >= 0), any = __ballot_sync(0xffffffffu, some >= 0);
+                const int src = any_over ? __ffs(any_over) - 1 : any ? 31 - __clz(any) : 0;
+                const int winner = __shfl_sync(0xffffffffu, any_over ? over : some, src);
+                const Two before = from_lane(any_over ? over_front : some_front, src);
+                if (lane == 0) {
+                    now.winner = mass.hi > 0.f ? winner : -1;
+                    now.before = pair(before), now.want = pair(want);
+                }
+            }
+            __syncwarp();
         }
-        if (child < 0) break;
-        node = child;
-        ++depth;
+        block_barrier();
+        if (!now.walking) break;
+        pass();
+        if (warp == 0) add_up();
     }
-    if (!fresh) mass = pass();
-    if (!(mass > 0.0) && (rows.q || rows.n_out)) {
-        // rounding left nothing: the target's own row
-        rows.q = nullptr;
-        rows.n_out = 0;
-        mass = pass();
-    }
-    if (rank == 0)
-        for (int i = depth + 1 + tid; i < n; i += kVerifyT) a.path[q0 + i] = -1;
-    if (writer) {
-        a.count[s] = depth + 1;
-        if (!(mass > 0.0)) a.token[s] = -1;
-    }
-    if (!(mass > 0.0)) return;
-    // the warp whose run the number falls to: the first up to which the sums are
-    // above it (none, for a number of 1 or more: the last with anything)
-    const double* buf = sums[(passes - 1) & 1];
-    const double want = (double)a.sample[s] * mass;
-    double before = 0.0;
-    int mine = -1;
-    double mine_before = 0.0;
+    if (now.winner < 0 || now.winner / NW != rank) return;
+    // the winner's run, NW steps at a time, each by a warp
+    const R rows = rows_now();
+    int first, last;
+    run_of(rows, now.winner, &first, &last);
+    const Two want = two(now.want);
+    Two reached = two(now.before);
+    int some = -1;  // the last entry with anything, of this thread
 #pragma unroll 1
-    for (int i = 0; i < W; ++i) {
-        if (buf[i] > 0.0) mine = i, mine_before = before;
-        before += buf[i];
-        if (before > want) break;
-    }
-    if (mine != me) return;
-    int found = -1, some = -1;  // the token; the last with anything
-    double run = mine_before;
-#pragma unroll 1
-    for (int k = first; k < last && found < 0; ++k) {
-        const int piece = k * 32 + lane;
+    for (int k0 = first; k0 < last; k0 += NW) {
+        const int piece = (k0 + warp) * 32 + lane;
         float x[N], y[N];
-        rows.load(piece, x, y);
-        rows.left(piece, x, y);
-        Sum2 sum;
-        int any = -1;
+        Two sum;
+        if (k0 + warp < last) {
+            uint4 p, q;
+            rows.load(piece, p, q);
+            rows.left(piece, p, q, x, y);
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            sum.add(x[i], y[i]);
-            if (x[i] + y[i] > 0.f) any = piece * N - rows.off + i;
-        }
-        const double v = sum.value();
-        double incl = v;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double z = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += z;
-        }
-        const unsigned have = __ballot_sync(0xffffffffu, any >= 0);
-        if (have) some = __shfl_sync(0xffffffffu, any, 31 - __clz(have));
-        const unsigned over = __ballot_sync(0xffffffffu, any >= 0 && run + incl > want);
-        if (over) {
-            double at = run + (incl - v);
-            int i_at = any;
-#pragma unroll
-            for (int i = N - 1; i >= 0; --i) {
-                // the entry's own end: the sum up to it, from the front
-                double end = at;
-#pragma unroll
-                for (int j = 0; j < N; ++j)
-                    if (j <= i) end += (double)x[j] + (double)y[j];
-                if (end > want && x[i] + y[i] > 0.f) i_at = piece * N - rows.off + i;
+            for (int i = 0; i < N; ++i) {
+                sum.add(x[i], y[i]);
+                if (x[i] + y[i] > 0.f) some = piece * N - rows.off + i;
             }
-            found = __shfl_sync(0xffffffffu, i_at, __ffs(over) - 1);
         }
-        run += __shfl_sync(0xffffffffu, incl, 31);
+        sum = sum.whole();
+        const Two all = over_warp(sum);
+        if (lane == 0) step_sum[warp] = pair(all);
+        __syncthreads();
+        // the first step up to which the sums are above the number
+        const Two mine = lane < NW ? two(step_sum[lane]) : Two(), upto = reached + warp_scan(mine, lane);
+        const unsigned hits = __ballot_sync(0xffffffffu, mine.hi > 0.f && upto.above(want));
+        if (hits) {
+            const int hit = __ffs(hits) - 1;
+            if (hit != warp) return;
+            Two at = from_lane(upto - mine, hit) + (warp_scan(sum, lane) - sum);
+            int found = -1;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                at.add(x[i], y[i]);
+                if (found < 0 && at.above(want) && x[i] + y[i] > 0.f) found = piece * N - rows.off + i;
+            }
+            // (rounding may put the border behind the step's last entry: that one then)
+            const unsigned m = __ballot_sync(0xffffffffu, found >= 0), have = __ballot_sync(0xffffffffu, sum.hi > 0.f);
+            const int tok = m ? __shfl_sync(0xffffffffu, found, __ffs(m) - 1) : __shfl_sync(0xffffffffu, some, 31 - __clz(have));
+            if (lane == 0) a.token[s] = tok;
+            return;
+        }
+        reached = from_lane(upto, 31);
+        __syncthreads();
     }
-    if (lane == 0) a.token[s] = found >= 0 ? found : some;
+    // rounding, or a number of 1 or more: the run's last entry with anything
+    some = __reduce_max_sync(0xffffffffu, some);
+    int* last_of = reinterpret_cast<int*>(step_sum);
+    if (lane == 0) last_of[warp] = some;
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 0; i < NW; ++i) some = imax(some, last_of[i]);
+        a.token[s] = some;
+    }
 }
 
 template <typename T>
@@ -488,8 +607,11 @@ extern "C" int bsp_draft_verify(bsp_window_t w, int dtype, const void* target, i
         return BSP_ERR_ALIGNMENT;
     const VerifyArgs a{target, draft, target_stride, draft_stride, tokens, q_start, parent, accept, sample,
                        path, count, token, T, V, w->status};
-    // few sequences: eight SMs share each one's vocabulary
-    const int cluster = n_seq <= 4 * bsp::sm_count() ? 8 : n_seq <= 16 * bsp::sm_count() ? 2 : 1;
+    // as many CTAs to a sequence as run at once, two on an SM, while each warp of
+    // theirs has a step of its own
+    const int per_step = kVerifyWarps * 32 * 16 / elt_bytes(dtype);
+    int cluster = 1;
+    while (cluster < kMaxCluster && 2 * cluster * n_seq <= 2 * bsp::sm_count() && cluster * per_step < V) cluster *= 2;
     cudaStream_t s = (cudaStream_t)stream;
     switch (dtype) {
         case BSP_F32: return verify_t<float>(a, n_seq, cluster, s);
