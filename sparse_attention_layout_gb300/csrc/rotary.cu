@@ -11,6 +11,7 @@
 // top two bits, what is left, at most an eighth of a turn either way, is exact to
 // 2^-25 of itself in fp32.
 #include <cmath>
+#include <cstring>
 #include <new>
 #include <type_traits>
 
@@ -31,6 +32,7 @@ namespace {
 
 constexpr int kMaxPairs = 64;
 constexpr int kThreads = 256;
+constexpr int kHeads = 16;  // of a thread, at most: what its sines serve (8: 113 us, 40: 105, with fewer blocks)
 
 struct Args {
     uint64_t turns[kMaxPairs];
@@ -62,78 +64,128 @@ __device__ __forceinline__ float2 unit_at(uint32_t turn) {
     return make_float2((q + 1) & 2 ? -a : a, q & 2 ? -b : b);
 }
 
-// A thread owns one vector of VE columns (half layout: the two vectors of VE
-// pairs) of one token in some heads, so its sines serve all of those.
-template <typename T, int VE, bool PAIRS>
+// How a thread's pairs lie: kPairs, within its vector; kHalves, over two vectors R / 2
+// columns apart; kSwap, the same, but the thread has one of the two and the
+// other comes from a thread of its warp.
+enum Kind { kPairs, kHalves, kSwap };
+
+// A thread owns one vector of VE columns (kHalves: the two vectors of VE pairs) of
+// one token in some heads, so its sines serve all of those.
+//
+// HBM-bound: each element is read and written once.  32768 tokens of 40 heads of 128
+// columns, bf16, 671 MB: 105 us (6.4 TB/s, 94 % of a copy's rate) with halves, 107
+// with pairs.  Halves as two vectors a thread (kHalves: 128 bytes of a row per
+// access, not 256) took 127; rows of a few heads per block, or one access of a
+// thread on its way at a time, 130 to 150.
+template <typename T, int VE, Kind KIND>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ Args a) {
-    constexpr int NP = PAIRS ? VE / 2 : VE;  // pairs of a thread
+    constexpr int NP = KIND == kPairs ? VE / 2 : VE;  // pairs of a thread
+    // heads on their way at once (kPairs in 16 bits: 107 us with 2, 110 with 4; kSwap
+    // 110 and 105; kHalves 127 and 157, by its registers)
+    constexpr int kAhead = KIND == kHalves || (KIND == kPairs && sizeof(T) == 2) ? 2 : 4;
     __shared__ uint64_t turns[kMaxPairs];
     const int tid = threadIdx.y * blockDim.x + threadIdx.x;
     for (int i = tid; i < a.R / 2; i += blockDim.x * blockDim.y) turns[i] = a.turns[i];
     __syncthreads();
     cudaGridDependencySynchronize();
-    const uint32_t t = blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= a.tokens) return;
+    // (threads without a token go along with the last one's, for the warp's sake)
+    const uint32_t token = blockIdx.x * blockDim.y + threadIdx.y, t = min(token, a.tokens - 1);
+    const bool live = token < a.tokens;
+    if (KIND != kSwap && !live) return;
     const uint32_t z = t / (uint32_t)a.S, s = t - z * (uint32_t)a.S;
     const int u = threadIdx.x;
     const bool turned = u < a.turned;
+    const int half = a.turned / 2;  // kSwap: vectors of one half of the pairs
     float cs[NP], sn[NP];
     if (turned) {
         const int64_t p = a.pos ? a.pos[z * a.pz + s] : (int64_t)s;
+        const int first = (KIND == kSwap && u >= half ? u - half : u) * NP;
+        const float sign = KIND == kSwap && u < half ? -a.sign : a.sign;
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            const uint64_t f = (uint64_t)p * turns[u * NP + k];
+            const uint64_t f = (uint64_t)p * turns[first + k];
             const float2 e = unit_at((uint32_t)(f >> 32));
             cs[k] = e.x * a.amplitude;
-            sn[k] = e.y * a.amplitude * a.sign;
+            sn[k] = e.y * a.amplitude * sign;
         }
     }
     using P = Pack<T, VE>;
-    // columns of the thread's first vector; half layout: the other is R / 2 further
+    // columns of the thread's first vector; kHalves: the other is R / 2 further
     const int c0 = !turned ? a.R + (u - a.turned) * VE : u * VE;
-    const int h1 = min((int)(blockIdx.y + 1) * a.heads, a.H);
-#pragma unroll 4
-    for (int h = blockIdx.y * a.heads; h < h1; ++h) {
-        const bool q = h < a.Hq;
-        const View& in = q ? a.Q : a.K;
-        const View& out = q ? a.Qo : a.Ko;
-        const int64_t g = q ? h : h - a.Hq;
-        const T* x = static_cast<const T*>(in.ptr) + z * in.s[0] + g * in.s[1] + s * in.s[2] + c0;
-        T* y = static_cast<T*>(out.ptr) + z * out.s[0] + g * out.s[1] + s * out.s[2] + c0;
-        P v = *reinterpret_cast<const P*>(x);
-        if (turned) {
-            if constexpr (PAIRS) {
+    const int h0 = blockIdx.y * a.heads, h1 = min(h0 + a.heads, a.H);
+    // heads h .. e - 1 of one tensor, kAhead of them on their way at once (a tensor
+    // may be turned in its own place, so the compiler keeps loads behind stores)
+    auto heads = [&](const View& in, const View& out, int h, int e) {
+        const T* x = static_cast<const T*>(in.ptr) + z * in.s[0] + h * in.s[1] + s * in.s[2] + c0;
+        T* y = static_cast<T*>(out.ptr) + z * out.s[0] + h * out.s[1] + s * out.s[2] + c0;
+#pragma unroll 1
+        for (; h < e; h += kAhead, x += kAhead * in.s[1], y += kAhead * out.s[1]) {
+            P v[kAhead], w[KIND == kHalves ? kAhead : 1];
 #pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    const float xa = to_f32(v.x[2 * k]), xb = to_f32(v.x[2 * k + 1]);
-                    v.x[2 * k] = from_f32<T>(fmaf(xa, cs[k], -(xb * sn[k])));
-                    v.x[2 * k + 1] = from_f32<T>(fmaf(xb, cs[k], xa * sn[k]));
+            for (int j = 0; j < kAhead; ++j)
+                if (h + j < e) {
+                    v[j] = *reinterpret_cast<const P*>(x + j * in.s[1]);
+                    if constexpr (KIND == kHalves)
+                        if (turned) w[j] = *reinterpret_cast<const P*>(x + j * in.s[1] + a.R / 2);
                 }
-            } else {
-                P w = *reinterpret_cast<const P*>(x + a.R / 2);
 #pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    const float xa = to_f32(v.x[k]), xb = to_f32(w.x[k]);
-                    v.x[k] = from_f32<T>(fmaf(xa, cs[k], -(xb * sn[k])));
-                    w.x[k] = from_f32<T>(fmaf(xb, cs[k], xa * sn[k]));
+            for (int j = 0; j < kAhead; ++j)
+                if (h + j < e) {
+                    P& f = v[j];
+                    if constexpr (KIND == kSwap) {
+                        constexpr int NW = sizeof(P) / 4;
+                        P g;
+                        uint32_t fw[NW], gw[NW];
+                        memcpy(fw, &f, sizeof(P));
+#pragma unroll
+                        for (int k = 0; k < NW; ++k) gw[k] = __shfl_xor_sync(0xffffffffu, fw[k], half);
+                        memcpy(&g, gw, sizeof(P));
+                        if (turned)
+#pragma unroll
+                            for (int k = 0; k < NP; ++k)
+                                f.x[k] = from_f32<T>(fmaf(to_f32(f.x[k]), cs[k], to_f32(g.x[k]) * sn[k]));
+                    } else if (turned) {
+                        if constexpr (KIND == kPairs) {
+#pragma unroll
+                            for (int k = 0; k < NP; ++k) {
+                                const float xa = to_f32(f.x[2 * k]), xb = to_f32(f.x[2 * k + 1]);
+                                f.x[2 * k] = from_f32<T>(fmaf(xa, cs[k], -(xb * sn[k])));
+                                f.x[2 * k + 1] = from_f32<T>(fmaf(xb, cs[k], xa * sn[k]));
+                            }
+                        } else {
+                            P& g = w[j];
+#pragma unroll
+                            for (int k = 0; k < NP; ++k) {
+                                const float xa = to_f32(f.x[k]), xb = to_f32(g.x[k]);
+                                f.x[k] = from_f32<T>(fmaf(xa, cs[k], -(xb * sn[k])));
+                                g.x[k] = from_f32<T>(fmaf(xb, cs[k], xa * sn[k]));
+                            }
+                            *reinterpret_cast<P*>(y + j * out.s[1] + a.R / 2) = g;
+                        }
+                    }
+                    if (KIND != kSwap || live) *reinterpret_cast<P*>(y + j * out.s[1]) = f;
                 }
-                *reinterpret_cast<P*>(y + a.R / 2) = w;
-            }
         }
-        *reinterpret_cast<P*>(y) = v;
-    }
+    };
+    if (h0 < a.Hq) heads(a.Q, a.Qo, h0, min(h1, a.Hq));
+    if (h1 > a.Hq) heads(a.K, a.Ko, max(h0 - a.Hq, 0), h1 - a.Hq);
 }
 
 template <typename T, int VE>
 int launch(Args a, bool pairs, bool rest, cudaStream_t s) {
-    a.turned = a.R / (pairs ? VE : 2 * VE);
-    a.units = a.turned + (rest ? (a.D - a.R) / VE : 0);
+    // kSwap where a token's vectors fill a power of two of a warp's lanes, so that the
+    // other half is an exclusive or away
+    const int vectors = a.R / VE, others = rest ? (a.D - a.R) / VE : 0;
+    const bool swap = VE * sizeof(T) >= 4 && !pairs && (vectors & (vectors - 1)) == 0 && others % vectors == 0 &&
+                      32 % (vectors + others) == 0;
+    a.turned = pairs || swap ? vectors : vectors / 2;
+    a.units = a.turned + others;
     const int rows = kThreads / a.units;
     const uint32_t blocks = (a.tokens + rows - 1) / rows;
     // few tokens: their heads go to several blocks, as many as fill the GPU
     const int64_t fill = 4 * (int64_t)sm_count();
     const int groups = (int)(blocks >= fill ? 1 : (fill + blocks - 1) / blocks);
-    a.heads = imax(1, (a.H + groups - 1) / groups);
+    a.heads = imin(kHeads, imax(1, (a.H + groups - 1) / groups));
     const dim3 grid(blocks, (a.H + a.heads - 1) / a.heads);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = grid;
@@ -144,9 +196,11 @@ int launch(Args a, bool pairs, bool rest, cudaStream_t s) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    void (*kern)(const Args) = rotary_kernel<T, VE, false>;
+    void (*kern)(const Args) = rotary_kernel<T, VE, kHalves>;
     if constexpr (VE > 1)
-        if (pairs) kern = rotary_kernel<T, VE, true>;
+        if (pairs) kern = rotary_kernel<T, VE, kPairs>;
+    if constexpr (VE * sizeof(T) >= 4)
+        if (swap) kern = rotary_kernel<T, VE, kSwap>;
     return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
 }
 
