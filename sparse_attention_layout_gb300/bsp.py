@@ -873,21 +873,18 @@ def bsp_paged_attention(W: Window, Q, K_cache, V_cache, q_start, kv_len, table, 
 
 # ------------------------------------------------------- drafted tokens --
 
-def _ints(W, what, t, shape):
+def _ints(W, what, t, shape, dtype=torch.int32):
     """A contiguous int32 tensor of that shape on the handle's device."""
+    if t.shape == shape and t.dtype is dtype and t.is_contiguous() and t.device == W.device:
+        return
     _shape(t, shape, what)
-    if t.dtype != torch.int32 or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 tensor")
-    if t.device != W.device:
-        raise ValueError(f"{what} is on {t.device}, the handle on {W.device}")
+    if t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {str(dtype)[6:]} tensor")
+    raise ValueError(f"{what} is on {t.device}, the handle on {W.device}")
 
 
 def _floats(W, what, t, shape):
-    _shape(t, shape, what)
-    if t.dtype != torch.float32 or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous float32 tensor")
-    if t.device != W.device:
-        raise ValueError(f"{what} is on {t.device}, the handle on {W.device}")
+    _ints(W, what, t, shape, torch.float32)
 
 
 def _starts(q_start):
@@ -1237,13 +1234,17 @@ def bsp_rotary(R: Rotary, Q, K=None, positions=None, Q_out=None, K_out=None, *, 
     return Q_out, K_out
 
 
+def _turn_taken(Q, K, positions, R, inverse):
+    return bsp_rotary(R, _taken(Q), None if K is None else _taken(K), positions, inverse=inverse)
+
+
 class _RotaryPositions(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, positions, R, inverse):
         ctx.set_materialize_grads(False)
         ctx.save_for_backward(positions)
         ctx.R, ctx.inverse = R, inverse
-        return bsp_rotary(R, _taken(Q), None if K is None else _taken(K), positions, inverse=inverse)
+        return _turn_taken(Q, K, positions, R, inverse)
 
     @staticmethod
     def backward(ctx, dQ, dK):
@@ -1251,7 +1252,9 @@ class _RotaryPositions(torch.autograd.Function):
         got = [g for g in (dQ, dK) if g is not None]
         if not got:
             return None, None, None, None, None
-        got = list(_RotaryPositions.apply(got[0], got[1] if len(got) > 1 else None, positions, ctx.R, not ctx.inverse))
+        # (a graph of the gradient only where one is asked for)
+        turn = _RotaryPositions.apply if torch.is_grad_enabled() else _turn_taken
+        got = list(turn(got[0], got[1] if len(got) > 1 else None, positions, ctx.R, not ctx.inverse))
         return (got.pop(0) if dQ is not None else None, got.pop(0) if dK is not None else None, None, None, None)
 
 

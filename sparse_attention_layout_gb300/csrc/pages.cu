@@ -294,10 +294,12 @@ struct CopyArgs {
 
 constexpr int kAhead = 4;
 
-// blockIdx.x: a pair of pages; blockIdx.y: a share of its pieces.  HBM-bound.
+// blockIdx.x: a pair of pages; blockIdx.y: a share of the pieces of K's page, or
+// (odd) of V's.
 __global__ void __launch_bounds__(kT) copy_kernel(const __grid_constant__ CopyArgs a) {
     cudaGridDependencySynchronize();
-    const int pieces = a.Hkv * a.page * a.row16, step = gridDim.y * kT;
+    const int pieces = a.Hkv * a.page * a.row16, step = (gridDim.y >> 1) * kT;
+    const View& v = blockIdx.y & 1 ? a.V : a.K;
     for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
         const int x = a.src[i], y = a.dst[i];
         if (x < 0 || y < 0) continue;
@@ -306,26 +308,24 @@ __global__ void __launch_bounds__(kT) copy_kernel(const __grid_constant__ CopyAr
             continue;
         }
         if (x == y) continue;
+        const uint4* from = static_cast<const uint4*>(v.ptr) + x * v.s[0];
+        uint4* to = static_cast<uint4*>(v.ptr) + y * v.s[0];
 #pragma unroll 1
-        for (int k0 = blockIdx.y * kT + threadIdx.x; k0 < pieces; k0 += kAhead * step) {
-            uint4 kv[kAhead], vv[kAhead];
-            int64_t at_k[kAhead], at_v[kAhead];
+        for (int k0 = (blockIdx.y >> 1) * kT + threadIdx.x; k0 < pieces; k0 += kAhead * step) {
+            uint4 row[kAhead];
+            int64_t at[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const int k = k0 + j * step;
                 if (k >= pieces) break;
-                const int r = k / a.row16, c = k - r * a.row16, h = r / a.page, slot = r - h * a.page;
-                at_k[j] = h * a.K.s[1] + slot * a.K.s[2] + c;
-                at_v[j] = h * a.V.s[1] + slot * a.V.s[2] + c;
-                kv[j] = static_cast<const uint4*>(a.K.ptr)[x * a.K.s[0] + at_k[j]];
-                vv[j] = static_cast<const uint4*>(a.V.ptr)[x * a.V.s[0] + at_v[j]];
+                const int r = (uint32_t)k / (uint32_t)a.row16, c = k - r * a.row16;
+                const int h = (uint32_t)r / (uint32_t)a.page, slot = r - h * a.page;
+                at[j] = h * v.s[1] + slot * v.s[2] + c;
+                row[j] = from[at[j]];
             }
 #pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                if (k0 + j * step >= pieces) break;
-                static_cast<uint4*>(a.K.ptr)[y * a.K.s[0] + at_k[j]] = kv[j];
-                static_cast<uint4*>(a.V.ptr)[y * a.V.s[0] + at_v[j]] = vv[j];
-            }
+            for (int j = 0; j < kAhead; ++j)
+                if (k0 + j * step < pieces) to[at[j]] = row[j];
         }
     }
 }
@@ -530,7 +530,7 @@ extern "C" int bsp_paged_copy(bsp_window_t w, int dtype, const bsp_tensor_t* K_c
     if (n == 0) return BSP_OK;
     if ((rc = check_ints(src, dst))) return rc;
     const CopyArgs a{in_16(k, elt), in_16(v, elt), src, dst, n, n_pages, page, Hkv, D * elt / 16, w->status};
-    const int pieces = Hkv * page * a.row16, parts = imax(1, imin(pieces / (kT * kAhead), 16));
+    const int pieces = Hkv * page * a.row16, parts = 2 * imax(1, imin(pieces / (kT * kAhead), 32));
     const int most = 16 * bsp::sm_count();
     return launch_behind(copy_kernel, dim3(imin(n, most), parts), kT, 0, (cudaStream_t)stream, a);
 }
