@@ -95,16 +95,16 @@ __device__ __forceinline__ void landed() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// s[u][v] = sum_d A[ty + 16 u][d] B[tx + 16 v][d]
+// s[u][v] = sum_d A[ty + 16 u][d] B[tx + 16 v][d], d < D
 template <int DP>
-__device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&s)[4][4]) {
+__device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&s)[4][4], int D = DP) {
     float2 acc[4][4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int v = 0; v < 4; ++v) acc[u][v] = make_float2(0.f, 0.f);
 #pragma unroll 4
-    for (int d = 0; d < DP; d += 4) {
+    for (int d = 0; d < D; d += 4) {
         float4 a[4], b[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) a[u] = *reinterpret_cast<const float4*>(A + (ty + 16 * u) * (DP + 4) + d);
@@ -185,7 +185,11 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
         if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
 }
 
-// TREE: the tokens are nodes of trees of drafted tokens (pages only).
+// TREE: the tokens are nodes of trees of drafted tokens (pages only).  Few rows and
+// keys to a CTA, so what a step and a start cost counts: products over the head's
+// own columns, and one CTA an SM where no more run at once (16 trees of 5 to 70
+// nodes over 300 to 6000 keys, 6 heads of 80: 67 us; 62 and 59 with one of the two,
+// 55 with both).
 template <typename T, int DP, bool PAGED, bool TREE>
 __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __grid_constant__ Args A,
                                                      const __grid_constant__ SimtPlan plan) {
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
             landed<1>();
             __syncthreads();
             float s[4][4];
-            dots<DP>(Qs, Ks, ty, tx, s);
+            dots<DP>(Qs, Ks, ty, tx, s, TREE ? A.D : DP);
             __syncthreads();
             copy(Ks, A.K, n + 1);
 #pragma unroll
@@ -619,7 +623,8 @@ int backward_t(Call& c, const Args& a, int grid) {
 
 #define BSP_WIN_DISPATCH(fn)                                                                    \
     const Args a = make_args(c);                                                                \
-    const int grid = imin(kSimtPerSm * sm_count(), SimtPlan::kCtas);                                                   \
+    const int per_sm = c.p.words && c.D > 64 ? 1 : kSimtPerSm;                                  \
+    const int grid = imin(per_sm * sm_count(), SimtPlan::kCtas);                                \
     switch (c.dtype) {                                                                          \
         case BSP_F32: return c.D <= 64 ? fn<float, 64>(c, a, grid) : fn<float, 128>(c, a, grid); \
         case BSP_BF16: return c.D <= 64 ? fn<__nv_bfloat16, 64>(c, a, grid) : fn<__nv_bfloat16, 128>(c, a, grid); \
