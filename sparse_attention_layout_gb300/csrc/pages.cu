@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kT) fork_kernel(const __grid_constant__ Book b
 
 // exclusive prefix over the 1024 threads of a block; *total = the block's sum
 constexpr int kBig = 1024;
+constexpr int kSteps = 4;  // pages of a thread and scan
 __device__ __forceinline__ int scan(int v, uint32_t* red, int* total) {
     uint32_t t;
     const int x = (int)block_scan<kBig>((uint32_t)v, red, &t);
@@ -190,19 +191,19 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
         need += __syncthreads_count(i < items && needs(i, item(i, &s, &j)));
     }
     int have = 0;
-    for (int x0 = 0; x0 < b.n_pages && have < need; x0 += 4 * kBig) {
-        const int x = x0 + 4 * tid;
-        bool is[4];
+    for (int x0 = 0; x0 < b.n_pages && have < need; x0 += kSteps * kBig) {
+        const int x = x0 + kSteps * tid;
+        bool is[kSteps];
         int n = 0;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
+        for (int k = 0; k < kSteps; ++k) {
             is[k] = x + k < b.n_pages && b.refs[x + k] <= 0;
             n += is[k];
         }
         int total;
         int at = have + scan(n, red, &total);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < kSteps; ++k)
             if (is[k]) a.list[at++] = x + k;
         have += total;
     }
@@ -250,16 +251,26 @@ __global__ void __launch_bounds__(kBig) compact_kernel(const __grid_constant__ C
     for (int x = tid; x < b.n_pages; x += kBig) n += b.refs[x] > 0;
     scan(n, red, &live);
     int moved = 0, holes = 0;
-    for (int x0 = 0; x0 < b.n_pages; x0 += kBig) {
-        const int x = x0 + tid;
-        const bool used = x < b.n_pages && b.refs[x] > 0;
-        const bool high = used && x >= live, low = x < live && !used;
-        // (a chunk's two counts, 1024 at the most, in one scan)
+    for (int x0 = 0; x0 < b.n_pages; x0 += kSteps * kBig) {
+        const int x = x0 + kSteps * tid;
+        bool high[kSteps], low[kSteps];
+        int mine = 0;  // (a chunk's two counts, 4096 at the most, in one scan)
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            const bool in = x + k < b.n_pages, used = in && b.refs[x + k] > 0;
+            high[k] = used && x + k >= live;
+            low[k] = x + k < live && !used;
+            mine += (int)high[k] | (int)low[k] << 16;
+            if (in && x + k >= live) a.map[x + k] = x + k;
+        }
         int total;
-        const int at = scan(high | low << 16, red, &total);
-        if (high && moved + (at & 0xffff) < half) a.src[moved + (at & 0xffff)] = x;
-        if (low && holes + (at >> 16) < half) a.dst[holes + (at >> 16)] = x;
-        if (x >= live && x < b.n_pages) a.map[x] = x;
+        const int before = scan(mine, red, &total);
+        int m = moved + (before & 0xffff), h = holes + (before >> 16);
+#pragma unroll
+        for (int k = 0; k < kSteps; ++k) {
+            if (high[k] && m < half) a.src[m++] = x + k;
+            if (low[k] && h < half) a.dst[h++] = x + k;
+        }
         moved += total & 0xffff;
         holes += total >> 16;
     }
@@ -297,12 +308,16 @@ struct CopyArgs {
 };
 
 constexpr int kAhead = 4;
+constexpr int kCopyT = 128;
 
 // blockIdx.x: a pair of pages; blockIdx.y: a share of the pieces of K's page, or
-// (odd) of V's.
-__global__ void __launch_bounds__(kT) copy_kernel(const __grid_constant__ CopyArgs a) {
+// (odd) of V's.  HBM-bound: 1122 pages of 32 slots of 8 heads of 128 columns, bf16,
+// 294 MB: 48 us (6.2 TB/s); pages of 128 slots 6.6 TB/s.  (256 threads a block 51 us,
+// 512 58; twice the pieces of a thread on their way 50, half as many 49; both
+// caches by one thread 57.)
+__global__ void __launch_bounds__(kCopyT) copy_kernel(const __grid_constant__ CopyArgs a) {
     cudaGridDependencySynchronize();
-    const int pieces = a.Hkv * a.page * a.row16, step = (gridDim.y >> 1) * kT;
+    const int pieces = a.Hkv * a.page * a.row16, step = (gridDim.y >> 1) * kCopyT;
     const View& v = blockIdx.y & 1 ? a.V : a.K;
     for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
         const int x = a.src[i], y = a.dst[i];
@@ -315,7 +330,7 @@ __global__ void __launch_bounds__(kT) copy_kernel(const __grid_constant__ CopyAr
         const uint4* from = static_cast<const uint4*>(v.ptr) + x * v.s[0];
         uint4* to = static_cast<uint4*>(v.ptr) + y * v.s[0];
 #pragma unroll 1
-        for (int k0 = (blockIdx.y >> 1) * kT + threadIdx.x; k0 < pieces; k0 += kAhead * step) {
+        for (int k0 = (blockIdx.y >> 1) * kCopyT + threadIdx.x; k0 < pieces; k0 += kAhead * step) {
             uint4 row[kAhead];
             int64_t at[kAhead];
 #pragma unroll
@@ -534,9 +549,9 @@ extern "C" int bsp_paged_copy(bsp_window_t w, int dtype, const bsp_tensor_t* K_c
     if (n == 0) return BSP_OK;
     if ((rc = check_ints(src, dst))) return rc;
     const CopyArgs a{in_16(k, elt), in_16(v, elt), src, dst, n, n_pages, page, Hkv, D * elt / 16, w->status};
-    const int pieces = Hkv * page * a.row16, parts = 2 * imax(1, imin(pieces / (kT * kAhead), 32));
+    const int pieces = Hkv * page * a.row16, parts = 2 * imax(1, imin(pieces / (kCopyT * kAhead), 32));
     const int most = 16 * bsp::sm_count();
-    return launch_behind(copy_kernel, dim3(imin(n, most), parts), kT, 0, (cudaStream_t)stream, a);
+    return launch_behind(copy_kernel, dim3(imin(n, most), parts), kCopyT, 0, (cudaStream_t)stream, a);
 }
 
 extern "C" int bsp_paged_keep(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const bsp_tensor_t* V_cache,
