@@ -1188,47 +1188,51 @@ def bsp_rotary_create(frequencies, amplitude: float = 1.0, interleaved: bool = F
     return Rotary(h, torch.device("cuda", torch.cuda.current_device()), len(f))
 
 
-def _turned_view(t):
-    """bsp_tensor_t, batch entries and heads of [Z, H, S, D] or [T, H, D]."""
-    if t.dim() == 4:
-        return _heads(t), t.shape[0], t.shape[1], t.shape[2]
-    return _rows(t), 1, t.shape[1], t.shape[0]
-
-
 @_entry
 def bsp_rotary(R: Rotary, Q, K=None, positions=None, Q_out=None, K_out=None, *, inverse: bool = False, stream=None):
     """(Q_out, K_out): Q [Z, Hq, S, D] and K [Z, Hkv, S, D] (or ragged [T, H, D];
     K None: Q alone) turned by their rows' positions, int32 [Z, S], [S] ([T]) or
     None for 0 .. S - 1; inverse: by the opposite angles.  Strides as for
     bsp_window_attention; Q_out may be Q itself, K_out K."""
-    if Q.dim() not in (3, 4) or (K is not None and K.dim() != Q.dim()):
+    n = Q.dim()
+    if n not in (3, 4) or (K is not None and K.dim() != n):
         raise ValueError("Q and K must be [Z, heads, rows, D] or [T, heads, D]")
-    Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device) if Q_out is None else Q_out
-    _shape(Q_out, Q.shape, "Q_out")
-    q, Z, Hq, S = _turned_view(Q)
-    D, Hkv, k, ko, ts = Q.shape[-1], 0, None, None, [Q, Q_out]
-    if K is not None:
-        K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device) if K_out is None else K_out
-        _shape(K_out, K.shape, "K_out")
-        k, Zk, Hkv, Sk = _turned_view(K)
-        if (Zk, Sk, K.shape[-1]) != (Z, S, D):
+    if n == 4:
+        view = _heads
+        Z, Hq, S, D = Q.shape
+    else:
+        view, Z = _rows, 1
+        S, Hq, D = Q.shape
+    if Q_out is None:
+        Q_out = torch.empty(Q.shape, dtype=Q.dtype, device=Q.device)
+    else:
+        _shape(Q_out, Q.shape, "Q_out")
+    Hkv, k, ko = 0, None, None
+    if K is None:
+        if K_out is not None:
+            raise ValueError("K_out without K")
+        dt = _same(R, Q, Q_out)
+    else:
+        if K_out is None:
+            K_out = torch.empty(K.shape, dtype=K.dtype, device=K.device)
+        else:
+            _shape(K_out, K.shape, "K_out")
+        Hkv = K.shape[1]
+        if K.shape != ((Z, Hkv, S, D) if n == 4 else (S, Hkv, D)):
             raise ValueError(f"K must have Q's batch, rows and head size, got {tuple(K.shape)}")
         if Hkv < 1:
             raise ValueError("K must have a head")
-        ko = _turned_view(K_out)[0]
-        ts += [K, K_out]
-    elif K_out is not None:
-        raise ValueError("K_out without K")
-    step = 0
+        dt = _same(R, Q, Q_out, K, K_out)
+        k, ko = view(K), view(K_out)
+    pos, step = None, 0
     if positions is not None:
-        if positions.dim() == 2 and Q.dim() == 4:
+        if n == 4 and positions.dim() == 2:
             _ints(R, "positions", positions, (Z, S))
             step = S
         else:
             _ints(R, "positions", positions, (S,))
-    rc = lib().bsp_rotary(R.handle, _same(R, *ts), q, _turned_view(Q_out)[0], k, ko,
-                          None if positions is None else positions.data_ptr(), step, int(bool(inverse)), Z, Hq, Hkv, S, D,
-                          stream)
+        pos = positions.data_ptr()
+    rc = lib().bsp_rotary(R.handle, dt, view(Q), view(Q_out), k, ko, pos, step, 1 if inverse else 0, Z, Hq, Hkv, S, D, stream)
     if rc:
         raise BspError(rc, "bsp_rotary")
     return Q_out, K_out

@@ -120,6 +120,9 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
     const Book& b = a.b;
     const int tid = threadIdx.x;
     cudaGridDependencySynchronize();
+    int head[kSteps];  // the first pages' holders, on their way early
+#pragma unroll
+    for (int k = 0; k < kSteps; ++k) head[k] = kSteps * tid + k < b.n_pages ? b.refs[kSteps * tid + k] : 1;
     int items = 0;
     for (int s0 = 0; s0 < b.n_seq; s0 += kBig) {
         const int s = s0 + tid;
@@ -137,23 +140,31 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
     }
     __syncthreads();
     if (items == 0) return;
-    // item i: sequence, place in its row, page
-    auto item = [&](int i, int* seq, int* place) {
+    // item i: its sequence, place in the row, what the entry holds, and the length
+    struct Item {
+        int s, j, e, len;
+    };
+    auto look_up = [&](int i) {
         int lo = 0, hi = b.n_seq - 1;
+#pragma unroll 1
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
             if (ends[mid] > i) hi = mid;
             else lo = mid + 1;
         }
-        const int len = b.kv_len[lo];
-        *seq = lo;
-        *place = imin((len >> b.page_shift) + i - (lo ? ends[lo - 1] : 0), b.max_pages - 1);
-        return b.table[lo * b.max_pages + *place];
+        Item it;
+        it.s = lo, it.len = b.kv_len[lo];
+        it.j = imin((it.len >> b.page_shift) + i - (lo ? ends[lo - 1] : 0), b.max_pages - 1);
+        it.e = b.table[lo * b.max_pages + it.j];
+        return it;
     };
-    int s, j;
+    // (each thread keeps its first one: looked up again in every phase, 192 items
+    // took 10 us, not 7)
+    const Item mine = tid < items ? look_up(tid) : Item{};
+    auto item = [&](int i) { return i == tid ? mine : look_up(i); };
     bool shared = false;
     for (int i = tid; i < items; i += kBig) {
-        const int x = b.page_of(item(i, &s, &j));
+        const int x = b.page_of(item(i).e);
         if (x < 0) continue;
         a.users[x] = 0;
         a.first[x] = INT32_MAX;
@@ -162,7 +173,7 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
     shared = __syncthreads_or(shared);
     if (shared) {
         for (int i = tid; i < items; i += kBig) {
-            const int x = b.page_of(item(i, &s, &j));
+            const int x = b.page_of(item(i).e);
             if (x < 0) continue;
             atomicAdd(&a.users[x], 1);
             atomicMin(&a.first[x], i);
@@ -171,7 +182,7 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
         // the first item of each page says what becomes of it: 0, it keeps the
         // page; 1, all of them leave it to others
         for (int i = tid; i < items; i += kBig) {
-            const int x = b.page_of(item(i, &s, &j));
+            const int x = b.page_of(item(i).e);
             if (x < 0 || a.first[x] != i) continue;
             const int holders = b.refs[x], here = a.users[x];
             const bool leave = holders > here;
@@ -184,12 +195,12 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
         if (e >= b.n_pages) return false;  // reported; left as it is
         return e < 0 || (shared && (a.users[e] != 0 || a.first[e] != i));
     };
-    // free pages, as many as there are needs
     int need = 0;
     for (int i0 = 0; i0 < items; i0 += kBig) {
         const int i = i0 + tid;
-        need += __syncthreads_count(i < items && needs(i, item(i, &s, &j)));
+        need += __syncthreads_count(i < items && needs(i, item(i).e));
     }
+    // free pages, as many as there are needs (a page that is left is never free)
     int have = 0;
     for (int x0 = 0; x0 < b.n_pages && have < need; x0 += kSteps * kBig) {
         const int x = x0 + kSteps * tid;
@@ -197,7 +208,7 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
         int n = 0;
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-            is[k] = x + k < b.n_pages && b.refs[x + k] <= 0;
+            is[k] = x + k < b.n_pages && (x0 == 0 ? head[k] : b.refs[x + k]) <= 0;
             n += is[k];
         }
         int total;
@@ -211,24 +222,24 @@ __global__ void __launch_bounds__(kBig) reserve_kernel(const __grid_constant__ R
     int given = 0;
     for (int i0 = 0; i0 < items; i0 += kBig) {
         const int i = i0 + tid;
-        int e = -1;
-        const bool on = i < items && needs(i, e = item(i, &s, &j));
+        const Item it = i < items ? item(i) : Item{};
+        const bool on = i < items && needs(i, it.e);
         int total;
         const int at = given + scan(on, red, &total);
         given += total;
         if (!on) continue;
         if (at >= have) {
             // none left: a shared page stays shared
-            if (e >= 0) atomicAdd(&b.refs[e], 1);
+            if (it.e >= 0) atomicAdd(&b.refs[it.e], 1);
             set_status(b.status, BSP_ERR_OOM);
             continue;
         }
-        const int x = a.list[at], len = b.kv_len[s];
-        b.table[s * b.max_pages + j] = x;
+        const int x = a.list[at];
+        b.table[it.s * b.max_pages + it.j] = x;
         b.refs[x] = 1;
-        if (e >= 0 && j == len >> b.page_shift && (len & ((1 << b.page_shift) - 1))) {
-            a.src[s] = e;
-            a.dst[s] = x;
+        if (it.e >= 0 && it.j == it.len >> b.page_shift && (it.len & ((1 << b.page_shift) - 1))) {
+            a.src[it.s] = it.e;
+            a.dst[it.s] = x;
         }
     }
 }
