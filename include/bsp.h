@@ -555,8 +555,8 @@ int bsp_draft_tree(bsp_window_t w, const int32_t* q_start, const int32_t* kv_len
                    int32_t* positions, uint32_t* bits, int T, int n_seq, int words, void* stream);
 
 /* bsp_paged_attention for trees: node i sees key j < ctx by the handle's rule at
- * its position (positions[i], at least ctx), and node a of its sequence where its
- * bit says so; any bits will do, a row without a visible key gets output 0 and
+ * its position (positions[i], taken as ctx at least and 2^30 - 1 at most), and node
+ * a of its sequence where its bit says so; any bits will do, a row without a visible key gets output 0 and
  * log-sum-exp -inf.  A sequence with more than 32 words nodes, or more nodes than
  * kv_len, is left out and reported.  The rest as bsp_paged_attention, with its
  * workspace. */
@@ -672,7 +672,7 @@ int bsp_paged_copy(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const
 typedef struct bsp_rotary_s* bsp_rotary_t;
 
 /* frequencies: HOST double [n_pairs], radians per position, finite; n_pairs 1 ..
- * 64; interleaved 0 or 1.  A handle of the current device that holds no memory
+ * 64; amplitude finite as a float; interleaved 0 or 1.  A handle of the current device that holds no memory
  * there; immutable. */
 int bsp_rotary_create(const double* frequencies, int n_pairs, double amplitude, int interleaved, bsp_rotary_t* out);
 int bsp_rotary_destroy(bsp_rotary_t r);

@@ -229,7 +229,7 @@ extern "C" int bsp_rotary_create(const double* frequencies, int n_pairs, double 
                                  bsp_rotary_t* out) {
     if (!out) return BSP_ERR_INVALID_ARG;
     *out = nullptr;
-    if (!frequencies || n_pairs < 1 || !std::isfinite(amplitude) || (interleaved != 0 && interleaved != 1))
+    if (!frequencies || n_pairs < 1 || !std::isfinite((float)amplitude) || (interleaved != 0 && interleaved != 1))
         return BSP_ERR_INVALID_ARG;
     if (n_pairs > kMaxPairs) return BSP_ERR_UNSUPPORTED;
     for (int i = 0; i < n_pairs; ++i)

@@ -472,7 +472,7 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
                 if constexpr (TREE) {
                     ctx = w.a, end = w.zhi + 1;
                     node = w.row0 + pos - w.a;
-                    pos = imax(p.pos[node], ctx);
+                    pos = tree_position(p, node, ctx);
                     seen.first = __reduce_min_sync(0xffffffffu, pos);
                     seen.last = __reduce_max_sync(0xffffffffu, pos);
                 } else {

@@ -170,6 +170,14 @@ struct Prob {
     }
 };
 
+#if defined(__CUDACC__)
+// Position of a tree's node behind a context of ctx keys: the caller's, within
+// what the arithmetic of positions is made for.
+__device__ __forceinline__ int tree_position(const Prob& p, int node, int ctx) {
+    return imin(imax(p.pos[node], ctx), kMaxLen - 1);
+}
+#endif
+
 // The dK / dV kernel's problem (dense only): tiles are key tiles, steps the
 // query tiles with a row that sees one of its keys.
 struct KProb {

@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
             pos[u] = r < rows ? q.a + r / p.G : -1;  // dead rows see nothing
             if (TREE && r < rows) {
                 node[u] = it.g.t0 + q.tok0 + r / p.G;
-                pos[u] = imax(p.pos[node[u]], q.a);
+                pos[u] = tree_position(p, node[u], q.a);
             }
             m[u] = -INFINITY;
             l[u] = 0.f;

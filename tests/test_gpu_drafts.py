@@ -194,6 +194,79 @@ def test_a_chain_is_what_new_tokens_are(bsp, path):
     b.check(O, lse, 0.1, 90, 2)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes", [[1] * 40, [0, 2, 0, 1, 0], [0, 0, 3]], ids=str)
+def test_no_more_nodes_than_sequences(bsp, path, nodes, dtype):
+    """Tiles are single nodes then."""
+    b = Trees(nodes, [n + 37 * (i + 1) for i, n in enumerate(nodes)], 6, 2, 96, 16, DT[dtype], 8, "tree")
+    W = bsp.bsp_window_create(300, 1)
+    pos, bits = b.plan(bsp, W)
+    O, lse = b.attend(bsp, W, pos, bits, scale=0.1)
+    assert bsp.bsp_window_status(W) == 0
+    b.check(O, lse, 0.1, 300, 1)
+
+
+def test_positions_out_of_range(bsp, path):
+    """Positions are taken as at least the first node's and at most 2^30 - 1."""
+    b = Trees([4], [300], 2, 1, 64, 16, torch.bfloat16, 8, "star")
+    for window in (0, 50):
+        W = bsp.bsp_window_create(window, 3)
+        pos, bits = b.plan(bsp, W)
+        wild = pos.clone()
+        wild[1:] = ints([2 ** 31 - 1, -2 ** 31, -1])
+        tame = pos.clone()
+        tame[1:] = ints([2 ** 30 - 1, 296, 296])
+        got, want = (b.attend(bsp, W, x, bits, scale=0.1) for x in (wild, tame))
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and bsp.bsp_window_status(W) == 0
+        b.check(*want, 0.1, window, 3, None, [tame])
+
+
+@pytest.mark.parametrize("limit", [1, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_wait_that_runs_out_is_reported(bsp, monkeypatch, D, limit):
+    """Tiles of 48 steps take tens of microseconds, the limits are 1.4 to 4: the call
+    ends with its status, and the next one is right."""
+    monkeypatch.delenv("BSP_FORCE_SIMT", raising=False)
+    b = Trees([30, 1] * 75, [6144] * 150, 4, 2, D, 64, torch.bfloat16, 165)
+    W = bsp.bsp_window_create()
+    pos, bits = b.plan(bsp, W)
+    want = b.attend(bsp, W, pos, bits, scale=0.1)
+    assert bsp.bsp_window_status(W) == 0
+    bsp.bsp_diag_window_wait_limit(W, limit)
+    b.attend(bsp, W, pos, bits, scale=0.1)
+    assert bsp.bsp_window_status(W) == -6 and bsp.bsp_window_status(W) == 0
+    bsp.bsp_diag_window_wait_limit(W)
+    for _ in range(2):
+        assert all(torch.equal(a, c) for a, c in zip(b.attend(bsp, W, pos, bits, scale=0.1), want))
+    assert bsp.bsp_window_status(W) == 0
+
+
+def test_two_streams_at_once(bsp, path):
+    """One handle's trees and verifications on two streams."""
+    W = bsp.bsp_window_create(500, 4)
+    batches = [Trees([20, 40, 7] * 8, [900 + 50 * i for i in range(24)], 8, 2, 128, 32, torch.bfloat16, s) for s in (1, 2)]
+    rows = [rows_of(b.T, 3001, i) for i, b in enumerate(batches)]
+    u = torch.rand(batches[0].T, device="cuda")
+
+    def run(b, pq, stream):
+        pos, bits = b.plan(bsp, W, stream=stream)
+        O = b.attend(bsp, W, pos, bits, scale=0.09, stream=stream)
+        return (pos, *O, *bsp.bsp_draft_verify(W, *pq, b.parent.clamp(min=0), b.q_start, b.parent, u, u[:24].contiguous(), stream=stream))
+
+    want = [run(b, pq, None) for b, pq in zip(batches, rows)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, b, pq in zip(streams, batches, rows):
+            with torch.cuda.stream(s):
+                got.append(run(b, pq, s))
+        torch.cuda.synchronize()
+        for a, c in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, c))
+    assert bsp.bsp_window_status(W) == 0
+
+
 def test_hidden_nodes_of_infinite_score(bsp, path):
     """A node's keys of +inf or NaN reach nobody but those that see it."""
     b = Trees([20], [200], 4, 1, 64, 16, torch.bfloat16, 9, "star")

@@ -477,6 +477,45 @@ def test_drafted_decoding(bsp, greedy, window, sinks):
         assert torch.equal(K[pg, :, sl], k) and torch.equal(V_[pg, :, sl], v)
 
 
+def test_a_captured_turn_follows_the_book(bsp):
+    """Free, fork, reserve and copy in a graph, replayed on other lengths and parents."""
+    d = Device(bsp, 80, 6, 8, 16)
+    K, V = (torch.randn(80, 2, 16, 32, device="cuda") for _ in range(2))
+    want, parent = ints([0] * 6), ints(list(range(6)))
+
+    def turn():
+        bsp.bsp_pages_free(d.W, d.refs, d.table, d.kv, 16)
+        bsp.bsp_pages_fork(d.W, d.refs, d.table, d.kv, parent, 16)
+        src, dst = bsp.bsp_pages_reserve(d.W, d.refs, d.table, d.kv, want, 16)
+        bsp.bsp_paged_copy(d.W, K, V, src, dst)
+        return src, dst
+
+    turn()  # (nothing held, nothing wanted)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        src, dst = turn()
+    r = random.Random(5)
+    for _ in range(12):
+        d.book.free()
+        p = [r.choice((i, r.randrange(6), -1)) for i in range(6)]
+        d.book.fork(p)
+        w = [min(128, n + r.randint(0, 30)) for n in d.book.kv]
+        s, t, enough = d.book.reserve(w)
+        assert enough
+        k = K.clone()
+        for a, b in zip(s, t):
+            if a >= 0:
+                k[b] = K[a]
+        parent.copy_(ints(p))
+        want.copy_(ints(w))
+        graph.replay()
+        torch.cuda.synchronize()
+        d.same()
+        assert src.tolist() == s and dst.tolist() == t and torch.equal(K, k) and d.status() == 0
+        d.book.kv = w
+        d.kv.copy_(ints(w))
+
+
 def test_two_streams(bsp):
     """Books and caches of their own on two streams at once."""
     side = torch.cuda.Stream()

@@ -234,6 +234,30 @@ def test_streams_and_graphs(bsp):
     assert torch.equal(q, want[0]) and torch.equal(k, want[1])
 
 
+def test_gradient_in_a_graph(bsp):
+    freq, amp = bsp.rotary_frequencies(64)
+    R = bsp.bsp_rotary_create(freq, amp, True)
+    Q, K, dQ, dK = (randn((2, H, 33, 64), torch.bfloat16, 20 + i) for i, H in enumerate((4, 2, 4, 2)))
+    pos = torch.arange(33, dtype=torch.int32, device="cuda")
+    Q.requires_grad_()
+    K.requires_grad_()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.autograd.grad(bsp.rotary(R, Q, K, pos), (Q, K), (dQ, dK))
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gq, gk = torch.autograd.grad(bsp.rotary(R, Q, K, pos), (Q, K), (dQ, dK))
+    pos += 77
+    dQ.normal_()
+    graph.replay()
+    torch.cuda.synchronize()
+    at = pos.expand(2, 33)
+    check(gq, *turned(dQ, at, freq, amp, True, True), "dQ")
+    check(gk, *turned(dK, at, freq, amp, True, True), "dK")
+
+
 def test_refusals(bsp):
     R = bsp.bsp_rotary_create([1.0, 0.5])
     Q, K = torch.zeros(1, 2, 8, 32, device="cuda"), torch.zeros(1, 1, 8, 32, device="cuda")
@@ -265,7 +289,8 @@ def test_refusals(bsp):
     with pytest.raises(bsp.BspError) as e:  # 17 pairs of 32 columns
         bsp.bsp_rotary(bsp.bsp_rotary_create([1.0] * 17), Q)
     assert e.value.code == -1
-    for freq, amp, code in (([], 1.0, -1), ([math.nan], 1.0, -1), ([math.inf], 1.0, -1), ([1.0], math.nan, -1), ([1.0] * 65, 1.0, -2)):
+    for freq, amp, code in (([], 1.0, -1), ([math.nan], 1.0, -1), ([math.inf], 1.0, -1), ([1.0], math.nan, -1), ([1.0], 1e39, -1),
+                            ([1.0] * 65, 1.0, -2)):
         with pytest.raises(bsp.BspError) as e:
             bsp.bsp_rotary_create(freq, amp)
         assert e.value.code == code
