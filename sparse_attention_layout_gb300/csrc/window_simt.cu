@@ -58,18 +58,19 @@ __device__ __forceinline__ T* at(const View& v, int64_t i, int64_t j, int64_t k)
     return static_cast<T*>(v.ptr) + i * v.s[0] + j * v.s[1] + k * v.s[2];
 }
 
-// 64 rows of `DP` columns into shared memory (pitch DP + 4); row r from
+// 64 rows of `cols` columns into shared memory (pitch cols + 4); row r from
 // rowptr(r), or zeros where that is null.  fp32 rows are copied behind the
 // thread's back: landed() and a barrier make them visible.
 template <typename T, int DP, typename F>
-__device__ __forceinline__ void load_tile(float* dst, int D, F rowptr) {
-    constexpr int N = Vec16<T>::N, C = DP / N;
+__device__ __forceinline__ void load_tile(float* dst, int D, F rowptr, int cols = DP) {
+    constexpr int N = Vec16<T>::N;
+    const int C = cols / N;
 #pragma unroll 4
     for (int i = threadIdx.x; i < R * C; i += kT) {
         const int r = i / C, c = (i % C) * N;
         const T* src = rowptr(r);
         const bool live = src && c < D;
-        float* to = dst + r * (DP + 4) + c;
+        float* to = dst + r * (cols + 4) + c;
         if constexpr (std::is_same<T, float>::value) {
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
                          "l"(live ? src + c : reinterpret_cast<const T*>(kNothing)), "r"(live ? 16 : 0)
@@ -97,7 +98,8 @@ __device__ __forceinline__ void landed() {
 
 // s[u][v] = sum_d A[ty + 16 u][d] B[tx + 16 v][d], d < D
 template <int DP>
-__device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&s)[4][4], int D = DP) {
+__device__ __forceinline__ void dots(const float* A, const float* B, int ty, int tx, float (&s)[4][4], int D = DP,
+                                     int pitch = DP + 4) {
     float2 acc[4][4];
 #pragma unroll
     for (int u = 0; u < 4; ++u)
@@ -107,9 +109,9 @@ __device__ __forceinline__ void dots(const float* A, const float* B, int ty, int
     for (int d = 0; d < D; d += 4) {
         float4 a[4], b[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) a[u] = *reinterpret_cast<const float4*>(A + (ty + 16 * u) * (DP + 4) + d);
+        for (int u = 0; u < 4; ++u) a[u] = *reinterpret_cast<const float4*>(A + (ty + 16 * u) * pitch + d);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) b[v] = *reinterpret_cast<const float4*>(B + (tx + 16 * v) * (DP + 4) + d);
+        for (int v = 0; v < 4; ++v) b[v] = *reinterpret_cast<const float4*>(B + (tx + 16 * v) * pitch + d);
 #pragma unroll
         for (int u = 0; u < 4; ++u)
 #pragma unroll
@@ -127,7 +129,7 @@ __device__ __forceinline__ void dots(const float* A, const float* B, int ty, int
 // acc[u][g] (columns 64 g + 4 tx ..) += sum_k P[ty + 16 u][k] B[k][..]
 template <int DP>
 __device__ __forceinline__ void accumulate(const float* P, const float* B, int ty, int tx,
-                                           float2 (&acc)[4][DP / 64][2]) {
+                                           float2 (&acc)[4][DP / 64][2], int pitch = DP + 4) {
     constexpr int NG = DP / 64;
 #pragma unroll 2
     for (int k4 = 0; k4 < R; k4 += 4) {
@@ -139,7 +141,7 @@ __device__ __forceinline__ void accumulate(const float* P, const float* B, int t
             float4 b[NG];
 #pragma unroll
             for (int g = 0; g < NG; ++g)
-                b[g] = *reinterpret_cast<const float4*>(B + (k4 + k) * (DP + 4) + 64 * g + 4 * tx);
+                b[g] = *reinterpret_cast<const float4*>(B + (k4 + k) * pitch + 64 * g + 4 * tx);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const float w = k == 0 ? pa[u].x : k == 1 ? pa[u].y : k == 2 ? pa[u].z : pa[u].w;
@@ -191,9 +193,11 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
 // nodes over 300 to 6000 keys, 6 heads of 80: 67 us; 62 and 59 with one of the two,
 // 55 with both).
 template <typename T, int DP, bool PAGED, bool TREE>
-__global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __grid_constant__ Args A,
+__global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(const __grid_constant__ Args A,
                                                      const __grid_constant__ SimtPlan plan) {
-    constexpr int NG = DP / 64, PITCH = DP + 4;
+    constexpr int NG = DP / 64;
+    // TREE: rows no longer than the head, so that two CTAs fit an SM's shared memory
+    const int cols = TREE ? A.D : DP, PITCH = cols + 4;
     extern __shared__ float sm[];
     float *Qs = sm, *Ks = Qs + R * PITCH, *Vs = Ks + R * PITCH, *Ps = Vs + R * PITCH;
     __shared__ Start start;
@@ -217,7 +221,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
         load_tile<T, DP>(Qs, A.D, [&](int r) -> const T* {
             if (r >= rows) return nullptr;
             return at<const T>(A.Q, w.z, (int64_t)w.hk * p.G + r % p.G, (int64_t)it.g.t0 + q.tok0 + r / p.G);
-        });
+        }, cols);
         float m[4], l[4];
         int pos[4], node[4];  // TREE: the row's token
         float2 acc[4][NG][2];
@@ -268,7 +272,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
                         return pg < 0 ? nullptr : at<const T>(v, pg, w.hk, j & ((1 << p.page_shift) - 1));
                     }
                     return wanted(j) ? at<const T>(v, w.z, w.hk, j) : nullptr;
-                });
+                }, cols);
             copies_end();
         };
         find_pages(0);
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
             landed<1>();
             __syncthreads();
             float s[4][4];
-            dots<DP>(Qs, Ks, ty, tx, s, TREE ? A.D : DP);
+            dots<DP>(Qs, Ks, ty, tx, s, cols, PITCH);
             __syncthreads();
             copy(Ks, A.K, n + 1);
 #pragma unroll
@@ -313,7 +317,7 @@ __global__ void __launch_bounds__(kT, DP == 64 ? 2 : 1) forward_kernel(const __g
             }
             landed<1>();
             __syncthreads();
-            accumulate<DP>(Ps, Vs, ty, tx, acc);
+            accumulate<DP>(Ps, Vs, ty, tx, acc, PITCH);  // (columns behind `cols` are never stored)
             __syncthreads();
             copy(Vs, A.V, n + 1);
         }
@@ -589,10 +593,13 @@ constexpr size_t tiles_bytes(int tiles, int patches) {
     return sizeof(float) * ((size_t)tiles * R * (DP + 4) + (size_t)patches * R * PP);
 }
 
+// the tiles of trees: rows of the head's own columns
+constexpr size_t tree_bytes(int D) { return sizeof(float) * ((size_t)3 * R * (D + 4) + (size_t)R * PP); }
+
 template <typename T, int DP>
 int forward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
-    size_t smem = tiles_bytes<DP>(3, 1);
+    size_t smem = c.p.words ? tree_bytes(c.D) : tiles_bytes<DP>(3, 1);
     if (smem < (size_t)c.p.nseg * sizeof(int)) smem = (size_t)c.p.nseg * sizeof(int);
     SimtPlan plan{};
     bool cut = true;
@@ -623,7 +630,7 @@ int backward_t(Call& c, const Args& a, int grid) {
 
 #define BSP_WIN_DISPATCH(fn)                                                                    \
     const Args a = make_args(c);                                                                \
-    const int per_sm = c.p.words && c.D > 64 ? 1 : kSimtPerSm;                                  \
+    const int per_sm = c.p.words && c.D > 112 ? 1 : kSimtPerSm;                                 \
     const int grid = imin(per_sm * sm_count(), SimtPlan::kCtas);                                \
     switch (c.dtype) {                                                                          \
         case BSP_F32: return c.D <= 64 ? fn<float, 64>(c, a, grid) : fn<float, 128>(c, a, grid); \
