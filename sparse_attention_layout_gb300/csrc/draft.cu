@@ -102,8 +102,8 @@ struct Tree {
 // sum whose additions' errors all go to its second part: some thousand terms are
 // off by 2^-45 of their sum.  (GB300 has two fp64 lanes an SM, and an fp64
 // operation takes over 100 cycles: with them for the walk and the sums of the
-// warps, one sequence of 32000 entries took 18 us, not 11, and with every warp
-// adding up the sums 69.)
+// warps, 64 sequences of 128000 entries took 27 us, not 23.5, and with every warp
+// adding up all sums 230.)
 struct Two {
     float hi = 0.f, lo = 0.f;
     __device__ __forceinline__ Two() {}
@@ -233,6 +233,14 @@ __device__ __forceinline__ void block_barrier() { asm volatile("bar.sync 1, %0;"
 // Each warp of the cluster holds a run of the vocabulary.  The sums of the runs go
 // to every CTA through the cluster's shared memory; the CTA that the number falls
 // to looks for the token in that run, a step of 32 pieces to a warp.
+//
+// Bound by the chain of what follows one another, most of all the reads: offsets,
+// parents and tokens, their probabilities (2.4 us), the pass (64 sequences of
+// 128000 fp32 entries: 65 MB of two rows each, 11 us for 9.6 at a copy's rate),
+// the sums and the search (3.3 us); with the launch 19 us, and 7 for one sequence of
+// 32000.  The walk's code stands once, and so does the pass': the first
+// instructions come from memory too, and with a copy of the pass wherever one is
+// asked for, one sequence took 18 us under the profiler, not 9.5.
 template <typename T, bool DRAWN>
 __global__ void __launch_bounds__(kVerifyT, 2) draft_verify_kernel(const __grid_constant__ VerifyArgs a) {
     using R = Rows<T, DRAWN>;

@@ -457,6 +457,29 @@ def test_rows_of_any_stride(bsp, dtype):
         verify(bsp, W, nodes, parents, P[:, a:a + V], None, tok, accept, sample)
 
 
+def test_a_large_vocabulary_and_far_rows(bsp):
+    """A million entries, and rows behind 2^31 elements."""
+    W = bsp.bsp_window_create()
+    r = random.Random(2)
+    nodes, V = [6, 9], 1000003
+    parents = [grown(n, r, 3) for n in nodes]
+    p, q = (x.to(torch.bfloat16) for x in rows_of(15, V, 2, 1.0))
+    tok = tokens_for(q, parents, [0, 6], 2, False)
+    accept, sample = torch.rand(15, device="cuda"), torch.rand(2, device="cuda")
+    for draft in (q, None):
+        want = verify(bsp, W, nodes, parents, p, draft, tok, accept, sample)
+        shift = 2200  # rows in front: the trees' begin at 2.2e9 elements
+        far = [torch.cat([torch.empty(shift, V, dtype=x.dtype, device="cuda"), x]) for x in (p, q)]
+
+        def behind(x):
+            return torch.cat([torch.zeros(shift, dtype=x.dtype, device="cuda"), x])
+
+        got = bsp.bsp_draft_verify(W, far[0], None if draft is None else far[1], behind(tok), ints([shift, shift + 6, shift + 15]),
+                                   behind(ints([x for t in parents for x in t])), behind(accept), sample)
+        assert torch.equal(got[0][shift:], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    assert bsp.bsp_window_status(W) == 0
+
+
 def test_borders(bsp):
     """Numbers on a border go to the entry behind it; entries of 0 are never taken."""
     W = bsp.bsp_window_create()

@@ -235,6 +235,20 @@ def test_copy(bsp, n_pages, H, page, D, slots_first, dtype):
     bsp.bsp_paged_copy(W, K, V, ints([]), ints([]))
 
 
+def test_both_caches_in_one_tensor(bsp):
+    """K and V of a page side by side; rows that the accepted ones move along too."""
+    both = torch.randn(30, 2, 3, 32, 48, device="cuda", dtype=torch.float32).to(torch.float16)
+    W, want = bsp.bsp_window_create(), both.clone()
+    want[[4, 9]] = both[[20, 2]]
+    bsp.bsp_paged_copy(W, both[:, 0], both[:, 1], ints([20, 2]), ints([4, 9]))
+    assert torch.equal(both, want)
+    table, kv, starts = ints([[7, 3]]), ints([40]), ints([0, 12])  # nodes at 28 .. 39
+    for to, at in ((28, 28), (29, 31), (30, 39)):
+        want[[7, 3][to // 32], :, :, to % 32] = both[[7, 3][at // 32], :, :, at % 32]
+    bsp.bsp_paged_keep(W, both[:, 0], both[:, 1], starts, kv, table, ints([0, 3, 11] + [-1] * 9), ints([3]))
+    assert torch.equal(both, want) and bsp.bsp_window_status(W) == 0
+
+
 def test_copy_beyond_32_bit_offsets(bsp):
     K = torch.zeros(16500, 8, 128, 128, dtype=torch.bfloat16, device="cuda")
     V = torch.zeros(16500, 8, 128, 128, dtype=torch.bfloat16, device="cuda")

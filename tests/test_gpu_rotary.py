@@ -123,6 +123,21 @@ def test_ragged_rows(bsp, pairs):
         assert torch.equal(a.transpose(0, 1), b[0])
 
 
+def test_a_fused_projection_in_place(bsp):
+    """Q and K as slices of one [T, heads, D] tensor, turned where they are; V beside
+    them stays."""
+    freq, amp = bsp.rotary_frequencies(64)
+    for dtype, pairs in ((torch.float16, False), (torch.float32, True)):
+        R = bsp.bsp_rotary_create(freq, amp, pairs)
+        x = randn((1, 6 + 2 + 2, 91, 64), dtype, 4, "rows")[0].transpose(0, 1)
+        assert x.is_contiguous()
+        pos = torch.arange(91, dtype=torch.int32, device="cuda") * 7
+        q, k = bsp.bsp_rotary(R, x[:, :6], x[:, 6:8], pos)
+        v = x[:, 8:].clone()
+        bsp.bsp_rotary(R, x[:, :6], x[:, 6:8], pos, x[:, :6], x[:, 6:8])
+        assert torch.equal(x[:, :6], q) and torch.equal(x[:, 6:8], k) and torch.equal(x[:, 8:], v)
+
+
 def test_far_positions(bsp):
     """Angles at any 32-bit position, against 50 decimal digits."""
     getcontext().prec = 50
