@@ -1238,28 +1238,55 @@ def bsp_rotary(R: Rotary, Q, K=None, positions=None, Q_out=None, K_out=None, *, 
     return Q_out, K_out
 
 
-def _turn_taken(Q, K, positions, R, inverse):
-    return bsp_rotary(R, _taken(Q), None if K is None else _taken(K), positions, inverse=inverse)
+def _strides_taken(t):
+    return t if t.is_contiguous() and t.data_ptr() % 16 == 0 else _taken(t)
+
+
+@_entry
+def _turned_back(R, dQ, dK, positions, inverse, stream=None):
+    """The gradients of a turn, given those of its outputs (either may be None):
+    the opposite turn.  Sizes and types are the forward's, which has checked them."""
+    first = dK if dQ is None else dQ
+    if first.dim() == 4:
+        view, (Z, H, S, D) = _heads, first.shape
+    else:
+        view, Z, (S, H, D) = _rows, 1, first.shape
+    out = torch.empty(first.shape, dtype=first.dtype, device=R.device)
+    first = _strides_taken(first)
+    Hkv, k, ko, other = 0, None, None, None
+    if dQ is not None and dK is not None:
+        Hkv, other = dK.shape[1], torch.empty(dK.shape, dtype=dK.dtype, device=R.device)
+        dK = _strides_taken(dK)
+        k, ko = view(dK), view(other)
+    pos, step = (None, 0) if positions is None else (positions.data_ptr(), S if positions.dim() == 2 else 0)
+    rc = lib().bsp_rotary(R.handle, _DTYPES[first.dtype], view(first), view(out), k, ko, pos, step, inverse, Z, H, Hkv, S, D,
+                          stream)
+    if rc:
+        raise BspError(rc, "bsp_rotary")
+    return (None, out) if dQ is None else (out, other)
 
 
 class _RotaryPositions(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, positions, R, inverse):
         ctx.set_materialize_grads(False)
-        ctx.save_for_backward(positions)
-        ctx.R, ctx.inverse = R, inverse
-        return _turn_taken(Q, K, positions, R, inverse)
+        ctx.args = R, positions, None if positions is None else positions._version, inverse
+        return bsp_rotary(R, _strides_taken(Q), None if K is None else _strides_taken(K), positions, inverse=inverse)
 
     @staticmethod
     def backward(ctx, dQ, dK):
-        positions, = ctx.saved_tensors
-        got = [g for g in (dQ, dK) if g is not None]
-        if not got:
+        R, positions, version, inverse = ctx.args
+        if positions is not None and positions._version != version:
+            raise RuntimeError("the positions of bsp.rotary were changed in place before its gradient was computed")
+        if dQ is None and dK is None:
             return None, None, None, None, None
-        # (a graph of the gradient only where one is asked for)
-        turn = _RotaryPositions.apply if torch.is_grad_enabled() else _turn_taken
-        got = list(turn(got[0], got[1] if len(got) > 1 else None, positions, ctx.R, not ctx.inverse))
-        return (got.pop(0) if dQ is not None else None, got.pop(0) if dK is not None else None, None, None, None)
+        if not torch.is_grad_enabled():
+            dQ, dK = _turned_back(R, dQ, dK, positions, 0 if inverse else 1)
+        elif dQ is None:
+            dK = _RotaryPositions.apply(dK, None, positions, R, not inverse)[0]
+        else:
+            dQ, dK = _RotaryPositions.apply(dQ, dK, positions, R, not inverse)
+        return dQ, dK, None, None, None
 
 
 def rotary(R: Rotary, Q, K=None, positions=None):

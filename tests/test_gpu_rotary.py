@@ -184,6 +184,28 @@ def test_gradient(bsp, pairs, dtype):
     assert torch.equal(bsp.rotary(R, Q.detach(), K.detach(), pos)[1], k)
 
 
+def test_gradient_of_ragged_rows(bsp):
+    """[T, heads, D] tokens, with shared, strided and missing gradients."""
+    freq, amp = bsp.rotary_frequencies(64)
+    R = bsp.bsp_rotary_create(freq, amp)
+    pos = torch.randint(0, 500, (41,), dtype=torch.int32).cuda()
+    Q, K = (randn((1, H, 41, 64), torch.float32, 30 + H, "rows")[0].transpose(0, 1).requires_grad_() for H in (4, 2))
+    dQ, dK = randn((1, 4, 41, 64), torch.float32, 40)[0].transpose(0, 1), randn((1, 1, 41, 64), torch.float32, 41)[0].transpose(0, 1)
+    dK = dK.expand(41, 2, 64)
+    for positions, at in ((pos, pos), (None, torch.arange(41, device="cuda"))):
+        q, k = bsp.rotary(R, Q, K, positions)
+        gq, gk = torch.autograd.grad((q, k), (Q, K), (dQ, dK), retain_graph=True)
+        for got, d in ((gq, dQ), (gk, dK)):
+            want, bound = turned(d.transpose(0, 1)[None], at[None], freq, amp, False, True)
+            check(got.transpose(0, 1)[None], want, bound, "gradient")
+        only, = torch.autograd.grad(k, K, dK)
+        assert torch.equal(only, gk)
+    q, k = bsp.rotary(R, Q, K, pos)
+    pos += 1
+    with pytest.raises(RuntimeError):
+        torch.autograd.grad(q, Q, dQ)
+
+
 def test_gradient_by_differences(bsp):
     """The map is linear: f(x + h d) - f(x - h d) is 2 h times the derivative but
     for rounding, 6 * 2^-24 A (|x_a| + |x_b|) per entry, against dot products of
