@@ -9,7 +9,20 @@
 namespace bsp {
 namespace {
 
+// The encoder is a driver call and fails without a current context, which a thread
+// has only once it has made a runtime call that needs one: a thread of autograd's
+// may come here with none.  Setting the device it has makes it current.
+bool context_is_current() {
+    thread_local int bound = -1;
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev != bound && cudaSetDevice(dev) != cudaSuccess) return false;
+    bound = dev;
+    return true;
+}
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    if (!context_is_current()) return nullptr;
     static std::once_flag once;
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     std::call_once(once, [] {
