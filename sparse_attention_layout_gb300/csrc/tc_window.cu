@@ -49,6 +49,8 @@ constexpr int kMinShare = 2;
 struct None {};
 template <int MODE>
 using Split = std::conditional_t<MODE == kDense, TcPlan, None>;
+template <bool TREE>
+using Problem = std::conditional_t<TREE, TreeProb, Prob>;
 
 template <int DP>
 struct Smem {
@@ -64,8 +66,9 @@ struct Smem {
     static constexpr int kAlloc = kBytes + 1024;
 };
 
+template <typename P>
 struct Args {
-    Prob p;
+    P p;
     View O;
     float* lse;
     int64_t lz, lh, lt;
@@ -82,7 +85,7 @@ struct Args {
 template <typename T, int DP, int MODE, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
 window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
-                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args args,
+                 const __grid_constant__ CUtensorMap tmV, const __grid_constant__ Args<Problem<TREE>> args,
                  const __grid_constant__ Split<MODE> plan) {
     using SM = Smem<DP>;
     constexpr bool PAGED = MODE != kDense;
@@ -110,7 +113,8 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
     __shared__ Ring ring;
     __shared__ Work cut;  // the tile that begins here and is cut at the end of the share
 
-    const Prob& p = args.p;
+    using P = Problem<TREE>;
+    const P& p = args.p;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Stop ab{&abort_flag};
 
@@ -178,10 +182,10 @@ window_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant_
         const int my_page = lane % pages, my_panel = lane / pages;
         const uint32_t page_bytes = PAGED ? 128u << p.page_shift : 128u * 128u;
         auto begin = [&] {
-            if constexpr (PAGED) return Walk<Prob, MODE>(p, start);
-            else return Walk<Prob, MODE>(p, plan.tab, plan.s[blockIdx.x]);
+            if constexpr (PAGED) return Walk<P, MODE>(p, start);
+            else return Walk<P, MODE>(p, plan.tab, plan.s[blockIdx.x]);
         };
-        Walk<Prob, MODE> walk = begin();
+        Walk<P, MODE> walk = begin();
         Work w;
         // one step is loaded while the next one's place, and its page number,
         // are on their way
@@ -647,7 +651,7 @@ int launch(Call& c) {
     static std::atomic<uint64_t> prepared{0};
     if ((rc = prepare_kernel(kern, smem, prepared))) return rc;
     const int grid = imin(sm_count(), TcPlan::kCtas);
-    Args a{p, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, c.cuts, c.slots};
+    const Args<Problem<TREE>> a{Problem<TREE>{p}, c.O, c.lse, c.lz, c.lh, c.lt, c.D, c.scale * kLog2e, c.cuts, c.slots};
     Split<MODE> plan;
     bool cut = true;
     if constexpr (!PAGED)

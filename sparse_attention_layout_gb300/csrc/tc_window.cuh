@@ -145,7 +145,10 @@ struct Unseen {
 };
 
 __device__ __forceinline__ Keys tile_keys(const Prob& p, const Work& w) {
-    return Keys{window_low(w.a, p.window), p.words ? w.zhi : w.a + w.nt - 1, p.sinks};
+    return Keys{window_low(w.a, p.window), w.a + w.nt - 1, p.sinks};
+}
+__device__ __forceinline__ Keys tile_keys(const TreeProb& p, const Work& w) {
+    return Keys{window_low(w.a, p.window), w.zhi, p.sinks};
 }
 
 __device__ __forceinline__ Work make_work(const Prob& p, const Item& it) {

@@ -113,8 +113,6 @@ struct Seg {
 };
 
 // A query tile: tokens tok0 .. tok0 + nt - 1 of its segment at positions a .. b.
-// Of a tree of drafted tokens: a is the position of the tree's first node, b the
-// last slot, whichever of its nodes the tile holds.
 struct QTile {
     int tok0, nt, a, b;
 };
@@ -133,14 +131,13 @@ struct Prob {
     const int* table;
     int* status;
     int attempts;   // of the wait for a tile (tensor-core kernels)
-    // trees of drafted tokens: positions, and the nodes that each sees (words 0: none)
+    // trees of drafted tokens (words 0: none): positions, and the nodes that each sees
     const int* pos;
     const uint32_t* bits;
     int words;
 
     BSP_HD bool bad_seg(int q0, int q1, int kv) const {
-        return q0 < 0 || q1 < q0 || q1 > T || kv < 0 || kv > (max_pages << page_shift) ||
-               (words && (q1 - q0 > 32 * words || q1 - q0 > kv));
+        return q0 < 0 || q1 < q0 || q1 > T || kv < 0 || kv > (max_pages << page_shift);
     }
 #if defined(__CUDACC__)
     __device__ __forceinline__ Seg seg(int s) const {
@@ -157,11 +154,39 @@ struct Prob {
         QTile q;
         q.tok0 = t * TQ;
         q.nt = imin(TQ, g.qlen - q.tok0);
-        q.a = g.kvlen - g.qlen + (words ? 0 : q.tok0);
-        q.b = words ? g.kvlen - 1 : q.a + q.nt - 1;
+        q.a = g.kvlen - g.qlen + q.tok0;
+        q.b = q.a + q.nt - 1;
         return q;
     }
     BSP_HD Span span(const QTile& q) const { return span_of(q.a, q.b, window, sinks, kshift); }
+    BSP_HD int steps(const Seg& g, int t) const { return span(qtile(g, t)).n; }
+    BSP_HD int describe(const Seg& g, int t, QTile& q, Span& sp) const {
+        q = qtile(g, t);
+        sp = span(q);
+        return sp.n;
+    }
+};
+
+// The same of trees of drafted tokens: whichever nodes a tile holds, a is the
+// position of its tree's first node and b the last one's slot.  (A type of its own:
+// with the question asked at run time, new tokens without trees took 2 % longer.)
+struct TreeProb : Prob {
+    BSP_HD bool bad_seg(int q0, int q1, int kv) const {
+        return Prob::bad_seg(q0, q1, kv) || q1 - q0 > 32 * words || q1 - q0 > kv;
+    }
+#if defined(__CUDACC__)
+    __device__ __forceinline__ Seg seg(int s) const {
+        const int q0 = q_start[s], q1 = q_start[s + 1], kv = kv_len[s];
+        if (bad_seg(q0, q1, kv)) return Seg{0, 0, 0, 0};
+        return Seg{q0, q1 - q0, kv, (q1 - q0 + TQ - 1) / TQ};
+    }
+#endif
+    BSP_HD QTile qtile(const Seg& g, int t) const {
+        QTile q = Prob::qtile(g, t);
+        q.a = g.kvlen - g.qlen;
+        q.b = g.kvlen - 1;
+        return q;
+    }
     BSP_HD int steps(const Seg& g, int t) const { return span(qtile(g, t)).n; }
     BSP_HD int describe(const Seg& g, int t, QTile& q, Span& sp) const {
         q = qtile(g, t);
@@ -359,8 +384,8 @@ __device__ __forceinline__ void locate_plain(const Prob& p, int min_share, uint3
 // gets this many steps.  Each thread adds up a run of the line, one scan gives
 // the runs' starts, and the thread whose run holds the share's first step finds
 // it.  Out of line: the kernels' loops then stay within the instruction cache.
-template <int NT>
-__device__ __noinline__ void locate(const Prob& p, int min_share, int* seg_end, uint32_t* red, Start* out) {
+template <int NT, typename P>
+__device__ __noinline__ void locate(const P& p, int min_share, int* seg_end, uint32_t* red, Start* out) {
     const int tid = threadIdx.x;
     int tiles = 0;  // one repetition of every segment
     bool bad = false;

@@ -33,8 +33,9 @@ constexpr int R = kSimtRows;      // query rows, and keys, per tile
 constexpr int kShift = 6;
 constexpr int PP = R + 4;         // pitch of P
 
-struct Args {
-    Prob p;
+template <typename P>
+struct ArgsOf {
+    P p;
     View Q, K, V, O, dO, dQ, dK, dV;
     float* lse;
     int64_t lz, lh, lt;
@@ -44,6 +45,10 @@ struct Args {
     Cut* cuts;
     float* slots;
 };
+
+using Args = ArgsOf<Prob>;
+template <bool TREE>
+using Problem = std::conditional_t<TREE, TreeProb, Prob>;
 
 struct Where {  // a segment repetition's batch entry and KV head
     int z, hk;
@@ -181,7 +186,8 @@ __device__ __forceinline__ void store4(T* dst, float a, float b, float c, float 
 }
 
 // Sequences with impossible lengths count as empty; one CTA reports them.
-__device__ __forceinline__ void report_bad_segs(const Prob& p) {
+template <typename P>
+__device__ __forceinline__ void report_bad_segs(const P& p) {
     if (!p.paged || blockIdx.x) return;
     for (int s = threadIdx.x; s < p.nseg; s += blockDim.x)
         if (p.bad_seg(p.q_start[s], p.q_start[s + 1], p.kv_len[s])) set_status(p.status, BSP_ERR_DEVICE_CHECK);
@@ -193,7 +199,7 @@ __device__ __forceinline__ void report_bad_segs(const Prob& p) {
 // nodes over 300 to 6000 keys, 6 heads of 80: 67 us; 62 and 59 with one of the two,
 // 55 with both).
 template <typename T, int DP, bool PAGED, bool TREE>
-__global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(const __grid_constant__ Args A,
+__global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(const __grid_constant__ ArgsOf<Problem<TREE>> A,
                                                      const __grid_constant__ SimtPlan plan) {
     constexpr int NG = DP / 64;
     // TREE: rows no longer than the head, so that two CTAs fit an SM's shared memory
@@ -203,13 +209,14 @@ __global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(c
     __shared__ Start start;
     __shared__ uint32_t red[32];
     __shared__ int pages[2][R];  // page of each key's slot, of this step and the next
-    const Prob& p = A.p;
+    using P = Problem<TREE>;
+    const P& p = A.p;
     report_bad_segs(p);
     if constexpr (PAGED) locate<kT>(p, 1, reinterpret_cast<int*>(sm), red, &start);
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    Walk<Prob, PAGED ? kRagged : kDense> walk(p, PAGED ? start.tab : plan.tab, PAGED ? start.cta : plan.s[blockIdx.x]);
+    Walk<P, PAGED ? kRagged : kDense> walk(p, PAGED ? start.tab : plan.tab, PAGED ? start.cta : plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
         const Where w = where(p, it.rep);
@@ -605,7 +612,9 @@ int forward_t(Call& c, const Args& a, int grid) {
     bool cut = true;
     int rc = c.p.paged ? BSP_OK : query_plan(c, grid, &plan.tab, plan.s, &cut);
     if (rc) return rc;
-    rc = c.p.words   ? launch(forward_kernel<T, DP, true, true>, grid, smem, c.stream, a, plan)
+    const ArgsOf<TreeProb> t{TreeProb{a.p}, a.Q, a.K, a.V, a.O, a.dO, a.dQ, a.dK, a.dV, a.lse, a.lz, a.lh, a.lt, a.delta,
+                             a.D, a.scale, a.c2, a.cuts, a.slots};
+    rc = c.p.words   ? launch(forward_kernel<T, DP, true, true>, grid, smem, c.stream, t, plan)
          : c.p.paged ? launch(forward_kernel<T, DP, true, false>, grid, smem, c.stream, a, plan)
                      : launch(forward_kernel<T, DP, false, false>, grid, smem, c.stream, a, plan);
     return rc || !cut ? rc : launch_join(c, R, grid, false);
