@@ -591,7 +591,7 @@ int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, c
  * with parent -1 behind node 0 are places without a token.  Checked on the device:
  * a sequence outside the T rows or of more than 1024 nodes counts as without
  * nodes, a node with a wrong parent or a token outside 0 .. V - 1 as without a
- * token. */
+ * token.  T, V <= 2^30. */
 int bsp_draft_verify(bsp_window_t w, int dtype, const void* target, int64_t target_stride, const void* draft,
                      int64_t draft_stride, const int32_t* tokens, const int32_t* q_start, const int32_t* parent,
                      const float* accept, const float* sample, int32_t* path, int32_t* count, int32_t* token, int T,
@@ -682,7 +682,8 @@ int bsp_rotary_destroy(bsp_rotary_t r);
  * z at positions[z * position_stride + i], or NULL: 0 .. S - 1.  inverse 1: by the
  * opposite angles, which is also the gradient (dQ, dK from those of Q_out, K_out).
  * A tensor may be turned in its own place (same pointer and strides), not over
- * another. */
+ * another.  Z * S <= 2^30 and at most 65535 heads together (beyond:
+ * BSP_ERR_UNSUPPORTED). */
 int bsp_rotary(bsp_rotary_t r, int dtype, const bsp_tensor_t* Q, const bsp_tensor_t* Q_out, const bsp_tensor_t* K,
                const bsp_tensor_t* K_out, const int32_t* positions, int64_t position_stride, int inverse, int Z, int Hq,
                int Hkv, int S, int D, void* stream);

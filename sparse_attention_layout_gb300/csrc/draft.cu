@@ -237,7 +237,7 @@ __device__ __forceinline__ void block_barrier() { asm volatile("bar.sync 1, %0;"
 // Bound by the chain of what follows one another, most of all the reads: offsets,
 // parents and tokens, their probabilities (2.4 us), the pass (64 sequences of
 // 128000 fp32 entries: 65 MB of two rows each, 11 us for 9.6 at a copy's rate),
-// the sums and the search (3.3 us); with the launch 19 us, and 7 for one sequence of
+// the sums and the search (3.3 us); with the launch 20 us, and 7 for one sequence of
 // 32000.  The walk's code stands once, and so does the pass': the first
 // instructions come from memory too, and with a copy of the pass wherever one is
 // asked for, one sequence took 18 us under the profiler, not 9.5.
@@ -262,6 +262,7 @@ __global__ void __launch_bounds__(kVerifyT, 2) draft_verify_kernel(const __grid_
     const int W = C * NW;
     const T* target = static_cast<const T*>(a.target);
     const T* draft = static_cast<const T*>(a.draft);
+    cluster.sync();  // all of them have begun: their shared memory may be written
     cudaGridDependencySynchronize();
     const float number = a.sample[s];
     if (rank == 0) {

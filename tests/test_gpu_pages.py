@@ -89,7 +89,9 @@ class Device:
 
 # (n_pages, n_seq, max_pages, page, turns)
 BOOKS = [(1, 1, 1, 16, 10), (7, 3, 4, 16, 60), (200, 12, 30, 16, 40), (5000, 60, 90, 32, 15), (3000, 1500, 8, 16, 8),
-         (20000, 5, 4000, 16, 6), (70000, 40, 1024, 64, 4)]
+         (20000, 5, 4000, 16, 6), (70000, 40, 1024, 64, 4),
+         (16384, 30, 500, 16, 4), (16385, 30, 500, 16, 4), (65537, 30, 500, 16, 3),
+         (100000, 300, 400, 16, 3)]
 
 
 @pytest.mark.parametrize("case", BOOKS, ids=str)
@@ -127,6 +129,33 @@ def test_turns(bsp, case):
     d.kv = ints(d.book.kv)
     d.free()
     assert d.book.refs == [0] * n_pages
+
+
+@pytest.mark.parametrize("n_pages", [4096, 4097, 16385, 65536, 200001])
+def test_compaction_of_far_pages(bsp, n_pages):
+    """Whole scans of pages that are free, or in use, or all of them."""
+    W = bsp.bsp_window_create()
+    g = torch.Generator(device="cuda").manual_seed(n_pages)
+    half = torch.zeros(n_pages, dtype=torch.int32, device="cuda")
+    half[n_pages - n_pages // 2:] = 1  # the last half: every page moves, or nearly
+    last = torch.zeros_like(half)
+    last[-1] = 3
+    for refs in (half, last, torch.zeros_like(half), torch.ones_like(half), 1 - half,
+                 torch.randint(0, 3, (n_pages,), generator=g, device="cuda", dtype=torch.int32)):
+        table = refs.nonzero()[:, 0].to(torch.int32)
+        table = torch.cat([table, table.new_full((7,), -1)]).flip(0)[None].contiguous()
+        live = int((refs > 0).sum())
+        high, low = (refs[live:] > 0).nonzero()[:, 0] + live, (refs[:live] == 0).nonzero()[:, 0]
+        place = torch.arange(n_pages, device="cuda")
+        place[high] = low
+        want = refs.clone()
+        want[low], want[high] = refs[high], 0
+        out, moved, src, dst = bsp.bsp_pages_compact(W, refs, table)
+        assert torch.equal(out, want) and torch.equal(moved, torch.where(table >= 0, place[table.clamp(min=0).long()].to(torch.int32), table))
+        n = len(high)
+        assert torch.equal(src[:n].long(), high) and torch.equal(dst[:n].long(), low)
+        assert bool((src[n:] == -1).all()) and bool((dst[n:] == -1).all())
+    assert bsp.bsp_window_status(W) == 0
 
 
 def test_reordered_sequences(bsp):
