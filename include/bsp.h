@@ -462,8 +462,8 @@ int bsp_window_destroy(bsp_window_t w);
 int bsp_window_info(bsp_window_t w, int* window, int* sinks);
 /* Return and clear the status word, in one step behind the work of `stream`, a
  * stream of the handle's device, and wait for it (BSP_ERR_DEVICE_CHECK: a call
- * met impossible lengths or a page out of range; BSP_ERR_TIMEOUT: a bounded wait
- * ran out; BSP_ERR_INVALID_ARG: the current device is not the handle's). */
+ * met impossible lengths or a page out of range; BSP_ERR_OOM: no free page was
+ * left; BSP_ERR_TIMEOUT: a bounded wait ran out; BSP_ERR_INVALID_ARG: the current device is not the handle's). */
 int bsp_window_status(bsp_window_t w, void* stream);
 
 /* O = softmax(scale Q K^T over the visible keys) V.  Q, O: (z, query head,
