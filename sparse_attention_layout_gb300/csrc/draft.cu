@@ -87,7 +87,11 @@ struct VerifyArgs {
     int* status;
 };
 
-constexpr int kVerifyT = 512, kVerifyWarps = kVerifyT / 32;
+// Threads of a CTA, four CTAs an SM: while one waits for the reads that its walk or its
+// search asks for, others pass over their rows (64 sequences of 128000 entries 18.5
+// us, 200 52.9, 2000 of 4000 32; with 512 threads, two CTAs an SM, 18.9, 57.6 and 55; with
+// 128 22, 57 and 24).
+constexpr int kVerifyT = 256;
 constexpr int kMaxCluster = 8;
 
 // What the walk needs of a tree.  One CTA of the cluster reads it and hands it to
@@ -237,14 +241,14 @@ __device__ __forceinline__ void block_barrier() { asm volatile("bar.sync 1, %0;"
 // Bound by the chain of what follows one another, most of all the reads: offsets,
 // parents and tokens, their probabilities (2.4 us), the pass (64 sequences of
 // 128000 fp32 entries: 65 MB of two rows each, 11 us for 9.6 at a copy's rate),
-// the sums and the search (3.3 us); with the launch 20 us, and 7 for one sequence of
+// the sums and the search (3.3 us); with the launch 18.5 us, and 7 for one sequence of
 // 32000.  The walk's code stands once, and so does the pass': the first
 // instructions come from memory too, and with a copy of the pass wherever one is
 // asked for, one sequence took 18 us under the profiler, not 9.5.
 template <typename T, bool DRAWN>
-__global__ void __launch_bounds__(kVerifyT, 2) draft_verify_kernel(const __grid_constant__ VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyT, 1024 / kVerifyT) draft_verify_kernel(const __grid_constant__ VerifyArgs a) {
     using R = Rows<T, DRAWN>;
-    constexpr int N = R::N, NW = kVerifyWarps;
+    constexpr int N = R::N, NW = kVerifyT / 32;
     __shared__ Tree tree;
     __shared__ float2 sums[2][kMaxCluster * NW];  // Two's of the cluster's warps, of this pass and the last
     __shared__ int out[kMaxNodes];
@@ -361,8 +365,9 @@ __global__ void __launch_bounds__(kVerifyT, 2) draft_verify_kernel(const __grid_
     };
     Two c, mass(1.f);
     int n_out = 0;
-    // the sums in front of the lane's 4 runs, and each of theirs
+    // the sums in front of the lane's runs, and each of theirs
     constexpr int kRuns = kMaxCluster * NW / 32;
+    static_assert(kRuns * 32 == kMaxCluster * NW, "a lane holds a whole number of runs");
     Two front, run[kRuns];
     auto add_up = [&]() {
         Two mine;
@@ -556,7 +561,13 @@ __global__ void __launch_bounds__(kVerifyT, 2) draft_verify_kernel(const __grid_
 }
 
 template <typename T>
-int verify_t(const VerifyArgs& a, int n_seq, int cluster, cudaStream_t s) {
+int verify_t(const VerifyArgs& a, int n_seq, cudaStream_t s) {
+    // As many CTAs to a sequence as run at once, while each warp of theirs has a step
+    // of its own: 1, 2, 4, 8 CTAs for one sequence of 128000 entries 55, 30, 17, 11 us, for
+    // 200 of them 86, 53, 53, 51, for 2000 of 4000 32, 48, 83, 155.
+    const int at_once = 1024 / kVerifyT * sm_count(), per_step = kVerifyT * 16 / (int)sizeof(T);
+    int cluster = 1;
+    while (cluster < kMaxCluster && 2 * cluster * n_seq <= at_once && cluster * per_step < a.V) cluster *= 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(n_seq * cluster);
     cfg.blockDim = dim3(kVerifyT);
@@ -616,15 +627,10 @@ extern "C" int bsp_draft_verify(bsp_window_t w, int dtype, const void* target, i
         return BSP_ERR_ALIGNMENT;
     const VerifyArgs a{target, draft, target_stride, draft_stride, tokens, q_start, parent, accept, sample,
                        path, count, token, T, V, w->status};
-    // as many CTAs to a sequence as run at once, two on an SM, while each warp of
-    // theirs has a step of its own
-    const int per_step = kVerifyWarps * 32 * 16 / elt_bytes(dtype);
-    int cluster = 1;
-    while (cluster < kMaxCluster && 2 * cluster * n_seq <= 2 * bsp::sm_count() && cluster * per_step < V) cluster *= 2;
     cudaStream_t s = (cudaStream_t)stream;
     switch (dtype) {
-        case BSP_F32: return verify_t<float>(a, n_seq, cluster, s);
-        case BSP_BF16: return verify_t<__nv_bfloat16>(a, n_seq, cluster, s);
-        default: return verify_t<__half>(a, n_seq, cluster, s);
+        case BSP_F32: return verify_t<float>(a, n_seq, s);
+        case BSP_BF16: return verify_t<__nv_bfloat16>(a, n_seq, s);
+        default: return verify_t<__half>(a, n_seq, s);
     }
 }
