@@ -9,7 +9,7 @@
 // modulo 2^64, is the exact fraction of a turn at any position (in fp32 the angle
 // of position 10^6 is off by 0.03).  The nearest quarter turn comes off as the
 // top two bits, what is left, at most an eighth of a turn either way, is exact to
-// 2^-25 of itself in fp32.
+// 2^-24 of itself in fp32.
 #include <cmath>
 #include <cstring>
 #include <new>
