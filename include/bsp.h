@@ -600,8 +600,9 @@ int bsp_draft_verify(bsp_window_t w, int dtype, const void* target, int64_t targ
 /* The rows of the accepted nodes (path and count as bsp_draft_verify gives them;
  * kv_len still with all nodes) to the positions ctx, ctx + 1, ... of their
  * sequences; the sequence's length is then ctx + count.  Rows behind stay as they
- * are.  A sequence whose path does not ascend within its nodes, or of more nodes
- * than kv_len, is left out, a row with a page outside [0, n_pages) is not moved,
+ * are.  Pages of these positions that other sequences hold too have to be made
+ * the sequence's own before they are written (bsp_pages_reserve).  A sequence whose
+ * path does not ascend within its nodes, or of more nodes than kv_len, is left out, a row with a page outside [0, n_pages) is not moved,
  * and both are reported. */
 int bsp_paged_keep(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const bsp_tensor_t* V_cache,
                    const int32_t* q_start, const int32_t* kv_len, const int32_t* table, const int32_t* path,
