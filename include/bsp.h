@@ -463,7 +463,8 @@ int bsp_window_info(bsp_window_t w, int* window, int* sinks);
 /* Return and clear the status word, in one step behind the work of `stream`, a
  * stream of the handle's device, and wait for it (BSP_ERR_DEVICE_CHECK: a call
  * met impossible lengths or a page out of range; BSP_ERR_OOM: no free page was
- * left; BSP_ERR_TIMEOUT: a bounded wait ran out; BSP_ERR_INVALID_ARG: the current device is not the handle's). */
+ * left; BSP_ERR_TIMEOUT: a bounded wait ran out; BSP_ERR_INVALID_ARG: the current
+ * device is not the handle's). */
 int bsp_window_status(bsp_window_t w, void* stream);
 
 /* O = softmax(scale Q K^T over the visible keys) V.  Q, O: (z, query head,
@@ -602,8 +603,8 @@ int bsp_draft_verify(bsp_window_t w, int dtype, const void* target, int64_t targ
  * sequences; the sequence's length is then ctx + count.  Rows behind stay as they
  * are.  Pages of these positions that other sequences hold too have to be made
  * the sequence's own before they are written (bsp_pages_reserve).  A sequence whose
- * path does not ascend within its nodes, or of more nodes than kv_len, is left out, a row with a page outside [0, n_pages) is not moved,
- * and both are reported. */
+ * path does not ascend within its nodes, or of more nodes than kv_len, is left out,
+ * a row with a page outside [0, n_pages) is not moved, and both are reported. */
 int bsp_paged_keep(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const bsp_tensor_t* V_cache,
                    const int32_t* q_start, const int32_t* kv_len, const int32_t* table, const int32_t* path,
                    const int32_t* count, int T, int n_seq, int max_pages, int n_pages, int page, int Hkv, int D,
