@@ -63,36 +63,54 @@ __device__ __forceinline__ T* at(const View& v, int64_t i, int64_t j, int64_t k)
     return static_cast<T*>(v.ptr) + i * v.s[0] + j * v.s[1] + k * v.s[2];
 }
 
-// 64 rows of `cols` columns into shared memory (pitch cols + 4); row r from
-// rowptr(r), or zeros where that is null.  fp32 rows are copied behind the
-// thread's back: landed() and a barrier make them visible.
-template <typename T, int DP, typename F>
-__device__ __forceinline__ void load_tile(float* dst, int D, F rowptr, int cols = DP) {
+// 16 bytes of a row into shared memory as fp32, zeros where `live` is not set.
+// fp32 pieces are copied behind the thread's back: landed() and a barrier make them
+// visible.
+template <typename T>
+__device__ __forceinline__ void load_piece(float* to, const T* src, bool live) {
     constexpr int N = Vec16<T>::N;
-    const int C = cols / N;
+    if constexpr (std::is_same<T, float>::value) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+                     "l"(live ? src : reinterpret_cast<const T*>(kNothing)), "r"(live ? 16 : 0)
+                     : "memory");
+    } else {
+        float v[N];
+        if (live) {
+            Vec16<T>::load(src, v);
+        } else {
+#pragma unroll
+            for (int k = 0; k < N; ++k) v[k] = 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < N; k += 4)
+            *reinterpret_cast<float4*>(to + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+    }
+}
+
+// 64 rows of `DP` columns into shared memory (pitch DP + 4); row r from
+// rowptr(r), or zeros where that is null.
+template <typename T, int DP, typename F>
+__device__ __forceinline__ void load_tile(float* dst, int D, F rowptr) {
+    constexpr int N = Vec16<T>::N, C = DP / N;
 #pragma unroll 4
     for (int i = threadIdx.x; i < R * C; i += kT) {
         const int r = i / C, c = (i % C) * N;
         const T* src = rowptr(r);
-        const bool live = src && c < D;
-        float* to = dst + r * (cols + 4) + c;
-        if constexpr (std::is_same<T, float>::value) {
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
-                         "l"(live ? src + c : reinterpret_cast<const T*>(kNothing)), "r"(live ? 16 : 0)
-                         : "memory");
-        } else {
-            float v[N];
-            if (live) {
-                Vec16<T>::load(src + c, v);
-            } else {
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[k] = 0.f;
-            }
-#pragma unroll
-            for (int k = 0; k < N; k += 4)
-                *reinterpret_cast<float4*>(to + k) = make_float4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-        }
+        load_piece(dst + r * (DP + 4) + c, src + c, src && c < D);
     }
+}
+// The same of rows of D columns (pitch D + 4), a row to 4 threads (2 in 16 bits), each
+// of which finds its row once: its page, and the division by the group's heads.
+// (Piece by piece, as above, a tile's begin took 4.7 us, not 3.4, and a step's copies
+// 1.1, not 0.6.)
+template <typename T, typename F>
+__device__ __forceinline__ void load_rows(float* dst, int D, F rowptr) {
+    constexpr int N = Vec16<T>::N, L = 16 / N;
+    const int r = threadIdx.x / L, c0 = threadIdx.x % L * N;
+    if (r >= R) return;
+    const T* src = rowptr(r);
+#pragma unroll 4
+    for (int c = c0; c < D; c += 16) load_piece(dst + r * (D + 4) + c, src + c, src != nullptr);
 }
 // ends a group of copies; waits until all but the last n groups have landed
 __device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -195,9 +213,11 @@ __device__ __forceinline__ void report_bad_segs(const P& p) {
 
 // TREE: the tokens are nodes of trees of drafted tokens (pages only).  Few rows and
 // keys to a CTA, so what a step and a start cost counts: products over the head's
-// own columns, and one CTA an SM where no more run at once (16 trees of 5 to 70
-// nodes over 300 to 6000 keys, 6 heads of 80: 67 us; 62 and 59 with one of the two,
-// 55 with both).
+// own columns, in rows of their length, so that two CTAs run on an SM up to 112
+// columns, and no more CTAs than run at once (16 trees of 6 to 44 nodes over 400 to
+// 6000 keys, 6 heads of 80: 67 us without any of it, now 47: the split 4.4 us, a tile's
+// begin 3.4, a step of 64 keys 11 beside another CTA's, bound by shared-memory reads;
+// the join 4).
 template <typename T, int DP, bool PAGED, bool TREE>
 __global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(const __grid_constant__ ArgsOf<Problem<TREE>> A,
                                                      const __grid_constant__ SimtPlan plan) {
@@ -216,6 +236,10 @@ __global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(c
     if (threadIdx.x == 0) A.cuts[blockIdx.x].pieces = 0;
     __syncthreads();
     const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+    auto load = [&](float* dst, auto rowptr) {
+        if constexpr (TREE) load_rows<T>(dst, A.D, rowptr);
+        else load_tile<T, DP>(dst, A.D, rowptr);
+    };
     Walk<P, PAGED ? kRagged : kDense> walk(p, PAGED ? start.tab : plan.tab, PAGED ? start.cta : plan.s[blockIdx.x]);
     Item it;
     while (walk.next(it)) {
@@ -225,10 +249,10 @@ __global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(c
         const int lo = window_low(q.a, p.window);
         const int rows = q.nt * p.G;
         __syncthreads();
-        load_tile<T, DP>(Qs, A.D, [&](int r) -> const T* {
+        load(Qs, [&](int r) -> const T* {
             if (r >= rows) return nullptr;
             return at<const T>(A.Q, w.z, (int64_t)w.hk * p.G + r % p.G, (int64_t)it.g.t0 + q.tok0 + r / p.G);
-        }, cols);
+        });
         float m[4], l[4];
         int pos[4], node[4];  // TREE: the row's token
         float2 acc[4][NG][2];
@@ -272,14 +296,14 @@ __global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(c
         auto copy = [&](float* dst, const View& v, int n) {
             const int kb = first_key(n);
             if (n < it.ns)
-                load_tile<T, DP>(dst, A.D, [&](int r) -> const T* {
+                load(dst, [&](int r) -> const T* {
                     const int j = kb + r;
                     if (PAGED) {
                         const int pg = pages[n & 1][r];
                         return pg < 0 ? nullptr : at<const T>(v, pg, w.hk, j & ((1 << p.page_shift) - 1));
                     }
                     return wanted(j) ? at<const T>(v, w.z, w.hk, j) : nullptr;
-                }, cols);
+                });
             copies_end();
         };
         find_pages(0);
