@@ -584,7 +584,8 @@ int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, c
  * token is the first one up to which r_k adds up to more than sample * sum r_k
  * (the target's own row if r_k is all 0; no entry above 0 in it: -1).  Sums keep
  * their rounding errors (relative error about 2^-45): a number that is no nearer
- * to a border than that falls as in exact arithmetic.  Entries that are negative or NaN count as 0.
+ * to a border than that falls as in exact arithmetic.  Entries of both rows that
+ * are negative or NaN count as 0.
  *
  * path: DEVICE int32 [T] (output), in the rows of each sequence its accepted nodes
  * from node 0 on, then -1; count: DEVICE int32 [n_seq], their number (0 for a

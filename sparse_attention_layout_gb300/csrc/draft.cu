@@ -152,6 +152,9 @@ __device__ __forceinline__ Two warp_scan(Two x, int lane) {
     return x;
 }
 
+// What an entry of a row counts as: one that is negative or no number, 0.
+__device__ __forceinline__ float weight(float x) { return fmaxf(x, 0.f); }
+
 // What is left of a row of the target: p - c q where that is positive, or p
 // without some tokens.
 template <typename T, bool DRAWN>
@@ -191,7 +194,7 @@ struct Rows {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
                 // p - c q, every rounding error kept
-                const float u = to_f32(pe[j]), v = to_f32(qe[j]);
+                const float u = to_f32(pe[j]), v = weight(to_f32(qe[j]));
                 const float m = __fmul_rn(c.hi, v), e = fmaf(c.lo, v, fmaf(c.hi, v, -m));
                 const float d = u - m, t = d - u;
                 const float r = ((u - (d - t)) - (m + t)) - e;
@@ -202,8 +205,7 @@ struct Rows {
         } else {
 #pragma unroll
             for (int j = 0; j < N; ++j) {
-                const float u = to_f32(pe[j]);
-                x[j] = u > 0.f ? u : 0.f;
+                x[j] = weight(to_f32(pe[j]));
                 y[j] = 0.f;
             }
             if (!DRAWN) {
@@ -294,8 +296,8 @@ __global__ void __launch_bounds__(kVerifyT, 1024 / kVerifyT) draft_verify_kernel
             }
             float p = 0.f, q = 0.f;
             if (up >= 0) {
-                p = to_f32(target[(q0 + up) * a.target_row + tok]);
-                if (DRAWN) q = to_f32(draft[(q0 + up) * a.draft_row + tok]);
+                p = weight(to_f32(target[(q0 + up) * a.target_row + tok]));
+                if (DRAWN) q = weight(to_f32(draft[(q0 + up) * a.draft_row + tok]));
             }
             const float u = a.accept[q0 + i];
             for (int r = 0; r < C; ++r) {

@@ -1,0 +1,97 @@
+"""Verification of drafted tokens where entries are no probabilities, against the
+walk in fp64 over the rows with such entries set to 0."""
+
+import math
+import random
+
+import pytest
+import torch
+
+import draft_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def bsp():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    from sparse_attention_layout_gb300 import build
+    build.build()
+    from sparse_attention_layout_gb300 import bsp as m
+    return m
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def counted(rows):
+    """The rows in fp64 on the host, entries that count as 0 set to it."""
+    return torch.where(rows > 0, rows, torch.zeros_like(rows)).double().cpu().numpy()
+
+
+def agrees(bsp, W, parents, target, draft, tok, accept, sample):
+    """Every sequence's path, count and token are those of the walk in fp64."""
+    starts = [0]
+    for t in parents:
+        starts.append(starts[-1] + len(t))
+    got = bsp.bsp_draft_verify(W, target, draft, tok, ints(starts), ints([x for t in parents for x in t]), accept, sample)
+    path, count, token = (x.tolist() for x in got)
+    p, q = counted(target), None if draft is None else counted(draft)
+    tl, al, sl = tok.tolist(), accept.double().tolist(), sample.double().tolist()
+    for i, t in enumerate(parents):
+        a, b = starts[i], starts[i + 1]
+        want, nxt = ref.verify(p[a:b], None if q is None else q[a:b], tl[a:b], t, al[a:b], sl[i])
+        assert (count[i], path[a:b], token[i]) == (len(want), want + [-1] * (b - a - len(want)), nxt), i
+    assert bsp.bsp_window_status(W) == 0
+    return got
+
+
+@pytest.mark.parametrize("chosen", [False, True], ids=["drawn", "chosen"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [5, 37, 3000])
+def test_entries_that_count_as_nothing(bsp, V, dtype, chosen):
+    """Negative entries, NaN and -inf in a third of the places of both rows, at the
+    children's tokens and elsewhere."""
+    W, n_seq = bsp.bsp_window_create(), 48
+    r, g = random.Random(V), torch.Generator(device="cuda").manual_seed(V)
+    parents = [[-1] + [r.randrange(max(0, i - 5), i) for i in range(1, 9)] for _ in range(n_seq)]
+    T = 9 * n_seq
+    rows = []
+    for _ in range(2):
+        x = torch.softmax(2 * torch.randn(T, V, generator=g, device="cuda"), -1)
+        kind = torch.randint(0, 9, (T, V), generator=g, device="cuda")
+        x = torch.where(kind == 0, -x, x)
+        x = torch.where(kind == 1, torch.full_like(x, math.nan), x)
+        rows.append(torch.where(kind == 2, torch.full_like(x, -math.inf), x).to(DT[dtype]))
+    # tokens from the likely entries of the parents' rows, without their signs, and bad ones
+    tok = torch.zeros(T, dtype=torch.int32, device="cuda")
+    for s, t in enumerate(parents):
+        for i in range(1, 9):
+            row = rows[r.randrange(2)][9 * s + t[i]].float()
+            bad = (~(row > 0)).nonzero()[:, 0].tolist()
+            likely = row.abs().nan_to_num(0.0, posinf=0.0).argsort(descending=True)[:4].tolist()
+            tok[9 * s + i] = r.choice(bad if bad and r.random() < 0.5 else likely)
+    for low in (0.0, 0.8):  # then mostly rejected
+        accept = low + (1 - low) * torch.rand(T, generator=g, device="cuda")
+        sample = torch.rand(n_seq, generator=g, device="cuda")
+        agrees(bsp, W, parents, rows[0], None if chosen else rows[1], tok, accept.clamp(max=1 - 2.0 ** -24), sample)
+
+
+@pytest.mark.parametrize("bad", [-0.2, math.nan, -math.inf, -0.0])
+def test_rejected_entries_that_count_as_nothing(bsp, bad):
+    W = bsp.bsp_window_create()
+    target = torch.tensor([[0.3, bad, 0.1, 0.3, 0.3]] * 3, device="cuda")
+    for u in (0.0, 0.1, 0.45, 0.9):
+        agrees(bsp, W, [[-1, 0, 0]], target, None, ints([0, 0, 1]), torch.full((3,), 0.9, device="cuda"), torch.full((1,), u, device="cuda"))
+    # a draft's entry that counts as nothing leaves the target's as it is, and gives no
+    # token that the target excludes
+    target = torch.tensor([[0.5, 0.0, 0.25, 0.25]] * 3, device="cuda")
+    draft = torch.tensor([[0.6, bad, bad, 0.4]] * 3, device="cuda")
+    for tokens in ([0, 0, 1], [0, 1, 0], [0, 1, 2], [0, 0, 3]):
+        for u in (0.0, 0.3, 0.6, 0.95):
+            agrees(bsp, W, [[-1, 0, 0]], target, draft, ints(tokens), torch.full((3,), 0.9, device="cuda"),
+                   torch.full((1,), u, device="cuda"))
