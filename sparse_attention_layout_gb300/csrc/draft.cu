@@ -503,10 +503,13 @@ __global__ void __launch_bounds__(kVerifyT, 1024 / kVerifyT) draft_verify_kernel
         if (warp == 0) add_up();
     }
     if (now.winner < 0 || now.winner / NW != rank) return;
-    // the winner's run, NW steps at a time, each by a warp
+    // from the winner's run on, NW steps at a time, each by a warp; its token stands
+    // behind the run only where rounding says so (a run whose tokens were all taken
+    // away may keep a sum above 0)
     const R rows = rows_now();
     int first, last;
     run_of(rows, now.winner, &first, &last);
+    last = (int)steps_of(rows);
     const Two want = two(now.want);
     Two reached = two(now.before);
     int some = -1;  // the last entry with anything, of this thread
@@ -551,15 +554,31 @@ __global__ void __launch_bounds__(kVerifyT, 1024 / kVerifyT) draft_verify_kernel
         reached = from_lane(upto, 31);
         __syncthreads();
     }
-    // rounding, or a number of 1 or more: the run's last entry with anything
-    some = __reduce_max_sync(0xffffffffu, some);
+    // rounding, or a number of 1 or more: the last entry with anything
     int* last_of = reinterpret_cast<int*>(step_sum);
-    if (lane == 0) last_of[warp] = some;
-    __syncthreads();
-    if (tid == 0) {
+    auto over_block = [&]() {
+        some = __reduce_max_sync(0xffffffffu, some);
+        if (lane == 0) last_of[warp] = some;
+        __syncthreads();
         for (int i = 0; i < NW; ++i) some = imax(some, last_of[i]);
-        a.token[s] = some;
+        __syncthreads();
+    };
+    over_block();
+    if (some < 0) {  // in front of the run, then
+#pragma unroll 1
+        for (int k = warp; k < first; k += NW) {
+            const int piece = k * 32 + lane;
+            uint4 p, q;
+            float x[N], y[N];
+            rows.load(piece, p, q);
+            rows.left(piece, p, q, x, y);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (x[i] + y[i] > 0.f) some = piece * N - rows.off + i;
+        }
+        over_block();
     }
+    if (tid == 0) a.token[s] = some;
 }
 
 template <typename T>

@@ -95,3 +95,29 @@ def test_rejected_entries_that_count_as_nothing(bsp, bad):
         for u in (0.0, 0.3, 0.6, 0.95):
             agrees(bsp, W, [[-1, 0, 0]], target, draft, ints(tokens), torch.full((3,), 0.9, device="cuda"),
                    torch.full((1,), u, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_all_of_a_run_rejected(bsp, dtype):
+    """Chosen drafts that are all that a stretch of the vocabulary holds, of 0.06 to
+    1e-13: what rounding leaves of the stretch's sum when they are taken away holds
+    no token, and the next one, for the number 0, lies behind it."""
+    W, n_seq, V = bsp.bsp_window_create(), 64, 32000
+    g, r = torch.Generator().manual_seed(7), random.Random(7)
+    target = torch.zeros(10 * n_seq, V)
+    tok = torch.zeros(n_seq, 10, dtype=torch.int32)
+    for s in range(n_seq):
+        at = r.sample(range(256), 9)
+        target[10 * s:10 * s + 10, at] = torch.tensor([10.0 ** -r.uniform(1.2, 13) for _ in at])
+        target[10 * s:10 * s + 10, r.sample(range(1000, V), 20)] = 0.025
+        tok[s, 1:] = torch.tensor(at)
+    accept = torch.full((10 * n_seq,), 0.999, device="cuda")
+    args = [[-1] + [0] * 9] * n_seq, target.to(DT[dtype]).cuda(), None, tok.view(-1).cuda(), accept
+    for u in (0.0, 2.0 ** -149, 0.3, 1 - 2.0 ** -24):
+        _, count, token = agrees(bsp, W, *args, torch.full((n_seq,), u, device="cuda"))
+        assert bool((count == 1).all()) and bool((token >= 1000).all())
+    # the same behind everything else, where a number that is too large falls to the last entry
+    back = args[1].flip(1).contiguous(), None, (V - 1 - args[3]).contiguous()
+    for u in (0.0, 1 - 2.0 ** -24, 1.0):
+        _, count, token = agrees(bsp, W, args[0], *back, accept, torch.full((n_seq,), u, device="cuda"))
+        assert bool((count == 1).all()) and bool((token < V - 1000).all())
