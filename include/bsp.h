@@ -583,9 +583,11 @@ int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, c
  * accept * s_k < r_k[x]), and the walk goes on at it.  Where none does, the next
  * token is the first one up to which r_k adds up to more than sample * sum r_k
  * (the target's own row if r_k is all 0; no entry above 0 in it: -1).  Sums keep
- * their rounding errors (relative error about 2^-45): a number that is no nearer
- * to a border than that falls as in exact arithmetic.  Entries of both rows that
- * are negative or NaN count as 0.
+ * their rounding errors, and are off by less than (V + 2^14) 2^-51 of what they add
+ * up (the target's row and s_0 + .. + s_(k-1) times the draft's): a number that is no
+ * nearer to a border than that falls as in exact arithmetic, if the products
+ * compared are above 2^-100 (below, fp32 has not all of their digits).
+ * Entries of both rows that are negative or NaN count as 0.
  *
  * path: DEVICE int32 [T] (output), in the rows of each sequence its accepted nodes
  * from node 0 on, then -1; count: DEVICE int32 [n_seq], their number (0 for a

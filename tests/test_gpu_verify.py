@@ -3,7 +3,9 @@ walk in fp64 over the rows with such entries set to 0."""
 
 import math
 import random
+from fractions import Fraction
 
+import numpy as np
 import pytest
 import torch
 
@@ -121,3 +123,46 @@ def test_all_of_a_run_rejected(bsp, dtype):
     for u in (0.0, 1 - 2.0 ** -24, 1.0):
         _, count, token = agrees(bsp, W, args[0], *back, accept, torch.full((n_seq,), u, device="cuda"))
         assert bool((count == 1).all()) and bool((token < V - 1000).all())
+
+
+def beside(border):
+    """The float32 numbers next to a border, and its least distance from them."""
+    x = np.float32(float(border))
+    below, above = (x, np.nextafter(x, np.float32(2))) if Fraction(float(x)) < border else (np.nextafter(x, np.float32(0)), x)
+    return float(below), float(above), min(border - Fraction(float(below)), Fraction(float(above)) - border) / border
+
+
+@pytest.mark.parametrize("chosen", [False, True], ids=["drawn", "chosen"])
+def test_sums_of_many_terms(bsp, chosen):
+    """16 million entries to one block, 65536 to a thread, all but two the same, so that
+    rounding errors add up: the sum decides on the second child, whose numbers are
+    the two next to the border, 2^-26 of it away at least (V is chosen so)."""
+    v, Z, q = 0.1 * 2.0 ** -20, 0.5, 0.25  # the rows' entries, the second child's
+    v = float(np.float32(v))
+    rest = Fraction(Z) - (0 if chosen else Fraction(q))
+    for V in range(2 ** 24 + 1, 2 ** 24 + 400):
+        total = (V - 2) * Fraction(v) + rest
+        low, high, margin = beside(rest / total if chosen else rest / (Fraction(q) * total))
+        if margin >= Fraction(1, 2 ** 26):
+            break
+    assert 0 < low < high < 1 and margin >= Fraction(1, 2 ** 26)
+    x1, x2 = 5, V // 2
+    target, draft = torch.full((3, V), v, device="cuda"), torch.zeros(3, V, device="cuda")
+    target[:, x1], target[:, x2] = 0.0, Z
+    draft[:, x1], draft[:, x2] = 0.5, q
+    W, n_seq = bsp.bsp_window_create(), 400  # (the others without nodes)
+    starts, parent, tok = ints([0] + [3] * n_seq), ints([-1, 0, 0]), ints([0, x1, x2])
+    sample = torch.full((n_seq,), 0.5, device="cuda")
+    for u, want in ((low, 2), (high, 1)):
+        accept = torch.tensor([0.0, 0.5, u], device="cuda")
+        _, count, _ = bsp.bsp_draft_verify(W, target, None if chosen else draft, tok, starts, parent, accept, sample)
+        assert count[0].item() == want
+    # and the next token, of a row of equal entries: the one that the number falls into
+    target.fill_(v)
+    for at in (3, 77777, 5555555, 12345678, 2 ** 24 - 9):
+        u = float(np.float32((at + 0.5) / V))
+        if not 0.25 <= u * V - int(u * V) <= 0.75:
+            continue
+        _, count, token = bsp.bsp_draft_verify(W, target, None, tok, starts, ints([-1, -1, -1]), accept, sample * 0 + u)
+        assert count[0].item() == 1 and token[0].item() == int(Fraction(u) * V)
+    assert bsp.bsp_window_status(W) == 0
