@@ -611,9 +611,11 @@ Args make_args(const Call& c) {
     return a;
 }
 
+// most: of the kernel's calls.  The limit belongs to the kernel, so one that followed a
+// call's own size would refuse a larger call of another host thread.
 template <typename K, typename... A>
-int launch(K kern, int grid, size_t smem, cudaStream_t s, const A&... args) {
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+int launch(K kern, int grid, size_t smem, size_t most, cudaStream_t s, const A&... args) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most) != cudaSuccess)
         return BSP_ERR_CUDA;
     kern<<<grid, kT, smem, s>>>(args...);
     return cudaGetLastError() == cudaSuccess ? BSP_OK : BSP_ERR_CUDA;
@@ -630,7 +632,11 @@ constexpr size_t tree_bytes(int D) { return sizeof(float) * ((size_t)3 * R * (D 
 template <typename T, int DP>
 int forward_t(Call& c, const Args& a, int grid) {
     c.p.TQ = a.p.TQ, c.p.kshift = a.p.kshift;
-    size_t smem = c.p.words ? tree_bytes(c.D) : tiles_bytes<DP>(3, 1);
+    // (at least the tile counts of the sequences)
+    constexpr size_t seqs = kMaxSeqs * sizeof(int), tiles = tiles_bytes<DP>(3, 1);
+    static_assert(tiles >= seqs, "tiles leave room for the sequences' counts");
+    constexpr size_t most = tree_bytes(DP) > seqs ? tree_bytes(DP) : seqs;
+    size_t smem = tree_bytes(c.D);
     if (smem < (size_t)c.p.nseg * sizeof(int)) smem = (size_t)c.p.nseg * sizeof(int);
     SimtPlan plan{};
     bool cut = true;
@@ -638,9 +644,9 @@ int forward_t(Call& c, const Args& a, int grid) {
     if (rc) return rc;
     const ArgsOf<TreeProb> t{TreeProb{a.p}, a.Q, a.K, a.V, a.O, a.dO, a.dQ, a.dK, a.dV, a.lse, a.lz, a.lh, a.lt, a.delta,
                              a.D, a.scale, a.c2, a.cuts, a.slots};
-    rc = c.p.words   ? launch(forward_kernel<T, DP, true, true>, grid, smem, c.stream, t, plan)
-         : c.p.paged ? launch(forward_kernel<T, DP, true, false>, grid, smem, c.stream, a, plan)
-                     : launch(forward_kernel<T, DP, false, false>, grid, smem, c.stream, a, plan);
+    rc = c.p.words   ? launch(forward_kernel<T, DP, true, true>, grid, smem, most, c.stream, t, plan)
+         : c.p.paged ? launch(forward_kernel<T, DP, true, false>, grid, tiles, tiles, c.stream, a, plan)
+                     : launch(forward_kernel<T, DP, false, false>, grid, tiles, tiles, c.stream, a, plan);
     return rc || !cut ? rc : launch_join(c, R, grid, false);
 }
 
@@ -653,9 +659,10 @@ int backward_t(Call& c, const Args& a, int grid) {
     int rc = query_plan(c, grid, &plan.tab, plan.s, &cut);
     if (!rc) rc = key_plan(c, kp, grid, &kplan.tab, kplan.s, &kcut);
     if (!rc) rc = launch_delta(c);
-    if (!rc) rc = launch(dq_kernel<T, DP>, grid, tiles_bytes<DP>(4, 1), c.stream, a, plan);
+    constexpr size_t dq = tiles_bytes<DP>(4, 1), dkv = tiles_bytes<DP>(4, 2);
+    if (!rc) rc = launch(dq_kernel<T, DP>, grid, dq, dq, c.stream, a, plan);
     if (!rc && cut) rc = launch_join(c, R, grid, true);
-    if (!rc) rc = launch(dkv_kernel<T, DP>, grid, tiles_bytes<DP>(4, 2), c.stream, a, kp, kplan);
+    if (!rc) rc = launch(dkv_kernel<T, DP>, grid, dkv, dkv, c.stream, a, kp, kplan);
     return rc || !kcut ? rc : launch_join_kv(c, kp, R, grid);
 }
 
