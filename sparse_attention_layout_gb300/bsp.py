@@ -1270,7 +1270,13 @@ class _RotaryPositions(torch.autograd.Function):
     @staticmethod
     def forward(ctx, Q, K, positions, R, inverse):
         ctx.set_materialize_grads(False)
-        ctx.args = R, positions, None if positions is None else positions._version, inverse
+        version = None
+        if positions is not None:
+            if positions.is_inference() and not torch.is_inference_mode_enabled():
+                positions = positions.clone()  # a tensor of inference mode has no version
+            if not positions.is_inference():
+                version = positions._version
+        ctx.args = R, positions, version, inverse
         return bsp_rotary(R, _strides_taken(Q), None if K is None else _strides_taken(K), positions, inverse=inverse)
 
     @staticmethod

@@ -65,3 +65,34 @@ def test_trees_of_two_threads(bsp, pair):
     assert [[x for x in c if x] for c in codes] == [[], []]
     for _, O, want, _ in calls:
         assert torch.equal(O, want)
+
+
+def test_rotary_positions_in_inference_mode(bsp):
+    """Positions made in inference mode, there and, for a gradient, outside of it."""
+    R = bsp.bsp_rotary_create(bsp.rotary_frequencies(64)[0])
+    Q, K = randn(2, 4, 9, 64, seed=1), randn(2, 2, 9, 64, seed=2)
+    rows = torch.randint(0, 5000, (2, 9), dtype=torch.int32).cuda()
+    want = bsp.bsp_rotary(R, Q, K, rows)
+    leaf = Q.clone().requires_grad_()
+    with torch.inference_mode():
+        pos = rows.clone()
+        inside = Q.clone()
+        for q in (Q, leaf, inside):  # (a weight's output, and tensors of the mode)
+            got = bsp.rotary(R, q, K, pos)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and not got[0].requires_grad
+        assert torch.equal(bsp.rotary(R, inside)[0], bsp.bsp_rotary(R, Q)[0])
+    with torch.no_grad():
+        assert torch.equal(bsp.rotary(R, leaf, None, pos)[0], want[0])
+    dQ = randn(2, 4, 9, 64, seed=3)
+    back, _ = bsp.bsp_rotary(R, dQ, None, rows, inverse=True)
+    q, _ = bsp.rotary(R, leaf, K, pos)
+    assert torch.equal(q, want[0])
+    with torch.inference_mode():
+        pos.zero_()  # the gradient's own positions stay
+    assert torch.equal(torch.autograd.grad(q, leaf, dQ)[0], back)
+    # positions of no mode that change before the gradient: refused as before
+    pos = rows.clone()
+    q, _ = bsp.rotary(R, leaf, K, pos)
+    pos.zero_()
+    with pytest.raises(RuntimeError, match="changed in place"):
+        torch.autograd.grad(q, leaf, dQ)
