@@ -2,37 +2,36 @@
 // dependency on libcuda: the runtime hands out the driver function).
 #include <cudaTypedefs.h>
 
-#include <mutex>
-
 #include "tc_common.cuh"
 
 namespace bsp {
 namespace {
 
+// A driver function through the runtime, which hands it out.
+template <typename F>
+F driver_fn(const char* name, unsigned version) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    const bool found = cudaGetDriverEntryPointByVersion(name, &p, version, cudaEnableDefault, &q) == cudaSuccess &&
+                       q == cudaDriverEntryPointSuccess;
+    return found ? reinterpret_cast<F>(p) : nullptr;
+}
+
 // The encoder is a driver call and fails without a current context, which a thread
 // has only once it has made a runtime call that needs one: a thread of autograd's
-// may come here with none.  Setting the device it has makes it current.
+// may come here with none.  Setting the device it has makes that one's current; a
+// context that is current stays, the caller's own among them.
 bool context_is_current() {
-    thread_local int bound = -1;
+    static const auto get = driver_fn<PFN_cuCtxGetCurrent_v4000>("cuCtxGetCurrent", 4000);
+    CUcontext current = nullptr;
+    if (get && get(&current) == CUDA_SUCCESS && current) return true;
     int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    if (dev != bound && cudaSetDevice(dev) != cudaSuccess) return false;
-    bound = dev;
-    return true;
+    return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess;
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     if (!context_is_current()) return nullptr;
-    static std::once_flag once;
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-    std::call_once(once, [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-                cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    });
+    static const auto fn = driver_fn<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled", 12000);
     return fn;
 }
 

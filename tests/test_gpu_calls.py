@@ -1,6 +1,7 @@
 """Calls as serving programs make them: from two host threads at once, in inference
 mode, with pages far into a cache."""
 
+import ctypes
 import threading
 
 import pytest
@@ -96,3 +97,50 @@ def test_rotary_positions_in_inference_mode(bsp):
     pos.zero_()
     with pytest.raises(RuntimeError, match="changed in place"):
         torch.autograd.grad(q, leaf, dQ)
+
+
+def test_tensor_maps_leave_the_current_context(bsp):
+    """A thread that works in a driver context of its own still does after a tensor map
+    was encoded there, and one without a context has one afterwards.  (The encoder that
+    the tensor-core calls share; nothing is launched in that context.)"""
+    cuda, lib = ctypes.CDLL("libcuda.so.1"), bsp.lib()
+    encode = lib._ZN3bsp12make_tmap_2dEP14CUtensorMap_stPKvimmjji
+    encode.argtypes = [ctypes.c_void_p] * 2 + [ctypes.c_int] + [ctypes.c_uint64] * 2 + [ctypes.c_uint32] * 2 + [ctypes.c_int]
+    rows = torch.zeros(256, 64, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    results = {}
+
+    def current():
+        c = ctypes.c_void_p()
+        assert cuda.cuCtxGetCurrent(ctypes.byref(c)) == 0
+        return c.value
+
+    def map_of(base):
+        room = ctypes.create_string_buffer(256)
+        at = -(-ctypes.addressof(room) // 64) * 64
+        return encode(at, base, 1, 256, 64, 128, 64, 128)
+
+    def own():
+        dev, ctx, base = ctypes.c_int(), ctypes.c_void_p(), ctypes.c_uint64()
+        assert cuda.cuInit(0) == 0 and cuda.cuDeviceGet(ctypes.byref(dev), torch.cuda.current_device()) == 0
+        assert cuda.cuCtxCreate_v2(ctypes.byref(ctx), 0, dev) == 0
+        try:
+            assert cuda.cuMemAlloc_v2(ctypes.byref(base), ctypes.c_size_t(256 * 64 * 2)) == 0
+            results["own"] = map_of(base.value), current() == ctx.value, map_of(base.value), current() == ctx.value
+            assert cuda.cuCtxSetCurrent(ctx) == 0 and cuda.cuMemFree_v2(base) == 0
+        finally:
+            cuda.cuCtxDestroy_v2(ctx)
+
+    def none():
+        first = current()
+        results["none"] = first, map_of(rows.data_ptr()), current()
+        assert cuda.cuCtxSetCurrent(None) == 0
+        results["again"] = map_of(rows.data_ptr()), current()
+
+    for f in (own, none):
+        t = threading.Thread(target=f)
+        t.start()
+        t.join()
+    primary = current()
+    assert results["own"] == (0, True, 0, True)
+    assert results["none"] == (None, 0, primary) and results["again"] == (0, primary)
