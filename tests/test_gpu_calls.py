@@ -144,3 +144,25 @@ def test_tensor_maps_leave_the_current_context(bsp):
     primary = current()
     assert results["own"] == (0, True, 0, True)
     assert results["none"] == (None, 0, primary) and results["again"] == (0, primary)
+
+
+def test_kept_rows_behind_32_bit_offsets(bsp):
+    """Accepted rows that move within and between pages behind 2^31 elements."""
+    n_pages, Hkv, page, D = 16500, 8, 128, 128  # 2.16e9 elements a cache
+    K, V = (torch.zeros(n_pages, Hkv, page, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table, n, kv = [3, n_pages - 2, n_pages - 1], 20, 270  # nodes at 250 .. 269, six of them in the second page
+    for i, c in enumerate((K, V)):
+        for x in table:
+            c[x] = randn(Hkv, page, D, seed=10 * i + x % 10, dtype=torch.bfloat16)
+    kept = [0, 2, 3, 5, 6, 7, 8, 11, 12, 15, 17, 19]
+    want = []
+    for c in (K, V):
+        rows = torch.cat([c[x] for x in table], 1)  # [Hkv, positions, D]
+        rows[:, 250:250 + len(kept)] = rows[:, [250 + x for x in kept]]
+        want.append(rows)
+    W = bsp.bsp_window_create()
+    bsp.bsp_paged_keep(W, K, V, ints([0, n]), ints([kv]), ints([table]), ints(kept + [-1] * (n - len(kept))), ints([len(kept)]))
+    assert bsp.bsp_window_status(W) == 0
+    for c, rows in zip((K, V), want):
+        assert torch.equal(torch.cat([c[x] for x in table], 1), rows)
+        assert not bool(c[:3].any()) and not bool(c[4:n_pages - 2].any())
