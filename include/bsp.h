@@ -573,7 +573,7 @@ int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, c
  * the next, V contiguous) = the probabilities of the token behind node t; draft:
  * the same for the distribution that each child of node t was drawn from,
  * independently, or NULL where the children were chosen without chance; rows of
- * nodes whose children need no look are not read.  tokens: DEVICE int32 [T];
+ * nodes whose children need no look are not read.  Entries are finite.  tokens: DEVICE int32 [T];
  * accept, sample: DEVICE float [T], [n_seq], uniform numbers in [0, 1).
  *
  * From node 0 down, before the k-th child of a node (in the order of their rows):
@@ -625,7 +625,8 @@ int bsp_paged_keep(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const
  *
  * Checked on the device, reported by bsp_window_status: a length below 0 or beyond
  * max_pages * page (the sequence is left out) and an entry of n_pages or more (it
- * counts as none) as BSP_ERR_DEVICE_CHECK, no free page left as BSP_ERR_OOM.
+ * counts as none; reserve and compact leave it as it is) as BSP_ERR_DEVICE_CHECK, no
+ * free page left as BSP_ERR_OOM (the word keeps the first report).
  * Workspace of fork, reserve and compact: bsp_pages_workspace() bytes. */
 
 /* Gives up the pages behind each sequence's length (of a sequence that ended:
@@ -672,7 +673,8 @@ int bsp_paged_copy(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const
  * frequencies[i] and grows by the amplitude A:
  *     y_a = A (x_a cos - x_b sin),  y_b = A (x_b cos + x_a sin)
  * for the columns (a, b) = (i, i + n_pairs), or interleaved (2 i, 2 i + 1); the
- * other columns stay.  Angles are exact to 2^-32 of a turn at any position. */
+ * other columns stay.  Angles are exact to 2^-31 of a turn at any position, for
+ * frequencies of up to a turn. */
 
 typedef struct bsp_rotary_s* bsp_rotary_t;
 

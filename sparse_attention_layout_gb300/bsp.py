@@ -1141,6 +1141,9 @@ def rotary_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "none
         "parts"   pairs that turn more than `fast` times over `length` as they
                   are, less than `slow` times divided by factor, a ramp in turns
                   between; amplitude 0.1 ln(factor) + 1
+
+    A model that was trained with a ramp in the pairs' index, as is common too, has
+    other frequencies between the two ends: give those to bsp_rotary_create.
     """
     if rot_dim < 2 or rot_dim % 2:
         raise ValueError("rot_dim must be an even number of columns")

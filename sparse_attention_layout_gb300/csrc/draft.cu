@@ -88,9 +88,9 @@ struct VerifyArgs {
 };
 
 // Threads of a CTA, four CTAs an SM: while one waits for the reads that its walk or its
-// search asks for, others pass over their rows (64 sequences of 128000 entries 18.5
-// us, 200 52.9, 2000 of 4000 32; with 512 threads, two CTAs an SM, 18.9, 57.6 and 55; with
-// 128 22, 57 and 24).
+// search asks for, others pass over their rows (64 sequences of 128000 entries 19.3
+// us, 200 53.8, 2000 of 4000 33; with 512 threads, two CTAs an SM, 20.1, 61.3 and 59; with
+// 128 23.0, 57.6 and 24).
 constexpr int kVerifyT = 256;
 constexpr int kMaxCluster = 8;
 
@@ -245,10 +245,10 @@ __device__ __forceinline__ void block_barrier() { asm volatile("bar.sync 1, %0;"
 // to looks for the token in that run, a step of 32 pieces to a warp.
 //
 // Bound by the chain of what follows one another, most of all the reads: offsets,
-// parents and tokens, their probabilities (2.4 us), the pass (64 sequences of
-// 128000 fp32 entries: 65 MB of two rows each, 11 us for 9.6 at a copy's rate),
-// the sums and the search (3.3 us); with the launch 18.5 us, and 7 for one sequence of
-// 32000.  The walk's code stands once, and so does the pass': the first
+// parents and tokens, their probabilities (2.5 us), the pass (64 sequences of
+// 128000 fp32 entries: 65 MB of two rows each, 9.2 us with what L2 holds of them, for
+// 9.6 from memory at a copy's rate), the sums (1.7) and the search (2.1); with the
+// launch 19.6 us, and 7 for one sequence of 32000.  The walk's code stands once, and so does the pass': the first
 // instructions come from memory too, and with a copy of the pass wherever one is
 // asked for, one sequence took 18 us under the profiler, not 9.5.
 template <typename T, bool DRAWN>

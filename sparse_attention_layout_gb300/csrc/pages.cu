@@ -522,7 +522,9 @@ int check_ints(P... ptr) {
 // Compaction of 5000 pages 7.7 us with one block, 9.0 with eight; of 65536 48 and 14; of
 // a million 700 and 124.  Reserving two pages for each of 200 sequences 5 and 10 us
 // whatever the pages, until only the last ones are free (65536: 18 and 11, a million:
-// 245 and 65); 128 pages for each of 256 prompts 103 and 26.
+// 245 and 65); 128 pages for each of 256 prompts 103 and 26.  (The rule asks for the
+// pages alone, since how many items there are is known on the device only: many
+// prompts among few pages stay on one block.)
 int team_of(int n_pages, int scans) { return n_pages > scans * kSteps * kBig ? kTeam : 1; }
 
 template <typename A>

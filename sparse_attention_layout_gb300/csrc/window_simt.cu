@@ -216,8 +216,11 @@ __device__ __forceinline__ void report_bad_segs(const P& p) {
 // own columns, in rows of their length, so that two CTAs run on an SM up to 112
 // columns, and no more CTAs than run at once (16 trees of 6 to 44 nodes over 400 to
 // 6000 keys, 6 heads of 80: 67 us without any of it, now 47: the split 4.4 us, a tile's
-// begin 3.4, a step of 64 keys 11 beside another CTA's, bound by shared-memory reads;
-// the join 4).
+// begin 3.4, a step of 64 keys 11 beside another CTA's, bound by shared-memory reads.
+// Of 304 CTAs, from the first one's start, 88 with one step end at 23 us, 208 with two
+// at 30 (27 to 37), and 8 whose two steps lie in two tiles at 35 (31 to 38); the join
+// takes 4, the rest lies between the launches.  At 128 registers D above 64 spills 20
+// bytes in fp32.)
 template <typename T, int DP, bool PAGED, bool TREE>
 __global__ void __launch_bounds__(kT, DP == 64 || TREE ? 2 : 1) forward_kernel(const __grid_constant__ ArgsOf<Problem<TREE>> A,
                                                      const __grid_constant__ SimtPlan plan) {
