@@ -573,7 +573,7 @@ int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, c
  * the next, V contiguous) = the probabilities of the token behind node t; draft:
  * the same for the distribution that each child of node t was drawn from,
  * independently, or NULL where the children were chosen without chance; rows of
- * nodes whose children need no look are not read.  Entries are finite.  tokens: DEVICE int32 [T];
+ * nodes whose children need no look are not read.  tokens: DEVICE int32 [T];
  * accept, sample: DEVICE float [T], [n_seq], uniform numbers in [0, 1).
  *
  * From node 0 down, before the k-th child of a node (in the order of their rows):
@@ -583,11 +583,11 @@ int bsp_paged_tree_attention(bsp_window_t w, int dtype, const bsp_tensor_t* Q, c
  * accept * s_k < r_k[x]), and the walk goes on at it.  Where none does, the next
  * token is the first one up to which r_k adds up to more than sample * sum r_k
  * (the target's own row if r_k is all 0; no entry above 0 in it: -1).  Sums keep
- * their rounding errors, and are off by less than (V + 2^14) 2^-51 of what they add
- * up (the target's row and s_0 + .. + s_(k-1) times the draft's): a number that is no
- * nearer to a border than that falls as in exact arithmetic, if the products
- * compared are above 2^-100 (below, fp32 has not all of their digits).
- * Entries of both rows that are negative or NaN count as 0.
+ * their rounding errors: each adds one below (V + 2^14) 2^-51 of what it adds up
+ * (the target's row and s_0 + .. + s_(k-1) times the draft's).  A number that is no
+ * nearer to a border than they are falls as in exact arithmetic, if the products
+ * compared are above 2^-100 (below, fp32 has not all of their digits).  Entries of
+ * both rows that are negative or NaN count as 0; +inf is no entry to give.
  *
  * path: DEVICE int32 [T] (output), in the rows of each sequence its accepted nodes
  * from node 0 on, then -1; count: DEVICE int32 [n_seq], their number (0 for a
@@ -674,7 +674,7 @@ int bsp_paged_copy(bsp_window_t w, int dtype, const bsp_tensor_t* K_cache, const
  *     y_a = A (x_a cos - x_b sin),  y_b = A (x_b cos + x_a sin)
  * for the columns (a, b) = (i, i + n_pairs), or interleaved (2 i, 2 i + 1); the
  * other columns stay.  Angles are exact to 2^-31 of a turn at any position, for
- * frequencies of up to a turn. */
+ * frequencies of up to a turn a position. */
 
 typedef struct bsp_rotary_s* bsp_rotary_t;
 
